@@ -29,6 +29,7 @@
 
 #include "dc.h"
 #include "dc_device.cuh"
+#include "dc_host.h"
 #include "dc_internal.h"
 
 namespace {
@@ -89,6 +90,8 @@ struct Options {
   std::atomic<long long> wait_limit_ns{1000000000};
   std::atomic<long long> test_bulk_short_tx{0};
 };
+constexpr int kMaxDevices = 64;
+std::atomic<int> g_sms[kMaxDevices];  // SM counts read so far
 Options g_opt;
 std::once_flag g_env_once;
 
@@ -143,6 +146,17 @@ void read_env_once() {
   });
 }
 
+}  // namespace
+
+// Shared with the other host units (dc_host.h).
+namespace dc {
+
+void read_options() { read_env_once(); }
+
+bool pdl_option() { return g_opt.pdl.load() != 0; }
+
+bool launch_failure_injected() { return g_opt.test_fail_launch.load() != 0; }
+
 dc_status_t fail(dc_status_t s, const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);
@@ -155,16 +169,6 @@ dc_status_t ok() {
   g_err[0] = '\0';
   return DC_OK;
 }
-
-bool overlaps(uint64_t a, uint64_t na, uint64_t b, uint64_t nb) {
-  return na > 0 && nb > 0 && a < b + nb && b < a + na;
-}
-
-// ---------------------------------------------------- device properties ---
-constexpr int kMaxDevices = 64;
-constexpr int kFamilies = 128;  // gather: family * kGatherModes + mode (< 18); reductions: 24 + (< 72); staged realigning reduction: 96 + (< 24); fused all-gather: 127
-std::atomic<int> g_sms[kMaxDevices];
-std::atomic<int> g_occ[kMaxDevices][kFamilies];
 
 dc_status_t current_device(int* dev) {
   cudaError_t e = cudaGetDevice(dev);
@@ -189,6 +193,28 @@ dc_status_t sm_count(int dev, int* sms) {
   *sms = v;
   return DC_OK;
 }
+
+dc_status_t check_launch(cudaError_t e, const char* what, int grid) {
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return fail(DC_ERR_CUDA, "%s launch failed: %s", what, cudaGetErrorString(e));
+  }
+  g_launches.fetch_add(1, std::memory_order_relaxed);
+  g_last_grid = grid;
+  return ok();
+}
+
+}  // namespace dc
+
+namespace {
+
+bool overlaps(uint64_t a, uint64_t na, uint64_t b, uint64_t nb) {
+  return na > 0 && nb > 0 && a < b + nb && b < a + na;
+}
+
+// ---------------------------------------------------- device properties ---
+constexpr int kFamilies = 128;  // gather: family * kGatherModes + mode (< 18); reductions: 24 + (< 72); staged realigning reduction: 96 + (< 24); fused all-gather: 127
+std::atomic<int> g_occ[kMaxDevices][kFamilies];
 
 template <class F>
 int occupancy(int dev, int family, F query) {
@@ -224,16 +250,6 @@ bool use_single(uint64_t size_bytes, long long threshold) {
   if (f == 1) return true;
   if (f == 2) return false;
   return size_bytes <= static_cast<uint64_t>(threshold);
-}
-
-dc_status_t check_launch(cudaError_t e, const char* what, int grid) {
-  if (e != cudaSuccess) {
-    cudaGetLastError();
-    return fail(DC_ERR_CUDA, "%s launch failed: %s", what, cudaGetErrorString(e));
-  }
-  g_launches.fetch_add(1, std::memory_order_relaxed);
-  g_last_grid = grid;
-  return ok();
 }
 
 // --------------------------------------------------------------- gather ---
