@@ -301,6 +301,209 @@ dc_status_t dc_fused_all_gather_static(const void *const *in_ptrs, void *const *
                                        size_t bytes_per_rank, dc_stream_t stream);
 
 /*
+ * Operators of language models beside the collectives, for reproducible
+ * rollouts and training on them: log probabilities over the vocabulary shards
+ * of a tensor-parallel head (with their gradient), and the paged key-value
+ * cache with the attention of single new tokens over it.  They follow the
+ * conventions above (one kernel a call, no allocation, checks first), and
+ * their results depend on no other row or sequence of the call, on no grid
+ * and, for the log probabilities, on no sharding: a token has the same bits
+ * in a batch of one and in a batch of a thousand.
+ *
+ * Each takes a block of arguments by address, read before the call returns.
+ * Strides count elements.  Sums, maxima and statistics are binary32.
+ */
+
+/*
+ * dc_token_logprobs -- for each row of logits x and its token y, with
+ * z = x / temperature over columns [0, vocab) of the concatenated shards:
+ *
+ *   lse = log(sum_i exp(z_i));  logprobs = z_y - lse;
+ *   entropy = lse - sum_i p_i z_i,  p = exp(z - lse);
+ *   top_tokens, top_logprobs = the `top` largest columns by x (equal logits:
+ *   lowest index first) and their log probabilities.
+ *
+ * shards, widths, row_strides: host arrays of `ranks` entries: rank r holds
+ *   `widths[r]` columns, row i at shards[r] + i * row_strides[r].  Shards may
+ *   be uneven, empty, or column ranges of one tensor; any alignment of the
+ *   element type.  Columns past `vocab` (padding) are not read.
+ * tokens: int32 or int64 (tokens_64).  A negative token asks for nothing:
+ *   its log probability is 0.  A token of vocab or more gives NaN.
+ * logprobs [rows]; entropy, lse [rows] and top_logprobs, top_tokens
+ *   [rows, top], all contiguous, NULL where not wanted.  top: 0..DC_MAX_TOP.
+ * Masked logits (-inf) have probability 0.  A row of nothing else has
+ * lse = -inf, log probabilities -inf and entropy 0.  A row with NaN or +inf
+ * gives NaN; NaN logits are never among the alternatives, and places that no
+ * number fills hold token -1 and NaN.
+ */
+#define DC_MAX_TOP 32
+#define DC_MAX_VOCAB (1 << 22)
+typedef struct {
+    const void *const *shards;
+    const uint64_t *widths;
+    const uint64_t *row_strides;
+    const void *tokens;
+    float *logprobs;
+    float *entropy;
+    float *lse;
+    float *top_logprobs;
+    void *top_tokens;
+    int64_t rows;
+    int64_t vocab;
+    double temperature;
+    int32_t ranks;
+    int32_t dtype;          /* dc_dtype_t of the logits */
+    int32_t tokens_64;
+    int32_t top_tokens_64;
+    int32_t top;
+    int32_t reserved;       /* 0 */
+} dc_token_logprobs_t;
+dc_status_t dc_token_logprobs(const dc_token_logprobs_t *args, dc_stream_t stream);
+
+/*
+ * dc_token_logprobs_backward -- the gradient of sum(g * logprobs + h *
+ * entropy) with respect to the logits, from the lse and entropy that
+ * dc_token_logprobs returned:
+ *
+ *   grads_i = (1/temperature) (g ([i = y] - p_i) - h p_i (log p_i + entropy))
+ *
+ * g = grad_logprobs and h = grad_entropy [rows], either NULL (zero); h needs
+ * `entropy`.  A negative token's g counts as 0.  grads[r] has widths[r]
+ * columns; padding columns receive 0, as do rows of nothing but masks (-inf or
+ * the type's lowest value: lse <= -1e30).
+ * grads[r] may be exactly shards[r] (in place); any other overlap is refused.
+ */
+typedef struct {
+    const void *const *shards;
+    const uint64_t *widths;
+    const uint64_t *row_strides;
+    void *const *grads;
+    const uint64_t *grad_row_strides;
+    const void *tokens;
+    const float *lse;
+    const float *entropy;
+    const float *grad_logprobs;
+    const float *grad_entropy;
+    int64_t rows;
+    int64_t vocab;
+    double temperature;
+    int32_t ranks;
+    int32_t dtype;
+    int32_t tokens_64;
+    int32_t reserved;       /* 0 */
+} dc_token_logprobs_backward_t;
+dc_status_t dc_token_logprobs_backward(const dc_token_logprobs_backward_t *args, dc_stream_t stream);
+
+/* One of the two tensors of a paged cache: element d of head h of token o of
+ * page g is data[g*page_stride + o*token_stride + h*head_stride + d], every
+ * head 16-byte aligned. */
+typedef struct {
+    void *data;
+    uint64_t page_stride;
+    uint64_t token_stride;
+    uint64_t head_stride;
+} dc_paged_cache_t;
+
+/*
+ * dc_kv_append -- puts the keys and values of `tokens` new tokens into a paged
+ * cache and rotates keys (and queries, q -> q_out) to their positions.  Token
+ * i of sequence s = seqs[i] at position t = positions[i] goes to slot
+ * t % page_size of page page_table[s * table_stride + t / page_size].
+ *
+ * Rotation: of the first rotary_dim elements of a head, pair (j, j +
+ * rotary_dim/2), or (2j, 2j + 1) if interleaved, (a, b) becomes (a c - b s,
+ * b c + a s) with c = cos_sin[t][j], s = cos_sin[t][rotary_dim/2 + j]; in
+ * binary32, rounded once.  rotary_dim 0: none.
+ *
+ * q, k, v, q_out: [tokens, heads, dim], 16-byte aligned heads, the last
+ * dimension contiguous.  q_heads 0: no queries.  q_out may be exactly q.
+ * dim: a multiple of 8 (of 4 for DC_F32) up to 1024; rotary_dim a multiple of
+ * 16 (half as much for DC_F32, and for pairs that are interleaved).
+ * A negative position marks padding: nothing is written for it.  A token
+ * whose sequence, position or page does not exist leaves the cache alone and
+ * its q_out row is NaN.  Two tokens for one slot: either may remain.
+ */
+typedef struct {
+    const void *q;
+    const void *k;
+    const void *v;
+    void *q_out;
+    const int32_t *positions;
+    const int32_t *seqs;
+    const int32_t *page_table;
+    const float *cos_sin;   /* [cos_sin_rows, rotary_dim] */
+    dc_paged_cache_t k_cache;
+    dc_paged_cache_t v_cache;
+    uint64_t q_token_stride, q_head_stride;
+    uint64_t k_token_stride, k_head_stride;
+    uint64_t v_token_stride, v_head_stride;
+    uint64_t q_out_token_stride, q_out_head_stride;
+    int64_t tokens;
+    int64_t table_rows, table_width, table_stride;
+    int64_t cos_sin_rows;
+    int64_t num_pages;
+    int32_t page_size;
+    int32_t q_heads;
+    int32_t kv_heads;
+    int32_t dim;
+    int32_t rotary_dim;
+    int32_t interleaved;
+    int32_t dtype;
+    int32_t reserved;       /* 0 */
+} dc_kv_append_t;
+dc_status_t dc_kv_append(const dc_kv_append_t *args, dc_stream_t stream);
+
+/*
+ * dc_paged_attention -- attention of one new token per sequence over a paged
+ * cache.  Query head h of sequence b attends, through key head
+ * h / (q_heads / kv_heads), to tokens t of [max(0, lengths[b] - window),
+ * lengths[b]) (window 0: all):
+ *
+ *   out = sum_t softmax_t(scale * q . k_t) v_t;
+ *   lse = log(sum_t exp(scale * q . k_t))           (NULL if not wanted)
+ *
+ * q, out: [seqs, q_heads, dim], 16-byte aligned heads; DC_BF16 or DC_F16;
+ * dim 64, 96, 128, 192 or 256.  lse [seqs, q_heads], contiguous.
+ * A sequence of length 0 gives zeros and lse = -inf.  A page number outside
+ * the cache among the attended ones, or a length past the table, gives NaN;
+ * entries of the table past a sequence's length are not read.
+ *
+ * workspace: device memory of at least dc_attention_workspace_bytes(seqs,
+ * q_heads, kv_heads, dim, max_tokens) bytes, 16-byte aligned, owned by the
+ * caller, zero before its first use (each call leaves it ready for the next,
+ * of any shape it is large enough for).  max_tokens: table_width * page_size,
+ * or the window if that is shorter.  Calls on one workspace must not overlap
+ * on the GPU: one per stream.
+ */
+typedef struct {
+    const void *q;
+    void *out;
+    float *lse;
+    const int32_t *page_table;
+    const int32_t *lengths;
+    void *workspace;
+    uint64_t workspace_bytes;
+    dc_paged_cache_t k_cache;
+    dc_paged_cache_t v_cache;
+    uint64_t q_seq_stride, q_head_stride;
+    uint64_t out_seq_stride, out_head_stride;
+    int64_t seqs;
+    int64_t table_width, table_stride;
+    int64_t num_pages;
+    int32_t page_size;
+    int32_t q_heads;
+    int32_t kv_heads;
+    int32_t dim;
+    int32_t window;
+    int32_t dtype;
+    float scale;
+    int32_t reserved;       /* 0 */
+} dc_paged_attention_t;
+dc_status_t dc_paged_attention(const dc_paged_attention_t *args, dc_stream_t stream);
+/* 0 if the arguments are not supported. */
+size_t dc_attention_workspace_bytes(int64_t seqs, int q_heads, int kv_heads, int dim, int64_t max_tokens);
+
+/*
  * dc_check_device -- reports the faults that this library's kernels recorded
  * on the current device since the last check, and clears them.
  *

@@ -27,6 +27,8 @@ __all__ = [
     "DCError", "LibraryMissing", "all_gather", "all_gather_many", "all_reduce",
     "reduce_scatter", "reduce", "all_reduce_many", "reduce_scatter_many", "inject_delay", "check_device",
     "fused_all_gather", "fused_workspace", "fused_reset",
+    "token_logprobs", "token_logprobs_backward", "logprobs_and_entropy", "kv_append", "paged_attention",
+    "attention_workspace",
     "set_option",
     "get_option",
     "launch_count", "last_grid", "last_error", "options", "lib", "LIB_PATH", "STATUS", "DTYPES", "ORDERS",
@@ -612,3 +614,10 @@ def last_grid() -> int:
 
 def last_error() -> str:
     return lib().dc_last_error().decode(errors="replace")
+
+
+# ------------------------------------------ operators of language models ---
+from .operators import (  # noqa: E402  (they use the binding above)
+    attention_workspace, dc_attention_workspace_bytes, dc_kv_append, dc_paged_attention, dc_token_logprobs,
+    dc_token_logprobs_backward, kv_append, logprobs_and_entropy, paged_attention, token_logprobs,
+    token_logprobs_backward)

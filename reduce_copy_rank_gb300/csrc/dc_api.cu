@@ -1295,9 +1295,11 @@ dc_status_t dc_check_device(void) {
   // bounds-check records of the checked build (empty in the normal build)
   static cudaError_t (*const kReaders[kBoundsReaders])(BoundsFault*) = {
       take_bounds_gather, take_bounds_bulk, take_bounds_fused,
-      take_bounds_reduce_bf16, take_bounds_reduce_f16, take_bounds_reduce_f32};
+      take_bounds_reduce_bf16, take_bounds_reduce_f16, take_bounds_reduce_f32,
+      take_bounds_logprobs, take_bounds_append, take_bounds_attention};
   static const char* const kFiles[kBoundsReaders] = {"dc_gather.cu", "dc_bulk.cu", "dc_fused.cu",
-                                                     "dc_reduce_bf16.cu", "dc_reduce_f16.cu", "dc_reduce_f32.cu"};
+                                                     "dc_reduce_bf16.cu", "dc_reduce_f16.cu", "dc_reduce_f32.cu",
+                                                     "dc_logprobs.cu", "dc_kv_append.cu", "dc_attention.cu"};
   BoundsFault first{};
   int first_file = -1;
   unsigned long long outside = 0;

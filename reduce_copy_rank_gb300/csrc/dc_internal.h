@@ -291,13 +291,16 @@ cudaError_t take_bulk_faults(uint32_t* bits);
 // returns an empty one in the normal build.  bounds_file names the file of
 // reader i (i < kBoundsReaders).
 struct BoundsFault;
-constexpr int kBoundsReaders = 6;
+constexpr int kBoundsReaders = 9;
 cudaError_t take_bounds_gather(BoundsFault* f);
 cudaError_t take_bounds_bulk(BoundsFault* f);
 cudaError_t take_bounds_fused(BoundsFault* f);
 cudaError_t take_bounds_reduce_bf16(BoundsFault* f);
 cudaError_t take_bounds_reduce_f16(BoundsFault* f);
 cudaError_t take_bounds_reduce_f32(BoundsFault* f);
+cudaError_t take_bounds_logprobs(BoundsFault* f);
+cudaError_t take_bounds_append(BoundsFault* f);
+cudaError_t take_bounds_attention(BoundsFault* f);
 bool bounds_checked_build();
 
 // One-thread delay of `ns` nanoseconds of the global timer (rank-skew

@@ -1,0 +1,189 @@
+// Appending keys and values to a paged cache, the position rotation applied
+// on the way (and to the queries of the same tokens).
+//
+// Mathematics.  A pair (a, b) of a head's first `rot` elements at position t
+// becomes (a cos - b sin, b cos + a sin), with the pair's cos and sin from
+// row t of a table; pairs are elements (i, i + rot/2), or (2i, 2i + 1) when
+// interleaved.  Products and sums in binary32, one rounding to the element
+// type.  Other elements and the values are copied.
+//
+// Bound: memory (every element is read and written once) for prompts, one
+// launch's latency for single tokens.  A CTA takes one token (or a share of
+// it when there are few): a thread owns one pair position across heads, so
+// its cos and sin stay in registers, and has several heads' loads in flight.
+#include "dc_llm.h"
+#include "dc_numeric.cuh"
+
+namespace dc {
+namespace {
+
+enum : uint32_t { kSiteTokenInfo = 1, kSiteTable = 2, kSiteIn = 3, kSiteOut = 4, kSiteCache = 5, kSiteAngle = 6 };
+
+constexpr int kHeadsInFlight = 4;
+
+__device__ __forceinline__ int32_t ld_i32(uint64_t base, uint64_t i, uint64_t n) {
+  const int32_t* a = reinterpret_cast<const int32_t*>(base) + i;
+  return in_bounds(a, 4, base, base + n * 4, kSiteTokenInfo) ? *a : -1;
+}
+
+// One 16-byte vector of a [tokens, heads, dim] tensor's token row; `span` is
+// the bytes of that row from its first head to its last.
+struct Row {
+  uint64_t base, head, span;
+};
+__device__ __forceinline__ uint4 ld_row(const Row& r, int h, uint32_t off) {
+  const uint4* a = reinterpret_cast<const uint4*>(r.base + h * r.head + off);
+  return in_bounds(a, 16, r.base, r.base + r.span, kSiteIn) ? ld_stream(a) : uint4{};
+}
+__device__ __forceinline__ void st_row(const Row& r, int h, uint32_t off, const uint4& v, uint32_t site) {
+  uint4* a = reinterpret_cast<uint4*>(r.base + h * r.head + off);
+  if (in_bounds(a, 16, r.base, r.base + r.span, site)) st16(a, v);
+}
+
+template <int DT>
+__global__ __launch_bounds__(kAppendThreads) void dc_append_kernel(const __grid_constant__ AppendParams p) {
+  constexpr uint32_t kB = Elem<DT>::kBytes;
+  constexpr int kPer = Elem<DT>::kPerVec;
+  pdl_enter();
+  const uint64_t token = blockIdx.x;
+  const int32_t pos = ld_i32(p.positions, token, p.tokens);
+  const int32_t seq = ld_i32(p.seqs, token, p.tokens);
+  if (pos < 0) return;  // padding: nothing is written for it
+  // where the token goes; a place that does not exist is never touched
+  bool ok = seq >= 0 && static_cast<uint32_t>(seq) < p.num_seqs;
+  const uint32_t col = static_cast<uint32_t>(pos) / p.page_size, slot = static_cast<uint32_t>(pos) % p.page_size;
+  ok = ok && col < p.table_width && (p.rot == 0 || static_cast<int64_t>(pos) < p.cos_rows);
+  int32_t page = -1;
+  if (ok) {
+    const int32_t* a = reinterpret_cast<const int32_t*>(p.table) + seq * p.table_stride + col;
+    const uint64_t hi = p.table + (static_cast<uint64_t>(p.num_seqs - 1) * p.table_stride + p.table_width) * 4;
+    if (in_bounds(a, 4, p.table, hi, kSiteTable)) page = *a;
+    ok = page >= 0 && page < p.num_pages;
+  }
+  const uint64_t row_bytes = static_cast<uint64_t>(p.dim) * kB;
+  Row q{p.q + token * p.q_token, p.q_head, (p.q_heads > 0 ? p.q_heads - 1 : 0) * p.q_head + row_bytes};
+  Row qo{p.qo + token * p.qo_token, p.qo_head, (p.q_heads > 0 ? p.q_heads - 1 : 0) * p.qo_head + row_bytes};
+  Row k{p.k + token * p.k_token, p.k_head, (p.kv_heads - 1) * p.k_head + row_bytes};
+  Row v{p.v + token * p.v_token, p.v_head, (p.kv_heads - 1) * p.v_head + row_bytes};
+  const int vecs = p.dim / kPer;
+  if (!ok) {  // the queries of a token that cannot be placed read NaN
+    if (p.q_heads == 0) return;
+    const uint32_t w = DT == kF32 ? 0x7FC00000u : DT == kF16 ? 0x7E007E00u : 0x7FC07FC0u;
+    for (int u = blockIdx.y * kAppendThreads + threadIdx.x; u < p.q_heads * vecs; u += gridDim.y * kAppendThreads)
+      st_row(qo, u / vecs, static_cast<uint32_t>(u % vecs) * 16, make_uint4(w, w, w, w), kSiteOut);
+    return;
+  }
+  Row kc{p.kc.base + static_cast<uint64_t>(page) * p.kc.page + slot * p.kc.token, p.kc.head,
+         (p.kv_heads - 1) * p.kc.head + row_bytes};
+  Row vc{p.vc.base + static_cast<uint64_t>(page) * p.vc.page + slot * p.vc.token, p.vc.head,
+         (p.kv_heads - 1) * p.vc.head + row_bytes};
+
+  // units of a head: pairs of vectors (or single vectors) that rotate, then vectors that do not
+  const int turning = p.interleaved ? p.rot / kPer : p.rot / (2 * kPer);
+  const int units = turning + (p.dim - p.rot) / kPer;
+  const int per = kAppendThreads / units;  // heads a pass
+  const int unit = static_cast<int>(threadIdx.x) % units, sub = static_cast<int>(threadIdx.x) / units;
+  const int heads = p.q_heads + p.kv_heads;
+  if (sub < per) {
+    const bool turns = unit < turning, pair = turns && !p.interleaved;
+    const uint32_t off0 = turns ? static_cast<uint32_t>(unit) * 16
+                                : static_cast<uint32_t>(p.rot * kB) + static_cast<uint32_t>(unit - turning) * 16;
+    const uint32_t off1 = off0 + static_cast<uint32_t>(p.rot / 2) * kB;
+    // pair: cos and sin of the vector's elements; interleaved: of its pairs
+    float cs[kPer], sn[kPer];
+    if (turns) {
+      const int n = p.interleaved ? kPer / 2 : kPer;
+      const uint64_t base = p.cos_sin + static_cast<uint64_t>(pos) * p.rot * 4;
+      const float* c = reinterpret_cast<const float*>(base) + unit * n;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (i < n && in_bounds(c + i, 4, base, base + p.rot * 4ull, kSiteAngle)) {
+          cs[i] = c[i];
+          sn[i] = c[i + p.rot / 2];
+        }
+    }
+    const int step = per * static_cast<int>(gridDim.y);
+    for (int h0 = static_cast<int>(blockIdx.y) * per + sub; h0 < heads; h0 += step * kHeadsInFlight) {
+      uint4 a[kHeadsInFlight], b[kHeadsInFlight];
+#pragma unroll
+      for (int i = 0; i < kHeadsInFlight; ++i) {
+        const int h = h0 + i * step;
+        if (h >= heads) break;
+        const Row& src = h < p.q_heads ? q : k;
+        const int hh = h < p.q_heads ? h : h - p.q_heads;
+        a[i] = ld_row(src, hh, off0);
+        if (pair) b[i] = ld_row(src, hh, off1);
+      }
+#pragma unroll
+      for (int i = 0; i < kHeadsInFlight; ++i) {
+        const int h = h0 + i * step;
+        if (h >= heads) break;
+        const bool is_q = h < p.q_heads;
+        const Row& dst = is_q ? qo : kc;
+        const int hh = is_q ? h : h - p.q_heads;
+        if (turns) {
+          float x[kPer], y[kPer];
+          unpack<DT>(a[i], x);
+          if (pair) {
+            unpack<DT>(b[i], y);
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) {
+              const float lo = x[e] * cs[e] - y[e] * sn[e];
+              y[e] = y[e] * cs[e] + x[e] * sn[e];
+              x[e] = lo;
+            }
+            st_row(dst, hh, off1, repack<DT>(y), is_q ? kSiteOut : kSiteCache);
+          } else {
+#pragma unroll
+            for (int e = 0; e < kPer; e += 2) {
+              const float lo = x[e] * cs[e / 2] - x[e + 1] * sn[e / 2];
+              x[e + 1] = x[e + 1] * cs[e / 2] + x[e] * sn[e / 2];
+              x[e] = lo;
+            }
+          }
+          a[i] = repack<DT>(x);
+        }
+        st_row(dst, hh, off0, a[i], is_q ? kSiteOut : kSiteCache);
+      }
+    }
+  }
+  const int vu = p.kv_heads * vecs;
+  for (int u = blockIdx.y * kAppendThreads + threadIdx.x; u < vu; u += gridDim.y * kAppendThreads) {
+    const int h = u / vecs;
+    const uint32_t off = static_cast<uint32_t>(u % vecs) * 16;
+    st_row(vc, h, off, ld_row(v, h, off), kSiteCache);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_append(const AppendParams& p, int dtype, int sms, bool pdl, cudaStream_t s, int* grid) {
+  // few tokens: several CTAs share one token's heads
+  const int per_vec = dtype == kF32 ? 4 : 8;
+  const int units = (p.q_heads + 2 * p.kv_heads) * (p.dim / per_vec);
+  int y = 1;
+  if (p.tokens < static_cast<uint64_t>(sms)) {
+    const int most = (units + kAppendThreads - 1) / kAppendThreads;
+    const int room = static_cast<int>(2 * static_cast<uint64_t>(sms) / p.tokens);
+    y = most < room ? most : room;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.tokens), static_cast<unsigned>(y));
+  cfg.blockDim = dim3(kAppendThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = pdl ? attr : nullptr;
+  cfg.numAttrs = pdl ? 1 : 0;
+  *grid = static_cast<int>(p.tokens) * y;
+  switch (dtype) {
+    case kF16: return cudaLaunchKernelEx(&cfg, dc_append_kernel<kF16>, p);
+    case kF32: return cudaLaunchKernelEx(&cfg, dc_append_kernel<kF32>, p);
+    default: return cudaLaunchKernelEx(&cfg, dc_append_kernel<kBF16>, p);
+  }
+}
+
+DC_BOUNDS_READER(take_bounds_append)
+
+}  // namespace dc
