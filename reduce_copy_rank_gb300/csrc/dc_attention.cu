@@ -1,23 +1,27 @@
 // Attention of one new token per sequence over a paged key-value cache.
 //
 // Mathematics.  For sequence b with n attended tokens and query head h of
-// key head k:  o = sum_t softmax_t(scale q.k_t) v_t.  The tokens are cut into
-// pieces whose length follows from n and the head counts alone, so what else
-// is in the batch changes no bit.  A piece keeps, per head, its maximum m,
-// its sum l = sum 2^(s_t - m) and its unnormalised output, all in binary32
-// (s_t = scale log2(e) q.k_t); the last piece to finish joins them in order:
-// M = max m, o = sum 2^(m-M) o_piece / sum 2^(m-M) l.
+// key head k:  o = sum_t softmax_t(scale q.k_t) v_t.  Any run of tokens keeps,
+// per head, a reference r, l = sum 2^(s_t - r) and the unnormalised output
+// u = sum 2^(s_t - r) v_t, in binary32 (s_t = scale log2(e) q.k_t).  r is the
+// running maximum rounded up to a whole number: changing it multiplies by a
+// power of two, which rounds nothing, so a result depends only on the order
+// in which the terms are added.  That order is one binary tree over leaves of
+// 64 tokens (more for very long sequences), fixed by n alone; how large a
+// subtree a warp, a CTA or a group of CTAs computes is free, and follows from
+// how much work there is.  So neither the rest of the batch nor the grid
+// changes a bit.  The last CTA to finish joins what is left of the tree.
 //
 // Bound: memory.  Every key and value is read once; at 8 query heads per key
 // head that is 8 multiply-adds per byte, which the matrix pipe does with a
 // wide margin (mma.m16n8k16, 16 heads x 8 tokens), so it is fed from shared
 // memory by cp.async and never waited for.  A warp owns 16 tokens at a time
-// with a ring of its own: no barrier until the piece is done.
+// with a ring of its own: no barrier until its subtree is done.
 //
-// Rounding.  The weights 2^(s-m) enter the second product as a pair of 16-bit
+// Rounding.  The weights 2^(s-r) enter the second product as a pair of 16-bit
 // numbers hi + lo (hi the weight cut to 16 bits, lo the rounded rest), so
-// that the output carries one rounding to 16 bits, the last.  With at most 8 heads to
-// a CTA the pair fills the tile's 16 rows and costs nothing.
+// that the output carries one rounding to 16 bits, the last.  With at most 8
+// heads to a CTA the pair fills the tile's 16 rows and costs nothing.
 #include <atomic>
 
 #include "dc_llm.h"
@@ -32,13 +36,19 @@ enum : uint32_t {
 
 constexpr int kThreads = kAttendWarps * 32;
 
-template <int D>
-struct Ring {
-  static constexpr int kRow = D * 2 + 16;                      // bytes; the 16 keep ldmatrix free of conflicts
-  static constexpr int kHalf = kAttendTile * kRow;             // keys or values of one tile
+// Shared memory of a head size: each warp's ring of tiles, then (heads above
+// 128, whose subtrees do not fit in registers) its waiting subtrees.
+template <int D, int HB>
+struct Shape {
+  static constexpr int kRow = D * 2 + 16;           // bytes; the 16 keep ldmatrix free of conflicts
+  static constexpr int kHalf = kAttendTile * kRow;  // keys or values of one tile
   static constexpr int kStage = 2 * kHalf;
-  static constexpr int kStages = D > 128 ? 2 : 3;
-  static constexpr int kBytes = kAttendWarps * kStages * kStage;
+  static constexpr int kStages = D > 192 ? 2 : 3;
+  static constexpr int kRing = kAttendWarps * kStages * kStage;
+  static constexpr int kValues = D / 4 * (HB / 8);  // of a head block's output that a lane holds
+  static constexpr int kLevels = attend_levels(D, HB);
+  static constexpr bool kInRegs = D <= 128;
+  static constexpr int kBytes = kRing + (kInRegs ? 0 : kAttendWarps * kLevels * kValues * 32 * 4);
 };
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
@@ -98,26 +108,112 @@ __device__ __forceinline__ void st_pair(uint64_t a, float x, float y, uint64_t l
     *reinterpret_cast<uint32_t*>(a) = Elem<DT>::pack(x, y);
 }
 
+// 2^(x - M) for whole numbers x <= M; 0 below 2^-126, and for x = -inf.
+__device__ __forceinline__ float pow2_diff(float x, float M) {
+  const int k = static_cast<int>(fmaxf(x - M, -127.0f));
+  return __int_as_float((k + 127) << 23);
+}
+
+// A run of tokens: reference, sum and output of a lane's heads.
+template <int NV, int R>
+struct Run {
+  float v[NV];  // [column group][half of the heads][2]
+  float ref[R], l[R];
+};
+
+// b = a + b, a the earlier tokens.
+template <int NV, int R>
+__device__ __forceinline__ void join(const Run<NV, R>& a, Run<NV, R>& b) {
+#pragma unroll
+  for (int h = 0; h < R; ++h) {
+    const float M = fmaxf(a.ref[h], b.ref[h]);
+    const float fa = pow2_diff(a.ref[h], M), fb = pow2_diff(b.ref[h], M);
+    b.ref[h] = M;
+    b.l[h] = __fmaf_rn(a.l[h], fa, b.l[h] * fb);
+#pragma unroll
+    for (int i = h * 2; i < NV; i += 2 * R)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) b.v[i + e] = __fmaf_rn(a.v[i + e], fa, b.v[i + e] * fb);
+  }
+}
+
+// The sum of 16 values as the tree of them.
+template <class F>
+__device__ __forceinline__ float tree16(F x) {
+  float a[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a[i] = x(2 * i) + x(2 * i + 1);
+  return ((a[0] + a[1]) + (a[2] + a[3])) + ((a[4] + a[5]) + (a[6] + a[7]));
+}
+
+// Where a unit's pieces leave their runs: [piece][head][D] outputs, then
+// [piece][head] (reference, sum).
+struct Pieces {
+  float* out;
+  float2* rl;
+  uint64_t lo, hi;  // their bytes
+};
+
+template <int D, int HB>
+__device__ __forceinline__ void st_piece(const Pieces& w, uint32_t piece, int h, int d, const float4& v, float ref,
+                                         float l) {
+  float4* a = reinterpret_cast<float4*>(w.out + (static_cast<uint64_t>(piece) * HB + h) * D + d);
+  if (in_bounds(a, 16, w.lo, w.hi, kSitePartial)) *a = v;
+  if (d == 0) {
+    float2* b = w.rl + static_cast<uint64_t>(piece) * HB + h;
+    if (in_bounds(b, 8, w.lo, w.hi, kSitePartial)) *b = make_float2(ref, l);
+  }
+}
+
+// The finished output of head h (of the CTA's), columns d .. d + 3.
+template <int DT, int D>
+__device__ __forceinline__ void st_result(const AttendParams& p, int seq, int head, int d, const float4& v, float ref,
+                                          float l) {
+  const float inv = 1.0f / l;
+  const uint64_t row = p.out + static_cast<uint64_t>(seq) * p.out_seq + static_cast<uint64_t>(head) * p.out_head;
+  st_pair<DT>(row + d * 2, v.x * inv, v.y * inv, row, row + D * 2);
+  st_pair<DT>(row + d * 2 + 4, v.z * inv, v.w * inv, row, row + D * 2);
+  if (d == 0 && p.lse) {
+    float* a = reinterpret_cast<float*>(p.lse) + static_cast<uint64_t>(seq) * p.q_heads + head;
+    if (in_bounds(a, 4, p.lse, p.lse + 4ull * p.seqs * p.q_heads, kSiteOut)) *a = (ref + log2f(l)) * kLn2;
+  }
+}
+
+// True in every thread of the CTA that arrives last of `n`; the counter is
+// then 0 again, and what the others wrote before arriving is visible.
+__device__ __forceinline__ bool arrive_last(uint32_t* counter, uint32_t n, uint32_t* flag) {
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const bool last = atomicAdd(counter, 1u) == n - 1;
+    if (last) *counter = 0;
+    *flag = last ? 1u : 0u;
+  }
+  __syncthreads();
+  const bool last = *flag != 0;
+  if (last) __threadfence();
+  return last;
+}
+
 template <int DT, int D, int HB>
 __global__ __launch_bounds__(kThreads) void dc_attend_kernel(const __grid_constant__ AttendParams p) {
-  using R = Ring<D>;
-  constexpr int kSteps = D / 16;          // k-steps of q.k, and 16-element column groups of the output
-  constexpr int kVecs = D / 8;            // 16-byte vectors of a token's key
-  constexpr int kCopies = kAttendTile * kVecs / 32;
-  static_assert(kAttendTile * kVecs % 32 == 0, "a tile is whole copies of a warp");
+  using S = Shape<D, HB>;
+  constexpr int R = HB / 8;
+  using State = Run<S::kValues, R>;
+  constexpr int kSteps = D / 16;  // k-steps of q.k, and 16-element column groups of the output
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float w_m[kAttendWarps][HB], w_l[kAttendWarps][HB];
-  __shared__ uint32_t last_piece;
-  int32_t* pages = reinterpret_cast<int32_t*>(smem + R::kBytes);
+  __shared__ float w_ref[kAttendWarps][HB], w_l[kAttendWarps][HB];
+  __shared__ float2 j_rl[kAttendJoin][HB];
+  __shared__ uint32_t last_flag;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 
-  const uint32_t split = blockIdx.x % static_cast<uint32_t>(p.splits);
-  const uint32_t unit = blockIdx.x / static_cast<uint32_t>(p.splits);  // (sequence, key head, head block)
+  const uint32_t piece = blockIdx.x % static_cast<uint32_t>(p.pieces);
+  const uint32_t unit = blockIdx.x / static_cast<uint32_t>(p.pieces);  // (sequence, key head, head block)
   const int hb = static_cast<int>(unit % static_cast<uint32_t>(p.head_blocks));
   const int kh = static_cast<int>(unit / static_cast<uint32_t>(p.head_blocks) % static_cast<uint32_t>(p.kv_heads));
   const int seq = static_cast<int>(unit / static_cast<uint32_t>(p.head_blocks) / static_cast<uint32_t>(p.kv_heads));
-  const int h0 = kh * p.group + hb * HB;                        // first query head
-  const int nh = min(HB, p.group - hb * HB);                    // query heads of this CTA
+  const int h0 = kh * p.group + hb * HB;          // first query head
+  const int nh = min(HB, p.group - hb * HB);      // query heads of this CTA
   pdl_enter();
 
   const int32_t* lp = reinterpret_cast<const int32_t*>(p.lengths) + seq;
@@ -126,16 +222,18 @@ __global__ __launch_bounds__(kThreads) void dc_attend_kernel(const __grid_consta
   const uint64_t room = static_cast<uint64_t>(p.table_width) * p.page_size;
   bool bad = len > 0 && static_cast<uint64_t>(len) > room;
   if (len < 0) len = 0;
-  if (bad) len = static_cast<int32_t>(min(room, static_cast<uint64_t>(1)));
+  if (bad) len = 1;
   const uint32_t start = p.window > 0 && len > p.window ? static_cast<uint32_t>(len - p.window) : 0u;
   const uint32_t n = static_cast<uint32_t>(len) - start;
-  const uint32_t chunk = attend_chunk(n, static_cast<uint32_t>(p.target));
-  const uint32_t pieces = n / chunk + (n % chunk != 0);
-  const uint64_t out_row = p.out + static_cast<uint64_t>(seq) * p.out_seq;
-  if (split >= pieces) {
-    if (split == 0) {  // nothing to attend to: zeros
+  const uint32_t leaf = attend_leaf(n);
+  const uint32_t small = attend_pieces(n, 0);     // pieces of one leaf per warp
+  const uint32_t level = attend_level(small, static_cast<uint32_t>(p.units), S::kLevels);
+  const uint32_t pieces = attend_pieces(n, level);
+  if (piece >= pieces) {
+    if (piece == 0) {  // nothing to attend to: zeros
       for (int i = threadIdx.x; i < nh * (D / 2); i += kThreads) {
-        const uint64_t row = out_row + static_cast<uint64_t>(h0 + i / (D / 2)) * p.out_head;
+        const uint64_t row = p.out + static_cast<uint64_t>(seq) * p.out_seq +
+                             static_cast<uint64_t>(h0 + i / (D / 2)) * p.out_head;
         st_pair<DT>(row + static_cast<uint64_t>(i % (D / 2)) * 4, 0.0f, 0.0f, row, row + D * 2);
       }
       if (p.lse && threadIdx.x < nh) {
@@ -145,28 +243,70 @@ __global__ __launch_bounds__(kThreads) void dc_attend_kernel(const __grid_consta
     }
     return;
   }
-  const uint32_t t0 = start + split * chunk;
-  const uint32_t t1 = min(t0 + chunk, static_cast<uint32_t>(len));
+  // this warp's tokens [t0, t1): a subtree of 2^level leaves
+  const uint32_t run = leaf << level;
+  const uint64_t first = static_cast<uint64_t>(start) + (static_cast<uint64_t>(piece) * kAttendWarps + warp) * run;
+  const uint32_t t0 = static_cast<uint32_t>(min(first, static_cast<uint64_t>(len)));
+  const uint32_t t1 = static_cast<uint32_t>(min(first + run, static_cast<uint64_t>(len)));
+  const uint32_t tiles = (t1 - t0 + kAttendTile - 1) / kAttendTile;
 
-  // the piece's page numbers; a page outside the cache is never touched
-  const uint32_t page0 = t0 / p.page_size, npages = (t1 - 1) / p.page_size - page0 + 1;
-  for (uint32_t i = threadIdx.x; i < npages; i += kThreads) {
-    const int32_t* a = reinterpret_cast<const int32_t*>(p.table) + seq * p.table_stride + page0 + i;
-    const uint64_t hi = p.table + (static_cast<uint64_t>(p.seqs - 1) * p.table_stride + p.table_width) * 4;
-    int32_t id = in_bounds(a, 4, p.table, hi, kSiteTable) ? *a : -1;
-    if (id < 0 || id >= p.num_pages) {
-      id = -1;
-      bad = true;
+  // lanes 0..15 look up where the keys of a tile's tokens are, lanes 16..31
+  // their values; a copy instruction then moves 128 bytes of each of 4 rows (64
+  // of 8 where rows are no multiple of 128 bytes)
+  constexpr int kLanes = D % 64 == 0 ? 8 : 4;       // lanes that copy one row
+  constexpr int kRows = 32 / kLanes;                // rows an instruction touches
+  const uint32_t ring = smem_addr(smem) + static_cast<uint32_t>(warp * S::kStages * S::kStage);
+  const uint64_t table_row = p.table + static_cast<uint64_t>(seq) * static_cast<uint64_t>(p.table_stride) * 4;
+  const uint64_t c_head = (lane < 16 ? p.kc.base : p.vc.base) + static_cast<uint64_t>(kh) * (lane < 16 ? p.kc.head : p.vc.head);
+  const uint64_t c_page = lane < 16 ? p.kc.page : p.vc.page, c_token = lane < 16 ? p.kc.token : p.vc.token;
+  int32_t next_id = -1;    // the page of this lane's token of the next tile to copy, -1: no token
+  uint32_t next_slot = 0;  // ... and its place in the page
+  auto look_up = [&](uint32_t i) {
+    const uint32_t t = t0 + i * kAttendTile + (lane & 15);
+    next_id = -1;
+    if (i < tiles && t < t1) {
+      const uint32_t pg = p.page_shift >= 0 ? t >> p.page_shift : t / p.page_size;
+      next_slot = t - pg * p.page_size;
+      const int32_t* a = reinterpret_cast<const int32_t*>(table_row) + pg;
+      next_id = in_bounds(a, 4, table_row, table_row + 4ull * p.table_width, kSiteTable) ? *a : -1;
+      if (next_id < 0 || next_id >= p.num_pages) {  // a page outside the cache is never touched
+        next_id = -1;
+        bad = true;
+      }
     }
-    pages[i] = id;
-  }
+  };
+  auto issue = [&](uint32_t i) {
+    if (i < tiles) {
+      // (no row starts at 0)
+      const uint64_t row = next_id < 0 ? 0 : c_head + static_cast<uint64_t>(next_id) * c_page +
+                                                 static_cast<uint64_t>(next_slot) * c_token;
+      const uint32_t dst = ring + (i % S::kStages) * S::kStage + (lane / kLanes) * S::kRow + (lane % kLanes) * 16;
+#pragma unroll
+      for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int r = 0; r < kAttendTile / kRows; ++r) {
+          const uint64_t at = __shfl_sync(~0u, row, lane / kLanes + kRows * r + 16 * half);
+          const uint64_t src = (at ? at : half ? p.vc.base : p.kc.base) + (lane % kLanes) * 16;
+#pragma unroll
+          for (int c = 0; c < D / 8 / kLanes; ++c) {
+            const uint64_t x = src + c * kLanes * 16;
+            const bool read = at != 0 && in_bounds(reinterpret_cast<const void*>(x), 16, half ? p.vc.lo : p.kc.lo,
+                                                   half ? p.vc.hi : p.kc.hi, half ? kSiteValue : kSiteKey);
+            cp_async16_or_zero(dst + half * S::kHalf + r * kRows * S::kRow + c * kLanes * 16, x, read);
+          }
+        }
+    }
+    cp_async_commit();
+    look_up(i + 1);
+  };
+  look_up(0);
 
   // query fragments: rows 0..7 heads h0.., rows 8..15 heads h0 + 8.. (HB 16)
-  uint32_t qf[kSteps][HB == 16 ? 4 : 2];
+  uint32_t qf[kSteps][2 * R];
   {
     const int g = lane >> 2;
 #pragma unroll
-    for (int half = 0; half < HB / 8; ++half) {
+    for (int half = 0; half < R; ++half) {
       const int h = g + 8 * half;
       const uint64_t row = p.q + static_cast<uint64_t>(seq) * p.q_seq + static_cast<uint64_t>(h0 + h) * p.q_head;
 #pragma unroll
@@ -176,70 +316,71 @@ __global__ __launch_bounds__(kThreads) void dc_attend_kernel(const __grid_consta
           const uint32_t* a =
               reinterpret_cast<const uint32_t*>(row + static_cast<uint64_t>(k * 16 + i * 8 + (lane & 3) * 2) * 2);
           // a[0]: row g, first 8 columns; a[1]: row g + 8; a[2], a[3]: the next 8 columns
-          qf[k][HB == 16 ? 2 * i + half : i] =
-              h < nh && in_bounds(a, 4, row, row + D * 2, kSiteQuery) ? *a : 0u;
+          qf[k][R * i + half] = h < nh && in_bounds(a, 4, row, row + D * 2, kSiteQuery) ? *a : 0u;
         }
     }
   }
-  bad = __syncthreads_or(bad);
-
-  const uint32_t tiles = (t1 - t0 + kAttendTile - 1) / kAttendTile;
-  const uint32_t mine = tiles > static_cast<uint32_t>(warp) ? (tiles - warp - 1) / kAttendWarps + 1 : 0;
-  const uint32_t ring = smem_addr(smem) + static_cast<uint32_t>(warp * R::kStages * R::kStage);
-
-  // issues the copies of this warp's tile i; lanes 0..15 look up the tokens'
-  // keys, lanes 16..31 their values
-  auto issue = [&](uint32_t i) {
-    if (i < mine) {
-      const uint32_t t = t0 + (i * kAttendWarps + warp) * kAttendTile + (lane & 15);
-      uint64_t row = 0;
-      if (t < t1) {
-        const uint32_t pg = t / p.page_size;
-        const int32_t id = pages[pg - page0];
-        const PagedView& c = lane < 16 ? p.kc : p.vc;
-        if (id >= 0)
-          row = c.base + static_cast<uint64_t>(id) * c.page + static_cast<uint64_t>(t - pg * p.page_size) * c.token +
-                static_cast<uint64_t>(kh) * c.head;
-      }
-      const uint32_t dst = ring + (i % R::kStages) * R::kStage;
 #pragma unroll
-      for (int half = 0; half < 2; ++half)
+  for (int i = 0; i < S::kStages - 1; ++i) issue(i);
+
+  float m[R], l[R], o[D / 8][4];
+  auto clear = [&]() {
 #pragma unroll
-        for (int j = 0; j < kCopies; ++j) {
-          const int v = j * 32 + lane, r = v / kVecs, col = v % kVecs;
-          const uint64_t a = __shfl_sync(~0u, row, r + 16 * half);
-          const uint64_t src = a ? a + col * 16 : (half ? p.vc.base : p.kc.base);
-          const bool read = a != 0 && in_bounds(reinterpret_cast<const void*>(src), 16, half ? p.vc.lo : p.kc.lo,
-                                                half ? p.vc.hi : p.kc.hi, half ? kSiteValue : kSiteKey);
-          cp_async16_or_zero(dst + half * R::kHalf + r * R::kRow + col * 16, src, read);
-        }
+    for (int i = 0; i < R; ++i) {
+      m[i] = neg_inf();
+      l[i] = 0.0f;
     }
-    cp_async_commit();
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[i][j] = 0.0f;
   };
-
-  float m[HB / 8], l[HB / 8], o[D / 8][4];
-#pragma unroll
-  for (int i = 0; i < HB / 8; ++i) {
-    m[i] = neg_inf();
-    l[i] = 0.0f;
-  }
-#pragma unroll
-  for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) o[i][j] = 0.0f;
+  clear();
   const float sc = p.scale * kLog2E;
 
+  // subtrees that wait for their right neighbour: slot b holds 2^b leaves
+  State cur;
+  State held[S::kInRegs ? S::kLevels : 1];
+  float2 held_rl[S::kLevels][R];
+  float* parked = reinterpret_cast<float*>(smem + S::kRing) + warp * S::kLevels * S::kValues * 32 + lane;
+  auto put = [&](int b, const State& x) {
+    if constexpr (S::kInRegs) {
+      held[b] = x;
+    } else {
 #pragma unroll
-  for (int i = 0; i < R::kStages - 1; ++i) issue(i);
-  for (uint32_t i = 0; i < mine; ++i) {
-    issue(i + R::kStages - 1);
-    cp_async_wait<R::kStages - 1>();
+      for (int i = 0; i < S::kValues; ++i) parked[(b * S::kValues + i) * 32] = x.v[i];
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        held_rl[b][i] = make_float2(x.ref[i], x.l[i]);
+      }
+    }
+  };
+  auto add_held = [&](int b) {
+    if constexpr (S::kInRegs) {
+      join(held[b], cur);
+    } else {
+      State x;
+#pragma unroll
+      for (int i = 0; i < S::kValues; ++i) x.v[i] = parked[(b * S::kValues + i) * 32];
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        x.ref[i] = held_rl[b][i].x;
+        x.l[i] = held_rl[b][i].y;
+      }
+      join(x, cur);
+    }
+  };
+
+  const uint32_t leaf_tiles = leaf / kAttendTile;
+  uint32_t in_leaf = 0, leaves = 0;
+  for (uint32_t i = 0; i < tiles; ++i) {
+    cp_async_wait<S::kStages - 2>();
     __syncwarp();
-    const uint32_t kt = ring + (i % R::kStages) * R::kStage, vt = kt + R::kHalf;
-    // scores: 16 heads x 16 tokens
-    float s[2][4] = {};
+    const uint32_t kt = ring + (i % S::kStages) * S::kStage, vt = kt + S::kHalf;
+    // scores: 16 heads x 16 tokens, even and odd k-steps apart
+    float s[2][2][4] = {};
     {
-      const uint32_t a = kt + ((lane >> 4) * 8 + (lane & 7)) * R::kRow + ((lane >> 3) & 1) * 16;
+      const uint32_t a = kt + ((lane >> 4) * 8 + (lane & 7)) * S::kRow + ((lane >> 3) & 1) * 16;
 #pragma unroll
       for (int k = 0; k < kSteps; ++k) {
         uint32_t b[4];
@@ -254,16 +395,20 @@ __global__ __launch_bounds__(kThreads) void dc_attend_kernel(const __grid_consta
           q[2] = qf[k][1];
           q[3] = 0;
         }
-        mma<DT>(s[0], q, b[0], b[1]);
-        mma<DT>(s[1], q, b[2], b[3]);
+        mma<DT>(s[k & 1][0], q, b[0], b[1]);
+        mma<DT>(s[k & 1][1], q, b[2], b[3]);
       }
     }
-    const uint32_t base = t0 + (i * kAttendWarps + warp) * kAttendTile;
+    issue(i + S::kStages - 1);  // (its stage was read in the last round)
+    const uint32_t base = t0 + i * kAttendTile;
     const bool partial = base + kAttendTile > t1;
     uint32_t phi[4], plo[4];
 #pragma unroll
-    for (int half = 0; half < HB / 8; ++half) {
-      float x[4] = {s[0][2 * half] * sc, s[0][2 * half + 1] * sc, s[1][2 * half] * sc, s[1][2 * half + 1] * sc};
+    for (int half = 0; half < R; ++half) {
+      float x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        x[j] = (s[0][j >> 1][2 * half + (j & 1)] + s[1][j >> 1][2 * half + (j & 1)]) * sc;
       if (partial) {
         const uint32_t t = base + (lane & 3) * 2;
         if (t >= t1) x[0] = neg_inf();
@@ -274,9 +419,9 @@ __global__ __launch_bounds__(kThreads) void dc_attend_kernel(const __grid_consta
       float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
       mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2));
-      const float mn = fmaxf(m[half], mx);
-      if (__any_sync(~0u, mn > m[half])) {
-        const float f = m[half] == neg_inf() ? 0.0f : ex2(m[half] - mn);
+      if (__any_sync(~0u, mx > m[half])) {
+        const float mn = fmaxf(m[half], ceilf(mx));
+        const float f = pow2_diff(m[half], mn);
         l[half] *= f;
 #pragma unroll
         for (int c = 0; c < D / 8; ++c) {
@@ -290,7 +435,7 @@ __global__ __launch_bounds__(kThreads) void dc_attend_kernel(const __grid_consta
         }
         m[half] = mn;
       }
-      const float ref = mn == neg_inf() ? 0.0f : mn;
+      const float ref = m[half] == neg_inf() ? 0.0f : m[half];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         x[j] = ex2(x[j] - ref);
@@ -300,7 +445,7 @@ __global__ __launch_bounds__(kThreads) void dc_attend_kernel(const __grid_consta
       split_pair<DT>(x[2], x[3], phi[2 + half], plo[2 + half]);
     }
     {
-      const uint32_t a = vt + (((lane >> 3) & 1) * 8 + (lane & 7)) * R::kRow + (lane >> 4) * 16;
+      const uint32_t a = vt + (((lane >> 3) & 1) * 8 + (lane & 7)) * S::kRow + (lane >> 4) * 16;
       uint32_t w[4];
       if constexpr (HB == 8) {
         w[0] = phi[0];
@@ -324,151 +469,160 @@ __global__ __launch_bounds__(kThreads) void dc_attend_kernel(const __grid_consta
       }
     }
     __syncwarp();
-  }
-  cp_async_wait<0>();
-
-  // the piece: the warps' maxima, sums and outputs joined in warp order
+    if (++in_leaf == leaf_tiles || i + 1 == tiles) {  // a leaf is done: up the tree
+      in_leaf = 0;
 #pragma unroll
-  for (int half = 0; half < HB / 8; ++half) {
-    l[half] += __shfl_xor_sync(~0u, l[half], 1);
-    l[half] += __shfl_xor_sync(~0u, l[half], 2);
-    if ((lane & 3) == 0) {
-      w_m[warp][(lane >> 2) + 8 * half] = m[half];
-      w_l[warp][(lane >> 2) + 8 * half] = l[half];
+      for (int half = 0; half < R; ++half) {
+        l[half] += __shfl_xor_sync(~0u, l[half], 1);
+        l[half] += __shfl_xor_sync(~0u, l[half], 2);
+        cur.ref[half] = m[half];
+        cur.l[half] = l[half];
+      }
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        if constexpr (HB == 16) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) cur.v[4 * c + j] = o[c][j];
+        } else {  // rows 8..15 hold the low parts
+          cur.v[2 * c] = o[c][0] + o[c][2];
+          cur.v[2 * c + 1] = o[c][1] + o[c][3];
+        }
+      }
+      // (at most 2^kLevels leaves; the last one's subtree stays in cur)
+      if (leaves & 1) add_held(0);
+      if constexpr (S::kLevels > 1)
+        if ((leaves & 3) == 3) add_held(1);
+      ++leaves;
+      if (i + 1 < tiles) {
+        if (leaves & 1) put(0, cur);
+        else if constexpr (S::kLevels > 1) put(1, cur);
+        clear();
+      }
     }
   }
-  __syncthreads();  // every warp has read its last tile: the ring is free
+  cp_async_wait<0>();
+  if (tiles == 0) {
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      cur.ref[i] = neg_inf();
+      cur.l[i] = 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < S::kValues; ++i) cur.v[i] = 0.0f;
+  } else if constexpr (S::kLevels > 1) {
+    if (leaves == 3) add_held(1);  // a last leaf without a neighbour
+  }
+
+  // the piece: the warps' subtrees
+  if ((lane & 3) == 0) {
+#pragma unroll
+    for (int half = 0; half < R; ++half) {
+      w_ref[warp][(lane >> 2) + 8 * half] = cur.ref[half];
+      w_l[warp][(lane >> 2) + 8 * half] = cur.l[half];
+    }
+  }
+  bad = __syncthreads_or(bad);  // every warp has read its last tile: the ring is free
   float* wo = reinterpret_cast<float*>(smem);  // [warp][head][D]
-  static_assert(kAttendWarps * HB * D * 4 <= R::kBytes, "the warps' outputs fit in the ring");
+  static_assert(kAttendWarps * HB * D * 4 <= S::kRing, "the warps' outputs fit in the ring");
   {
     const int g = lane >> 2;
 #pragma unroll
-    for (int c = 0; c < D / 8; ++c) {
-      float* a = wo + (warp * HB + g) * D + c * 8 + (lane & 3) * 2;
-      if constexpr (HB == 16) {
-        *reinterpret_cast<float2*>(a) = make_float2(o[c][0], o[c][1]);
-        *reinterpret_cast<float2*>(a + 8 * D) = make_float2(o[c][2], o[c][3]);
-      } else {  // rows 8..15 hold the low parts
-        *reinterpret_cast<float2*>(a) = make_float2(o[c][0] + o[c][2], o[c][1] + o[c][3]);
-      }
-    }
+    for (int c = 0; c < D / 8; ++c)
+#pragma unroll
+      for (int half = 0; half < R; ++half)
+        *reinterpret_cast<float2*>(wo + (warp * HB + g + 8 * half) * D + c * 8 + (lane & 3) * 2) =
+            make_float2(cur.v[c * 2 * R + 2 * half], cur.v[c * 2 * R + 2 * half + 1]);
   }
   __syncthreads();
-  const uint64_t unit_floats = static_cast<uint64_t>(p.splits) * HB * (D + 2);
-  float* part = reinterpret_cast<float*>(p.partial) + unit * unit_floats;
-  const uint64_t part_lo = reinterpret_cast<uint64_t>(part), part_hi = part_lo + unit_floats * 4;
-  float* part_ml = part + static_cast<uint64_t>(p.splits) * HB * D;
+  Pieces w;
+  {
+    const uint64_t floats = static_cast<uint64_t>(p.pieces) * HB * (D + 2);
+    w.out = reinterpret_cast<float*>(p.partial) + unit * floats;
+    w.rl = reinterpret_cast<float2*>(w.out + static_cast<uint64_t>(p.pieces) * HB * D);
+    w.lo = reinterpret_cast<uint64_t>(w.out);
+    w.hi = w.lo + floats * 4;
+  }
   for (int i = threadIdx.x; i < nh * (D / 4); i += kThreads) {
     const int h = i / (D / 4), d = i % (D / 4) * 4;
-    float M = w_m[0][h];
+    float M = w_ref[0][h], f[kAttendWarps];
 #pragma unroll
-    for (int w = 1; w < kAttendWarps; ++w) M = fmaxf(M, w_m[w][h]);
-    float lsum = 0.0f;
-    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int k = 1; k < kAttendWarps; ++k) M = fmaxf(M, w_ref[k][h]);
+    float4 x[kAttendWarps];
+    float ls[kAttendWarps];
 #pragma unroll
-    for (int w = 0; w < kAttendWarps; ++w) {
-      const float f = w_m[w][h] == neg_inf() ? 0.0f : ex2(w_m[w][h] - M);
-      const float4 x = *reinterpret_cast<const float4*>(wo + (w * HB + h) * D + d);
-      lsum = __fmaf_rn(w_l[w][h], f, lsum);
-      acc.x = __fmaf_rn(x.x, f, acc.x);
-      acc.y = __fmaf_rn(x.y, f, acc.y);
-      acc.z = __fmaf_rn(x.z, f, acc.z);
-      acc.w = __fmaf_rn(x.w, f, acc.w);
+    for (int k = 0; k < kAttendWarps; ++k) {
+      f[k] = pow2_diff(w_ref[k][h], M);
+      x[k] = *reinterpret_cast<const float4*>(wo + (k * HB + h) * D + d);
+      ls[k] = w_l[k][h] * f[k];
     }
-    // scores that are all NaN leave no maximum; they and a missing page give NaN
-    if (bad) lsum = __int_as_float(0x7FC00000);
-    if (pieces == 1) {
-      const float inv = 1.0f / lsum;
-      const uint64_t row = out_row + static_cast<uint64_t>(h0 + h) * p.out_head;
-      st_pair<DT>(row + d * 2, acc.x * inv, acc.y * inv, row, row + D * 2);
-      st_pair<DT>(row + d * 2 + 4, acc.z * inv, acc.w * inv, row, row + D * 2);
-      if (d == 0 && p.lse) {
-        float* a = reinterpret_cast<float*>(p.lse) + static_cast<uint64_t>(seq) * p.q_heads + h0 + h;
-        if (in_bounds(a, 4, p.lse, p.lse + 4ull * p.seqs * p.q_heads, kSiteOut)) *a = (M + log2f(lsum)) * kLn2;
-      }
-    } else {
-      float* a = part + (static_cast<uint64_t>(split) * HB + h) * D + d;
-      if (in_bounds(a, 16, part_lo, part_hi, kSitePartial)) *reinterpret_cast<float4*>(a) = acc;
-      if (d == 0) {
-        float* b = part_ml + (static_cast<uint64_t>(split) * HB + h) * 2;
-        if (in_bounds(b, 8, part_lo, part_hi, kSitePartial)) *reinterpret_cast<float2*>(b) = make_float2(M, lsum);
-      }
-    }
+    static_assert(kAttendWarps == 4, "the tree below is of four");
+    float l4 = (ls[0] + ls[1]) + (ls[2] + ls[3]);
+    if (bad) l4 = __int_as_float(0x7FC00000);
+    const float4 v = make_float4((x[0].x * f[0] + x[1].x * f[1]) + (x[2].x * f[2] + x[3].x * f[3]),
+                                 (x[0].y * f[0] + x[1].y * f[1]) + (x[2].y * f[2] + x[3].y * f[3]),
+                                 (x[0].z * f[0] + x[1].z * f[1]) + (x[2].z * f[2] + x[3].z * f[3]),
+                                 (x[0].w * f[0] + x[1].w * f[1]) + (x[2].w * f[2] + x[3].w * f[3]));
+    if (pieces == 1) st_result<DT, D>(p, seq, h0 + h, d, v, M, l4);
+    else st_piece<D, HB>(w, piece, h, d, v, M, l4);
   }
   if (pieces == 1) return;
 
-  // the last piece to arrive joins them all, in order
-  __threadfence();
-  __syncthreads();
-  uint32_t* counter = reinterpret_cast<uint32_t*>(p.counters) + unit;
-  if (threadIdx.x == 0) last_piece = atomicAdd(counter, 1u) == pieces - 1 ? 1u : 0u;
-  __syncthreads();
-  if (!last_piece) return;
-  __threadfence();
-  if (threadIdx.x == 0) *counter = 0;  // ready for the next call
-  float* jw = reinterpret_cast<float*>(smem);  // weights [piece][HB]; then M and 1/L of every head
-  for (int h = warp; h < nh; h += kAttendWarps) {
-    float M = neg_inf();
-    for (uint32_t i = lane; i < pieces; i += 32) M = max_nan(M, __ldcg(part_ml + (i * HB + h) * 2));
+  // the last of 16 neighbouring pieces joins them, the last such group the groups
+  uint32_t* counters = reinterpret_cast<uint32_t*>(p.counters) + static_cast<uint64_t>(unit) * kAttendCounters;
+  const uint32_t groups = (pieces + kAttendJoin - 1) / kAttendJoin;
+  uint32_t base = piece / kAttendJoin * kAttendJoin, step = 1;
+  uint32_t count = min(static_cast<uint32_t>(kAttendJoin), pieces - base);
+  if (!arrive_last(counters + 1 + piece / kAttendJoin, count, &last_flag)) return;
+  while (true) {
+    const bool done = step > 1 || groups == 1;
+    for (uint32_t i = threadIdx.x; i < count * HB; i += kThreads) {
+      const float2* a = w.rl + (static_cast<uint64_t>(base) + i / HB * step) * HB + i % HB;
+      j_rl[i / HB][i % HB] = static_cast<int>(i % HB) < nh && in_bounds(a, 8, w.lo, w.hi, kSitePartial)
+                                 ? __ldcg(a) : make_float2(neg_inf(), 0.0f);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < nh * (D / 4); i += kThreads) {
+      const int h = i / (D / 4), d = i % (D / 4) * 4;
+      float4 x[kAttendJoin];
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) M = max_nan(M, __shfl_xor_sync(~0u, M, x));
-    const float ref = M == neg_inf() ? 0.0f : M;
-    float L = 0.0f;
-    for (uint32_t i = lane; i < pieces; i += 32) {
-      const float2 ml = __ldcg(reinterpret_cast<const float2*>(part_ml + (i * HB + h) * 2));
-      const float f = ex2(ml.x - ref);
-      jw[i * HB + h] = f;
-      L = __fmaf_rn(ml.y, f, L);
-    }
+      for (uint32_t k = 0; k < kAttendJoin; ++k) {
+        const float4* a = reinterpret_cast<const float4*>(w.out + ((static_cast<uint64_t>(base) + k * step) * HB + h) * D + d);
+        x[k] = k < count && in_bounds(a, 16, w.lo, w.hi, kSitePartial) ? __ldcg(a) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      }
+      float M = neg_inf();
+      for (uint32_t k = 0; k < count; ++k) M = fmaxf(M, j_rl[k][h].x);
+      float f[kAttendJoin];
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) L += __shfl_xor_sync(~0u, L, x);
-    if (lane == 0) {
-      w_m[0][h] = M;
-      w_l[0][h] = L;
+      for (uint32_t k = 0; k < kAttendJoin; ++k) f[k] = k < count ? pow2_diff(j_rl[k][h].x, M) : 0.0f;
+      const float l16 = tree16([&](int k) { return k < static_cast<int>(count) ? j_rl[k][h].y * f[k] : 0.0f; });
+      const float4 v = make_float4(tree16([&](int k) { return x[k].x * f[k]; }), tree16([&](int k) { return x[k].y * f[k]; }),
+                                   tree16([&](int k) { return x[k].z * f[k]; }), tree16([&](int k) { return x[k].w * f[k]; }));
+      if (done) st_result<DT, D>(p, seq, h0 + h, d, v, M, l16);
+      else st_piece<D, HB>(w, base, h, d, v, M, l16);
     }
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < nh * (D / 4); i += kThreads) {
-    const int h = i / (D / 4), d = i % (D / 4) * 4;
-    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-    for (uint32_t s = 0; s < pieces; ++s) {
-      const float4* a = reinterpret_cast<const float4*>(part + (static_cast<uint64_t>(s) * HB + h) * D + d);
-      const float4 x = in_bounds(a, 16, part_lo, part_hi, kSitePartial) ? __ldcg(a) : float4{};
-      const float f = jw[s * HB + h];
-      acc.x = __fmaf_rn(x.x, f, acc.x);
-      acc.y = __fmaf_rn(x.y, f, acc.y);
-      acc.z = __fmaf_rn(x.z, f, acc.z);
-      acc.w = __fmaf_rn(x.w, f, acc.w);
-    }
-    const float inv = 1.0f / w_l[0][h];
-    const uint64_t row = out_row + static_cast<uint64_t>(h0 + h) * p.out_head;
-    st_pair<DT>(row + d * 2, acc.x * inv, acc.y * inv, row, row + D * 2);
-    st_pair<DT>(row + d * 2 + 4, acc.z * inv, acc.w * inv, row, row + D * 2);
-    if (d == 0 && p.lse) {
-      float* a = reinterpret_cast<float*>(p.lse) + static_cast<uint64_t>(seq) * p.q_heads + h0 + h;
-      if (in_bounds(a, 4, p.lse, p.lse + 4ull * p.seqs * p.q_heads, kSiteOut)) *a = (w_m[0][h] + log2f(w_l[0][h])) * kLn2;
-    }
+    if (done) return;
+    if (!arrive_last(counters, groups, &last_flag)) return;
+    base = 0;
+    step = kAttendJoin;
+    count = groups;
   }
 }
 
 template <int DT, int D, int HB>
 cudaError_t launch_one(const AttendParams& p, bool pdl, cudaStream_t s, int grid) {
-  constexpr int kMost = Ring<D>::kBytes + (kAttendMaxChunk + 4) * 4;
-  static_assert(kMost + 2048 <= 227 * 1024, "the ring and the page numbers fit");
-  static_assert(kAttendMaxSplits * HB * 4 <= Ring<D>::kBytes, "the pieces' weights fit in the ring");
-  const size_t smem = static_cast<size_t>(Ring<D>::kBytes) + static_cast<size_t>(p.page_slots) * 4;
+  constexpr int kSmem = Shape<D, HB>::kBytes;
+  static_assert(kSmem + 4096 <= 227 * 1024, "the ring and the waiting subtrees fit");
   static std::atomic<uint64_t> allowed{0};  // devices whose limit is set
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (!(allowed.load(std::memory_order_relaxed) & bit)) {
-    e = cudaFuncSetAttribute(dc_attend_kernel<DT, D, HB>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+    e = cudaFuncSetAttribute(dc_attend_kernel<DT, D, HB>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     allowed.fetch_or(bit, std::memory_order_relaxed);
   }
-  return launch_ex(dc_attend_kernel<DT, D, HB>, grid, kThreads, pdl, s, p, smem);
+  return launch_ex(dc_attend_kernel<DT, D, HB>, grid, kThreads, pdl, s, p, kSmem);
 }
 
 template <int DT, int D>
@@ -490,7 +644,7 @@ cudaError_t launch_dim(const AttendParams& p, int dim, bool pdl, cudaStream_t s,
 }  // namespace
 
 cudaError_t launch_attend(const AttendParams& p, int dtype, int dim, bool pdl, cudaStream_t s, int* grid) {
-  *grid = p.seqs * p.kv_heads * p.head_blocks * p.splits;
+  *grid = p.seqs * p.kv_heads * p.head_blocks * p.pieces;
   return dtype == kF16 ? launch_dim<kF16>(p, dim, pdl, s, *grid) : launch_dim<kBF16>(p, dim, pdl, s, *grid);
 }
 

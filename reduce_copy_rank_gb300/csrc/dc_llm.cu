@@ -203,7 +203,8 @@ dc_status_t check_table(const void* p, int64_t rows, int64_t width, int64_t stri
 uint64_t counter_bytes(uint64_t workspace) { return (workspace / 64 + 15) / 16 * 16; }
 
 struct AttendPlan {
-  int head_blocks, hb, target, splits;
+  int head_blocks, hb;
+  uint32_t pieces;         // most pieces that one sequence is cut into
   uint64_t units, partial_bytes;
 };
 
@@ -214,27 +215,28 @@ dc_status_t plan_attend(int64_t seqs, int q_heads, int kv_heads, int dim, uint64
   if (dim != 64 && dim != 96 && dim != 128 && dim != 192 && dim != 256)
     return fail(DC_ERR_INVALID, "head dimension %d is not 64, 96, 128, 192 or 256", dim);
   if (seqs < 0 || seqs > 0x7FFFFFFF) return fail(DC_ERR_INVALID, "%lld sequences", static_cast<long long>(seqs));
+  if (max_tokens > 0x7FFFFFFFull)
+    return fail(DC_ERR_INVALID, "sequences of up to %llu tokens", static_cast<unsigned long long>(max_tokens));
   const int group = q_heads / kv_heads;
   a->hb = attend_head_block(group);
   a->head_blocks = (group + a->hb - 1) / a->hb;
-  a->target = attend_target(kv_heads * a->head_blocks);
-  if (max_tokens > static_cast<uint64_t>(kAttendMaxSplits) * kAttendMaxChunk)
-    return fail(DC_ERR_INVALID, "sequences of up to %llu tokens; at most %d are supported",
-                static_cast<unsigned long long>(max_tokens), kAttendMaxSplits * kAttendMaxChunk);
-  // the pieces of a shorter sequence can outnumber the longest one's: n up to
-  // target x the shortest piece is cut into that many
-  const uint32_t n = static_cast<uint32_t>(max_tokens);
-  const uint32_t knee = static_cast<uint32_t>(a->target) * kAttendMinChunk;
-  const uint32_t most = std::max(attend_splits(n, static_cast<uint32_t>(a->target)),
-                                 attend_splits(std::min(n, knee), static_cast<uint32_t>(a->target)));
-  a->splits = static_cast<int>(std::max(1u, std::max(most, n > knee ? static_cast<uint32_t>(a->target) : 1u)));
   a->units = static_cast<uint64_t>(seqs) * static_cast<uint64_t>(kv_heads) * static_cast<uint64_t>(a->head_blocks);
-  if (a->units * static_cast<uint64_t>(a->splits) > 0x7FFFFFFFull)
-    return fail(DC_ERR_INVALID, "%llu pieces of work exceed a grid",
-                static_cast<unsigned long long>(a->units * static_cast<uint64_t>(a->splits)));
-  a->partial_bytes = a->splits > 1 ? a->units * static_cast<uint64_t>(a->splits) * static_cast<uint64_t>(a->hb) *
-                                         (static_cast<uint64_t>(dim) + 2) * 4
-                                   : 0;
+  if (a->units * kAttendMaxPieces > 0x7FFFFFFFull)
+    return fail(DC_ERR_INVALID, "%llu units of work exceed a grid", static_cast<unsigned long long>(a->units));
+  const uint32_t units = static_cast<uint32_t>(a->units);
+  // the longest sequence has `most` pieces at level 0; a shorter one may be cut finer
+  const uint32_t n = static_cast<uint32_t>(max_tokens);
+  const uint32_t most = n > 512 * 64 ? kAttendMaxPieces : attend_pieces(n, 0);
+  const int levels = attend_levels(dim, a->hb);
+  a->pieces = 1;
+  for (uint32_t s = 1; s <= most; ++s) {
+    const uint32_t k = attend_level(s, units, levels);
+    a->pieces = std::max(a->pieces, (s + (1u << k) - 1) >> k);
+  }
+  // room for this call and for any of fewer units (which may be cut finer)
+  const uint64_t slots = std::max<uint64_t>(
+      a->units * a->pieces, std::min<uint64_t>(a->units * most, static_cast<uint64_t>(kAttendCtas)));
+  a->partial_bytes = most > 1 ? slots * static_cast<uint64_t>(a->hb) * (static_cast<uint64_t>(dim) + 2) * 4 : 0;
   return DC_OK;
 }
 
@@ -478,8 +480,8 @@ dc_status_t dc_paged_attention(const dc_paged_attention_t* a, dc_stream_t stream
   DC_TRY(check_tokens(a->out, "out", n, a->q_heads, a->dim, a->out_seq_stride, a->out_head_stride, 2, out));
   if (a->lse) DC_TRY(take(a->lse, "lse", n * static_cast<uint64_t>(a->q_heads) * 4, 4, out));
   const uint64_t head = counter_bytes(a->workspace_bytes);
-  if (plan.splits > 1) {
-    if (plan.units * 4 > head || head + plan.partial_bytes > a->workspace_bytes)
+  if (plan.partial_bytes) {
+    if (plan.units * kAttendCounters * 4 > head || head + plan.partial_bytes > a->workspace_bytes)
       return fail(DC_ERR_INVALID, "the workspace holds %llu bytes; dc_attention_workspace_bytes says %llu",
                   static_cast<unsigned long long>(a->workspace_bytes),
                   static_cast<unsigned long long>(dc_attention_workspace_bytes(
@@ -510,11 +512,9 @@ dc_status_t dc_paged_attention(const dc_paged_attention_t* a, dc_stream_t stream
   p.group = a->q_heads / a->kv_heads;
   p.head_blocks = plan.head_blocks;
   p.window = a->window;
-  p.target = plan.target;
-  p.splits = plan.splits;
-  const uint32_t chunk = std::min<uint32_t>(attend_chunk(static_cast<uint32_t>(most), static_cast<uint32_t>(plan.target)),
-                                            static_cast<uint32_t>(most));
-  p.page_slots = (std::max(chunk, 1u) - 1) / p.page_size + 2;
+  p.units = static_cast<int32_t>(plan.units);
+  p.pieces = static_cast<int32_t>(plan.pieces);
+  p.page_shift = (p.page_size & (p.page_size - 1)) == 0 ? __builtin_ctz(p.page_size) : -1;
   p.scale = a->scale;
   int grid = 0;
   const cudaError_t e = launch_attend(p, a->dtype, a->dim, pdl_option(), static_cast<cudaStream_t>(stream), &grid);

@@ -106,46 +106,53 @@ cudaError_t launch_append(const AppendParams& p, int dtype, int sms, bool pdl, c
 // --------------------------------------------------------------- attention
 constexpr int kAttendWarps = 4;
 constexpr int kAttendTile = 16;       // tokens a warp takes at a time
-constexpr int kAttendMinChunk = 128;  // tokens of the shortest piece of a sequence
-constexpr int kAttendMaxChunk = 4096; // ... and of the longest
+constexpr int kAttendJoin = 16;       // pieces that one CTA joins at a time
+constexpr int kAttendCounters = 9;    // arrival counters of a unit: its groups', and one per group of pieces
 
 struct AttendParams {
   uint64_t q, q_seq, q_head;            // bytes
   uint64_t out, out_seq, out_head;
   uint64_t lse;                         // f32 [seqs, q_heads] or 0
   uint64_t table, lengths;              // int32
-  uint64_t counters;                    // uint32 [seqs * kv_heads * head blocks], zero between calls
-  uint64_t partial;                     // f32 [seqs * kv_heads * head blocks, splits, HB, dim + 2]
+  uint64_t counters;                    // uint32 [units][kAttendCounters], zero between calls
+  uint64_t partial;                     // f32 [units][pieces][HB][dim + 2]
   int64_t table_stride;
   int64_t num_pages;
   uint32_t page_size, table_width;
   int32_t seqs, q_heads, kv_heads, group, head_blocks;
   int32_t window;
-  int32_t target;                       // pieces a long sequence is cut into
-  int32_t splits;                       // pieces of the longest sequence that the table holds
-  uint32_t page_slots;                  // page numbers one piece may touch
+  int32_t units;                        // seqs * kv_heads * head_blocks
+  int32_t pieces;                       // most pieces of one sequence
+  int32_t page_shift;                   // log2 of the page size, -1 if it is no power of two
   float scale;
   PagedView kc, vc;
 };
 
-// Pieces a sequence of n attended tokens is cut into, and their length: a
-// function of n and of `target` (which the head counts give) alone.
-__host__ __device__ inline uint32_t attend_chunk(uint32_t n, uint32_t target) {
-  const uint32_t per = (n / target + (n % target != 0) + 63u) / 64u * 64u;
-  return per < kAttendMinChunk ? kAttendMinChunk : per > kAttendMaxChunk ? kAttendMaxChunk : per;
+// The tree over a sequence of n attended tokens has leaves of attend_leaf(n)
+// tokens, at most 512 of them; a warp takes 2^level neighbouring leaves and a
+// CTA four neighbouring warps' (a piece).  The leaves are a function of n
+// alone, the level of how much work there is.
+__host__ __device__ inline uint32_t attend_leaf(uint32_t n) {
+  uint32_t leaf = 64;
+  while (n / leaf > 512 || (n / leaf == 512 && n % leaf)) leaf *= 2;
+  return leaf;
 }
-__host__ __device__ inline uint32_t attend_splits(uint32_t n, uint32_t target) {
-  const uint32_t c = attend_chunk(n, target);
-  return n / c + (n % c != 0);
+__host__ __device__ inline uint32_t attend_pieces(uint32_t n, uint32_t level) {
+  const uint32_t leaf = attend_leaf(n), leaves = n / leaf + (n % leaf != 0), per = 4u << level;
+  return (leaves + per - 1) / per;
 }
-// `target` for the units (key heads x head blocks) of one sequence: enough
-// pieces that one long sequence alone fills 304 CTAs, two for each of the
-// GPU's 152 SMs.
-__host__ __device__ inline int attend_target(int units) {
-  const int t = 304 / units;
-  return t < 16 ? 16 : t > 128 ? 128 : t;
+constexpr uint32_t kAttendMaxPieces = 128;  // 512 leaves, one a warp
+// Levels that a warp can hold: waiting subtrees live in registers up to a
+// head size of 128 and in shared memory above.
+__host__ __device__ constexpr int attend_levels(int dim, int hb) { return hb == 8 || dim <= 64 ? 2 : 1; }
+// The level for a sequence of `small` pieces at level 0, if all `units` of the
+// call were like it: the smallest that leaves at most kAttendCtas CTAs.
+constexpr uint32_t kAttendCtas = 608;
+__host__ __device__ inline uint32_t attend_level(uint32_t small, uint32_t units, int levels) {
+  uint32_t k = 0;
+  while (k < static_cast<uint32_t>(levels) && units * ((small + (1u << k) - 1) >> k) > kAttendCtas) ++k;
+  return k;
 }
-constexpr int kAttendMaxSplits = 512; // of the longest sequence (2M tokens)
 // Heads that one CTA serves: 8, or 16 where a key head has more than 8 query heads.
 __host__ __device__ inline int attend_head_block(int group) { return group > 8 ? 16 : 8; }
 cudaError_t launch_attend(const AttendParams& p, int dtype, int dim, bool pdl, cudaStream_t s, int* grid);
