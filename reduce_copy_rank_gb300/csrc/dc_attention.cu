@@ -147,7 +147,8 @@ __device__ __forceinline__ float tree16(F x) {
 }
 
 // Where a unit's pieces leave their runs: [piece][head][D] outputs, then
-// [piece][head] (reference, sum).
+// [piece][head] (reference, sum), then the same of each joined group (whose
+// output replaces its first piece's).
 struct Pieces {
   float* out;
   float2* rl;
@@ -155,12 +156,12 @@ struct Pieces {
 };
 
 template <int D, int HB>
-__device__ __forceinline__ void st_piece(const Pieces& w, uint32_t piece, int h, int d, const float4& v, float ref,
-                                         float l) {
+__device__ __forceinline__ void st_piece(const Pieces& w, uint32_t piece, uint32_t rl, int h, int d, const float4& v,
+                                         float ref, float l) {
   float4* a = reinterpret_cast<float4*>(w.out + (static_cast<uint64_t>(piece) * HB + h) * D + d);
   if (in_bounds(a, 16, w.lo, w.hi, kSitePartial)) *a = v;
   if (d == 0) {
-    float2* b = w.rl + static_cast<uint64_t>(piece) * HB + h;
+    float2* b = w.rl + static_cast<uint64_t>(rl) * HB + h;
     if (in_bounds(b, 8, w.lo, w.hi, kSitePartial)) *b = make_float2(ref, l);
   }
 }
@@ -180,19 +181,20 @@ __device__ __forceinline__ void st_result(const AttendParams& p, int seq, int he
 }
 
 // True in every thread of the CTA that arrives last of `n`; the counter is
-// then 0 again, and what the others wrote before arriving is visible.
+// then 0 again, and what the others wrote before arriving is visible (the
+// barrier orders the CTA's writes before thread 0's release; its acquire and
+// the second barrier order the other CTAs' writes before this CTA's reads,
+// which bypass L1).
 __device__ __forceinline__ bool arrive_last(uint32_t* counter, uint32_t n, uint32_t* flag) {
-  __threadfence();
   __syncthreads();
   if (threadIdx.x == 0) {
-    const bool last = atomicAdd(counter, 1u) == n - 1;
-    if (last) *counter = 0;
-    *flag = last ? 1u : 0u;
+    uint32_t before;
+    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
+    if (before == n - 1) *counter = 0;
+    *flag = before == n - 1 ? 1u : 0u;
   }
   __syncthreads();
-  const bool last = *flag != 0;
-  if (last) __threadfence();
-  return last;
+  return *flag != 0;
 }
 
 template <int DT, int D, int HB>
@@ -203,7 +205,6 @@ __global__ __launch_bounds__(kThreads) void dc_attend_kernel(const __grid_consta
   constexpr int kSteps = D / 16;  // k-steps of q.k, and 16-element column groups of the output
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float w_ref[kAttendWarps][HB], w_l[kAttendWarps][HB];
-  __shared__ float2 j_rl[kAttendJoin][HB];
   __shared__ uint32_t last_flag;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 
@@ -536,7 +537,7 @@ __global__ __launch_bounds__(kThreads) void dc_attend_kernel(const __grid_consta
   __syncthreads();
   Pieces w;
   {
-    const uint64_t floats = static_cast<uint64_t>(p.pieces) * HB * (D + 2);
+    const uint64_t floats = static_cast<uint64_t>(HB) * (static_cast<uint64_t>(p.pieces) * (D + 2) + 2 * kAttendGroups);
     w.out = reinterpret_cast<float*>(p.partial) + unit * floats;
     w.rl = reinterpret_cast<float2*>(w.out + static_cast<uint64_t>(p.pieces) * HB * D);
     w.lo = reinterpret_cast<uint64_t>(w.out);
@@ -563,7 +564,7 @@ __global__ __launch_bounds__(kThreads) void dc_attend_kernel(const __grid_consta
                                  (x[0].z * f[0] + x[1].z * f[1]) + (x[2].z * f[2] + x[3].z * f[3]),
                                  (x[0].w * f[0] + x[1].w * f[1]) + (x[2].w * f[2] + x[3].w * f[3]));
     if (pieces == 1) st_result<DT, D>(p, seq, h0 + h, d, v, M, l4);
-    else st_piece<D, HB>(w, piece, h, d, v, M, l4);
+    else st_piece<D, HB>(w, piece, piece, h, d, v, M, l4);
   }
   if (pieces == 1) return;
 
@@ -575,30 +576,30 @@ __global__ __launch_bounds__(kThreads) void dc_attend_kernel(const __grid_consta
   if (!arrive_last(counters + 1 + piece / kAttendJoin, count, &last_flag)) return;
   while (true) {
     const bool done = step > 1 || groups == 1;
-    for (uint32_t i = threadIdx.x; i < count * HB; i += kThreads) {
-      const float2* a = w.rl + (static_cast<uint64_t>(base) + i / HB * step) * HB + i % HB;
-      j_rl[i / HB][i % HB] = static_cast<int>(i % HB) < nh && in_bounds(a, 8, w.lo, w.hi, kSitePartial)
-                                 ? __ldcg(a) : make_float2(neg_inf(), 0.0f);
-    }
-    __syncthreads();
     for (int i = threadIdx.x; i < nh * (D / 4); i += kThreads) {
       const int h = i / (D / 4), d = i % (D / 4) * 4;
+      // every load is issued before the first is used: one latency
       float4 x[kAttendJoin];
+      float2 rl[kAttendJoin];
 #pragma unroll
       for (uint32_t k = 0; k < kAttendJoin; ++k) {
         const float4* a = reinterpret_cast<const float4*>(w.out + ((static_cast<uint64_t>(base) + k * step) * HB + h) * D + d);
-        x[k] = k < count && in_bounds(a, 16, w.lo, w.hi, kSitePartial) ? __ldcg(a) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        const float2* b = w.rl + (static_cast<uint64_t>(step == 1 ? base : p.pieces) + k) * HB + h;
+        const bool read = k < count && in_bounds(a, 16, w.lo, w.hi, kSitePartial) &&
+                          in_bounds(b, 8, w.lo, w.hi, kSitePartial);
+        x[k] = read ? __ldcg(a) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        rl[k] = read ? __ldcg(b) : make_float2(neg_inf(), 0.0f);
       }
-      float M = neg_inf();
-      for (uint32_t k = 0; k < count; ++k) M = fmaxf(M, j_rl[k][h].x);
-      float f[kAttendJoin];
+      float M = rl[0].x, f[kAttendJoin];
 #pragma unroll
-      for (uint32_t k = 0; k < kAttendJoin; ++k) f[k] = k < count ? pow2_diff(j_rl[k][h].x, M) : 0.0f;
-      const float l16 = tree16([&](int k) { return k < static_cast<int>(count) ? j_rl[k][h].y * f[k] : 0.0f; });
+      for (int k = 1; k < kAttendJoin; ++k) M = fmaxf(M, rl[k].x);
+#pragma unroll
+      for (int k = 0; k < kAttendJoin; ++k) f[k] = pow2_diff(rl[k].x, M);
+      const float l16 = tree16([&](int k) { return rl[k].y * f[k]; });
       const float4 v = make_float4(tree16([&](int k) { return x[k].x * f[k]; }), tree16([&](int k) { return x[k].y * f[k]; }),
                                    tree16([&](int k) { return x[k].z * f[k]; }), tree16([&](int k) { return x[k].w * f[k]; }));
       if (done) st_result<DT, D>(p, seq, h0 + h, d, v, M, l16);
-      else st_piece<D, HB>(w, base, h, d, v, M, l16);
+      else st_piece<D, HB>(w, base, p.pieces + base / kAttendJoin, h, d, v, M, l16);
     }
     if (done) return;
     if (!arrive_last(counters, groups, &last_flag)) return;

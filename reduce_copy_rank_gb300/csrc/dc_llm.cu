@@ -236,7 +236,9 @@ dc_status_t plan_attend(int64_t seqs, int q_heads, int kv_heads, int dim, uint64
   // room for this call and for any of fewer units (which may be cut finer)
   const uint64_t slots = std::max<uint64_t>(
       a->units * a->pieces, std::min<uint64_t>(a->units * most, static_cast<uint64_t>(kAttendCtas)));
-  a->partial_bytes = most > 1 ? slots * static_cast<uint64_t>(a->hb) * (static_cast<uint64_t>(dim) + 2) * 4 : 0;
+  a->partial_bytes = most > 1 ? (slots * (static_cast<uint64_t>(dim) + 2) + a->units * 2 * kAttendGroups) *
+                                    static_cast<uint64_t>(a->hb) * 4
+                              : 0;
   return DC_OK;
 }
 

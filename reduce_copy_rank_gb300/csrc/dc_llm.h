@@ -107,7 +107,8 @@ cudaError_t launch_append(const AppendParams& p, int dtype, int sms, bool pdl, c
 constexpr int kAttendWarps = 4;
 constexpr int kAttendTile = 16;       // tokens a warp takes at a time
 constexpr int kAttendJoin = 16;       // pieces that one CTA joins at a time
-constexpr int kAttendCounters = 9;    // arrival counters of a unit: its groups', and one per group of pieces
+constexpr int kAttendGroups = 8;      // groups of them, at most (128 pieces)
+constexpr int kAttendCounters = 1 + kAttendGroups;  // arrival counters of a unit: of its groups, and of each group's pieces
 
 struct AttendParams {
   uint64_t q, q_seq, q_head;            // bytes
@@ -115,7 +116,7 @@ struct AttendParams {
   uint64_t lse;                         // f32 [seqs, q_heads] or 0
   uint64_t table, lengths;              // int32
   uint64_t counters;                    // uint32 [units][kAttendCounters], zero between calls
-  uint64_t partial;                     // f32 [units][pieces][HB][dim + 2]
+  uint64_t partial;                     // f32 [units][HB * (pieces * (dim + 2) + 2 * kAttendGroups)]
   int64_t table_stride;
   int64_t num_pages;
   uint32_t page_size, table_width;
@@ -141,7 +142,7 @@ __host__ __device__ inline uint32_t attend_pieces(uint32_t n, uint32_t level) {
   const uint32_t leaf = attend_leaf(n), leaves = n / leaf + (n % leaf != 0), per = 4u << level;
   return (leaves + per - 1) / per;
 }
-constexpr uint32_t kAttendMaxPieces = 128;  // 512 leaves, one a warp
+constexpr uint32_t kAttendMaxPieces = kAttendJoin * kAttendGroups;  // 512 leaves, one a warp
 // Levels that a warp can hold: waiting subtrees live in registers up to a
 // head size of 128 and in shared memory above.
 __host__ __device__ constexpr int attend_levels(int dim, int hb) { return hb == 8 || dim <= 64 ? 2 : 1; }

@@ -16,7 +16,8 @@
 // overflow.  All of it in binary32.
 //
 // Bound: memory.  The logits are read once (and the gradient written once);
-// an element costs about eight instructions and one exponential.
+// an element costs about five instructions, one of them
+// the exponential (pairs of elements share the additions and products).
 #include "dc_llm.h"
 #include "dc_numeric.cuh"
 
@@ -91,8 +92,16 @@ __device__ __forceinline__ uint64_t merge_desc(uint64_t a, uint64_t b, int lane)
   const uint64_t r = __shfl_sync(~0u, b, 31 - lane);
   return bitonic_tail(a > r ? a : r, lane);
 }
-// The k-th largest of the lanes' values (k = 1..32).
-__device__ __forceinline__ float kth_of_lanes(float v, int k, int lane) {
+// The same of binary32 values (no NaN among them).
+__device__ __forceinline__ float tail_lanes(float v, int lane) {
+#pragma unroll
+  for (int j = 16; j > 0; j >>= 1) {
+    const float o = __shfl_xor_sync(~0u, v, j);
+    v = (lane & j) == 0 ? fmaxf(v, o) : fminf(v, o);
+  }
+  return v;
+}
+__device__ __forceinline__ float sort_lanes(float v, int lane) {
 #pragma unroll
   for (int size = 2; size <= 32; size <<= 1)
 #pragma unroll
@@ -100,8 +109,13 @@ __device__ __forceinline__ float kth_of_lanes(float v, int k, int lane) {
       const float o = __shfl_xor_sync(~0u, v, j);
       v = (((lane & j) == 0) == ((lane & size) == 0)) ? fmaxf(v, o) : fminf(v, o);
     }
-  return __shfl_sync(~0u, v, k - 1);
+  return v;
 }
+__device__ __forceinline__ float merge_lanes(float a, float b, int lane) {
+  return tail_lanes(fmaxf(a, __shfl_sync(~0u, b, 31 - lane)), lane);
+}
+
+constexpr uint32_t kFewCandidates = 128;  // of a CTA; a warp sorts 32 at a time
 
 struct TopList {
   uint64_t key;    // this lane's entry of the list, largest in lane 0
@@ -125,78 +139,129 @@ __device__ __noinline__ void flush_candidates(TopList& t, uint64_t* buf, int k, 
 }
 
 // --------------------------------------------------------- one segment ---
+// How a segment's entries lie in a warp: 16-bit types as 8 vectors of 8
+// entries a lane, vector j at (j * 32 + lane) * 8; binary32 as 64 single
+// entries, entry j at j * 32 + lane.  (Rows of binary32 logits start at any
+// multiple of 4 bytes: single entries load at full width from all of them.
+// 16-bit rows that do not start at a multiple of 16 bytes read the two blocks
+// around each vector and shift.)  The layout is the same for every alignment
+// and sharding, and with it the order of the additions.
 template <int DT>
 struct SegLoader {
   static constexpr int kPer = Elem<DT>::kPerVec;
-  static constexpr int kVecs = kVocabSeg / kPer / 32;  // 16-byte vectors a lane holds
+  static constexpr int kVecs = kVocabSeg / kPer / 32;  // 16-byte groups a lane holds
 
-  // Lane `lane`'s vectors of segment `seg` of row `row`: vector j holds entries
-  // (seg * kVocabSeg) + (j * 32 + lane) * kPer ...; entries past the vocabulary read -inf.
-  // r: the shard of the previous segment of this warp (segments come in order).
+  // The index in the segment of element i of group j.
+  __device__ static __forceinline__ uint32_t index(int j, int i, int lane) {
+    if constexpr (DT == kF32) return static_cast<uint32_t>((j * 4 + i) * 32 + lane);
+    else return static_cast<uint32_t>((j * 32 + lane) * kPer + i);
+  }
+
+  template <int W>  // byte offset / 4 of the vectors in their 16-byte blocks
+  __device__ static __forceinline__ void load_shifted(const uint4* b, uint32_t bits, uint64_t lo, uint64_t hi,
+                                                      uint4 (&raw)[kVecs]) {
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) {
+      const uint4 x = in_bounds(b + 32 * j, 16, lo, hi, kSiteLogit) ? ld_nc_cached(b + 32 * j) : uint4{};
+      const uint4 y = in_bounds(b + 32 * j + 1, 16, lo, hi, kSiteLogit) ? ld_nc_cached(b + 32 * j + 1) : uint4{};
+      const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+      raw[j] = make_uint4(__funnelshift_r(w[W], w[W + 1], bits), __funnelshift_r(w[W + 1], w[W + 2], bits),
+                          __funnelshift_r(w[W + 2], w[W + 3], bits), __funnelshift_r(w[W + 3], w[W + 4], bits));
+    }
+  }
+
+  // Lane `lane`'s part of segment `seg` of row `row`; entries past the
+  // vocabulary read -inf.  r: the shard of the previous segment of this warp
+  // (segments come in order).
   __device__ static __forceinline__ void load(const ScoreParams& p, uint64_t row, int seg, int lane, int& r,
                                               uint4 (&raw)[kVecs]) {
     const uint32_t e0 = static_cast<uint32_t>(seg) * kVocabSeg;
     while (p.shard[r].end <= e0) ++r;
     const LogitShard& sh = p.shard[r];
-    const uint64_t lo = hull_lo(sh.base);
-    const uint64_t hi =
-        hull_hi(sh.base, (p.rows - 1) * sh.stride + static_cast<uint64_t>(sh.end - sh.first) * Elem<DT>::kBytes);
+    const uint64_t bytes = (p.rows - 1) * sh.stride + static_cast<uint64_t>(sh.end - sh.first) * Elem<DT>::kBytes;
     if (e0 + kVocabSeg <= sh.end) {
-      const uint64_t a = sh.base + row * sh.stride + static_cast<uint64_t>(e0 - sh.first) * Elem<DT>::kBytes +
-                         static_cast<uint64_t>(lane) * 16;
-      const uint32_t s = static_cast<uint32_t>(a & 15u);
-      const uint4* b = reinterpret_cast<const uint4*>(a - s);
-      if (s == 0) {
+      const uint64_t a0 = sh.base + row * sh.stride + static_cast<uint64_t>(e0 - sh.first) * Elem<DT>::kBytes;
+      if constexpr (DT == kF32) {
+        const uint32_t* a = reinterpret_cast<const uint32_t*>(a0) + lane;
+        const uint64_t lo = sh.base, hi = sh.base + bytes;
+        auto get = [&](int k) {
+          uint32_t v = 0;
+          if (in_bounds(a + 32 * k, 4, lo, hi, kSiteLogit))
+            asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v) : "l"(a + 32 * k));
+          return v;
+        };
 #pragma unroll
-        for (int j = 0; j < kVecs; ++j)
-          raw[j] = in_bounds(b + 32 * j, 16, lo, hi, kSiteLogit) ? ld_nc_stream(b + 32 * j) : uint4{};
+        for (int j = 0; j < kVecs; ++j) raw[j] = make_uint4(get(4 * j), get(4 * j + 1), get(4 * j + 2), get(4 * j + 3));
       } else {
+        const uint64_t lo = hull_lo(sh.base), hi = hull_hi(sh.base, bytes);
+        const uint64_t a = a0 + static_cast<uint64_t>(lane) * 16;
+        const uint32_t s = static_cast<uint32_t>(a & 15u), bits = (s & 3u) * 8;
+        const uint4* b = reinterpret_cast<const uint4*>(a - s);
+        if (s == 0) {
 #pragma unroll
-        for (int j = 0; j < kVecs; ++j) {
-          const uint4 x = in_bounds(b + 32 * j, 16, lo, hi, kSiteLogit) ? ld_nc_cached(b + 32 * j) : uint4{};
-          const uint4 y = in_bounds(b + 32 * j + 1, 16, lo, hi, kSiteLogit) ? ld_nc_cached(b + 32 * j + 1) : uint4{};
-          raw[j] = realign16_sel(x, y, s);
+          for (int j = 0; j < kVecs; ++j)
+            raw[j] = in_bounds(b + 32 * j, 16, lo, hi, kSiteLogit) ? ld_nc_stream(b + 32 * j) : uint4{};
+        } else if (s < 8) {
+          if (s < 4) load_shifted<0>(b, bits, lo, hi, raw);
+          else load_shifted<1>(b, bits, lo, hi, raw);
+        } else {
+          if (s < 12) load_shifted<2>(b, bits, lo, hi, raw);
+          else load_shifted<3>(b, bits, lo, hi, raw);
         }
       }
       return;
     }
-    // a segment that crosses shards or ends the vocabulary
+    // a segment that crosses shards or ends the vocabulary: shard by shard,
+    // every load of a shard's part in flight at once
 #pragma unroll
-    for (int j = 0; j < kVecs; ++j) {
-      const uint32_t e = e0 + static_cast<uint32_t>(j * 32 + lane) * kPer;
+    for (int j = 0; j < kVecs; ++j)
       raw[j] = make_uint4(Elem<DT>::kNegInfWord, Elem<DT>::kNegInfWord, Elem<DT>::kNegInfWord, Elem<DT>::kNegInfWord);
-      if (e >= p.vocab) continue;
-      int q = r;
-      while (p.shard[q].end <= e) ++q;
-      uint64_t a = p.shard[q].base + row * p.shard[q].stride +
-                   static_cast<uint64_t>(e - p.shard[q].first) * Elem<DT>::kBytes;
-      if (e + kPer <= p.shard[q].end && (a & 15u) == 0) {
-        const LogitShard& t = p.shard[q];
-        if (in_bounds(reinterpret_cast<const void*>(a), 16, t.base,
-                      t.base + (p.rows - 1) * t.stride + static_cast<uint64_t>(t.end - t.first) * Elem<DT>::kBytes,
-                      kSiteLogit))
-          raw[j] = ld_nc_stream(reinterpret_cast<const uint4*>(a));
-        continue;
-      }
-      uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        if (e + i >= p.vocab) break;
-        while (p.shard[q].end <= e + i) ++q;
-        const LogitShard& t = p.shard[q];
-        a = t.base + row * t.stride + static_cast<uint64_t>(e + i - t.first) * Elem<DT>::kBytes;
-        if (!in_bounds(reinterpret_cast<const void*>(a), Elem<DT>::kBytes, t.base,
-                       t.base + (p.rows - 1) * t.stride + static_cast<uint64_t>(t.end - t.first) * Elem<DT>::kBytes,
-                       kSiteLogit))
-          continue;
+    for (int q = r; q < p.P && p.shard[q].first < e0 + kVocabSeg; ++q) {
+      const LogitShard& t = p.shard[q];
+      const uint32_t from = max(e0, t.first), to = min(e0 + kVocabSeg, t.end);
+      const uint64_t at = t.base + row * t.stride - static_cast<uint64_t>(t.first) * Elem<DT>::kBytes;  // column 0
+      const uint64_t end = t.base + (p.rows - 1) * t.stride + static_cast<uint64_t>(t.end - t.first) * Elem<DT>::kBytes;
+      auto one = [&](uint32_t e, uint32_t& w, bool high) {
+        const uint64_t a = at + static_cast<uint64_t>(e) * Elem<DT>::kBytes;
+        if (!in_bounds(reinterpret_cast<const void*>(a), Elem<DT>::kBytes, t.base, end, kSiteLogit)) return;
         if constexpr (DT == kF32) {
-          w[i] = *reinterpret_cast<const uint32_t*>(a);
+          w = *reinterpret_cast<const uint32_t*>(a);
         } else {
           const uint32_t h = *reinterpret_cast<const uint16_t*>(a);
-          w[i / 2] = (i & 1) ? (w[i / 2] & 0x0000FFFFu) | (h << 16) : (w[i / 2] & 0xFFFF0000u) | h;
+          w = high ? (w & 0x0000FFFFu) | (h << 16) : (w & 0xFFFF0000u) | h;
         }
+      };
+#pragma unroll
+      for (int j = 0; j < kVecs; ++j) {
+        uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+        if constexpr (DT == kF32) {
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) {
+            const uint32_t e = e0 + index(j, i, lane);
+            if (e >= from && e < to) one(e, w[i], false);
+          }
+        } else {
+          const uint32_t e = e0 + index(j, 0, lane);
+          if (e >= from && e + kPer <= to) {
+            const uint64_t a = at + static_cast<uint64_t>(e) * Elem<DT>::kBytes;
+            const uint32_t s = static_cast<uint32_t>(a & 15u);
+            const uint4* b = reinterpret_cast<const uint4*>(a - s);
+            if (in_bounds(b, s ? 32 : 16, hull_lo(t.base), hull_hi(t.base, end - t.base), kSiteLogit)) {
+              uint4 v = ld_nc_cached(b);
+              if (s) v = realign16_sel(v, ld_nc_cached(b + 1), s);
+              w[0] = v.x;
+              w[1] = v.y;
+              w[2] = v.z;
+              w[3] = v.w;
+            }
+          } else if (e < to && e + kPer > from) {  // a vector across a boundary
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+              if (e + i >= from && e + i < to) one(e + i, w[i / 2], i & 1);
+          }
+        }
+        raw[j] = make_uint4(w[0], w[1], w[2], w[3]);
       }
-      raw[j] = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
 };
@@ -218,13 +283,82 @@ __device__ __forceinline__ float pick(const uint4& v, int i) {
   }
 }
 
+// Two binary32 numbers, added and multiplied by one instruction each.
+struct Two {
+  uint64_t v;
+};
+__device__ __forceinline__ Two two(float a, float b) {
+  Two r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void apart(const Two& x, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x.v));
+}
+__device__ __forceinline__ Two add2(const Two& a, const Two& b) {
+  Two r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ Two mul2(const Two& a, const Two& b) {
+  Two r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ Two fma2(const Two& a, const Two& b, const Two& c) {
+  Two r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+
+// s = sum 2^a, t = sum 2^a a over a lane's part of a segment, a = (x - m) c.
+// 16-bit logits are first raised, two at a time, to `floor2` (two copies of a
+// number far enough below m that 2^a is 0 there), so that a masked logit adds
+// 0 and not 0 * -inf; CLAMP does it on every exponent instead.
+template <int DT, bool CLAMP>
+__device__ __forceinline__ void lane_sums(const uint4 (&raw)[SegLoader<DT>::kVecs], float m, float c, uint32_t floor2,
+                                          float& s, float& t) {
+  const Two nm = two(-m, -m), cc = two(c, c);
+  Two s2[2] = {two(0.0f, 0.0f), two(0.0f, 0.0f)}, t2[2] = {two(0.0f, 0.0f), two(0.0f, 0.0f)};
+#pragma unroll
+  for (int j = 0; j < SegLoader<DT>::kVecs; ++j) {
+    uint4 v = raw[j];
+    if constexpr (!CLAMP && DT != kF32)
+      v = make_uint4(Elem<DT>::max2(v.x, floor2), Elem<DT>::max2(v.y, floor2), Elem<DT>::max2(v.z, floor2),
+                     Elem<DT>::max2(v.w, floor2));
+    float x[SegLoader<DT>::kPer];
+    unpack<DT>(v, x);
+#pragma unroll
+    for (int i = 0; i < SegLoader<DT>::kPer; i += 2) {
+      Two a = mul2(add2(two(x[i], x[i + 1]), nm), cc);
+      float a0, a1;
+      apart(a, a0, a1);
+      if constexpr (CLAMP || DT == kF32) {
+        a0 = max_nan(a0, -400.0f);
+        a1 = max_nan(a1, -400.0f);
+        a = two(a0, a1);
+      }
+      const Two e = two(ex2(a0), ex2(a1));
+      s2[(i >> 1) & 1] = add2(s2[(i >> 1) & 1], e);
+      t2[(i >> 1) & 1] = fma2(e, a, t2[(i >> 1) & 1]);
+    }
+  }
+  float a, b, d, e;
+  apart(add2(s2[0], s2[1]), a, b);
+  apart(add2(t2[0], t2[1]), d, e);
+  s = a + b;
+  t = d + e;
+}
+
 template <int DT, bool TOP>
-__global__ __launch_bounds__(kScoreWarps * 32) void dc_score_kernel(const __grid_constant__ ScoreParams p) {
+__global__ __launch_bounds__(kScoreWarps * 32, DT == kF32 ? 2 : TOP ? 3 : 4) void dc_score_kernel(const __grid_constant__ ScoreParams p) {
   using L = SegLoader<DT>;
-  extern __shared__ float part[];  // leader: m, s, t of every segment
+  extern __shared__ float part[];  // leader: m, s, t of every segment; then (TOP) this CTA's segments' m
   __shared__ uint64_t cand[TOP ? kScoreWarps : 1][64];
   __shared__ uint64_t lists[TOP ? kScoreWarps : 1][32];
   __shared__ uint64_t cta_lists[TOP ? kScoreMaxCluster : 1][32];
+  __shared__ float maxima[TOP ? kScoreWarps : 1][32];
+  __shared__ uint32_t cta_count;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t cl = static_cast<uint32_t>(p.cluster);
   const uint64_t row = blockIdx.x / cl;
@@ -250,40 +384,32 @@ __global__ __launch_bounds__(kScoreWarps * 32) void dc_score_kernel(const __grid
 
   const float c = p.inv_t * kLog2E;
   const uint32_t dst = leader_addr(smem_addr(part));
-  TopList top{0, 0, neg_inf()};
+  float thread_max = neg_inf();
+  if (TOP && threadIdx.x == 0) cta_count = 0;
   int r_shard = 0;
   bool waited = cl == 1;
-  const int step = kScoreWarps * static_cast<int>(cl);
-  for (int seg = rank * kScoreWarps + warp; seg < p.nseg; seg += step) {
+  const int seg0 = rank * kScoreWarps + warp, step = kScoreWarps * static_cast<int>(cl);
+  for (int seg = seg0; seg < p.nseg; seg += step) {
     uint4 raw[L::kVecs];
     L::load(p, row, seg, lane, r_shard, raw);
     uint32_t mw = vec_max<DT>(raw[0]);
 #pragma unroll
     for (int j = 1; j < L::kVecs; ++j) mw = Elem<DT>::max2(mw, vec_max<DT>(raw[j]));
     const float lane_max = word_max<DT>(mw);
+    thread_max = fmaxf(thread_max, lane_max);  // (a lane with NaN has no say)
     float m = lane_max;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(~0u, m, o));
-    const bool empty = m == neg_inf();
-    const float r = empty ? 0.0f : m;
-    float s0 = 0.0f, s1 = 0.0f, t0 = 0.0f, t1 = 0.0f;
-#pragma unroll
-    for (int j = 0; j < L::kVecs; ++j) {
-      float x[L::kPer];
-      unpack<DT>(raw[j], x);
-#pragma unroll
-      for (int i = 0; i < L::kPer; i += 2) {
-        // 2^-400 is 0 in binary32; the floor keeps 0 * -inf out of t
-        const float a0 = max_nan((x[i] - r) * c, -400.0f);
-        const float a1 = max_nan((x[i + 1] - r) * c, -400.0f);
-        const float e0 = ex2(a0), e1 = ex2(a1);
-        s0 += e0;
-        s1 += e1;
-        t0 = __fmaf_rn(e0, a0, t0);
-        t1 = __fmaf_rn(e1, a1, t1);
-      }
+    const float ref = m == neg_inf() ? 0.0f : m;
+    float s, t;
+    if constexpr (DT == kF32) {
+      lane_sums<DT, true>(raw, ref, c, 0u, s, t);
+    } else {
+      // 2^-400 is 0 in binary32; the step below the rounded number makes sure that it is low enough
+      const uint32_t floor2 = Elem<DT>::below2(ref - 400.0f / c);
+      if (floor2 != Elem<DT>::kNegInfWord) lane_sums<DT, false>(raw, ref, c, floor2, s, t);
+      else lane_sums<DT, true>(raw, ref, c, 0u, s, t);
     }
-    float s = s0 + s1, t = t0 + t1;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       s += __shfl_xor_sync(~0u, s, o);
@@ -297,49 +423,95 @@ __global__ __launch_bounds__(kScoreWarps * 32) void dc_score_kernel(const __grid
       const float v = lane == 0 ? m : lane == 1 ? s : t;
       st_cluster(dst + static_cast<uint32_t>(seg * 3 + lane) * 4, __float_as_uint(v));
     }
-    if constexpr (TOP) {
-      // k lanes hold a value of at least the k-th largest lane maximum
-      if (m == m) top.thr = fmaxf(top.thr, kth_of_lanes(lane_max, p.top, lane));
-      const uint32_t e0 = static_cast<uint32_t>(seg) * kVocabSeg;
-#pragma unroll
-      for (int j = 0; j < L::kVecs; ++j) {
-        const float vm = word_max<DT>(vec_max<DT>(raw[j]));
-        if (!__any_sync(~0u, !(vm < top.thr))) continue;
-        const uint32_t ev = e0 + static_cast<uint32_t>(j * 32 + lane) * L::kPer;
-        float x[L::kPer];
-        unpack<DT>(raw[j], x);
-        uint32_t mask = 0;
-#pragma unroll
-        for (int i = 0; i < L::kPer; ++i)
-          if (x[i] >= top.thr && ev + i < p.vocab) mask |= 1u << i;
-        while (true) {
-          const uint32_t who = __ballot_sync(~0u, mask != 0);
-          if (who == 0) break;
-          if (mask != 0) {
-            const int i = __ffs(static_cast<int>(mask)) - 1;
-            mask &= mask - 1;
-            cand[warp][top.count + __popc(who & ((1u << lane) - 1u))] =
-                (static_cast<uint64_t>(ordered(pick<DT>(raw[j], i))) << 32) | (0xFFFFFFFFu - (ev + i));
-          }
-          top.count += __popc(who);
-          if (top.count >= 32) flush_candidates(top, cand[warp], p.top, lane);
-        }
-      }
-    }
+    if (TOP && lane == 0) part[3 * p.nseg + seg] = m;
   }
   if (!waited) cluster_wait();
 
   if constexpr (TOP) {
-    if (top.count) flush_candidates(top, cand[warp], p.top, lane);
-    lists[warp][lane] = top.key;
+    // A bound for the k-th largest logit of this CTA's part of the row: the
+    // k-th largest of the threads' maxima, of which k are at least that.  A
+    // second look at the segments that reach it (from L2) then meets little
+    // more than the k entries that are wanted.
+    TopList top{0, 0, neg_inf()};
+    float v = sort_lanes(thread_max, lane);
+    maxima[warp][lane] = v;
     __syncthreads();
 #pragma unroll
     for (int n = kScoreWarps / 2; n > 0; n >>= 1) {
       if (warp < n) {
-        top.key = merge_desc(top.key, lists[warp + n][lane], lane);
-        lists[warp][lane] = top.key;
+        v = merge_lanes(v, maxima[warp + n][lane], lane);
+        maxima[warp][lane] = v;
       }
       __syncthreads();
+    }
+    top.thr = maxima[0][p.top - 1];
+    // push(lanes that have a candidate, this lane's key): keys of the entries
+    // that reach the bound
+    auto scan = [&](auto push) {
+      int r = 0;
+      for (int seg = seg0; seg < p.nseg; seg += step) {
+        if (part[3 * p.nseg + seg] < top.thr) continue;
+        uint4 raw[L::kVecs];
+        L::load(p, row, seg, lane, r, raw);
+        const uint32_t e0 = static_cast<uint32_t>(seg) * kVocabSeg;
+#pragma unroll
+        for (int j = 0; j < L::kVecs; ++j) {
+          if (!__any_sync(~0u, !(word_max<DT>(vec_max<DT>(raw[j])) < top.thr))) continue;
+          float x[L::kPer];
+          unpack<DT>(raw[j], x);
+          uint32_t mask = 0;
+#pragma unroll
+          for (int i = 0; i < L::kPer; ++i)
+            if (x[i] >= top.thr && e0 + L::index(j, i, lane) < p.vocab) mask |= 1u << i;
+          while (true) {
+            const uint32_t who = __ballot_sync(~0u, mask != 0);
+            if (who == 0) break;
+            uint64_t key = 0;
+            if (mask != 0) {
+              const int i = __ffs(static_cast<int>(mask)) - 1;
+              mask &= mask - 1;
+              key = (static_cast<uint64_t>(ordered(pick<DT>(raw[j], i))) << 32) |
+                    (0xFFFFFFFFu - (e0 + L::index(j, i, lane)));
+            }
+            push(who, key);
+          }
+        }
+      }
+    };
+    // most often the CTA's candidates are few: one warp sorts them
+    scan([&](uint32_t who, uint64_t key) {
+      uint32_t at = 0;
+      if (lane == 0) at = atomicAdd(&cta_count, static_cast<uint32_t>(__popc(who)));
+      at = __shfl_sync(~0u, at, 0) + __popc(who & ((1u << lane) - 1u));
+      if (key != 0 && at < kFewCandidates) cand[at / 64][at % 64] = key;
+    });
+    __syncthreads();
+    const uint32_t found = cta_count;
+    if (found <= kFewCandidates) {
+      if (warp == 0)
+        for (uint32_t i = 0; i < found; i += 32) {
+          const uint64_t c32 = sort_desc(i + lane < found ? cand[(i + lane) / 64][(i + lane) % 64] : 0, lane);
+          top.key = i == 0 ? c32 : merge_desc(top.key, c32, lane);
+        }
+    } else {
+      // many logits near or equal to the bound: every warp keeps its own list
+      __syncthreads();
+      scan([&](uint32_t who, uint64_t key) {
+        if (key != 0) cand[warp][top.count + __popc(who & ((1u << lane) - 1u))] = key;
+        top.count += __popc(who);
+        if (top.count >= 32) flush_candidates(top, cand[warp], p.top, lane);
+      });
+      if (top.count) flush_candidates(top, cand[warp], p.top, lane);
+      lists[warp][lane] = top.key;
+      __syncthreads();
+#pragma unroll
+      for (int n = kScoreWarps / 2; n > 0; n >>= 1) {
+        if (warp < n) {
+          top.key = merge_desc(top.key, lists[warp + n][lane], lane);
+          lists[warp][lane] = top.key;
+        }
+        __syncthreads();
+      }
     }
     if (warp == 0) st_cluster64(leader_addr(smem_addr(&cta_lists[rank][lane])), top.key);
   }
@@ -494,7 +666,7 @@ cudaError_t launch_score_t(const ScoreParams& p, int grid, bool pdl, cudaStream_
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(kScoreWarps * 32);
-  cfg.dynamicSmemBytes = static_cast<size_t>(p.nseg) * 12;
+  cfg.dynamicSmemBytes = static_cast<size_t>(p.nseg) * (TOP ? 16 : 12);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   int n = 0;

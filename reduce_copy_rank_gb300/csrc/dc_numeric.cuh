@@ -29,6 +29,14 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
+// The 16-bit number next below the one with bits h, twice in a word; -inf
+// (bits 0x8000 | inf) stays, and so do NaN and +inf, whose sums are NaN anyway.
+__device__ __forceinline__ uint32_t detail_below2(uint32_t h, uint32_t inf) {
+  const uint32_t mag = h & 0x7FFFu;
+  if (mag < inf) h = (h & 0x8000u) ? h + 1 : mag ? h - 1 : 0x8001u;
+  return h | (h << 16);
+}
+
 // Element types: DT is kBF16, kF16 or kF32.
 template <int DT>
 struct Elem;
@@ -49,6 +57,8 @@ struct Elem<kBF16> {
     asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
   }
+  // two copies of a number below x (at most two steps of the type below), -inf if there is none
+  __device__ static __forceinline__ uint32_t below2(float x) { return detail_below2(bits(x), 0x7F80u); }
 };
 
 template <>
@@ -66,6 +76,7 @@ struct Elem<kF16> {
     asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
   }
+  __device__ static __forceinline__ uint32_t below2(float x) { return detail_below2(bits(x), 0x7C00u); }
 };
 
 template <>
