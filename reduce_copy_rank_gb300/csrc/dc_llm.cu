@@ -282,7 +282,8 @@ dc_status_t dc_token_logprobs(const dc_token_logprobs_t* a, dc_stream_t stream) 
   p.rows = n;
   p.inv_t = static_cast<float>(1.0 / a->temperature);
   p.vocab = static_cast<uint32_t>(a->vocab);
-  p.nseg = static_cast<int32_t>((a->vocab + kVocabSeg - 1) / kVocabSeg);
+  const int seg = vocab_seg(a->dtype);
+  p.nseg = static_cast<int32_t>((a->vocab + seg - 1) / seg);
   p.top = a->top;
   p.tokens64 = a->tokens_64 != 0;
   p.top64 = a->top_tokens_64 != 0;

@@ -12,14 +12,15 @@
 namespace dc {
 
 // --------------------------------------------------------- log probabilities
-// The vocabulary is cut into segments of kVocabSeg entries, counted over the
+// The vocabulary is cut into segments of 4 KB of logits, counted over the
 // concatenated shards; one warp reduces one segment, and a row's segments are
 // folded in one fixed order.  The tree of additions therefore depends on the
-// vocabulary alone: not on the rows of the call, the shards or the grid.
-constexpr int kVocabSeg = 2048;
+// vocabulary and its type alone: not on the rows of the call, the shards or
+// the grid.
+__host__ __device__ constexpr int vocab_seg(int dtype) { return dtype == kF32 ? 1024 : 2048; }
 constexpr int kScoreWarps = 8;      // warps per CTA
 constexpr int kScoreMaxCluster = 8; // CTAs that may share a row
-constexpr int kMaxVocab = 1 << 22;  // 24 KB of segment partials
+constexpr int kMaxVocab = 1 << 22;  // at most 4096 segments: 64 KB of partials
 constexpr int kMaxTop = 32;         // alternatives: one lane each
 
 // One rank's columns [first, end) of the vocabulary; row i starts at base + i * stride bytes.

@@ -92,30 +92,16 @@ __device__ __forceinline__ uint64_t merge_desc(uint64_t a, uint64_t b, int lane)
   const uint64_t r = __shfl_sync(~0u, b, 31 - lane);
   return bitonic_tail(a > r ? a : r, lane);
 }
-// The same of binary32 values (no NaN among them).
-__device__ __forceinline__ float tail_lanes(float v, int lane) {
+// Entries of a sorted list of 32 that are larger than `key`.
+__device__ __forceinline__ uint32_t larger_in(const uint64_t* list, uint64_t key) {
+  uint32_t n = 0;
 #pragma unroll
-  for (int j = 16; j > 0; j >>= 1) {
-    const float o = __shfl_xor_sync(~0u, v, j);
-    v = (lane & j) == 0 ? fmaxf(v, o) : fminf(v, o);
-  }
-  return v;
-}
-__device__ __forceinline__ float sort_lanes(float v, int lane) {
-#pragma unroll
-  for (int size = 2; size <= 32; size <<= 1)
-#pragma unroll
-    for (int j = size >> 1; j > 0; j >>= 1) {
-      const float o = __shfl_xor_sync(~0u, v, j);
-      v = (((lane & j) == 0) == ((lane & size) == 0)) ? fmaxf(v, o) : fminf(v, o);
-    }
-  return v;
-}
-__device__ __forceinline__ float merge_lanes(float a, float b, int lane) {
-  return tail_lanes(fmaxf(a, __shfl_sync(~0u, b, 31 - lane)), lane);
+  for (uint32_t s = 16; s > 0; s >>= 1)
+    if (list[n + s - 1] > key) n += s;
+  return n + (list[n] > key ? 1u : 0u);
 }
 
-constexpr uint32_t kFewCandidates = 128;  // of a CTA; a warp sorts 32 at a time
+constexpr uint32_t kFewCandidates = 128;  // of a CTA: a thread each
 
 struct TopList {
   uint64_t key;    // this lane's entry of the list, largest in lane 0
@@ -140,7 +126,7 @@ __device__ __noinline__ void flush_candidates(TopList& t, uint64_t* buf, int k, 
 
 // --------------------------------------------------------- one segment ---
 // How a segment's entries lie in a warp: 16-bit types as 8 vectors of 8
-// entries a lane, vector j at (j * 32 + lane) * 8; binary32 as 64 single
+// entries a lane, vector j at (j * 32 + lane) * 8; binary32 as 32 single
 // entries, entry j at j * 32 + lane.  (Rows of binary32 logits start at any
 // multiple of 4 bytes: single entries load at full width from all of them.
 // 16-bit rows that do not start at a multiple of 16 bytes read the two blocks
@@ -149,7 +135,8 @@ __device__ __noinline__ void flush_candidates(TopList& t, uint64_t* buf, int k, 
 template <int DT>
 struct SegLoader {
   static constexpr int kPer = Elem<DT>::kPerVec;
-  static constexpr int kVecs = kVocabSeg / kPer / 32;  // 16-byte groups a lane holds
+  static constexpr uint32_t kSeg = vocab_seg(DT);
+  static constexpr int kVecs = static_cast<int>(kSeg) / kPer / 32;  // 16-byte groups a lane holds
 
   // The index in the segment of element i of group j.
   __device__ static __forceinline__ uint32_t index(int j, int i, int lane) {
@@ -175,11 +162,11 @@ struct SegLoader {
   // (segments come in order).
   __device__ static __forceinline__ void load(const ScoreParams& p, uint64_t row, int seg, int lane, int& r,
                                               uint4 (&raw)[kVecs]) {
-    const uint32_t e0 = static_cast<uint32_t>(seg) * kVocabSeg;
+    const uint32_t e0 = static_cast<uint32_t>(seg) * kSeg;
     while (p.shard[r].end <= e0) ++r;
     const LogitShard& sh = p.shard[r];
     const uint64_t bytes = (p.rows - 1) * sh.stride + static_cast<uint64_t>(sh.end - sh.first) * Elem<DT>::kBytes;
-    if (e0 + kVocabSeg <= sh.end) {
+    if (e0 + kSeg <= sh.end) {
       const uint64_t a0 = sh.base + row * sh.stride + static_cast<uint64_t>(e0 - sh.first) * Elem<DT>::kBytes;
       if constexpr (DT == kF32) {
         const uint32_t* a = reinterpret_cast<const uint32_t*>(a0) + lane;
@@ -216,9 +203,9 @@ struct SegLoader {
 #pragma unroll
     for (int j = 0; j < kVecs; ++j)
       raw[j] = make_uint4(Elem<DT>::kNegInfWord, Elem<DT>::kNegInfWord, Elem<DT>::kNegInfWord, Elem<DT>::kNegInfWord);
-    for (int q = r; q < p.P && p.shard[q].first < e0 + kVocabSeg; ++q) {
+    for (int q = r; q < p.P && p.shard[q].first < e0 + kSeg; ++q) {
       const LogitShard& t = p.shard[q];
-      const uint32_t from = max(e0, t.first), to = min(e0 + kVocabSeg, t.end);
+      const uint32_t from = max(e0, t.first), to = min(e0 + kSeg, t.end);
       const uint64_t at = t.base + row * t.stride - static_cast<uint64_t>(t.first) * Elem<DT>::kBytes;  // column 0
       const uint64_t end = t.base + (p.rows - 1) * t.stride + static_cast<uint64_t>(t.end - t.first) * Elem<DT>::kBytes;
       auto one = [&](uint32_t e, uint32_t& w, bool high) {
@@ -351,14 +338,16 @@ __device__ __forceinline__ void lane_sums(const uint4 (&raw)[SegLoader<DT>::kVec
 }
 
 template <int DT, bool TOP>
-__global__ __launch_bounds__(kScoreWarps * 32, DT == kF32 ? 2 : TOP ? 3 : 4) void dc_score_kernel(const __grid_constant__ ScoreParams p) {
+__global__ __launch_bounds__(kScoreWarps * 32, 4) void dc_score_kernel(const __grid_constant__ ScoreParams p) {
   using L = SegLoader<DT>;
   extern __shared__ float part[];  // leader: m, s, t of every segment; then (TOP) this CTA's segments' m
   __shared__ uint64_t cand[TOP ? kScoreWarps : 1][64];
   __shared__ uint64_t lists[TOP ? kScoreWarps : 1][32];
   __shared__ uint64_t cta_lists[TOP ? kScoreMaxCluster : 1][32];
-  __shared__ float maxima[TOP ? kScoreWarps : 1][32];
+  __shared__ float4 maxima[TOP ? kScoreWarps * 2 : 1];
+  __shared__ float bound;
   __shared__ uint32_t cta_count;
+  __shared__ float row_m, row_log_s;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t cl = static_cast<uint32_t>(p.cluster);
   const uint64_t row = blockIdx.x / cl;
@@ -389,8 +378,10 @@ __global__ __launch_bounds__(kScoreWarps * 32, DT == kF32 ? 2 : TOP ? 3 : 4) voi
   int r_shard = 0;
   bool waited = cl == 1;
   const int seg0 = rank * kScoreWarps + warp, step = kScoreWarps * static_cast<int>(cl);
+  int last = -1;
+  uint4 raw[L::kVecs];
   for (int seg = seg0; seg < p.nseg; seg += step) {
-    uint4 raw[L::kVecs];
+    last = seg;
     L::load(p, row, seg, lane, r_shard, raw);
     uint32_t mw = vec_max<DT>(raw[0]);
 #pragma unroll
@@ -429,31 +420,38 @@ __global__ __launch_bounds__(kScoreWarps * 32, DT == kF32 ? 2 : TOP ? 3 : 4) voi
 
   if constexpr (TOP) {
     // A bound for the k-th largest logit of this CTA's part of the row: the
-    // k-th largest of the threads' maxima, of which k are at least that.  A
-    // second look at the segments that reach it (from L2) then meets little
-    // more than the k entries that are wanted.
+    // k-th largest of the maxima of 64 groups of 4 threads, of which k are at
+    // least that.  A second look at the segments that reach it (from L2; the
+    // last one is still in registers) then meets little more than the k
+    // entries that are wanted: 20 of 64 groups hold about the 24 largest.
     TopList top{0, 0, neg_inf()};
-    float v = sort_lanes(thread_max, lane);
-    maxima[warp][lane] = v;
+    float v = fmaxf(thread_max, __shfl_xor_sync(~0u, thread_max, 1));
+    v = fmaxf(v, __shfl_xor_sync(~0u, v, 2));
+    if ((lane & 3) == 0) reinterpret_cast<float*>(maxima)[threadIdx.x >> 2] = v;
+    if (threadIdx.x < 32) lists[0][lane] = 0;
     __syncthreads();
+    if (threadIdx.x < 64) {
+      const float mine = reinterpret_cast<const float*>(maxima)[threadIdx.x];
+      int rank = 0;  // groups before this one, equal ones by their number
 #pragma unroll
-    for (int n = kScoreWarps / 2; n > 0; n >>= 1) {
-      if (warp < n) {
-        v = merge_lanes(v, maxima[warp + n][lane], lane);
-        maxima[warp][lane] = v;
+      for (int i = 0; i < 16; ++i) {
+        const float4 q = maxima[i];
+        const int n = static_cast<int>(threadIdx.x) - 4 * i;
+        rank += (q.x > mine || (q.x == mine && n > 0)) + (q.y > mine || (q.y == mine && n > 1)) +
+                (q.z > mine || (q.z == mine && n > 2)) + (q.w > mine || (q.w == mine && n > 3));
       }
-      __syncthreads();
+      if (rank == p.top - 1) bound = mine;
     }
-    top.thr = maxima[0][p.top - 1];
+    __syncthreads();
+    top.thr = bound;
     // push(lanes that have a candidate, this lane's key): keys of the entries
-    // that reach the bound
-    auto scan = [&](auto push) {
-      int r = 0;
-      for (int seg = seg0; seg < p.nseg; seg += step) {
+    // that reach the bound, from the last segment back
+    auto scan = [&](bool loaded, auto push) {
+      for (int seg = last; seg >= seg0 && seg >= 0; seg -= step) {
         if (part[3 * p.nseg + seg] < top.thr) continue;
-        uint4 raw[L::kVecs];
-        L::load(p, row, seg, lane, r, raw);
-        const uint32_t e0 = static_cast<uint32_t>(seg) * kVocabSeg;
+        int r = 0;
+        if (!loaded || seg != last) L::load(p, row, seg, lane, r, raw);
+        const uint32_t e0 = static_cast<uint32_t>(seg) * L::kSeg;
 #pragma unroll
         for (int j = 0; j < L::kVecs; ++j) {
           if (!__any_sync(~0u, !(word_max<DT>(vec_max<DT>(raw[j])) < top.thr))) continue;
@@ -478,8 +476,8 @@ __global__ __launch_bounds__(kScoreWarps * 32, DT == kF32 ? 2 : TOP ? 3 : 4) voi
         }
       }
     };
-    // most often the CTA's candidates are few: one warp sorts them
-    scan([&](uint32_t who, uint64_t key) {
+    // most often the CTA's candidates are few: a thread ranks each of them
+    scan(true, [&](uint32_t who, uint64_t key) {
       uint32_t at = 0;
       if (lane == 0) at = atomicAdd(&cta_count, static_cast<uint32_t>(__popc(who)));
       at = __shfl_sync(~0u, at, 0) + __popc(who & ((1u << lane) - 1u));
@@ -488,15 +486,18 @@ __global__ __launch_bounds__(kScoreWarps * 32, DT == kF32 ? 2 : TOP ? 3 : 4) voi
     __syncthreads();
     const uint32_t found = cta_count;
     if (found <= kFewCandidates) {
-      if (warp == 0)
-        for (uint32_t i = 0; i < found; i += 32) {
-          const uint64_t c32 = sort_desc(i + lane < found ? cand[(i + lane) / 64][(i + lane) % 64] : 0, lane);
-          top.key = i == 0 ? c32 : merge_desc(top.key, c32, lane);
-        }
+      if (threadIdx.x < found) {
+        const uint64_t* all = &cand[0][0];
+        const uint64_t key = all[threadIdx.x];
+        uint32_t rank = 0;
+        for (uint32_t i = 0; i < found; ++i) rank += all[i] > key ? 1u : 0u;  // (keys are distinct)
+        if (rank < 32) lists[0][rank] = key;
+      }
+      __syncthreads();
     } else {
       // many logits near or equal to the bound: every warp keeps its own list
       __syncthreads();
-      scan([&](uint32_t who, uint64_t key) {
+      scan(false, [&](uint32_t who, uint64_t key) {
         if (key != 0) cand[warp][top.count + __popc(who & ((1u << lane) - 1u))] = key;
         top.count += __popc(who);
         if (top.count >= 32) flush_candidates(top, cand[warp], p.top, lane);
@@ -513,7 +514,7 @@ __global__ __launch_bounds__(kScoreWarps * 32, DT == kF32 ? 2 : TOP ? 3 : 4) voi
         __syncthreads();
       }
     }
-    if (warp == 0) st_cluster64(leader_addr(smem_addr(&cta_lists[rank][lane])), top.key);
+    if (warp == 0) st_cluster64(leader_addr(smem_addr(&cta_lists[rank][lane])), lists[0][lane]);
   }
   if (cl > 1) {
     cluster_arrive();
@@ -521,50 +522,68 @@ __global__ __launch_bounds__(kScoreWarps * 32, DT == kF32 ? 2 : TOP ? 3 : 4) voi
   } else {
     __syncthreads();
   }
-  if (rank != 0 || warp != 0) return;
+  if (rank != 0 || (!TOP && warp != 0)) return;
 
   // the row's segments: the largest logit, then lane l folds segments l,
   // l + 32, ... in order and the lanes join in a fixed exchange
-  float M = neg_inf();
-  for (int i = lane; i < p.nseg; i += 32) M = max_nan(M, part[3 * i]);
+  const bool scored = warp == 0;
+  if (scored) {
+    float M = neg_inf();
+    for (int i = lane; i < p.nseg; i += 32) M = max_nan(M, part[3 * i]);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = max_nan(M, __shfl_xor_sync(~0u, M, o));
-  float S = 0.0f, U = 0.0f;
-  for (int i = lane; i < p.nseg; i += 32) {
-    const float mi = part[3 * i];
-    if (mi == neg_inf()) continue;
-    const float d = max_nan((mi - M) * c, -400.0f);
-    const float w = ex2(d), si = part[3 * i + 1];
-    S = __fmaf_rn(si, w, S);
-    U = __fmaf_rn(w, __fmaf_rn(si, d, part[3 * i + 2]), U);
-  }
+    for (int o = 16; o > 0; o >>= 1) M = max_nan(M, __shfl_xor_sync(~0u, M, o));
+    float S = 0.0f, U = 0.0f;
+    for (int i = lane; i < p.nseg; i += 32) {
+      const float mi = part[3 * i];
+      if (mi == neg_inf()) continue;
+      const float d = max_nan((mi - M) * c, -400.0f);
+      const float w = ex2(d), si = part[3 * i + 1];
+      S = __fmaf_rn(si, w, S);
+      U = __fmaf_rn(w, __fmaf_rn(si, d, part[3 * i + 2]), U);
+    }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    S += __shfl_xor_sync(~0u, S, o);
-    U += __shfl_xor_sync(~0u, U, o);
-  }
-  const bool none = M == neg_inf();  // every entry of the row is masked
-  const float log_s = logf(S);
-  if (lane == 0) {
-    float lp;
-    if (token < 0) lp = 0.0f;
-    else if (token >= static_cast<int64_t>(p.vocab)) lp = __int_as_float(0x7FC00000);
-    else if (none) lp = neg_inf();
-    else lp = __fmaf_rn(x_token - M, p.inv_t, -log_s);
-    st_entry<float>(p.logprobs, row, p.rows, lp, kSiteScore);
-    if (p.lse) st_entry<float>(p.lse, row, p.rows, none ? neg_inf() : __fmaf_rn(M, p.inv_t, log_s), kSiteScore);
-    if (p.entropy) st_entry<float>(p.entropy, row, p.rows, none ? 0.0f : log_s - U / S * kLn2, kSiteScore);
+    for (int o = 16; o > 0; o >>= 1) {
+      S += __shfl_xor_sync(~0u, S, o);
+      U += __shfl_xor_sync(~0u, U, o);
+    }
+    const bool none = M == neg_inf();  // every entry of the row is masked
+    const float log_s = logf(S);
+    if (lane == 0) {
+      row_m = M;
+      row_log_s = log_s;
+      float lp;
+      if (token < 0) lp = 0.0f;
+      else if (token >= static_cast<int64_t>(p.vocab)) lp = __int_as_float(0x7FC00000);
+      else if (none) lp = neg_inf();
+      else lp = __fmaf_rn(x_token - M, p.inv_t, -log_s);
+      st_entry<float>(p.logprobs, row, p.rows, lp, kSiteScore);
+      if (p.lse) st_entry<float>(p.lse, row, p.rows, none ? neg_inf() : __fmaf_rn(M, p.inv_t, log_s), kSiteScore);
+      if (p.entropy) st_entry<float>(p.entropy, row, p.rows, none ? 0.0f : log_s - U / S * kLn2, kSiteScore);
+    }
   }
   if constexpr (TOP) {
-    uint64_t key = cta_lists[0][lane];
-    for (int i = 1; i < static_cast<int>(cl); ++i) key = merge_desc(key, cta_lists[i][lane], lane);
-    if (lane < p.top) {
-      const uint64_t at = row * static_cast<uint64_t>(p.top) + lane;
-      const int64_t id = key == 0 ? -1 : static_cast<int64_t>(0xFFFFFFFFu - static_cast<uint32_t>(key));
+    // a key's place among all lists: its place in its own and how many of
+    // each other one are larger
+    static_assert(kScoreMaxCluster * 32 <= kScoreWarps * 32, "a thread per key");
+    uint64_t key = 0;
+    uint32_t place = lane;
+    if (warp < static_cast<int>(cl)) {
+      key = cta_lists[warp][lane];
+      for (int i = 0; i < static_cast<int>(cl); ++i)
+        if (i != warp) place += larger_in(cta_lists[i], key);
+    }
+    const uint32_t filled = __syncthreads_count(key != 0);  // (row_m and row_log_s are visible after this)
+    // places that no number fills: token -1
+    const bool fill = threadIdx.x < static_cast<uint32_t>(p.top) && threadIdx.x >= filled;
+    const float M = row_m;
+    for (int k = 0; k < 2; ++k) {
+      if (k == 0 ? key == 0 || place >= static_cast<uint32_t>(p.top) : !fill) continue;
+      const uint64_t at = row * static_cast<uint64_t>(p.top) + (k == 0 ? place : threadIdx.x);
+      const int64_t id = k == 0 ? static_cast<int64_t>(0xFFFFFFFFu - static_cast<uint32_t>(key)) : -1;
       const float x = from_ordered(static_cast<uint32_t>(key >> 32));
-      float lp = __fmaf_rn(x - M, p.inv_t, -log_s);
-      if (none) lp = neg_inf();
-      if (key == 0) lp = __int_as_float(0x7FC00000);
+      float lp = __fmaf_rn(x - M, p.inv_t, -row_log_s);
+      if (M == neg_inf()) lp = neg_inf();
+      if (k == 1) lp = __int_as_float(0x7FC00000);
       const uint64_t n = p.rows * static_cast<uint64_t>(p.top);
       if (p.top_logprobs) st_entry<float>(p.top_logprobs, at, n, lp, kSiteTop);
       if (p.top_tokens && p.top64) st_entry<int64_t>(p.top_tokens, at, n, id, kSiteTop);
@@ -663,10 +682,15 @@ __global__ __launch_bounds__(kGradThreads) void dc_score_grad_kernel(const __gri
 
 template <int DT, bool TOP>
 cudaError_t launch_score_t(const ScoreParams& p, int grid, bool pdl, cudaStream_t s) {
+  const size_t smem = static_cast<size_t>(p.nseg) * (TOP ? 16 : 12);
+  if (smem > 32 * 1024) {  // vocabularies of millions: more than a CTA may have unasked
+    const cudaError_t e = cudaFuncSetAttribute(dc_score_kernel<DT, TOP>, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(kScoreWarps * 32);
-  cfg.dynamicSmemBytes = static_cast<size_t>(p.nseg) * (TOP ? 16 : 12);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   int n = 0;

@@ -462,3 +462,11 @@ def test_refusals():
     empty = torch.empty(0, 100, device="cuda")
     dc.token_logprobs([empty], tokens[:0], lp[:0])  # no rows: nothing to do
     assert dc.launch_count() == before
+
+
+@pytest.mark.parametrize("dtype,vocab", [("f32", 4 << 20), ("bf16", (4 << 20) - 3)])
+def test_largest_vocabulary(dtype, vocab):
+    x, tokens = logits(2, vocab, DT[dtype])
+    check(score([x], tokens, top=32), x, tokens, top=32)
+    with pytest.raises(dc.DCError):
+        score([torch.empty(1, (4 << 20) + 1, device="cuda", dtype=DT[dtype])], tokens[:1])
