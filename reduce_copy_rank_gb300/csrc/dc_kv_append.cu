@@ -9,8 +9,10 @@
 //
 // Bound: memory (every element is read and written once) for prompts, one
 // launch's latency for single tokens.  A CTA takes one token (or a share of
-// it when there are few): a thread owns one pair position across heads, so
-// its cos and sin stay in registers, and has several heads' loads in flight.
+// it when there are few): a thread owns one position in the head across query,
+// key and value heads, so its cos and sin stay in registers; all its loads are
+// issued before the token's place is looked up, which costs two dependent
+// reads.
 #include "dc_llm.h"
 #include "dc_numeric.cuh"
 
@@ -40,12 +42,48 @@ __device__ __forceinline__ void st_row(const Row& r, int h, uint32_t off, const 
   if (in_bounds(a, 16, r.base, r.base + r.span, site)) st16(a, v);
 }
 
-template <int DT>
-__global__ __launch_bounds__(kAppendThreads) void dc_append_kernel(const __grid_constant__ AppendParams p) {
+template <int DT, bool INTERLEAVED>
+__global__ __launch_bounds__(kAppendThreads, 4) void dc_append_kernel(const __grid_constant__ AppendParams p) {
   constexpr uint32_t kB = Elem<DT>::kBytes;
   constexpr int kPer = Elem<DT>::kPerVec;
+  constexpr int kAngles = INTERLEAVED ? kPer / 2 : kPer;  // of a thread's vector
   pdl_enter();
   const uint64_t token = blockIdx.x;
+  const uint64_t row_bytes = static_cast<uint64_t>(p.dim) * kB;
+  const Row q{p.q + token * p.q_token, p.q_head, (p.q_heads > 0 ? p.q_heads - 1 : 0) * p.q_head + row_bytes};
+  const Row qo{p.qo + token * p.qo_token, p.qo_head, (p.q_heads > 0 ? p.q_heads - 1 : 0) * p.qo_head + row_bytes};
+  const Row k{p.k + token * p.k_token, p.k_head, (p.kv_heads - 1) * p.k_head + row_bytes};
+  const Row v{p.v + token * p.v_token, p.v_head, (p.kv_heads - 1) * p.v_head + row_bytes};
+
+  // units of a head: pairs of vectors (INTERLEAVED: single vectors) that
+  // rotate, then vectors that do not
+  const int turning = INTERLEAVED ? p.rot / kPer : p.rot / (2 * kPer);
+  const int units = turning + (p.dim - p.rot) / kPer;
+  const int per = kAppendThreads / units;  // heads a pass
+  const int unit = static_cast<int>(threadIdx.x) % units, sub = static_cast<int>(threadIdx.x) / units;
+  const int heads = p.q_heads + 2 * p.kv_heads;  // queries, keys, values
+  const bool turns = unit < turning, pair = turns && !INTERLEAVED;
+  const uint32_t off0 = turns ? static_cast<uint32_t>(unit) * 16
+                              : static_cast<uint32_t>(p.rot * kB) + static_cast<uint32_t>(unit - turning) * 16;
+  const uint32_t off1 = off0 + static_cast<uint32_t>(p.rot / 2) * kB;
+  const int step = per * static_cast<int>(gridDim.y);
+  const int first = sub < per ? static_cast<int>(blockIdx.y) * per + sub : heads;
+
+  uint4 a[kHeadsInFlight], b[kHeadsInFlight];
+  auto load = [&](int h0) {
+#pragma unroll
+    for (int i = 0; i < kHeadsInFlight; ++i) {
+      const int h = h0 + i * step;
+      if (h >= heads) break;
+      const bool is_q = h < p.q_heads, is_k = h < p.q_heads + p.kv_heads;
+      const Row src = is_q ? q : is_k ? k : v;
+      const int hh = h - (is_q ? 0 : is_k ? p.q_heads : p.q_heads + p.kv_heads);
+      a[i] = ld_row(src, hh, off0);
+      if (pair) b[i] = ld_row(src, hh, off1);
+    }
+  };
+  load(first);
+
   const int32_t pos = ld_i32(p.positions, token, p.tokens);
   const int32_t seq = ld_i32(p.seqs, token, p.tokens);
   if (pos < 0) return;  // padding: nothing is written for it
@@ -55,104 +93,77 @@ __global__ __launch_bounds__(kAppendThreads) void dc_append_kernel(const __grid_
   ok = ok && col < p.table_width && (p.rot == 0 || static_cast<int64_t>(pos) < p.cos_rows);
   int32_t page = -1;
   if (ok) {
-    const int32_t* a = reinterpret_cast<const int32_t*>(p.table) + seq * p.table_stride + col;
+    const int32_t* t = reinterpret_cast<const int32_t*>(p.table) + seq * p.table_stride + col;
     const uint64_t hi = p.table + (static_cast<uint64_t>(p.num_seqs - 1) * p.table_stride + p.table_width) * 4;
-    if (in_bounds(a, 4, p.table, hi, kSiteTable)) page = *a;
-    ok = page >= 0 && page < p.num_pages;
+    if (in_bounds(t, 4, p.table, hi, kSiteTable)) page = *t;
   }
-  const uint64_t row_bytes = static_cast<uint64_t>(p.dim) * kB;
-  Row q{p.q + token * p.q_token, p.q_head, (p.q_heads > 0 ? p.q_heads - 1 : 0) * p.q_head + row_bytes};
-  Row qo{p.qo + token * p.qo_token, p.qo_head, (p.q_heads > 0 ? p.q_heads - 1 : 0) * p.qo_head + row_bytes};
-  Row k{p.k + token * p.k_token, p.k_head, (p.kv_heads - 1) * p.k_head + row_bytes};
-  Row v{p.v + token * p.v_token, p.v_head, (p.kv_heads - 1) * p.v_head + row_bytes};
-  const int vecs = p.dim / kPer;
+  // the cosines and sines of this thread's elements (of its pairs)
+  float cs[kAngles], sn[kAngles];
+  if (turns && ok) {
+    const uint64_t base = p.cos_sin + static_cast<uint64_t>(pos) * p.rot * 4;
+    const float* c = reinterpret_cast<const float*>(base) + unit * kAngles;
+#pragma unroll
+    for (int i = 0; i < kAngles; ++i) {
+      const bool read = in_bounds(c + i, 4, base, base + p.rot * 4ull, kSiteAngle);
+      cs[i] = read ? __ldg(c + i) : 0.0f;
+      sn[i] = read ? __ldg(c + i + p.rot / 2) : 0.0f;
+    }
+  }
+  ok = ok && page >= 0 && page < p.num_pages;
   if (!ok) {  // the queries of a token that cannot be placed read NaN
-    if (p.q_heads == 0) return;
+    const int vecs = p.dim / kPer;
     const uint32_t w = DT == kF32 ? 0x7FC00000u : DT == kF16 ? 0x7E007E00u : 0x7FC07FC0u;
     for (int u = blockIdx.y * kAppendThreads + threadIdx.x; u < p.q_heads * vecs; u += gridDim.y * kAppendThreads)
       st_row(qo, u / vecs, static_cast<uint32_t>(u % vecs) * 16, make_uint4(w, w, w, w), kSiteOut);
     return;
   }
-  Row kc{p.kc.base + static_cast<uint64_t>(page) * p.kc.page + slot * p.kc.token, p.kc.head,
-         (p.kv_heads - 1) * p.kc.head + row_bytes};
-  Row vc{p.vc.base + static_cast<uint64_t>(page) * p.vc.page + slot * p.vc.token, p.vc.head,
-         (p.kv_heads - 1) * p.vc.head + row_bytes};
-
-  // units of a head: pairs of vectors (or single vectors) that rotate, then vectors that do not
-  const int turning = p.interleaved ? p.rot / kPer : p.rot / (2 * kPer);
-  const int units = turning + (p.dim - p.rot) / kPer;
-  const int per = kAppendThreads / units;  // heads a pass
-  const int unit = static_cast<int>(threadIdx.x) % units, sub = static_cast<int>(threadIdx.x) / units;
-  const int heads = p.q_heads + p.kv_heads;
-  if (sub < per) {
-    const bool turns = unit < turning, pair = turns && !p.interleaved;
-    const uint32_t off0 = turns ? static_cast<uint32_t>(unit) * 16
-                                : static_cast<uint32_t>(p.rot * kB) + static_cast<uint32_t>(unit - turning) * 16;
-    const uint32_t off1 = off0 + static_cast<uint32_t>(p.rot / 2) * kB;
-    // pair: cos and sin of the vector's elements; interleaved: of its pairs
-    float cs[kPer], sn[kPer];
-    if (turns) {
-      const int n = p.interleaved ? kPer / 2 : kPer;
-      const uint64_t base = p.cos_sin + static_cast<uint64_t>(pos) * p.rot * 4;
-      const float* c = reinterpret_cast<const float*>(base) + unit * n;
+  const Row kc{p.kc.base + static_cast<uint64_t>(page) * p.kc.page + slot * p.kc.token, p.kc.head,
+               (p.kv_heads - 1) * p.kc.head + row_bytes};
+  const Row vc{p.vc.base + static_cast<uint64_t>(page) * p.vc.page + slot * p.vc.token, p.vc.head,
+               (p.kv_heads - 1) * p.vc.head + row_bytes};
+  for (int h0 = first; h0 < heads; h0 += step * kHeadsInFlight) {
+    if (h0 != first) load(h0);
 #pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (i < n && in_bounds(c + i, 4, base, base + p.rot * 4ull, kSiteAngle)) {
-          cs[i] = c[i];
-          sn[i] = c[i + p.rot / 2];
-        }
-    }
-    const int step = per * static_cast<int>(gridDim.y);
-    for (int h0 = static_cast<int>(blockIdx.y) * per + sub; h0 < heads; h0 += step * kHeadsInFlight) {
-      uint4 a[kHeadsInFlight], b[kHeadsInFlight];
+    for (int i = 0; i < kHeadsInFlight; ++i) {
+      const int h = h0 + i * step;
+      if (h >= heads) break;
+      const bool is_q = h < p.q_heads, is_k = h < p.q_heads + p.kv_heads;
+      const Row dst = is_q ? qo : is_k ? kc : vc;
+      const int hh = h - (is_q ? 0 : is_k ? p.q_heads : p.q_heads + p.kv_heads);
+      const uint32_t site = is_q ? kSiteOut : kSiteCache;
+      if (turns && is_k) {
+        float x[kPer];
+        unpack<DT>(a[i], x);
+        if constexpr (INTERLEAVED) {
 #pragma unroll
-      for (int i = 0; i < kHeadsInFlight; ++i) {
-        const int h = h0 + i * step;
-        if (h >= heads) break;
-        const Row& src = h < p.q_heads ? q : k;
-        const int hh = h < p.q_heads ? h : h - p.q_heads;
-        a[i] = ld_row(src, hh, off0);
-        if (pair) b[i] = ld_row(src, hh, off1);
-      }
-#pragma unroll
-      for (int i = 0; i < kHeadsInFlight; ++i) {
-        const int h = h0 + i * step;
-        if (h >= heads) break;
-        const bool is_q = h < p.q_heads;
-        const Row& dst = is_q ? qo : kc;
-        const int hh = is_q ? h : h - p.q_heads;
-        if (turns) {
-          float x[kPer], y[kPer];
-          unpack<DT>(a[i], x);
-          if (pair) {
-            unpack<DT>(b[i], y);
-#pragma unroll
-            for (int e = 0; e < kPer; ++e) {
-              const float lo = x[e] * cs[e] - y[e] * sn[e];
-              y[e] = y[e] * cs[e] + x[e] * sn[e];
-              x[e] = lo;
-            }
-            st_row(dst, hh, off1, repack<DT>(y), is_q ? kSiteOut : kSiteCache);
-          } else {
-#pragma unroll
-            for (int e = 0; e < kPer; e += 2) {
-              const float lo = x[e] * cs[e / 2] - x[e + 1] * sn[e / 2];
-              x[e + 1] = x[e + 1] * cs[e / 2] + x[e] * sn[e / 2];
-              x[e] = lo;
-            }
+          for (int e = 0; e < kPer; e += 2) {
+            const float lo = x[e] * cs[e / 2] - x[e + 1] * sn[e / 2];
+            x[e + 1] = x[e + 1] * cs[e / 2] + x[e] * sn[e / 2];
+            x[e] = lo;
           }
-          a[i] = repack<DT>(x);
+        } else {
+          float y[kPer];
+          unpack<DT>(b[i], y);
+#pragma unroll
+          for (int e = 0; e < kPer; ++e) {
+            const float lo = x[e] * cs[e] - y[e] * sn[e];
+            y[e] = y[e] * cs[e] + x[e] * sn[e];
+            x[e] = lo;
+          }
+          b[i] = repack<DT>(y);
         }
-        st_row(dst, hh, off0, a[i], is_q ? kSiteOut : kSiteCache);
+        a[i] = repack<DT>(x);
       }
+      st_row(dst, hh, off0, a[i], site);
+      if (pair) st_row(dst, hh, off1, b[i], site);
     }
   }
-  const int vu = p.kv_heads * vecs;
-  for (int u = blockIdx.y * kAppendThreads + threadIdx.x; u < vu; u += gridDim.y * kAppendThreads) {
-    const int h = u / vecs;
-    const uint32_t off = static_cast<uint32_t>(u % vecs) * 16;
-    st_row(vc, h, off, ld_row(v, h, off), kSiteCache);
-  }
+}
+
+template <int DT>
+cudaError_t launch_t(const cudaLaunchConfig_t& cfg, const AppendParams& p) {
+  return p.interleaved ? cudaLaunchKernelEx(&cfg, dc_append_kernel<DT, true>, p)
+                       : cudaLaunchKernelEx(&cfg, dc_append_kernel<DT, false>, p);
 }
 
 }  // namespace
@@ -160,10 +171,11 @@ __global__ __launch_bounds__(kAppendThreads) void dc_append_kernel(const __grid_
 cudaError_t launch_append(const AppendParams& p, int dtype, int sms, bool pdl, cudaStream_t s, int* grid) {
   // few tokens: several CTAs share one token's heads
   const int per_vec = dtype == kF32 ? 4 : 8;
-  const int units = (p.q_heads + 2 * p.kv_heads) * (p.dim / per_vec);
+  const int units = p.interleaved ? p.dim / per_vec : p.rot / (2 * per_vec) + (p.dim - p.rot) / per_vec;
+  const int per = kAppendThreads / units, heads = p.q_heads + 2 * p.kv_heads;
   int y = 1;
   if (p.tokens < static_cast<uint64_t>(sms)) {
-    const int most = (units + kAppendThreads - 1) / kAppendThreads;
+    const int most = (heads + per - 1) / per;
     const int room = static_cast<int>(2 * static_cast<uint64_t>(sms) / p.tokens);
     y = most < room ? most : room;
   }
@@ -178,9 +190,9 @@ cudaError_t launch_append(const AppendParams& p, int dtype, int sms, bool pdl, c
   cfg.numAttrs = pdl ? 1 : 0;
   *grid = static_cast<int>(p.tokens) * y;
   switch (dtype) {
-    case kF16: return cudaLaunchKernelEx(&cfg, dc_append_kernel<kF16>, p);
-    case kF32: return cudaLaunchKernelEx(&cfg, dc_append_kernel<kF32>, p);
-    default: return cudaLaunchKernelEx(&cfg, dc_append_kernel<kBF16>, p);
+    case kF16: return launch_t<kF16>(cfg, p);
+    case kF32: return launch_t<kF32>(cfg, p);
+    default: return launch_t<kBF16>(cfg, p);
   }
 }
 

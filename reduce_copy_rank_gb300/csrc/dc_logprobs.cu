@@ -593,23 +593,29 @@ __global__ __launch_bounds__(kScoreWarps * 32, 4) void dc_score_kernel(const __g
 }
 
 // ---------------------------------------------------------- the gradient ---
+// What a row's gradient needs: log p_i = x_i / T - lse, rounded once, and
+// d_i = p_i (nh log p_i + ngh), with g added at the token's column.
 struct RowTerms {
-  float inv_t, lse; // log p_i = x_i / T - lse, rounded once
-  float g, h;       // upstream gradients, times 1/T
-  float ghH;        // g + h H
-  int64_t token;    // column of the token in this shard, or out of its range
-  bool zero;        // a row of nothing but masks (-inf or the type's lowest): no gradient
+  float inv_t, lse;
+  float g;         // upstream gradient of the log probability, times 1/T
+  float nh, ngh;   // -h / T and -(g + h H) / T
+  uint32_t token;  // column of the token in this shard, ~0u if it is not here
 };
 
-// (1/T) [ g (1[i=y] - p) - h p (log p + H) ]
-template <int DT>
-__device__ __forceinline__ float grad_of(const RowTerms& t, float x, int64_t col) {
-  // exp(-200) is 0 in binary32; the floor keeps 0 * -inf out
-  const float logp = max_nan(__fmaf_rn(x, t.inv_t, -t.lse), -200.0f);
-  const float p = ex2(logp * kLog2E);
-  float d = -p * __fmaf_rn(t.h, logp, t.ghH);
-  if (col == t.token) d += t.g;
-  return t.zero ? 0.0f : d;
+// Pairs of elements share products and sums.  exp(-200) is 0 in binary32: the
+// floor keeps 0 * -inf out.
+template <int N>
+__device__ __forceinline__ void grad_of(const RowTerms& t, float (&x)[N]) {
+  const Two inv = two(t.inv_t, t.inv_t), nl = two(-t.lse, -t.lse), nh = two(t.nh, t.nh), ngh = two(t.ngh, t.ngh),
+            l2e = two(kLog2E, kLog2E);
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    float a, b;
+    apart(fma2(two(x[i], x[i + 1]), inv, nl), a, b);
+    const Two logp = two(max_nan(a, -200.0f), max_nan(b, -200.0f));
+    apart(mul2(logp, l2e), a, b);
+    apart(mul2(two(ex2(a), ex2(b)), fma2(nh, logp, ngh)), x[i], x[i + 1]);
+  }
 }
 
 template <int DT>
@@ -620,39 +626,18 @@ __global__ __launch_bounds__(kGradThreads) void dc_score_grad_kernel(const __gri
   const uint64_t total = p.rows * p.chunks;
   for (uint64_t item = blockIdx.x; item < total; item += gridDim.x) {
     const uint64_t row = item / p.chunks;
-    const uint32_t chunk = static_cast<uint32_t>(item % p.chunks);
+    const uint32_t chunk = static_cast<uint32_t>(item - row * p.chunks);
     int q = 0;
     while (q + 1 < p.P && p.shard[q + 1].chunk0 <= chunk) ++q;
     const GradShard& sh = p.shard[q];
     const uint32_t k = chunk - sh.chunk0;
-    RowTerms t;
-    const int64_t token = ld_token(p.tokens, row, p.rows, p.tokens64 != 0);
-    const float lse = ld_entry<float>(p.lse, row, p.rows, kSiteRow);
-    t.g = p.grad_logprobs ? ld_entry<float>(p.grad_logprobs, row, p.rows, kSiteRow) * p.inv_t : 0.0f;
-    if (token < 0) t.g = 0.0f;
-    if (token >= static_cast<int64_t>(p.vocab)) t.g = __int_as_float(0x7FC00000);
-    t.h = p.grad_entropy ? ld_entry<float>(p.grad_entropy, row, p.rows, kSiteRow) * p.inv_t : 0.0f;
-    t.ghH = t.g + (p.grad_entropy ? t.h * ld_entry<float>(p.entropy, row, p.rows, kSiteRow) : 0.0f);
-    t.inv_t = p.inv_t;
-    t.lse = lse;
-    t.token = token < 0 ? -1 : token - static_cast<int64_t>(sh.first);
-    t.zero = lse <= -1e30f;
     const uint64_t in = sh.in + row * sh.in_stride, out = sh.out + row * sh.out_stride;
-    // columns of the vocabulary; the rest of the row is padding, whose gradient is 0
-    const uint32_t real = p.vocab <= sh.first ? 0u : min(sh.width, p.vocab - sh.first);
     const uint64_t ilo = hull_lo(in), ihi = hull_hi(in, static_cast<uint64_t>(sh.width) * kB);
     const uint64_t olo = out, ohi = out + static_cast<uint64_t>(sh.width) * kB;
     const uint32_t head = min(sh.width, static_cast<uint32_t>((-out) & 15u) / kB);
     const uint32_t nvec = (sh.width - head) / kPer;
     const uint32_t tail = head + nvec * kPer;
-    if (k == 0) {  // the elements outside the 16-byte vectors
-      uint32_t col = threadIdx.x;
-      if (col >= head) col = tail + (col - head);
-      if (col < sh.width && threadIdx.x < head + kPer &&
-          in_bounds(reinterpret_cast<const void*>(out + col * static_cast<uint64_t>(kB)), kB, olo, ohi, kSiteGradOut))
-        store_elem<DT>(out + col * static_cast<uint64_t>(kB),
-                       col < real ? grad_of<DT>(t, load_elem<DT>(in + col * static_cast<uint64_t>(kB)), col) : 0.0f);
-    }
+    // the logits first: the row's numbers arrive meanwhile
     uint4 raw[kGradVecs];
 #pragma unroll
     for (int j = 0; j < kGradVecs; ++j) {
@@ -664,6 +649,37 @@ __global__ __launch_bounds__(kGradThreads) void dc_score_grad_kernel(const __gri
       if (!in_bounds(b, s ? 32 : 16, ilo, ihi, kSiteGradIn)) continue;
       raw[j] = s == 0 ? ld_stream(b) : realign16_sel(ld_cached(b), ld_cached(b + 1), s);
     }
+    RowTerms t;
+    const int64_t token = ld_token(p.tokens, row, p.rows, p.tokens64 != 0);
+    const float lse = ld_entry<float>(p.lse, row, p.rows, kSiteRow);
+    t.g = p.grad_logprobs ? ld_entry<float>(p.grad_logprobs, row, p.rows, kSiteRow) * p.inv_t : 0.0f;
+    if (token < 0) t.g = 0.0f;
+    if (token >= static_cast<int64_t>(p.vocab)) t.g = __int_as_float(0x7FC00000);
+    const float h = p.grad_entropy ? ld_entry<float>(p.grad_entropy, row, p.rows, kSiteRow) * p.inv_t : 0.0f;
+    t.nh = -h;
+    t.ngh = -(t.g + (p.grad_entropy ? h * ld_entry<float>(p.entropy, row, p.rows, kSiteRow) : 0.0f));
+    t.inv_t = p.inv_t;
+    // a row of nothing but masks (-inf or the type's lowest) has no gradient: p = 0 everywhere
+    const bool none = lse <= -1e30f;
+    t.lse = none ? __int_as_float(0x7F800000) : lse;
+    t.token = !none && token >= static_cast<int64_t>(sh.first) && token < static_cast<int64_t>(sh.first) + sh.width
+                  ? static_cast<uint32_t>(token - static_cast<int64_t>(sh.first)) : ~0u;
+    // columns of the vocabulary; the rest of the row is padding, whose gradient is 0
+    const uint32_t real = p.vocab <= sh.first ? 0u : min(sh.width, p.vocab - sh.first);
+    if (k == 0) {  // the elements outside the 16-byte vectors
+      uint32_t col = threadIdx.x;
+      if (col >= head) col = tail + (col - head);
+      if (col < sh.width && threadIdx.x < head + kPer &&
+          in_bounds(reinterpret_cast<const void*>(out + col * static_cast<uint64_t>(kB)), kB, olo, ohi, kSiteGradOut)) {
+        float x[2] = {0.0f, 0.0f};
+        if (col < real) {
+          x[0] = load_elem<DT>(in + col * static_cast<uint64_t>(kB));
+          grad_of(t, x);
+          if (col == t.token) x[0] += t.g;
+        }
+        store_elem<DT>(out + col * static_cast<uint64_t>(kB), x[0]);
+      }
+    }
 #pragma unroll
     for (int j = 0; j < kGradVecs; ++j) {
       const uint32_t v = k * kGradChunk + j * kGradThreads + threadIdx.x;
@@ -671,8 +687,17 @@ __global__ __launch_bounds__(kGradThreads) void dc_score_grad_kernel(const __gri
       const uint32_t col = head + v * kPer;
       float x[kPer];
       unpack<DT>(raw[j], x);
+      grad_of(t, x);
+      if (t.token - col < kPer) {  // (once a row)
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) x[i] = col + i < real ? grad_of<DT>(t, x[i], col + i) : 0.0f;
+        for (int i = 0; i < kPer; ++i)
+          if (col + i == t.token) x[i] += t.g;
+      }
+      if (col + kPer > real) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+          if (col + i >= real) x[i] = 0.0f;
+      }
       const uint64_t a = out + static_cast<uint64_t>(col) * kB;
       if (in_bounds(reinterpret_cast<const void*>(a), 16, olo, ohi, kSiteGradOut))
         st16(reinterpret_cast<uint4*>(a), repack<DT>(x));
