@@ -21,7 +21,17 @@ namespace {
 
 enum : uint32_t { kSiteTokenInfo = 1, kSiteTable = 2, kSiteIn = 3, kSiteOut = 4, kSiteCache = 5, kSiteAngle = 6 };
 
-constexpr int kHeadsInFlight = 4;
+// CTAs of 128 threads (binary32, whose heads of up to 1024 elements are 256
+// vectors: 256).  Measured on 16-bit heads, heads in flight a thread x CTAs
+// per SM x threads: 8191 tokens, 32 + 8 + 8 heads of 128, rotated by halves:
+// 2 x 10 x 128 36.7 us, 4 x 8 x 128 39.9, 2 x 5 x 256 42.7, 4 x 4 x 256 48.8;
+// 32 + 32 + 32 heads of 80, neighbouring pairs: 45.7, 43.3, 49.3, 53.6.
+template <int DT, bool INTERLEAVED>
+struct Shape {
+  static constexpr int kThreads = DT == kF32 ? 256 : 128;
+  static constexpr int kHeads = INTERLEAVED ? 4 : 2;  // whose loads a thread has in flight
+  static constexpr int kCtas = DT == kF32 ? 4 : INTERLEAVED ? 8 : 10;
+};
 
 __device__ __forceinline__ int32_t ld_i32(uint64_t base, uint64_t i, uint64_t n) {
   const int32_t* a = reinterpret_cast<const int32_t*>(base) + i;
@@ -43,7 +53,10 @@ __device__ __forceinline__ void st_row(const Row& r, int h, uint32_t off, const 
 }
 
 template <int DT, bool INTERLEAVED>
-__global__ __launch_bounds__(kAppendThreads, 4) void dc_append_kernel(const __grid_constant__ AppendParams p) {
+__global__ __launch_bounds__(Shape<DT, INTERLEAVED>::kThreads, Shape<DT, INTERLEAVED>::kCtas) void dc_append_kernel(
+    const __grid_constant__ AppendParams p) {
+  constexpr int kHeadsInFlight = Shape<DT, INTERLEAVED>::kHeads;
+  constexpr int kThreads = Shape<DT, INTERLEAVED>::kThreads;
   constexpr uint32_t kB = Elem<DT>::kBytes;
   constexpr int kPer = Elem<DT>::kPerVec;
   constexpr int kAngles = INTERLEAVED ? kPer / 2 : kPer;  // of a thread's vector
@@ -59,7 +72,7 @@ __global__ __launch_bounds__(kAppendThreads, 4) void dc_append_kernel(const __gr
   // rotate, then vectors that do not
   const int turning = INTERLEAVED ? p.rot / kPer : p.rot / (2 * kPer);
   const int units = turning + (p.dim - p.rot) / kPer;
-  const int per = kAppendThreads / units;  // heads a pass
+  const int per = kThreads / units;  // heads a pass
   const int unit = static_cast<int>(threadIdx.x) % units, sub = static_cast<int>(threadIdx.x) / units;
   const int heads = p.q_heads + 2 * p.kv_heads;  // queries, keys, values
   const bool turns = unit < turning, pair = turns && !INTERLEAVED;
@@ -113,7 +126,7 @@ __global__ __launch_bounds__(kAppendThreads, 4) void dc_append_kernel(const __gr
   if (!ok) {  // the queries of a token that cannot be placed read NaN
     const int vecs = p.dim / kPer;
     const uint32_t w = DT == kF32 ? 0x7FC00000u : DT == kF16 ? 0x7E007E00u : 0x7FC07FC0u;
-    for (int u = blockIdx.y * kAppendThreads + threadIdx.x; u < p.q_heads * vecs; u += gridDim.y * kAppendThreads)
+    for (int u = blockIdx.y * kThreads + threadIdx.x; u < p.q_heads * vecs; u += gridDim.y * kThreads)
       st_row(qo, u / vecs, static_cast<uint32_t>(u % vecs) * 16, make_uint4(w, w, w, w), kSiteOut);
     return;
   }
@@ -160,28 +173,21 @@ __global__ __launch_bounds__(kAppendThreads, 4) void dc_append_kernel(const __gr
   }
 }
 
-template <int DT>
-cudaError_t launch_t(const cudaLaunchConfig_t& cfg, const AppendParams& p) {
-  return p.interleaved ? cudaLaunchKernelEx(&cfg, dc_append_kernel<DT, true>, p)
-                       : cudaLaunchKernelEx(&cfg, dc_append_kernel<DT, false>, p);
-}
-
-}  // namespace
-
-cudaError_t launch_append(const AppendParams& p, int dtype, int sms, bool pdl, cudaStream_t s, int* grid) {
+template <int DT, bool INTERLEAVED>
+cudaError_t launch_t(const AppendParams& p, int sms, bool pdl, cudaStream_t s, int* grid) {
+  constexpr int kPer = Elem<DT>::kPerVec, kThreads = Shape<DT, INTERLEAVED>::kThreads;
   // few tokens: several CTAs share one token's heads
-  const int per_vec = dtype == kF32 ? 4 : 8;
-  const int units = p.interleaved ? p.dim / per_vec : p.rot / (2 * per_vec) + (p.dim - p.rot) / per_vec;
-  const int per = kAppendThreads / units, heads = p.q_heads + 2 * p.kv_heads;
+  const int units = INTERLEAVED ? p.dim / kPer : p.rot / (2 * kPer) + (p.dim - p.rot) / kPer;
+  const int per = kThreads / units, heads = p.q_heads + 2 * p.kv_heads;
   int y = 1;
-  if (p.tokens < static_cast<uint64_t>(sms)) {
+  if (p.tokens < 2 * static_cast<uint64_t>(sms)) {
     const int most = (heads + per - 1) / per;
-    const int room = static_cast<int>(2 * static_cast<uint64_t>(sms) / p.tokens);
+    const int room = static_cast<int>(4 * static_cast<uint64_t>(sms) / p.tokens);
     y = most < room ? most : room;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.tokens), static_cast<unsigned>(y));
-  cfg.blockDim = dim3(kAppendThreads);
+  cfg.blockDim = dim3(kThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -189,10 +195,21 @@ cudaError_t launch_append(const AppendParams& p, int dtype, int sms, bool pdl, c
   cfg.attrs = pdl ? attr : nullptr;
   cfg.numAttrs = pdl ? 1 : 0;
   *grid = static_cast<int>(p.tokens) * y;
+  return cudaLaunchKernelEx(&cfg, dc_append_kernel<DT, INTERLEAVED>, p);
+}
+
+template <int DT>
+cudaError_t launch_dt(const AppendParams& p, int sms, bool pdl, cudaStream_t s, int* grid) {
+  return p.interleaved ? launch_t<DT, true>(p, sms, pdl, s, grid) : launch_t<DT, false>(p, sms, pdl, s, grid);
+}
+
+}  // namespace
+
+cudaError_t launch_append(const AppendParams& p, int dtype, int sms, bool pdl, cudaStream_t s, int* grid) {
   switch (dtype) {
-    case kF16: return launch_t<kF16>(cfg, p);
-    case kF32: return launch_t<kF32>(cfg, p);
-    default: return launch_t<kBF16>(cfg, p);
+    case kF16: return launch_dt<kF16>(p, sms, pdl, s, grid);
+    case kF32: return launch_dt<kF32>(p, sms, pdl, s, grid);
+    default: return launch_dt<kBF16>(p, sms, pdl, s, grid);
   }
 }
 

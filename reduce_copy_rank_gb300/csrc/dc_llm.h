@@ -86,7 +86,6 @@ struct PagedView {
   uint64_t lo, hi;  // the bytes it spans
 };
 
-constexpr int kAppendThreads = 256;
 struct AppendParams {
   uint64_t q, q_token, q_head;          // bytes; 0 if no queries
   uint64_t qo, qo_token, qo_head;

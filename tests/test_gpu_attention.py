@@ -296,7 +296,7 @@ def rotated(x, cs, rot, interleaved):
 @pytest.mark.parametrize("tokens,hq,hk,d,rot,interleaved,page", [
     (1, 8, 1, 128, 128, False, 16), (7, 4, 4, 64, 32, False, 1), (33, 32, 8, 128, 128, True, 64), (300, 6, 2, 80, 32, True, 24),
     (5, 0, 3, 8, 0, False, 16), (513, 16, 16, 96, 96, False, 16), (64, 3, 1, 256, 64, False, 128), (2, 1, 1, 1024, 1024, False, 2),
-    (2, 64, 8, 16, 16, True, 5)])
+    (2, 64, 8, 16, 16, True, 5), (3, 2, 1, 1024, 0, False, 4), (9, 1, 2, 1024, 512, True, 4)])
 def test_append(dtype, tokens, hq, hk, d, rot, interleaved, page):
     dt = DT[dtype]
     g = torch.Generator(device="cuda").manual_seed(tokens)
