@@ -12,7 +12,6 @@ from __future__ import annotations
 
 import array
 import ctypes
-import math
 import struct
 from typing import Sequence
 
@@ -107,76 +106,102 @@ def dc_attention_workspace_bytes(seqs: int, q_heads: int, kv_heads: int, dim: in
 
 
 # ------------------------------------------------------------ tensor checks ---
+# A small call's time is mostly these checks, so each reads a tensor's
+# properties once, and words its refusal only when one of them is wrong.
+# (get_device() is -1 for a tensor that is on no GPU.)
 
-def _on_device(t, what: str, dev: int) -> None:
+def _refuse_device(t, what: str, dev: int) -> None:
     if not t.is_cuda:
         raise ValueError(f"{what} must be a CUDA tensor (got device {t.device})")
-    if t.get_device() != dev:
-        _dc._wrong_device(what, t, dev)
+    _dc._wrong_device(what, t, dev)
+
+
+def _refuse_dtype(t, what: str, dtypes) -> None:
+    raise ValueError(f"{what} has dtype {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
 
 
 def _vector(t, what: str, n: int, dtypes, dev: int) -> int:
     """The data pointer of a contiguous [n] tensor of one of `dtypes`."""
-    if not t.is_cuda or t.get_device() != dev:
-        _on_device(t, what, dev)
+    if t.get_device() != dev:
+        _refuse_device(t, what, dev)
     if t.dtype not in dtypes:
-        raise ValueError(f"{what} has dtype {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
-    if t.dim() != 1 or t.shape[0] != n:
+        _refuse_dtype(t, what, dtypes)
+    if t.shape != (n,):
         raise ValueError(f"{what} has shape {tuple(t.shape)}, expected ({n},)")
     if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
     return t.data_ptr()
 
 
-_types = None
+class _Torch:
+    """What the checks use of torch, looked up once."""
 
-
-def _T():
-    """torch's element types that the operators take."""
-    global _types
-    if _types is None:
+    def __init__(self):
         import torch
 
-        class _types:  # noqa: N801
-            f32 = (torch.float32,)
-            i32 = (torch.int32,)
-            index = (torch.int64, torch.int32)
-            i64 = torch.int64
-            code = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
-    return _types
+        self.f32 = (torch.float32,)
+        self.i32 = (torch.int32,)
+        self.index = (torch.int64, torch.int32)
+        self.i64 = torch.int64
+        self.code = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+        C = torch._C
+        self.device = getattr(C, "_cuda_getDevice", None) or torch.cuda.current_device
+        raw = getattr(C, "_cuda_getCurrentRawStream", None)
+        self.stream = raw or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+_torch = None
+
+
+def _T() -> _Torch:
+    global _torch
+    if _torch is None:
+        _torch = _Torch()
+    return _torch
+
+
+def _current(t, T: _Torch) -> int:
+    """The current device (-1 if `t`, the call's first tensor, is on none: the
+    checks then refuse it without touching CUDA)."""
+    return T.device() if t.is_cuda else -2
+
+
+def _stream(stream, dev: int, T: _Torch) -> int:
+    return T.stream(dev) if stream is None else _dc._stream_handle(stream)
 
 
 def _matrices(ts: Sequence, what: str, rows: int, dtype, dev: int):
     """Pointers, widths and row strides of [rows, width] tensors."""
     ptrs, widths, strides = [], [], []
-    for r, t in enumerate(ts):
-        if not t.is_cuda or t.get_device() != dev:
-            _on_device(t, f"{what}[{r}]", dev)
-        if t.dtype is not dtype:
-            raise ValueError(f"{what}[{r}] has dtype {t.dtype}, expected {dtype}")
+    for t in ts:
         shape = t.shape
-        if len(shape) != 2 or shape[0] != rows:
+        if t.get_device() != dev or t.dtype is not dtype or len(shape) != 2 or shape[0] != rows:
+            r = len(ptrs)
+            if t.get_device() != dev:
+                _refuse_device(t, f"{what}[{r}]", dev)
+            if t.dtype is not dtype:
+                _refuse_dtype(t, f"{what}[{r}]", (dtype,))
             raise ValueError(f"{what}[{r}] has shape {tuple(shape)}, expected ({rows}, columns)")
         s0, s1 = t.stride()
         if s1 != 1 and shape[1] > 1:
-            raise ValueError(f"{what}[{r}]: the vocabulary dimension must be contiguous")
+            raise ValueError(f"{what}[{len(ptrs)}]: the vocabulary dimension must be contiguous")
         ptrs.append(t.data_ptr())
         widths.append(shape[1])
         strides.append(s0)
-    return array.array("Q", ptrs), array.array("Q", widths), array.array("Q", strides)
+    return ptrs, widths, strides
 
 
-def _logits(shards: Sequence):
+def _logits(shards: Sequence, T: _Torch):
     if len(shards) == 0:
         raise ValueError("need at least one shard")
     first = shards[0]
     if first.dim() != 2:
         raise ValueError(f"shards[0] has shape {tuple(first.shape)}, expected (rows, columns)")
-    code = _T().code.get(first.dtype)
+    dtype = first.dtype
+    code = T.code.get(dtype)
     if code is None:
-        raise ValueError(f"logits are bfloat16, float16 or float32 (got {first.dtype})")
-    dev = _dc._cur_dev() if first.is_cuda else -1
-    return first.shape[0], code, dev
+        raise ValueError(f"logits are bfloat16, float16 or float32 (got {dtype})")
+    return first.shape[0], dtype, code, _current(first, T)
 
 
 # ------------------------------------------------------- log probabilities ---
@@ -198,32 +223,42 @@ def token_logprobs(shards: Sequence, tokens, logprobs, entropy=None, lse=None, t
     vocabulary gives NaN.  Logits of -inf have probability 0; a row of
     nothing else gives -inf.  Bits depend on the row alone: not on the other
     rows, the number of shards or where they are cut.  Returns ``logprobs``."""
-    rows, code, dev = _logits(shards)
-    ptrs, widths, strides = _matrices(shards, "shards", rows, shards[0].dtype, dev)
     T = _T()
-    top = 0
-    top_lp = top_id = top64 = 0
-    for name, t, types in (("top_logprobs", top_logprobs, T.f32), ("top_tokens", top_tokens, T.index)):
-        if t is None:
-            continue
-        _on_device(t, name, dev)
-        if t.dtype not in types:
-            raise ValueError(f"{name} has dtype {t.dtype}, expected {' or '.join(str(d) for d in types)}")
-        if t.dim() != 2 or t.shape[0] != rows or (top and t.shape[1] != top) or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous ({rows}, {top or 'k'}) tensor (got {tuple(t.shape)})")
-        top = t.shape[1]
-        if name == "top_tokens":
-            top_id, top64 = t.data_ptr(), int(t.dtype is T.i64)
-        else:
-            top_lp = t.data_ptr()
+    rows, dtype, code, dev = _logits(shards, T)
+    ptrs, widths, strides = _matrices(shards, "shards", rows, dtype, dev)
+    P = len(ptrs)
+    top = top_lp = top_id = top64 = 0
+    if top_logprobs is not None:
+        top, top_lp = _alternatives(top_logprobs, "top_logprobs", rows, None, T.f32, dev)
+    if top_tokens is not None:
+        top, top_id = _alternatives(top_tokens, "top_tokens", rows, top if top_lp else None, T.index, dev)
+        top64 = top_tokens.dtype is T.i64
+    total = sum(widths)
+    host = array.array("Q", ptrs + widths + strides)
+    at = host.buffer_info()[0]
+    f32 = T.f32
     block = _SCORE.pack(
-        ptrs.buffer_info()[0], widths.buffer_info()[0], strides.buffer_info()[0],
-        _vector(tokens, "tokens", rows, T.index, dev), _vector(logprobs, "logprobs", rows, T.f32, dev),
-        0 if entropy is None else _vector(entropy, "entropy", rows, T.f32, dev),
-        0 if lse is None else _vector(lse, "lse", rows, T.f32, dev), top_lp, top_id, rows,
-        sum(widths) if vocab is None else vocab, temperature, len(ptrs), code, int(tokens.dtype is T.i64), top64, top, 0)
-    _dc._check(_lib().dc_token_logprobs(block, _dc._stream_handle(stream)))
+        at, at + 8 * P, at + 16 * P, _vector(tokens, "tokens", rows, T.index, dev),
+        _vector(logprobs, "logprobs", rows, f32, dev),
+        0 if entropy is None else _vector(entropy, "entropy", rows, f32, dev),
+        0 if lse is None else _vector(lse, "lse", rows, f32, dev), top_lp, top_id, rows,
+        total if vocab is None else vocab, temperature, P, code, tokens.dtype is T.i64, top64, top, 0)
+    status = _lib().dc_token_logprobs(block, _stream(stream, dev, T))
+    if status:
+        _dc._check(status)
     return logprobs
+
+
+def _alternatives(t, what: str, rows: int, k, dtypes, dev: int):
+    """k and the data pointer of a contiguous [rows, k] tensor."""
+    if t.get_device() != dev:
+        _refuse_device(t, what, dev)
+    if t.dtype not in dtypes:
+        _refuse_dtype(t, what, dtypes)
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != rows or (k is not None and shape[1] != k) or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous ({rows}, {'k' if k is None else k}) tensor (got {tuple(shape)})")
+    return shape[1], t.data_ptr()
 
 
 def token_logprobs_backward(shards: Sequence, tokens, lse, grad_logprobs, grads: Sequence, entropy=None,
@@ -235,25 +270,30 @@ def token_logprobs_backward(shards: Sequence, tokens, lse, grad_logprobs, grads:
     (``entropy`` only with ``grad_entropy``); the upstream gradients are
     float32 [rows], either may be None.  Padding columns receive 0.  Returns
     ``grads``."""
-    rows, code, dev = _logits(shards)
-    dtype = shards[0].dtype
+    T = _T()
+    rows, dtype, code, dev = _logits(shards, T)
     ptrs, widths, strides = _matrices(shards, "shards", rows, dtype, dev)
-    if len(grads) != len(shards):
-        raise ValueError(f"need one gradient per shard (got {len(grads)} for {len(shards)})")
+    P = len(ptrs)
+    if len(grads) != P:
+        raise ValueError(f"need one gradient per shard (got {len(grads)} for {P})")
     gptrs, gwidths, gstrides = _matrices(grads, "grads", rows, dtype, dev)
     if gwidths != widths:
         raise ValueError("grads must have the shards' shapes")
     if grad_entropy is not None and entropy is None:
         raise ValueError("grad_entropy needs the forward call's entropy")
-    T = _T()
+    total = sum(widths)
+    host = array.array("Q", ptrs + widths + strides + gptrs + gstrides)
+    at = host.buffer_info()[0]
+    f32 = T.f32
     block = _GRAD.pack(
-        ptrs.buffer_info()[0], widths.buffer_info()[0], strides.buffer_info()[0], gptrs.buffer_info()[0],
-        gstrides.buffer_info()[0], _vector(tokens, "tokens", rows, T.index, dev), _vector(lse, "lse", rows, T.f32, dev),
-        0 if entropy is None else _vector(entropy, "entropy", rows, T.f32, dev),
-        0 if grad_logprobs is None else _vector(grad_logprobs, "grad_logprobs", rows, T.f32, dev),
-        0 if grad_entropy is None else _vector(grad_entropy, "grad_entropy", rows, T.f32, dev), rows,
-        sum(widths) if vocab is None else vocab, temperature, len(ptrs), code, int(tokens.dtype is T.i64), 0)
-    _dc._check(_lib().dc_token_logprobs_backward(block, _dc._stream_handle(stream)))
+        at, at + 8 * P, at + 16 * P, at + 24 * P, at + 32 * P, _vector(tokens, "tokens", rows, T.index, dev),
+        _vector(lse, "lse", rows, f32, dev), 0 if entropy is None else _vector(entropy, "entropy", rows, f32, dev),
+        0 if grad_logprobs is None else _vector(grad_logprobs, "grad_logprobs", rows, f32, dev),
+        0 if grad_entropy is None else _vector(grad_entropy, "grad_entropy", rows, f32, dev), rows,
+        total if vocab is None else vocab, temperature, P, code, tokens.dtype is T.i64, 0)
+    status = _lib().dc_token_logprobs_backward(block, _stream(stream, dev, T))
+    if status:
+        _dc._check(status)
     return grads
 
 
@@ -295,46 +335,50 @@ def logprobs_and_entropy(shards: Sequence, tokens, vocab: int | None = None, tem
 
 # ------------------------------------------------------------ paged cache ---
 
-def _heads(t, what: str, n: int, dtype, dev: int):
-    """Pointer, token and head strides of a [n, heads, dim] tensor."""
-    if not t.is_cuda or t.get_device() != dev:
-        _on_device(t, what, dev)
-    if t.dtype is not dtype:
-        raise ValueError(f"{what} has dtype {t.dtype}, expected {dtype}")
-    shape = t.shape
-    if len(shape) != 3 or shape[0] != n:
-        raise ValueError(f"{what} has shape {tuple(shape)}, expected ({n}, heads, dim)")
-    st = t.stride()
-    if st[2] != 1:
+def _heads(t, what: str, shape, dtype, dev: int):
+    """Pointer, token and head strides of a tensor of `shape`, (n, heads, dim);
+    heads None: any number."""
+    got = t.shape
+    if t.get_device() != dev or t.dtype is not dtype or got != shape:
+        if t.get_device() != dev:
+            _refuse_device(t, what, dev)
+        if t.dtype is not dtype:
+            _refuse_dtype(t, what, (dtype,))
+        if len(got) != 3 or got[0] != shape[0] or got[2] != shape[2] or shape[1] is not None:
+            raise ValueError(f"{what} has shape {tuple(got)}, expected "
+                             f"({shape[0]}, {'heads' if shape[1] is None else shape[1]}, {shape[2]})")
+    s0, s1, s2 = t.stride()
+    if s2 != 1:
         raise ValueError(f"{what}: the last dimension must be contiguous")
-    return t.data_ptr(), st[0], st[1]
+    return t.data_ptr(), s0, s1
 
 
 def _cache(t, what: str, shape, dtype, dev: int):
-    if not t.is_cuda or t.get_device() != dev:
-        _on_device(t, what, dev)
-    if t.dtype is not dtype:
-        raise ValueError(f"{what} has dtype {t.dtype}, expected {dtype}")
-    if t.dim() != 4 or (shape is not None and t.shape != shape):
-        raise ValueError(f"{what} has shape {tuple(t.shape)}, expected "
-                         f"{'(pages, page size, heads, dim)' if shape is None else tuple(shape)}")
-    st = t.stride()
-    if st[3] != 1:
+    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape:
+        if t.get_device() != dev:
+            _refuse_device(t, what, dev)
+        if t.dtype is not dtype:
+            _refuse_dtype(t, what, (dtype,))
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    s0, s1, s2, s3 = t.stride()
+    if s3 != 1:
         raise ValueError(f"{what}: the last dimension must be contiguous")
-    return t.data_ptr(), st[0], st[1], st[2]
+    return t.data_ptr(), s0, s1, s2
 
 
-def _table(t, rows, dev: int):
-    if not t.is_cuda or t.get_device() != dev:
-        _on_device(t, "page_table", dev)
-    if t.dtype not in _T().i32:
-        raise ValueError(f"page_table has dtype {t.dtype}, expected torch.int32")
-    if t.dim() != 2 or (rows is not None and t.shape[0] != rows):
-        raise ValueError(f"page_table has shape {tuple(t.shape)}, expected ({'sequences' if rows is None else rows}, pages)")
-    st = t.stride()
-    if st[1] != 1 and t.shape[1] > 1:
+def _table(t, rows, dev: int, T: _Torch):
+    """Pointer, rows, columns and row stride of a page table."""
+    if t.get_device() != dev:
+        _refuse_device(t, "page_table", dev)
+    if t.dtype not in T.i32:
+        _refuse_dtype(t, "page_table", T.i32)
+    shape = t.shape
+    if len(shape) != 2 or (rows is not None and shape[0] != rows):
+        raise ValueError(f"page_table has shape {tuple(shape)}, expected ({'sequences' if rows is None else rows}, pages)")
+    s0, s1 = t.stride()
+    if s1 != 1 and shape[1] > 1:
         raise ValueError("page_table: rows must be contiguous")
-    return t.data_ptr(), st[0]
+    return t.data_ptr(), shape[0], shape[1], s0
 
 
 def kv_append(k, v, positions, seqs, page_table, k_cache, v_cache, q=None, q_out=None, cos_sin=None,
@@ -355,48 +399,48 @@ def kv_append(k, v, positions, seqs, page_table, k_cache, v_cache, q=None, q_out
     A negative position is padding and writes nothing.  A token whose
     sequence, position or page does not exist writes no cache; its queries
     become NaN.  Returns ``q_out``."""
+    T = _T()
     dtype = k.dtype
-    code = _T().code.get(dtype)
+    code = T.code.get(dtype)
     if code is None:
         raise ValueError(f"keys are bfloat16, float16 or float32 (got {dtype})")
-    dev = _dc._cur_dev() if k.is_cuda else -1
-    if k.dim() != 3:
-        raise ValueError(f"k has shape {tuple(k.shape)}, expected (tokens, heads, dim)")
-    n, hk, d = k.shape
-    kp = _heads(k, "k", n, dtype, dev)
-    vp = _heads(v, "v", n, dtype, dev)
-    if v.shape != k.shape:
-        raise ValueError(f"v has shape {tuple(v.shape)}, expected {tuple(k.shape)}")
-    hq, qp, op = 0, (0, 0, 0), (0, 0, 0)
+    dev = _current(k, T)
+    shape = k.shape
+    if len(shape) != 3:
+        raise ValueError(f"k has shape {tuple(shape)}, expected (tokens, heads, dim)")
+    n, hk, d = shape
+    kp, k0, k1 = _heads(k, "k", shape, dtype, dev)
+    vp, v0, v1 = _heads(v, "v", shape, dtype, dev)
+    hq = qp = q0 = q1 = op = o0 = o1 = 0
     if q is not None:
         if q_out is None:
             raise ValueError("q needs q_out")
-        qp, op = _heads(q, "q", n, dtype, dev), _heads(q_out, "q_out", n, dtype, dev)
+        qp, q0, q1 = _heads(q, "q", (n, None, d), dtype, dev)
         hq = q.shape[1]
-        if q.shape[2] != d or q_out.shape != q.shape:
-            raise ValueError(f"q and q_out have shapes {tuple(q.shape)} and {tuple(q_out.shape)}, expected ({n}, heads, {d})")
+        op, o0, o1 = _heads(q_out, "q_out", (n, hq, d), dtype, dev)
     elif q_out is not None:
         raise ValueError("q_out needs q")
-    rot, cos_rows, cs = 0, 0, 0
+    rot = cos_rows = cs = 0
     if cos_sin is not None:
-        _on_device(cos_sin, "cos_sin", dev)
-        if cos_sin.dtype not in _T().f32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+        if cos_sin.get_device() != dev:
+            _refuse_device(cos_sin, "cos_sin", dev)
+        if cos_sin.dtype not in T.f32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
             raise ValueError(f"cos_sin must be a contiguous float32 (positions, rotary_dim) tensor "
                              f"(got {cos_sin.dtype} {tuple(cos_sin.shape)})")
         cos_rows, rot = cos_sin.shape
         cs = cos_sin.data_ptr()
-    kc = _cache(k_cache, "k_cache", None, dtype, dev)
     shape = k_cache.shape
-    if shape[2] != hk or shape[3] != d:
+    if len(shape) != 4 or shape[2] != hk or shape[3] != d:
         raise ValueError(f"k_cache has shape {tuple(shape)}, expected (pages, page size, {hk}, {d})")
-    vc = _cache(v_cache, "v_cache", shape, dtype, dev)
-    T = _T()
-    table, table_stride = _table(page_table, None, dev)
+    table, table_rows, table_width, table_stride = _table(page_table, None, dev, T)
     block = _APPEND.pack(
-        qp[0], kp[0], vp[0], op[0], _vector(positions, "positions", n, T.i32, dev), _vector(seqs, "seqs", n, T.i32, dev),
-        table, cs, *kc, *vc, qp[1], qp[2], kp[1], kp[2], vp[1], vp[2], op[1], op[2], n, page_table.shape[0],
-        page_table.shape[1], table_stride, cos_rows, shape[0], shape[1], hq, hk, d, rot, int(interleaved), code, 0)
-    _dc._check(_lib().dc_kv_append(block, _dc._stream_handle(stream)))
+        qp, kp, vp, op, _vector(positions, "positions", n, T.i32, dev), _vector(seqs, "seqs", n, T.i32, dev), table, cs,
+        *_cache(k_cache, "k_cache", shape, dtype, dev), *_cache(v_cache, "v_cache", shape, dtype, dev), q0, q1, k0, k1,
+        v0, v1, o0, o1, n, table_rows, table_width, table_stride, cos_rows, shape[0], shape[1], hq, hk, d, rot,
+        1 if interleaved else 0, code, 0)
+    status = _lib().dc_kv_append(block, _stream(stream, dev, T))
+    if status:
+        _dc._check(status)
     return q_out
 
 
@@ -428,37 +472,39 @@ def paged_attention(q, k_cache, v_cache, page_table, lengths, out, workspace, sc
     A length of 0 gives zeros (lse -inf).  A page number outside the cache, or
     a length past the table, gives NaN.  ``workspace``: see
     :func:`attention_workspace`.  Returns ``out``."""
+    T = _T()
     dtype = q.dtype
-    code = _T().code.get(dtype)
+    code = T.code.get(dtype)
     if code is None or code == 2:
         raise ValueError(f"queries are bfloat16 or float16 (got {dtype})")
-    dev = _dc._cur_dev() if q.is_cuda else -1
-    if q.dim() != 3:
-        raise ValueError(f"q has shape {tuple(q.shape)}, expected (sequences, heads, dim)")
-    n, hq, d = q.shape
-    qp = _heads(q, "q", n, dtype, dev)
-    op = _heads(out, "out", n, dtype, dev)
-    if out.shape != q.shape:
-        raise ValueError(f"out has shape {tuple(out.shape)}, expected {tuple(q.shape)}")
-    kc = _cache(k_cache, "k_cache", None, dtype, dev)
-    shape = k_cache.shape
-    if shape[3] != d:
-        raise ValueError(f"k_cache has shape {tuple(shape)}, expected (pages, page size, heads, {d})")
-    vc = _cache(v_cache, "v_cache", shape, dtype, dev)
-    T = _T()
-    table, table_stride = _table(page_table, n, dev)
+    dev = _current(q, T)
+    shape = q.shape
+    if len(shape) != 3:
+        raise ValueError(f"q has shape {tuple(shape)}, expected (sequences, heads, dim)")
+    n, hq, d = shape
+    qp, q0, q1 = _heads(q, "q", shape, dtype, dev)
+    op, o0, o1 = _heads(out, "out", shape, dtype, dev)
+    cache = k_cache.shape
+    if len(cache) != 4 or cache[3] != d:
+        raise ValueError(f"k_cache has shape {tuple(cache)}, expected (pages, page size, heads, {d})")
+    table, _, table_width, table_stride = _table(page_table, n, dev, T)
     lse_ptr = 0
     if lse is not None:
-        _on_device(lse, "lse", dev)
-        if lse.dtype not in T.f32 or lse.shape != q.shape[:2] or not lse.is_contiguous():
+        if lse.get_device() != dev:
+            _refuse_device(lse, "lse", dev)
+        if lse.dtype not in T.f32 or lse.shape != (n, hq) or not lse.is_contiguous():
             raise ValueError(f"lse must be a contiguous float32 ({n}, {hq}) tensor (got {lse.dtype} {tuple(lse.shape)})")
         lse_ptr = lse.data_ptr()
-    if not workspace.is_cuda or workspace.get_device() != dev or not workspace.is_contiguous():
-        _on_device(workspace, "workspace", dev)
+    if workspace.get_device() != dev:
+        _refuse_device(workspace, "workspace", dev)
+    if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     block = _ATTEND.pack(
-        qp[0], op[0], lse_ptr, table, _vector(lengths, "lengths", n, T.i32, dev), workspace.data_ptr(), workspace.nbytes,
-        *kc, *vc, qp[1], qp[2], op[1], op[2], n, page_table.shape[1], table_stride, shape[0], shape[1], hq, shape[2], d,
-        window, code, 1.0 / math.sqrt(d) if scale is None else scale, 0)
-    _dc._check(_lib().dc_paged_attention(block, _dc._stream_handle(stream)))
+        qp, op, lse_ptr, table, _vector(lengths, "lengths", n, T.i32, dev), workspace.data_ptr(), workspace.nbytes,
+        *_cache(k_cache, "k_cache", cache, dtype, dev), *_cache(v_cache, "v_cache", cache, dtype, dev), q0, q1, o0, o1,
+        n, table_width, table_stride, cache[0], cache[1], hq, cache[2], d, window, code,
+        d ** -0.5 if scale is None else scale, 0)
+    status = _lib().dc_paged_attention(block, _stream(stream, dev, T))
+    if status:
+        _dc._check(status)
     return out
