@@ -37,7 +37,8 @@ enum : uint32_t {
 constexpr int kThreads = kAttendWarps * 32;
 
 // Shared memory of a head size: each warp's ring of tiles, then (heads above
-// 128, whose subtrees do not fit in registers) its waiting subtrees.
+// 128, whose subtrees and queries do not fit in registers) its waiting
+// subtrees and the queries.
 template <int D, int HB>
 struct Shape {
   static constexpr int kRow = D * 2 + 16;           // bytes; the 16 keep ldmatrix free of conflicts
@@ -48,7 +49,9 @@ struct Shape {
   static constexpr int kValues = D / 4 * (HB / 8);  // of a head block's output that a lane holds
   static constexpr int kLevels = attend_levels(D, HB);
   static constexpr bool kInRegs = D <= 128;
-  static constexpr int kBytes = kRing + (kInRegs ? 0 : kAttendWarps * kLevels * kValues * 32 * 4);
+  static constexpr bool kQueryShared = D > 128;
+  static constexpr int kHeld = kInRegs ? 0 : kAttendWarps * kLevels * kValues * 32 * 4;
+  static constexpr int kBytes = kRing + kHeld + (kQueryShared ? HB * kRow : 0);
 };
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
@@ -251,74 +254,113 @@ __global__ __launch_bounds__(kThreads) void dc_attend_kernel(const __grid_consta
   const uint32_t t1 = static_cast<uint32_t>(min(first + run, static_cast<uint64_t>(len)));
   const uint32_t tiles = (t1 - t0 + kAttendTile - 1) / kAttendTile;
 
-  // lanes 0..15 look up where the keys of a tile's tokens are, lanes 16..31
-  // their values; a copy instruction then moves 128 bytes of each of 4 rows (64
-  // of 8 where rows are no multiple of 128 bytes)
+  // A copy instruction moves 128 bytes of each of 4 rows (64 of 8 where rows
+  // are no multiple of 128 bytes).  Most tiles lie in one page: their rows are
+  // a stride apart.  In the others lanes 0..15 look up where the keys of the
+  // tile's tokens are, lanes 16..31 their values, and hand the addresses on.
   constexpr int kLanes = D % 64 == 0 ? 8 : 4;       // lanes that copy one row
   constexpr int kRows = 32 / kLanes;                // rows an instruction touches
+  constexpr int kGroups = kAttendTile / kRows;
   const uint32_t ring = smem_addr(smem) + static_cast<uint32_t>(warp * S::kStages * S::kStage);
   const uint64_t table_row = p.table + static_cast<uint64_t>(seq) * static_cast<uint64_t>(p.table_stride) * 4;
-  const uint64_t c_head = (lane < 16 ? p.kc.base : p.vc.base) + static_cast<uint64_t>(kh) * (lane < 16 ? p.kc.head : p.vc.head);
-  const uint64_t c_page = lane < 16 ? p.kc.page : p.vc.page, c_token = lane < 16 ? p.kc.token : p.vc.token;
-  int32_t next_id = -1;    // the page of this lane's token of the next tile to copy, -1: no token
-  uint32_t next_slot = 0;  // ... and its place in the page
+  const uint64_t k_head = p.kc.base + static_cast<uint64_t>(kh) * p.kc.head;
+  const uint64_t v_head = p.vc.base + static_cast<uint64_t>(kh) * p.vc.head;
+  int32_t next_id = -1;     // the page of this lane's token of the next tile to copy, -1: no token
+  uint32_t next_slot = 0;   // ... and its place in the page
+  bool next_whole = false;  // the tile is 16 tokens of one page, next_slot its first token's place
   auto look_up = [&](uint32_t i) {
-    const uint32_t t = t0 + i * kAttendTile + (lane & 15);
-    next_id = -1;
-    if (i < tiles && t < t1) {
-      const uint32_t pg = p.page_shift >= 0 ? t >> p.page_shift : t / p.page_size;
+    if (i >= tiles) return;
+    const uint32_t tile = t0 + i * kAttendTile;
+    uint32_t pg = p.page_shift >= 0 ? tile >> p.page_shift : tile / p.page_size;
+    next_slot = tile - pg * p.page_size;
+    next_whole = tile + kAttendTile <= t1 && next_slot + kAttendTile <= p.page_size;
+    if (!next_whole) {
+      const uint32_t t = tile + (lane & 15);
+      pg = p.page_shift >= 0 ? t >> p.page_shift : t / p.page_size;
       next_slot = t - pg * p.page_size;
-      const int32_t* a = reinterpret_cast<const int32_t*>(table_row) + pg;
-      next_id = in_bounds(a, 4, table_row, table_row + 4ull * p.table_width, kSiteTable) ? *a : -1;
-      if (next_id < 0 || next_id >= p.num_pages) {  // a page outside the cache is never touched
-        next_id = -1;
-        bad = true;
-      }
+      next_id = -1;
+      if (t >= t1) return;
+    }
+    const int32_t* a = reinterpret_cast<const int32_t*>(table_row) + pg;
+    next_id = in_bounds(a, 4, table_row, table_row + 4ull * p.table_width, kSiteTable) ? *a : -1;
+  };
+  auto copy = [&](uint32_t dst, int half, uint64_t src, bool read) {
+#pragma unroll
+    for (int c = 0; c < D / 8 / kLanes; ++c) {
+      const uint64_t x = src + c * kLanes * 16;
+      const bool ok = read && in_bounds(reinterpret_cast<const void*>(x), 16, half ? p.vc.lo : p.kc.lo,
+                                        half ? p.vc.hi : p.kc.hi, half ? kSiteValue : kSiteKey);
+      cp_async16_or_zero(dst + half * S::kHalf + c * kLanes * 16, ok ? x : p.kc.base, ok);
     }
   };
   auto issue = [&](uint32_t i) {
     if (i < tiles) {
-      // (no row starts at 0)
-      const uint64_t row = next_id < 0 ? 0 : c_head + static_cast<uint64_t>(next_id) * c_page +
-                                                 static_cast<uint64_t>(next_slot) * c_token;
       const uint32_t dst = ring + (i % S::kStages) * S::kStage + (lane / kLanes) * S::kRow + (lane % kLanes) * 16;
+      // (a page outside the cache is never touched; ids past a sequence's end are not looked at)
+      const bool there = next_id >= 0 && next_id < p.num_pages;
+      if (!there && (next_whole || t0 + i * kAttendTile + (lane & 15) < t1)) bad = true;
+      if (next_whole && there) {
+        const uint64_t at = next_slot + lane / kLanes;
+        uint64_t k = k_head + static_cast<uint64_t>(next_id) * p.kc.page + at * p.kc.token + (lane % kLanes) * 16;
+        uint64_t v = v_head + static_cast<uint64_t>(next_id) * p.vc.page + at * p.vc.token + (lane % kLanes) * 16;
 #pragma unroll
-      for (int half = 0; half < 2; ++half)
-#pragma unroll
-        for (int r = 0; r < kAttendTile / kRows; ++r) {
-          const uint64_t at = __shfl_sync(~0u, row, lane / kLanes + kRows * r + 16 * half);
-          const uint64_t src = (at ? at : half ? p.vc.base : p.kc.base) + (lane % kLanes) * 16;
-#pragma unroll
-          for (int c = 0; c < D / 8 / kLanes; ++c) {
-            const uint64_t x = src + c * kLanes * 16;
-            const bool read = at != 0 && in_bounds(reinterpret_cast<const void*>(x), 16, half ? p.vc.lo : p.kc.lo,
-                                                   half ? p.vc.hi : p.kc.hi, half ? kSiteValue : kSiteKey);
-            cp_async16_or_zero(dst + half * S::kHalf + r * kRows * S::kRow + c * kLanes * 16, x, read);
-          }
+        for (int r = 0; r < kGroups; ++r) {
+          copy(dst + r * kRows * S::kRow, 0, k, true);
+          k += kRows * p.kc.token;
         }
+#pragma unroll
+        for (int r = 0; r < kGroups; ++r) {
+          copy(dst + r * kRows * S::kRow, 1, v, true);
+          v += kRows * p.vc.token;
+        }
+      } else {
+        // (no row starts at 0; a whole tile of a missing page is 16 missing rows)
+        const uint64_t row = !there ? 0 : (lane < 16 ? k_head : v_head) +
+                                              static_cast<uint64_t>(next_id) * (lane < 16 ? p.kc.page : p.vc.page) +
+                                              next_slot * (lane < 16 ? p.kc.token : p.vc.token);
+#pragma unroll
+        for (int r = 0; r < 2 * kGroups; ++r) {
+          const uint64_t at = __shfl_sync(~0u, row, lane / kLanes + kRows * (r % kGroups) + 16 * (r / kGroups));
+          copy(dst + r % kGroups * kRows * S::kRow, r / kGroups, at + (lane % kLanes) * 16, at != 0);
+        }
+      }
     }
     cp_async_commit();
     look_up(i + 1);
   };
   look_up(0);
 
-  // query fragments: rows 0..7 heads h0.., rows 8..15 heads h0 + 8.. (HB 16)
-  uint32_t qf[kSteps][2 * R];
+  // query fragments: rows 0..7 heads h0.., rows 8..15 heads h0 + 8.. (HB 16);
+  // of heads above 128 they stay in shared memory (in registers they spilled:
+  // 1800 cycles a tile for q.k at D = 256)
+  uint32_t qf[S::kQueryShared ? 1 : kSteps][2 * R];
+  uint8_t* const q_smem = smem + S::kRing + S::kHeld;
   {
-    const int g = lane >> 2;
+    const uint64_t q_seq = p.q + static_cast<uint64_t>(seq) * p.q_seq + static_cast<uint64_t>(h0) * p.q_head;
+    if constexpr (S::kQueryShared) {
+      for (int i = threadIdx.x; i < HB * (D / 8); i += kThreads) {
+        const int h = i / (D / 8), c = i % (D / 8);
+        const uint64_t row = q_seq + static_cast<uint64_t>(h) * p.q_head;
+        const uint4* a = reinterpret_cast<const uint4*>(row) + c;
+        *reinterpret_cast<uint4*>(q_smem + h * S::kRow + c * 16) =
+            h < nh && in_bounds(a, 16, row, row + D * 2, kSiteQuery) ? *a : make_uint4(0, 0, 0, 0);
+      }
+      __syncthreads();
+    } else {
 #pragma unroll
-    for (int half = 0; half < R; ++half) {
-      const int h = g + 8 * half;
-      const uint64_t row = p.q + static_cast<uint64_t>(seq) * p.q_seq + static_cast<uint64_t>(h0 + h) * p.q_head;
+      for (int half = 0; half < R; ++half) {
+        const int h = (lane >> 2) + 8 * half;
+        const uint64_t row = q_seq + static_cast<uint64_t>(h) * p.q_head;
 #pragma unroll
-      for (int k = 0; k < kSteps; ++k)
+        for (int k = 0; k < kSteps; ++k)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t* a =
-              reinterpret_cast<const uint32_t*>(row + static_cast<uint64_t>(k * 16 + i * 8 + (lane & 3) * 2) * 2);
-          // a[0]: row g, first 8 columns; a[1]: row g + 8; a[2], a[3]: the next 8 columns
-          qf[k][R * i + half] = h < nh && in_bounds(a, 4, row, row + D * 2, kSiteQuery) ? *a : 0u;
-        }
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t* a =
+                reinterpret_cast<const uint32_t*>(row + static_cast<uint64_t>(k * 16 + i * 8 + (lane & 3) * 2) * 2);
+            // a[0]: row g, first 8 columns; a[1]: row g + 8; a[2], a[3]: the next 8 columns
+            qf[k][R * i + half] = h < nh && in_bounds(a, 4, row, row + D * 2, kSiteQuery) ? *a : 0u;
+          }
+      }
     }
   }
 #pragma unroll
@@ -387,7 +429,19 @@ __global__ __launch_bounds__(kThreads) void dc_attend_kernel(const __grid_consta
         uint32_t b[4];
         ldmatrix4(a + k * 32, b);
         uint32_t q[4];
-        if constexpr (HB == 16) {
+        if constexpr (S::kQueryShared) {
+          const uint32_t qa = smem_addr(q_smem) + k * 32;
+          if constexpr (HB == 16) {
+            ldmatrix4(qa + (((lane >> 3) & 1) * 8 + (lane & 7)) * S::kRow + (lane >> 4) * 16, q);
+          } else {
+            uint32_t x[4];  // (the upper 16 lanes' addresses repeat the lower ones')
+            ldmatrix4(qa + (lane & 7) * S::kRow + ((lane >> 3) & 1) * 16, x);
+            q[0] = x[0];
+            q[1] = 0;
+            q[2] = x[1];
+            q[3] = 0;
+          }
+        } else if constexpr (HB == 16) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) q[j] = qf[k][j];
         } else {

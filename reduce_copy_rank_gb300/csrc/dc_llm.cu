@@ -224,9 +224,11 @@ dc_status_t plan_attend(int64_t seqs, int q_heads, int kv_heads, int dim, uint64
   if (a->units * kAttendMaxPieces > 0x7FFFFFFFull)
     return fail(DC_ERR_INVALID, "%llu units of work exceed a grid", static_cast<unsigned long long>(a->units));
   const uint32_t units = static_cast<uint32_t>(a->units);
-  // the longest sequence has `most` pieces at level 0; a shorter one may be cut finer
+  // no sequence of up to n tokens has more than `most` pieces at level 0; one
+  // with fewer may be cut finer
   const uint32_t n = static_cast<uint32_t>(max_tokens);
-  const uint32_t most = n > 512 * 64 ? kAttendMaxPieces : attend_pieces(n, 0);
+  const uint32_t most = n > 512 * 128 ? kAttendMaxPieces
+                                      : std::max(attend_pieces(n, 0), attend_pieces(std::min(n, kAttendShort), 0));
   const int levels = attend_levels(dim, a->hb);
   a->pieces = 1;
   for (uint32_t s = 1; s <= most; ++s) {
