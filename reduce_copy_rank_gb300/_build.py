@@ -4,14 +4,18 @@ Each ``csrc/*.cu`` is compiled on its own nvcc process (in parallel), then
 linked into ``reduce_copy_rank_gb300/libdc.so`` with the CUDA runtime linked
 statically, so the library needs nothing but the driver at run time.
 Floating point: no fast-math, no flush-to-zero, no contraction.
+Beside it, ``csrc/binding.cpp`` becomes the extension module ``_binding``, which
+reads torch tensors for the language-model operators (needs torch's headers).
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -25,6 +29,9 @@ LIB = os.path.join(PKG, "libdc.so")
 # environment variable DC_LIBRARY is "bounds".
 OBJDIR_BOUNDS = os.path.join(PKG, "_build_bounds")
 LIB_BOUNDS = os.path.join(PKG, "libdc_bounds.so")
+
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING = os.path.join(PKG, "_binding" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVFLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
@@ -55,11 +62,38 @@ def up_to_date(lib: str = LIB) -> bool:
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
+def build_binding(force: bool = False) -> str | None:
+    """Compile the extension module unless it is newer than its sources; None
+    if torch is not installed."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.origin:
+        return None
+    root = os.path.dirname(spec.origin)
+    deps = [BINDING_SRC, os.path.join(INCLUDE, "dc.h"), os.path.abspath(__file__), os.path.join(root, "version.py")]
+    if not force and os.path.exists(BINDING) and \
+            all(os.path.getmtime(d) <= os.path.getmtime(BINDING) for d in deps if os.path.exists(d)):
+        return BINDING
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    includes = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                sysconfig.get_paths()["include"], os.path.join(cuda, "include"), INCLUDE]
+    lib = os.path.join(root, "lib")
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX") or shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           *[x for i in includes for x in ("-isystem" if i != INCLUDE else "-I", i)], BINDING_SRC, "-o", tmp, "-L", lib,
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compiling the binding failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False, bounds: bool = False) -> str:
     """Compile and link libdc.so (bounds=True: the bounds-checked
     libdc_bounds.so) unless it is newer than every source."""
     lib, objdir = (LIB_BOUNDS, OBJDIR_BOUNDS) if bounds else (LIB, OBJDIR)
     if not force and up_to_date(lib):
+        build_binding()
         return lib
     nvcc = _nvcc()
     os.makedirs(objdir, exist_ok=True)
@@ -78,8 +112,10 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False, 
         return obj
 
     srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
+        binding = ex.submit(build_binding, force)
         objs = list(ex.map(compile_one, srcs))
+        binding.result()
     tmp = lib + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -3,7 +3,8 @@ vocabulary shards and their gradient, the paged key-value cache and the
 attention of single new tokens over it.
 
 A thin binding like the rest of the package: tensors become pointers, sizes
-and strides in the argument blocks of ``include/dc.h``, and the work runs in
+and strides in the argument blocks of ``include/dc.h`` (read by the extension
+module ``_binding``, whose checks raise ``ValueError``), and the work runs in
 the library's CUDA kernels, one launch a call.  A row's or a sequence's
 result depends on nothing else in the call: the same bits in a batch of one
 and of a thousand, and, for the log probabilities, under every sharding.
@@ -105,103 +106,27 @@ def dc_attention_workspace_bytes(seqs: int, q_heads: int, kv_heads: int, dim: in
     return int(_lib().dc_attention_workspace_bytes(seqs, q_heads, kv_heads, dim, max_tokens))
 
 
-# ------------------------------------------------------------ tensor checks ---
-# A small call's time is mostly these checks, so each reads a tensor's
-# properties once, and words its refusal only when one of them is wrong.
-# (get_device() is -1 for a tensor that is on no GPU.)
+# ------------------------------------------------------------ tensor API ---
 
-def _refuse_device(t, what: str, dev: int) -> None:
-    if not t.is_cuda:
-        raise ValueError(f"{what} must be a CUDA tensor (got device {t.device})")
-    _dc._wrong_device(what, t, dev)
+_module = None
 
 
-def _refuse_dtype(t, what: str, dtypes) -> None:
-    raise ValueError(f"{what} has dtype {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
+def _binding():
+    """The extension module that reads the tensors, bound to the library."""
+    global _module
+    if _module is None:
+        L = _lib()
+        import torch  # noqa: F401  (its libraries first)
 
-
-def _vector(t, what: str, n: int, dtypes, dev: int) -> int:
-    """The data pointer of a contiguous [n] tensor of one of `dtypes`."""
-    if t.get_device() != dev:
-        _refuse_device(t, what, dev)
-    if t.dtype not in dtypes:
-        _refuse_dtype(t, what, dtypes)
-    if t.shape != (n,):
-        raise ValueError(f"{what} has shape {tuple(t.shape)}, expected ({n},)")
-    if not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous")
-    return t.data_ptr()
-
-
-class _Torch:
-    """What the checks use of torch, looked up once."""
-
-    def __init__(self):
-        import torch
-
-        self.f32 = (torch.float32,)
-        self.i32 = (torch.int32,)
-        self.index = (torch.int64, torch.int32)
-        self.i64 = torch.int64
-        self.code = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
-        C = torch._C
-        self.device = getattr(C, "_cuda_getDevice", None) or torch.cuda.current_device
-        raw = getattr(C, "_cuda_getCurrentRawStream", None)
-        self.stream = raw or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-
-
-_torch = None
-
-
-def _T() -> _Torch:
-    global _torch
-    if _torch is None:
-        _torch = _Torch()
-    return _torch
-
-
-def _current(t, T: _Torch) -> int:
-    """The current device (-1 if `t`, the call's first tensor, is on none: the
-    checks then refuse it without touching CUDA)."""
-    return T.device() if t.is_cuda else -2
-
-
-def _stream(stream, dev: int, T: _Torch) -> int:
-    return T.stream(dev) if stream is None else _dc._stream_handle(stream)
-
-
-def _matrices(ts: Sequence, what: str, rows: int, dtype, dev: int):
-    """Pointers, widths and row strides of [rows, width] tensors."""
-    ptrs, widths, strides = [], [], []
-    for t in ts:
-        shape = t.shape
-        if t.get_device() != dev or t.dtype is not dtype or len(shape) != 2 or shape[0] != rows:
-            r = len(ptrs)
-            if t.get_device() != dev:
-                _refuse_device(t, f"{what}[{r}]", dev)
-            if t.dtype is not dtype:
-                _refuse_dtype(t, f"{what}[{r}]", (dtype,))
-            raise ValueError(f"{what}[{r}] has shape {tuple(shape)}, expected ({rows}, columns)")
-        s0, s1 = t.stride()
-        if s1 != 1 and shape[1] > 1:
-            raise ValueError(f"{what}[{len(ptrs)}]: the vocabulary dimension must be contiguous")
-        ptrs.append(t.data_ptr())
-        widths.append(shape[1])
-        strides.append(s0)
-    return ptrs, widths, strides
-
-
-def _logits(shards: Sequence, T: _Torch):
-    if len(shards) == 0:
-        raise ValueError("need at least one shard")
-    first = shards[0]
-    if first.dim() != 2:
-        raise ValueError(f"shards[0] has shape {tuple(first.shape)}, expected (rows, columns)")
-    dtype = first.dtype
-    code = T.code.get(dtype)
-    if code is None:
-        raise ValueError(f"logits are bfloat16, float16 or float32 (got {dtype})")
-    return first.shape[0], dtype, code, _current(first, T)
+        try:
+            from . import _binding as module
+        except ImportError as e:
+            raise _dc.LibraryMissing(f"the extension module _binding cannot be loaded ({e}): build it with `python -m "
+                                     "reduce_copy_rank_gb300._build` or __graft_entry__.build()") from e
+        module.bind(*(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in (
+            "dc_token_logprobs", "dc_token_logprobs_backward", "dc_kv_append", "dc_paged_attention")))
+        _module = module
+    return _module
 
 
 # ------------------------------------------------------- log probabilities ---
@@ -223,42 +148,11 @@ def token_logprobs(shards: Sequence, tokens, logprobs, entropy=None, lse=None, t
     vocabulary gives NaN.  Logits of -inf have probability 0; a row of
     nothing else gives -inf.  Bits depend on the row alone: not on the other
     rows, the number of shards or where they are cut.  Returns ``logprobs``."""
-    T = _T()
-    rows, dtype, code, dev = _logits(shards, T)
-    ptrs, widths, strides = _matrices(shards, "shards", rows, dtype, dev)
-    P = len(ptrs)
-    top = top_lp = top_id = top64 = 0
-    if top_logprobs is not None:
-        top, top_lp = _alternatives(top_logprobs, "top_logprobs", rows, None, T.f32, dev)
-    if top_tokens is not None:
-        top, top_id = _alternatives(top_tokens, "top_tokens", rows, top if top_lp else None, T.index, dev)
-        top64 = top_tokens.dtype is T.i64
-    total = sum(widths)
-    host = array.array("Q", ptrs + widths + strides)
-    at = host.buffer_info()[0]
-    f32 = T.f32
-    block = _SCORE.pack(
-        at, at + 8 * P, at + 16 * P, _vector(tokens, "tokens", rows, T.index, dev),
-        _vector(logprobs, "logprobs", rows, f32, dev),
-        0 if entropy is None else _vector(entropy, "entropy", rows, f32, dev),
-        0 if lse is None else _vector(lse, "lse", rows, f32, dev), top_lp, top_id, rows,
-        total if vocab is None else vocab, temperature, P, code, tokens.dtype is T.i64, top64, top, 0)
-    status = _lib().dc_token_logprobs(block, _stream(stream, dev, T))
+    status = (_module or _binding()).token_logprobs(shards, tokens, logprobs, entropy, lse, top_logprobs, top_tokens, vocab,
+                                                    temperature, stream)
     if status:
         _dc._check(status)
     return logprobs
-
-
-def _alternatives(t, what: str, rows: int, k, dtypes, dev: int):
-    """k and the data pointer of a contiguous [rows, k] tensor."""
-    if t.get_device() != dev:
-        _refuse_device(t, what, dev)
-    if t.dtype not in dtypes:
-        _refuse_dtype(t, what, dtypes)
-    shape = t.shape
-    if len(shape) != 2 or shape[0] != rows or (k is not None and shape[1] != k) or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous ({rows}, {'k' if k is None else k}) tensor (got {tuple(shape)})")
-    return shape[1], t.data_ptr()
 
 
 def token_logprobs_backward(shards: Sequence, tokens, lse, grad_logprobs, grads: Sequence, entropy=None,
@@ -270,28 +164,8 @@ def token_logprobs_backward(shards: Sequence, tokens, lse, grad_logprobs, grads:
     (``entropy`` only with ``grad_entropy``); the upstream gradients are
     float32 [rows], either may be None.  Padding columns receive 0.  Returns
     ``grads``."""
-    T = _T()
-    rows, dtype, code, dev = _logits(shards, T)
-    ptrs, widths, strides = _matrices(shards, "shards", rows, dtype, dev)
-    P = len(ptrs)
-    if len(grads) != P:
-        raise ValueError(f"need one gradient per shard (got {len(grads)} for {P})")
-    gptrs, gwidths, gstrides = _matrices(grads, "grads", rows, dtype, dev)
-    if gwidths != widths:
-        raise ValueError("grads must have the shards' shapes")
-    if grad_entropy is not None and entropy is None:
-        raise ValueError("grad_entropy needs the forward call's entropy")
-    total = sum(widths)
-    host = array.array("Q", ptrs + widths + strides + gptrs + gstrides)
-    at = host.buffer_info()[0]
-    f32 = T.f32
-    block = _GRAD.pack(
-        at, at + 8 * P, at + 16 * P, at + 24 * P, at + 32 * P, _vector(tokens, "tokens", rows, T.index, dev),
-        _vector(lse, "lse", rows, f32, dev), 0 if entropy is None else _vector(entropy, "entropy", rows, f32, dev),
-        0 if grad_logprobs is None else _vector(grad_logprobs, "grad_logprobs", rows, f32, dev),
-        0 if grad_entropy is None else _vector(grad_entropy, "grad_entropy", rows, f32, dev), rows,
-        total if vocab is None else vocab, temperature, P, code, tokens.dtype is T.i64, 0)
-    status = _lib().dc_token_logprobs_backward(block, _stream(stream, dev, T))
+    status = (_module or _binding()).token_logprobs_backward(shards, tokens, lse, grad_logprobs, grads, entropy,
+                                                             grad_entropy, vocab, temperature, stream)
     if status:
         _dc._check(status)
     return grads
@@ -335,52 +209,6 @@ def logprobs_and_entropy(shards: Sequence, tokens, vocab: int | None = None, tem
 
 # ------------------------------------------------------------ paged cache ---
 
-def _heads(t, what: str, shape, dtype, dev: int):
-    """Pointer, token and head strides of a tensor of `shape`, (n, heads, dim);
-    heads None: any number."""
-    got = t.shape
-    if t.get_device() != dev or t.dtype is not dtype or got != shape:
-        if t.get_device() != dev:
-            _refuse_device(t, what, dev)
-        if t.dtype is not dtype:
-            _refuse_dtype(t, what, (dtype,))
-        if len(got) != 3 or got[0] != shape[0] or got[2] != shape[2] or shape[1] is not None:
-            raise ValueError(f"{what} has shape {tuple(got)}, expected "
-                             f"({shape[0]}, {'heads' if shape[1] is None else shape[1]}, {shape[2]})")
-    s0, s1, s2 = t.stride()
-    if s2 != 1:
-        raise ValueError(f"{what}: the last dimension must be contiguous")
-    return t.data_ptr(), s0, s1
-
-
-def _cache(t, what: str, shape, dtype, dev: int):
-    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape:
-        if t.get_device() != dev:
-            _refuse_device(t, what, dev)
-        if t.dtype is not dtype:
-            _refuse_dtype(t, what, (dtype,))
-        raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    s0, s1, s2, s3 = t.stride()
-    if s3 != 1:
-        raise ValueError(f"{what}: the last dimension must be contiguous")
-    return t.data_ptr(), s0, s1, s2
-
-
-def _table(t, rows, dev: int, T: _Torch):
-    """Pointer, rows, columns and row stride of a page table."""
-    if t.get_device() != dev:
-        _refuse_device(t, "page_table", dev)
-    if t.dtype not in T.i32:
-        _refuse_dtype(t, "page_table", T.i32)
-    shape = t.shape
-    if len(shape) != 2 or (rows is not None and shape[0] != rows):
-        raise ValueError(f"page_table has shape {tuple(shape)}, expected ({'sequences' if rows is None else rows}, pages)")
-    s0, s1 = t.stride()
-    if s1 != 1 and shape[1] > 1:
-        raise ValueError("page_table: rows must be contiguous")
-    return t.data_ptr(), shape[0], shape[1], s0
-
-
 def kv_append(k, v, positions, seqs, page_table, k_cache, v_cache, q=None, q_out=None, cos_sin=None,
               interleaved: bool = False, stream=None):
     """Puts the keys and values of new tokens ([tokens, kv_heads, dim]) into a
@@ -399,46 +227,8 @@ def kv_append(k, v, positions, seqs, page_table, k_cache, v_cache, q=None, q_out
     A negative position is padding and writes nothing.  A token whose
     sequence, position or page does not exist writes no cache; its queries
     become NaN.  Returns ``q_out``."""
-    T = _T()
-    dtype = k.dtype
-    code = T.code.get(dtype)
-    if code is None:
-        raise ValueError(f"keys are bfloat16, float16 or float32 (got {dtype})")
-    dev = _current(k, T)
-    shape = k.shape
-    if len(shape) != 3:
-        raise ValueError(f"k has shape {tuple(shape)}, expected (tokens, heads, dim)")
-    n, hk, d = shape
-    kp, k0, k1 = _heads(k, "k", shape, dtype, dev)
-    vp, v0, v1 = _heads(v, "v", shape, dtype, dev)
-    hq = qp = q0 = q1 = op = o0 = o1 = 0
-    if q is not None:
-        if q_out is None:
-            raise ValueError("q needs q_out")
-        qp, q0, q1 = _heads(q, "q", (n, None, d), dtype, dev)
-        hq = q.shape[1]
-        op, o0, o1 = _heads(q_out, "q_out", (n, hq, d), dtype, dev)
-    elif q_out is not None:
-        raise ValueError("q_out needs q")
-    rot = cos_rows = cs = 0
-    if cos_sin is not None:
-        if cos_sin.get_device() != dev:
-            _refuse_device(cos_sin, "cos_sin", dev)
-        if cos_sin.dtype not in T.f32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
-            raise ValueError(f"cos_sin must be a contiguous float32 (positions, rotary_dim) tensor "
-                             f"(got {cos_sin.dtype} {tuple(cos_sin.shape)})")
-        cos_rows, rot = cos_sin.shape
-        cs = cos_sin.data_ptr()
-    shape = k_cache.shape
-    if len(shape) != 4 or shape[2] != hk or shape[3] != d:
-        raise ValueError(f"k_cache has shape {tuple(shape)}, expected (pages, page size, {hk}, {d})")
-    table, table_rows, table_width, table_stride = _table(page_table, None, dev, T)
-    block = _APPEND.pack(
-        qp, kp, vp, op, _vector(positions, "positions", n, T.i32, dev), _vector(seqs, "seqs", n, T.i32, dev), table, cs,
-        *_cache(k_cache, "k_cache", shape, dtype, dev), *_cache(v_cache, "v_cache", shape, dtype, dev), q0, q1, k0, k1,
-        v0, v1, o0, o1, n, table_rows, table_width, table_stride, cos_rows, shape[0], shape[1], hq, hk, d, rot,
-        1 if interleaved else 0, code, 0)
-    status = _lib().dc_kv_append(block, _stream(stream, dev, T))
+    status = (_module or _binding()).kv_append(k, v, positions, seqs, page_table, k_cache, v_cache, q, q_out, cos_sin,
+                                               interleaved, stream)
     if status:
         _dc._check(status)
     return q_out
@@ -472,39 +262,8 @@ def paged_attention(q, k_cache, v_cache, page_table, lengths, out, workspace, sc
     A length of 0 gives zeros (lse -inf).  A page number outside the cache, or
     a length past the table, gives NaN.  ``workspace``: see
     :func:`attention_workspace`.  Returns ``out``."""
-    T = _T()
-    dtype = q.dtype
-    code = T.code.get(dtype)
-    if code is None or code == 2:
-        raise ValueError(f"queries are bfloat16 or float16 (got {dtype})")
-    dev = _current(q, T)
-    shape = q.shape
-    if len(shape) != 3:
-        raise ValueError(f"q has shape {tuple(shape)}, expected (sequences, heads, dim)")
-    n, hq, d = shape
-    qp, q0, q1 = _heads(q, "q", shape, dtype, dev)
-    op, o0, o1 = _heads(out, "out", shape, dtype, dev)
-    cache = k_cache.shape
-    if len(cache) != 4 or cache[3] != d:
-        raise ValueError(f"k_cache has shape {tuple(cache)}, expected (pages, page size, heads, {d})")
-    table, _, table_width, table_stride = _table(page_table, n, dev, T)
-    lse_ptr = 0
-    if lse is not None:
-        if lse.get_device() != dev:
-            _refuse_device(lse, "lse", dev)
-        if lse.dtype not in T.f32 or lse.shape != (n, hq) or not lse.is_contiguous():
-            raise ValueError(f"lse must be a contiguous float32 ({n}, {hq}) tensor (got {lse.dtype} {tuple(lse.shape)})")
-        lse_ptr = lse.data_ptr()
-    if workspace.get_device() != dev:
-        _refuse_device(workspace, "workspace", dev)
-    if not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    block = _ATTEND.pack(
-        qp, op, lse_ptr, table, _vector(lengths, "lengths", n, T.i32, dev), workspace.data_ptr(), workspace.nbytes,
-        *_cache(k_cache, "k_cache", cache, dtype, dev), *_cache(v_cache, "v_cache", cache, dtype, dev), q0, q1, o0, o1,
-        n, table_width, table_stride, cache[0], cache[1], hq, cache[2], d, window, code,
-        d ** -0.5 if scale is None else scale, 0)
-    status = _lib().dc_paged_attention(block, _stream(stream, dev, T))
+    status = (_module or _binding()).paged_attention(q, k_cache, v_cache, page_table, lengths, out, workspace, scale, window,
+                                                     lse, stream)
     if status:
         _dc._check(status)
     return out
