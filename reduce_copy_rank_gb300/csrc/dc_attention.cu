@@ -7,7 +7,7 @@
 // running maximum rounded up to a whole number: changing it multiplies by a
 // power of two, which rounds nothing, so a result depends only on the order
 // in which the terms are added.  That order is one binary tree over leaves of
-// 64 tokens (more for very long sequences), fixed by n alone; how large a
+// 32 to 128 tokens (more in very long sequences), fixed by n alone; how large a
 // subtree a warp, a CTA or a group of CTAs computes is free, and follows from
 // how much work there is.  So neither the rest of the batch nor the grid
 // changes a bit.  The last CTA to finish joins what is left of the tree.
@@ -52,10 +52,36 @@ struct Shape {
   static constexpr bool kQueryShared = D > 128;
   static constexpr int kHeld = kInRegs ? 0 : kAttendWarps * kLevels * kValues * 32 * 4;
   static constexpr int kBytes = kRing + kHeld + (kQueryShared ? HB * kRow : 0);
+  static constexpr int kCtas = D <= 64 && HB == 8 ? 3 : D <= 128 ? 2 : 1;  // per SM
 };
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+
+// Shared memory of CTA `rank` of the cluster, at this CTA's address `a`.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t a, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t a, uint32_t rank) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(cluster_addr(a, rank))
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 ld_cluster2(uint32_t a, uint32_t rank) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(cluster_addr(a, rank)) : "memory");
+  return v;
+}
+// All threads of the cluster.
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 
 // 16 bytes global -> shared, or 16 zero bytes (nothing is read then).
@@ -140,6 +166,12 @@ __device__ __forceinline__ void join(const Run<NV, R>& a, Run<NV, R>& b) {
   }
 }
 
+// The sum of 8 values as the tree of them.
+template <class F>
+__device__ __forceinline__ float tree8(F x) {
+  return ((x(0) + x(1)) + (x(2) + x(3))) + ((x(4) + x(5)) + (x(6) + x(7)));
+}
+
 // The sum of 16 values as the tree of them.
 template <class F>
 __device__ __forceinline__ float tree16(F x) {
@@ -201,7 +233,7 @@ __device__ __forceinline__ bool arrive_last(uint32_t* counter, uint32_t n, uint3
 }
 
 template <int DT, int D, int HB>
-__global__ __launch_bounds__(kThreads) void dc_attend_kernel(const __grid_constant__ AttendParams p) {
+__global__ __launch_bounds__(kThreads, Shape<D, HB>::kCtas) void dc_attend_kernel(const __grid_constant__ AttendParams p) {
   using S = Shape<D, HB>;
   constexpr int R = HB / 8;
   using State = Run<S::kValues, R>;
@@ -211,8 +243,9 @@ __global__ __launch_bounds__(kThreads) void dc_attend_kernel(const __grid_consta
   __shared__ uint32_t last_flag;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 
-  const uint32_t piece = blockIdx.x % static_cast<uint32_t>(p.pieces);
-  const uint32_t unit = blockIdx.x / static_cast<uint32_t>(p.pieces);  // (sequence, key head, head block)
+  __shared__ float2 c_rl[HB];  // this CTA's piece, for its cluster
+  const uint32_t piece = blockIdx.x % static_cast<uint32_t>(p.places);
+  const uint32_t unit = blockIdx.x / static_cast<uint32_t>(p.places);  // (sequence, key head, head block)
   const int hb = static_cast<int>(unit % static_cast<uint32_t>(p.head_blocks));
   const int kh = static_cast<int>(unit / static_cast<uint32_t>(p.head_blocks) % static_cast<uint32_t>(p.kv_heads));
   const int seq = static_cast<int>(unit / static_cast<uint32_t>(p.head_blocks) / static_cast<uint32_t>(p.kv_heads));
@@ -233,6 +266,7 @@ __global__ __launch_bounds__(kThreads) void dc_attend_kernel(const __grid_consta
   const uint32_t small = attend_pieces(n, 0);     // pieces of one leaf per warp
   const uint32_t level = attend_level(small, static_cast<uint32_t>(p.units), S::kLevels);
   const uint32_t pieces = attend_pieces(n, level);
+  const bool in_cluster = p.cluster > 1 && pieces > 1;  // the unit's CTAs are one cluster
   if (piece >= pieces) {
     if (piece == 0) {  // nothing to attend to: zeros
       for (int i = threadIdx.x; i < nh * (D / 2); i += kThreads) {
@@ -245,8 +279,14 @@ __global__ __launch_bounds__(kThreads) void dc_attend_kernel(const __grid_consta
         if (in_bounds(a, 4, p.lse, p.lse + 4ull * p.seqs * p.q_heads, kSiteOut)) *a = neg_inf();
       }
     }
+    if (in_cluster) {  // (all of a cluster take part in its two barriers)
+      cluster_barrier();
+      cluster_barrier();
+    }
     return;
   }
+  uint32_t qf[S::kQueryShared ? 1 : kSteps][2 * R];
+  uint8_t* const q_smem = smem + S::kRing + S::kHeld;
   // this warp's tokens [t0, t1): a subtree of 2^level leaves
   const uint32_t run = leaf << level;
   const uint64_t first = static_cast<uint64_t>(start) + (static_cast<uint64_t>(piece) * kAttendWarps + warp) * run;
@@ -333,8 +373,6 @@ __global__ __launch_bounds__(kThreads) void dc_attend_kernel(const __grid_consta
   // query fragments: rows 0..7 heads h0.., rows 8..15 heads h0 + 8.. (HB 16);
   // of heads above 128 they stay in shared memory (in registers they spilled:
   // 1800 cycles a tile for q.k at D = 256)
-  uint32_t qf[S::kQueryShared ? 1 : kSteps][2 * R];
-  uint8_t* const q_smem = smem + S::kRing + S::kHeld;
   {
     const uint64_t q_seq = p.q + static_cast<uint64_t>(seq) * p.q_seq + static_cast<uint64_t>(h0) * p.q_head;
     if constexpr (S::kQueryShared) {
@@ -618,17 +656,50 @@ __global__ __launch_bounds__(kThreads) void dc_attend_kernel(const __grid_consta
                                  (x[0].z * f[0] + x[1].z * f[1]) + (x[2].z * f[2] + x[3].z * f[3]),
                                  (x[0].w * f[0] + x[1].w * f[1]) + (x[2].w * f[2] + x[3].w * f[3]));
     if (pieces == 1) st_result<DT, D>(p, seq, h0 + h, d, v, M, l4);
-    else st_piece<D, HB>(w, piece, piece, h, d, v, M, l4);
+    else if (in_cluster) {
+      // for the cluster: in place of what this thread alone has read
+      *reinterpret_cast<float4*>(wo + h * D + d) = v;
+      if (d == 0) c_rl[h] = make_float2(M, l4);
+    } else st_piece<D, HB>(w, piece, piece, h, d, v, M, l4);
   }
   if (pieces == 1) return;
 
-  // the last of 16 neighbouring pieces joins them, the last such group the groups
   uint32_t* counters = reinterpret_cast<uint32_t*>(p.counters) + static_cast<uint64_t>(unit) * kAttendCounters;
+  if (in_cluster) {
+    // the pieces are one cluster's CTAs: each joins a share of the columns
+    // from all of them, through shared memory
+    const uint32_t count = pieces, rank = piece;
+    cluster_barrier();
+    const uint32_t wo_at = smem_addr(wo), rl_at = smem_addr(c_rl);
+    for (int i = static_cast<int>(rank) * kThreads + threadIdx.x; i < nh * (D / 4); i += static_cast<int>(count) * kThreads) {
+      const int h = i / (D / 4), d = i % (D / 4) * 4;
+      float4 x[kAttendCluster];
+      float2 rl[kAttendCluster];
+#pragma unroll
+      for (uint32_t k = 0; k < kAttendCluster; ++k) {
+        x[k] = k < count ? ld_cluster4(wo_at + static_cast<uint32_t>(h * D + d) * 4, k) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        rl[k] = k < count ? ld_cluster2(rl_at + h * 8, k) : make_float2(neg_inf(), 0.0f);
+      }
+      float M = rl[0].x, f[kAttendCluster];
+#pragma unroll
+      for (int k = 1; k < kAttendCluster; ++k) M = fmaxf(M, rl[k].x);
+#pragma unroll
+      for (int k = 0; k < kAttendCluster; ++k) f[k] = pow2_diff(rl[k].x, M);
+      const float l8 = tree8([&](int k) { return rl[k].y * f[k]; });
+      const float4 v = make_float4(tree8([&](int k) { return x[k].x * f[k]; }), tree8([&](int k) { return x[k].y * f[k]; }),
+                                   tree8([&](int k) { return x[k].z * f[k]; }), tree8([&](int k) { return x[k].w * f[k]; }));
+      st_result<DT, D>(p, seq, h0 + h, d, v, M, l8);
+    }
+    cluster_barrier();  // no CTA leaves while another reads its shared memory
+    return;
+  }
+
+  // the last of 16 neighbouring pieces joins them, the last such group the groups
   const uint32_t groups = (pieces + kAttendJoin - 1) / kAttendJoin;
   uint32_t base = piece / kAttendJoin * kAttendJoin, step = 1;
   uint32_t count = min(static_cast<uint32_t>(kAttendJoin), pieces - base);
-  if (!arrive_last(counters + 1 + piece / kAttendJoin, count, &last_flag)) return;
-  while (true) {
+  bool last = arrive_last(counters + 1 + piece / kAttendJoin, count, &last_flag);
+  while (last) {
     const bool done = step > 1 || groups == 1;
     for (int i = threadIdx.x; i < nh * (D / 4); i += kThreads) {
       const int h = i / (D / 4), d = i % (D / 4) * 4;
@@ -656,7 +727,7 @@ __global__ __launch_bounds__(kThreads) void dc_attend_kernel(const __grid_consta
       else st_piece<D, HB>(w, base, p.pieces + base / kAttendJoin, h, d, v, M, l16);
     }
     if (done) return;
-    if (!arrive_last(counters, groups, &last_flag)) return;
+    last = arrive_last(counters, groups, &last_flag);
     base = 0;
     step = kAttendJoin;
     count = groups;
@@ -677,7 +748,28 @@ cudaError_t launch_one(const AttendParams& p, bool pdl, cudaStream_t s, int grid
     if (e != cudaSuccess) return e;
     allowed.fetch_or(bit, std::memory_order_relaxed);
   }
-  return launch_ex(dc_attend_kernel<DT, D, HB>, grid, kThreads, pdl, s, p, kSmem);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  unsigned n = 0;
+  if (p.cluster > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = static_cast<unsigned>(p.cluster);
+    attr[n].val.clusterDim.y = 1;
+    attr[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  if (pdl) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
+  }
+  cfg.attrs = n ? attr : nullptr;
+  cfg.numAttrs = n;
+  return cudaLaunchKernelEx(&cfg, dc_attend_kernel<DT, D, HB>, p);
 }
 
 template <int DT, int D>
@@ -699,7 +791,7 @@ cudaError_t launch_dim(const AttendParams& p, int dim, bool pdl, cudaStream_t s,
 }  // namespace
 
 cudaError_t launch_attend(const AttendParams& p, int dtype, int dim, bool pdl, cudaStream_t s, int* grid) {
-  *grid = p.seqs * p.kv_heads * p.head_blocks * p.pieces;
+  *grid = p.seqs * p.kv_heads * p.head_blocks * p.places;
   return dtype == kF16 ? launch_dim<kF16>(p, dim, pdl, s, *grid) : launch_dim<kBF16>(p, dim, pdl, s, *grid);
 }
 

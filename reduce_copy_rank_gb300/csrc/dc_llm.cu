@@ -228,7 +228,8 @@ dc_status_t plan_attend(int64_t seqs, int q_heads, int kv_heads, int dim, uint64
   // with fewer may be cut finer
   const uint32_t n = static_cast<uint32_t>(max_tokens);
   const uint32_t most = n > 512 * 128 ? kAttendMaxPieces
-                                      : std::max(attend_pieces(n, 0), attend_pieces(std::min(n, kAttendShort), 0));
+                                      : std::max({attend_pieces(n, 0), attend_pieces(std::min(n, kAttendShort), 0),
+                                                  attend_pieces(std::min(n, kAttendTiny), 0)});
   const int levels = attend_levels(dim, a->hb);
   a->pieces = 1;
   for (uint32_t s = 1; s <= most; ++s) {
@@ -519,6 +520,15 @@ dc_status_t dc_paged_attention(const dc_paged_attention_t* a, dc_stream_t stream
   p.window = a->window;
   p.units = static_cast<int32_t>(plan.units);
   p.pieces = static_cast<int32_t>(plan.pieces);
+  // Few CTAs, all resident at once, and few enough pieces: a unit's CTAs are a
+  // cluster and join them in shared memory.  Measured, us, workspace / cluster:
+  // one sequence of 1025 tokens, 8/1 heads of 128 (5 pieces): 8.2 / 6.9; of 4096
+  // (16 pieces, two clusters and the workspace): 8.1 / 10.
+  const uint32_t resident = static_cast<uint32_t>(sms) * (a->dim <= 128 ? 2u : 1u);
+  const uint32_t c = plan.pieces > 4 ? 8u : plan.pieces > 2 ? 4u : 2u;
+  const bool cluster = plan.pieces > 1 && plan.pieces <= c && plan.units * c <= resident;
+  p.cluster = cluster ? static_cast<int32_t>(c) : 1;
+  p.places = cluster ? static_cast<int32_t>(c) : p.pieces;
   p.page_shift = (p.page_size & (p.page_size - 1)) == 0 ? __builtin_ctz(p.page_size) : -1;
   p.scale = a->scale;
   int grid = 0;

@@ -107,8 +107,9 @@ cudaError_t launch_append(const AppendParams& p, int dtype, int sms, bool pdl, c
 constexpr int kAttendWarps = 4;
 constexpr int kAttendTile = 16;       // tokens a warp takes at a time
 constexpr int kAttendJoin = 16;       // pieces that one CTA joins at a time
+constexpr int kAttendCluster = 8;     // most CTAs of a cluster, which join their pieces in shared memory
 constexpr int kAttendGroups = 8;      // groups of them, at most (128 pieces)
-constexpr int kAttendCounters = 1 + kAttendGroups;  // arrival counters of a unit: of its groups, and of each group's pieces
+constexpr int kAttendCounters = 9;    // arrival counters of a unit: of its groups, and of each group's pieces
 
 struct AttendParams {
   uint64_t q, q_seq, q_head;            // bytes
@@ -124,6 +125,8 @@ struct AttendParams {
   int32_t window;
   int32_t units;                        // seqs * kv_heads * head_blocks
   int32_t pieces;                       // most pieces of one sequence
+  int32_t places;                       // CTAs of a unit: pieces, or the cluster they fit in
+  int32_t cluster;                      // places, or 1: pieces are joined through the workspace
   int32_t page_shift;                   // log2 of the page size, -1 if it is no power of two
   float scale;
   PagedView kc, vc;
@@ -133,14 +136,16 @@ struct AttendParams {
 // tokens, at most 512 of them; a warp takes 2^level neighbouring leaves and a
 // CTA four neighbouring warps' (a piece).  The leaves are a function of n
 // alone, the level of how much work there is.
-// Leaves of 64 tokens up to 8192, 128 above: a leaf costs a climb up the tree,
-// and long sequences have leaves enough.  Measured, us (64 throughout / 128
-// above 8192 / 128 above 4096 tokens): one sequence of 16384 tokens, 32/8
-// heads of 128: 22.7 / 19.3 / 19.3; 128 ragged ones up to 8192: 347 / 347 / 339;
-// 32 up to 8000, 64/8 heads of 64: 54 / 54 / 63; 16/4 heads of 256: 104 / 104 / 113.
-constexpr uint32_t kAttendShort = 8192;
+// Leaves of 32 tokens up to 1024, which a cluster's 32 warps share, of 64 up to
+// 8192 and 128 above: a leaf costs a climb up the tree, and long sequences have
+// leaves enough.  Measured, us.  64 / 32 up to 1024: one sequence of 1024
+// tokens, 32/8 heads of 128: 7.2 / 5.9; 64 ragged ones up to 1024: 33.5 / 35.9.
+// 64 throughout / 128 above 8192 / 128 above 4096: one of 16384: 22.7 / 19.3 /
+// 19.3; 128 ragged ones up to 8192: 347 / 347 / 339; 32 up to 8000, 64/8 heads
+// of 64: 54 / 54 / 63; 16/4 heads of 256: 104 / 104 / 113.
+constexpr uint32_t kAttendTiny = 1024, kAttendShort = 8192;
 __host__ __device__ inline uint32_t attend_leaf(uint32_t n) {
-  uint32_t leaf = n <= kAttendShort ? 64 : 128;
+  uint32_t leaf = n <= kAttendTiny ? 32 : n <= kAttendShort ? 64 : 128;
   while (n / leaf > 512 || (n / leaf == 512 && n % leaf)) leaf *= 2;
   return leaf;
 }
@@ -148,7 +153,7 @@ __host__ __device__ inline uint32_t attend_pieces(uint32_t n, uint32_t level) {
   const uint32_t leaf = attend_leaf(n), leaves = n / leaf + (n % leaf != 0), per = 4u << level;
   return (leaves + per - 1) / per;
 }
-constexpr uint32_t kAttendMaxPieces = kAttendJoin * kAttendGroups;  // 512 leaves, one a warp
+constexpr uint32_t kAttendMaxPieces = 128;  // 512 leaves, one a warp
 // Levels that a warp can hold: waiting subtrees live in registers up to a
 // head size of 128 and in shared memory above.
 __host__ __device__ constexpr int attend_levels(int dim, int hb) { return hb == 8 || dim <= 64 ? 2 : 1; }

@@ -417,3 +417,28 @@ def test_append_refusals():
     assert dc.launch_count() == before
     dc.kv_append(k[:0], v[:0], pos[:0], seqs[:0], table, kc, vc)
     assert dc.launch_count() == before
+
+
+def test_one_long_sequence_among_short_ones():
+    """Many sequences and one far longer."""
+    lengths = [70001] + [40 + 7 * b for b in range(39)]
+    q, kc, vc, table, lengths = build(lengths, 8, 8, 64, 64, "f16", spare=1)
+    got = attend(q, kc, vc, table, lengths)
+    check(got, q, kc, vc, table, lengths, dtype="f16")
+    one = attend(q[:1], kc, vc, table[:1], lengths[:1])
+    assert torch.equal(got[0][:1], one[0]) and torch.equal(got[1][:1], one[1])
+
+
+@pytest.mark.parametrize("hq,hk,d", [(4, 1, 64), (8, 2, 128), (16, 1, 128), (6, 2, 192), (32, 1, 256), (6, 2, 96)])
+def test_bits_do_not_depend_on_the_grid(hq, hk, d):
+    """A sequence alone (pieces joined in a cluster or by the last to finish),
+    in a small batch and in one that fills the GPU several times."""
+    q, kc, vc, table, lengths = build([3000, 700, 257, 5000, 64, 9000], hq, hk, d, 16)
+    want = attend(q, kc, vc, table, lengths)
+    for copies in (2, 9, 60):
+        many = attend(q.repeat(copies, 1, 1), kc, vc, table.repeat(copies, 1), lengths.repeat(copies))
+        for i in (0, copies - 1):
+            assert torch.equal(many[0][6 * i:6 * i + 6], want[0]) and torch.equal(many[1][6 * i:6 * i + 6], want[1]), copies
+    for b in range(6):
+        one = attend(q[b:b + 1], kc, vc, table[b:b + 1], lengths[b:b + 1])
+        assert torch.equal(one[0][0], want[0][b]) and torch.equal(one[1][0], want[1][b]), b
