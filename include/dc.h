@@ -422,6 +422,9 @@ typedef struct {
  * A negative position marks padding: nothing is written for it.  A token
  * whose sequence, position or page does not exist leaves the cache alone and
  * its q_out row is NaN.  Two tokens for one slot: either may remain.
+ * The caches may be interleaved in one tensor (pages of keys beside pages of
+ * values); what a call writes must not fold onto itself (a broadcast q_out or
+ * cache) or overlap what it reads (DC_ERR_OVERLAP).
  */
 typedef struct {
     const void *q;

@@ -18,6 +18,15 @@
 // memory by cp.async and never waited for.  A warp owns 16 tokens at a time
 // with a ring of its own: no barrier until its subtree is done.
 //
+// Where a unit's pieces fit one cluster and the GPU has room, its CTAs join them
+// through shared memory; else through the workspace, the last to arrive doing
+// it.  Measured on GB300 (copy rate 6.78 TB/s): 128 ragged sequences up to 8192
+// tokens, 32/8 heads of 128: 349 us, 6.3 TB/s; one of 131072, 64/8 heads: 94 us,
+// 5.7 TB/s; one of 1024, 32/8 heads: 5.6 us.  What is left is latency: a piece of
+// 256 tokens spends 0.35 us on its length, 1.3 on its page, query and first
+// copies, 2.4 on its tiles (16 cp.async hold a warp for 450 of a tile's 1200
+// cycles) and 0.6 on its end, and 8 warps an SM are all that registers allow.
+//
 // Rounding.  The weights 2^(s-r) enter the second product as a pair of 16-bit
 // numbers hi + lo (hi the weight cut to 16 bits, lo the rounded rest), so
 // that the output carries one rounding to 16 bits, the last.  With at most 8

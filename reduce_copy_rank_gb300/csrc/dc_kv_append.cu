@@ -12,7 +12,9 @@
 // it when there are few): a thread owns one position in the head across query,
 // key and value heads, so its cos and sin stay in registers; all its loads are
 // issued before the token's place is looked up, which costs two dependent
-// reads.
+// reads.  Measured on GB300 (copy rate 6.78 TB/s): 8191 tokens, 32 + 8 + 8 heads
+// of 128: 37 us, 5.6 TB/s; 32 + 32 + 32 heads of 80: 43 us, 5.8 TB/s; 64 tokens
+// of 32 + 8 + 8 heads of 128: 2.2 us.
 #include "dc_llm.h"
 #include "dc_numeric.cuh"
 

@@ -169,8 +169,30 @@ dc_status_t check_tokens(const void* p, const char* name, uint64_t n, int heads,
   return take(p, name, (last + static_cast<uint64_t>(dim)) * es, 16, to);
 }
 
+// Whether elements of a strided tensor share memory: dimensions of n[i]
+// entries every stride[i] elements around `inner` contiguous ones.
+bool folds(const uint64_t* n, const uint64_t* stride, int dims, uint64_t inner) {
+  int order[4] = {0, 1, 2, 3};
+  std::sort(order, order + dims, [&](int a, int b) { return stride[a] < stride[b]; });
+  uint64_t extent = inner;
+  for (int i = 0; i < dims; ++i) {
+    const int d = order[i];
+    if (n[d] < 2) continue;
+    if (stride[d] < extent) return true;
+    extent += (n[d] - 1) * stride[d];
+  }
+  return false;
+}
+
+// A written [n, heads, dim] tensor must not fold onto itself.
+dc_status_t check_written(const char* name, uint64_t n, int heads, int dim, uint64_t tok, uint64_t head) {
+  const uint64_t count[2] = {n, static_cast<uint64_t>(heads)}, stride[2] = {tok, head};
+  if (folds(count, stride, 2, static_cast<uint64_t>(dim))) return fail(DC_ERR_OVERLAP, "%s: its rows overlap", name);
+  return DC_OK;
+}
+
 dc_status_t check_cache(const dc_paged_cache_t& c, const char* name, int64_t pages, int page_size, int heads, int dim,
-                        int es, PagedView* v, Spans& to) {
+                        int es, bool written, PagedView* v, Spans& to) {
   if (pages < 1 || pages > 0x7FFFFFFF) return fail(DC_ERR_INVALID, "%lld pages", static_cast<long long>(pages));
   if (page_size < 1) return fail(DC_ERR_INVALID, "page_size = %d is not positive", page_size);
   const uint64_t st[3] = {c.page_stride, c.token_stride, c.head_stride};
@@ -181,6 +203,7 @@ dc_status_t check_cache(const dc_paged_cache_t& c, const char* name, int64_t pag
     if (n[i] > 1 && st[i] * es % 16) return fail(DC_ERR_ALIGN, "%s: strides must be multiples of 16 bytes", name);
     if (n[i] > 1) last += (n[i] - 1) * st[i];
   }
+  if (written && folds(n, st, 3, static_cast<uint64_t>(dim))) return fail(DC_ERR_OVERLAP, "%s: its tokens overlap", name);
   DC_TRY(take(c.data, name, (last + static_cast<uint64_t>(dim)) * es, 16, to));
   *v = PagedView{addr(c.data), st[0] * es, st[1] * es, st[2] * es, to[to.n - 1].lo, to[to.n - 1].hi};
   return DC_OK;
@@ -303,6 +326,14 @@ dc_status_t dc_token_logprobs(const dc_token_logprobs_t* a, dc_stream_t stream) 
   while (p.cluster < kScoreMaxCluster && p.cluster * kScoreWarps < p.nseg &&
          n * static_cast<uint64_t>(p.cluster) < 2 * static_cast<uint64_t>(sms))
     p.cluster *= 2;
+  // a row of few segments: a CTA of as many warps; of a few more than 8 leave
+  // idle in their last round (9 segments take 16 warps' time): 4, where there
+  // are rows enough to fill the GPU so (alternatives cost a CTA more than that saves)
+  p.warps = kScoreWarps;
+  while (p.warps > 1 && p.warps / 2 >= p.nseg) p.warps /= 2;
+  const auto slots = [&](int w) { return (p.nseg + w - 1) / w * w; };
+  if (p.top == 0 && p.cluster == 1 && p.warps == kScoreWarps && n >= 6 * static_cast<uint64_t>(sms) && 8 * slots(8) >= 9 * slots(4))
+    p.warps = kScoreWarps / 2;
   if (n * static_cast<uint64_t>(p.cluster) > 0x7FFFFFFFull)
     return fail(DC_ERR_INVALID, "%lld rows exceed a grid", static_cast<long long>(a->rows));
   int grid = 0;
@@ -399,8 +430,8 @@ dc_status_t dc_kv_append(const dc_kv_append_t* a, dc_stream_t stream) {
       return fail(DC_ERR_INVALID, "cos_sin has %lld rows", static_cast<long long>(a->cos_sin_rows));
     DC_TRY(take(a->cos_sin, "cos_sin", static_cast<uint64_t>(a->cos_sin_rows) * a->rotary_dim * 4, 4, in));
   }
-  DC_TRY(check_cache(a->k_cache, "k_cache", a->num_pages, a->page_size, a->kv_heads, a->dim, es, &p.kc, cache));
-  DC_TRY(check_cache(a->v_cache, "v_cache", a->num_pages, a->page_size, a->kv_heads, a->dim, es, &p.vc, cache));
+  DC_TRY(check_cache(a->k_cache, "k_cache", a->num_pages, a->page_size, a->kv_heads, a->dim, es, true, &p.kc, cache));
+  DC_TRY(check_cache(a->v_cache, "v_cache", a->num_pages, a->page_size, a->kv_heads, a->dim, es, true, &p.vc, cache));
   if (a->k_cache.data == a->v_cache.data) return fail(DC_ERR_OVERLAP, "k_cache is v_cache");
   // (the caches may be interleaved in one tensor: their spans may meet)
   for (const Span& c : cache) DC_TRY(check_apart(c, in));
@@ -408,6 +439,7 @@ dc_status_t dc_kv_append(const dc_kv_append_t* a, dc_stream_t stream) {
     Spans q;
     DC_TRY(check_tokens(a->q, "q", n, a->q_heads, a->dim, a->q_token_stride, a->q_head_stride, es, q));
     DC_TRY(check_tokens(a->q_out, "q_out", n, a->q_heads, a->dim, a->q_out_token_stride, a->q_out_head_stride, es, out));
+    DC_TRY(check_written("q_out", n, a->q_heads, a->dim, a->q_out_token_stride, a->q_out_head_stride));
     const bool same = a->q == a->q_out && a->q_token_stride == a->q_out_token_stride &&
                       a->q_head_stride == a->q_out_head_stride;
     if (!same) {
@@ -481,9 +513,10 @@ dc_status_t dc_paged_attention(const dc_paged_attention_t* a, dc_stream_t stream
   AttendParams p{};
   DC_TRY(check_tokens(a->q, "q", n, a->q_heads, a->dim, a->q_seq_stride, a->q_head_stride, 2, in));
   DC_TRY(take(a->lengths, "lengths", n * 4, 4, in));
-  DC_TRY(check_cache(a->k_cache, "k_cache", a->num_pages, a->page_size, a->kv_heads, a->dim, 2, &p.kc, in));
-  DC_TRY(check_cache(a->v_cache, "v_cache", a->num_pages, a->page_size, a->kv_heads, a->dim, 2, &p.vc, in));
+  DC_TRY(check_cache(a->k_cache, "k_cache", a->num_pages, a->page_size, a->kv_heads, a->dim, 2, false, &p.kc, in));
+  DC_TRY(check_cache(a->v_cache, "v_cache", a->num_pages, a->page_size, a->kv_heads, a->dim, 2, false, &p.vc, in));
   DC_TRY(check_tokens(a->out, "out", n, a->q_heads, a->dim, a->out_seq_stride, a->out_head_stride, 2, out));
+  DC_TRY(check_written("out", n, a->q_heads, a->dim, a->out_seq_stride, a->out_head_stride));
   if (a->lse) DC_TRY(take(a->lse, "lse", n * static_cast<uint64_t>(a->q_heads) * 4, 4, out));
   const uint64_t head = counter_bytes(a->workspace_bytes);
   if (plan.partial_bytes) {

@@ -18,7 +18,7 @@ namespace dc {
 // vocabulary and its type alone: not on the rows of the call, the shards or
 // the grid.
 __host__ __device__ constexpr int vocab_seg(int dtype) { return dtype == kF32 ? 1024 : 2048; }
-constexpr int kScoreWarps = 8;      // warps per CTA
+constexpr int kScoreWarps = 8;      // most warps per CTA
 constexpr int kScoreMaxCluster = 8; // CTAs that may share a row
 constexpr int kMaxVocab = 1 << 22;  // at most 4096 segments: 64 KB of partials
 constexpr int kMaxTop = 32;         // alternatives: one lane each
@@ -44,6 +44,7 @@ struct ScoreParams {
   int32_t P;
   int32_t nseg;
   int32_t cluster;         // CTAs per row
+  int32_t warps;           // per CTA: a power of two; all of them in a cluster
   int32_t top;
   int32_t tokens64;
   int32_t top64;

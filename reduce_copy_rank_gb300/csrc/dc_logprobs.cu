@@ -15,9 +15,18 @@
 // and logits of any finite size (masks of the type's lowest value) do not
 // overflow.  All of it in binary32.
 //
-// Bound: memory.  The logits are read once (and the gradient written once);
-// an element costs about five instructions, one of them
-// the exponential (pairs of elements share the additions and products).
+// Bound: memory for many rows.  The logits are read once (and the gradient
+// written once); an element costs about five instructions, one of them the
+// exponential: pairs of elements share the additions and products, which took
+// 8192 x 128000 bf16 from 322 to 301 us.  For few rows a cluster of up to 8
+// CTAs shares a row and the time is the chain of one load, one reduction, the
+// cluster's barrier and (with alternatives) the search for them.  Between, a
+// row's CTA spends as long on that chain as on its logits.
+//
+// Measured on GB300 (copy rate 6.78 TB/s), scores: 8192 x 128000 bf16 299 us,
+// 7.0 TB/s; 1021 x 50021 f32 on 3 ranks with 5 alternatives 53 us, 3.9 TB/s; 128
+// x 131072 bf16 on 8 ranks with 20 16 us; 4 x 32768 with 1 6.1 us.  Gradient:
+// 8192 x 127900 bf16 on 8 ranks 610 us, 6.9 TB/s; 509 x 50021 f16 17 us, 5.9 TB/s.
 #include "dc_llm.h"
 #include "dc_numeric.cuh"
 
@@ -101,7 +110,7 @@ __device__ __forceinline__ uint32_t larger_in(const uint64_t* list, uint64_t key
   return n + (list[n] > key ? 1u : 0u);
 }
 
-constexpr uint32_t kFewCandidates = 128;  // of a CTA: a thread each
+constexpr uint32_t kFewCandidates = 256;  // of a CTA
 
 struct TopList {
   uint64_t key;    // this lane's entry of the list, largest in lane 0
@@ -270,6 +279,33 @@ __device__ __forceinline__ float pick(const uint4& v, int i) {
   }
 }
 
+// The entries of a segment that reach the bound, into a warp's own list: the
+// slow way, for rows with many logits near or equal to the bound.  (Out of
+// line: its code and registers are not the common path's.)
+template <int DT>
+__device__ __noinline__ void list_segment(const ScoreParams& p, uint64_t row, int seg, int lane, TopList& top,
+                                          uint64_t* waiting) {
+  using L = SegLoader<DT>;
+  uint4 raw[L::kVecs];
+  int r = 0;
+  L::load(p, row, seg, lane, r, raw);
+  const uint32_t e0 = static_cast<uint32_t>(seg) * L::kSeg;
+#pragma unroll
+  for (int j = 0; j < L::kVecs; ++j)
+#pragma unroll 1
+    for (int i = 0; i < L::kPer; ++i) {  // an entry of every lane at a time: at most 32 join the 31 that wait
+      const float x = pick<DT>(raw[j], i);
+      const bool take = x >= top.thr && e0 + L::index(j, i, lane) < p.vocab;
+      const uint32_t who = __ballot_sync(~0u, take);
+      if (who == 0) continue;
+      if (take)
+        waiting[top.count + __popc(who & ((1u << lane) - 1u))] =
+            (static_cast<uint64_t>(ordered(x)) << 32) | (0xFFFFFFFFu - (e0 + L::index(j, i, lane)));
+      top.count += __popc(who);
+      if (top.count >= 32) flush_candidates(top, waiting, p.top, lane);
+    }
+}
+
 // Two binary32 numbers, added and multiplied by one instruction each.
 struct Two {
   uint64_t v;
@@ -341,14 +377,14 @@ template <int DT, bool TOP>
 __global__ __launch_bounds__(kScoreWarps * 32, 4) void dc_score_kernel(const __grid_constant__ ScoreParams p) {
   using L = SegLoader<DT>;
   extern __shared__ float part[];  // leader: m, s, t of every segment; then (TOP) this CTA's segments' m
-  __shared__ uint64_t cand[TOP ? kScoreWarps : 1][64];
+  __shared__ __align__(16) uint64_t cand[TOP ? kScoreWarps : 1][64];
   __shared__ uint64_t lists[TOP ? kScoreWarps : 1][32];
   __shared__ uint64_t cta_lists[TOP ? kScoreMaxCluster : 1][32];
-  __shared__ float4 maxima[TOP ? kScoreWarps * 2 : 1];
+  __shared__ float4 maxima[TOP ? 32 : 1];  // at most 128 groups
   __shared__ float bound;
   __shared__ uint32_t cta_count;
   __shared__ float row_m, row_log_s;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = static_cast<int>(blockDim.x >> 5);
   const uint32_t cl = static_cast<uint32_t>(p.cluster);
   const uint64_t row = blockIdx.x / cl;
   const int rank = static_cast<int>(blockIdx.x % cl);
@@ -377,7 +413,7 @@ __global__ __launch_bounds__(kScoreWarps * 32, 4) void dc_score_kernel(const __g
   if (TOP && threadIdx.x == 0) cta_count = 0;
   int r_shard = 0;
   bool waited = cl == 1;
-  const int seg0 = rank * kScoreWarps + warp, step = kScoreWarps * static_cast<int>(cl);
+  const int seg0 = rank * warps + warp, step = warps * static_cast<int>(cl);
   int last = -1;
   uint4 raw[L::kVecs];
   for (int seg = seg0; seg < p.nseg; seg += step) {
@@ -420,93 +456,120 @@ __global__ __launch_bounds__(kScoreWarps * 32, 4) void dc_score_kernel(const __g
 
   if constexpr (TOP) {
     // A bound for the k-th largest logit of this CTA's part of the row: the
-    // k-th largest of the maxima of 64 groups of 4 threads, of which k are at
-    // least that.  A second look at the segments that reach it (from L2; the
-    // last one is still in registers) then meets little more than the k
-    // entries that are wanted: 20 of 64 groups hold about the 24 largest.
-    TopList top{0, 0, neg_inf()};
-    float v = fmaxf(thread_max, __shfl_xor_sync(~0u, thread_max, 1));
-    v = fmaxf(v, __shfl_xor_sync(~0u, v, 2));
-    if ((lane & 3) == 0) reinterpret_cast<float*>(maxima)[threadIdx.x >> 2] = v;
+    // k-th largest of the maxima of groups of lanes, of which k are at least
+    // that.  (64 groups or more, of 4 lanes, 2 or 1 as there are warps with
+    // something to look at; one warp's 32 lanes.)  A second look at the
+    // segments that reach it (from L2; the last one is still in registers)
+    // then meets little more than the k entries that are wanted: 20 of 64
+    // groups hold about the 24 largest.
+    const int busy = min(warps, p.nseg - rank * warps);  // warps with a segment (may be negative: none)
+    const int wide = busy >= 8 ? 4 : busy >= 4 ? 2 : 1, groups = busy > 0 ? (busy * 32) >> (wide >> 1) : 0;
+    float v = thread_max;
+    for (int o = 1; o < wide; o <<= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, o));
+    float* const mx = reinterpret_cast<float*>(maxima);
+    if (warp < busy && (lane & (wide - 1)) == 0) mx[static_cast<int>(threadIdx.x) >> (wide >> 1)] = v;
     if (threadIdx.x < 32) lists[0][lane] = 0;
     __syncthreads();
-    if (threadIdx.x < 64) {
-      const float mine = reinterpret_cast<const float*>(maxima)[threadIdx.x];
-      int rank = 0;  // groups before this one, equal ones by their number
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
+    {
+      // a group's place: 4, 2 or 1 threads compare it with a part of the others each
+      const int share = 4 * groups <= static_cast<int>(blockDim.x) ? 4 : 2 * groups <= static_cast<int>(blockDim.x) ? 2 : 1;
+      const int t = static_cast<int>(threadIdx.x) >> (share >> 1), part_of = static_cast<int>(threadIdx.x) & (share - 1);
+      const float mine = t < groups ? mx[t] : 0.0f;
+      int rank_of = 0;  // groups before this one, equal ones by their number
+      for (int i = part_of; i < groups / 4; i += share) {
         const float4 q = maxima[i];
-        const int n = static_cast<int>(threadIdx.x) - 4 * i;
-        rank += (q.x > mine || (q.x == mine && n > 0)) + (q.y > mine || (q.y == mine && n > 1)) +
-                (q.z > mine || (q.z == mine && n > 2)) + (q.w > mine || (q.w == mine && n > 3));
+        const int n = t - 4 * i;
+        rank_of += (q.x > mine || (q.x == mine && n > 0)) + (q.y > mine || (q.y == mine && n > 1)) +
+                   (q.z > mine || (q.z == mine && n > 2)) + (q.w > mine || (q.w == mine && n > 3));
       }
-      if (rank == p.top - 1) bound = mine;
+      for (int o = 1; o < share; o <<= 1) rank_of += __shfl_xor_sync(~0u, rank_of, o);
+      if (t < groups && part_of == 0 && rank_of == p.top - 1) bound = mine;
     }
     __syncthreads();
-    top.thr = bound;
-    // push(lanes that have a candidate, this lane's key): keys of the entries
-    // that reach the bound, from the last segment back
-    auto scan = [&](bool loaded, auto push) {
+    const float thr = bound;
+    // From the last segment back: begin(n) with the candidates of a segment
+    // that each lane has, then put(key) for each of them.  Their keys are the
+    // entries that reach the bound.
+    auto scan = [&](auto begin, auto put) {
       for (int seg = last; seg >= seg0 && seg >= 0; seg -= step) {
-        if (part[3 * p.nseg + seg] < top.thr) continue;
+        if (part[3 * p.nseg + seg] < thr) continue;
         int r = 0;
-        if (!loaded || seg != last) L::load(p, row, seg, lane, r, raw);
+        if (seg != last) L::load(p, row, seg, lane, r, raw);
         const uint32_t e0 = static_cast<uint32_t>(seg) * L::kSeg;
+        static_assert(L::kVecs * L::kPer <= 64, "a bit per entry");
+        uint32_t bits[2] = {0, 0};
 #pragma unroll
         for (int j = 0; j < L::kVecs; ++j) {
-          if (!__any_sync(~0u, !(word_max<DT>(vec_max<DT>(raw[j])) < top.thr))) continue;
+          if (!__any_sync(~0u, !(word_max<DT>(vec_max<DT>(raw[j])) < thr))) continue;
           float x[L::kPer];
           unpack<DT>(raw[j], x);
           uint32_t mask = 0;
 #pragma unroll
           for (int i = 0; i < L::kPer; ++i)
-            if (x[i] >= top.thr && e0 + L::index(j, i, lane) < p.vocab) mask |= 1u << i;
-          while (true) {
-            const uint32_t who = __ballot_sync(~0u, mask != 0);
-            if (who == 0) break;
-            uint64_t key = 0;
-            if (mask != 0) {
-              const int i = __ffs(static_cast<int>(mask)) - 1;
-              mask &= mask - 1;
-              key = (static_cast<uint64_t>(ordered(pick<DT>(raw[j], i))) << 32) |
-                    (0xFFFFFFFFu - (e0 + L::index(j, i, lane)));
-            }
-            push(who, key);
+            if (x[i] >= thr && e0 + L::index(j, i, lane) < p.vocab) mask |= 1u << i;
+          bits[j * L::kPer / 32] |= mask << (j * L::kPer % 32);
+        }
+        begin(__popc(bits[0]) + __popc(bits[1]));
+#pragma unroll
+        for (int j = 0; j < L::kVecs; ++j) {
+          uint32_t mask = (bits[j * L::kPer / 32] >> (j * L::kPer % 32)) & ((1u << L::kPer) - 1u);
+          while (mask != 0) {
+            const int i = __ffs(static_cast<int>(mask)) - 1;
+            mask &= mask - 1;
+            put((static_cast<uint64_t>(ordered(pick<DT>(raw[j], i))) << 32) | (0xFFFFFFFFu - (e0 + L::index(j, i, lane))));
           }
         }
       }
     };
-    // most often the CTA's candidates are few: a thread ranks each of them
-    scan(true, [&](uint32_t who, uint64_t key) {
-      uint32_t at = 0;
-      if (lane == 0) at = atomicAdd(&cta_count, static_cast<uint32_t>(__popc(who)));
-      at = __shfl_sync(~0u, at, 0) + __popc(who & ((1u << lane) - 1u));
-      if (key != 0 && at < kFewCandidates) cand[at / 64][at % 64] = key;
-    });
+    // most often the CTA's candidates are few: each is ranked among all
+    uint32_t at = 0;
+    scan(
+        [&](uint32_t mine) {
+          // the lanes' places: from a vote where no lane has two, else a sum over the lanes
+          const uint32_t who = __ballot_sync(~0u, mine != 0);
+          uint32_t before = __popc(who & ((1u << lane) - 1u)), all = __popc(who);
+          if (__any_sync(~0u, mine > 1)) {
+            uint32_t upto = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+              const uint32_t x = __shfl_up_sync(~0u, upto, o);
+              if (lane >= o) upto += x;
+            }
+            before = upto - mine;
+            all = __shfl_sync(~0u, upto, 31);
+          }
+          if (lane == 0 && all != 0) at = atomicAdd(&cta_count, all);
+          at = __shfl_sync(~0u, at, 0) + before;
+        },
+        [&](uint64_t key) {
+          if (at < kFewCandidates) (&cand[0][0])[at] = key;
+          ++at;
+        });
     __syncthreads();
     const uint32_t found = cta_count;
     if (found <= kFewCandidates) {
-      if (threadIdx.x < found) {
-        const uint64_t* all = &cand[0][0];
-        const uint64_t key = all[threadIdx.x];
-        uint32_t rank = 0;
-        for (uint32_t i = 0; i < found; ++i) rank += all[i] > key ? 1u : 0u;  // (keys are distinct)
-        if (rank < 32) lists[0][rank] = key;
+      const ulonglong2* all = reinterpret_cast<const ulonglong2*>(&cand[0][0]);
+      for (uint32_t t = threadIdx.x; t < found; t += blockDim.x) {
+        const uint64_t key = (&cand[0][0])[t];
+        uint32_t place = 0;
+#pragma unroll 4
+        for (uint32_t i = 0; i < (found + 1) / 2; ++i) {  // (keys are distinct; an odd one's neighbour does not count)
+          const ulonglong2 k2 = all[i];
+          place += (k2.x > key ? 1u : 0u) + (k2.y > key && 2 * i + 1 < found ? 1u : 0u);
+        }
+        if (place < 32) lists[0][place] = key;
       }
       __syncthreads();
     } else {
       // many logits near or equal to the bound: every warp keeps its own list
       __syncthreads();
-      scan(false, [&](uint32_t who, uint64_t key) {
-        if (key != 0) cand[warp][top.count + __popc(who & ((1u << lane) - 1u))] = key;
-        top.count += __popc(who);
-        if (top.count >= 32) flush_candidates(top, cand[warp], p.top, lane);
-      });
+      TopList top{0, 0, thr};
+      for (int seg = seg0; seg < p.nseg; seg += step)
+        if (!(part[3 * p.nseg + seg] < thr)) list_segment<DT>(p, row, seg, lane, top, cand[warp]);
       if (top.count) flush_candidates(top, cand[warp], p.top, lane);
       lists[warp][lane] = top.key;
       __syncthreads();
-#pragma unroll
-      for (int n = kScoreWarps / 2; n > 0; n >>= 1) {
+      for (int n = warps / 2; n > 0; n >>= 1) {
         if (warp < n) {
           top.key = merge_desc(top.key, lists[warp + n][lane], lane);
           lists[warp][lane] = top.key;
@@ -564,7 +627,7 @@ __global__ __launch_bounds__(kScoreWarps * 32, 4) void dc_score_kernel(const __g
   if constexpr (TOP) {
     // a key's place among all lists: its place in its own and how many of
     // each other one are larger
-    static_assert(kScoreMaxCluster * 32 <= kScoreWarps * 32, "a thread per key");
+    static_assert(kScoreMaxCluster <= kScoreWarps, "a thread per key: clusters have CTAs of all warps");
     uint64_t key = 0;
     uint32_t place = lane;
     if (warp < static_cast<int>(cl)) {
@@ -714,7 +777,7 @@ cudaError_t launch_score_t(const ScoreParams& p, int grid, bool pdl, cudaStream_
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(kScoreWarps * 32);
+  cfg.blockDim = dim3(static_cast<unsigned>(p.warps) * 32);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];

@@ -94,7 +94,7 @@ def check(out, x, tokens, temperature=1.0, top=0):
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("rows,vocab,P,top", [
     (1, 1, 1, 1), (3, 2, 2, 2), (2, 31, 1, 5), (5, 2047, 1, 3), (4, 2048, 2, 8), (7, 2049, 3, 32),
-    (1, 50021, 8, 20), (33, 16385, 5, 1), (340, 5003, 1, 4), (700, 3000, 2, 0)])
+    (1, 50021, 8, 20), (33, 16385, 5, 1), (340, 5003, 1, 4), (700, 3000, 2, 0), (50, 1500, 1, 32), (21, 9000, 3, 32), (2, 67187, 1, 32), (3, 20000, 2, 31), (9, 1031, 2, 20)])
 def test_scores(dtype, rows, vocab, P, top):
     x, tokens = logits(rows, vocab, DT[dtype])
     out = score(split(x, uneven(vocab, P)), tokens, top=top)

@@ -146,7 +146,13 @@ def test_grad_checks(kw, want):
     (dict(positions=at(4) + 2), ALIGN), (dict(v_cache=at(8)), OVERLAP), (dict(v_cache=at(8) + 256), CUDA),
     (dict(q_out=at(0)), CUDA), (dict(q_out=at(0), q_out_token_stride=1024), OVERLAP), (dict(q_out=at(1)), OVERLAP),
     (dict(k=at(8)), OVERLAP), (dict(q_out=at(9)), OVERLAP), (dict(page_table=at(8)), OVERLAP),
-    (dict(q_heads=0, q=0, q_out=0), CUDA), (dict(k_page_stride=1 << 62), INVALID)])
+    (dict(q_heads=0, q=0, q_out=0), CUDA), (dict(k_page_stride=1 << 62), INVALID),
+    # written tensors that fold onto themselves: a broadcast dimension, pages or heads that overlap
+    (dict(q_out_token_stride=0), OVERLAP), (dict(q_out_head_stride=32), OVERLAP), (dict(k_page_stride=0), OVERLAP),
+    (dict(v_slot_stride=64), OVERLAP), (dict(k_page_stride=16 * 2 * 64 - 8), OVERLAP),
+    # heads outside tokens, and keys beside values
+    (dict(k_slot_stride=64, k_cache_head_stride=16 * 64), CUDA), (dict(q_out_token_stride=64, q_out_head_stride=7 * 64), CUDA),
+    (dict(k_page_stride=2 * 16 * 2 * 64, v_page_stride=2 * 16 * 2 * 64, v_cache=at(8) + 16 * 2 * 64 * 2), CUDA)])
 def test_append_checks(kw, want):
     assert append(**kw) == want, dc.last_error()
 
@@ -161,7 +167,8 @@ def test_append_checks(kw, want):
     (dict(q=at(0) + 8), ALIGN), (dict(q_head_stride=68), ALIGN), (dict(out=at(0)), OVERLAP), (dict(lse=at(1)), OVERLAP),
     (dict(workspace=at(6)), OVERLAP), (dict(out=at(7)), OVERLAP), (dict(lse=0), CUDA),
     (dict(table_width=1 << 30, page_size=16), INVALID), (dict(seqs=1, table_width=1 << 28, window=1000), CUDA),
-    (dict(seqs=0x7FFFFFFF), INVALID)])
+    (dict(seqs=0x7FFFFFFF), INVALID), (dict(out_seq_stride=0), OVERLAP), (dict(out_head_stride=0), OVERLAP),
+    (dict(k_page_stride=0), CUDA), (dict(q_seq_stride=0), CUDA)])  # what is only read may be broadcast
 def test_attend_checks(kw, want):
     assert attend(**kw) == want, dc.last_error()
 
