@@ -241,7 +241,9 @@ __device__ __forceinline__ bool arrive_last(uint32_t* counter, uint32_t n, uint3
   return *flag != 0;
 }
 
-template <int DT, int D, int HB>
+// LOOP: a unit has fewer CTAs than its longest sequence could have pieces, and
+// a CTA takes every p.places-th of them.
+template <int DT, int D, int HB, bool LOOP>
 __global__ __launch_bounds__(kThreads, Shape<D, HB>::kCtas) void dc_attend_kernel(const __grid_constant__ AttendParams p) {
   using S = Shape<D, HB>;
   constexpr int R = HB / 8;
@@ -253,7 +255,7 @@ __global__ __launch_bounds__(kThreads, Shape<D, HB>::kCtas) void dc_attend_kerne
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 
   __shared__ float2 c_rl[HB];  // this CTA's piece, for its cluster
-  const uint32_t piece = blockIdx.x % static_cast<uint32_t>(p.places);
+  uint32_t piece = blockIdx.x % static_cast<uint32_t>(p.places);
   const uint32_t unit = blockIdx.x / static_cast<uint32_t>(p.places);  // (sequence, key head, head block)
   const int hb = static_cast<int>(unit % static_cast<uint32_t>(p.head_blocks));
   const int kh = static_cast<int>(unit / static_cast<uint32_t>(p.head_blocks) % static_cast<uint32_t>(p.kv_heads));
@@ -296,6 +298,7 @@ __global__ __launch_bounds__(kThreads, Shape<D, HB>::kCtas) void dc_attend_kerne
   }
   uint32_t qf[S::kQueryShared ? 1 : kSteps][2 * R];
   uint8_t* const q_smem = smem + S::kRing + S::kHeld;
+  do {
   // this warp's tokens [t0, t1): a subtree of 2^level leaves
   const uint32_t run = leaf << level;
   const uint64_t first = static_cast<uint64_t>(start) + (static_cast<uint64_t>(piece) * kAttendWarps + warp) * run;
@@ -735,15 +738,17 @@ __global__ __launch_bounds__(kThreads, Shape<D, HB>::kCtas) void dc_attend_kerne
       if (done) st_result<DT, D>(p, seq, h0 + h, d, v, M, l16);
       else st_piece<D, HB>(w, base, p.pieces + base / kAttendJoin, h, d, v, M, l16);
     }
-    if (done) return;
+    if (done) break;
     last = arrive_last(counters, groups, &last_flag);
     base = 0;
     step = kAttendJoin;
     count = groups;
   }
+  if (LOOP) __syncthreads();  // the ring is free for the CTA's next piece
+  } while (LOOP && (piece += static_cast<uint32_t>(p.places)) < pieces);
 }
 
-template <int DT, int D, int HB>
+template <int DT, int D, int HB, bool LOOP>
 cudaError_t launch_one(const AttendParams& p, bool pdl, cudaStream_t s, int grid) {
   constexpr int kSmem = Shape<D, HB>::kBytes;
   static_assert(kSmem + 4096 <= 227 * 1024, "the ring and the waiting subtrees fit");
@@ -753,7 +758,7 @@ cudaError_t launch_one(const AttendParams& p, bool pdl, cudaStream_t s, int grid
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (!(allowed.load(std::memory_order_relaxed) & bit)) {
-    e = cudaFuncSetAttribute(dc_attend_kernel<DT, D, HB>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    e = cudaFuncSetAttribute(dc_attend_kernel<DT, D, HB, LOOP>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     allowed.fetch_or(bit, std::memory_order_relaxed);
   }
@@ -778,12 +783,15 @@ cudaError_t launch_one(const AttendParams& p, bool pdl, cudaStream_t s, int grid
   }
   cfg.attrs = n ? attr : nullptr;
   cfg.numAttrs = n;
-  return cudaLaunchKernelEx(&cfg, dc_attend_kernel<DT, D, HB>, p);
+  return cudaLaunchKernelEx(&cfg, dc_attend_kernel<DT, D, HB, LOOP>, p);
 }
 
 template <int DT, int D>
 cudaError_t launch_hb(const AttendParams& p, bool pdl, cudaStream_t s, int grid) {
-  return attend_head_block(p.group) == 16 ? launch_one<DT, D, 16>(p, pdl, s, grid) : launch_one<DT, D, 8>(p, pdl, s, grid);
+  const bool loop = p.places < p.pieces;
+  if (attend_head_block(p.group) == 16)
+    return loop ? launch_one<DT, D, 16, true>(p, pdl, s, grid) : launch_one<DT, D, 16, false>(p, pdl, s, grid);
+  return loop ? launch_one<DT, D, 8, true>(p, pdl, s, grid) : launch_one<DT, D, 8, false>(p, pdl, s, grid);
 }
 
 template <int DT>

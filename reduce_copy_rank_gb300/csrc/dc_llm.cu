@@ -562,6 +562,11 @@ dc_status_t dc_paged_attention(const dc_paged_attention_t* a, dc_stream_t stream
   const bool cluster = plan.pieces > 1 && plan.pieces <= c && plan.units * c <= resident;
   p.cluster = cluster ? static_cast<int32_t>(c) : 1;
   p.places = cluster ? static_cast<int32_t>(c) : p.pieces;
+  // A table with room for much longer sequences than most are must not flood
+  // the GPU with CTAs that find nothing to do (about 0.5 us each, two at a time
+  // on an SM): beyond four times the CTAs that fill it, a unit's take turns.
+  if (!cluster && plan.pieces > 8 && plan.units * plan.pieces > 4 * kAttendCtas)
+    p.places = static_cast<int32_t>(std::max<uint64_t>(8, std::min<uint64_t>(plan.pieces, 4 * kAttendCtas / plan.units)));
   p.page_shift = (p.page_size & (p.page_size - 1)) == 0 ? __builtin_ctz(p.page_size) : -1;
   p.scale = a->scale;
   int grid = 0;

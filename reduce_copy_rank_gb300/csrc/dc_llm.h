@@ -126,7 +126,7 @@ struct AttendParams {
   int32_t window;
   int32_t units;                        // seqs * kv_heads * head_blocks
   int32_t pieces;                       // most pieces of one sequence
-  int32_t places;                       // CTAs of a unit: pieces, or the cluster they fit in
+  int32_t places;                       // CTAs of a unit: pieces, the cluster they fit in, or fewer that take turns
   int32_t cluster;                      // places, or 1: pieces are joined through the workspace
   int32_t page_shift;                   // log2 of the page size, -1 if it is no power of two
   float scale;

@@ -442,3 +442,16 @@ def test_bits_do_not_depend_on_the_grid(hq, hk, d):
     for b in range(6):
         one = attend(q[b:b + 1], kc, vc, table[b:b + 1], lengths[b:b + 1])
         assert torch.equal(one[0][0], want[0][b]) and torch.equal(one[1][0], want[1][b]), b
+
+
+@pytest.mark.parametrize("seqs,hk", [(1, 1), (3, 8), (40, 8)])
+def test_tables_far_wider_than_the_sequences(seqs, hk):
+    lengths = [(b * 337) % 2900 for b in range(seqs)]
+    lengths[0] = 1500
+    q, kc, vc, table, lengths = build(lengths, 2 * hk, hk, 64, 16)
+    want = attend(q, kc, vc, table, lengths)
+    check(want, q, kc, vc, table, lengths)
+    wide = torch.full((seqs, 8192), -1, dtype=torch.int32, device="cuda")
+    wide[:, :table.shape[1]] = table
+    got = attend(q, kc, vc, wide, lengths)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
