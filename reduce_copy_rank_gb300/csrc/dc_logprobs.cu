@@ -24,7 +24,7 @@
 // row's CTA spends as long on that chain as on its logits.
 //
 // Measured on GB300 (copy rate 6.78 TB/s), scores: 8192 x 128000 bf16 299 us,
-// 7.0 TB/s; 1021 x 50021 f32 on 3 ranks with 5 alternatives 53 us, 3.9 TB/s; 128
+// 7.0 TB/s; 1021 x 50021 f32 on 3 ranks with 5 alternatives 51 us, 4.1 TB/s; 128
 // x 131072 bf16 on 8 ranks with 20 16 us; 4 x 32768 with 1 6.1 us.  Gradient:
 // 8192 x 127900 bf16 on 8 ranks 610 us, 6.9 TB/s; 509 x 50021 f16 17 us, 5.9 TB/s.
 #include "dc_llm.h"
@@ -133,6 +133,16 @@ __device__ __noinline__ void flush_candidates(TopList& t, uint64_t* buf, int k, 
   if (kth != 0) t.thr = fmaxf(t.thr, from_ordered(static_cast<uint32_t>(kth >> 32)));
 }
 
+// Loads where `ok`, without a branch; the rest keep what they hold.
+__device__ __forceinline__ void ld_where(uint32_t& v, uint64_t a, bool ok) {
+  asm volatile("{ .reg .pred q; setp.ne.u32 q, %2, 0; @q ld.global.nc.u32 %0, [%1]; }"
+               : "+r"(v) : "l"(a), "r"(static_cast<uint32_t>(ok)));
+}
+__device__ __forceinline__ void ld16_where(uint4& v, uint64_t a, bool ok) {
+  asm volatile("{ .reg .pred q; setp.ne.u32 q, %5, 0; @q ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4]; }"
+               : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w) : "l"(a), "r"(static_cast<uint32_t>(ok)));
+}
+
 // --------------------------------------------------------- one segment ---
 // How a segment's entries lie in a warp: 16-bit types as 8 vectors of 8
 // entries a lane, vector j at (j * 32 + lane) * 8; binary32 as 32 single
@@ -207,58 +217,102 @@ struct SegLoader {
       }
       return;
     }
-    // a segment that crosses shards or ends the vocabulary: shard by shard,
-    // every load of a shard's part in flight at once
+    // A segment that crosses shards or ends the vocabulary: two shards at a
+    // time, every load of theirs in flight at once (each lane picks the shard
+    // of its entry and loads under a predicate: as branches per shard and
+    // vector they waited for one another; 1024 x 128256 bf16 on 8 ranks, 7 of
+    // 63 segments, 78 us that way and 46 this way).  A vector that a shard's
+    // end cuts is put together by lanes 0..7 (8..15 for the second shard's
+    // end), an entry each.
 #pragma unroll
     for (int j = 0; j < kVecs; ++j)
       raw[j] = make_uint4(Elem<DT>::kNegInfWord, Elem<DT>::kNegInfWord, Elem<DT>::kNegInfWord, Elem<DT>::kNegInfWord);
-    for (int q = r; q < p.P && p.shard[q].first < e0 + kSeg; ++q) {
-      const LogitShard& t = p.shard[q];
-      const uint32_t from = max(e0, t.first), to = min(e0 + kSeg, t.end);
-      const uint64_t at = t.base + row * t.stride - static_cast<uint64_t>(t.first) * Elem<DT>::kBytes;  // column 0
-      const uint64_t end = t.base + (p.rows - 1) * t.stride + static_cast<uint64_t>(t.end - t.first) * Elem<DT>::kBytes;
-      auto one = [&](uint32_t e, uint32_t& w, bool high) {
-        const uint64_t a = at + static_cast<uint64_t>(e) * Elem<DT>::kBytes;
-        if (!in_bounds(reinterpret_cast<const void*>(a), Elem<DT>::kBytes, t.base, end, kSiteLogit)) return;
-        if constexpr (DT == kF32) {
-          w = *reinterpret_cast<const uint32_t*>(a);
-        } else {
-          const uint32_t h = *reinterpret_cast<const uint16_t*>(a);
-          w = high ? (w & 0x0000FFFFu) | (h << 16) : (w & 0xFFFF0000u) | h;
-        }
-      };
+    for (int q = r; q < p.P && p.shard[q].first < e0 + kSeg; q += 2) {
+      const bool pair = q + 1 < p.P;
+      const LogitShard& s0 = p.shard[q];
+      const LogitShard& s1 = p.shard[pair ? q + 1 : q];
+      const uint32_t cut = s0.end, end = pair ? s1.end : s0.end;
+      // addresses of column 0
+      const uint64_t at0 = s0.base + row * s0.stride - static_cast<uint64_t>(s0.first) * Elem<DT>::kBytes;
+      const uint64_t at1 = s1.base + row * s1.stride - static_cast<uint64_t>(s1.first) * Elem<DT>::kBytes;
+      if constexpr (DT == kF32) {
 #pragma unroll
-      for (int j = 0; j < kVecs; ++j) {
-        uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
-        if constexpr (DT == kF32) {
+        for (int j = 0; j < kVecs; ++j) {
+          uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
 #pragma unroll
           for (int i = 0; i < kPer; ++i) {
             const uint32_t e = e0 + index(j, i, lane);
-            if (e >= from && e < to) one(e, w[i], false);
+            const uint64_t x = (e < cut ? at0 : at1) + static_cast<uint64_t>(e) * 4;
+            ld_where(w[i], x, e >= s0.first && e < end && inside(p, e < cut ? s0 : s1, x, 4));
           }
-        } else {
-          const uint32_t e = e0 + index(j, 0, lane);
-          if (e >= from && e + kPer <= to) {
-            const uint64_t a = at + static_cast<uint64_t>(e) * Elem<DT>::kBytes;
-            const uint32_t s = static_cast<uint32_t>(a & 15u);
-            const uint4* b = reinterpret_cast<const uint4*>(a - s);
-            if (in_bounds(b, s ? 32 : 16, hull_lo(t.base), hull_hi(t.base, end - t.base), kSiteLogit)) {
-              uint4 v = ld_nc_cached(b);
-              if (s) v = realign16_sel(v, ld_nc_cached(b + 1), s);
-              w[0] = v.x;
-              w[1] = v.y;
-              w[2] = v.z;
-              w[3] = v.w;
-            }
-          } else if (e < to && e + kPer > from) {  // a vector across a boundary
-#pragma unroll
-            for (int i = 0; i < kPer; ++i)
-              if (e + i >= from && e + i < to) one(e + i, w[i / 2], i & 1);
+          raw[j] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      } else {
+        uint32_t odd = Elem<DT>::kNegInfWord;  // this lane's entry of a cut vector
+        const uint32_t of = (lane < 8 ? cut : end) - e0;  // where the cut is in the segment
+        {
+          const uint32_t e = e0 + of / kPer * kPer + (lane & 7);
+          if (lane < 16 && of < kSeg && of % kPer != 0 && e < p.vocab) {
+            int n = r;
+            while (p.shard[n].end <= e) ++n;
+            const LogitShard& t = p.shard[n];
+            const uint64_t x = t.base + row * t.stride + static_cast<uint64_t>(e - t.first) * 2;
+            if (inside(p, t, x, 2)) odd = *reinterpret_cast<const uint16_t*>(x);
           }
         }
-        raw[j] = make_uint4(w[0], w[1], w[2], w[3]);
+        const uint32_t o0 = static_cast<uint32_t>(at0 + static_cast<uint64_t>(e0) * 2) & 15u,
+                       o1 = static_cast<uint32_t>(at1 + static_cast<uint64_t>(e0) * 2) & 15u;
+        auto whole = [&](uint32_t e) { return e >= s0.first && (e + kPer <= cut || (e >= cut && e + kPer <= end)); };
+        if ((o0 | o1) == 0) {
+#pragma unroll
+          for (int j = 0; j < kVecs; ++j) {
+            const uint32_t e = e0 + index(j, 0, lane);
+            const uint64_t x = (e < cut ? at0 : at1) + static_cast<uint64_t>(e) * 2;
+            ld16_where(raw[j], x, whole(e) && inside(p, e < cut ? s0 : s1, x, 16));
+          }
+        } else {
+          constexpr int kBatch = 2;  // (4: registers spill, and with alternatives that costs more than it saves)
+#pragma unroll
+          for (int j0 = 0; j0 < kVecs; j0 += kBatch) {
+            uint4 next[kBatch];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+              const uint32_t e = e0 + index(j0 + k, 0, lane);
+              const uint32_t o = e < cut ? o0 : o1;
+              const uint64_t x = (e < cut ? at0 : at1) + static_cast<uint64_t>(e) * 2 - o;
+              const bool ok = whole(e) && inside(p, e < cut ? s0 : s1, x + o, 16);
+              ld16_where(raw[j0 + k], x, ok);
+              next[k] = raw[j0 + k];
+              ld16_where(next[k], x + 16, ok && o != 0);
+            }
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+              const uint32_t e = e0 + index(j0 + k, 0, lane);
+              if (whole(e)) raw[j0 + k] = realign16_sel(raw[j0 + k], next[k], e < cut ? o0 : o1);
+            }
+          }
+        }
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const uint32_t at = __shfl_sync(~0u, of, 8 * b);
+          if (at >= kSeg || at % kPer == 0) continue;
+          uint32_t w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            w[i] = (__shfl_sync(~0u, odd, 8 * b + 2 * i) & 0xFFFFu) | (__shfl_sync(~0u, odd, 8 * b + 2 * i + 1) << 16);
+#pragma unroll
+          for (int j = 0; j < kVecs; ++j)
+            if (at / kPer == static_cast<uint32_t>(j * 32 + lane)) raw[j] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
       }
     }
+  }
+
+  // Whether [x, x + n) is of shard `t` (always, but in the checked build).
+  __device__ static __forceinline__ bool inside(const ScoreParams& p, const LogitShard& t, uint64_t x, uint32_t n) {
+    return in_bounds(reinterpret_cast<const void*>(x), n, t.base,
+                     t.base + (p.rows - 1) * t.stride + static_cast<uint64_t>(t.end - t.first) * Elem<DT>::kBytes,
+                     kSiteLogit);
   }
 };
 

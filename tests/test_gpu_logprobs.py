@@ -147,6 +147,31 @@ def test_every_alignment(dtype, offset, pad):
     check(score([view], tokens, top=4), x, tokens, top=4)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("widths", [
+    [1, 3, 7, 9, 2047, 2, 2031],          # several ends in one 16-byte vector, and on both sides of it
+    [8, 2040, 8, 2048, 16, 1],            # ends on vectors and on segments of 2048
+    [1024, 1023, 1, 5, 4, 3, 2, 1],       # three and more shards in a segment of 1024
+    [2049, 4095, 6, 13],
+])
+@pytest.mark.parametrize("skew", [0, 1, 5])
+def test_segments_of_many_shards(dtype, widths, skew):
+    """Shards whose ends lie anywhere: the bits of the undivided row, and nothing beside a shard's rows."""
+    vocab = sum(widths)
+    x, tokens = logits(9, vocab, DT[dtype], seed=3)
+    shards = []
+    for r, part in enumerate(torch.split(x, widths, dim=1)):
+        w, at = part.shape[1], 8 + skew * (r + 1) % 8
+        room = torch.full((9, (at + w + 15) // 8 * 8 + (skew if r % 2 else 0)), float("nan"), device="cuda", dtype=DT[dtype])
+        room[:, at:at + w] = part
+        shards.append(room[:, at:at + w])
+    got, want = score(shards, tokens, 20), score([x], tokens, 20)
+    check(got, x, tokens, top=20)
+    for name in want:
+        assert torch.equal(got[name].view(torch.int32) if got[name].is_floating_point() else got[name],
+                           want[name].view(torch.int32) if want[name].is_floating_point() else want[name]), name
+
+
 def test_padding_columns_are_not_read():
     x, tokens = logits(5, 5000, torch.bfloat16)
     padded = torch.full((5, 5120), float("nan"), device="cuda", dtype=torch.bfloat16)
