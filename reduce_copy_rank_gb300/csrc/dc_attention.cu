@@ -16,7 +16,9 @@
 // head that is 8 multiply-adds per byte, which the matrix pipe does with a
 // wide margin (mma.m16n8k16, 16 heads x 8 tokens), so it is fed from shared
 // memory by cp.async and never waited for.  A warp owns 16 tokens at a time
-// with a ring of its own: no barrier until its subtree is done.
+// with a ring of its own: no barrier until its subtree is done.  (Above 128
+// columns two or three warps share the tokens, a part of the columns each, and
+// add their scores up through shared memory.)
 //
 // Where a unit's pieces fit one cluster and the GPU has room, its CTAs join them
 // through shared memory; else through the workspace, the last to arrive doing
@@ -43,29 +45,46 @@ enum : uint32_t {
   kSiteLength = 1, kSiteTable = 2, kSiteQuery = 3, kSiteKey = 4, kSiteValue = 5, kSiteOut = 6, kSitePartial = 7,
 };
 
-constexpr int kThreads = kAttendWarps * 32;
-
-// Shared memory of a head size: each warp's ring of tiles, then (heads above
-// 128, whose subtrees and queries do not fit in registers) its waiting
-// subtrees and the queries.
+// A head size's share of a CTA: kAttendWarps runs of tokens, each of one warp,
+// or of two or three that hold a part of the columns each where a head has more
+// than 128.  (One warp's registers held no subtrees of so many and its ring two
+// tiles, and an SM had four warps.  32 ragged sequences up to 8000 tokens, 16/4
+// heads of 256, one / two warps: 105 / 90 us; of 192, one / two / three: 73.5 /
+// 81 / 70: halves of 192 columns cut the 128-byte lines.)  Shared memory: each
+// warp's ring of tiles, then the partial scores of a run's warps.
 template <int D, int HB>
 struct Shape {
-  static constexpr int kRow = D * 2 + 16;           // bytes; the 16 keep ldmatrix free of conflicts
+  static constexpr int kParts = D == 192 && HB == 8 ? 3 : D > 128 ? 2 : 1;  // warps per run of tokens
+  static constexpr int kThreads = kAttendWarps * kParts * 32;
+  static constexpr int kCols = D / kParts;          // columns of a warp
+  static constexpr int kRow = kCols * 2 + 16;       // bytes; the 16 keep ldmatrix free of conflicts
   static constexpr int kHalf = kAttendTile * kRow;  // keys or values of one tile
   static constexpr int kStage = 2 * kHalf;
-  static constexpr int kStages = D > 192 ? 2 : 3;
-  static constexpr int kRing = kAttendWarps * kStages * kStage;
-  static constexpr int kValues = D / 4 * (HB / 8);  // of a head block's output that a lane holds
+  static constexpr int kStages = 3;
+  static constexpr int kRing = kAttendWarps * kParts * kStages * kStage;
+  static constexpr int kValues = kCols / 4 * (HB / 8);  // of a head block's output that a lane holds
   static constexpr int kLevels = attend_levels(D, HB);
-  static constexpr bool kInRegs = D <= 128;
-  static constexpr bool kQueryShared = D > 128;
-  static constexpr int kHeld = kInRegs ? 0 : kAttendWarps * kLevels * kValues * 32 * 4;
-  static constexpr int kBytes = kRing + kHeld + (kQueryShared ? HB * kRow : 0);
+  static constexpr int kExchange = kParts > 1 ? kAttendWarps * 2 * kParts * (HB / 8) * 512 : 0;
+  static constexpr int kBytes = kRing + kExchange;
   static constexpr int kCtas = D <= 64 && HB == 8 ? 3 : D <= 128 ? 2 : 1;  // per SM
 };
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+
+__device__ __forceinline__ void st_shared4(uint32_t a, const float4& v) {
+  asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+}
+__device__ __forceinline__ float4 ld_shared4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+  return v;
+}
+// The warps of a run of tokens wait for one another (all take as many tiles).
+template <int WARPS>
+__device__ __forceinline__ void run_barrier(int run) {
+  asm volatile("bar.sync %0, %1;" ::"r"(run + 1), "n"(WARPS * 32) : "memory");
 }
 
 // Shared memory of CTA `rank` of the cluster, at this CTA's address `a`.
@@ -244,15 +263,20 @@ __device__ __forceinline__ bool arrive_last(uint32_t* counter, uint32_t n, uint3
 // LOOP: a unit has fewer CTAs than its longest sequence could have pieces, and
 // a CTA takes every p.places-th of them.
 template <int DT, int D, int HB, bool LOOP>
-__global__ __launch_bounds__(kThreads, Shape<D, HB>::kCtas) void dc_attend_kernel(const __grid_constant__ AttendParams p) {
+__global__ __launch_bounds__(Shape<D, HB>::kThreads, Shape<D, HB>::kCtas) void dc_attend_kernel(const __grid_constant__ AttendParams p) {
   using S = Shape<D, HB>;
   constexpr int R = HB / 8;
   using State = Run<S::kValues, R>;
-  constexpr int kSteps = D / 16;  // k-steps of q.k, and 16-element column groups of the output
+  constexpr int C = S::kCols;
+  constexpr int kThreads = S::kThreads;
+  constexpr int kSteps = C / 16;  // k-steps of q.k, and 16-element column groups of the output
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float w_ref[kAttendWarps][HB], w_l[kAttendWarps][HB];
   __shared__ uint32_t last_flag;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  // run of tokens `warp`, columns [col0, col0 + C)
+  const int warp = static_cast<int>(threadIdx.x >> 5) / S::kParts, column = static_cast<int>(threadIdx.x >> 5) % S::kParts;
+  const int col0 = column * C;
 
   __shared__ float2 c_rl[HB];  // this CTA's piece, for its cluster
   uint32_t piece = blockIdx.x % static_cast<uint32_t>(p.places);
@@ -296,8 +320,7 @@ __global__ __launch_bounds__(kThreads, Shape<D, HB>::kCtas) void dc_attend_kerne
     }
     return;
   }
-  uint32_t qf[S::kQueryShared ? 1 : kSteps][2 * R];
-  uint8_t* const q_smem = smem + S::kRing + S::kHeld;
+  uint32_t qf[kSteps][2 * R];
   do {
   // this warp's tokens [t0, t1): a subtree of 2^level leaves
   const uint32_t run = leaf << level;
@@ -310,13 +333,13 @@ __global__ __launch_bounds__(kThreads, Shape<D, HB>::kCtas) void dc_attend_kerne
   // are no multiple of 128 bytes).  Most tiles lie in one page: their rows are
   // a stride apart.  In the others lanes 0..15 look up where the keys of the
   // tile's tokens are, lanes 16..31 their values, and hand the addresses on.
-  constexpr int kLanes = D % 64 == 0 ? 8 : 4;       // lanes that copy one row
+  constexpr int kLanes = C % 64 == 0 ? 8 : 4;       // lanes that copy one row
   constexpr int kRows = 32 / kLanes;                // rows an instruction touches
   constexpr int kGroups = kAttendTile / kRows;
-  const uint32_t ring = smem_addr(smem) + static_cast<uint32_t>(warp * S::kStages * S::kStage);
+  const uint32_t ring = smem_addr(smem) + static_cast<uint32_t>((warp * S::kParts + column) * S::kStages * S::kStage);
   const uint64_t table_row = p.table + static_cast<uint64_t>(seq) * static_cast<uint64_t>(p.table_stride) * 4;
-  const uint64_t k_head = p.kc.base + static_cast<uint64_t>(kh) * p.kc.head;
-  const uint64_t v_head = p.vc.base + static_cast<uint64_t>(kh) * p.vc.head;
+  const uint64_t k_head = p.kc.base + static_cast<uint64_t>(kh) * p.kc.head + col0 * 2;
+  const uint64_t v_head = p.vc.base + static_cast<uint64_t>(kh) * p.vc.head + col0 * 2;
   int32_t next_id = -1;     // the page of this lane's token of the next tile to copy, -1: no token
   uint32_t next_slot = 0;   // ... and its place in the page
   bool next_whole = false;  // the tile is 16 tokens of one page, next_slot its first token's place
@@ -338,7 +361,7 @@ __global__ __launch_bounds__(kThreads, Shape<D, HB>::kCtas) void dc_attend_kerne
   };
   auto copy = [&](uint32_t dst, int half, uint64_t src, bool read) {
 #pragma unroll
-    for (int c = 0; c < D / 8 / kLanes; ++c) {
+    for (int c = 0; c < C / 8 / kLanes; ++c) {
       const uint64_t x = src + c * kLanes * 16;
       const bool ok = read && in_bounds(reinterpret_cast<const void*>(x), 16, half ? p.vc.lo : p.kc.lo,
                                         half ? p.vc.hi : p.kc.hi, half ? kSiteValue : kSiteKey);
@@ -382,41 +405,28 @@ __global__ __launch_bounds__(kThreads, Shape<D, HB>::kCtas) void dc_attend_kerne
   };
   look_up(0);
 
-  // query fragments: rows 0..7 heads h0.., rows 8..15 heads h0 + 8.. (HB 16);
-  // of heads above 128 they stay in shared memory (in registers they spilled:
-  // 1800 cycles a tile for q.k at D = 256)
+  // query fragments: rows 0..7 heads h0.., rows 8..15 heads h0 + 8.. (HB 16)
   {
     const uint64_t q_seq = p.q + static_cast<uint64_t>(seq) * p.q_seq + static_cast<uint64_t>(h0) * p.q_head;
-    if constexpr (S::kQueryShared) {
-      for (int i = threadIdx.x; i < HB * (D / 8); i += kThreads) {
-        const int h = i / (D / 8), c = i % (D / 8);
-        const uint64_t row = q_seq + static_cast<uint64_t>(h) * p.q_head;
-        const uint4* a = reinterpret_cast<const uint4*>(row) + c;
-        *reinterpret_cast<uint4*>(q_smem + h * S::kRow + c * 16) =
-            h < nh && in_bounds(a, 16, row, row + D * 2, kSiteQuery) ? *a : make_uint4(0, 0, 0, 0);
-      }
-      __syncthreads();
-    } else {
 #pragma unroll
-      for (int half = 0; half < R; ++half) {
-        const int h = (lane >> 2) + 8 * half;
-        const uint64_t row = q_seq + static_cast<uint64_t>(h) * p.q_head;
+    for (int half = 0; half < R; ++half) {
+      const int h = (lane >> 2) + 8 * half;
+      const uint64_t row = q_seq + static_cast<uint64_t>(h) * p.q_head;
 #pragma unroll
-        for (int k = 0; k < kSteps; ++k)
+      for (int k = 0; k < kSteps; ++k)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t* a =
-                reinterpret_cast<const uint32_t*>(row + static_cast<uint64_t>(k * 16 + i * 8 + (lane & 3) * 2) * 2);
-            // a[0]: row g, first 8 columns; a[1]: row g + 8; a[2], a[3]: the next 8 columns
-            qf[k][R * i + half] = h < nh && in_bounds(a, 4, row, row + D * 2, kSiteQuery) ? *a : 0u;
-          }
-      }
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t* a =
+              reinterpret_cast<const uint32_t*>(row + static_cast<uint64_t>(col0 + k * 16 + i * 8 + (lane & 3) * 2) * 2);
+          // a[0]: row g, first 8 columns; a[1]: row g + 8; a[2], a[3]: the next 8 columns
+          qf[k][R * i + half] = h < nh && in_bounds(a, 4, row, row + D * 2, kSiteQuery) ? *a : 0u;
+        }
     }
   }
 #pragma unroll
   for (int i = 0; i < S::kStages - 1; ++i) issue(i);
 
-  float m[R], l[R], o[D / 8][4];
+  float m[R], l[R], o[C / 8][4];
   auto clear = [&]() {
 #pragma unroll
     for (int i = 0; i < R; ++i) {
@@ -424,7 +434,7 @@ __global__ __launch_bounds__(kThreads, Shape<D, HB>::kCtas) void dc_attend_kerne
       l[i] = 0.0f;
     }
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i)
+    for (int i = 0; i < C / 8; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[i][j] = 0.0f;
   };
@@ -433,36 +443,8 @@ __global__ __launch_bounds__(kThreads, Shape<D, HB>::kCtas) void dc_attend_kerne
 
   // subtrees that wait for their right neighbour: slot b holds 2^b leaves
   State cur;
-  State held[S::kInRegs ? S::kLevels : 1];
-  float2 held_rl[S::kLevels][R];
-  float* parked = reinterpret_cast<float*>(smem + S::kRing) + warp * S::kLevels * S::kValues * 32 + lane;
-  auto put = [&](int b, const State& x) {
-    if constexpr (S::kInRegs) {
-      held[b] = x;
-    } else {
-#pragma unroll
-      for (int i = 0; i < S::kValues; ++i) parked[(b * S::kValues + i) * 32] = x.v[i];
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        held_rl[b][i] = make_float2(x.ref[i], x.l[i]);
-      }
-    }
-  };
-  auto add_held = [&](int b) {
-    if constexpr (S::kInRegs) {
-      join(held[b], cur);
-    } else {
-      State x;
-#pragma unroll
-      for (int i = 0; i < S::kValues; ++i) x.v[i] = parked[(b * S::kValues + i) * 32];
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        x.ref[i] = held_rl[b][i].x;
-        x.l[i] = held_rl[b][i].y;
-      }
-      join(x, cur);
-    }
-  };
+  State held[S::kLevels];
+  [[maybe_unused]] const uint32_t exchange = smem_addr(smem) + S::kRing + static_cast<uint32_t>(warp * 2 * S::kParts * R * 512 + lane * 16);
 
   const uint32_t leaf_tiles = leaf / kAttendTile;
   uint32_t in_leaf = 0, leaves = 0;
@@ -479,19 +461,7 @@ __global__ __launch_bounds__(kThreads, Shape<D, HB>::kCtas) void dc_attend_kerne
         uint32_t b[4];
         ldmatrix4(a + k * 32, b);
         uint32_t q[4];
-        if constexpr (S::kQueryShared) {
-          const uint32_t qa = smem_addr(q_smem) + k * 32;
-          if constexpr (HB == 16) {
-            ldmatrix4(qa + (((lane >> 3) & 1) * 8 + (lane & 7)) * S::kRow + (lane >> 4) * 16, q);
-          } else {
-            uint32_t x[4];  // (the upper 16 lanes' addresses repeat the lower ones')
-            ldmatrix4(qa + (lane & 7) * S::kRow + ((lane >> 3) & 1) * 16, x);
-            q[0] = x[0];
-            q[1] = 0;
-            q[2] = x[1];
-            q[3] = 0;
-          }
-        } else if constexpr (HB == 16) {
+        if constexpr (HB == 16) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) q[j] = qf[k][j];
         } else {
@@ -505,6 +475,30 @@ __global__ __launch_bounds__(kThreads, Shape<D, HB>::kCtas) void dc_attend_kerne
       }
     }
     issue(i + S::kStages - 1);  // (its stage was read in the last round)
+    if constexpr (S::kParts > 1) {
+      // the sums over all columns: the warps' shares in order (two buffers: a
+      // warp writes one again only after the others have read it)
+      const uint32_t at = exchange + (i & 1) * (S::kParts * R * 512);
+#pragma unroll
+      for (int half = 0; half < R; ++half)
+        st_shared4(at + (column * R + half) * 512,
+                   make_float4(s[0][0][2 * half] + s[1][0][2 * half], s[0][0][2 * half + 1] + s[1][0][2 * half + 1],
+                               s[0][1][2 * half] + s[1][1][2 * half], s[0][1][2 * half + 1] + s[1][1][2 * half + 1]));
+      run_barrier<S::kParts>(warp);
+#pragma unroll
+      for (int half = 0; half < R; ++half) {
+        float4 v = ld_shared4(at + half * 512);
+#pragma unroll
+        for (int c = 1; c < S::kParts; ++c) {
+          const float4 w = ld_shared4(at + (c * R + half) * 512);
+          v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
+        }
+        s[0][0][2 * half] = v.x;
+        s[0][0][2 * half + 1] = v.y;
+        s[0][1][2 * half] = v.z;
+        s[0][1][2 * half + 1] = v.w;
+      }
+    }
     const uint32_t base = t0 + i * kAttendTile;
     const bool partial = base + kAttendTile > t1;
     uint32_t phi[4], plo[4];
@@ -513,7 +507,7 @@ __global__ __launch_bounds__(kThreads, Shape<D, HB>::kCtas) void dc_attend_kerne
       float x[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        x[j] = (s[0][j >> 1][2 * half + (j & 1)] + s[1][j >> 1][2 * half + (j & 1)]) * sc;
+        x[j] = (s[0][j >> 1][2 * half + (j & 1)] + (S::kParts == 1 ? s[1][j >> 1][2 * half + (j & 1)] : 0.0f)) * sc;
       if (partial) {
         const uint32_t t = base + (lane & 3) * 2;
         if (t >= t1) x[0] = neg_inf();
@@ -529,7 +523,7 @@ __global__ __launch_bounds__(kThreads, Shape<D, HB>::kCtas) void dc_attend_kerne
         const float f = pow2_diff(m[half], mn);
         l[half] *= f;
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
+        for (int c = 0; c < C / 8; ++c) {
           if constexpr (HB == 16) {
             o[c][2 * half] *= f;
             o[c][2 * half + 1] *= f;
@@ -584,7 +578,7 @@ __global__ __launch_bounds__(kThreads, Shape<D, HB>::kCtas) void dc_attend_kerne
         cur.l[half] = l[half];
       }
 #pragma unroll
-      for (int c = 0; c < D / 8; ++c) {
+      for (int c = 0; c < C / 8; ++c) {
         if constexpr (HB == 16) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) cur.v[4 * c + j] = o[c][j];
@@ -594,13 +588,13 @@ __global__ __launch_bounds__(kThreads, Shape<D, HB>::kCtas) void dc_attend_kerne
         }
       }
       // (at most 2^kLevels leaves; the last one's subtree stays in cur)
-      if (leaves & 1) add_held(0);
+      if (leaves & 1) join(held[0], cur);
       if constexpr (S::kLevels > 1)
-        if ((leaves & 3) == 3) add_held(1);
+        if ((leaves & 3) == 3) join(held[1], cur);
       ++leaves;
       if (i + 1 < tiles) {
-        if (leaves & 1) put(0, cur);
-        else if constexpr (S::kLevels > 1) put(1, cur);
+        if (leaves & 1) held[0] = cur;
+        else if constexpr (S::kLevels > 1) held[1] = cur;
         clear();
       }
     }
@@ -615,11 +609,11 @@ __global__ __launch_bounds__(kThreads, Shape<D, HB>::kCtas) void dc_attend_kerne
 #pragma unroll
     for (int i = 0; i < S::kValues; ++i) cur.v[i] = 0.0f;
   } else if constexpr (S::kLevels > 1) {
-    if (leaves == 3) add_held(1);  // a last leaf without a neighbour
+    if (leaves == 3) join(held[1], cur);  // a last leaf without a neighbour
   }
 
   // the piece: the warps' subtrees
-  if ((lane & 3) == 0) {
+  if ((lane & 3) == 0 && column == 0) {
 #pragma unroll
     for (int half = 0; half < R; ++half) {
       w_ref[warp][(lane >> 2) + 8 * half] = cur.ref[half];
@@ -632,10 +626,10 @@ __global__ __launch_bounds__(kThreads, Shape<D, HB>::kCtas) void dc_attend_kerne
   {
     const int g = lane >> 2;
 #pragma unroll
-    for (int c = 0; c < D / 8; ++c)
+    for (int c = 0; c < C / 8; ++c)
 #pragma unroll
       for (int half = 0; half < R; ++half)
-        *reinterpret_cast<float2*>(wo + (warp * HB + g + 8 * half) * D + c * 8 + (lane & 3) * 2) =
+        *reinterpret_cast<float2*>(wo + (warp * HB + g + 8 * half) * D + col0 + c * 8 + (lane & 3) * 2) =
             make_float2(cur.v[c * 2 * R + 2 * half], cur.v[c * 2 * R + 2 * half + 1]);
   }
   __syncthreads();
@@ -751,7 +745,7 @@ __global__ __launch_bounds__(kThreads, Shape<D, HB>::kCtas) void dc_attend_kerne
 template <int DT, int D, int HB, bool LOOP>
 cudaError_t launch_one(const AttendParams& p, bool pdl, cudaStream_t s, int grid) {
   constexpr int kSmem = Shape<D, HB>::kBytes;
-  static_assert(kSmem + 4096 <= 227 * 1024, "the ring and the waiting subtrees fit");
+  static_assert(kSmem + 4096 <= 227 * 1024, "the ring and the partial scores fit");
   static std::atomic<uint64_t> allowed{0};  // devices whose limit is set
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -764,7 +758,7 @@ cudaError_t launch_one(const AttendParams& p, bool pdl, cudaStream_t s, int grid
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(Shape<D, HB>::kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];

@@ -155,8 +155,8 @@ __host__ __device__ inline uint32_t attend_pieces(uint32_t n, uint32_t level) {
   return (leaves + per - 1) / per;
 }
 constexpr uint32_t kAttendMaxPieces = 128;  // 512 leaves, one a warp
-// Levels that a warp can hold: waiting subtrees live in registers up to a
-// head size of 128 and in shared memory above.
+// Levels that a warp can hold: waiting subtrees live in registers (heads above
+// 128 are shared by two or three warps).
 __host__ __device__ constexpr int attend_levels(int dim, int hb) { return hb == 8 || dim <= 64 ? 2 : 1; }
 // The level for a sequence of `small` pieces at level 0, if all `units` of the
 // call were like it: the smallest that leaves at most kAttendCtas CTAs.
