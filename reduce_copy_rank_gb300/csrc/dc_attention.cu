@@ -52,9 +52,9 @@ enum : uint32_t {
 // heads of 256, one / two warps: 105 / 90 us; of 192, one / two / three: 73.5 /
 // 81 / 70: halves of 192 columns cut the 128-byte lines.)  Shared memory: each
 // warp's ring of tiles, then the partial scores of a run's warps.
-template <int D, int HB>
+template <int D, int HB, bool APART>
 struct Shape {
-  static constexpr int kParts = D == 192 && HB == 8 ? 3 : D > 128 ? 2 : 1;  // warps per run of tokens
+  static constexpr int kParts = D == 192 && HB == 8 && !APART ? 3 : D > 128 ? 2 : 1;  // warps per run of tokens
   static constexpr int kThreads = kAttendWarps * kParts * 32;
   static constexpr int kCols = D / kParts;          // columns of a warp
   static constexpr int kRow = kCols * 2 + 16;       // bytes; the 16 keep ldmatrix free of conflicts
@@ -66,7 +66,7 @@ struct Shape {
   static constexpr int kLevels = attend_levels(D, HB);
   static constexpr int kExchange = kParts > 1 ? kAttendWarps * 2 * kParts * (HB / 8) * 512 : 0;
   static constexpr int kBytes = kRing + kExchange;
-  static constexpr int kCtas = D <= 64 && HB == 8 ? 3 : D <= 128 ? 2 : 1;  // per SM
+  static constexpr int kCtas = attend_ctas_per_sm(D, HB);
 };
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
@@ -260,11 +260,13 @@ __device__ __forceinline__ bool arrive_last(uint32_t* counter, uint32_t n, uint3
   return *flag != 0;
 }
 
+// APART: 8 heads that share their keys with 8 others, computed as 16 in a block
+// are, with the weights' high and low parts in a product each.
 // LOOP: a unit has fewer CTAs than its longest sequence could have pieces, and
 // a CTA takes every p.places-th of them.
-template <int DT, int D, int HB, bool LOOP>
-__global__ __launch_bounds__(Shape<D, HB>::kThreads, Shape<D, HB>::kCtas) void dc_attend_kernel(const __grid_constant__ AttendParams p) {
-  using S = Shape<D, HB>;
+template <int DT, int D, int HB, bool LOOP, bool APART>
+__global__ __launch_bounds__(Shape<D, HB, APART>::kThreads, Shape<D, HB, APART>::kCtas) void dc_attend_kernel(const __grid_constant__ AttendParams p) {
+  using S = Shape<D, HB, APART>;
   constexpr int R = HB / 8;
   using State = Run<S::kValues, R>;
   constexpr int C = S::kCols;
@@ -548,10 +550,11 @@ __global__ __launch_bounds__(Shape<D, HB>::kThreads, Shape<D, HB>::kCtas) void d
       uint32_t w[4];
       if constexpr (HB == 8) {
         w[0] = phi[0];
-        w[1] = plo[0];
+        w[1] = APART ? 0 : plo[0];
         w[2] = phi[2];
-        w[3] = plo[2];
+        w[3] = APART ? 0 : plo[2];
       }
+      [[maybe_unused]] const uint32_t low[4] = {plo[0], 0, plo[2], 0};  // (APART)
 #pragma unroll
       for (int c = 0; c < kSteps; ++c) {
         uint32_t b[4];
@@ -564,6 +567,10 @@ __global__ __launch_bounds__(Shape<D, HB>::kThreads, Shape<D, HB>::kCtas) void d
         } else {
           mma<DT>(o[2 * c], w, b[0], b[1]);
           mma<DT>(o[2 * c + 1], w, b[2], b[3]);
+          if constexpr (APART) {
+            mma<DT>(o[2 * c], low, b[0], b[1]);
+            mma<DT>(o[2 * c + 1], low, b[2], b[3]);
+          }
         }
       }
     }
@@ -582,9 +589,9 @@ __global__ __launch_bounds__(Shape<D, HB>::kThreads, Shape<D, HB>::kCtas) void d
         if constexpr (HB == 16) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) cur.v[4 * c + j] = o[c][j];
-        } else {  // rows 8..15 hold the low parts
-          cur.v[2 * c] = o[c][0] + o[c][2];
-          cur.v[2 * c + 1] = o[c][1] + o[c][3];
+        } else {  // rows 8..15 hold the low parts (nothing if those have a product of their own)
+          cur.v[2 * c] = APART ? o[c][0] : o[c][0] + o[c][2];
+          cur.v[2 * c + 1] = APART ? o[c][1] : o[c][1] + o[c][3];
         }
       }
       // (at most 2^kLevels leaves; the last one's subtree stays in cur)
@@ -742,9 +749,9 @@ __global__ __launch_bounds__(Shape<D, HB>::kThreads, Shape<D, HB>::kCtas) void d
   } while (LOOP && (piece += static_cast<uint32_t>(p.places)) < pieces);
 }
 
-template <int DT, int D, int HB, bool LOOP>
+template <int DT, int D, int HB, bool LOOP, bool APART>
 cudaError_t launch_one(const AttendParams& p, bool pdl, cudaStream_t s, int grid) {
-  constexpr int kSmem = Shape<D, HB>::kBytes;
+  constexpr int kSmem = Shape<D, HB, APART>::kBytes;
   static_assert(kSmem + 4096 <= 227 * 1024, "the ring and the partial scores fit");
   static std::atomic<uint64_t> allowed{0};  // devices whose limit is set
   int dev = 0;
@@ -752,13 +759,13 @@ cudaError_t launch_one(const AttendParams& p, bool pdl, cudaStream_t s, int grid
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (!(allowed.load(std::memory_order_relaxed) & bit)) {
-    e = cudaFuncSetAttribute(dc_attend_kernel<DT, D, HB, LOOP>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    e = cudaFuncSetAttribute(dc_attend_kernel<DT, D, HB, LOOP, APART>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     allowed.fetch_or(bit, std::memory_order_relaxed);
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(Shape<D, HB>::kThreads);
+  cfg.blockDim = dim3(Shape<D, HB, APART>::kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -777,15 +784,17 @@ cudaError_t launch_one(const AttendParams& p, bool pdl, cudaStream_t s, int grid
   }
   cfg.attrs = n ? attr : nullptr;
   cfg.numAttrs = n;
-  return cudaLaunchKernelEx(&cfg, dc_attend_kernel<DT, D, HB, LOOP>, p);
+  return cudaLaunchKernelEx(&cfg, dc_attend_kernel<DT, D, HB, LOOP, APART>, p);
 }
 
 template <int DT, int D>
 cudaError_t launch_hb(const AttendParams& p, bool pdl, cudaStream_t s, int grid) {
   const bool loop = p.places < p.pieces;
-  if (attend_head_block(p.group) == 16)
-    return loop ? launch_one<DT, D, 16, true>(p, pdl, s, grid) : launch_one<DT, D, 16, false>(p, pdl, s, grid);
-  return loop ? launch_one<DT, D, 8, true>(p, pdl, s, grid) : launch_one<DT, D, 8, false>(p, pdl, s, grid);
+  if (p.hb == 16)
+    return loop ? launch_one<DT, D, 16, true, false>(p, pdl, s, grid) : launch_one<DT, D, 16, false, false>(p, pdl, s, grid);
+  // (few CTAs, or there would be 16 heads to a block: never in turns)
+  if (p.group > 8) return loop ? cudaErrorInvalidValue : launch_one<DT, D, 8, false, true>(p, pdl, s, grid);
+  return loop ? launch_one<DT, D, 8, true, false>(p, pdl, s, grid) : launch_one<DT, D, 8, false, false>(p, pdl, s, grid);
 }
 
 template <int DT>

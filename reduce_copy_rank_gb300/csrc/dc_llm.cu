@@ -241,18 +241,19 @@ dc_status_t plan_attend(int64_t seqs, int q_heads, int kv_heads, int dim, uint64
   if (max_tokens > 0x7FFFFFFFull)
     return fail(DC_ERR_INVALID, "sequences of up to %llu tokens", static_cast<unsigned long long>(max_tokens));
   const int group = q_heads / kv_heads;
-  a->hb = attend_head_block(group);
-  a->head_blocks = (group + a->hb - 1) / a->hb;
-  a->units = static_cast<uint64_t>(seqs) * static_cast<uint64_t>(kv_heads) * static_cast<uint64_t>(a->head_blocks);
-  if (a->units * kAttendMaxPieces > 0x7FFFFFFFull)
-    return fail(DC_ERR_INVALID, "%llu units of work exceed a grid", static_cast<unsigned long long>(a->units));
-  const uint32_t units = static_cast<uint32_t>(a->units);
   // no sequence of up to n tokens has more than `most` pieces at level 0; one
   // with fewer may be cut finer
   const uint32_t n = static_cast<uint32_t>(max_tokens);
   const uint32_t most = n > 512 * 128 ? kAttendMaxPieces
                                       : std::max({attend_pieces(n, 0), attend_pieces(std::min(n, kAttendShort), 0),
                                                   attend_pieces(std::min(n, kAttendTiny), 0)});
+  const uint64_t kv_units = static_cast<uint64_t>(seqs) * static_cast<uint64_t>(kv_heads);
+  a->hb = attend_head_block(group, kv_units, most, dim);
+  a->head_blocks = (group + a->hb - 1) / a->hb;
+  a->units = kv_units * static_cast<uint64_t>(a->head_blocks);
+  if (a->units * kAttendMaxPieces > 0x7FFFFFFFull)
+    return fail(DC_ERR_INVALID, "%llu units of work exceed a grid", static_cast<unsigned long long>(a->units));
+  const uint32_t units = static_cast<uint32_t>(a->units);
   const int levels = attend_levels(dim, a->hb);
   a->pieces = 1;
   for (uint32_t s = 1; s <= most; ++s) {
@@ -550,6 +551,7 @@ dc_status_t dc_paged_attention(const dc_paged_attention_t* a, dc_stream_t stream
   p.kv_heads = a->kv_heads;
   p.group = a->q_heads / a->kv_heads;
   p.head_blocks = plan.head_blocks;
+  p.hb = plan.hb;
   p.window = a->window;
   p.units = static_cast<int32_t>(plan.units);
   p.pieces = static_cast<int32_t>(plan.pieces);

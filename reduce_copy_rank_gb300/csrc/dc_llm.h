@@ -123,6 +123,7 @@ struct AttendParams {
   int64_t num_pages;
   uint32_t page_size, table_width;
   int32_t seqs, q_heads, kv_heads, group, head_blocks;
+  int32_t hb;                           // heads of a block: attend_head_block
   int32_t window;
   int32_t units;                        // seqs * kv_heads * head_blocks
   int32_t pieces;                       // most pieces of one sequence
@@ -166,8 +167,20 @@ __host__ __device__ inline uint32_t attend_level(uint32_t small, uint32_t units,
   while (k < static_cast<uint32_t>(levels) && units * ((small + (1u << k) - 1) >> k) > kAttendCtas) ++k;
   return k;
 }
-// Heads that one CTA serves: 8, or 16 where a key head has more than 8 query heads.
-__host__ __device__ inline int attend_head_block(int group) { return group > 8 ? 16 : 8; }
+// Heads that one CTA serves.  Where a key head has more than 8 query heads: 16,
+// which read keys and values once, or 8 while the GPU would hold all of those
+// CTAs at once (two read the same keys, the second from L2; same bits).
+// Measured, us, 16 / 8: one sequence of 1024, 16/1 heads of 128: 7.5 / 6.2 (16
+// CTAs of 8); of 131072: 32.9 / 28.9 (256 CTAs); of 16384, 128/8 heads: 29.3 /
+// 31.0 (512); 32 up to 8000, 64/4 heads: 64 / 69.
+constexpr uint32_t kAttendSms = 152;
+__host__ __device__ constexpr int attend_ctas_per_sm(int dim, int hb) {
+  return dim <= 64 && hb == 8 ? 3 : dim <= 128 ? 2 : 1;
+}
+__host__ __device__ inline int attend_head_block(int group, uint64_t kv_units, uint32_t pieces, int dim) {
+  const uint64_t ctas = kv_units * static_cast<uint64_t>((group + 7) / 8) * pieces;
+  return group > 8 && ctas > kAttendSms * static_cast<uint64_t>(attend_ctas_per_sm(dim, 8)) ? 16 : 8;
+}
 cudaError_t launch_attend(const AttendParams& p, int dtype, int dim, bool pdl, cudaStream_t s, int* grid);
 
 }  // namespace dc

@@ -444,6 +444,24 @@ def test_bits_do_not_depend_on_the_grid(hq, hk, d):
         assert torch.equal(one[0][0], want[0][b]) and torch.equal(one[1][0], want[1][b]), b
 
 
+@pytest.mark.parametrize("hq,hk,d", [(9, 1, 64), (32, 2, 64), (12, 1, 96), (20, 1, 128), (64, 4, 128), (11, 1, 192), (48, 3, 256)])
+def test_bits_of_large_groups_do_not_depend_on_the_grid(hq, hk, d):
+    """More than 8 query heads a key head: alone a sequence's heads are split over CTAs, in a batch not."""
+    q, kc, vc, table, lengths = build([1500, 33, 5, 260], hq, hk, d, 16)
+    kc[2, 3, 0, :5] = 40.0
+    vc[1, 2, 0, :7] = float("inf")
+    want = attend(q, kc, vc, table, lengths)
+    many = attend(q.repeat(80, 1, 1), kc, vc, table.repeat(80, 1), lengths.repeat(80))
+    for i in (0, 79):
+        for k in (0, 1):
+            a, b = many[k][4 * i:4 * i + 4], want[k]
+            bits = torch.int16 if k == 0 else torch.int32
+            assert torch.equal(a.view(bits), b.view(bits))
+    for b in range(4):
+        one = attend(q[b:b + 1], kc, vc, table[b:b + 1], lengths[b:b + 1])
+        assert torch.equal(one[0][0].view(torch.int16), want[0][b].view(torch.int16)) and torch.equal(one[1][0], want[1][b]), b
+
+
 @pytest.mark.parametrize("seqs,hk", [(1, 1), (3, 8), (40, 8)])
 def test_tables_far_wider_than_the_sequences(seqs, hk):
     lengths = [(b * 337) % 2900 for b in range(seqs)]
