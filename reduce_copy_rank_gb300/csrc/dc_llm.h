@@ -144,7 +144,7 @@ struct AttendParams {
 // tokens, 32/8 heads of 128: 7.2 / 5.9; 64 ragged ones up to 1024: 33.5 / 35.9.
 // 64 throughout / 128 above 8192 / 128 above 4096: one of 16384: 22.7 / 19.3 /
 // 19.3; 128 ragged ones up to 8192: 347 / 347 / 339; 32 up to 8000, 64/8 heads
-// of 64: 54 / 54 / 63; 16/4 heads of 256: 104 / 104 / 113.
+// of 64: 54 / 54 / 63.
 constexpr uint32_t kAttendTiny = 1024, kAttendShort = 8192;
 __host__ __device__ inline uint32_t attend_leaf(uint32_t n) {
   uint32_t leaf = n <= kAttendTiny ? 32 : n <= kAttendShort ? 64 : 128;
