@@ -33,6 +33,13 @@
 // numbers hi + lo (hi the weight cut to 16 bits, lo the rounded rest), so
 // that the output carries one rounding to 16 bits, the last.  With at most 8
 // heads to a CTA the pair fills the tile's 16 rows and costs nothing.
+// binary16 has no numbers below 2^-24, so there the weights enter times 2^15 and
+// lo times 2^11 more, summed apart from hi (in the lower 8 rows; of more heads,
+// tile by tile), the powers of two taken out again in binary32.  A weight is then
+// held to 2^-20 of itself and 2^-50 of its leaf's largest: with values up to
+// 65504 in a leaf of 128 tokens that is 2^-27, less than half the least binary16
+// number.  (In units of the weights alone it was 2^-25, and a token far ahead
+// with a small value left nothing of the others.)
 #include <atomic>
 
 #include "dc_llm.h"
@@ -145,17 +152,29 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// The weights' units in the second product: hi is weight * kWeightUnit, lo the
+// rest of that times kLowUnit.  (A weight is at most 1, so in binary16 hi is at
+// most 2^15 and lo, less than 2^-10 of it, below 2^16.)
+template <int DT>
+constexpr float kWeightUnit = DT == kF16 ? 32768.0f : 1.0f;
+template <int DT>
+constexpr float kLowUnit = DT == kF16 ? 2048.0f : 1.0f;
+
 // hi: both weights cut to 16 bits; lo: what that left out, rounded.  lo stays
 // positive (2^-20 of the weight at least), so that an infinite value gives an
-// infinity and not 0 * inf.
+// infinity and not 0 * inf (in binary16, where 2^-24 is the least, for weights
+// above 2^-31 of the leaf's largest; below, an infinite value gives NaN).
 template <int DT>
 __device__ __forceinline__ void split_pair(float x, float y, uint32_t& hi, uint32_t& lo) {
+  x *= kWeightUnit<DT>;
+  y *= kWeightUnit<DT>;
   if constexpr (DT == kF16)
     asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(y), "f"(x));
   else
     asm("cvt.rz.bf16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(y), "f"(x));
-  constexpr float kLeast = 1.0f / (1 << 20);
-  lo = Elem<DT>::pack(fmaxf(x - Elem<DT>::lo(hi), x * kLeast), fmaxf(y - Elem<DT>::hi(hi), y * kLeast));
+  constexpr float kLeast = kLowUnit<DT> / (1 << 20);
+  lo = Elem<DT>::pack(fmaxf((x - Elem<DT>::lo(hi)) * kLowUnit<DT>, x * kLeast),
+                      fmaxf((y - Elem<DT>::hi(hi)) * kLowUnit<DT>, y * kLeast));
 }
 
 // Stores `v` as a 16-bit element pair.
@@ -272,6 +291,7 @@ __global__ __launch_bounds__(Shape<D, HB, APART>::kThreads, Shape<D, HB, APART>:
   constexpr int C = S::kCols;
   constexpr int kThreads = S::kThreads;
   constexpr int kSteps = C / 16;  // k-steps of q.k, and 16-element column groups of the output
+  constexpr bool kLowApart = kLowUnit<DT> != 1.0f;  // hi and lo do not add up as they are
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float w_ref[kAttendWarps][HB], w_l[kAttendWarps][HB];
   __shared__ uint32_t last_flag;
@@ -550,9 +570,9 @@ __global__ __launch_bounds__(Shape<D, HB, APART>::kThreads, Shape<D, HB, APART>:
       uint32_t w[4];
       if constexpr (HB == 8) {
         w[0] = phi[0];
-        w[1] = APART ? 0 : plo[0];
+        w[1] = APART && !kLowApart ? 0 : plo[0];
         w[2] = phi[2];
-        w[3] = APART ? 0 : plo[2];
+        w[3] = APART && !kLowApart ? 0 : plo[2];
       }
       [[maybe_unused]] const uint32_t low[4] = {plo[0], 0, plo[2], 0};  // (APART)
 #pragma unroll
@@ -562,12 +582,30 @@ __global__ __launch_bounds__(Shape<D, HB, APART>::kThreads, Shape<D, HB, APART>:
         if constexpr (HB == 16) {
           mma<DT>(o[2 * c], phi, b[0], b[1]);
           mma<DT>(o[2 * c + 1], phi, b[2], b[3]);
-          mma<DT>(o[2 * c], plo, b[0], b[1]);
-          mma<DT>(o[2 * c + 1], plo, b[2], b[3]);
+          if constexpr (kLowApart) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float t[4] = {};
+              mma<DT>(t, plo, b[2 * i], b[2 * i + 1]);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) o[2 * c + i][j] = __fmaf_rn(t[j], 1.0f / kLowUnit<DT>, o[2 * c + i][j]);
+            }
+          } else {
+            mma<DT>(o[2 * c], plo, b[0], b[1]);
+            mma<DT>(o[2 * c + 1], plo, b[2], b[3]);
+          }
         } else {
           mma<DT>(o[2 * c], w, b[0], b[1]);
           mma<DT>(o[2 * c + 1], w, b[2], b[3]);
-          if constexpr (APART) {
+          if constexpr (APART && kLowApart) {  // the tile's low parts, added as 16 heads' are
+#pragma unroll
+            for (int i = 2 * c; i < 2 * c + 2; ++i)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                o[i][j] = __fmaf_rn(o[i][2 + j], 1.0f / kLowUnit<DT>, o[i][j]);
+                o[i][2 + j] = 0.0f;
+              }
+          } else if constexpr (APART) {
             mma<DT>(o[2 * c], low, b[0], b[1]);
             mma<DT>(o[2 * c + 1], low, b[2], b[3]);
           }
@@ -584,14 +622,16 @@ __global__ __launch_bounds__(Shape<D, HB, APART>::kThreads, Shape<D, HB, APART>:
         cur.ref[half] = m[half];
         cur.l[half] = l[half];
       }
+      constexpr float kUnit = 1.0f / kWeightUnit<DT>, kLow = kUnit / kLowUnit<DT>;
 #pragma unroll
       for (int c = 0; c < C / 8; ++c) {
         if constexpr (HB == 16) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) cur.v[4 * c + j] = o[c][j];
+          for (int j = 0; j < 4; ++j) cur.v[4 * c + j] = o[c][j] * kUnit;
         } else {  // rows 8..15 hold the low parts (nothing if those have a product of their own)
-          cur.v[2 * c] = APART ? o[c][0] : o[c][0] + o[c][2];
-          cur.v[2 * c + 1] = APART ? o[c][1] : o[c][1] + o[c][3];
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            cur.v[2 * c + j] = APART ? o[c][j] * kUnit : __fmaf_rn(o[c][2 + j], kLow, o[c][j] * kUnit);
         }
       }
       // (at most 2^kLevels leaves; the last one's subtree stays in cur)

@@ -473,3 +473,53 @@ def test_tables_far_wider_than_the_sequences(seqs, hk):
     wide[:, :table.shape[1]] = table
     got = attend(q, kc, vc, wide, lengths)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("hq,hk,d", [(1, 1, 64), (8, 1, 128), (6, 2, 192), (12, 1, 96), (16, 1, 64), (32, 2, 256)])
+@pytest.mark.parametrize("copies", [1, 60])
+def test_one_token_far_ahead_of_the_others(dtype, hq, hk, d, copies):
+    """A token of value 0 whose score is far above all others': what is left of
+    them is the result, and it carries the output's rounding alone."""
+    cases = [(n, gap, size) for n in (17, 32, 100, 700) for gap, size in (
+        (3.0, 1.0), (8.3, 1.0), (10.2, 20.0), (12.9, 900.0), (16.6, 5000.0), (20.3, 60000.0), (24.7, 60000.0))]
+    q, kc, vc, table, lengths = build([c[0] for c in cases], hq, hk, d, 16, dtype)
+    held = torch.isfinite(vc[..., :1])
+    g = torch.Generator(device="cuda").manual_seed(9)
+    near = torch.rand(kc.shape[:3], generator=g, device="cuda")
+    kc[..., 0], kc[..., 1], kc[..., 2:] = 0.0, near.to(DT[dtype]), 0.0
+    vc.copy_(torch.rand(vc.shape, generator=g, device="cuda") + 0.5)
+    for b, (n, gap, size) in enumerate(cases):
+        pages = table[b, :-(-n // 16)].long()
+        vc[pages] = (vc[pages].float() * size / 1.5).to(DT[dtype])
+        first = (n * 7) // 11
+        kc[pages[first // 16], first % 16, :, 0] = gap
+        vc[pages[first // 16], first % 16] = 0.0
+    kc.masked_fill_(~held, math.nan)
+    vc.masked_fill_(~held, math.nan)
+    q.zero_()
+    q[..., 0] = q[..., 1] = 1.0
+    many = attend(q.repeat(copies, 1, 1), kc, vc, table.repeat(copies, 1), lengths.repeat(copies), scale=1.0)
+    n = len(cases)
+    check((many[0][-n:], many[1][-n:]), q, kc, vc, table, lengths, scale=1.0, dtype=dtype)
+
+
+def test_long_and_large_scores_of_binary16():
+    q, kc, vc, table, lengths = build([70001, 3], 8, 1, 64, 64, "f16", spare=1)
+    q *= 8
+    check(attend(q, kc, vc, table, lengths), q, kc, vc, table, lengths, dtype="f16")
+    kc[table[0, 1000].long(), 5] = q[0, :1] * 2  # one key far ahead of the rest
+    check(attend(q, kc, vc, table, lengths), q, kc, vc, table, lengths, dtype="f16")
+
+
+@pytest.mark.parametrize("hq", [8, 16])
+def test_nan_and_infinity_of_attended_tokens_of_binary16(hq):
+    q, kc, vc, table, lengths = build([40, 40, 40], hq, 1, 64, 16, "f16")
+    kc[table[0, 1].long(), 3] = math.nan
+    vc[table[1, 1].long(), 3, 0, 7] = math.inf
+    out, lse = attend(q, kc, vc, table, lengths)
+    assert bool(torch.isnan(out[0]).all()) and bool(torch.isnan(lse[0]).all())
+    assert bool((out[1, :, 7] == math.inf).all())
+    keep = [i for i in range(64) if i != 7]
+    assert bool(torch.isfinite(out[1][:, keep]).all())
+    check((out[2:], lse[2:]), q[2:], kc, vc, table[2:], lengths[2:], dtype="f16")
