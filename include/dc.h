@@ -474,9 +474,11 @@ dc_status_t dc_kv_append(const dc_kv_append_t *args, dc_stream_t stream);
  * workspace: device memory of at least dc_attention_workspace_bytes(seqs,
  * q_heads, kv_heads, dim, max_tokens) bytes, 16-byte aligned, owned by the
  * caller, zero before its first use (each call leaves it ready for the next,
- * of any shape it is large enough for).  max_tokens: table_width * page_size,
- * or the window if that is shorter.  Calls on one workspace must not overlap
- * on the GPU: one per stream.
+ * of any shape it is large enough for, and with any workspace_bytes that is
+ * enough for that call).  Memory that starts elsewhere, inside a workspace too,
+ * is another workspace.  max_tokens: table_width * page_size, or the window if
+ * that is shorter.  Calls on one workspace must not overlap on the GPU: one per
+ * stream.
  */
 typedef struct {
     const void *q;

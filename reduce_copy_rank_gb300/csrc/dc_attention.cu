@@ -717,7 +717,8 @@ __global__ __launch_bounds__(Shape<D, HB, APART>::kThreads, Shape<D, HB, APART>:
   }
   if (pieces == 1) return;
 
-  uint32_t* counters = reinterpret_cast<uint32_t*>(p.counters) + static_cast<uint64_t>(unit) * kAttendCounters;
+  const uint32_t per_unit = attend_counters(static_cast<uint32_t>(p.pieces));
+  uint32_t* counters = reinterpret_cast<uint32_t*>(p.counters) + static_cast<uint64_t>(unit) * per_unit;
   if (in_cluster) {
     // the pieces are one cluster's CTAs: each joins a share of the columns
     // from all of them, through shared memory
@@ -751,7 +752,14 @@ __global__ __launch_bounds__(Shape<D, HB, APART>::kThreads, Shape<D, HB, APART>:
   const uint32_t groups = (pieces + kAttendJoin - 1) / kAttendJoin;
   uint32_t base = piece / kAttendJoin * kAttendJoin, step = 1;
   uint32_t count = min(static_cast<uint32_t>(kAttendJoin), pieces - base);
-  bool last = arrive_last(counters + 1 + piece / kAttendJoin, count, &last_flag);
+  const bool alone = LOOP && p.places == 1;  // this CTA has computed them all, in order
+  bool last;
+  if (alone) {
+    __syncthreads();  // its threads' parts of the pieces
+    last = piece + 1 == base + count;
+  } else {
+    last = arrive_last(counters + (per_unit > 1 ? 1 : 0) + piece / kAttendJoin, count, &last_flag);
+  }
   while (last) {
     const bool done = step > 1 || groups == 1;
     for (int i = threadIdx.x; i < nh * (D / 4); i += kThreads) {
@@ -780,7 +788,12 @@ __global__ __launch_bounds__(Shape<D, HB, APART>::kThreads, Shape<D, HB, APART>:
       else st_piece<D, HB>(w, base, p.pieces + base / kAttendJoin, h, d, v, M, l16);
     }
     if (done) break;
-    last = arrive_last(counters, groups, &last_flag);
+    if (alone) {
+      __syncthreads();
+      last = piece + 1 == pieces;
+    } else {
+      last = arrive_last(counters, groups, &last_flag);
+    }
     base = 0;
     step = kAttendJoin;
     count = groups;

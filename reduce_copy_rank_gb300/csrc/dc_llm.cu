@@ -220,11 +220,6 @@ dc_status_t check_table(const void* p, int64_t rows, int64_t width, int64_t stri
   return take(p, "page_table", static_cast<uint64_t>((rows - 1) * (rows > 1 ? stride : 0) + width) * 4, 4, to);
 }
 
-// Workspace: the arrival counters at its start, in a part whose size follows
-// from the workspace's alone (so calls of different shapes agree on it), then
-// the pieces' partial results.  A unit's partials take more than 256 bytes.
-uint64_t counter_bytes(uint64_t workspace) { return (workspace / 64 + 15) / 16 * 16; }
-
 struct AttendPlan {
   int head_blocks, hb;
   uint32_t pieces;         // most pieces that one sequence is cut into
@@ -493,7 +488,8 @@ size_t dc_attention_workspace_bytes(int64_t seqs, int q_heads, int kv_heads, int
   AttendPlan plan{};
   if (max_tokens < 0 || plan_attend(seqs, q_heads, kv_heads, dim, static_cast<uint64_t>(max_tokens), &plan) != DC_OK)
     return 0;
-  return static_cast<size_t>((plan.partial_bytes + plan.partial_bytes / 32 + 1024) / 256 * 256);
+  // (1024: a workspace of a call that needs none is not empty; 0 says that there is no such call)
+  return static_cast<size_t>(plan.partial_bytes ? (kAttendCounterBytes + plan.partial_bytes + 255) / 256 * 256 : 1024);
 }
 
 dc_status_t dc_paged_attention(const dc_paged_attention_t* a, dc_stream_t stream) {
@@ -519,9 +515,8 @@ dc_status_t dc_paged_attention(const dc_paged_attention_t* a, dc_stream_t stream
   DC_TRY(check_tokens(a->out, "out", n, a->q_heads, a->dim, a->out_seq_stride, a->out_head_stride, 2, out));
   DC_TRY(check_written("out", n, a->q_heads, a->dim, a->out_seq_stride, a->out_head_stride));
   if (a->lse) DC_TRY(take(a->lse, "lse", n * static_cast<uint64_t>(a->q_heads) * 4, 4, out));
-  const uint64_t head = counter_bytes(a->workspace_bytes);
-  if (plan.partial_bytes) {
-    if (plan.units * kAttendCounters * 4 > head || head + plan.partial_bytes > a->workspace_bytes)
+  if (plan.partial_bytes) {  // the counters, then the pieces' partial results
+    if (kAttendCounterBytes + plan.partial_bytes > a->workspace_bytes)
       return fail(DC_ERR_INVALID, "the workspace holds %llu bytes; dc_attention_workspace_bytes says %llu",
                   static_cast<unsigned long long>(a->workspace_bytes),
                   static_cast<unsigned long long>(dc_attention_workspace_bytes(
@@ -541,7 +536,7 @@ dc_status_t dc_paged_attention(const dc_paged_attention_t* a, dc_stream_t stream
   p.table = addr(a->page_table);
   p.lengths = addr(a->lengths);
   p.counters = addr(a->workspace);
-  p.partial = addr(a->workspace) + head;
+  p.partial = addr(a->workspace) + kAttendCounterBytes;
   p.table_stride = a->seqs > 1 ? a->table_stride : 0;
   p.num_pages = a->num_pages;
   p.page_size = static_cast<uint32_t>(a->page_size);
@@ -569,6 +564,8 @@ dc_status_t dc_paged_attention(const dc_paged_attention_t* a, dc_stream_t stream
   // on an SM): beyond four times the CTAs that fill it, a unit's take turns.
   if (!cluster && plan.pieces > 8 && plan.units * plan.pieces > 4 * kAttendCtas)
     p.places = static_cast<int32_t>(std::max<uint64_t>(8, std::min<uint64_t>(plan.pieces, 4 * kAttendCtas / plan.units)));
+  // more units than the counters have room for (29127 at least): a CTA each
+  if (!cluster && plan.pieces > 1 && plan.units * attend_counters(plan.pieces) * 4 > kAttendCounterBytes) p.places = 1;
   p.page_shift = (p.page_size & (p.page_size - 1)) == 0 ? __builtin_ctz(p.page_size) : -1;
   p.scale = a->scale;
   int grid = 0;

@@ -110,14 +110,22 @@ constexpr int kAttendTile = 16;       // tokens a warp takes at a time
 constexpr int kAttendJoin = 16;       // pieces that one CTA joins at a time
 constexpr int kAttendCluster = 8;     // most CTAs of a cluster, which join their pieces in shared memory
 constexpr int kAttendGroups = 8;      // groups of them, at most (128 pieces)
-constexpr int kAttendCounters = 9;    // arrival counters of a unit: of its groups, and of each group's pieces
+// Arrival counters, at the start of a workspace: an area of one size, whatever
+// the workspace's, so that calls on parts of it of different lengths agree on
+// what has to be zero.  A unit has one, or, if it may have several groups, one
+// for them and one for each group's pieces; units beyond the area's room are
+// computed by a CTA each.
+constexpr uint64_t kAttendCounterBytes = 1 << 20;
+__host__ __device__ constexpr uint32_t attend_counters(uint32_t pieces) {
+  return pieces <= static_cast<uint32_t>(kAttendJoin) ? 1u : 1u + (pieces + kAttendJoin - 1) / kAttendJoin;
+}
 
 struct AttendParams {
   uint64_t q, q_seq, q_head;            // bytes
   uint64_t out, out_seq, out_head;
   uint64_t lse;                         // f32 [seqs, q_heads] or 0
   uint64_t table, lengths;              // int32
-  uint64_t counters;                    // uint32 [units][kAttendCounters], zero between calls
+  uint64_t counters;                    // uint32 [units][attend_counters(pieces)], zero between calls
   uint64_t partial;                     // f32 [units][HB * (pieces * (dim + 2) + 2 * kAttendGroups)]
   int64_t table_stride;
   int64_t num_pages;
@@ -127,7 +135,7 @@ struct AttendParams {
   int32_t window;
   int32_t units;                        // seqs * kv_heads * head_blocks
   int32_t pieces;                       // most pieces of one sequence
-  int32_t places;                       // CTAs of a unit: pieces, the cluster they fit in, or fewer that take turns
+  int32_t places;                       // CTAs of a unit: pieces, the cluster they fit in, fewer that take turns, or one
   int32_t cluster;                      // places, or 1: pieces are joined through the workspace
   int32_t page_shift;                   // log2 of the page size, -1 if it is no power of two
   float scale;

@@ -238,7 +238,8 @@ def attention_workspace(seqs: int, q_heads: int, kv_heads: int, dim: int, max_to
     """A zeroed workspace tensor for :func:`paged_attention` with up to
     ``seqs`` sequences and page tables of up to ``max_tokens`` tokens a row
     (allocated by torch; the library itself allocates nothing).  Keep it: a
-    call leaves it ready for the next.  One workspace per stream."""
+    call leaves it, and any part of it that starts where it does, ready for
+    the next.  One workspace per stream."""
     import torch
 
     n = dc_attention_workspace_bytes(seqs, q_heads, kv_heads, dim, max_tokens)

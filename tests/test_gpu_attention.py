@@ -523,3 +523,35 @@ def test_nan_and_infinity_of_attended_tokens_of_binary16(hq):
     keep = [i for i in range(64) if i != 7]
     assert bool(torch.isfinite(out[1][:, keep]).all())
     check((out[2:], lse[2:]), q[2:], kc, vc, table[2:], lengths[2:], dtype="f16")
+
+
+def test_one_buffer_passed_in_parts_of_different_lengths():
+    """Calls that pass as much of a workspace as they need: a small one's partial results are no counters of a larger one."""
+    small, large = dc.dc_attention_workspace_bytes(4, 8, 1, 128, 4096), dc.dc_attention_workspace_bytes(64, 32, 8, 128, 8192)
+    assert small < large
+    ws = torch.zeros(large, dtype=torch.uint8, device="cuda")
+    a = build([4096, 3000, 17, 4000], 8, 1, 128, 64, spare=1)
+    b = build([8192 - 37 * i for i in range(64)], 32, 8, 128, 64, spare=1)
+    want_a, want_b = attend(*a), attend(*b)
+    for _ in range(2):
+        got = attend(*a, workspace=ws[:small])
+        assert torch.equal(got[0], want_a[0]) and torch.equal(got[1], want_a[1])
+        got = attend(*b, workspace=ws)
+        assert torch.equal(got[0], want_b[0]) and torch.equal(got[1], want_b[1])
+
+
+def test_more_sequences_than_counters():
+    """So many sequences and key heads that a CTA computes each from end to end."""
+    hk, d, page, pages = 64, 64, 1024, 129
+    lengths = [131072, 70001, 9000, 700, 0, 1, 130] + [(b * 37) % 200 for b in range(1363)]
+    g = torch.Generator(device="cuda").manual_seed(6)
+    kc, vc = (torch.randn(pages, page, hk, d, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    table = torch.randint(0, pages, (len(lengths), 128), generator=g, device="cuda", dtype=torch.int32)
+    table[0] = torch.arange(128, 0, -1)
+    q = torch.randn(len(lengths), hk, d, generator=g, device="cuda").to(torch.bfloat16)
+    n = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    out, lse = attend(q, kc, vc, table, n)
+    for b in (*range(8), 700, 1369):
+        one = attend(q[b:b + 1], kc, vc, table[b:b + 1], n[b:b + 1])
+        assert torch.equal(out[b], one[0][0]) and torch.equal(lse[b], one[1][0]), b
+    check((out[1:9], lse[1:9]), q[1:9], kc, vc, table[1:9], n[1:9])
