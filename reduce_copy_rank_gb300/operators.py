@@ -177,7 +177,7 @@ _function = None
 def logprobs_and_entropy(shards: Sequence, tokens, vocab: int | None = None, temperature: float = 1.0):
     """``(logprobs, entropy)`` of :func:`token_logprobs` as new tensors that
     autograd differentiates with respect to every shard (through
-    :func:`token_logprobs_backward`)."""
+    :func:`token_logprobs_backward`), once: a second derivative raises."""
     global _function
     import torch
 
@@ -201,7 +201,20 @@ def logprobs_and_entropy(shards: Sequence, tokens, vocab: int | None = None, tem
                 g, h = (None if u is None else u.to(torch.float32).contiguous() for u in (g, h))
                 token_logprobs_backward(shards, tokens, lse, g, grads, entropy=entropy, grad_entropy=h,
                                         vocab=ctx.vocab, temperature=ctx.temperature)
+                if torch.is_grad_enabled():  # create_graph: the gradients leave a kernel, no graph holds them
+                    grads = FirstDerivative.apply(len(grads), *grads, *shards, *(u for u in (g, h) if u is not None))
                 return (None, None, None, *grads)
+
+        class FirstDerivative(torch.autograd.Function):
+            """The gradients, with the tensors that they depend on: their own derivative is refused."""
+
+            @staticmethod
+            def forward(ctx, count, *tensors):
+                return tuple(t.detach() for t in tensors[:count])
+
+            @staticmethod
+            def backward(ctx, *_):
+                raise RuntimeError("logprobs_and_entropy has no second derivative: its gradients cannot be differentiated")
 
         _function = TokenLogprobs
     return _function.apply(tokens, vocab, temperature, *shards)

@@ -495,3 +495,21 @@ def test_largest_vocabulary(dtype, vocab):
     check(score([x], tokens, top=32), x, tokens, top=32)
     with pytest.raises(dc.DCError):
         score([torch.empty(1, (4 << 20) + 1, device="cuda", dtype=DT[dtype])], tokens[:1])
+
+
+def test_second_derivative_is_refused():
+    """A penalty on the gradient raises instead of counting for nothing."""
+    x, tokens = logits(4, 900, torch.float32)
+    x.requires_grad_()
+    lp, _ = dc.logprobs_and_entropy([x], tokens)
+    g, = torch.autograd.grad(lp.sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="no second derivative"):
+        (g.square().sum() + x.square().sum()).backward()
+    up = torch.ones(4, device="cuda", requires_grad=True)  # nor with respect to the upstream gradient
+    lp, _ = dc.logprobs_and_entropy([x], tokens)
+    g2, = torch.autograd.grad(lp, x, up, create_graph=True)
+    with pytest.raises(RuntimeError, match="no second derivative"):
+        torch.autograd.grad(g2.sum(), up)
+    lp, _ = dc.logprobs_and_entropy([x], tokens)  # the first derivative is what it was
+    again, = torch.autograd.grad(lp.sum(), x)
+    assert torch.equal(again, g)
