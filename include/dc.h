@@ -327,6 +327,7 @@ dc_status_t dc_fused_all_gather_static(const void *const *in_ptrs, void *const *
  *   `widths[r]` columns, row i at shards[r] + i * row_strides[r].  Shards may
  *   be uneven, empty, or column ranges of one tensor; any alignment of the
  *   element type.  Columns past `vocab` (padding) are not read.
+ * temperature: 4.24e-39 (so that log2(e) / temperature fits binary32) to 1e30.
  * tokens: int32 or int64 (tokens_64).  A negative token asks for nothing:
  *   its log probability is 0.  A token of vocab or more gives NaN.
  * logprobs [rows]; entropy, lse [rows] and top_logprobs, top_tokens

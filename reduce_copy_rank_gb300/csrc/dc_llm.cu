@@ -107,8 +107,9 @@ dc_status_t check_logits(const void* const* shards, const uint64_t* widths, cons
   if (vocab < 1 || vocab > kMaxVocab)
     return fail(DC_ERR_INVALID, "vocab = %lld is outside 1..%d", static_cast<long long>(vocab), kMaxVocab);
   if (dtype < kBF16 || dtype > kF32) return fail(DC_ERR_INVALID, "dtype %d is not DC_BF16, DC_F16 or DC_F32", dtype);
-  if (!(temperature > 0.0) || !std::isfinite(temperature) || !std::isfinite(static_cast<float>(1.0 / temperature)) ||
-      static_cast<float>(1.0 / temperature) < 1e-30f)
+  // (the kernels' exponents are in units of log2(e) / temperature, in binary32)
+  if (!(temperature > 0.0) || !std::isfinite(temperature) ||
+      !std::isfinite(static_cast<float>(1.0 / temperature) * 1.44269504f) || static_cast<float>(1.0 / temperature) < 1e-30f)
     return fail(DC_ERR_INVALID, "temperature %g is not a positive number of usable size", temperature);
   if (!shards || !widths || !strides) return fail(DC_ERR_INVALID, "%s, widths and strides must not be NULL", what);
   const uint64_t es = static_cast<uint64_t>(elem_bytes(dtype));

@@ -27,6 +27,8 @@
 // 7.0 TB/s; 1021 x 50021 f32 on 3 ranks with 5 alternatives 51 us, 4.1 TB/s; 128
 // x 131072 bf16 on 8 ranks with 20 16 us; 4 x 32768 with 1 6.1 us.  Gradient:
 // 8192 x 127900 bf16 on 8 ranks 610 us, 6.9 TB/s; 509 x 50021 f16 17 us, 5.9 TB/s.
+#include <cfloat>
+
 #include "dc_llm.h"
 #include "dc_numeric.cuh"
 
@@ -487,8 +489,10 @@ __global__ __launch_bounds__(kScoreWarps * 32, 4) void dc_score_kernel(const __g
       lane_sums<DT, true>(raw, ref, c, 0u, s, t);
     } else {
       // 2^-400 is 0 in binary32; the step below the rounded number makes sure that it is low enough
+      // (and its exponent finite: at very low temperatures one step of the type may be beyond binary32)
       const uint32_t floor2 = Elem<DT>::below2(ref - 400.0f / c);
-      if (floor2 != Elem<DT>::kNegInfWord) lane_sums<DT, false>(raw, ref, c, floor2, s, t);
+      if (floor2 != Elem<DT>::kNegInfWord && (Elem<DT>::lo(floor2) - ref) * c >= -FLT_MAX)
+        lane_sums<DT, false>(raw, ref, c, floor2, s, t);
       else lane_sums<DT, true>(raw, ref, c, 0u, s, t);
     }
 #pragma unroll

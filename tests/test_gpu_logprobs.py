@@ -513,3 +513,30 @@ def test_second_derivative_is_refused():
     lp, _ = dc.logprobs_and_entropy([x], tokens)  # the first derivative is what it was
     again, = torch.autograd.grad(lp.sum(), x)
     assert torch.equal(again, g)
+
+
+@pytest.mark.parametrize("dtype,size,temperature", [
+    ("bf16", 1e38, 1e-3), ("bf16", 1e38, 1.0), ("bf16", 3.0, 1e-38), ("f16", 6e4, 5e-39), ("f16", 3e3, 5e-39), ("f16", 3.0, 1e-20),
+    ("f32", 1e38, 1e-3), ("f32", 3.0, 4.3e-39)])
+def test_temperatures_at_which_only_the_largest_logits_count(dtype, size, temperature):
+    """One step of the type is far more than the temperature: the row's largest
+    logits share the probability evenly, and nothing overflows to NaN."""
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x = ((torch.rand(5, 4100, generator=g, device="cuda") - 0.3) * size).to(DT[dtype])
+    x[0] = -x[0].abs()
+    x[1, :4000] = -math.inf
+    x[2, ::7] = torch.finfo(DT[dtype]).min
+    m = x.max(1, keepdim=True).values
+    tokens = x.argmax(1)
+    tokens[3] = x[3].argmin()
+    out = score([x], tokens, top=2, temperature=temperature)
+    ties = (x == m).sum(1).double().log().cpu()
+    lp = out["logprobs"].cpu().double()
+    tol = REL * (1 + math.log(4100))
+    assert bool(((out["entropy"].cpu().double() - ties).abs() <= tol).all())
+    rest = [0, 1, 2, 4]
+    assert bool(((lp + ties)[rest].abs() <= tol).all())
+    assert float(lp[3]) < -1e3
+    assert not bool(torch.isnan(out["lse"]).any())
+    first = torch.where(x == m, torch.arange(4100, device="cuda"), 4100).min(1).values
+    assert torch.equal(out["top_tokens"][:, 0], first)

@@ -211,3 +211,11 @@ def test_python_layouts_match_the_header(tmp_path):
 def test_unknown_fields_are_refused():
     with pytest.raises(TypeError):
         dc.dc_token_logprobs(shard=[1])
+
+
+@pytest.mark.parametrize("temperature,want", [
+    (1e-38, CUDA), (4.3e-39, CUDA), (4.2e-39, INVALID), (3e-39, INVALID), (1e30, CUDA), (1.1e30, INVALID)])
+def test_temperatures_whose_exponents_do_not_fit_binary32(temperature, want):
+    """log2(e) / temperature is at most FLT_MAX (3.4028e38, from 4.2397e-39 on), 1 / temperature at least 1e-30."""
+    assert score(temperature=temperature) == want, dc.last_error()
+    assert grad(temperature=temperature) == want, dc.last_error()
