@@ -2,6 +2,7 @@
 // the choice of grid, launch.
 #include <algorithm>
 #include <cmath>
+#include <numeric>
 
 #include "dc.h"
 #include "dc_host.h"
@@ -190,6 +191,65 @@ dc_status_t check_written(const char* name, uint64_t n, int heads, int dim, uint
   const uint64_t count[2] = {n, static_cast<uint64_t>(heads)}, stride[2] = {tok, head};
   if (folds(count, stride, 2, static_cast<uint64_t>(dim))) return fail(DC_ERR_OVERLAP, "%s: its rows overlap", name);
   return DC_OK;
+}
+
+// A strided tensor as blocks of `inner` bytes: its dimensions of more than one
+// place, the longest stride first.
+struct Blocks {
+  uint64_t base, inner;
+  uint64_t n[3], stride[3];
+  int dims;
+};
+Blocks blocks(const void* base, uint64_t inner, const uint64_t* n, const uint64_t* stride, int dims) {
+  Blocks b{addr(base), inner, {}, {}, 0};
+  for (int i = 0; i < dims; ++i) {
+    if (n[i] < 2 || stride[i] == 0) continue;
+    int at = b.dims++;
+    for (; at > 0 && b.stride[at - 1] < stride[i]; --at) {
+      b.n[at] = b.n[at - 1];
+      b.stride[at] = b.stride[at - 1];
+    }
+    b.n[at] = n[i];
+    b.stride[at] = stride[i];
+  }
+  return b;
+}
+// Bytes from the first to the last of the dimensions from `dim` on.
+uint64_t extent(const Blocks& b, int dim) {
+  uint64_t e = b.inner;
+  for (int i = dim; i < b.dims; ++i) e += (b.n[i] - 1) * b.stride[i];
+  return e;
+}
+// False if the dimensions of `a` from i on and those of `b` from j on, `off`
+// bytes behind, share no byte; true if they do or it cannot be shown that they
+// do not.  Where a byte of both is i * S + x = off + j * S + y, x and y inside
+// their blocks of at most S bytes, x - y is off modulo S: one of two numbers.
+bool blocks_meet(const Blocks& a, int i, const Blocks& b, int j, int64_t off) {
+  const uint64_t ea = extent(a, i), eb = extent(b, j);
+  if (off >= static_cast<int64_t>(ea) || off + static_cast<int64_t>(eb) <= 0) return false;
+  const uint64_t sa = i < a.dims ? a.stride[i] : 0, sb = j < b.dims ? b.stride[j] : 0;
+  uint64_t s = std::max(sa, sb);
+  if (s == 0) return true;
+  int ni = i + (sa == s), nj = j + (sb == s);
+  if (extent(a, ni) > s || extent(b, nj) > s) {
+    if (sa == 0 || sb == 0 || sa == sb) return true;
+    s = std::gcd(sa, sb);  // both in rows of what divides both strides
+    ni = i + 1;
+    nj = j + 1;
+    if (extent(a, ni) > s || extent(b, nj) > s) return true;
+  }
+  const int64_t m = static_cast<int64_t>(s), d = (off % m + m) % m;
+  return blocks_meet(a, ni, b, nj, d) || blocks_meet(a, ni, b, nj, d - m);
+}
+bool blocks_meet(const Blocks& a, const Blocks& b) {
+  if (!(a.base < b.base + extent(b, 0) && b.base < a.base + extent(a, 0))) return false;
+  return blocks_meet(a, 0, b, 0, static_cast<int64_t>(b.base - a.base));
+}
+
+// The blocks of a [n, heads, dim] tensor.
+Blocks token_blocks(const void* p, uint64_t n, int heads, int dim, uint64_t tok, uint64_t head, int es) {
+  const uint64_t e = static_cast<uint64_t>(es), count[2] = {n, static_cast<uint64_t>(heads)}, stride[2] = {tok * e, head * e};
+  return blocks(p, static_cast<uint64_t>(dim) * e, count, stride, 2);
 }
 
 dc_status_t check_cache(const dc_paged_cache_t& c, const char* name, int64_t pages, int page_size, int heads, int dim,
@@ -443,8 +503,13 @@ dc_status_t dc_kv_append(const dc_kv_append_t* a, dc_stream_t stream) {
       DC_TRY(check_disjoint(out, q));
       DC_TRY(check_disjoint(out, in));
     } else {
-      // in place: rows of queries beside rows of keys and values in one tensor are fine
-      DC_TRY(check_apart(out[0], in, 2));
+      // in place: heads of queries beside those of keys and values in one tensor are fine
+      const Blocks qb = token_blocks(a->q_out, n, a->q_heads, a->dim, a->q_out_token_stride, a->q_out_head_stride, es);
+      if (blocks_meet(qb, token_blocks(a->k, n, a->kv_heads, a->dim, a->k_token_stride, a->k_head_stride, es)))
+        return fail(DC_ERR_OVERLAP, "q_out overlaps k");
+      if (blocks_meet(qb, token_blocks(a->v, n, a->kv_heads, a->dim, a->v_token_stride, a->v_head_stride, es)))
+        return fail(DC_ERR_OVERLAP, "q_out overlaps v");
+      DC_TRY(check_apart(out[0], in, 2));  // (k and v are the first two)
     }
     DC_TRY(check_disjoint(out, cache));
     for (const Span& c : cache) DC_TRY(check_apart(c, q));

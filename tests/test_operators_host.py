@@ -219,3 +219,69 @@ def test_temperatures_whose_exponents_do_not_fit_binary32(temperature, want):
     """log2(e) / temperature is at most FLT_MAX (3.4028e38, from 4.2397e-39 on), 1 / temperature at least 1e-30."""
     assert score(temperature=temperature) == want, dc.last_error()
     assert grad(temperature=temperature) == want, dc.last_error()
+
+
+# queries, keys and values as heads of one tensor of 12 heads of 64 a token, the queries rotated in place
+FUSED = dict(q_out=at(0), k=at(0) + 8 * 128, v=at(0) + 10 * 128, q_token_stride=768, q_out_token_stride=768, k_token_stride=768,
+             v_token_stride=768)
+# ... and of 2 heads of each, side by side head by head
+TURNS = dict(q_out=at(0), k=at(0) + 128, v=at(0) + 256, q_heads=2, **{f"{x}_token_stride": 384 for x in ("q", "k", "v", "q_out")},
+             **{f"{x}_head_stride": 192 for x in ("q", "k", "v", "q_out")})
+
+
+@pytest.mark.parametrize("kw,want", [
+    ({}, CUDA), (dict(q=at(0) + 512, q_out=at(0) + 512, k=at(0), v=at(0) + 256), CUDA), (dict(k=at(1), v=at(2)), CUDA),
+    (dict(tokens=1), CUDA), (dict(tokens=1, k=at(0) + 7 * 128), OVERLAP),
+    (dict(k=at(0)), OVERLAP), (dict(v=at(0)), OVERLAP),                            # keys or values are queries
+    (dict(k=at(0) + 7 * 128), OVERLAP), (dict(v=at(0) + 128), OVERLAP),            # share a head, or are one head on
+    (dict(k=at(0) + 8 * 128 - 16), OVERLAP), (dict(v=at(0) + 11 * 128), OVERLAP),  # end or begin inside one; the next token's
+    (dict(k=at(0) + 768 * 2), OVERLAP), (dict(v=at(0) + 3 * 768 * 2 + 5 * 128), OVERLAP),  # a later token's queries
+    (dict(k_token_stride=0), CUDA), (dict(k=at(0) + 128, k_token_stride=0), OVERLAP),  # one token's keys for all
+    (dict(k_head_stride=0), CUDA), (dict(k=at(0) + 7 * 128, k_head_stride=0), OVERLAP),
+    (dict(k_token_stride=1536), CUDA), (dict(k=at(0) + 6 * 128, k_token_stride=1536), OVERLAP),
+    (dict(k_token_stride=776), OVERLAP),                                           # cannot be shown apart (and is not)
+    (dict(TURNS), CUDA), (dict(TURNS, k=at(0)), OVERLAP), (dict(TURNS, v=at(0) + 384), OVERLAP),
+    (dict(TURNS, k=at(0) + 112), OVERLAP), (dict(TURNS, k=at(0) + 144, v=at(0) + 256), CUDA),
+    # heads outside tokens: 7 tokens of 64 a head
+    (dict(k=at(0) + 8 * 7 * 128, v=at(0) + 10 * 7 * 128, **{f"{x}_token_stride": 64 for x in ("q", "k", "v", "q_out")},
+          **{f"{x}_head_stride": 448 for x in ("q", "k", "v", "q_out")}), CUDA),
+    (dict(k=at(0) + 7 * 7 * 128, v=at(0) + 10 * 7 * 128, **{f"{x}_token_stride": 64 for x in ("q", "k", "v", "q_out")},
+          **{f"{x}_head_stride": 448 for x in ("q", "k", "v", "q_out")}), OVERLAP)])
+def test_queries_in_place_share_nothing_with_keys_and_values(kw, want):
+    assert append(**{**FUSED, **kw}) == want, dc.last_error()
+
+
+def test_overlap_of_queries_in_place_against_every_byte():
+    """Random layouts: whatever shares a byte is refused, and what shares none in one fused layout is not."""
+    import random
+
+    rng = random.Random(11)
+    seen = {CUDA: 0, OVERLAP: 0}
+    for _ in range(4000):
+        n, hq, hk, unit = rng.randint(1, 4), rng.randint(1, 3), rng.randint(1, 2), 8 * rng.choice([1, 2, 4])
+        dim = 8 * rng.randint(1, 3)
+
+        def strides(heads):
+            head = unit * rng.randint(1, 4) if rng.random() < 0.8 else 0
+            token = unit * rng.randint(1, 14)
+            return token, head
+
+        qt, qh = strides(hq)
+        kt, kh = strides(hk) if rng.random() < 0.4 else (qt, qh)
+        base = at(0) + 4096
+        k = base + 2 * unit * rng.randint(-8, 24)
+
+        def covered(p, heads, t, h):
+            return {p + 2 * (i * t + j * h + e) for i in range(n) for j in range(heads) for e in range(dim)}
+
+        got = append(q=base, q_out=base, k=k, tokens=n, q_heads=hq, kv_heads=hk, dim=dim, rotary_dim=0, cos_sin=0,
+                     q_token_stride=qt, q_head_stride=qh, q_out_token_stride=qt, q_out_head_stride=qh, k_token_stride=kt,
+                     k_head_stride=kh, k_page_stride=16 * hk * 64, v_page_stride=16 * hk * 64, k_slot_stride=hk * 64,
+                     v_slot_stride=hk * 64)
+        if got == OVERLAP and "q_out: its rows" in dc.last_error():
+            continue
+        shared = covered(base, hq, qt, qh) & covered(k, hk, kt, kh)
+        assert got in (CUDA, OVERLAP), dc.last_error()
+        assert got == OVERLAP or not shared, (n, hq, hk, dim, qt, qh, kt, kh, k - base)
+        seen[got] += 1
+    assert min(seen.values()) > 500, seen
