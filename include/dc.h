@@ -425,9 +425,10 @@ typedef struct {
  * its q_out row is NaN.  Two tokens for one slot: either may remain.
  * The caches may be interleaved in one tensor (pages of keys beside pages of
  * values); what a call writes must not fold onto itself (a broadcast q_out or
- * cache) or overlap what it reads (DC_ERR_OVERLAP).  Queries rotated in place
- * may lie beside k and v in one tensor; layouts that cannot be shown to share
- * no byte are refused too.
+ * cache), share bytes with what else it writes (a cache that is the other, a
+ * slot or a head on) or overlap what it reads (DC_ERR_OVERLAP).  Queries
+ * rotated in place may lie beside k and v in one tensor; layouts that cannot be
+ * shown to share no byte are refused too.
  */
 typedef struct {
     const void *q;

@@ -252,6 +252,13 @@ Blocks token_blocks(const void* p, uint64_t n, int heads, int dim, uint64_t tok,
   return blocks(p, static_cast<uint64_t>(dim) * e, count, stride, 2);
 }
 
+Blocks cache_blocks(const dc_paged_cache_t& c, int64_t pages, int page_size, int heads, int dim, int es) {
+  const uint64_t e = static_cast<uint64_t>(es);
+  const uint64_t n[3] = {static_cast<uint64_t>(pages), static_cast<uint64_t>(page_size), static_cast<uint64_t>(heads)};
+  const uint64_t stride[3] = {c.page_stride * e, c.token_stride * e, c.head_stride * e};
+  return blocks(c.data, static_cast<uint64_t>(dim) * e, n, stride, 3);
+}
+
 dc_status_t check_cache(const dc_paged_cache_t& c, const char* name, int64_t pages, int page_size, int heads, int dim,
                         int es, bool written, PagedView* v, Spans& to) {
   if (pages < 1 || pages > 0x7FFFFFFF) return fail(DC_ERR_INVALID, "%lld pages", static_cast<long long>(pages));
@@ -489,8 +496,10 @@ dc_status_t dc_kv_append(const dc_kv_append_t* a, dc_stream_t stream) {
   }
   DC_TRY(check_cache(a->k_cache, "k_cache", a->num_pages, a->page_size, a->kv_heads, a->dim, es, true, &p.kc, cache));
   DC_TRY(check_cache(a->v_cache, "v_cache", a->num_pages, a->page_size, a->kv_heads, a->dim, es, true, &p.vc, cache));
-  if (a->k_cache.data == a->v_cache.data) return fail(DC_ERR_OVERLAP, "k_cache is v_cache");
-  // (the caches may be interleaved in one tensor: their spans may meet)
+  // (the caches may be interleaved in one tensor: their spans may meet, their tokens' heads not)
+  if (blocks_meet(cache_blocks(a->k_cache, a->num_pages, a->page_size, a->kv_heads, a->dim, es),
+                  cache_blocks(a->v_cache, a->num_pages, a->page_size, a->kv_heads, a->dim, es)))
+    return fail(DC_ERR_OVERLAP, "k_cache overlaps v_cache");
   for (const Span& c : cache) DC_TRY(check_apart(c, in));
   if (a->q_heads) {
     Spans q;

@@ -29,6 +29,18 @@ def pytest_configure(config):
         os.environ["DC_LIBRARY"] = "bounds"
 
 
+def pytest_collection_modifyitems(items):
+    # One parameter set of test_append_checks holds a wrong value and stays as it is: it expects
+    # v_cache = k_cache + 256 bytes to launch, where a slot is 256 bytes (2 heads of 64 in two bytes
+    # each), so that each value lies where the next slot's key does.  dc_kv_append refuses caches
+    # that share bytes (test_caches_share_nothing).
+    for item in items:
+        if getattr(item, "originalname", "") == "test_append_checks":
+            kw = item.callspec.params["kw"]
+            if set(kw) == {"v_cache"} and kw["v_cache"] - item.module.at(8) == 256:
+                item.add_marker(pytest.mark.xfail(strict=True, reason="its caches overlap by all slots but one"))
+
+
 @pytest.fixture(autouse=True)
 def _no_bounds_fault(request):
     """With --dc-bounds: after every GPU test, no kernel may have skipped an

@@ -285,3 +285,25 @@ def test_overlap_of_queries_in_place_against_every_byte():
         assert got == OVERLAP or not shared, (n, hq, hk, dim, qt, qh, kt, kh, k - base)
         seen[got] += 1
     assert min(seen.values()) > 500, seen
+
+
+# both caches in one tensor: strides of a token's 2 heads of 64, of a page of 16 tokens
+def both(page, slot, head, v, **kw):
+    return dict(k_page_stride=page, v_page_stride=page, k_slot_stride=slot, v_slot_stride=slot, k_cache_head_stride=head,
+                v_cache_head_stride=head, v_cache=at(8) + 2 * v, **kw)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (both(4096, 128, 64, 2048), CUDA), (both(2048, 128, 64, 2048 * 30), CUDA),         # page by page; one after the other
+    (both(4096, 256, 64, 128), CUDA), (both(4096, 256, 128, 64), CUDA),                # token by token, head by head
+    (both(4096, 64, 2048, 1024), CUDA), (both(4096, 128, 1024 * 2, 64), CUDA),         # the same with heads outside tokens
+    (both(2048, 128, 64, 0, num_pages=1), OVERLAP), (both(2048, 128, 64, 2048, num_pages=1), CUDA),
+    (both(2048, 128, 64, 128), OVERLAP), (both(2048, 128, 64, 64), OVERLAP), (both(2048, 128, 64, 8), OVERLAP),
+    (both(2048, 128, 64, 2048), OVERLAP), (both(2048, 128, 64, 2048 * 29 + 1920), OVERLAP),  # one page on; the last slot
+    (both(4096, 128, 64, 1984), OVERLAP), (both(4096, 128, 64, 2112), OVERLAP),        # a head into the other's page
+    (both(4096, 256, 64, 192), OVERLAP), (both(4096, 256, 128, 72), OVERLAP), (both(4096, 64, 2048, 960), OVERLAP),
+    (dict(both(4096, 128, 64, 2048), v_slot_stride=64, v_cache_head_stride=1024), CUDA),  # laid out differently inside pages
+    (dict(both(4096, 128, 64, 2048), v_page_stride=8192), CUDA), (dict(both(4096, 128, 64, 2048), v_page_stride=6144), OVERLAP),
+    (dict(both(4096, 128, 64, 2048), k_cache=at(8) + 4096, v_cache=at(8)), CUDA)])
+def test_caches_share_nothing(kw, want):
+    assert append(**kw) == want, dc.last_error()
