@@ -370,8 +370,12 @@ dc_status_t dc_token_logprobs(const dc_token_logprobs_t *args, dc_stream_t strea
  *
  * g = grad_logprobs and h = grad_entropy [rows], either NULL (zero); h needs
  * `entropy`.  A negative token's g counts as 0.  grads[r] has widths[r]
- * columns; padding columns receive 0, as do rows of nothing but masks (-inf or
- * the type's lowest value: lse <= -1e30).
+ * columns; padding columns receive 0, as do rows whose lse is -1e30 or less:
+ * rows of nothing but -inf, or but the lowest value of DC_BF16 or DC_F32, whose
+ * lse cannot hold the log of how many they are.  A row of nothing but DC_F16's
+ * lowest value (-65504) is a row like others, with the gradient of its uniform
+ * probabilities.  log p_i = z_i - lse is good to 2^-24 |lse|, the rounding of
+ * lse, and p_i with it.
  * grads[r] may be exactly shards[r] (in place); any other overlap is refused.
  */
 typedef struct {

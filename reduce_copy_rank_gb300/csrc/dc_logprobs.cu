@@ -780,7 +780,8 @@ __global__ __launch_bounds__(kGradThreads) void dc_score_grad_kernel(const __gri
     t.nh = -h;
     t.ngh = -(t.g + (p.grad_entropy ? h * ld_entry<float>(p.entropy, row, p.rows, kSiteRow) : 0.0f));
     t.inv_t = p.inv_t;
-    // a row of nothing but masks (-inf or the type's lowest) has no gradient: p = 0 everywhere
+    // a row of nothing but -inf, or but the lowest of BF16 or FP32 beside which lse loses the row's
+    // log of a count, has no gradient: p = 0 everywhere (FP16's lowest, -65504, is a number like others)
     const bool none = lse <= -1e30f;
     t.lse = none ? __int_as_float(0x7F800000) : lse;
     t.token = !none && token >= static_cast<int64_t>(sh.first) && token < static_cast<int64_t>(sh.first) + sh.width

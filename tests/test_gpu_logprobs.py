@@ -540,3 +540,29 @@ def test_temperatures_at_which_only_the_largest_logits_count(dtype, size, temper
     assert not bool(torch.isnan(out["lse"]).any())
     first = torch.where(x == m, torch.arange(4100, device="cuda"), 4100).min(1).values
     assert torch.equal(out["top_tokens"][:, 0], first)
+
+
+@pytest.mark.parametrize("temperature", [0.5, 1.0])
+@pytest.mark.parametrize("dtype,value", [("bf16", None), ("f16", None), ("f32", None), ("f32", -2e30), ("f16", -math.inf)])
+def test_gradient_of_rows_of_one_mask(dtype, value, temperature):
+    """Rows of nothing but the type's lowest value (or a number like it): no
+    gradient where lse is -1e30 or less, the uniform one where it is not."""
+    vocab = 5000
+    x = torch.full((3, vocab), torch.finfo(DT[dtype]).min if value is None else value, device="cuda", dtype=DT[dtype])
+    tokens = torch.tensor([3, 4999, -1], device="cuda")
+    out = score([x], tokens, temperature=temperature)
+    g, h = torch.tensor([1.0, -2.0, 1.0], device="cuda"), torch.tensor([0.0, 0.5, 0.5], device="cuda")
+    grads = [torch.full_like(x, 7.0)]
+    dc.token_logprobs_backward([x], tokens, out["lse"], g, grads, entropy=out["entropy"], grad_entropy=h,
+                               temperature=temperature)
+    if float(out["lse"].max()) <= -1e30:
+        assert value is not None or dtype != "f16"
+        assert bool((grads[0] == 0).all())
+        return
+    assert dtype == "f16"
+    z = torch.zeros_like(x)  # the same probabilities
+    want, size = exact_grad(z, tokens, g, h, temperature)
+    # lse of magnitude 65504 / temperature is off by half its last place, log p + H by that and H's own error
+    lse_off = 2.0 ** -24 * 65536 / temperature + 2 * REL * (1 + math.log(vocab))
+    over = (grads[0].cpu().double() - want).abs() - (UNIT[dtype] * want.abs() + lse_off * (1 + lse_off) * size + 2.0 ** -25)
+    assert float(over.max()) <= 0
