@@ -5,7 +5,9 @@ linked into ``reduce_copy_rank_gb300/libdc.so`` with the CUDA runtime linked
 statically, so the library needs nothing but the driver at run time.
 Floating point: no fast-math, no flush-to-zero, no contraction.
 Beside it, ``csrc/binding.cpp`` becomes the extension module ``_binding``, which
-reads torch tensors for the language-model operators (needs torch's headers).
+reads torch tensors for the language-model operators (needs torch's headers and
+Python's).  The library does not need it: where it cannot be built, that is a
+warning, and those operators' tensor functions raise when called.
 """
 from __future__ import annotations
 
@@ -16,6 +18,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -64,7 +67,7 @@ def up_to_date(lib: str = LIB) -> bool:
 
 def build_binding(force: bool = False) -> str | None:
     """Compile the extension module unless it is newer than its sources; None
-    if torch is not installed."""
+    if torch is not installed.  Raises RuntimeError (or OSError) if it fails."""
     spec = importlib.util.find_spec("torch")
     if spec is None or not spec.origin:
         return None
@@ -88,12 +91,25 @@ def build_binding(force: bool = False) -> str | None:
     return BINDING
 
 
+def _try_binding(force: bool) -> None:
+    """The extension module if it can be built; else a warning, and no module:
+    one of older sources would read the argument blocks of other layouts."""
+    try:
+        build_binding(force)
+    except (RuntimeError, OSError) as e:
+        if os.path.exists(BINDING):
+            os.unlink(BINDING)
+        warnings.warn(f"the extension module of the language-model operators was not built (the library does not need it): {e}",
+                      RuntimeWarning, stacklevel=3)
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False, bounds: bool = False) -> str:
     """Compile and link libdc.so (bounds=True: the bounds-checked
-    libdc_bounds.so) unless it is newer than every source."""
+    libdc_bounds.so) unless it is newer than every source, and the extension
+    module where that is possible."""
     lib, objdir = (LIB_BOUNDS, OBJDIR_BOUNDS) if bounds else (LIB, OBJDIR)
     if not force and up_to_date(lib):
-        build_binding()
+        _try_binding(False)
         return lib
     nvcc = _nvcc()
     os.makedirs(objdir, exist_ok=True)
@@ -113,7 +129,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False, 
 
     srcs = sources()
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
-        binding = ex.submit(build_binding, force)
+        binding = ex.submit(_try_binding, force)
         objs = list(ex.map(compile_one, srcs))
         binding.result()
     tmp = lib + f".tmp{os.getpid()}"
