@@ -5,7 +5,9 @@
 // of seven tensors cost 5 of the 8 microseconds of a paged attention call.
 // This extension module reads them in C++ and calls the library.  It holds no
 // state but the library's entry points, and does no work of its own: every
-// function returns the library's status.
+// function returns the library's status.  What a call has written counts as
+// changed in place (its version moves on), so that autograd notices where it
+// had kept those numbers.
 #include <Python.h>
 
 #include <c10/cuda/CUDAStream.h>
@@ -102,12 +104,6 @@ const void* vector(const Call& c, PyObject* o, const char* what, int64_t n, at::
   shaped(t, what, n);
   return t.const_data_ptr();
 }
-void* out_vector(const Call& c, PyObject* o, const char* what, int64_t n, at::ScalarType type, bool optional = false) {
-  if (optional && o == Py_None) return nullptr;
-  const at::Tensor& t = on(c, o, what, type);
-  shaped(t, what, n);
-  return t.mutable_data_ptr();
-}
 
 // The call's device and stream; `first` is its first tensor: if that is on no
 // GPU the checks refuse it without touching CUDA.
@@ -155,13 +151,28 @@ struct Items {
   PyObject* operator[](Py_ssize_t i) const { return PySequence_Fast_GET_ITEM(fast, i); }
 };
 
+// The tensors that a call writes.
+struct Written {
+  const at::Tensor* t[DC_MAX_RANKS];
+  int n = 0;
+  const at::Tensor& operator()(const at::Tensor& x) {
+    if (n < DC_MAX_RANKS) t[n++] = &x;
+    return x;
+  }
+  PyObject* after(dc_status_t status) const {
+    for (int i = 0; i < n && status == DC_OK; ++i)
+      if (!t[i]->is_inference()) t[i]->unsafeGetTensorImpl()->bump_version();
+    return PyLong_FromLong(status);
+  }
+};
+
 // Ranks' [rows, width] matrices.
 struct Matrices {
   const void* data[DC_MAX_RANKS];
   uint64_t width[DC_MAX_RANKS], stride[DC_MAX_RANKS];
   int64_t total = 0;
 };
-void matrices(const Call& c, const Items& items, const char* what, int64_t rows, at::ScalarType type, bool written,
+void matrices(const Call& c, const Items& items, const char* what, int64_t rows, at::ScalarType type, Written* w,
               Matrices& m) {
   for (Py_ssize_t r = 0; r < items.size(); ++r) {
     const at::Tensor& t = on(c, items[r], what, type, r);
@@ -170,7 +181,7 @@ void matrices(const Call& c, const Items& items, const char* what, int64_t rows,
     if (t.stride(1) != 1 && t.size(1) > 1) wrong(indexed(what, r) + ": the vocabulary dimension must be contiguous");
     m.total += t.size(1);
     if (r >= DC_MAX_RANKS) continue;  // (the library refuses the count)
-    m.data[r] = written ? t.mutable_data_ptr() : t.const_data_ptr();
+    m.data[r] = w ? (*w)(t).mutable_data_ptr() : t.const_data_ptr();
     m.width[r] = static_cast<uint64_t>(t.size(1));
     m.stride[r] = static_cast<uint64_t>(t.stride(0));
   }
@@ -191,14 +202,23 @@ Logits logits(const Items& shards) {
   return Logits{first.size(0), first.scalar_type(), code};
 }
 
+// A contiguous [n] output; NULL for None where that is allowed.
+void* out_vector(const Call& c, PyObject* o, const char* what, int64_t n, at::ScalarType type, Written& w,
+                 bool optional = false) {
+  if (optional && o == Py_None) return nullptr;
+  const at::Tensor& t = on(c, o, what, type);
+  shaped(t, what, n);
+  return w(t).mutable_data_ptr();
+}
+
 // A contiguous [rows, k] output; k < 0: any, and it is set.
-void* alternatives(const Call& c, PyObject* o, const char* what, int64_t rows, at::ScalarType type, int64_t& k) {
+void* alternatives(const Call& c, PyObject* o, const char* what, int64_t rows, at::ScalarType type, Written& w, int64_t& k) {
   const at::Tensor& t = on(c, o, what, type);
   if (t.dim() != 2 || t.size(0) != rows || (k >= 0 && t.size(1) != k) || !t.is_contiguous())
     wrong(std::string(what) + " must be a contiguous (" + std::to_string(rows) + ", " + (k < 0 ? "k" : std::to_string(k)) +
           ") tensor (got " + text(t) + ")");
   k = t.size(1);
-  return t.mutable_data_ptr();
+  return w(t).mutable_data_ptr();
 }
 
 // token_logprobs(shards, tokens, logprobs, entropy, lse, top_logprobs,
@@ -207,8 +227,9 @@ PyObject* score(PyObject* const* a) {
   const Items shards(a[0], "shards must be a sequence of tensors");
   const Logits l = logits(shards);
   const Call c = call_of(THPVariable_Unpack(shards[0]), a[9]);
+  Written w;
   Matrices m;
-  matrices(c, shards, "shards", l.rows, l.type, false, m);
+  matrices(c, shards, "shards", l.rows, l.type, nullptr, m);
   dc_token_logprobs_t b{};
   b.shards = m.data;
   b.widths = m.width;
@@ -217,15 +238,15 @@ PyObject* score(PyObject* const* a) {
   shaped(tokens, "tokens", l.rows);
   b.tokens = tokens.const_data_ptr();
   b.tokens_64 = tokens.scalar_type() == at::kLong;
-  b.logprobs = static_cast<float*>(out_vector(c, a[2], "logprobs", l.rows, at::kFloat));
-  b.entropy = static_cast<float*>(out_vector(c, a[3], "entropy", l.rows, at::kFloat, true));
-  b.lse = static_cast<float*>(out_vector(c, a[4], "lse", l.rows, at::kFloat, true));
+  b.logprobs = static_cast<float*>(out_vector(c, a[2], "logprobs", l.rows, at::kFloat, w));
+  b.entropy = static_cast<float*>(out_vector(c, a[3], "entropy", l.rows, at::kFloat, w, true));
+  b.lse = static_cast<float*>(out_vector(c, a[4], "lse", l.rows, at::kFloat, w, true));
   int64_t top = -1;
   if (a[5] != Py_None)
-    b.top_logprobs = static_cast<float*>(alternatives(c, a[5], "top_logprobs", l.rows, at::kFloat, top));
+    b.top_logprobs = static_cast<float*>(alternatives(c, a[5], "top_logprobs", l.rows, at::kFloat, w, top));
   if (a[6] != Py_None) {
     const at::Tensor& t = indexes(c, a[6], "top_tokens");
-    b.top_tokens = alternatives(c, a[6], "top_tokens", l.rows, t.scalar_type(), top);
+    b.top_tokens = alternatives(c, a[6], "top_tokens", l.rows, t.scalar_type(), w, top);
     b.top_tokens_64 = t.scalar_type() == at::kLong;
   }
   b.top = top < 0 ? 0 : static_cast<int32_t>(top > 1 << 20 ? 1 << 20 : top);
@@ -234,7 +255,7 @@ PyObject* score(PyObject* const* a) {
   b.temperature = number(a[8]);
   b.ranks = static_cast<int32_t>(shards.size());
   b.dtype = l.code;
-  return PyLong_FromLong(g_score(&b, c.stream));
+  return w.after(g_score(&b, c.stream));
 }
 
 // token_logprobs_backward(shards, tokens, lse, grad_logprobs, grads, entropy,
@@ -245,9 +266,10 @@ PyObject* grad(PyObject* const* a) {
   const Call c = call_of(THPVariable_Unpack(shards[0]), a[9]);
   if (grads.size() != shards.size())
     wrong("need one gradient per shard (got " + std::to_string(grads.size()) + " for " + std::to_string(shards.size()) + ")");
+  Written w;
   Matrices m, g;
-  matrices(c, shards, "shards", l.rows, l.type, false, m);
-  matrices(c, grads, "grads", l.rows, l.type, true, g);
+  matrices(c, shards, "shards", l.rows, l.type, nullptr, m);
+  matrices(c, grads, "grads", l.rows, l.type, &w, g);
   for (Py_ssize_t r = 0; r < shards.size() && r < DC_MAX_RANKS; ++r)
     if (m.width[r] != g.width[r]) wrong("grads must have the shards' shapes");
   if (a[6] != Py_None && a[5] == Py_None) wrong("grad_entropy needs the forward call's entropy");
@@ -272,7 +294,7 @@ PyObject* grad(PyObject* const* a) {
   b.temperature = number(a[8]);
   b.ranks = static_cast<int32_t>(shards.size());
   b.dtype = l.code;
-  return PyLong_FromLong(g_grad(&b, c.stream));
+  return w.after(g_grad(&b, c.stream));
 }
 
 // A [n, heads, dim] tensor's strides; heads or dim < 0: any.
@@ -292,7 +314,7 @@ const at::Tensor& heads_of(const Call& c, PyObject* o, const char* what, int64_t
 struct Caches {
   int64_t pages, page_size, heads;
 };
-Caches caches(const Call& c, PyObject* ko, PyObject* vo, int64_t heads, int64_t dim, at::ScalarType type, bool written,
+Caches caches(const Call& c, PyObject* ko, PyObject* vo, int64_t heads, int64_t dim, at::ScalarType type, Written* w,
               dc_paged_cache_t& k, dc_paged_cache_t& v) {
   Caches r{0, 0, heads};
   for (int i = 0; i < 2; ++i) {
@@ -306,7 +328,7 @@ Caches caches(const Call& c, PyObject* ko, PyObject* vo, int64_t heads, int64_t 
     if (t.stride(3) != 1 && t.size(3) > 1) wrong(std::string(what) + ": the last dimension must be contiguous");
     r = Caches{t.size(0), t.size(1), t.size(2)};
     dc_paged_cache_t& x = i ? v : k;
-    x.data = written ? t.mutable_data_ptr() : const_cast<void*>(t.const_data_ptr());
+    x.data = w ? (*w)(t).mutable_data_ptr() : const_cast<void*>(t.const_data_ptr());
     x.page_stride = static_cast<uint64_t>(t.stride(0));
     x.token_stride = static_cast<uint64_t>(t.stride(1));
     x.head_stride = static_cast<uint64_t>(t.stride(2));
@@ -332,6 +354,7 @@ PyObject* append(PyObject* const* a) {
   const Call c = call_of(first, a[11]);
   if (first.dim() != 3) wrong("k has shape " + text(first) + ", expected (tokens, heads, dim)");
   const int64_t n = first.size(0), hk = first.size(1), d = first.size(2);
+  Written w;
   dc_kv_append_t b{};
   b.k = heads_of(c, a[0], "k", n, hk, d, type, b.k_token_stride, b.k_head_stride).const_data_ptr();
   b.v = heads_of(c, a[1], "v", n, hk, d, type, b.v_token_stride, b.v_head_stride).const_data_ptr();
@@ -341,7 +364,7 @@ PyObject* append(PyObject* const* a) {
     const at::Tensor& q = heads_of(c, a[7], "q", n, -1, d, type, b.q_token_stride, b.q_head_stride);
     hq = q.size(1);
     b.q = q.const_data_ptr();
-    b.q_out = heads_of(c, a[8], "q_out", n, hq, d, type, b.q_out_token_stride, b.q_out_head_stride).mutable_data_ptr();
+    b.q_out = w(heads_of(c, a[8], "q_out", n, hq, d, type, b.q_out_token_stride, b.q_out_head_stride)).mutable_data_ptr();
   } else if (a[8] != Py_None) {
     wrong("q_out needs q");
   }
@@ -355,7 +378,7 @@ PyObject* append(PyObject* const* a) {
     b.cos_sin_rows = t.size(0);
     b.rotary_dim = static_cast<int32_t>(t.size(1) > 1 << 20 ? 1 << 20 : t.size(1));
   }
-  const Caches x = caches(c, a[5], a[6], hk, d, type, true, b.k_cache, b.v_cache);
+  const Caches x = caches(c, a[5], a[6], hk, d, type, &w, b.k_cache, b.v_cache);
   const at::Tensor& table = page_table(c, a[4], -1);
   b.positions = static_cast<const int32_t*>(vector(c, a[2], "positions", n, at::kInt));
   b.seqs = static_cast<const int32_t*>(vector(c, a[3], "seqs", n, at::kInt));
@@ -374,7 +397,7 @@ PyObject* append(PyObject* const* a) {
   if (truth < 0) throw Refused{};
   b.interleaved = truth;
   b.dtype = code;
-  return PyLong_FromLong(g_append(&b, c.stream));
+  return w.after(g_append(&b, c.stream));
 }
 
 // paged_attention(q, k_cache, v_cache, page_table, lengths, out, workspace,
@@ -387,10 +410,11 @@ PyObject* attend(PyObject* const* a) {
   const Call c = call_of(first, a[10]);
   if (first.dim() != 3) wrong("q has shape " + text(first) + ", expected (sequences, heads, dim)");
   const int64_t n = first.size(0), hq = first.size(1), d = first.size(2);
+  Written w;
   dc_paged_attention_t b{};
   b.q = heads_of(c, a[0], "q", n, hq, d, type, b.q_seq_stride, b.q_head_stride).const_data_ptr();
-  b.out = heads_of(c, a[5], "out", n, hq, d, type, b.out_seq_stride, b.out_head_stride).mutable_data_ptr();
-  const Caches x = caches(c, a[1], a[2], -1, d, type, false, b.k_cache, b.v_cache);
+  b.out = w(heads_of(c, a[5], "out", n, hq, d, type, b.out_seq_stride, b.out_head_stride)).mutable_data_ptr();
+  const Caches x = caches(c, a[1], a[2], -1, d, type, nullptr, b.k_cache, b.v_cache);
   const at::Tensor& table = page_table(c, a[3], n);
   b.page_table = static_cast<const int32_t*>(table.const_data_ptr());
   b.table_width = table.size(1);
@@ -407,7 +431,7 @@ PyObject* attend(PyObject* const* a) {
       wrong("lse must be a contiguous float32 (" + std::to_string(n) + ", " + std::to_string(hq) + ") tensor (got " +
             dtype_name(t.scalar_type()) + " " + text(t) + ")");
     on(c, a[9], "lse", at::kFloat);
-    b.lse = static_cast<float*>(t.mutable_data_ptr());
+    b.lse = static_cast<float*>(w(t).mutable_data_ptr());
   }
   if (x.page_size > INT32_MAX || hq > INT32_MAX || x.heads > INT32_MAX || d > INT32_MAX) wrong("a dimension is too large");
   b.seqs = n;
@@ -419,7 +443,7 @@ PyObject* attend(PyObject* const* a) {
   b.window = small(a[8], "window");
   b.dtype = code;
   b.scale = a[7] == Py_None ? static_cast<float>(1.0 / std::sqrt(static_cast<double>(d))) : static_cast<float>(number(a[7]));
-  return PyLong_FromLong(g_attend(&b, c.stream));
+  return w.after(g_attend(&b, c.stream));
 }
 
 // Counts the arguments and turns C++ exceptions into Python's.

@@ -8,6 +8,8 @@ module ``_binding``, whose checks raise ``ValueError``), and the work runs in
 the library's CUDA kernels, one launch a call.  A row's or a sequence's
 result depends on nothing else in the call: the same bits in a batch of one
 and of a thousand, and, for the log probabilities, under every sharding.
+What a call has written counts as changed in place: where autograd had kept
+those numbers for a gradient, that gradient raises.
 """
 from __future__ import annotations
 

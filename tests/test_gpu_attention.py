@@ -555,3 +555,15 @@ def test_more_sequences_than_counters():
         one = attend(q[b:b + 1], kc, vc, table[b:b + 1], n[b:b + 1])
         assert torch.equal(out[b], one[0][0]) and torch.equal(lse[b], one[1][0]), b
     check((out[1:9], lse[1:9]), q[1:9], kc, vc, table[1:9], n[1:9])
+
+
+def test_writes_count_as_changes_in_place():
+    q, kc, vc, table, lengths = build([30, 5], 8, 2, 64, 16)
+    k, v = torch.randn(2, 2, 2, 64, device="cuda").to(torch.bfloat16)
+    seqs = torch.arange(2, device="cuda", dtype=torch.int32)
+    before = [t._version for t in (kc, vc, q, k, v, lengths)]
+    dc.kv_append(k, v, lengths - 1, seqs, table, kc, vc, q=q, q_out=q)
+    assert [t._version - n for t, n in zip((kc, vc, q, k, v, lengths), before)] == [1, 1, 1, 0, 0, 0]
+    out, lse, ws = torch.empty_like(q), torch.empty(2, 8, device="cuda"), dc.attention_workspace(2, 8, 2, 64, 32)
+    dc.paged_attention(q, kc, vc, table, lengths, out, ws, lse=lse)
+    assert (out._version, lse._version, kc._version - before[0]) == (1, 1, 1)

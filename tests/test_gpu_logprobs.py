@@ -566,3 +566,31 @@ def test_gradient_of_rows_of_one_mask(dtype, value, temperature):
     lse_off = 2.0 ** -24 * 65536 / temperature + 2 * REL * (1 + math.log(vocab))
     over = (grads[0].cpu().double() - want).abs() - (UNIT[dtype] * want.abs() + lse_off * (1 + lse_off) * size + 2.0 ** -25)
     assert float(over.max()) <= 0
+
+
+def test_writes_count_as_changes_in_place():
+    """Autograd notices that numbers which it had kept are overwritten; a refused call changes nothing."""
+    x, tokens = logits(4, 700, torch.float32)
+    out = score([x], tokens)
+    one = torch.ones(4, device="cuda")
+    x.requires_grad_()
+    p = torch.softmax(x, 1)  # (keeps its result for its gradient)
+    dc.token_logprobs_backward([p], tokens, out["lse"], one, [p])
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        p.sum().backward()
+    y = x.detach().clone()
+    outs = {"logprobs": torch.empty(4, device="cuda"), "entropy": torch.empty(4, device="cuda"),
+            "lse": torch.empty(4, device="cuda"), "top_logprobs": torch.empty(4, 2, device="cuda"),
+            "top_tokens": torch.empty(4, 2, device="cuda", dtype=torch.int64)}
+    dc.token_logprobs([y], tokens, **outs)
+    assert [t._version for t in outs.values()] == [1] * 5 and y._version == 0
+    grads = [torch.empty_like(y[:, :300]), torch.empty_like(y[:, 300:])]
+    with pytest.raises(dc.DCError):
+        dc.token_logprobs_backward([y[:, :300], y[:, 300:]], tokens, outs["lse"], None, grads)
+    assert [t._version for t in grads] == [0, 0]
+    dc.token_logprobs_backward([y[:, :300], y[:, 300:]], tokens, outs["lse"], one, grads)
+    assert [t._version for t in grads] == [1, 1] and y._version == 0
+    with torch.inference_mode():
+        z = y.clone()
+        dc.token_logprobs_backward([z], tokens, outs["lse"], one, [z])
+    assert torch.equal(z, torch.cat(grads, 1))
