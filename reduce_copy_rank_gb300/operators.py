@@ -179,7 +179,8 @@ _function = None
 def logprobs_and_entropy(shards: Sequence, tokens, vocab: int | None = None, temperature: float = 1.0):
     """``(logprobs, entropy)`` of :func:`token_logprobs` as new tensors that
     autograd differentiates with respect to every shard (through
-    :func:`token_logprobs_backward`), once: a second derivative raises."""
+    :func:`token_logprobs_backward`, which computes every shard's gradient,
+    wanted or not), once: a second derivative raises."""
     global _function
     import torch
 
@@ -191,6 +192,7 @@ def logprobs_and_entropy(shards: Sequence, tokens, vocab: int | None = None, tem
                 logprobs, entropy, lse = (torch.empty(rows, dtype=torch.float32, device=shards[0].device)
                                           for _ in range(3))
                 token_logprobs(shards, tokens, logprobs, entropy=entropy, lse=lse, vocab=vocab, temperature=temperature)
+                ctx.set_materialize_grads(False)  # an output that is not used has no upstream gradient to read
                 ctx.save_for_backward(tokens, lse, entropy, *shards)
                 ctx.vocab, ctx.temperature = vocab, temperature
                 return logprobs, entropy
@@ -198,6 +200,8 @@ def logprobs_and_entropy(shards: Sequence, tokens, vocab: int | None = None, tem
             @staticmethod
             def backward(ctx, g, h):
                 tokens, lse, entropy, *shards = ctx.saved_tensors
+                if g is None and h is None:
+                    return (None,) * (3 + len(shards))
                 grads = [torch.empty_like(x, memory_format=torch.contiguous_format) for x in shards]
                 # upstream gradients may be broadcast (a sum's is one number for all rows)
                 g, h = (None if u is None else u.to(torch.float32).contiguous() for u in (g, h))

@@ -594,3 +594,36 @@ def test_writes_count_as_changes_in_place():
         z = y.clone()
         dc.token_logprobs_backward([z], tokens, outs["lse"], one, [z])
     assert torch.equal(z, torch.cat(grads, 1))
+
+
+def test_autograd_of_one_output_and_of_some_shards(monkeypatch):
+    """An unused output's upstream gradient is not made up, and a frozen shard stays without one."""
+    from reduce_copy_rank_gb300 import operators
+
+    seen = []
+    backward = operators.token_logprobs_backward
+
+    def spy(*a, **kw):
+        seen.append((a[3] is not None, kw["grad_entropy"] is not None))
+        return backward(*a, **kw)
+
+    monkeypatch.setattr(operators, "token_logprobs_backward", spy)
+    x, tokens = logits(7, 5001, torch.float32)
+    up = torch.linspace(-1, 1, 7, device="cuda")
+    whole = x.double().requires_grad_()
+    logp = torch.log_softmax(whole, 1)
+    for pick, want in (((True, False), (logp.gather(1, tokens[:, None])[:, 0] * up).sum()),
+                       ((False, True), (-(logp.exp() * logp).sum(1) * up).sum())):
+        exact_g, = torch.autograd.grad(want, whole, retain_graph=True)
+        for frozen in (None, 0, 1):
+            shards = [x[:, :2000].clone(), x[:, 2000:].clone()]
+            for i, s in enumerate(shards):
+                s.requires_grad_(i != frozen)
+            both = dc.logprobs_and_entropy(shards, tokens)
+            (both[pick.index(True)] * up).sum().backward()
+            assert seen.pop() == pick and not seen
+            for i, (s, w) in enumerate(zip(shards, (exact_g[:, :2000], exact_g[:, 2000:]))):
+                if i == frozen:
+                    assert s.grad is None
+                else:
+                    assert float((s.grad.double() - w).abs().max()) <= 1e-4
