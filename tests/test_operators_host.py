@@ -307,3 +307,25 @@ def both(page, slot, head, v, **kw):
     (dict(both(4096, 128, 64, 2048), k_cache=at(8) + 4096, v_cache=at(8)), CUDA)])
 def test_caches_share_nothing(kw, want):
     assert append(**kw) == want, dc.last_error()
+
+
+def test_python_layouts_have_the_headers_offsets(tmp_path):
+    """Every field of the argument blocks lies where the C structures have it."""
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if cc is None:
+        pytest.skip("no C compiler")
+    caches = {f"{x}{a}": f"{x}_cache.{b}" for x in "kv" for a, b in (
+        ("_cache", "data"), ("_page_stride", "page_stride"), ("_slot_stride", "token_stride"), ("_cache_head_stride", "head_stride"))}
+    blocks = {"dc_token_logprobs_t": operators._SCORE, "dc_token_logprobs_backward_t": operators._GRAD,
+              "dc_kv_append_t": operators._APPEND, "dc_paged_attention_t": operators._ATTEND}
+    lines = [f'printf("%zu\\n", offsetof({t}, {caches.get(n, n)}));' for t, b in blocks.items() for n in b.names]
+    src = tmp_path / "offsets.c"
+    src.write_text('#include <stddef.h>\n#include <stdio.h>\n#include "dc.h"\nint main(void){' + "\n".join(lines) + "return 0;}\n")
+    exe = tmp_path / "offsets"
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    subprocess.run([cc, "-std=c11", "-I", os.path.join(root, "include"), str(src), "-o", str(exe)], check=True)
+    want = [int(x) for x in subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.split()]
+    # a field whose lowest byte alone is not 0 (little-endian: the number's first byte)
+    least = {"temperature": 2.0 ** -1074, "scale": 2.0 ** -149}
+    got = [b.of({n: least.get(n, 1)}).index(1) for b in blocks.values() for n in b.names]
+    assert got == want
