@@ -426,7 +426,8 @@ typedef struct {
  * 16 (half as much for DC_F32, and for pairs that are interleaved).
  * A negative position marks padding: nothing is written for it.  A token
  * whose sequence, position or page does not exist leaves the cache alone and
- * its q_out row is NaN.  Two tokens for one slot: either may remain.
+ * its q_out row is NaN.  Two tokens for one slot: each 16 bytes of its heads
+ * hold either's numbers, not all of them the same one's.
  * The caches may be interleaved in one tensor (pages of keys beside pages of
  * values); what a call writes must not fold onto itself (a broadcast q_out or
  * cache), share bytes with what else it writes (a cache that is the other, a
