@@ -22,9 +22,10 @@
 //
 // Where a unit's pieces fit one cluster and the GPU has room, its CTAs join them
 // through shared memory; else through the workspace, the last to arrive doing
-// it.  Measured on GB300 (copy rate 6.78 TB/s): 128 ragged sequences up to 8192
-// tokens, 32/8 heads of 128: 349 us, 6.3 TB/s; one of 131072, 64/8 heads: 94 us,
-// 5.7 TB/s; one of 1024, 32/8 heads: 5.6 us.  What is left is latency: a piece of
+// it.  Measured on GB300 (copy rate 6.78 TB/s; launches replayed from a graph), heads
+// of 128: 128 ragged sequences up to 8192 tokens, 32/8 heads: 348 us, 6.3 TB/s; one
+// of 131072, 64/8 heads: 94 us, 5.7 TB/s; 32 ragged up to 8000, 64/4 heads: 64 us, 3.2
+// TB/s; one of 1024, 32/8 heads: 5.6 us.  What is left is latency: a piece of
 // 256 tokens spends 0.35 us on its length, 1.3 on its page, query and first
 // copies, 2.4 on its tiles (16 cp.async hold a warp for 450 of a tile's 1200
 // cycles) and 0.6 on its end, and 8 warps an SM are all that registers allow.

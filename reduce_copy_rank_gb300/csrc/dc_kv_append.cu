@@ -12,9 +12,10 @@
 // it when there are few): a thread owns one position in the head across query,
 // key and value heads, so its cos and sin stay in registers; all its loads are
 // issued before the token's place is looked up, which costs two dependent
-// reads.  Measured on GB300 (copy rate 6.78 TB/s): 8191 tokens, 32 + 8 + 8 heads
-// of 128: 37 us, 5.6 TB/s; 32 + 32 + 32 heads of 80: 43 us, 5.8 TB/s; 64 tokens
-// of 32 + 8 + 8 heads of 128: 2.2 us.
+// reads.  Measured on GB300 (copy rate 6.78 TB/s; launches replayed from a graph),
+// 16 bits / binary32: 8191 tokens, 32 + 8 + 8 heads of 128: 37 / 69 us, 5.6 / 5.9
+// TB/s; 32 + 32 + 32 heads of 80, neighbouring pairs: 43 / 82 us, 5.8 / 6.2 TB/s; 64
+// tokens of 32 + 8 + 8 heads of 128: 2.2 / 2.2 us.
 #include "dc_llm.h"
 #include "dc_numeric.cuh"
 
@@ -24,8 +25,8 @@ namespace {
 enum : uint32_t { kSiteTokenInfo = 1, kSiteTable = 2, kSiteIn = 3, kSiteOut = 4, kSiteCache = 5, kSiteAngle = 6 };
 
 // CTAs of 128 threads (binary32, whose heads of up to 1024 elements are 256
-// vectors: 256).  Measured on 16-bit heads, heads in flight a thread x CTAs
-// per SM x threads: 8191 tokens, 32 + 8 + 8 heads of 128, rotated by halves:
+// vectors: 256, 4 an SM, not swept).  Measured on 16-bit heads, heads in flight a
+// thread x CTAs per SM x threads: 8191 tokens, 32 + 8 + 8 heads of 128, by halves:
 // 2 x 10 x 128 36.7 us, 4 x 8 x 128 39.9, 2 x 5 x 256 42.7, 4 x 4 x 256 48.8;
 // 32 + 32 + 32 heads of 80, neighbouring pairs: 45.7, 43.3, 49.3, 53.6.
 template <int DT, bool INTERLEAVED>

@@ -181,6 +181,8 @@ __host__ __device__ inline uint32_t attend_level(uint32_t small, uint32_t units,
 // Measured, us, 16 / 8: one sequence of 1024, 16/1 heads of 128: 7.5 / 6.2 (16
 // CTAs of 8); of 131072: 32.9 / 28.9 (256 CTAs); of 16384, 128/8 heads: 29.3 /
 // 31.0 (512); 32 up to 8000, 64/4 heads: 64 / 69.
+// (The GPU's SMs by a constant: a workspace's size follows from them, and is asked
+// for without a device.)
 constexpr uint32_t kAttendSms = 152;
 __host__ __device__ constexpr int attend_ctas_per_sm(int dim, int hb) {
   return dim <= 64 && hb == 8 ? 3 : dim <= 128 ? 2 : 1;

@@ -23,10 +23,13 @@
 // cluster's barrier and (with alternatives) the search for them.  Between, a
 // row's CTA spends as long on that chain as on its logits.
 //
-// Measured on GB300 (copy rate 6.78 TB/s), scores: 8192 x 128000 bf16 299 us,
-// 7.0 TB/s; 1021 x 50021 f32 on 3 ranks with 5 alternatives 51 us, 4.1 TB/s; 128
-// x 131072 bf16 on 8 ranks with 20 16 us; 4 x 32768 with 1 6.1 us.  Gradient:
-// 8192 x 127900 bf16 on 8 ranks 610 us, 6.9 TB/s; 509 x 50021 f16 17 us, 5.9 TB/s.
+// Measured on GB300 (copy rate 6.78 TB/s; launches replayed from a graph), scores:
+// 8192 x 128000 bf16 303 us, 6.9 TB/s; 1021 x 50021 f32 on 3 ranks with 5
+// alternatives 51 us, 4.0 TB/s; 128 x 131072 bf16 on 8 ranks with 20 16.7 us; 4 x
+// 32768 with 1 6.3 us.  Gradient: 8192 x 127900 bf16 on 8 ranks 611 us, 6.9 TB/s;
+// 509 x 50021 f16 17 us, 5.9 TB/s; narrow shards (2849 x 14007 bf16 on 8 ranks: 219
+// vectors a row of a shard, for CTAs of up to 1024) 60 us, 2.7 TB/s, issue slots 87 %
+// busy with what a CTA does once.
 #include <cfloat>
 
 #include "dc_llm.h"
