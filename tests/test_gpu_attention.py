@@ -567,3 +567,23 @@ def test_writes_count_as_changes_in_place():
     out, lse, ws = torch.empty_like(q), torch.empty(2, 8, device="cuda"), dc.attention_workspace(2, 8, 2, 64, 32)
     dc.paged_attention(q, kc, vc, table, lengths, out, ws, lse=lse)
     assert (out._version, lse._version, kc._version - before[0]) == (1, 1, 1)
+
+
+@pytest.mark.parametrize("hq,hk,d", [(4, 1, 64), (8, 2, 128), (6, 2, 192), (9, 1, 64), (12, 1, 96), (20, 1, 128), (64, 4, 128), (11, 1, 192),
+                                     (48, 3, 256)])
+def test_bits_of_binary16_do_not_depend_on_the_grid(hq, hk, d):
+    """Low parts of the weights in rows of their own, in the same product or in a second one: the same sums."""
+    q, kc, vc, table, lengths = build([1500, 33, 5, 260, 9000], hq, hk, d, 16, "f16")
+    kc[2, 3, 0, :5] = 40.0
+    vc[1, 2, 0, :7] = float("inf")
+    kc[5, 1, 0] = 0.0
+    q *= 4  # weights over the whole range
+    want = attend(q, kc, vc, table, lengths)
+    many = attend(q.repeat(60, 1, 1), kc, vc, table.repeat(60, 1), lengths.repeat(60))
+    for i in (0, 59):
+        for k in (0, 1):
+            bits = torch.int16 if k == 0 else torch.int32
+            assert torch.equal(many[k][5 * i:5 * i + 5].view(bits), want[k].view(bits))
+    for b in range(5):
+        one = attend(q[b:b + 1], kc, vc, table[b:b + 1], lengths[b:b + 1])
+        assert torch.equal(one[0][0].view(torch.int16), want[0][b].view(torch.int16)) and torch.equal(one[1][0], want[1][b]), b
