@@ -197,8 +197,7 @@ def prepare(case, seed):
         if own:  # the library's workspace, kept by the caller from call to call
             import reduce_copy_rank_gb300 as dc
 
-            s["workspace"] = dc.linear_logprobs_workspace(n, h, sum(_widths(case)), backward=case["op"] == "head_grad",
-                                                          dtype=dt)
+            s["workspace"] = dc.linear_logprobs_workspace(n, h, sum(_widths(case)), backward=case["op"] == "head_grad")
         return s
     hq, hk, d = case["q_heads"], case["kv_heads"], case["dim"]
     if case["op"] in ("append", "norm"):
