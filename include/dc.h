@@ -399,6 +399,106 @@ typedef struct {
 } dc_token_logprobs_backward_t;
 dc_status_t dc_token_logprobs_backward(const dc_token_logprobs_backward_t *args, dc_stream_t stream);
 
+/*
+ * dc_linear_logprobs -- dc_token_logprobs from the rows that a linear head
+ * takes, without keeping the logits: with x = hidden W^T, W the concatenated
+ * shards (one row per column of the vocabulary), and z = x / temperature,
+ *
+ *   lse = log(sum_i exp(z_i));  logprobs = z_y - lse;
+ *   entropy = lse - sum_i p_i z_i,  p = exp(z - lse).
+ *
+ * hidden [rows, hidden_size]; weights[r] [widths[r], hidden_size]; DC_BF16 or
+ *   DC_F16, rows 16-byte aligned, hidden_size a multiple of 8 up to 2^20.
+ *   The products are exact and their sums binary32, as are all statistics.
+ * ranks, widths, vocab, temperature, tokens: as for dc_token_logprobs (rows of
+ *   the weights past `vocab` are not read).  Infinities and NaN are those of
+ *   the formulas.  Up to 2^24 rows.
+ * logprobs [rows]; entropy, lse [rows] or NULL.
+ * A row's bits do not depend on the other rows, and not on the shards where
+ * every shard but the last is a multiple of 256 wide.
+ *
+ * workspace: device memory of at least dc_linear_logprobs_workspace_bytes(rows,
+ * hidden_size, columns, 0) bytes (columns: all shards' rows), 256-byte aligned,
+ * whose contents do not matter; calls that overlap on the GPU need one each.
+ * Two kernels.  The waits inside are bounded ("wait_limit_ns"): one that ran
+ * out leaves wrong results, which dc_check_device reports.
+ */
+typedef struct {
+    const void *hidden;
+    const void *const *weights;
+    const uint64_t *widths;
+    const uint64_t *weight_row_strides;
+    const void *tokens;
+    float *logprobs;
+    float *entropy;
+    float *lse;
+    void *workspace;
+    uint64_t workspace_bytes;
+    uint64_t hidden_row_stride;
+    int64_t rows;
+    int64_t hidden_size;
+    int64_t vocab;
+    double temperature;
+    int32_t ranks;
+    int32_t dtype;
+    int32_t tokens_64;
+    int32_t reserved;       /* 0 */
+} dc_linear_logprobs_t;
+dc_status_t dc_linear_logprobs(const dc_linear_logprobs_t *args, dc_stream_t stream);
+/* 0 if the arguments are not supported. */
+size_t dc_linear_logprobs_workspace_bytes(int64_t rows, int64_t hidden_size, int64_t columns, int backward);
+
+/*
+ * dc_linear_logprobs_backward -- the gradient of sum(g * logprobs + h *
+ * entropy) with respect to hidden and the weights, from the lse and entropy
+ * that dc_linear_logprobs returned.  With d the logits' gradient (that of
+ * dc_token_logprobs_backward, where g, h and `entropy` are described),
+ *
+ *   grad_hidden = d W;   grad_weights[r] = (d^T hidden) of the shard's columns.
+ *
+ * The logits are computed again, 16384 columns of a shard at a time; d is
+ * rounded to 16 bits before its products (for DC_F16 times one power of two for
+ * all rows, so that the largest d that these g and h allow fits: rows whose g
+ * and h are 2^20 times smaller than the largest lose precision), the sums are
+ * binary32 and rounded once.
+ *
+ * grad_hidden [rows, hidden_size] or NULL; grad_weights: host array of
+ *   `ranks` pointers, shaped as the weights, or NULL; either is needed.  They
+ *   replace what was there.  Rows of the weights' gradient past `vocab` are 0,
+ *   as are all of them if there are no rows.  No output may meet an input.
+ * A row of grad_hidden does not depend on the other rows (for DC_F16: beyond
+ * the power of two); the order of every sum is fixed.
+ * workspace: dc_linear_logprobs_workspace_bytes(rows, hidden_size, columns, 1)
+ * bytes, as above.  Several kernels.
+ */
+typedef struct {
+    const void *hidden;
+    const void *const *weights;
+    const uint64_t *widths;
+    const uint64_t *weight_row_strides;
+    const void *tokens;
+    const float *lse;
+    const float *entropy;
+    const float *grad_logprobs;
+    const float *grad_entropy;
+    void *grad_hidden;
+    void *const *grad_weights;
+    const uint64_t *grad_weight_row_strides;
+    void *workspace;
+    uint64_t workspace_bytes;
+    uint64_t hidden_row_stride;
+    uint64_t grad_hidden_row_stride;
+    int64_t rows;
+    int64_t hidden_size;
+    int64_t vocab;
+    double temperature;
+    int32_t ranks;
+    int32_t dtype;
+    int32_t tokens_64;
+    int32_t reserved;       /* 0 */
+} dc_linear_logprobs_backward_t;
+dc_status_t dc_linear_logprobs_backward(const dc_linear_logprobs_backward_t *args, dc_stream_t stream);
+
 /* One of the two tensors of a paged cache: element d of head h of token o of
  * page g is data[g*page_stride + o*token_stride + h*head_stride + d], every
  * head 16-byte aligned. */

@@ -28,7 +28,8 @@ __all__ = [
     "reduce_scatter", "reduce", "all_reduce_many", "reduce_scatter_many", "inject_delay", "check_device",
     "fused_all_gather", "fused_workspace", "fused_reset",
     "token_logprobs", "token_logprobs_backward", "logprobs_and_entropy", "kv_append", "paged_attention",
-    "attention_workspace",
+    "attention_workspace", "linear_logprobs", "linear_logprobs_backward", "linear_logprobs_and_entropy",
+    "linear_logprobs_workspace",
     "set_option",
     "get_option",
     "launch_count", "last_grid", "last_error", "options", "lib", "LIB_PATH", "STATUS", "DTYPES", "ORDERS",
@@ -618,6 +619,7 @@ def last_error() -> str:
 
 # ------------------------------------------ operators of language models ---
 from .operators import (  # noqa: E402  (they use the binding above)
-    attention_workspace, dc_attention_workspace_bytes, dc_kv_append, dc_paged_attention, dc_token_logprobs,
-    dc_token_logprobs_backward, kv_append, logprobs_and_entropy, paged_attention, token_logprobs,
-    token_logprobs_backward)
+    attention_workspace, dc_attention_workspace_bytes, dc_kv_append, dc_linear_logprobs, dc_linear_logprobs_backward,
+    dc_linear_logprobs_workspace_bytes, dc_paged_attention, dc_token_logprobs, dc_token_logprobs_backward, kv_append,
+    linear_logprobs, linear_logprobs_and_entropy, linear_logprobs_backward, linear_logprobs_workspace, logprobs_and_entropy,
+    paged_attention, token_logprobs, token_logprobs_backward)

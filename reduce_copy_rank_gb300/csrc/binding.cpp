@@ -25,6 +25,8 @@ decltype(&dc_token_logprobs) g_score = nullptr;
 decltype(&dc_token_logprobs_backward) g_grad = nullptr;
 decltype(&dc_kv_append) g_append = nullptr;
 decltype(&dc_paged_attention) g_attend = nullptr;
+decltype(&dc_linear_logprobs) g_linear = nullptr;
+decltype(&dc_linear_logprobs_backward) g_linear_grad = nullptr;
 
 // A refusal: the Python exception is set.
 struct Refused {};
@@ -165,6 +167,14 @@ struct Written {
     return PyLong_FromLong(status);
   }
 };
+
+// A call's workspace, whatever its type.
+const at::Tensor& workspace_of(const Call& c, PyObject* o) {
+  const at::Tensor& t = tensor(o, "workspace");
+  on(c, o, "workspace", t.scalar_type());
+  if (!t.is_contiguous()) wrong("workspace must be contiguous");
+  return t;
+}
 
 // Ranks' [rows, width] matrices.
 struct Matrices {
@@ -420,9 +430,7 @@ PyObject* attend(PyObject* const* a) {
   b.table_width = table.size(1);
   b.table_stride = table.stride(0);
   b.lengths = static_cast<const int32_t*>(vector(c, a[4], "lengths", n, at::kInt));
-  const at::Tensor& ws = tensor(a[6], "workspace");
-  on(c, a[6], "workspace", ws.scalar_type());
-  if (!ws.is_contiguous()) wrong("workspace must be contiguous");
+  const at::Tensor& ws = workspace_of(c, a[6]);
   b.workspace = ws.mutable_data_ptr();
   b.workspace_bytes = static_cast<uint64_t>(ws.nbytes());
   if (a[9] != Py_None) {
@@ -446,6 +454,123 @@ PyObject* attend(PyObject* const* a) {
   return w.after(g_attend(&b, c.stream));
 }
 
+// A head: hidden [rows, size] and its shards [columns, size].
+struct HeadArgs {
+  int64_t rows, size, columns = 0;
+  at::ScalarType type;
+  int code;
+  Call call;
+  const void* weights[DC_MAX_RANKS];
+  uint64_t width[DC_MAX_RANKS], stride[DC_MAX_RANKS];
+};
+const at::Tensor& head_matrix(const Call& c, PyObject* o, const char* what, int64_t i, int64_t rows, int64_t size,
+                              at::ScalarType type) {
+  const at::Tensor& t = on(c, o, what, type, i);
+  if (t.dim() != 2 || (rows >= 0 && t.size(0) != rows) || t.size(1) != size)
+    wrong(indexed(what, i) + " has shape " + text(t) + ", expected (" + (rows < 0 ? "columns" : std::to_string(rows)) + ", " +
+          std::to_string(size) + ")");
+  if (t.stride(1) != 1 && t.size(1) > 1) wrong(indexed(what, i) + ": the hidden dimension must be contiguous");
+  return t;
+}
+void head(PyObject* hidden, const Items& weights, PyObject* stream, HeadArgs& h) {
+  const at::Tensor& x = tensor(hidden, "hidden");
+  if (x.dim() != 2) wrong("hidden has shape " + text(x) + ", expected (rows, hidden size)");
+  h.type = x.scalar_type();
+  h.code = code_of(h.type);
+  if (h.code != DC_BF16 && h.code != DC_F16)
+    wrong(std::string("hidden rows are bfloat16 or float16 (got ") + dtype_name(h.type) + ")");
+  h.call = call_of(x, stream);
+  h.rows = x.size(0);
+  h.size = x.size(1);
+  head_matrix(h.call, hidden, "hidden", -1, h.rows, h.size, h.type);
+  if (weights.size() == 0) wrong("need at least one shard of the weights");
+  for (Py_ssize_t r = 0; r < weights.size(); ++r) {
+    const at::Tensor& w = head_matrix(h.call, weights[r], "weights", r, -1, h.size, h.type);
+    h.columns += w.size(0);
+    if (r >= DC_MAX_RANKS) continue;  // (the library refuses the count)
+    h.weights[r] = w.const_data_ptr();
+    h.width[r] = static_cast<uint64_t>(w.size(0));
+    h.stride[r] = static_cast<uint64_t>(w.stride(0));
+  }
+}
+template <class Block>
+void fill_head(Block& b, const HeadArgs& h, PyObject* hidden, const Items& weights, PyObject* tokens_of, PyObject* workspace,
+               PyObject* vocab, PyObject* temperature) {
+  const at::Tensor& x = THPVariable_Unpack(hidden);
+  b.hidden = x.const_data_ptr();
+  b.hidden_row_stride = static_cast<uint64_t>(x.stride(0));
+  b.weights = h.weights;
+  b.widths = h.width;
+  b.weight_row_strides = h.stride;
+  const at::Tensor& tokens = indexes(h.call, tokens_of, "tokens");
+  shaped(tokens, "tokens", h.rows);
+  b.tokens = tokens.const_data_ptr();
+  b.tokens_64 = tokens.scalar_type() == at::kLong;
+  const at::Tensor& ws = workspace_of(h.call, workspace);
+  b.workspace = ws.mutable_data_ptr();
+  b.workspace_bytes = static_cast<uint64_t>(ws.nbytes());
+  b.rows = h.rows;
+  b.hidden_size = h.size;
+  b.vocab = vocab == Py_None ? h.columns : integer(vocab);
+  b.temperature = number(temperature);
+  b.ranks = static_cast<int32_t>(weights.size());
+  b.dtype = h.code;
+}
+
+// linear_logprobs(hidden, weights, tokens, logprobs, workspace, entropy, lse,
+//                 vocab, temperature, stream) -> status
+PyObject* linear(PyObject* const* a) {
+  const Items weights(a[1], "weights must be a sequence of tensors");
+  HeadArgs h;
+  head(a[0], weights, a[9], h);
+  Written w;
+  dc_linear_logprobs_t b{};
+  fill_head(b, h, a[0], weights, a[2], a[4], a[7], a[8]);
+  b.logprobs = static_cast<float*>(out_vector(h.call, a[3], "logprobs", h.rows, at::kFloat, w));
+  b.entropy = static_cast<float*>(out_vector(h.call, a[5], "entropy", h.rows, at::kFloat, w, true));
+  b.lse = static_cast<float*>(out_vector(h.call, a[6], "lse", h.rows, at::kFloat, w, true));
+  return w.after(g_linear(&b, h.call.stream));
+}
+
+// linear_logprobs_backward(hidden, weights, tokens, lse, grad_logprobs,
+//   grad_hidden, grad_weights, workspace, entropy, grad_entropy, vocab,
+//   temperature, stream) -> status
+PyObject* linear_grad(PyObject* const* a) {
+  const Items weights(a[1], "weights must be a sequence of tensors");
+  HeadArgs h;
+  head(a[0], weights, a[12], h);
+  Written w, w_hidden;
+  dc_linear_logprobs_backward_t b{};
+  fill_head(b, h, a[0], weights, a[2], a[7], a[10], a[11]);
+  if (a[9] != Py_None && a[8] == Py_None) wrong("grad_entropy needs the forward call's entropy");
+  b.lse = static_cast<const float*>(vector(h.call, a[3], "lse", h.rows, at::kFloat));
+  b.grad_logprobs = static_cast<const float*>(vector(h.call, a[4], "grad_logprobs", h.rows, at::kFloat, true));
+  b.entropy = static_cast<const float*>(vector(h.call, a[8], "entropy", h.rows, at::kFloat, true));
+  b.grad_entropy = static_cast<const float*>(vector(h.call, a[9], "grad_entropy", h.rows, at::kFloat, true));
+  if (a[5] != Py_None) {
+    const at::Tensor& g = head_matrix(h.call, a[5], "grad_hidden", -1, h.rows, h.size, h.type);
+    b.grad_hidden = w_hidden(g).mutable_data_ptr();
+    b.grad_hidden_row_stride = static_cast<uint64_t>(g.stride(0));
+  }
+  void* out[DC_MAX_RANKS];
+  uint64_t stride[DC_MAX_RANKS];
+  if (a[6] != Py_None) {
+    const Items grads(a[6], "grad_weights must be a sequence of tensors");
+    if (grads.size() != weights.size())
+      wrong("need one gradient per shard (got " + std::to_string(grads.size()) + " for " + std::to_string(weights.size()) + ")");
+    for (Py_ssize_t r = 0; r < grads.size() && r < DC_MAX_RANKS; ++r) {
+      const at::Tensor& g = head_matrix(h.call, grads[r], "grad_weights", r, static_cast<int64_t>(h.width[r]), h.size, h.type);
+      out[r] = w(g).mutable_data_ptr();
+      stride[r] = static_cast<uint64_t>(g.stride(0));
+    }
+    b.grad_weights = out;
+    b.grad_weight_row_strides = stride;
+  }
+  const dc_status_t status = g_linear_grad(&b, h.call.stream);
+  Py_XDECREF(w_hidden.after(status));
+  return w.after(status);
+}
+
 // Counts the arguments and turns C++ exceptions into Python's.
 template <PyObject* (*F)(PyObject* const*), int N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -467,22 +592,24 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   }
 }
 
-// bind(dc_token_logprobs, dc_token_logprobs_backward, dc_kv_append,
-//      dc_paged_attention): the loaded library's entry points, as addresses.
+// bind(...): the loaded library's entry points as addresses, in the order of
+// the pointers below.
 PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  void* at[4];
-  if (n != 4) {
-    PyErr_SetString(PyExc_TypeError, "expected 4 addresses");
+  void** const to[] = {
+      reinterpret_cast<void**>(&g_score), reinterpret_cast<void**>(&g_grad), reinterpret_cast<void**>(&g_append),
+      reinterpret_cast<void**>(&g_attend), reinterpret_cast<void**>(&g_linear), reinterpret_cast<void**>(&g_linear_grad),
+  };
+  constexpr Py_ssize_t count = sizeof to / sizeof to[0];
+  if (n != count) {
+    PyErr_Format(PyExc_TypeError, "expected %zd addresses", count);
     return nullptr;
   }
-  for (int i = 0; i < 4; ++i) {
+  void* at[count];
+  for (Py_ssize_t i = 0; i < count; ++i) {
     at[i] = PyLong_AsVoidPtr(args[i]);
     if (PyErr_Occurred()) return nullptr;
   }
-  g_score = reinterpret_cast<decltype(g_score)>(at[0]);
-  g_grad = reinterpret_cast<decltype(g_grad)>(at[1]);
-  g_append = reinterpret_cast<decltype(g_append)>(at[2]);
-  g_attend = reinterpret_cast<decltype(g_attend)>(at[3]);
+  for (Py_ssize_t i = 0; i < count; ++i) *to[i] = at[i];
   Py_RETURN_NONE;
 }
 
@@ -497,6 +624,8 @@ PyMethodDef kMethods[] = {
     {"token_logprobs_backward", as_function(&entry<grad, 10>), METH_FASTCALL, nullptr},
     {"kv_append", as_function(&entry<append, 12>), METH_FASTCALL, nullptr},
     {"paged_attention", as_function(&entry<attend, 11>), METH_FASTCALL, nullptr},
+    {"linear_logprobs", as_function(&entry<linear, 10>), METH_FASTCALL, nullptr},
+    {"linear_logprobs_backward", as_function(&entry<linear_grad, 13>), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};

@@ -157,6 +157,8 @@ bool pdl_option() { return g_opt.pdl.load() != 0; }
 
 bool launch_failure_injected() { return g_opt.test_fail_launch.load() != 0; }
 
+uint64_t wait_limit_option() { return static_cast<uint64_t>(std::max(g_opt.wait_limit_ns.load(), 1000LL)); }
+
 dc_status_t fail(dc_status_t s, const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);
@@ -1289,17 +1291,19 @@ dc_status_t dc_fused_reset(void* workspace, int P, dc_stream_t stream) {
 
 dc_status_t dc_check_device(void) {
   read_env_once();
-  uint32_t bits = 0, fused[4] = {0, 0, 0, 0};
+  uint32_t bits = 0, tensor = 0, fused[4] = {0, 0, 0, 0};
   cudaError_t e = take_bulk_faults(&bits);
   if (e == cudaSuccess) e = take_fused_faults(fused);
+  if (e == cudaSuccess) e = take_linear_faults(&tensor);
   // bounds-check records of the checked build (empty in the normal build)
   static cudaError_t (*const kReaders[kBoundsReaders])(BoundsFault*) = {
       take_bounds_gather, take_bounds_bulk, take_bounds_fused,
       take_bounds_reduce_bf16, take_bounds_reduce_f16, take_bounds_reduce_f32,
-      take_bounds_logprobs, take_bounds_append, take_bounds_attention};
+      take_bounds_logprobs, take_bounds_append, take_bounds_attention, take_bounds_linear};
   static const char* const kFiles[kBoundsReaders] = {"dc_gather.cu", "dc_bulk.cu", "dc_fused.cu",
                                                      "dc_reduce_bf16.cu", "dc_reduce_f16.cu", "dc_reduce_f32.cu",
-                                                     "dc_logprobs.cu", "dc_kv_append.cu", "dc_attention.cu"};
+                                                     "dc_logprobs.cu", "dc_kv_append.cu", "dc_attention.cu",
+                                                     "dc_linear.cu"};
   BoundsFault first{};
   int first_file = -1;
   unsigned long long outside = 0;
@@ -1334,6 +1338,10 @@ dc_status_t dc_check_device(void) {
     return fail(DC_ERR_TIMEOUT,
                 "a bulk-copy all-gather gave up waiting for its loads after wait_limit_ns; "
                 "its output is incomplete");
+  if (tensor & kFaultTensorWait)
+    return fail(DC_ERR_TIMEOUT,
+                "a matrix product of the language-model operators gave up waiting for its operands after "
+                "wait_limit_ns; its output is incomplete");
   return ok();
 }
 

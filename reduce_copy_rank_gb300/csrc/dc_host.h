@@ -22,5 +22,6 @@ dc_status_t sm_count(int dev, int* sms);
 void read_options();               // the environment's initial values, once
 bool pdl_option();                 // "pdl"
 bool launch_failure_injected();    // "test_fail_launch"
+uint64_t wait_limit_option();      // "wait_limit_ns"
 
 }  // namespace dc

@@ -151,7 +151,7 @@ struct BulkParams {
 };
 enum : uint32_t { kBulkTestShortTx = 1u };
 // Device fault bits (sticky until read by dc_check_device).
-enum : uint32_t { kFaultBulkWait = 1u, kFaultFusedWait = 2u };
+enum : uint32_t { kFaultBulkWait = 1u, kFaultFusedWait = 2u, kFaultTensorWait = 4u };
 
 // The staged all-gather protocol (dc_fused.cu): P ranks, each a group of G
 // CTAs of one cooperative launch; rank r's bytes are cut into G chunks of
@@ -291,7 +291,7 @@ cudaError_t take_bulk_faults(uint32_t* bits);
 // returns an empty one in the normal build.  bounds_file names the file of
 // reader i (i < kBoundsReaders).
 struct BoundsFault;
-constexpr int kBoundsReaders = 9;
+constexpr int kBoundsReaders = 10;
 cudaError_t take_bounds_gather(BoundsFault* f);
 cudaError_t take_bounds_bulk(BoundsFault* f);
 cudaError_t take_bounds_fused(BoundsFault* f);
@@ -301,6 +301,9 @@ cudaError_t take_bounds_reduce_f32(BoundsFault* f);
 cudaError_t take_bounds_logprobs(BoundsFault* f);
 cudaError_t take_bounds_append(BoundsFault* f);
 cudaError_t take_bounds_attention(BoundsFault* f);
+cudaError_t take_bounds_linear(BoundsFault* f);
+// Reads and clears the fault bits of the tensor-core products (dc_linear.cu).
+cudaError_t take_linear_faults(uint32_t* bits);
 bool bounds_checked_build();
 
 // One-thread delay of `ns` nanoseconds of the global timer (rank-skew

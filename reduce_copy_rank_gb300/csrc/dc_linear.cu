@@ -1,0 +1,533 @@
+// Log probabilities of tokens from hidden rows and a head's weights, without
+// keeping the logits, and the gradient of that.
+//
+// Mathematics.  x = h W^T over a vocabulary, z = x / temperature; lse =
+// log sum exp z, log p_y = z_y - lse, entropy = lse - sum p z.  With upstream
+// gradients g and e of a row's log probability and entropy the logits' gradient
+// is d_j = (g ([j = y] - p_j) - e p_j (log p_j + entropy)) / temperature, and
+// dh = d W, dW = d^T h.
+//
+// The products run on the tensor cores (tcgen05.mma, operands by TMA, binary32
+// accumulators in tensor memory).  A CTA takes tiles of 128 x 256 in turn; while
+// one is computed four warps reduce the one before from tensor memory:
+//  * forward: a row's part of the tile as its maximum (rounded up to a whole
+//    number r in units of log2), sum 2^(z-r) and sum 2^(z-r) (z-r), written as
+//    16 bytes; a second kernel adds a row's parts up in one fixed order, which
+//    depends on the shards' widths alone.
+//  * backward, for up to 16384 columns of a shard at a time: the logits again,
+//    from which d is written in 16 bits; d W added to a binary32 sum; d^T h.
+// Neither the number of rows nor the grid changes a bit of a row's results.
+//
+// Rounding: d is rounded to 16 bits before its products (2^-9 of each for
+// DC_BF16, 2^-12 for DC_F16), as an activation's gradient is; the sums are
+// binary32.  For DC_F16 d is multiplied by one power of two for all rows, so
+// that the largest possible is between 2^14 and 2^15: what is 2^-29 of that is
+// still a normal number.
+//
+// Bound: the tensor cores for training batches, the weights' bytes for few rows.
+#include <atomic>
+
+#include "dc_llm.h"
+#include "dc_numeric.cuh"
+#include "dc_tc.cuh"
+
+namespace dc {
+namespace {
+
+using namespace tc;
+
+enum : uint32_t { kSitePart = 1, kSiteRow = 2, kSiteD = 3, kSiteAcc = 4, kSiteOut = 5 };
+
+__device__ unsigned int g_linear_fault_bits;
+
+constexpr int kStages = 4;
+constexpr int kTileBytes = 64 * 128;                  // 64 rows of 64 elements: what one TMA copy loads
+constexpr int kABytes = kLinearM / 64 * kTileBytes, kBBytes = kLinearN / 64 * kTileBytes;
+constexpr int kStageBytes = kABytes + kBBytes;
+constexpr int kSmem = kStages * kStageBytes + 1024;   // (the ring starts at a multiple of 1024)
+constexpr int kThreads = 192;                         // loads, products, four warps of results
+constexpr uint32_t kColumns = 2 * kLinearN;           // of tensor memory: two tiles' accumulators
+
+template <int NB>
+struct LinearArgs {
+  CUtensorMap a, b[NB];
+  LinearParams p;
+  LinearShard shard[NB];
+};
+
+__device__ __forceinline__ int64_t token_of(uint64_t tokens, int tokens64, uint64_t row) {
+  return tokens64 ? reinterpret_cast<const int64_t*>(tokens)[row] : reinterpret_cast<const int32_t*>(tokens)[row];
+}
+__device__ __forceinline__ float ld_row(uint64_t base, uint64_t row, uint64_t rows) {
+  const float* a = reinterpret_cast<const float*>(base) + row;
+  return in_bounds(a, 4, base, base + rows * 4, kSiteRow) ? *a : 0.0f;
+}
+
+// ------------------------------------------------------------- the results ---
+// Each runs in a thread that has row `row` of C (of rows0 = kLinearM tile rows)
+// and the tile's accumulators at `at` in tensor memory.
+
+// Forward: one row's part of a tile.  limit: the tile's columns that exist.
+__device__ __forceinline__ void stats(const LinearParams& p, uint32_t at, uint64_t row, bool own, uint32_t tile,
+                                      uint32_t column0, uint32_t limit) {
+  const float c = p.inv_t * kLog2E;
+  float top = neg_inf();
+#pragma unroll 1
+  for (uint32_t j0 = 0; j0 < kLinearN; j0 += 32) {
+    if (j0 >= limit) break;
+    float v[32];
+    tmem_ld32(at + j0, v);
+    tmem_wait_ld();
+    if (j0 + 32 <= limit) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) top = fmaxf(top, v[j] * c);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) top = fmaxf(top, j0 + j < limit ? v[j] * c : neg_inf());
+    }
+  }
+  const float ref = ceilf(top), base = ref == neg_inf() ? 0.0f : ref;
+  float s[4] = {}, t[4] = {};
+  const int64_t token = own ? token_of(p.tokens, p.tokens64, row) : -1;
+  const int64_t mine = token - static_cast<int64_t>(column0);  // the token's column in this tile, if it has it
+#pragma unroll 1
+  for (uint32_t j0 = 0; j0 < kLinearN; j0 += 32) {
+    if (j0 >= limit) break;
+    float v[32];
+    tmem_ld32(at + j0, v);
+    tmem_wait_ld();
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      const float z = v[j] * c;
+      if (mine == static_cast<int64_t>(j0 + j) && j0 + j < limit) {
+        float* a = reinterpret_cast<float*>(p.target) + row;
+        if (in_bounds(a, 4, p.target, p.target + p.rows * 4, kSitePart)) *a = z;
+      }
+      const float x = j0 + j < limit ? z - base : neg_inf();
+      const float e = ex2(x);
+      s[j & 3] += e;
+      t[j & 3] = __fmaf_rn(e, x < -1e4f ? -1e4f : x, t[j & 3]);
+    }
+  }
+  if (!own) return;
+  float4* a = reinterpret_cast<float4*>(p.part) + static_cast<uint64_t>(tile) * p.rows + row;
+  if (in_bounds(a, 16, p.part, p.part + static_cast<uint64_t>(p.n_tiles) * p.rows * 16, kSitePart))
+    *a = make_float4(ref, (s[0] + s[1]) + (s[2] + s[3]), (t[0] + t[1]) + (t[2] + t[3]), 0.0f);
+}
+
+// Stores 32 results of a row as 16-bit elements; `left` of them exist (a
+// multiple of 8, or more than 32).
+template <int DT>
+__device__ __forceinline__ void st_row32(uint64_t at, const float (&v)[32], int left, uint64_t lo, uint64_t hi, uint32_t site) {
+#pragma unroll
+  for (int j = 0; j < 32; j += 8) {
+    uint4* a = reinterpret_cast<uint4*>(at + j * 2);
+    const float x[8] = {v[j], v[j + 1], v[j + 2], v[j + 3], v[j + 4], v[j + 5], v[j + 6], v[j + 7]};
+    if (j < left && in_bounds(a, 16, lo, hi, site)) st16(a, repack<DT>(x));
+  }
+}
+
+// Backward: the gradient of one row's logits in a tile.
+template <int DT>
+__device__ __forceinline__ void dlogits(const LinearParams& p, uint32_t at, uint64_t row, bool own, uint32_t n0) {
+  const float c = p.inv_t * kLog2E;
+  float lse2 = 0.0f, a0 = 0.0f, a1 = 0.0f, hot = 0.0f;
+  int64_t token = -1;
+  if (own) {
+    token = token_of(p.tokens, p.tokens64, row);
+    const float unit = p.scale ? *reinterpret_cast<const float*>(p.scale) : 1.0f;
+    const float g = p.grad_logprobs && token >= 0 ? ld_row(p.grad_logprobs, row, p.rows) : 0.0f;
+    const float e = p.grad_entropy ? ld_row(p.grad_entropy, row, p.rows) : 0.0f;
+    const float h = p.grad_entropy ? ld_row(p.entropy, row, p.rows) : 0.0f;
+    lse2 = ld_row(p.lse, row, p.rows) * kLog2E;
+    const float f = p.inv_t * unit;
+    hot = g * f;
+    a0 = -(g + e * h) * f;   // d = p (a0 + a1 log2 p), and hot at the token
+    a1 = -(e * kLn2) * f;
+  }
+  const int64_t mine = token - static_cast<int64_t>(p.first) - n0;
+  const uint32_t ld = static_cast<uint32_t>(p.d_stride / 2);
+  const uint32_t exist = p.vocab > p.first + n0 ? p.vocab - p.first - n0 : 0;  // columns before the padding
+  const uint64_t lo = p.d + row * p.d_stride;
+#pragma unroll 1
+  for (uint32_t j0 = 0; j0 < kLinearN && n0 + j0 < ld; j0 += 32) {
+    float v[32];
+    tmem_ld32(at + j0, v);
+    tmem_wait_ld();
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      const float x = __fmaf_rn(v[j], c, -lse2);
+      v[j] = ex2(x) * __fmaf_rn(a1, x < -1e4f ? -1e4f : x, a0);
+      if (mine == static_cast<int64_t>(j0 + j)) v[j] += hot;
+      if (j0 + j >= exist) v[j] = 0.0f;
+    }
+    if (own) st_row32<DT>(lo + (n0 + j0) * 2, v, static_cast<int>(ld - n0 - j0), lo, lo + p.d_stride, kSiteD);
+  }
+}
+
+// A row of a product that is stored: plus what `acc` holds of it, to `acc` or
+// (when complete) to the output.
+template <int MODE, int DT>
+__device__ __forceinline__ void result(const LinearParams& p, uint32_t at, uint64_t row, bool own, uint32_t n0) {
+  const float unit = p.scale ? reinterpret_cast<const float*>(p.scale)[1] : 1.0f;
+  const uint64_t out = p.out + row * p.out_stride;
+  float* acc = reinterpret_cast<float*>(p.acc) + row * p.n;
+  const uint64_t acc_hi = p.acc + p.rows * p.n * 4;
+#pragma unroll 1
+  for (uint32_t j0 = 0; j0 < kLinearN && n0 + j0 < p.n; j0 += 32) {
+    float v[32];
+    tmem_ld32(at + j0, v);
+    tmem_wait_ld();
+    if (!own) continue;
+    const int left = static_cast<int>(p.n - n0 - j0);
+    if constexpr (MODE == kLinearDHidden) {
+      float4* a = reinterpret_cast<float4*>(acc + n0 + j0);
+      if (p.add) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (4 * j < left && in_bounds(a + j, 16, p.acc, acc_hi, kSiteAcc)) {
+            const float4 x = a[j];
+            v[4 * j] += x.x;
+            v[4 * j + 1] += x.y;
+            v[4 * j + 2] += x.z;
+            v[4 * j + 3] += x.w;
+          }
+      }
+      if (!p.last) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (4 * j < left && in_bounds(a + j, 16, p.acc, acc_hi, kSiteAcc))
+            a[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        continue;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] *= unit;
+    st_row32<DT>(out + (n0 + j0) * 2, v, left, out, out + p.n * 2ull, kSiteOut);
+  }
+}
+
+template <int MODE, int DT, int NB>
+__global__ __launch_bounds__(kThreads, 1) void dc_linear_kernel(const __grid_constant__ LinearArgs<NB> args) {
+  // which operands' rows run across the inner dimension
+  constexpr bool kAcrossA = MODE == kLinearDWeights, kAcrossB = MODE == kLinearDHidden || MODE == kLinearDWeights;
+  const LinearParams& p = args.p;
+  extern __shared__ uint8_t smem[];
+  __shared__ __align__(8) uint64_t bars[2 * kStages + 5];
+  __shared__ uint32_t tmem_at;
+  __shared__ volatile uint32_t stop;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t ring = (smem_addr(smem) + 1023u) & ~1023u;
+  const uint32_t full = smem_addr(bars), empty = full + 8 * kStages;
+  const uint32_t done = empty + 8 * kStages, drained = done + 16, over = drained + 16;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      tma::mbar_init(full + 8 * i, 1);
+      tma::mbar_init(empty + 8 * i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tma::mbar_init(done + 8 * i, 1);
+      tma::mbar_init(drained + 8 * i, 128);
+    }
+    tma::mbar_init(over, 1);
+    tma::mbar_init_fence();
+    stop = 0;
+    prefetch_map(&args.a);
+    prefetch_map(&args.b[0]);
+  }
+  if (warp == 1) tmem_alloc(smem_addr(&tmem_at), kColumns);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = tmem_at;
+  pdl_enter();
+  tma::fence_proxy_async_global();  // (the operands may be an earlier kernel's stores)
+
+  const Waits waits{&stop, p.wait_ns};
+  const uint32_t tiles = p.m_tiles * p.n_tiles;
+  // tile t: its rows, its columns and the tensor that they belong to
+  struct Place {
+    uint32_t m0, n0;
+    int r;
+  };
+  auto place = [&](uint32_t t) {
+    Place x{t % p.m_tiles * kLinearM, t / p.m_tiles, 0};
+    if constexpr (MODE == kLinearStats) {
+      if constexpr (NB > 1)
+        while (x.r + 1 < p.shards && args.shard[x.r + 1].tile0 <= x.n0) ++x.r;
+      x.n0 -= args.shard[x.r].tile0;
+    }
+    x.n0 *= kLinearN;
+    return x;
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t i = 0;  // stages filled so far
+      for (uint32_t t = blockIdx.x; t < tiles && !stop; t += gridDim.x) {
+        const Place x = place(t);
+        for (uint32_t kb = 0; kb < p.k_blocks; ++kb, ++i) {
+          const uint32_t st = i % kStages, bar = full + 8 * st, to = ring + st * kStageBytes;
+          if (i >= kStages && !wait(waits, empty + 8 * st, (i / kStages - 1) & 1)) break;
+          tma::mbar_arrive_expect_tx(bar, kStageBytes);
+          const int32_t k0 = static_cast<int32_t>(kb * kLinearK);
+#pragma unroll
+          for (int j = 0; j < kLinearM / 64; ++j) {
+            const int32_t mj = static_cast<int32_t>(x.m0) + 64 * j;
+            load_tile(to + j * kTileBytes, &args.a, bar, kAcrossA ? mj : k0, kAcrossA ? k0 : mj);
+          }
+#pragma unroll
+          for (int j = 0; j < kLinearN / 64; ++j) {
+            const int32_t nj = static_cast<int32_t>(x.n0) + 64 * j, off = static_cast<int32_t>(p.b_row0);
+            load_tile(to + kABytes + j * kTileBytes, &args.b[NB > 1 ? x.r : 0], bar, kAcrossB ? nj : k0,
+                      kAcrossB ? k0 + off : nj + off);
+          }
+        }
+      }
+      if (stop) {  // no copy may land after this CTA's shared memory is gone
+        const uint32_t from = i > kStages ? i - kStages : 0;
+        for (uint32_t k = from; k < i; ++k)
+          tma::mbar_wait_bounded(full + 8 * (k % kStages), (k / kStages) & 1, p.wait_ns);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = instruction<DT>(kLinearM, kLinearN, (kAcrossA ? kMajorA : 0u) | (kAcrossB ? kMajorB : 0u));
+      uint32_t i = 0, n = 0;
+      for (uint32_t t = blockIdx.x; t < tiles && !stop; t += gridDim.x, ++n) {
+        const uint32_t buf = n & 1, acc = tmem + buf * kLinearN;
+        if (n >= 2 && !wait(waits, drained + 8 * buf, (n / 2 - 1) & 1)) break;
+        fence_after();
+        for (uint32_t kb = 0; kb < p.k_blocks; ++kb, ++i) {
+          const uint32_t st = i % kStages, a = ring + st * kStageBytes, b = a + kABytes;
+          if (!wait(waits, full + 8 * st, (i / kStages) & 1)) break;
+          fence_after();
+#pragma unroll
+          for (int k = 0; k < kLinearK / 16; ++k)
+            mma(acc, kAcrossA ? desc_mn(a + k * 2048, kTileBytes) : desc_k(a + k * 32),
+                kAcrossB ? desc_mn(b + k * 2048, kTileBytes) : desc_k(b + k * 32), idesc, (kb | k) != 0);
+          commit(empty + 8 * st);
+        }
+        commit(done + 8 * buf);
+      }
+      if (stop) {
+        commit(over);
+        tma::mbar_wait_bounded(over, 0, p.wait_ns);
+      }
+    }
+  } else {
+    const uint32_t quarter = static_cast<uint32_t>(warp & 3) * 32;  // the lanes of tensor memory that this warp reads
+    uint32_t n = 0;
+    for (uint32_t t = blockIdx.x; t < tiles; t += gridDim.x, ++n) {
+      const Place x = place(t);
+      const uint32_t buf = n & 1, at = tmem + buf * kLinearN + (quarter << 16);
+      const bool there = wait(waits, done + 8 * buf, (n / 2) & 1);
+      if (!__all_sync(~0u, there)) break;
+      fence_after();
+      const uint64_t row = x.m0 + quarter + lane;
+      const bool own = row < p.m;
+      if (x.m0 + quarter < p.m) {
+        if constexpr (MODE == kLinearStats) {
+          const LinearShard& s = args.shard[NB > 1 ? x.r : 0];
+          const uint32_t column0 = s.first + x.n0;
+          stats(p, at, row, own, t / p.m_tiles, column0, s.end - column0 < kLinearN ? s.end - column0 : kLinearN);
+        } else if constexpr (MODE == kLinearDLogits) {
+          dlogits<DT>(p, at, row, own, x.n0);
+        } else {
+          result<MODE, DT>(p, at, row, own, x.n0);
+        }
+      }
+      fence_before();
+      mbar_arrive(drained + 8 * buf);
+    }
+  }
+  __syncwarp();
+  __syncthreads();
+  if (threadIdx.x == 0 && stop) atomicOr(&g_linear_fault_bits, kFaultTensorWait);
+  if (warp == 1) {
+    fence_after();
+    tmem_free(tmem, kColumns);
+  }
+}
+
+// One warp adds a row's parts up: lane l takes parts l, l + 32, ..., then the
+// lanes join in pairs.
+constexpr int kFinishThreads = 128;
+__global__ __launch_bounds__(kFinishThreads) void dc_linear_finish_kernel(const __grid_constant__ LinearFinishParams p) {
+  pdl_enter();
+  const uint64_t row = static_cast<uint64_t>(blockIdx.x) * (kFinishThreads / 32) + (threadIdx.x >> 5);
+  const uint32_t lane = threadIdx.x & 31;
+  if (row >= p.rows) return;
+  float ref = neg_inf(), s = 0.0f, t = 0.0f;
+  auto add = [&](float r, float s1, float t1) {
+    // t = sum 2^(z-ref) (z-ref): moving ref by k adds k times the sum
+    const float m = fmaxf(ref, r);
+    const float k0 = ref == neg_inf() ? 0.0f : ref - m, k1 = r == neg_inf() ? 0.0f : r - m;
+    const float f0 = ex2(k0), f1 = ex2(k1);
+    t = __fmaf_rn(f0, __fmaf_rn(s, k0, t), f1 * __fmaf_rn(s1, k1, t1));
+    s = __fmaf_rn(f0, s, f1 * s1);
+    ref = m;
+  };
+  for (uint32_t i = lane; i < p.tiles; i += 32) {
+    const float4* a = reinterpret_cast<const float4*>(p.part) + static_cast<uint64_t>(i) * p.rows + row;
+    const float4 x = in_bounds(a, 16, p.part, p.part + static_cast<uint64_t>(p.tiles) * p.rows * 16, kSitePart)
+                         ? *a : make_float4(neg_inf(), 0.0f, 0.0f, 0.0f);
+    add(x.x, x.y, x.z);
+  }
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const float r1 = __shfl_xor_sync(~0u, ref, d), s1 = __shfl_xor_sync(~0u, s, d), t1 = __shfl_xor_sync(~0u, t, d);
+    add(r1, s1, t1);
+  }
+  if (lane) return;
+  const float log_s = log2f(s), nan = __int_as_float(0x7FC00000);
+  const int64_t token = token_of(p.tokens, p.tokens64, row);
+  auto put = [&](uint64_t base, float v) {
+    float* a = reinterpret_cast<float*>(base) + row;
+    if (in_bounds(a, 4, base, base + p.rows * 4, kSiteOut)) *a = v;
+  };
+  float lp = 0.0f;
+  if (token >= static_cast<int64_t>(p.vocab)) lp = nan;
+  else if (token >= 0) lp = ((ld_row(p.target, row, p.rows) - ref) - log_s) * kLn2;
+  put(p.logprobs, lp);
+  if (p.entropy) put(p.entropy, (log_s - t / s) * kLn2);
+  if (p.lse) put(p.lse, (ref + log_s) * kLn2);
+}
+
+// The power of two for DC_F16: no |d_j| is above (|g| + 16 |e|) / temperature,
+// as p |log p| <= 1/e and p entropy <= log DC_MAX_VOCAB < 16.
+__global__ __launch_bounds__(1024) void dc_linear_scale_kernel(uint64_t grad_logprobs, uint64_t grad_entropy, uint64_t tokens,
+                                                               int tokens64, uint64_t rows, float inv_t, uint64_t scale) {
+  pdl_enter();
+  __shared__ float most[32];
+  float m = 0.0f;
+  for (uint64_t i = threadIdx.x; i < rows; i += blockDim.x) {
+    float b = 0.0f;
+    if (grad_logprobs && token_of(tokens, tokens64, i) >= 0) b += fabsf(ld_row(grad_logprobs, i, rows));
+    if (grad_entropy) b += 16.0f * fabsf(ld_row(grad_entropy, i, rows));
+    m = fmaxf(m, b * inv_t);
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
+  if ((threadIdx.x & 31) == 0) most[threadIdx.x >> 5] = m;
+  __syncthreads();
+  if (threadIdx.x) return;
+  for (int i = 1; i < 32; ++i) m = fmaxf(m, most[i]);
+  int k = 0;
+  if (m > 0.0f && m < __int_as_float(0x7F800000)) k = max(-100, min(100, 14 - ilogbf(m)));
+  float* to = reinterpret_cast<float*>(scale);
+  to[0] = __int_as_float((127 + k) << 23);
+  to[1] = __int_as_float((127 - k) << 23);
+}
+
+template <int MODE, int DT, int NB>
+cudaError_t launch_one(const LinearParams& p, const LinearOperand& a, const LinearOperand* b, const LinearShard* shards,
+                       int sms, bool pdl, cudaStream_t s, int* grid) {
+  static std::atomic<uint64_t> allowed{0};  // devices whose limit is set
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(allowed.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(dc_linear_kernel<MODE, DT, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    allowed.fetch_or(bit, std::memory_order_relaxed);
+  }
+  LinearArgs<NB> args{};
+  args.p = p;
+  e = make_map(&args.a, DT, a.base, a.rows, a.columns, a.stride, 64);
+  const int nb = MODE == kLinearStats ? p.shards : 1;
+  for (int r = 0; r < nb && e == cudaSuccess; ++r) {
+    e = make_map(&args.b[r], DT, b[r].base, b[r].rows, b[r].columns, b[r].stride, 64);
+    if (MODE == kLinearStats) args.shard[r] = shards[r];
+  }
+  if (e != cudaSuccess) return e;
+  const uint64_t tiles = static_cast<uint64_t>(p.m_tiles) * p.n_tiles;
+  *grid = static_cast<int>(tiles < static_cast<uint64_t>(sms) ? tiles : static_cast<uint64_t>(sms));
+  return launch_ex(dc_linear_kernel<MODE, DT, NB>, *grid, kThreads, pdl, s, args, kSmem);
+}
+
+template <int DT>
+cudaError_t launch_mode(int mode, const LinearParams& p, const LinearOperand& a, const LinearOperand* b,
+                        const LinearShard* shards, int sms, bool pdl, cudaStream_t s, int* grid) {
+  switch (mode) {
+    case kLinearStats:
+      return p.shards == 1 ? launch_one<kLinearStats, DT, 1>(p, a, b, shards, sms, pdl, s, grid)
+                           : launch_one<kLinearStats, DT, kMaxRanks>(p, a, b, shards, sms, pdl, s, grid);
+    case kLinearDLogits: return launch_one<kLinearDLogits, DT, 1>(p, a, b, shards, sms, pdl, s, grid);
+    case kLinearDHidden: return launch_one<kLinearDHidden, DT, 1>(p, a, b, shards, sms, pdl, s, grid);
+    default: return launch_one<kLinearDWeights, DT, 1>(p, a, b, shards, sms, pdl, s, grid);
+  }
+}
+
+}  // namespace
+
+namespace tc {
+
+cudaError_t make_map(CUtensorMap* map, int dtype, uint64_t base, uint64_t rows, uint64_t columns, uint64_t row_stride,
+                     uint32_t tile_rows) {
+  using Encode = decltype(&cuTensorMapEncodeTiled);
+  static std::atomic<Encode> encode{nullptr};  // the driver's function, looked up once
+  Encode f = encode.load(std::memory_order_acquire);
+  if (!f) {
+    void* at = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &at, 12000, cudaEnableDefault, &found);
+    if (e != cudaSuccess) return e;
+    if (!at || found != cudaDriverEntryPointSuccess) return cudaErrorNotSupported;
+    f = reinterpret_cast<Encode>(at);
+    encode.store(f, std::memory_order_release);
+  }
+  const cuuint64_t size[2] = {columns, rows}, stride[1] = {row_stride};
+  const cuuint32_t box[2] = {64, tile_rows}, step[2] = {1, 1};
+  const CUresult r = f(map, dtype == kF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                       reinterpret_cast<void*>(base), size, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+}  // namespace tc
+
+cudaError_t launch_linear(int mode, int dtype, const LinearParams& p, const LinearOperand& a, const LinearOperand* b,
+                          const LinearShard* shards, int sms, bool pdl, cudaStream_t s, int* grid) {
+  return dtype == kF16 ? launch_mode<kF16>(mode, p, a, b, shards, sms, pdl, s, grid)
+                       : launch_mode<kBF16>(mode, p, a, b, shards, sms, pdl, s, grid);
+}
+
+cudaError_t launch_linear_finish(const LinearFinishParams& p, bool pdl, cudaStream_t s, int* grid) {
+  constexpr uint64_t per = kFinishThreads / 32;
+  *grid = static_cast<int>((p.rows + per - 1) / per);
+  return launch_ex(dc_linear_finish_kernel, *grid, kFinishThreads, pdl, s, p);
+}
+
+cudaError_t launch_linear_scale(uint64_t grad_logprobs, uint64_t grad_entropy, uint64_t tokens, bool tokens64, uint64_t rows,
+                                float inv_t, uint64_t scale, bool pdl, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(1);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = pdl ? attr : nullptr;
+  cfg.numAttrs = pdl ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, dc_linear_scale_kernel, grad_logprobs, grad_entropy, tokens, tokens64 ? 1 : 0, rows, inv_t, scale);
+}
+
+DC_BOUNDS_READER(take_bounds_linear)
+
+cudaError_t take_linear_faults(uint32_t* bits) {
+  *bits = 0;
+  cudaError_t e = cudaDeviceSynchronize();
+  if (e != cudaSuccess) return e;
+  unsigned int v = 0;
+  e = cudaMemcpyFromSymbol(&v, g_linear_fault_bits, sizeof v);
+  if (e == cudaSuccess && v) {
+    const unsigned int zero = 0;
+    e = cudaMemcpyToSymbol(g_linear_fault_bits, &zero, sizeof zero);
+  }
+  *bits = v;
+  return e;
+}
+
+}  // namespace dc

@@ -193,4 +193,57 @@ __host__ __device__ inline int attend_head_block(int group, uint64_t kv_units, u
 }
 cudaError_t launch_attend(const AttendParams& p, int dtype, int dim, bool pdl, cudaStream_t s, int* grid);
 
+// ------------------------------------------- log probabilities of a linear head
+// Matrix products on the tensor cores: tiles of kLinearM x kLinearN, kLinearK
+// of the inner dimension a stage.
+constexpr int kLinearM = 128, kLinearN = 256, kLinearK = 64;
+// The gradient takes this many columns of a shard at a time, whatever the call's
+// rows: how the products over the vocabulary are cut decides their bits.
+constexpr uint32_t kLinearChunk = 16384;
+
+enum : int { kLinearStats = 0, kLinearDLogits = 1, kLinearDHidden = 2, kLinearDWeights = 3 };
+
+// Columns [first, end) of the vocabulary, in tiles from tile0 on (end: without padding).
+struct LinearShard {
+  uint32_t tile0, first, end, pad;
+};
+
+// One product C [m, n] = A B^T over k, and what becomes of it.
+struct LinearParams {
+  uint32_t m, n;               // extents of C (kLinearStats: n is not used)
+  uint32_t m_tiles, n_tiles, k_blocks;
+  uint32_t b_row0;             // first row of B's tensor (kLinearDLogits: of n; kLinearDHidden: of k)
+  uint32_t vocab, first;       // kLinearDLogits: the vocabulary index of column 0
+  float inv_t;
+  int32_t tokens64;
+  int32_t shards;              // kLinearStats
+  int32_t add, last;           // kLinearDHidden: what `acc` holds is added; the sum is complete
+  uint64_t rows;
+  uint64_t tokens;
+  uint64_t part, target;       // kLinearStats: f32 [tiles][rows][4], f32 [rows]
+  uint64_t lse, entropy, grad_logprobs, grad_entropy;  // f32 [rows]; the last two or 0
+  uint64_t scale;              // f32 [2] or 0: the gradient's power of two and its inverse
+  uint64_t d, d_stride;        // kLinearDLogits: [rows] of d_stride bytes
+  uint64_t acc;                // kLinearDHidden: f32 [rows][n] or 0
+  uint64_t out, out_stride;    // kLinearDHidden, kLinearDWeights: bytes
+  uint64_t wait_ns;
+};
+
+struct LinearFinishParams {
+  uint64_t part, target, tokens, logprobs, entropy, lse;  // the last three f32 [rows], two of them or 0
+  uint64_t rows;
+  uint32_t tiles, vocab;
+  int32_t tokens64, pad;
+};
+
+// The operands as tensors of 16-bit rows.
+struct LinearOperand {
+  uint64_t base, rows, columns, stride;  // stride in bytes
+};
+cudaError_t launch_linear(int mode, int dtype, const LinearParams& p, const LinearOperand& a, const LinearOperand* b,
+                          const LinearShard* shards, int sms, bool pdl, cudaStream_t s, int* grid);
+cudaError_t launch_linear_finish(const LinearFinishParams& p, bool pdl, cudaStream_t s, int* grid);
+cudaError_t launch_linear_scale(uint64_t grad_logprobs, uint64_t grad_entropy, uint64_t tokens, bool tokens64, uint64_t rows,
+                                float inv_t, uint64_t scale, bool pdl, cudaStream_t s);
+
 }  // namespace dc

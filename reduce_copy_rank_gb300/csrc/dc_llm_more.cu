@@ -1,0 +1,321 @@
+// dc_llm_more.cu -- the C ABI of the operators around a rollout and a training
+// step on it: log probabilities from hidden rows.  Argument checks, the cut of
+// the work, launches.
+#include "dc_checks.h"
+
+namespace {
+
+using namespace dc;
+
+constexpr int64_t kMaxLinearRows = 1 << 24;
+constexpr int64_t kMaxHidden = 1 << 20;
+
+uint64_t round_up(uint64_t n, uint64_t to) { return (n + to - 1) / to * to; }
+
+// A [rows, columns] matrix of 16-bit elements whose rows TMA can copy: 16-byte
+// aligned, `columns` a multiple of 8.
+dc_status_t check_matrix(const void* p, uint64_t rows, uint64_t columns, uint64_t stride, const char* name, int r, Strided* out) {
+  char what[48];
+  if (r < 0) std::snprintf(what, sizeof what, "%s", name);
+  else std::snprintf(what, sizeof what, "%s[%d]", name, r);
+  *out = Strided{0, 1, 0, 0};
+  if (rows == 0) return DC_OK;
+  if (!p) return fail(DC_ERR_INVALID, "%s is NULL", what);
+  if (rows < 2) stride = columns;
+  if (stride < columns)
+    return fail(DC_ERR_INVALID, "%s: rows of %llu elements every %llu overlap", what,
+                static_cast<unsigned long long>(columns), static_cast<unsigned long long>(stride));
+  if (stride > (1ull << 38)) return fail(DC_ERR_INVALID, "%s is too large", what);
+  if (addr(p) % 16 || stride % 8) return fail(DC_ERR_ALIGN, "%s: rows must be 16-byte aligned", what);
+  const uint64_t lo = addr(p), hi = lo + ((rows - 1) * stride + columns) * 2;
+  if (hi < lo) return fail(DC_ERR_INVALID, "%s wraps around", what);
+  *out = Strided{lo, stride * 2, columns * 2, hi};
+  return DC_OK;
+}
+
+// What both directions take: hidden rows, the head's shards, tokens.
+struct Head {
+  Strided hidden;
+  Shards weights;
+  Spans in;
+};
+
+dc_status_t check_head(const void* hidden, uint64_t hidden_stride, const void* const* weights, const uint64_t* widths,
+                       const uint64_t* strides, const void* tokens, int64_t rows, int64_t size, int64_t vocab,
+                       double temperature, int ranks, int dtype, int tokens_64, Head* h) {
+  if (ranks < 1 || ranks > kMaxRanks) return fail(DC_ERR_INVALID, "ranks = %d is outside 1..%d", ranks, kMaxRanks);
+  if (rows < 0 || rows > kMaxLinearRows)
+    return fail(DC_ERR_INVALID, "rows = %lld is outside 0..%lld", static_cast<long long>(rows), static_cast<long long>(kMaxLinearRows));
+  if (size < 8 || size > kMaxHidden || size % 8)
+    return fail(DC_ERR_INVALID, "a hidden size of %lld is not a multiple of 8 up to %lld", static_cast<long long>(size),
+                static_cast<long long>(kMaxHidden));
+  if (vocab < 1 || vocab > kMaxVocab)
+    return fail(DC_ERR_INVALID, "vocab = %lld is outside 1..%d", static_cast<long long>(vocab), kMaxVocab);
+  if (dtype != kBF16 && dtype != kF16) return fail(DC_ERR_INVALID, "dtype %d is not DC_BF16 or DC_F16", dtype);
+  DC_TRY(check_temperature(temperature));
+  if (!weights || !widths || !strides) return fail(DC_ERR_INVALID, "weights, widths and strides must not be NULL");
+  uint64_t sum = 0;
+  for (int r = 0; r < ranks; ++r) {
+    if (widths[r] > static_cast<uint64_t>(kMaxVocab))
+      return fail(DC_ERR_INVALID, "weights[%d] has %llu rows, more than %d", r, static_cast<unsigned long long>(widths[r]), kMaxVocab);
+    sum += widths[r];
+    Strided m;
+    DC_TRY(check_matrix(weights[r], widths[r], static_cast<uint64_t>(size), strides[r], "weights", r, &m));
+    h->weights.add(m);
+  }
+  if (sum < static_cast<uint64_t>(vocab) || sum > static_cast<uint64_t>(kMaxVocab))
+    return fail(DC_ERR_INVALID, "the shards hold %llu columns; vocab = %lld, and at most %d", static_cast<unsigned long long>(sum),
+                static_cast<long long>(vocab), kMaxVocab);
+  DC_TRY(check_matrix(hidden, static_cast<uint64_t>(rows), static_cast<uint64_t>(size), hidden_stride, "hidden", -1, &h->hidden));
+  if (rows) DC_TRY(take(tokens, "tokens", static_cast<uint64_t>(rows) * (tokens_64 ? 8 : 4), tokens_64 ? 8 : 4, h->in));
+  return DC_OK;
+}
+
+// The forward's workspace: every tile's parts, then the tokens' logits.
+uint64_t stats_bytes(uint64_t rows, uint64_t tiles) { return rows * (tiles * 16 + 4); }
+// The gradient's: its power of two, then d of one chunk of the vocabulary, then
+// the sum of d W.
+uint64_t chunk_stride(uint64_t columns) { return round_up(std::min<uint64_t>(columns, kLinearChunk), 64) * 2; }
+uint64_t d_bytes(uint64_t rows, uint64_t stride) { return round_up(rows * stride, 256); }
+
+dc_status_t check_workspace(void* p, uint64_t have, uint64_t need, Spans& out) {
+  if (have < need)
+    return fail(DC_ERR_INVALID, "the workspace holds %llu bytes, this call needs %llu (dc_linear_logprobs_workspace_bytes)",
+                static_cast<unsigned long long>(have), static_cast<unsigned long long>(need));
+  return take(p, "workspace", have, 256, out);
+}
+
+// Written spans meet neither one another, what is read, nor the matrices.
+dc_status_t check_head_outputs(const Spans& out, const Head& h) {
+  DC_TRY(check_disjoint(out, h.in));
+  DC_TRY(outside_shards(out, h.weights, "a shard of the weights"));
+  Shards hidden;
+  hidden.add(h.hidden);
+  return outside_shards(out, hidden, "hidden");
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t dc_linear_logprobs_workspace_bytes(int64_t rows, int64_t hidden_size, int64_t columns, int backward) {
+  if (rows < 0 || rows > kMaxLinearRows || hidden_size < 8 || hidden_size > kMaxHidden || hidden_size % 8 || columns < 1 ||
+      columns > kMaxVocab) {
+    fail(DC_ERR_INVALID, "no such head: %lld rows of %lld, %lld columns", static_cast<long long>(rows),
+         static_cast<long long>(hidden_size), static_cast<long long>(columns));
+    return 0;
+  }
+  const uint64_t n = static_cast<uint64_t>(std::max<int64_t>(rows, 1)), v = static_cast<uint64_t>(columns);
+  // (a shard's last tile may be narrower: at most one more tile a rank)
+  if (!backward) return round_up(stats_bytes(n, (v + kLinearN - 1) / kLinearN + kMaxRanks), 256);
+  return 256 + d_bytes(n, chunk_stride(v)) + round_up(n * static_cast<uint64_t>(hidden_size) * 4, 256);
+}
+
+dc_status_t dc_linear_logprobs(const dc_linear_logprobs_t* a, dc_stream_t stream) {
+  read_options();
+  if (!a) return fail(DC_ERR_INVALID, "the argument block is NULL");
+  Head h;
+  DC_TRY(check_head(a->hidden, a->hidden_row_stride, a->weights, a->widths, a->weight_row_strides, a->tokens, a->rows,
+                    a->hidden_size, a->vocab, a->temperature, a->ranks, a->dtype, a->tokens_64, &h));
+  if (a->rows == 0) return ok();
+  const uint64_t n = static_cast<uint64_t>(a->rows), size = static_cast<uint64_t>(a->hidden_size);
+  Spans out;
+  DC_TRY(take(a->logprobs, "logprobs", n * 4, 4, out));
+  if (a->entropy) DC_TRY(take(a->entropy, "entropy", n * 4, 4, out));
+  if (a->lse) DC_TRY(take(a->lse, "lse", n * 4, 4, out));
+  LinearOperand b[kMaxRanks];
+  LinearShard shard[kMaxRanks];
+  LinearParams p{};
+  uint64_t first = 0, tiles = 0;
+  for (int r = 0; r < a->ranks && first < static_cast<uint64_t>(a->vocab); ++r) {
+    if (a->widths[r] == 0) continue;
+    const uint64_t end = std::min<uint64_t>(first + a->widths[r], static_cast<uint64_t>(a->vocab));
+    b[p.shards] = LinearOperand{h.weights[r].base, end - first, size, h.weights[r].stride};  // (padding is not read)
+    shard[p.shards++] = LinearShard{static_cast<uint32_t>(tiles), static_cast<uint32_t>(first), static_cast<uint32_t>(end), 0};
+    tiles += (end - first + kLinearN - 1) / kLinearN;
+    first = end;
+  }
+  DC_TRY(check_workspace(a->workspace, a->workspace_bytes, stats_bytes(n, tiles), out));
+  DC_TRY(check_head_outputs(out, h));
+  p.m = static_cast<uint32_t>(n);
+  p.m_tiles = static_cast<uint32_t>((n + kLinearM - 1) / kLinearM);
+  p.n_tiles = static_cast<uint32_t>(tiles);
+  if (static_cast<uint64_t>(p.m_tiles) * tiles > 0x7FFFFFFFull)
+    return fail(DC_ERR_INVALID, "%lld rows of %llu tiles are too many", static_cast<long long>(a->rows), static_cast<unsigned long long>(tiles));
+  int sms = 0;
+  DC_TRY(device(&sms));
+  p.k_blocks = static_cast<uint32_t>((size + kLinearK - 1) / kLinearK);
+  p.vocab = static_cast<uint32_t>(a->vocab);
+  p.inv_t = static_cast<float>(1.0 / a->temperature);
+  p.tokens64 = a->tokens_64 != 0;
+  p.rows = n;
+  p.tokens = addr(a->tokens);
+  p.part = addr(a->workspace);
+  p.target = p.part + tiles * n * 16;
+  p.wait_ns = wait_limit_option();
+  const LinearOperand x{h.hidden.base, n, size, h.hidden.stride};
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int grid = 0;
+  cudaError_t e = launch_linear(kLinearStats, a->dtype, p, x, b, shard, sms, pdl_option(), s, &grid);
+  DC_TRY(check_launch(e, "log probabilities of a linear head", grid));
+  LinearFinishParams f{};
+  f.part = p.part;
+  f.target = p.target;
+  f.tokens = p.tokens;
+  f.logprobs = addr(a->logprobs);
+  f.entropy = addr(a->entropy);
+  f.lse = addr(a->lse);
+  f.rows = n;
+  f.tiles = p.n_tiles;
+  f.vocab = p.vocab;
+  f.tokens64 = p.tokens64;
+  e = launch_linear_finish(f, pdl_option(), s, &grid);
+  return check_launch(e, "log probabilities of a linear head", grid);
+}
+
+dc_status_t dc_linear_logprobs_backward(const dc_linear_logprobs_backward_t* a, dc_stream_t stream) {
+  read_options();
+  if (!a) return fail(DC_ERR_INVALID, "the argument block is NULL");
+  Head h;
+  DC_TRY(check_head(a->hidden, a->hidden_row_stride, a->weights, a->widths, a->weight_row_strides, a->tokens, a->rows,
+                    a->hidden_size, a->vocab, a->temperature, a->ranks, a->dtype, a->tokens_64, &h));
+  const uint64_t n = static_cast<uint64_t>(a->rows), size = static_cast<uint64_t>(a->hidden_size);
+  const uint64_t vocab = static_cast<uint64_t>(a->vocab);
+  // (without rows the vectors of rows may be NULL: only the weights' gradient, zeros, is written)
+  if (n && !a->grad_logprobs && !a->grad_entropy)
+    return fail(DC_ERR_INVALID, "neither grad_logprobs nor grad_entropy is given");
+  const bool want_h = a->grad_hidden != nullptr, want_w = a->grad_weights != nullptr;
+  if (n && !want_h && !want_w) return fail(DC_ERR_INVALID, "neither grad_hidden nor grad_weights is given");
+  if (want_w && !a->grad_weight_row_strides) return fail(DC_ERR_INVALID, "grad_weights need their strides");
+  // what is written: grad_hidden, then the shards' gradients
+  Strided gh{0, 1, 0, 0};
+  Shards gw;
+  if (want_h) DC_TRY(check_matrix(a->grad_hidden, n, size, a->grad_hidden_row_stride, "grad_hidden", -1, &gh));
+  uint64_t widest = 0, chunks = 0, first = 0;
+  for (int r = 0; r < a->ranks; ++r) {
+    Strided m{0, 1, 0, 0};
+    if (want_w)
+      DC_TRY(check_matrix(a->grad_weights[r], a->widths[r], size, a->grad_weight_row_strides[r], "grad_weights", r, &m));
+    gw.add(m);
+    const uint64_t held = first < vocab ? std::min<uint64_t>(a->widths[r], vocab - first) : 0;
+    widest = std::max(widest, held);
+    chunks += (held + kLinearChunk - 1) / kLinearChunk;
+    first += a->widths[r];
+  }
+  auto apart = [&](const Strided& x, const char* name, int r) -> dc_status_t {
+    if (x.width == 0) return DC_OK;
+    const char* with = nullptr;
+    if (h.hidden.width && rows_meet(x, h.hidden, 2)) with = "hidden";
+    for (int q = 0; q < h.weights.n; ++q)
+      if (h.weights[q].width && rows_meet(x, h.weights[q], 2)) with = "a shard of the weights";
+    for (int q = r + 1; q < gw.n; ++q)
+      if (gw[q].width && rows_meet(x, gw[q], 2)) with = "a shard of grad_weights";
+    return with ? fail(DC_ERR_OVERLAP, "%s overlaps %s", name, with) : DC_OK;
+  };
+  DC_TRY(apart(gh, "grad_hidden", -1));
+  for (int r = 0; r < gw.n; ++r) DC_TRY(apart(gw[r], "grad_weights", r));
+  Spans out;
+  const uint64_t stride = chunk_stride(widest);
+  const bool sum = want_h && chunks > 1;
+  if (n) {
+    DC_TRY(take(a->lse, "lse", n * 4, 4, h.in));
+    if (a->grad_logprobs) DC_TRY(take(a->grad_logprobs, "grad_logprobs", n * 4, 4, h.in));
+    if (a->grad_entropy) {
+      DC_TRY(take(a->grad_entropy, "grad_entropy", n * 4, 4, h.in));
+      DC_TRY(take(a->entropy, "entropy", n * 4, 4, h.in));
+    }
+    DC_TRY(check_workspace(a->workspace, a->workspace_bytes, 256 + d_bytes(n, stride) + (sum ? n * size * 4 : 0), out));
+    DC_TRY(check_head_outputs(out, h));
+    Shards written = gw;
+    DC_TRY(outside_shards(out, written, "a shard of grad_weights"));
+    DC_TRY(outside_shards(h.in, written, "a shard of grad_weights"));
+    Shards hidden;
+    hidden.add(gh);
+    DC_TRY(outside_shards(out, hidden, "grad_hidden"));
+    DC_TRY(outside_shards(h.in, hidden, "grad_hidden"));
+  }
+  int sms = 0;
+  DC_TRY(device(&sms));
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool pdl = pdl_option();
+  int grid = 0;
+  LinearParams p{};
+  p.tokens64 = a->tokens_64 != 0;
+  p.vocab = static_cast<uint32_t>(vocab);
+  p.inv_t = static_cast<float>(1.0 / a->temperature);
+  p.rows = n;
+  p.tokens = addr(a->tokens);
+  p.lse = addr(a->lse);
+  p.entropy = addr(a->entropy);
+  p.grad_logprobs = addr(a->grad_logprobs);
+  p.grad_entropy = addr(a->grad_entropy);
+  p.d = addr(a->workspace) + 256;
+  p.d_stride = stride;
+  p.acc = sum ? p.d + d_bytes(n, stride) : 0;
+  p.wait_ns = wait_limit_option();
+  if (n && a->dtype == kF16) {
+    p.scale = addr(a->workspace);
+    const cudaError_t e = launch_linear_scale(p.grad_logprobs, p.grad_entropy, p.tokens, p.tokens64 != 0, n, p.inv_t, p.scale, pdl, s);
+    DC_TRY(check_launch(e, "a linear head's gradient", 1));
+  }
+  const LinearOperand x{h.hidden.base, n, size, h.hidden.stride};
+  const uint32_t m_rows = static_cast<uint32_t>((n + kLinearM - 1) / kLinearM);
+  const uint32_t size_tiles = static_cast<uint32_t>((size + kLinearN - 1) / kLinearN);
+  uint64_t at = 0, chunk = 0;
+  for (int r = 0; r < a->ranks; at += a->widths[r], ++r) {
+    const uint64_t held = n && at < vocab ? std::min<uint64_t>(a->widths[r], vocab - at) : 0;  // padding has no gradient
+    if (want_w && held < a->widths[r]) {
+      const cudaError_t e = cudaMemset2DAsync(reinterpret_cast<void*>(gw[r].base + held * gw[r].stride), gw[r].stride, 0,
+                                              gw[r].width, a->widths[r] - held, s);
+      if (e != cudaSuccess) {
+        cudaGetLastError();
+        return fail(DC_ERR_CUDA, "clearing the padding's gradient failed: %s", cudaGetErrorString(e));
+      }
+    }
+    for (uint64_t c = 0; c < held; c += kLinearChunk, ++chunk) {
+      const uint32_t columns = static_cast<uint32_t>(std::min<uint64_t>(kLinearChunk, held - c));
+      const LinearOperand w{h.weights[r].base, c + columns, size, h.weights[r].stride};
+      const LinearOperand d{p.d, n, columns, stride};
+      LinearParams l = p;
+      l.m = static_cast<uint32_t>(n);
+      l.n = columns;
+      l.m_tiles = m_rows;
+      l.n_tiles = (columns + kLinearN - 1) / kLinearN;
+      l.k_blocks = static_cast<uint32_t>((size + kLinearK - 1) / kLinearK);
+      l.b_row0 = static_cast<uint32_t>(c);
+      l.first = static_cast<uint32_t>(at + c);
+      cudaError_t e = launch_linear(kLinearDLogits, a->dtype, l, x, &w, nullptr, sms, pdl, s, &grid);
+      DC_TRY(check_launch(e, "a linear head's gradient", grid));
+      if (want_h) {
+        LinearParams q = p;
+        q.m = static_cast<uint32_t>(n);
+        q.n = static_cast<uint32_t>(size);
+        q.m_tiles = m_rows;
+        q.n_tiles = size_tiles;
+        q.k_blocks = (columns + kLinearK - 1) / kLinearK;
+        q.b_row0 = static_cast<uint32_t>(c);
+        q.add = chunk > 0;
+        q.last = chunk + 1 == chunks;
+        q.out = gh.base;
+        q.out_stride = gh.stride;
+        e = launch_linear(kLinearDHidden, a->dtype, q, d, &w, nullptr, sms, pdl, s, &grid);
+        DC_TRY(check_launch(e, "a linear head's gradient", grid));
+      }
+      if (want_w) {
+        LinearParams q = p;
+        q.m = columns;
+        q.n = static_cast<uint32_t>(size);
+        q.m_tiles = (columns + kLinearM - 1) / kLinearM;
+        q.n_tiles = size_tiles;
+        q.k_blocks = static_cast<uint32_t>((n + kLinearK - 1) / kLinearK);
+        q.out = gw[r].base + c * gw[r].stride;
+        q.out_stride = gw[r].stride;
+        e = launch_linear(kLinearDWeights, a->dtype, q, d, &x, nullptr, sms, pdl, s, &grid);
+        DC_TRY(check_launch(e, "a linear head's gradient", grid));
+      }
+    }
+  }
+  return ok();
+}
+
+}  // extern "C"

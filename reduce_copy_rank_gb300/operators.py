@@ -53,6 +53,17 @@ _ATTEND = _Block("19Q4q6ifi", "q out lse page_table lengths workspace workspace_
                  "q_seq_stride q_head_stride out_seq_stride out_head_stride seqs table_width table_stride num_pages "
                  "page_size q_heads kv_heads dim window dtype scale reserved")
 
+_HEAD = "hidden weights widths weight_row_strides tokens "
+_LINEAR = _Block("11Q3qd4i", _HEAD + "logprobs entropy lse workspace workspace_bytes hidden_row_stride rows hidden_size "
+                 "vocab temperature ranks dtype tokens_64 reserved")
+_LINEAR_GRAD = _Block("16Q3qd4i", _HEAD + "lse entropy grad_logprobs grad_entropy grad_hidden grad_weights "
+                      "grad_weight_row_strides workspace workspace_bytes hidden_row_stride grad_hidden_row_stride rows "
+                      "hidden_size vocab temperature ranks dtype tokens_64 reserved")
+
+# the entry points, as the extension module takes them
+_ENTRIES = ("dc_token_logprobs", "dc_token_logprobs_backward", "dc_kv_append", "dc_paged_attention",
+            "dc_linear_logprobs", "dc_linear_logprobs_backward")
+
 _bound = None
 
 
@@ -61,12 +72,14 @@ def _lib():
     global _bound
     if _bound is None:
         L = _dc.lib()
-        for f in ("dc_token_logprobs", "dc_token_logprobs_backward", "dc_kv_append", "dc_paged_attention"):
+        for f in _ENTRIES:
             getattr(L, f).argtypes = [ctypes.c_char_p, ctypes.c_void_p]
             getattr(L, f).restype = ctypes.c_int
         L.dc_attention_workspace_bytes.argtypes = [ctypes.c_int64, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                                    ctypes.c_int64]
         L.dc_attention_workspace_bytes.restype = ctypes.c_size_t
+        L.dc_linear_logprobs_workspace_bytes.argtypes = [ctypes.c_int64] * 3 + [ctypes.c_int]
+        L.dc_linear_logprobs_workspace_bytes.restype = ctypes.c_size_t
         _bound = L
     return _bound
 
@@ -79,7 +92,8 @@ def _lib():
 
 def _with_arrays(block: _Block, fields: dict, keep: list) -> bytes:
     f = dict(fields)
-    for name in ("shards", "widths", "row_strides", "grads", "grad_row_strides"):
+    for name in ("shards", "widths", "row_strides", "grads", "grad_row_strides", "weights", "weight_row_strides",
+                 "grad_weights", "grad_weight_row_strides"):
         if name in f and not isinstance(f[name], int):
             keep.append(array.array("Q", f[name]))
             f[name] = keep[-1].buffer_info()[0]
@@ -108,6 +122,20 @@ def dc_attention_workspace_bytes(seqs: int, q_heads: int, kv_heads: int, dim: in
     return int(_lib().dc_attention_workspace_bytes(seqs, q_heads, kv_heads, dim, max_tokens))
 
 
+def dc_linear_logprobs(stream: int = 0, **fields) -> int:
+    keep = []
+    return _lib().dc_linear_logprobs(_with_arrays(_LINEAR, fields, keep), stream)
+
+
+def dc_linear_logprobs_backward(stream: int = 0, **fields) -> int:
+    keep = []
+    return _lib().dc_linear_logprobs_backward(_with_arrays(_LINEAR_GRAD, fields, keep), stream)
+
+
+def dc_linear_logprobs_workspace_bytes(rows: int, hidden_size: int, columns: int, backward: bool) -> int:
+    return int(_lib().dc_linear_logprobs_workspace_bytes(rows, hidden_size, columns, int(backward)))
+
+
 # ------------------------------------------------------------ tensor API ---
 
 _module = None
@@ -125,8 +153,7 @@ def _binding():
         except ImportError as e:
             raise _dc.LibraryMissing(f"the extension module _binding cannot be loaded ({e}): build it with `python -m "
                                      "reduce_copy_rank_gb300._build` or __graft_entry__.build()") from e
-        module.bind(*(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in (
-            "dc_token_logprobs", "dc_token_logprobs_backward", "dc_kv_append", "dc_paged_attention")))
+        module.bind(*(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in _ENTRIES))
         _module = module
     return _module
 
@@ -224,6 +251,133 @@ def logprobs_and_entropy(shards: Sequence, tokens, vocab: int | None = None, tem
 
         _function = TokenLogprobs
     return _function.apply(tokens, vocab, temperature, *shards)
+
+
+# ------------------------------------ log probabilities from hidden rows ---
+
+def linear_logprobs_workspace(rows: int, hidden_size: int, columns: int, backward: bool = False, device=None):
+    """A workspace tensor for :func:`linear_logprobs` (``backward``: for
+    :func:`linear_logprobs_backward`) with up to ``rows`` rows of
+    ``hidden_size`` and shards of ``columns`` columns in all.  Its contents do
+    not matter; calls that may run at the same time need one each."""
+    import torch
+
+    n = dc_linear_logprobs_workspace_bytes(rows, hidden_size, columns, backward)
+    if n == 0:
+        raise _dc.DCError(1, _dc.last_error() or "no such head")
+    return torch.empty(n, dtype=torch.uint8, device=device if device is not None else "cuda")
+
+
+def linear_logprobs(hidden, weights: Sequence, tokens, logprobs, workspace, entropy=None, lse=None,
+                    vocab: int | None = None, temperature: float = 1.0, stream=None):
+    """:func:`token_logprobs` of the logits ``hidden @ weights.T`` without
+    keeping them: ``hidden`` [rows, hidden size], the head as P vocabulary
+    shards ``weights[r]`` [columns of rank r, hidden size] (bfloat16 or
+    float16; 16-byte aligned rows, a hidden size that is a multiple of 8).
+
+    ``logprobs``, and where given ``entropy`` and ``lse`` (float32 [rows]), as
+    there; the logits are binary32 sums and are not rounded.  ``workspace``:
+    :func:`linear_logprobs_workspace`.
+
+    A negative token is not scored (its entry is 0), a token past the
+    vocabulary gives NaN.  A row's bits do not depend on the other rows, nor
+    on the sharding where shards are multiples of 256 columns (the last one
+    may be any).  Returns ``logprobs``."""
+    status = (_module or _binding()).linear_logprobs(hidden, weights, tokens, logprobs, workspace, entropy, lse, vocab,
+                                                     temperature, stream)
+    if status:
+        _dc._check(status)
+    return logprobs
+
+
+def linear_logprobs_backward(hidden, weights: Sequence, tokens, lse, grad_logprobs, grad_hidden, grad_weights,
+                             workspace, entropy=None, grad_entropy=None, vocab: int | None = None,
+                             temperature: float = 1.0, stream=None):
+    """The gradient of :func:`linear_logprobs` with respect to the hidden rows
+    and the head's weights: ``grad_hidden`` and ``grad_weights[r]`` (shaped and
+    typed as ``hidden`` and ``weights[r]``; either may be None) receive that of
+    ``sum(grad_logprobs * logprobs + grad_entropy * entropy)``.  ``lse`` and
+    ``entropy`` are the forward call's outputs (``entropy`` only with
+    ``grad_entropy``); the upstream gradients are float32 [rows], either may be
+    None.
+
+    The logits are computed again, 16384 columns at a time; their gradient is
+    rounded to 16 bits before its products, whose sums are binary32.  Rows of
+    the weights' gradient past ``vocab`` receive 0.  ``workspace``:
+    :func:`linear_logprobs_workspace` with ``backward``.  Returns
+    ``(grad_hidden, grad_weights)``."""
+    status = (_module or _binding()).linear_logprobs_backward(hidden, weights, tokens, lse, grad_logprobs, grad_hidden,
+                                                              grad_weights, workspace, entropy, grad_entropy, vocab,
+                                                              temperature, stream)
+    if status:
+        _dc._check(status)
+    return grad_hidden, grad_weights
+
+
+_linear_function = None
+
+
+def linear_logprobs_and_entropy(hidden, weights: Sequence, tokens, vocab: int | None = None, temperature: float = 1.0):
+    """``(logprobs, entropy)`` of :func:`linear_logprobs` as new tensors that
+    autograd differentiates with respect to the hidden rows and every shard
+    (through :func:`linear_logprobs_backward`), once: a second derivative
+    raises.  Workspaces come from torch's allocator."""
+    global _linear_function
+    import torch
+
+    if _linear_function is None:
+        class LinearLogprobs(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, tokens, vocab, temperature, hidden, *weights):
+                rows, size = hidden.shape
+                logprobs, entropy, lse = (torch.empty(rows, dtype=torch.float32, device=hidden.device) for _ in range(3))
+                ws = linear_logprobs_workspace(rows, size, sum(w.shape[0] for w in weights), device=hidden.device)
+                linear_logprobs(hidden, weights, tokens, logprobs, ws, entropy=entropy, lse=lse, vocab=vocab,
+                                temperature=temperature)
+                ctx.set_materialize_grads(False)  # an output that is not used has no upstream gradient to read
+                ctx.save_for_backward(tokens, lse, entropy, hidden, *weights)
+                ctx.vocab, ctx.temperature = vocab, temperature
+                return logprobs, entropy
+
+            @staticmethod
+            def backward(ctx, g, h):
+                tokens, lse, entropy, hidden, *weights = ctx.saved_tensors
+                want_hidden, want_weights = ctx.needs_input_grad[3], any(ctx.needs_input_grad[4:])
+                if (g is None and h is None) or not (want_hidden or want_weights):
+                    return (None,) * (4 + len(weights))
+                grad_hidden = torch.empty_like(hidden, memory_format=torch.contiguous_format) if want_hidden else None
+                grads = [torch.empty_like(w, memory_format=torch.contiguous_format) for w in weights] if want_weights else None
+                # upstream gradients may be broadcast (a sum's is one number for all rows)
+                g, h = (None if u is None else u.to(torch.float32).contiguous() for u in (g, h))
+                ws = linear_logprobs_workspace(*hidden.shape, sum(w.shape[0] for w in weights), backward=True,
+                                               device=hidden.device)
+                linear_logprobs_backward(hidden, weights, tokens, lse, g, grad_hidden, grads, ws, entropy=entropy,
+                                         grad_entropy=h, vocab=ctx.vocab, temperature=ctx.temperature)
+                out = [x for x in (grad_hidden, *(grads or ())) if x is not None]
+                if torch.is_grad_enabled():  # create_graph: the gradients leave a kernel, no graph holds them
+                    out = list(_first_derivative("linear_logprobs_and_entropy").apply(
+                        len(out), *out, hidden, *weights, *(u for u in (g, h) if u is not None)))
+                grad_hidden = out.pop(0) if want_hidden else None
+                return (None, None, None, grad_hidden, *(out if want_weights else (None,) * len(weights)))
+
+        _linear_function = LinearLogprobs
+    return _linear_function.apply(tokens, vocab, temperature, hidden, *weights)
+
+
+def _first_derivative(name: str):
+    """A function that passes gradients on with the tensors that they depend on: their own derivative is refused."""
+    import torch
+
+    class FirstDerivative(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, count, *tensors):
+            return tuple(t.detach() for t in tensors[:count])
+
+        @staticmethod
+        def backward(ctx, *_):
+            raise RuntimeError(f"{name} has no second derivative: its gradients cannot be differentiated")
+
+    return FirstDerivative
 
 
 # ------------------------------------------------------------ paged cache ---
