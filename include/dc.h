@@ -566,6 +566,101 @@ typedef struct {
 dc_status_t dc_kv_append(const dc_kv_append_t *args, dc_stream_t stream);
 
 /*
+ * dc_kv_append_norm -- dc_kv_append of keys and queries that are normed first:
+ * a head x of `dim` elements becomes x w / sqrt(mean x^2 + eps), with weights
+ * w = q_norm or k_norm [dim] (of the heads' type, or binary32 if norm_32), and
+ * is rotated then; in binary32, rounded once.  Values are copied.  q_norm may be
+ * NULL without queries.  dim up to 512; everything else as for dc_kv_append.
+ */
+typedef struct {
+    dc_kv_append_t append;
+    const void *q_norm;
+    const void *k_norm;
+    float eps;
+    int32_t norm_32;
+} dc_kv_append_norm_t;
+dc_status_t dc_kv_append_norm(const dc_kv_append_norm_t *args, dc_stream_t stream);
+
+/* A [tokens, heads, dim] tensor: element d of head h of token t is
+ * data[t*token_stride + h*head_stride + d], every head 16-byte aligned. */
+typedef struct {
+    void *data;
+    uint64_t token_stride;
+    uint64_t head_stride;
+} dc_heads_t;
+
+/*
+ * dc_qk_norm_rotate -- the queries and keys of a training step: q -> q_out and
+ * k -> k_out, each head normed and rotated as dc_kv_append_norm does it (the
+ * same bits), to positions[i].
+ *
+ * A negative position marks padding: its rows are 0, and so is its gradient.  A
+ * position past cos_sin gives NaN in its rows.  cos_sin NULL with rotary_dim 0:
+ * no rotation.  dim: a multiple of 8 (of 4 for DC_F32) up to 512; rotary_dim as
+ * for dc_kv_append.  q_out may be exactly q, and k_out exactly k; outputs lie
+ * apart otherwise (heads of one tensor beside one another are fine).
+ */
+typedef struct {
+    dc_heads_t q, k, q_out, k_out;
+    const int32_t *positions;
+    const float *cos_sin;   /* [cos_sin_rows, rotary_dim] */
+    const void *q_norm;
+    const void *k_norm;
+    int64_t tokens;
+    int64_t cos_sin_rows;
+    int32_t q_heads;
+    int32_t kv_heads;
+    int32_t dim;
+    int32_t rotary_dim;
+    int32_t interleaved;
+    int32_t dtype;
+    int32_t norm_32;
+    float eps;
+} dc_qk_norm_rotate_t;
+dc_status_t dc_qk_norm_rotate(const dc_qk_norm_rotate_t *args, dc_stream_t stream);
+
+/*
+ * dc_qk_norm_rotate_backward -- its gradient: from that of q_out and k_out
+ * (grad_q_out, grad_k_out) those of q, k and the weights.  With g the gradient
+ * rotated back, r = 1 / sqrt(mean x^2 + eps) and n = x r:
+ *
+ *   grad_x = r (g w - n mean(g w n));   grad_w = sum over tokens and heads of g n.
+ *
+ * grad_q and grad_k may be exactly grad_q_out and grad_k_out.  grad_q_norm and
+ * grad_k_norm [dim] (typed as the weights) replace what was there; NULL: not
+ * wanted.  Their sums are binary32 in one fixed order, which follows from the
+ * number of tokens and heads; without tokens they are 0.  A token whose position
+ * is past cos_sin makes them NaN.
+ * workspace (for them): dc_qk_norm_workspace_bytes bytes, 16-byte aligned, whose
+ * contents do not matter; calls that overlap on the GPU need one each.  One or
+ * two kernels.
+ */
+typedef struct {
+    dc_heads_t q, k, grad_q_out, grad_k_out, grad_q, grad_k;
+    const int32_t *positions;
+    const float *cos_sin;
+    const void *q_norm;
+    const void *k_norm;
+    void *grad_q_norm;
+    void *grad_k_norm;
+    void *workspace;
+    uint64_t workspace_bytes;
+    int64_t tokens;
+    int64_t cos_sin_rows;
+    int32_t q_heads;
+    int32_t kv_heads;
+    int32_t dim;
+    int32_t rotary_dim;
+    int32_t interleaved;
+    int32_t dtype;
+    int32_t norm_32;
+    float eps;
+} dc_qk_norm_rotate_backward_t;
+dc_status_t dc_qk_norm_rotate_backward(const dc_qk_norm_rotate_backward_t *args, dc_stream_t stream);
+/* 0 if the arguments are not supported. */
+size_t dc_qk_norm_workspace_bytes(int64_t tokens, int q_heads, int kv_heads, int dim);
+
+/*
  * dc_paged_attention -- attention of one new token per sequence over a paged
  * cache.  Query head h of sequence b attends, through key head
  * h / (q_heads / kv_heads), to tokens t of [max(0, lengths[b] - window),

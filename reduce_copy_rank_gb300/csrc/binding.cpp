@@ -27,6 +27,9 @@ decltype(&dc_kv_append) g_append = nullptr;
 decltype(&dc_paged_attention) g_attend = nullptr;
 decltype(&dc_linear_logprobs) g_linear = nullptr;
 decltype(&dc_linear_logprobs_backward) g_linear_grad = nullptr;
+decltype(&dc_kv_append_norm) g_append_norm = nullptr;
+decltype(&dc_qk_norm_rotate) g_norm = nullptr;
+decltype(&dc_qk_norm_rotate_backward) g_norm_grad = nullptr;
 
 // A refusal: the Python exception is set.
 struct Refused {};
@@ -354,9 +357,26 @@ const at::Tensor& page_table(const Call& c, PyObject* o, int64_t rows) {
   return t;
 }
 
-// kv_append(k, v, positions, seqs, page_table, k_cache, v_cache, q, q_out,
-//           cos_sin, interleaved, stream) -> status
-PyObject* append(PyObject* const* a) {
+const float* angles(const Call& c, PyObject* o, int64_t& rows, int32_t& rotary) {
+  if (o == Py_None) return nullptr;
+  const at::Tensor& t = tensor(o, "cos_sin");
+  if (t.scalar_type() != at::kFloat || t.dim() != 2 || !t.is_contiguous())
+    wrong(std::string("cos_sin must be a contiguous float32 (positions, rotary_dim) tensor (got ") +
+          dtype_name(t.scalar_type()) + " " + text(t) + ")");
+  on(c, o, "cos_sin", at::kFloat);
+  rows = t.size(0);
+  rotary = static_cast<int32_t>(t.size(1) > 1 << 20 ? 1 << 20 : t.size(1));
+  return static_cast<const float*>(t.const_data_ptr());
+}
+
+int truth(PyObject* o) {
+  const int t = PyObject_IsTrue(o);
+  if (t < 0) throw Refused{};
+  return t;
+}
+
+// The arguments of kv_append, in their order.
+Call fill_append(PyObject* const* a, dc_kv_append_t& b, Written& w) {
   const at::Tensor& first = tensor(a[0], "k");
   const at::ScalarType type = first.scalar_type();
   const int code = code_of(type);
@@ -364,8 +384,6 @@ PyObject* append(PyObject* const* a) {
   const Call c = call_of(first, a[11]);
   if (first.dim() != 3) wrong("k has shape " + text(first) + ", expected (tokens, heads, dim)");
   const int64_t n = first.size(0), hk = first.size(1), d = first.size(2);
-  Written w;
-  dc_kv_append_t b{};
   b.k = heads_of(c, a[0], "k", n, hk, d, type, b.k_token_stride, b.k_head_stride).const_data_ptr();
   b.v = heads_of(c, a[1], "v", n, hk, d, type, b.v_token_stride, b.v_head_stride).const_data_ptr();
   int64_t hq = 0;
@@ -378,16 +396,7 @@ PyObject* append(PyObject* const* a) {
   } else if (a[8] != Py_None) {
     wrong("q_out needs q");
   }
-  if (a[9] != Py_None) {
-    const at::Tensor& t = tensor(a[9], "cos_sin");
-    if (t.scalar_type() != at::kFloat || t.dim() != 2 || !t.is_contiguous())
-      wrong(std::string("cos_sin must be a contiguous float32 (positions, rotary_dim) tensor (got ") +
-            dtype_name(t.scalar_type()) + " " + text(t) + ")");
-    on(c, a[9], "cos_sin", at::kFloat);
-    b.cos_sin = static_cast<const float*>(t.const_data_ptr());
-    b.cos_sin_rows = t.size(0);
-    b.rotary_dim = static_cast<int32_t>(t.size(1) > 1 << 20 ? 1 << 20 : t.size(1));
-  }
+  b.cos_sin = angles(c, a[9], b.cos_sin_rows, b.rotary_dim);
   const Caches x = caches(c, a[5], a[6], hk, d, type, &w, b.k_cache, b.v_cache);
   const at::Tensor& table = page_table(c, a[4], -1);
   b.positions = static_cast<const int32_t*>(vector(c, a[2], "positions", n, at::kInt));
@@ -403,11 +412,125 @@ PyObject* append(PyObject* const* a) {
   b.q_heads = static_cast<int32_t>(hq);
   b.kv_heads = static_cast<int32_t>(hk);
   b.dim = static_cast<int32_t>(d);
-  const int truth = PyObject_IsTrue(a[10]);
-  if (truth < 0) throw Refused{};
-  b.interleaved = truth;
+  b.interleaved = truth(a[10]);
   b.dtype = code;
+  return c;
+}
+
+// kv_append(k, v, positions, seqs, page_table, k_cache, v_cache, q, q_out,
+//           cos_sin, interleaved, stream) -> status
+PyObject* append(PyObject* const* a) {
+  Written w;
+  dc_kv_append_t b{};
+  const Call c = fill_append(a, b, w);
   return w.after(g_append(&b, c.stream));
+}
+
+// The weights of a norm: [dim] in binary32 or the heads' type; `f32` < 0: either.
+const void* norm_weight(const Call& c, PyObject* o, const char* what, int64_t dim, at::ScalarType type, int& f32) {
+  const at::Tensor& t = tensor(o, what);
+  const at::ScalarType s = t.scalar_type();
+  if (s != at::kFloat && s != type)
+    wrong(std::string(what) + " has dtype " + dtype_name(s) + ", expected torch.float32 or " + dtype_name(type));
+  if (f32 >= 0 && f32 != (s == at::kFloat)) wrong("q_norm and k_norm must have one dtype");
+  on(c, o, what, s);
+  shaped(t, what, dim);
+  f32 = s == at::kFloat;
+  return t.const_data_ptr();
+}
+
+// kv_append_norm(the arguments of kv_append, then q_norm, k_norm, eps) -> status
+PyObject* append_norm(PyObject* const* a) {
+  Written w;
+  dc_kv_append_norm_t b{};
+  const Call c = fill_append(a, b.append, w);
+  const at::ScalarType type = THPVariable_Unpack(a[0]).scalar_type();
+  int f32 = -1;
+  if (a[13] == Py_None) wrong("q_norm needs k_norm");
+  b.k_norm = norm_weight(c, a[13], "k_norm", b.append.dim, type, f32);
+  if (b.append.q_heads || a[12] != Py_None) {
+    if (a[12] == Py_None) wrong("k_norm needs q_norm where there are queries");
+    b.q_norm = norm_weight(c, a[12], "q_norm", b.append.dim, type, f32);
+  }
+  b.norm_32 = f32;
+  b.eps = static_cast<float>(number(a[14]));
+  return w.after(g_append_norm(&b, c.stream));
+}
+
+// The tokens, heads and angles of a norm of queries and keys.
+struct NormArgs {
+  int64_t n, hq, hk, d;
+  at::ScalarType type;
+  Call call;
+};
+void heads_in(const NormArgs& s, PyObject* o, const char* what, bool keys, dc_heads_t& h, Written* w) {
+  const at::Tensor& t = heads_of(s.call, o, what, s.n, keys ? s.hk : s.hq, s.d, s.type, h.token_stride, h.head_stride);
+  h.data = w ? (*w)(t).mutable_data_ptr() : const_cast<void*>(t.const_data_ptr());
+}
+template <class Block>
+NormArgs fill_norm(Block& b, PyObject* const* a, PyObject* eps, PyObject* interleaved, PyObject* stream) {
+  const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k");
+  NormArgs s{};
+  s.type = q.scalar_type();
+  const int code = code_of(s.type);
+  if (code < 0) wrong(std::string("queries are bfloat16, float16 or float32 (got ") + dtype_name(s.type) + ")");
+  s.call = call_of(q, stream);
+  if (q.dim() != 3) wrong("q has shape " + text(q) + ", expected (tokens, heads, dim)");
+  if (k.dim() != 3) wrong("k has shape " + text(k) + ", expected (tokens, heads, dim)");
+  s.n = q.size(0);
+  s.hq = q.size(1);
+  s.hk = k.size(1);
+  s.d = q.size(2);
+  if (s.hq > INT32_MAX || s.hk > INT32_MAX || s.d > INT32_MAX) wrong("a dimension is too large");
+  heads_in(s, a[0], "q", false, b.q, nullptr);
+  heads_in(s, a[1], "k", true, b.k, nullptr);
+  b.positions = static_cast<const int32_t*>(vector(s.call, a[2], "positions", s.n, at::kInt));
+  b.cos_sin = angles(s.call, a[3], b.cos_sin_rows, b.rotary_dim);
+  int f32 = -1;
+  b.q_norm = norm_weight(s.call, a[4], "q_norm", s.d, s.type, f32);
+  b.k_norm = norm_weight(s.call, a[5], "k_norm", s.d, s.type, f32);
+  b.norm_32 = f32;
+  b.tokens = s.n;
+  b.q_heads = static_cast<int32_t>(s.hq);
+  b.kv_heads = static_cast<int32_t>(s.hk);
+  b.dim = static_cast<int32_t>(s.d);
+  b.dtype = code;
+  b.eps = static_cast<float>(number(eps));
+  b.interleaved = truth(interleaved);
+  return s;
+}
+
+// qk_norm_rotate(q, k, positions, cos_sin, q_norm, k_norm, q_out, k_out, eps,
+//                interleaved, stream) -> status
+PyObject* norm(PyObject* const* a) {
+  Written w;
+  dc_qk_norm_rotate_t b{};
+  const NormArgs s = fill_norm(b, a, a[8], a[9], a[10]);
+  heads_in(s, a[6], "q_out", false, b.q_out, &w);
+  heads_in(s, a[7], "k_out", true, b.k_out, &w);
+  return w.after(g_norm(&b, s.call.stream));
+}
+
+// qk_norm_rotate_backward(q, k, positions, cos_sin, q_norm, k_norm,
+//   grad_q_out, grad_k_out, grad_q, grad_k, grad_q_norm, grad_k_norm,
+//   workspace, eps, interleaved, stream) -> status
+PyObject* norm_grad(PyObject* const* a) {
+  Written w;
+  dc_qk_norm_rotate_backward_t b{};
+  const NormArgs s = fill_norm(b, a, a[13], a[14], a[15]);
+  heads_in(s, a[6], "grad_q_out", false, b.grad_q_out, nullptr);
+  heads_in(s, a[7], "grad_k_out", true, b.grad_k_out, nullptr);
+  heads_in(s, a[8], "grad_q", false, b.grad_q, &w);
+  heads_in(s, a[9], "grad_k", true, b.grad_k, &w);
+  const at::ScalarType type = b.norm_32 ? at::kFloat : s.type;
+  b.grad_q_norm = out_vector(s.call, a[10], "grad_q_norm", s.d, type, w, true);
+  b.grad_k_norm = out_vector(s.call, a[11], "grad_k_norm", s.d, type, w, true);
+  if (a[12] != Py_None) {
+    const at::Tensor& ws = workspace_of(s.call, a[12]);
+    b.workspace = ws.mutable_data_ptr();
+    b.workspace_bytes = static_cast<uint64_t>(ws.nbytes());
+  }
+  return w.after(g_norm_grad(&b, s.call.stream));
 }
 
 // paged_attention(q, k_cache, v_cache, page_table, lengths, out, workspace,
@@ -598,6 +721,7 @@ PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
   void** const to[] = {
       reinterpret_cast<void**>(&g_score), reinterpret_cast<void**>(&g_grad), reinterpret_cast<void**>(&g_append),
       reinterpret_cast<void**>(&g_attend), reinterpret_cast<void**>(&g_linear), reinterpret_cast<void**>(&g_linear_grad),
+      reinterpret_cast<void**>(&g_append_norm), reinterpret_cast<void**>(&g_norm), reinterpret_cast<void**>(&g_norm_grad),
   };
   constexpr Py_ssize_t count = sizeof to / sizeof to[0];
   if (n != count) {
@@ -624,6 +748,9 @@ PyMethodDef kMethods[] = {
     {"token_logprobs_backward", as_function(&entry<grad, 10>), METH_FASTCALL, nullptr},
     {"kv_append", as_function(&entry<append, 12>), METH_FASTCALL, nullptr},
     {"paged_attention", as_function(&entry<attend, 11>), METH_FASTCALL, nullptr},
+    {"kv_append_norm", as_function(&entry<append_norm, 15>), METH_FASTCALL, nullptr},
+    {"qk_norm_rotate", as_function(&entry<norm, 11>), METH_FASTCALL, nullptr},
+    {"qk_norm_rotate_backward", as_function(&entry<norm_grad, 16>), METH_FASTCALL, nullptr},
     {"linear_logprobs", as_function(&entry<linear, 10>), METH_FASTCALL, nullptr},
     {"linear_logprobs_backward", as_function(&entry<linear_grad, 13>), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},

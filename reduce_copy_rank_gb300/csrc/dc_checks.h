@@ -166,6 +166,13 @@ inline dc_status_t check_heads(int q_heads, int kv_heads, int dim, bool need_q) 
   return DC_OK;
 }
 
+// What the norms of heads add to check_heads.
+inline dc_status_t check_norm(int dim, float eps) {
+  if (dim > kNormMaxDim) return fail(DC_ERR_INVALID, "normed heads have up to %d elements (got %d)", kNormMaxDim, dim);
+  if (!(eps >= 0.0f) || !std::isfinite(eps)) return fail(DC_ERR_INVALID, "eps is not a finite number of at least 0");
+  return DC_OK;
+}
+
 // A [n, heads, dim] tensor with strides in elements, every head 16-byte aligned.
 inline dc_status_t check_tokens(const void* p, const char* name, uint64_t n, int heads, int dim, uint64_t tok, uint64_t head,
                          int es, Spans& to) {

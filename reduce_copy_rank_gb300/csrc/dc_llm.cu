@@ -50,6 +50,96 @@ dc_status_t plan_attend(int64_t seqs, int q_heads, int kv_heads, int dim, uint64
   return DC_OK;
 }
 
+// Checks an append's arguments (of at least one token) and fills its parameters;
+// `written`: the spans that it writes.
+dc_status_t take_append(const dc_kv_append_t* a, AppendParams& p, Spans& written) {
+  if (a->dtype < kBF16 || a->dtype > kF32)
+    return fail(DC_ERR_INVALID, "dtype %d is not DC_BF16, DC_F16 or DC_F32", a->dtype);
+  const int es = elem_bytes(a->dtype), per = 16 / es;
+  DC_TRY(check_heads(a->q_heads, a->kv_heads, a->dim, false));
+  if (a->dim % per || a->dim > 1024)
+    return fail(DC_ERR_INVALID, "head dimension %d is not a multiple of %d up to 1024", a->dim, per);
+  if (a->rotary_dim < 0 || a->rotary_dim > a->dim || a->rotary_dim % (a->interleaved ? per : 2 * per))
+    return fail(DC_ERR_INVALID, "rotary_dim = %d is not a multiple of %d up to the head dimension", a->rotary_dim,
+                a->interleaved ? per : 2 * per);
+  if (a->tokens < 0 || a->tokens > 0x7FFFFFFF / 512)
+    return fail(DC_ERR_INVALID, "%lld tokens", static_cast<long long>(a->tokens));
+  if (a->tokens == 0) return DC_OK;
+  const uint64_t n = static_cast<uint64_t>(a->tokens);
+  Spans in, cache, out;
+  DC_TRY(check_tokens(a->k, "k", n, a->kv_heads, a->dim, a->k_token_stride, a->k_head_stride, es, in));
+  DC_TRY(check_tokens(a->v, "v", n, a->kv_heads, a->dim, a->v_token_stride, a->v_head_stride, es, in));
+  DC_TRY(take(a->positions, "positions", n * 4, 4, in));
+  DC_TRY(take(a->seqs, "seqs", n * 4, 4, in));
+  DC_TRY(check_table(a->page_table, a->table_rows, a->table_width, a->table_stride, in));
+  if (a->rotary_dim) {
+    if (a->cos_sin_rows < 1 || a->cos_sin_rows > (1ll << 40))
+      return fail(DC_ERR_INVALID, "cos_sin has %lld rows", static_cast<long long>(a->cos_sin_rows));
+    DC_TRY(take(a->cos_sin, "cos_sin", static_cast<uint64_t>(a->cos_sin_rows) * a->rotary_dim * 4, 4, in));
+  }
+  DC_TRY(check_cache(a->k_cache, "k_cache", a->num_pages, a->page_size, a->kv_heads, a->dim, es, true, &p.kc, cache));
+  DC_TRY(check_cache(a->v_cache, "v_cache", a->num_pages, a->page_size, a->kv_heads, a->dim, es, true, &p.vc, cache));
+  // (the caches may be interleaved in one tensor: their spans may meet, their tokens' heads not)
+  if (blocks_meet(cache_blocks(a->k_cache, a->num_pages, a->page_size, a->kv_heads, a->dim, es),
+                  cache_blocks(a->v_cache, a->num_pages, a->page_size, a->kv_heads, a->dim, es)))
+    return fail(DC_ERR_OVERLAP, "k_cache overlaps v_cache");
+  for (const Span& c : cache) DC_TRY(check_apart(c, in));
+  if (a->q_heads) {
+    Spans q;
+    DC_TRY(check_tokens(a->q, "q", n, a->q_heads, a->dim, a->q_token_stride, a->q_head_stride, es, q));
+    DC_TRY(check_tokens(a->q_out, "q_out", n, a->q_heads, a->dim, a->q_out_token_stride, a->q_out_head_stride, es, out));
+    DC_TRY(check_written("q_out", n, a->q_heads, a->dim, a->q_out_token_stride, a->q_out_head_stride));
+    const bool same = a->q == a->q_out && a->q_token_stride == a->q_out_token_stride &&
+                      a->q_head_stride == a->q_out_head_stride;
+    if (!same) {
+      DC_TRY(check_disjoint(out, q));
+      DC_TRY(check_disjoint(out, in));
+    } else {
+      // in place: heads of queries beside those of keys and values in one tensor are fine
+      const Blocks qb = token_blocks(a->q_out, n, a->q_heads, a->dim, a->q_out_token_stride, a->q_out_head_stride, es);
+      if (blocks_meet(qb, token_blocks(a->k, n, a->kv_heads, a->dim, a->k_token_stride, a->k_head_stride, es)))
+        return fail(DC_ERR_OVERLAP, "q_out overlaps k");
+      if (blocks_meet(qb, token_blocks(a->v, n, a->kv_heads, a->dim, a->v_token_stride, a->v_head_stride, es)))
+        return fail(DC_ERR_OVERLAP, "q_out overlaps v");
+      DC_TRY(check_apart(out[0], in, 2));  // (k and v are the first two)
+    }
+    DC_TRY(check_disjoint(out, cache));
+    for (const Span& c : cache) DC_TRY(check_apart(c, q));
+  }
+  for (const Span& c : cache) written.add(c);
+  for (const Span& o : out) written.add(o);
+  const uint64_t e8 = static_cast<uint64_t>(es);
+  p.q = addr(a->q);
+  p.q_token = a->q_token_stride * e8;
+  p.q_head = a->q_head_stride * e8;
+  p.qo = addr(a->q_out);
+  p.qo_token = a->q_out_token_stride * e8;
+  p.qo_head = a->q_out_head_stride * e8;
+  p.k = addr(a->k);
+  p.k_token = a->k_token_stride * e8;
+  p.k_head = a->k_head_stride * e8;
+  p.v = addr(a->v);
+  p.v_token = a->v_token_stride * e8;
+  p.v_head = a->v_head_stride * e8;
+  p.positions = addr(a->positions);
+  p.seqs = addr(a->seqs);
+  p.table = addr(a->page_table);
+  p.cos_sin = addr(a->cos_sin);
+  p.tokens = n;
+  p.table_stride = a->table_rows > 1 ? a->table_stride : 0;
+  p.cos_rows = a->cos_sin_rows;
+  p.num_pages = a->num_pages;
+  p.page_size = static_cast<uint32_t>(a->page_size);
+  p.table_width = static_cast<uint32_t>(a->table_width);
+  p.num_seqs = static_cast<uint32_t>(a->table_rows);
+  p.q_heads = a->q_heads;
+  p.kv_heads = a->kv_heads;
+  p.dim = a->dim;
+  p.rot = a->rotary_dim;
+  p.interleaved = a->interleaved != 0;
+  return DC_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -187,93 +277,58 @@ dc_status_t dc_token_logprobs_backward(const dc_token_logprobs_backward_t* a, dc
 dc_status_t dc_kv_append(const dc_kv_append_t* a, dc_stream_t stream) {
   read_options();
   if (!a) return fail(DC_ERR_INVALID, "the argument block is NULL");
-  if (a->dtype < kBF16 || a->dtype > kF32)
-    return fail(DC_ERR_INVALID, "dtype %d is not DC_BF16, DC_F16 or DC_F32", a->dtype);
-  const int es = elem_bytes(a->dtype), per = 16 / es;
-  DC_TRY(check_heads(a->q_heads, a->kv_heads, a->dim, false));
-  if (a->dim % per || a->dim > 1024)
-    return fail(DC_ERR_INVALID, "head dimension %d is not a multiple of %d up to 1024", a->dim, per);
-  if (a->rotary_dim < 0 || a->rotary_dim > a->dim || a->rotary_dim % (a->interleaved ? per : 2 * per))
-    return fail(DC_ERR_INVALID, "rotary_dim = %d is not a multiple of %d up to the head dimension", a->rotary_dim,
-                a->interleaved ? per : 2 * per);
-  if (a->tokens < 0 || a->tokens > 0x7FFFFFFF / 512)
-    return fail(DC_ERR_INVALID, "%lld tokens", static_cast<long long>(a->tokens));
-  if (a->tokens == 0) return ok();
-  const uint64_t n = static_cast<uint64_t>(a->tokens);
   AppendParams p{};
-  Spans in, cache, out;
-  DC_TRY(check_tokens(a->k, "k", n, a->kv_heads, a->dim, a->k_token_stride, a->k_head_stride, es, in));
-  DC_TRY(check_tokens(a->v, "v", n, a->kv_heads, a->dim, a->v_token_stride, a->v_head_stride, es, in));
-  DC_TRY(take(a->positions, "positions", n * 4, 4, in));
-  DC_TRY(take(a->seqs, "seqs", n * 4, 4, in));
-  DC_TRY(check_table(a->page_table, a->table_rows, a->table_width, a->table_stride, in));
-  if (a->rotary_dim) {
-    if (a->cos_sin_rows < 1 || a->cos_sin_rows > (1ll << 40))
-      return fail(DC_ERR_INVALID, "cos_sin has %lld rows", static_cast<long long>(a->cos_sin_rows));
-    DC_TRY(take(a->cos_sin, "cos_sin", static_cast<uint64_t>(a->cos_sin_rows) * a->rotary_dim * 4, 4, in));
-  }
-  DC_TRY(check_cache(a->k_cache, "k_cache", a->num_pages, a->page_size, a->kv_heads, a->dim, es, true, &p.kc, cache));
-  DC_TRY(check_cache(a->v_cache, "v_cache", a->num_pages, a->page_size, a->kv_heads, a->dim, es, true, &p.vc, cache));
-  // (the caches may be interleaved in one tensor: their spans may meet, their tokens' heads not)
-  if (blocks_meet(cache_blocks(a->k_cache, a->num_pages, a->page_size, a->kv_heads, a->dim, es),
-                  cache_blocks(a->v_cache, a->num_pages, a->page_size, a->kv_heads, a->dim, es)))
-    return fail(DC_ERR_OVERLAP, "k_cache overlaps v_cache");
-  for (const Span& c : cache) DC_TRY(check_apart(c, in));
-  if (a->q_heads) {
-    Spans q;
-    DC_TRY(check_tokens(a->q, "q", n, a->q_heads, a->dim, a->q_token_stride, a->q_head_stride, es, q));
-    DC_TRY(check_tokens(a->q_out, "q_out", n, a->q_heads, a->dim, a->q_out_token_stride, a->q_out_head_stride, es, out));
-    DC_TRY(check_written("q_out", n, a->q_heads, a->dim, a->q_out_token_stride, a->q_out_head_stride));
-    const bool same = a->q == a->q_out && a->q_token_stride == a->q_out_token_stride &&
-                      a->q_head_stride == a->q_out_head_stride;
-    if (!same) {
-      DC_TRY(check_disjoint(out, q));
-      DC_TRY(check_disjoint(out, in));
-    } else {
-      // in place: heads of queries beside those of keys and values in one tensor are fine
-      const Blocks qb = token_blocks(a->q_out, n, a->q_heads, a->dim, a->q_out_token_stride, a->q_out_head_stride, es);
-      if (blocks_meet(qb, token_blocks(a->k, n, a->kv_heads, a->dim, a->k_token_stride, a->k_head_stride, es)))
-        return fail(DC_ERR_OVERLAP, "q_out overlaps k");
-      if (blocks_meet(qb, token_blocks(a->v, n, a->kv_heads, a->dim, a->v_token_stride, a->v_head_stride, es)))
-        return fail(DC_ERR_OVERLAP, "q_out overlaps v");
-      DC_TRY(check_apart(out[0], in, 2));  // (k and v are the first two)
-    }
-    DC_TRY(check_disjoint(out, cache));
-    for (const Span& c : cache) DC_TRY(check_apart(c, q));
-  }
+  Spans written;
+  DC_TRY(take_append(a, p, written));
+  if (a->tokens == 0) return ok();
   int sms = 0;
   DC_TRY(device(&sms));
-  const uint64_t e8 = static_cast<uint64_t>(es);
-  p.q = addr(a->q);
-  p.q_token = a->q_token_stride * e8;
-  p.q_head = a->q_head_stride * e8;
-  p.qo = addr(a->q_out);
-  p.qo_token = a->q_out_token_stride * e8;
-  p.qo_head = a->q_out_head_stride * e8;
-  p.k = addr(a->k);
-  p.k_token = a->k_token_stride * e8;
-  p.k_head = a->k_head_stride * e8;
-  p.v = addr(a->v);
-  p.v_token = a->v_token_stride * e8;
-  p.v_head = a->v_head_stride * e8;
-  p.positions = addr(a->positions);
-  p.seqs = addr(a->seqs);
-  p.table = addr(a->page_table);
-  p.cos_sin = addr(a->cos_sin);
-  p.tokens = n;
-  p.table_stride = a->table_rows > 1 ? a->table_stride : 0;
-  p.cos_rows = a->cos_sin_rows;
-  p.num_pages = a->num_pages;
-  p.page_size = static_cast<uint32_t>(a->page_size);
-  p.table_width = static_cast<uint32_t>(a->table_width);
-  p.num_seqs = static_cast<uint32_t>(a->table_rows);
-  p.q_heads = a->q_heads;
-  p.kv_heads = a->kv_heads;
-  p.dim = a->dim;
-  p.rot = a->rotary_dim;
-  p.interleaved = a->interleaved != 0;
   int grid = 0;
   const cudaError_t e = launch_append(p, a->dtype, sms, pdl_option(), static_cast<cudaStream_t>(stream), &grid);
+  return check_launch(e, "cache append", grid);
+}
+
+dc_status_t dc_kv_append_norm(const dc_kv_append_norm_t* a, dc_stream_t stream) {
+  read_options();
+  if (!a) return fail(DC_ERR_INVALID, "the argument block is NULL");
+  AppendParams x{};
+  Spans written, in;
+  DC_TRY(take_append(&a->append, x, written));
+  DC_TRY(check_norm(a->append.dim, a->eps));
+  const int es = a->norm_32 ? 4 : elem_bytes(a->append.dtype);
+  const uint64_t bytes = static_cast<uint64_t>(a->append.dim) * static_cast<uint64_t>(es);
+  if (a->append.q_heads) DC_TRY(take(a->q_norm, "q_norm", bytes, es, in));
+  DC_TRY(take(a->k_norm, "k_norm", bytes, es, in));
+  if (a->append.tokens == 0) return ok();
+  for (const Span& w : written) DC_TRY(check_apart(w, in));
+  int sms = 0;
+  DC_TRY(device(&sms));
+  NormParams p{};
+  p.job[0] = NormJob{{x.q, x.q_token, x.q_head}, {x.qo, x.qo_token, x.qo_head}, {}, addr(a->q_norm), 0, x.q_heads, 1, 0, 0};
+  p.job[1] = NormJob{{x.k, x.k_token, x.k_head}, {x.kc.base, 0, x.kc.head}, {}, addr(a->k_norm), 0, x.kv_heads, 1, 0, 0};
+  p.job[2] = NormJob{{x.v, x.v_token, x.v_head}, {x.vc.base, 0, x.vc.head}, {}, 0, 0, x.kv_heads, 1, 0, 0};
+  p.jobs = 3;
+  p.cached = 1;
+  p.positions = x.positions;
+  p.cos_sin = x.cos_sin;
+  p.tokens = x.tokens;
+  p.cos_rows = x.cos_rows;
+  p.seqs = x.seqs;
+  p.table = x.table;
+  p.table_stride = x.table_stride;
+  p.num_pages = x.num_pages;
+  p.page_size = x.page_size;
+  p.table_width = x.table_width;
+  p.num_seqs = x.num_seqs;
+  p.kc = x.kc;
+  p.vc = x.vc;
+  p.dim = x.dim;
+  p.rot = x.rot;
+  p.w32 = a->norm_32 != 0;
+  p.eps = a->eps;
+  plan_norm(&p, a->append.dtype, x.interleaved != 0, false);
+  int grid = 0;
+  const cudaError_t e = launch_norm(p, a->append.dtype, x.interleaved != 0, false, pdl_option(), static_cast<cudaStream_t>(stream), &grid);
   return check_launch(e, "cache append", grid);
 }
 

@@ -246,4 +246,54 @@ cudaError_t launch_linear_finish(const LinearFinishParams& p, bool pdl, cudaStre
 cudaError_t launch_linear_scale(uint64_t grad_logprobs, uint64_t grad_entropy, uint64_t tokens, bool tokens64, uint64_t rows,
                                 float inv_t, uint64_t scale, bool pdl, cudaStream_t s);
 
+// ---------------------------------------------- normed queries and keys
+// A token's heads of one kind: element d of head h of token t is at
+// base + t*token + h*head + d*element size.
+struct HeadsView {
+  uint64_t base, token, head;
+};
+
+// CTAs of a launch, by a constant: the weights' gradient is added up over them.
+constexpr int kNormThreads = 128;
+constexpr int kNormCtas = 152 * 8;
+constexpr int kNormGradCtas = 152 * 4;
+constexpr int kNormMaxDim = 512;  // at most 128 work units a head
+
+// One kind of heads: queries, keys, or values (which are copied).
+struct NormJob {
+  HeadsView x, y;              // in and out; y of keys and values is the cache where there is one
+  HeadsView dy;                // (gradient) of the output; y is that of the input
+  uint64_t w;                  // [dim], 0 for values
+  uint64_t partial;            // (gradient) f32 [CTAs][dim] or 0
+  int32_t heads, split;        // warps that share a token
+  uint32_t cta0, ctas;
+};
+
+struct NormParams {
+  NormJob job[3];
+  uint64_t positions, cos_sin; // int32 [tokens], f32 [cos_rows][rot] or 0
+  uint64_t tokens;
+  int64_t cos_rows;
+  // a cache, where keys and values go to one
+  uint64_t seqs, table;
+  int64_t table_stride, num_pages;
+  uint32_t page_size, table_width, num_seqs;
+  PagedView kc, vc;
+  int32_t jobs, cached;
+  int32_t dim, rot, w32;       // w32: the weights are binary32, else of the heads' type
+  int32_t units, lanes;        // of a head: work units, and lanes that share it (a power of two)
+  float eps;
+};
+// Fills units, lanes, split, cta0 and ctas.
+void plan_norm(NormParams* p, int dtype, bool interleaved, bool gradient);
+cudaError_t launch_norm(const NormParams& p, int dtype, bool interleaved, bool gradient, bool pdl, cudaStream_t s, int* grid);
+
+// The weights' gradients from the CTAs' parts.
+struct NormFinishParams {
+  uint64_t partial[2], out[2];  // out 0: not wanted
+  uint32_t ctas[2];
+  int32_t dim, out32;
+};
+cudaError_t launch_norm_finish(const NormFinishParams& p, int dtype, bool pdl, cudaStream_t s, int* grid);
+
 }  // namespace dc

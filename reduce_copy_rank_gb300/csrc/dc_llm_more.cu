@@ -1,6 +1,6 @@
 // dc_llm_more.cu -- the C ABI of the operators around a rollout and a training
-// step on it: log probabilities from hidden rows.  Argument checks, the cut of
-// the work, launches.
+// step on it: log probabilities from hidden rows, normed and rotated queries and
+// keys.  Argument checks, the cut of the work, launches.
 #include "dc_checks.h"
 
 namespace {
@@ -93,6 +93,94 @@ dc_status_t check_head_outputs(const Spans& out, const Head& h) {
   hidden.add(h.hidden);
   return outside_shards(out, hidden, "hidden");
 }
+
+// ------------------------------------------------- normed queries and keys ---
+struct NormShape {
+  int64_t tokens;
+  int q_heads, kv_heads, dim, rotary, dtype;
+  bool interleaved;
+};
+
+dc_status_t check_norm_shape(const NormShape& s, float eps) {
+  if (s.dtype < kBF16 || s.dtype > kF32) return fail(DC_ERR_INVALID, "dtype %d is not DC_BF16, DC_F16 or DC_F32", s.dtype);
+  const int per = 16 / elem_bytes(s.dtype);
+  DC_TRY(check_heads(s.q_heads, s.kv_heads, s.dim, true));
+  if (s.dim % per) return fail(DC_ERR_INVALID, "head dimension %d is not a multiple of %d", s.dim, per);
+  DC_TRY(check_norm(s.dim, eps));
+  if (s.rotary < 0 || s.rotary > s.dim || s.rotary % (s.interleaved ? per : 2 * per))
+    return fail(DC_ERR_INVALID, "rotary_dim = %d is not a multiple of %d up to the head dimension", s.rotary,
+                s.interleaved ? per : 2 * per);
+  if (s.tokens < 0 || s.tokens > 0x7FFFFFFF) return fail(DC_ERR_INVALID, "%lld tokens", static_cast<long long>(s.tokens));
+  return DC_OK;
+}
+
+// The positions, angles and weights of both directions.
+dc_status_t take_norm_inputs(const NormShape& s, const void* positions, const void* cos_sin, int64_t rows, const void* q_norm,
+                             const void* k_norm, bool norm_32, NormParams& p, Spans& in) {
+  DC_TRY(take(positions, "positions", static_cast<uint64_t>(s.tokens) * 4, 4, in));
+  if (s.rotary) {
+    if (rows < 1 || rows > (1ll << 40)) return fail(DC_ERR_INVALID, "cos_sin has %lld rows", static_cast<long long>(rows));
+    DC_TRY(take(cos_sin, "cos_sin", static_cast<uint64_t>(rows) * s.rotary * 4, 4, in));
+  }
+  const int es = norm_32 ? 4 : elem_bytes(s.dtype);
+  DC_TRY(take(q_norm, "q_norm", static_cast<uint64_t>(s.dim) * es, es, in));
+  DC_TRY(take(k_norm, "k_norm", static_cast<uint64_t>(s.dim) * es, es, in));
+  p.positions = addr(positions);
+  p.cos_sin = s.rotary ? addr(cos_sin) : 0;
+  p.tokens = static_cast<uint64_t>(s.tokens);
+  p.cos_rows = rows;
+  p.jobs = 2;
+  p.dim = s.dim;
+  p.rot = s.rotary;
+  p.w32 = norm_32;
+  p.job[0].w = addr(q_norm);
+  p.job[1].w = addr(k_norm);
+  p.job[0].heads = s.q_heads;
+  p.job[1].heads = s.kv_heads;
+  return DC_OK;
+}
+
+struct Heads {
+  const dc_heads_t* t;
+  const char* name;
+  int heads;
+};
+
+dc_status_t take_heads(const NormShape& s, const Heads& h, HeadsView* v, Spans& to) {
+  const uint64_t es = static_cast<uint64_t>(elem_bytes(s.dtype));
+  DC_TRY(check_tokens(h.t->data, h.name, static_cast<uint64_t>(s.tokens), h.heads, s.dim, h.t->token_stride, h.t->head_stride,
+                      static_cast<int>(es), to));
+  *v = HeadsView{addr(h.t->data), h.t->token_stride * es, h.t->head_stride * es};
+  return DC_OK;
+}
+
+Blocks heads_blocks(const NormShape& s, const Heads& h) {
+  return token_blocks(h.t->data, static_cast<uint64_t>(s.tokens), h.heads, s.dim, h.t->token_stride, h.t->head_stride,
+                      elem_bytes(s.dtype));
+}
+
+bool same_place(const Heads& a, const Heads& b) {
+  return a.t->data == b.t->data && a.t->token_stride == b.t->token_stride && a.t->head_stride == b.t->head_stride && a.heads == b.heads;
+}
+
+// The written heads fold onto neither themselves nor one another, and meet what
+// is read only where they are exactly it (out[i] and in_place[i]).
+dc_status_t check_heads_apart(const NormShape& s, const Heads* out, const Heads* in_place, int n_out, const Heads* in, int n_in) {
+  for (int i = 0; i < n_out; ++i) {
+    DC_TRY(check_written(out[i].name, static_cast<uint64_t>(s.tokens), out[i].heads, s.dim, out[i].t->token_stride,
+                         out[i].t->head_stride));
+    const Blocks b = heads_blocks(s, out[i]);
+    for (int k = i + 1; k < n_out; ++k)
+      if (blocks_meet(b, heads_blocks(s, out[k]))) return fail(DC_ERR_OVERLAP, "%s overlaps %s", out[i].name, out[k].name);
+    for (int k = 0; k < n_in; ++k) {
+      if (in[k].t == in_place[i].t && same_place(out[i], in[k])) continue;
+      if (blocks_meet(b, heads_blocks(s, in[k]))) return fail(DC_ERR_OVERLAP, "%s overlaps %s", out[i].name, in[k].name);
+    }
+  }
+  return DC_OK;
+}
+
+uint64_t norm_workspace(int dim) { return 2ull * kNormGradCtas * static_cast<uint64_t>(dim) * 4; }
 
 }  // namespace
 
@@ -316,6 +404,105 @@ dc_status_t dc_linear_logprobs_backward(const dc_linear_logprobs_backward_t* a, 
     }
   }
   return ok();
+}
+
+dc_status_t dc_qk_norm_rotate(const dc_qk_norm_rotate_t* a, dc_stream_t stream) {
+  read_options();
+  if (!a) return fail(DC_ERR_INVALID, "the argument block is NULL");
+  const NormShape s{a->tokens, a->q_heads, a->kv_heads, a->dim, a->rotary_dim, a->dtype, a->interleaved != 0};
+  DC_TRY(check_norm_shape(s, a->eps));
+  if (a->tokens == 0) return ok();
+  NormParams p{};
+  Spans in, heads, out;
+  DC_TRY(take_norm_inputs(s, a->positions, a->cos_sin, a->cos_sin_rows, a->q_norm, a->k_norm, a->norm_32 != 0, p, in));
+  const Heads x[2] = {{&a->q, "q", a->q_heads}, {&a->k, "k", a->kv_heads}};
+  const Heads y[2] = {{&a->q_out, "q_out", a->q_heads}, {&a->k_out, "k_out", a->kv_heads}};
+  for (int j = 0; j < 2; ++j) {
+    DC_TRY(take_heads(s, x[j], &p.job[j].x, heads));
+    DC_TRY(take_heads(s, y[j], &p.job[j].y, out));
+  }
+  DC_TRY(check_heads_apart(s, y, x, 2, x, 2));
+  for (const Span& o : out) DC_TRY(check_apart(o, in));
+  int sms = 0, grid = 0;
+  DC_TRY(device(&sms));
+  p.eps = a->eps;
+  plan_norm(&p, a->dtype, s.interleaved, false);
+  const cudaError_t e = launch_norm(p, a->dtype, s.interleaved, false, pdl_option(), static_cast<cudaStream_t>(stream), &grid);
+  return check_launch(e, "normed queries and keys", grid);
+}
+
+size_t dc_qk_norm_workspace_bytes(int64_t tokens, int q_heads, int kv_heads, int dim) {
+  const NormShape s{tokens, q_heads, kv_heads, dim, 0, kF32, false};
+  if (check_norm_shape(s, 0.0f) != DC_OK) return 0;
+  return static_cast<size_t>(norm_workspace(dim));
+}
+
+dc_status_t dc_qk_norm_rotate_backward(const dc_qk_norm_rotate_backward_t* a, dc_stream_t stream) {
+  read_options();
+  if (!a) return fail(DC_ERR_INVALID, "the argument block is NULL");
+  const NormShape s{a->tokens, a->q_heads, a->kv_heads, a->dim, a->rotary_dim, a->dtype, a->interleaved != 0};
+  DC_TRY(check_norm_shape(s, a->eps));
+  const int es = a->norm_32 ? 4 : elem_bytes(a->dtype);
+  const uint64_t bytes = static_cast<uint64_t>(a->dim) * static_cast<uint64_t>(es);
+  const bool sums = a->grad_q_norm || a->grad_k_norm;
+  NormParams p{};
+  Spans in, heads, out, sums_out;
+  if (a->grad_q_norm) DC_TRY(take(a->grad_q_norm, "grad_q_norm", bytes, es, sums_out));
+  if (a->grad_k_norm) DC_TRY(take(a->grad_k_norm, "grad_k_norm", bytes, es, sums_out));
+  const cudaStream_t stream_ = static_cast<cudaStream_t>(stream);
+  if (a->tokens == 0) {  // a sum over no tokens
+    DC_TRY(check_disjoint(sums_out, in));
+    if (!sums) return ok();
+    int sms = 0;
+    DC_TRY(device(&sms));
+    for (const Span& o : sums_out) {
+      const cudaError_t e = cudaMemsetAsync(reinterpret_cast<void*>(o.lo), 0, o.hi - o.lo, stream_);
+      if (e != cudaSuccess) {
+        cudaGetLastError();
+        return fail(DC_ERR_CUDA, "clearing %s failed: %s", o.name, cudaGetErrorString(e));
+      }
+    }
+    return ok();
+  }
+  DC_TRY(take_norm_inputs(s, a->positions, a->cos_sin, a->cos_sin_rows, a->q_norm, a->k_norm, a->norm_32 != 0, p, in));
+  const Heads x[4] = {{&a->grad_q_out, "grad_q_out", a->q_heads}, {&a->grad_k_out, "grad_k_out", a->kv_heads},
+                      {&a->q, "q", a->q_heads}, {&a->k, "k", a->kv_heads}};
+  const Heads y[2] = {{&a->grad_q, "grad_q", a->q_heads}, {&a->grad_k, "grad_k", a->kv_heads}};
+  for (int j = 0; j < 2; ++j) {
+    DC_TRY(take_heads(s, x[j], &p.job[j].dy, heads));
+    DC_TRY(take_heads(s, x[j + 2], &p.job[j].x, heads));
+    DC_TRY(take_heads(s, y[j], &p.job[j].y, out));
+  }
+  DC_TRY(check_heads_apart(s, y, x, 2, x, 4));
+  for (const Span& o : out) DC_TRY(check_apart(o, in));
+  if (sums) {
+    if (a->workspace_bytes < norm_workspace(a->dim))
+      return fail(DC_ERR_INVALID, "the workspace holds %llu bytes; dc_qk_norm_workspace_bytes says %llu",
+                  static_cast<unsigned long long>(a->workspace_bytes), static_cast<unsigned long long>(norm_workspace(a->dim)));
+    DC_TRY(take(a->workspace, "workspace", a->workspace_bytes, 16, sums_out));
+    p.job[0].partial = a->grad_q_norm ? addr(a->workspace) : 0;
+    p.job[1].partial = a->grad_k_norm ? addr(a->workspace) + norm_workspace(a->dim) / 2 : 0;
+  }
+  DC_TRY(check_disjoint(sums_out, in));
+  DC_TRY(check_disjoint(sums_out, heads));
+  DC_TRY(check_disjoint(sums_out, out));
+  int sms = 0, grid = 0;
+  DC_TRY(device(&sms));
+  p.eps = a->eps;
+  plan_norm(&p, a->dtype, s.interleaved, true);
+  cudaError_t e = launch_norm(p, a->dtype, s.interleaved, true, pdl_option(), stream_, &grid);
+  DC_TRY(check_launch(e, "normed queries' and keys' gradient", grid));
+  if (!sums) return ok();
+  NormFinishParams f{};
+  f.dim = a->dim;
+  f.out32 = a->norm_32 != 0;
+  for (int j = 0; j < 2; ++j) {
+    f.partial[j] = p.job[j].partial;
+    f.ctas[j] = p.job[j].ctas;
+    f.out[j] = addr(j ? a->grad_k_norm : a->grad_q_norm);
+  }
+  e = launch_norm_finish(f, a->dtype, pdl_option(), stream_, &grid);
+  return check_launch(e, "normed queries' and keys' gradient", grid);
 }
 
 }  // extern "C"

@@ -60,9 +60,23 @@ _LINEAR_GRAD = _Block("16Q3qd4i", _HEAD + "lse entropy grad_logprobs grad_entrop
                       "grad_weight_row_strides workspace workspace_bytes hidden_row_stride grad_hidden_row_stride rows "
                       "hidden_size vocab temperature ranks dtype tokens_64 reserved")
 
+_APPEND_NORM = _Block("24Q6q8i2Qfi", " ".join(_APPEND.names) + " q_norm k_norm eps norm_32")
+
+
+def _heads(*names):
+    return " ".join(f"{n} {n}_token_stride {n}_head_stride" for n in names)
+
+
+_NORM = _Block("16Q2q7if", _heads("q", "k", "q_out", "k_out") + " positions cos_sin q_norm k_norm tokens cos_sin_rows q_heads "
+               "kv_heads dim rotary_dim interleaved dtype norm_32 eps")
+_NORM_GRAD = _Block("26Q2q7if", _heads("q", "k", "grad_q_out", "grad_k_out", "grad_q", "grad_k") + " positions cos_sin q_norm "
+                    "k_norm grad_q_norm grad_k_norm workspace workspace_bytes tokens cos_sin_rows q_heads kv_heads dim "
+                    "rotary_dim interleaved dtype norm_32 eps")
+
 # the entry points, as the extension module takes them
 _ENTRIES = ("dc_token_logprobs", "dc_token_logprobs_backward", "dc_kv_append", "dc_paged_attention",
-            "dc_linear_logprobs", "dc_linear_logprobs_backward")
+            "dc_linear_logprobs", "dc_linear_logprobs_backward", "dc_kv_append_norm", "dc_qk_norm_rotate",
+            "dc_qk_norm_rotate_backward")
 
 _bound = None
 
@@ -78,6 +92,8 @@ def _lib():
         L.dc_attention_workspace_bytes.argtypes = [ctypes.c_int64, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                                    ctypes.c_int64]
         L.dc_attention_workspace_bytes.restype = ctypes.c_size_t
+        L.dc_qk_norm_workspace_bytes.argtypes = [ctypes.c_int64, ctypes.c_int, ctypes.c_int, ctypes.c_int]
+        L.dc_qk_norm_workspace_bytes.restype = ctypes.c_size_t
         L.dc_linear_logprobs_workspace_bytes.argtypes = [ctypes.c_int64] * 3 + [ctypes.c_int]
         L.dc_linear_logprobs_workspace_bytes.restype = ctypes.c_size_t
         _bound = L
@@ -134,6 +150,22 @@ def dc_linear_logprobs_backward(stream: int = 0, **fields) -> int:
 
 def dc_linear_logprobs_workspace_bytes(rows: int, hidden_size: int, columns: int, backward: bool) -> int:
     return int(_lib().dc_linear_logprobs_workspace_bytes(rows, hidden_size, columns, int(backward)))
+
+
+def dc_kv_append_norm(stream: int = 0, **fields) -> int:
+    return _lib().dc_kv_append_norm(_APPEND_NORM.of(fields), stream)
+
+
+def dc_qk_norm_rotate(stream: int = 0, **fields) -> int:
+    return _lib().dc_qk_norm_rotate(_NORM.of(fields), stream)
+
+
+def dc_qk_norm_rotate_backward(stream: int = 0, **fields) -> int:
+    return _lib().dc_qk_norm_rotate_backward(_NORM_GRAD.of(fields), stream)
+
+
+def dc_qk_norm_workspace_bytes(tokens: int, q_heads: int, kv_heads: int, dim: int) -> int:
+    return int(_lib().dc_qk_norm_workspace_bytes(tokens, q_heads, kv_heads, dim))
 
 
 # ------------------------------------------------------------ tensor API ---
@@ -383,7 +415,7 @@ def _first_derivative(name: str):
 # ------------------------------------------------------------ paged cache ---
 
 def kv_append(k, v, positions, seqs, page_table, k_cache, v_cache, q=None, q_out=None, cos_sin=None,
-              interleaved: bool = False, stream=None):
+              interleaved: bool = False, stream=None, q_norm=None, k_norm=None, eps: float = 1e-6):
     """Puts the keys and values of new tokens ([tokens, kv_heads, dim]) into a
     paged cache ([pages, page_size, kv_heads, dim] tensors, or views of that
     shape with any strides), rotating the keys, and the queries ``q`` into
@@ -397,14 +429,109 @@ def kv_append(k, v, positions, seqs, page_table, k_cache, v_cache, q=None, q_out
     elements j and j + rotary_dim/2, or 2j and 2j + 1 if ``interleaved``;
     elements past rotary_dim stay.
 
+    ``k_norm`` (and ``q_norm`` where there are queries; [dim], float32 or the
+    heads' type): keys and queries are normed per head before they are rotated,
+    ``x * w / sqrt(mean(x * x) + eps)`` (dim up to 512).
+
     A negative position is padding and writes nothing.  A token whose
     sequence, position or page does not exist writes no cache; its queries
     become NaN.  Returns ``q_out``."""
-    status = (_module or _binding()).kv_append(k, v, positions, seqs, page_table, k_cache, v_cache, q, q_out, cos_sin,
-                                               interleaved, stream)
+    if q_norm is None and k_norm is None:
+        status = (_module or _binding()).kv_append(k, v, positions, seqs, page_table, k_cache, v_cache, q, q_out, cos_sin,
+                                                   interleaved, stream)
+    else:
+        status = (_module or _binding()).kv_append_norm(k, v, positions, seqs, page_table, k_cache, v_cache, q, q_out,
+                                                        cos_sin, interleaved, stream, q_norm, k_norm, eps)
     if status:
         _dc._check(status)
     return q_out
+
+
+def qk_norm_rotate(q, k, positions, cos_sin, q_norm, k_norm, q_out, k_out, eps: float = 1e-6, interleaved: bool = False,
+                   stream=None):
+    """The queries and keys ([tokens, heads, dim]; bfloat16, float16 or
+    float32) of a training step, normed per head and rotated to ``positions``
+    (int32 [tokens]) into ``q_out`` and ``k_out``, with the bits that
+    :func:`kv_append` gives with ``q_norm`` and ``k_norm``; ``cos_sin`` and
+    ``interleaved`` as there, dim up to 512.
+
+    A negative position is padding: its rows are 0.  A position past
+    ``cos_sin`` gives NaN.  Returns ``(q_out, k_out)``, which may be exactly
+    ``q`` and ``k``."""
+    status = (_module or _binding()).qk_norm_rotate(q, k, positions, cos_sin, q_norm, k_norm, q_out, k_out, eps, interleaved,
+                                                    stream)
+    if status:
+        _dc._check(status)
+    return q_out, k_out
+
+
+def qk_norm_workspace(tokens: int, q_heads: int, kv_heads: int, dim: int, device=None):
+    """A workspace tensor for :func:`qk_norm_rotate_backward`; its contents do
+    not matter, and calls that may run at the same time need one each."""
+    import torch
+
+    n = dc_qk_norm_workspace_bytes(tokens, q_heads, kv_heads, dim)
+    if n == 0:
+        raise _dc.DCError(1, _dc.last_error() or "no such heads")
+    return torch.empty(n, dtype=torch.uint8, device=device if device is not None else "cuda")
+
+
+def qk_norm_rotate_backward(q, k, positions, cos_sin, q_norm, k_norm, grad_q_out, grad_k_out, grad_q, grad_k,
+                            grad_q_norm=None, grad_k_norm=None, workspace=None, eps: float = 1e-6,
+                            interleaved: bool = False, stream=None):
+    """The gradient of :func:`qk_norm_rotate`: ``grad_q`` and ``grad_k``
+    (which may be exactly ``grad_q_out`` and ``grad_k_out``), and, where given,
+    those of the weights (typed as the weights; they need ``workspace``:
+    :func:`qk_norm_workspace`), summed in binary32 in one fixed order.
+    Padding has no gradient.  Returns ``(grad_q, grad_k)``."""
+    status = (_module or _binding()).qk_norm_rotate_backward(q, k, positions, cos_sin, q_norm, k_norm, grad_q_out, grad_k_out,
+                                                             grad_q, grad_k, grad_q_norm, grad_k_norm, workspace, eps,
+                                                             interleaved, stream)
+    if status:
+        _dc._check(status)
+    return grad_q, grad_k
+
+
+_norm_function = None
+
+
+def normed_queries_and_keys(q, k, positions, cos_sin, q_norm, k_norm, eps: float = 1e-6, interleaved: bool = False):
+    """``(q_out, k_out)`` of :func:`qk_norm_rotate` as new tensors that
+    autograd differentiates with respect to ``q``, ``k``, ``q_norm`` and
+    ``k_norm`` (through :func:`qk_norm_rotate_backward`), once: a second
+    derivative raises."""
+    global _norm_function
+    import torch
+
+    if _norm_function is None:
+        class NormRotate(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, q, k, q_norm, k_norm, positions, cos_sin, eps, interleaved):
+                outs = [torch.empty_like(t, memory_format=torch.contiguous_format) for t in (q, k)]
+                qk_norm_rotate(q, k, positions, cos_sin, q_norm, k_norm, *outs, eps=eps, interleaved=interleaved)
+                ctx.save_for_backward(q, k, q_norm, k_norm, positions, *([] if cos_sin is None else [cos_sin]))
+                ctx.eps, ctx.interleaved = eps, interleaved
+                return tuple(outs)
+
+            @staticmethod
+            def backward(ctx, gq, gk):
+                q, k, q_norm, k_norm, positions, *rest = ctx.saved_tensors
+                cos_sin = rest[0] if rest else None
+                # upstream gradients may be broadcast, or laid out in a way that the kernel does not read
+                gq, gk = (g.to(t.dtype).contiguous() for g, t in zip((gq, gk), (q, k)))
+                grads = [torch.empty_like(t, memory_format=torch.contiguous_format) for t in (q, k)]
+                want = any(ctx.needs_input_grad[2:4])
+                sums = [torch.empty_like(t, memory_format=torch.contiguous_format) for t in (q_norm, k_norm)] if want else [None] * 2
+                ws = qk_norm_workspace(q.shape[0], q.shape[1], k.shape[1], q.shape[2], q.device) if want else None
+                qk_norm_rotate_backward(q, k, positions, cos_sin, q_norm, k_norm, gq, gk, *grads, *sums, workspace=ws,
+                                        eps=ctx.eps, interleaved=ctx.interleaved)
+                out = [g for g in (*grads, *sums) if g is not None]
+                if torch.is_grad_enabled():  # create_graph: the gradients leave a kernel, no graph holds them
+                    out = list(_first_derivative("normed_queries_and_keys").apply(len(out), *out, q, k, q_norm, k_norm, gq, gk))
+                return (*out, *(() if want else (None, None)), None, None, None, None)
+
+        _norm_function = NormRotate
+    return _norm_function.apply(q, k, q_norm, k_norm, positions, cos_sin, eps, interleaved)
 
 
 def attention_workspace(seqs: int, q_heads: int, kv_heads: int, dim: int, max_tokens: int, device=None):
