@@ -713,6 +713,39 @@ dc_status_t dc_paged_attention(const dc_paged_attention_t *args, dc_stream_t str
 size_t dc_attention_workspace_bytes(int64_t seqs, int q_heads, int kv_heads, int dim, int64_t max_tokens);
 
 /*
+ * dc_prefix_attention -- dc_paged_attention of sequences that share prefixes:
+ * the `seqs` sequences are `prefixes` groups of seqs / prefixes neighbours, and
+ * sequence b attends to the first prefix_lengths[g] tokens of its group's row g
+ * of prefix_table, then to its own lengths[b] tokens of page_table, under one
+ * softmax.  A prefix's keys and values are read once for its whole group.
+ *
+ * own: the arguments of dc_paged_attention (no window); prefix_table int32
+ * [prefixes, prefix_table_width], pages of the same caches.  Either part may be
+ * empty, or both (zeros and lse = -inf).  A page outside the cache, or a length
+ * past its table, gives NaN in the sequences that it belongs to.
+ * The prefix's weights are rounded to 16 bits before they meet the values (half
+ * a step each, of either sign), everything else as in dc_paged_attention; an
+ * infinite value gives infinities or NaN.
+ * A sequence's bits depend on its own tokens and its prefix's, not on the other
+ * sequences or prefixes.
+ * own.workspace: dc_prefix_attention_workspace_bytes(seqs, prefixes, q_heads,
+ * kv_heads, dim, max_prefix_tokens, max_tokens) bytes (widths of the tables
+ * times the page size), 16-byte aligned, zero before its first use; each call
+ * leaves it ready for the next of these sizes.  One per stream.  Three kernels.
+ */
+typedef struct {
+    dc_paged_attention_t own;
+    const int32_t *prefix_table;
+    const int32_t *prefix_lengths;
+    int64_t prefixes;
+    int64_t prefix_table_width, prefix_table_stride;
+} dc_prefix_attention_t;
+dc_status_t dc_prefix_attention(const dc_prefix_attention_t *args, dc_stream_t stream);
+/* 0 if the arguments are not supported. */
+size_t dc_prefix_attention_workspace_bytes(int64_t seqs, int64_t prefixes, int q_heads, int kv_heads, int dim,
+                                           int64_t max_prefix_tokens, int64_t max_tokens);
+
+/*
  * dc_check_device -- reports the faults that this library's kernels recorded
  * on the current device since the last check, and clears them.
  *

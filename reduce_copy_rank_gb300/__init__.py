@@ -30,6 +30,7 @@ __all__ = [
     "token_logprobs", "token_logprobs_backward", "logprobs_and_entropy", "kv_append", "paged_attention",
     "attention_workspace", "linear_logprobs", "linear_logprobs_backward", "linear_logprobs_and_entropy",
     "linear_logprobs_workspace", "qk_norm_rotate", "qk_norm_rotate_backward", "qk_norm_workspace", "normed_queries_and_keys",
+    "prefix_attention", "prefix_attention_workspace",
     "set_option",
     "get_option",
     "launch_count", "last_grid", "last_error", "options", "lib", "LIB_PATH", "STATUS", "DTYPES", "ORDERS",
@@ -620,8 +621,9 @@ def last_error() -> str:
 # ------------------------------------------ operators of language models ---
 from .operators import (  # noqa: E402  (they use the binding above)
     attention_workspace, dc_attention_workspace_bytes, dc_kv_append, dc_kv_append_norm, dc_linear_logprobs,
-    dc_linear_logprobs_backward, dc_linear_logprobs_workspace_bytes, dc_paged_attention, dc_qk_norm_rotate,
-    dc_qk_norm_rotate_backward, dc_qk_norm_workspace_bytes, dc_token_logprobs, dc_token_logprobs_backward, kv_append,
-    linear_logprobs, linear_logprobs_and_entropy, linear_logprobs_backward, linear_logprobs_workspace, logprobs_and_entropy,
-    normed_queries_and_keys, paged_attention, qk_norm_rotate, qk_norm_rotate_backward, qk_norm_workspace, token_logprobs,
-    token_logprobs_backward)
+    dc_linear_logprobs_backward, dc_linear_logprobs_workspace_bytes, dc_paged_attention, dc_prefix_attention,
+    dc_prefix_attention_workspace_bytes, dc_qk_norm_rotate, dc_qk_norm_rotate_backward, dc_qk_norm_workspace_bytes,
+    dc_token_logprobs, dc_token_logprobs_backward, kv_append, linear_logprobs, linear_logprobs_and_entropy,
+    linear_logprobs_backward, linear_logprobs_workspace, logprobs_and_entropy, normed_queries_and_keys, paged_attention,
+    prefix_attention, prefix_attention_workspace, qk_norm_rotate, qk_norm_rotate_backward, qk_norm_workspace,
+    token_logprobs, token_logprobs_backward)

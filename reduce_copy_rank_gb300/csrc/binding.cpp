@@ -30,6 +30,7 @@ decltype(&dc_linear_logprobs_backward) g_linear_grad = nullptr;
 decltype(&dc_kv_append_norm) g_append_norm = nullptr;
 decltype(&dc_qk_norm_rotate) g_norm = nullptr;
 decltype(&dc_qk_norm_rotate_backward) g_norm_grad = nullptr;
+decltype(&dc_prefix_attention) g_prefix = nullptr;
 
 // A refusal: the Python exception is set.
 struct Refused {};
@@ -349,11 +350,11 @@ Caches caches(const Call& c, PyObject* ko, PyObject* vo, int64_t heads, int64_t 
   return r;
 }
 
-const at::Tensor& page_table(const Call& c, PyObject* o, int64_t rows) {
-  const at::Tensor& t = on(c, o, "page_table", at::kInt);
+const at::Tensor& page_table(const Call& c, PyObject* o, int64_t rows, const char* what = "page_table") {
+  const at::Tensor& t = on(c, o, what, at::kInt);
   if (t.dim() != 2 || (rows >= 0 && t.size(0) != rows))
-    wrong("page_table has shape " + text(t) + ", expected (" + (rows < 0 ? "sequences" : std::to_string(rows)) + ", pages)");
-  if (t.stride(1) != 1 && t.size(1) > 1) wrong("page_table: rows must be contiguous");
+    wrong(std::string(what) + " has shape " + text(t) + ", expected (" + (rows < 0 ? "sequences" : std::to_string(rows)) + ", pages)");
+  if (t.stride(1) != 1 && t.size(1) > 1) wrong(std::string(what) + ": rows must be contiguous");
   return t;
 }
 
@@ -533,9 +534,8 @@ PyObject* norm_grad(PyObject* const* a) {
   return w.after(g_norm_grad(&b, s.call.stream));
 }
 
-// paged_attention(q, k_cache, v_cache, page_table, lengths, out, workspace,
-//                 scale, window, lse, stream) -> status
-PyObject* attend(PyObject* const* a) {
+// The arguments of paged_attention, in their order.
+Call fill_attend(PyObject* const* a, dc_paged_attention_t& b, Written& w) {
   const at::Tensor& first = tensor(a[0], "q");
   const at::ScalarType type = first.scalar_type();
   const int code = code_of(type);
@@ -543,8 +543,6 @@ PyObject* attend(PyObject* const* a) {
   const Call c = call_of(first, a[10]);
   if (first.dim() != 3) wrong("q has shape " + text(first) + ", expected (sequences, heads, dim)");
   const int64_t n = first.size(0), hq = first.size(1), d = first.size(2);
-  Written w;
-  dc_paged_attention_t b{};
   b.q = heads_of(c, a[0], "q", n, hq, d, type, b.q_seq_stride, b.q_head_stride).const_data_ptr();
   b.out = w(heads_of(c, a[5], "out", n, hq, d, type, b.out_seq_stride, b.out_head_stride)).mutable_data_ptr();
   const Caches x = caches(c, a[1], a[2], -1, d, type, nullptr, b.k_cache, b.v_cache);
@@ -574,7 +572,31 @@ PyObject* attend(PyObject* const* a) {
   b.window = small(a[8], "window");
   b.dtype = code;
   b.scale = a[7] == Py_None ? static_cast<float>(1.0 / std::sqrt(static_cast<double>(d))) : static_cast<float>(number(a[7]));
+  return c;
+}
+
+// paged_attention(q, k_cache, v_cache, page_table, lengths, out, workspace,
+//                 scale, window, lse, stream) -> status
+PyObject* attend(PyObject* const* a) {
+  Written w;
+  dc_paged_attention_t b{};
+  const Call c = fill_attend(a, b, w);
   return w.after(g_attend(&b, c.stream));
+}
+
+// prefix_attention(the arguments of paged_attention, then prefix_table,
+//                  prefix_lengths) -> status
+PyObject* prefix(PyObject* const* a) {
+  Written w;
+  dc_prefix_attention_t b{};
+  const Call c = fill_attend(a, b.own, w);
+  const at::Tensor& table = page_table(c, a[11], -1, "prefix_table");
+  b.prefix_table = static_cast<const int32_t*>(table.const_data_ptr());
+  b.prefixes = table.size(0);
+  b.prefix_table_width = table.size(1);
+  b.prefix_table_stride = table.stride(0);
+  b.prefix_lengths = static_cast<const int32_t*>(vector(c, a[12], "prefix_lengths", b.prefixes, at::kInt));
+  return w.after(g_prefix(&b, c.stream));
 }
 
 // A head: hidden [rows, size] and its shards [columns, size].
@@ -722,6 +744,7 @@ PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
       reinterpret_cast<void**>(&g_score), reinterpret_cast<void**>(&g_grad), reinterpret_cast<void**>(&g_append),
       reinterpret_cast<void**>(&g_attend), reinterpret_cast<void**>(&g_linear), reinterpret_cast<void**>(&g_linear_grad),
       reinterpret_cast<void**>(&g_append_norm), reinterpret_cast<void**>(&g_norm), reinterpret_cast<void**>(&g_norm_grad),
+      reinterpret_cast<void**>(&g_prefix),
   };
   constexpr Py_ssize_t count = sizeof to / sizeof to[0];
   if (n != count) {
@@ -751,6 +774,7 @@ PyMethodDef kMethods[] = {
     {"kv_append_norm", as_function(&entry<append_norm, 15>), METH_FASTCALL, nullptr},
     {"qk_norm_rotate", as_function(&entry<norm, 11>), METH_FASTCALL, nullptr},
     {"qk_norm_rotate_backward", as_function(&entry<norm_grad, 16>), METH_FASTCALL, nullptr},
+    {"prefix_attention", as_function(&entry<prefix, 13>), METH_FASTCALL, nullptr},
     {"linear_logprobs", as_function(&entry<linear, 10>), METH_FASTCALL, nullptr},
     {"linear_logprobs_backward", as_function(&entry<linear_grad, 13>), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},

@@ -1291,20 +1291,21 @@ dc_status_t dc_fused_reset(void* workspace, int P, dc_stream_t stream) {
 
 dc_status_t dc_check_device(void) {
   read_env_once();
-  uint32_t bits = 0, tensor = 0, fused[4] = {0, 0, 0, 0};
+  uint32_t bits = 0, tensor = 0, prefix = 0, fused[4] = {0, 0, 0, 0};
   cudaError_t e = take_bulk_faults(&bits);
   if (e == cudaSuccess) e = take_fused_faults(fused);
   if (e == cudaSuccess) e = take_linear_faults(&tensor);
+  if (e == cudaSuccess) e = take_prefix_faults(&prefix);
   // bounds-check records of the checked build (empty in the normal build)
   static cudaError_t (*const kReaders[kBoundsReaders])(BoundsFault*) = {
       take_bounds_gather, take_bounds_bulk, take_bounds_fused,
       take_bounds_reduce_bf16, take_bounds_reduce_f16, take_bounds_reduce_f32,
       take_bounds_logprobs, take_bounds_append, take_bounds_attention, take_bounds_linear,
-      take_bounds_norm};
+      take_bounds_norm, take_bounds_prefix};
   static const char* const kFiles[kBoundsReaders] = {"dc_gather.cu", "dc_bulk.cu", "dc_fused.cu",
                                                      "dc_reduce_bf16.cu", "dc_reduce_f16.cu", "dc_reduce_f32.cu",
                                                      "dc_logprobs.cu", "dc_kv_append.cu", "dc_attention.cu",
-                                                     "dc_linear.cu", "dc_qk_norm.cu"};
+                                                     "dc_linear.cu", "dc_qk_norm.cu", "dc_prefix.cu"};
   BoundsFault first{};
   int first_file = -1;
   unsigned long long outside = 0;
@@ -1339,10 +1340,10 @@ dc_status_t dc_check_device(void) {
     return fail(DC_ERR_TIMEOUT,
                 "a bulk-copy all-gather gave up waiting for its loads after wait_limit_ns; "
                 "its output is incomplete");
-  if (tensor & kFaultTensorWait)
+  if ((tensor | prefix) & kFaultTensorWait)
     return fail(DC_ERR_TIMEOUT,
-                "a matrix product of the language-model operators gave up waiting for its operands after "
-                "wait_limit_ns; its output is incomplete");
+                "%s gave up waiting for a matrix product's operands after wait_limit_ns; its output is incomplete",
+                tensor ? "a linear head's log probabilities or gradient" : "an attention to shared prefixes");
   return ok();
 }
 

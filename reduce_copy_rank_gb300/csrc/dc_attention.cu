@@ -253,6 +253,14 @@ __device__ __forceinline__ void st_piece(const Pieces& w, uint32_t piece, uint32
 template <int DT, int D>
 __device__ __forceinline__ void st_result(const AttendParams& p, int seq, int head, int d, const float4& v, float ref,
                                           float l) {
+  if (p.raw) {  // to be joined with a prefix's part
+    const uint64_t i = static_cast<uint64_t>(seq) * p.q_heads + head, n = static_cast<uint64_t>(p.seqs) * p.q_heads;
+    float4* a = reinterpret_cast<float4*>(p.raw + (i * D + d) * 4);
+    if (in_bounds(a, 16, p.raw, p.raw + n * D * 4, kSitePartial)) *a = v;
+    float2* b = reinterpret_cast<float2*>(p.raw_rl) + i;
+    if (d == 0 && in_bounds(b, 8, p.raw_rl, p.raw_rl + n * 8, kSitePartial)) *b = make_float2(ref, l);
+    return;
+  }
   const float inv = 1.0f / l;
   const uint64_t row = p.out + static_cast<uint64_t>(seq) * p.out_seq + static_cast<uint64_t>(head) * p.out_head;
   st_pair<DT>(row + d * 2, v.x * inv, v.y * inv, row, row + D * 2);
@@ -326,7 +334,10 @@ __global__ __launch_bounds__(Shape<D, HB, APART>::kThreads, Shape<D, HB, APART>:
   const uint32_t pieces = attend_pieces(n, level);
   const bool in_cluster = p.cluster > 1 && pieces > 1;  // the unit's CTAs are one cluster
   if (piece >= pieces) {
-    if (piece == 0) {  // nothing to attend to: zeros
+    if (piece == 0 && p.raw) {
+      for (int i = threadIdx.x; i < nh * (D / 4); i += kThreads)
+        st_result<DT, D>(p, seq, h0 + i / (D / 4), i % (D / 4) * 4, make_float4(0.0f, 0.0f, 0.0f, 0.0f), neg_inf(), 0.0f);
+    } else if (piece == 0) {  // nothing to attend to: zeros
       for (int i = threadIdx.x; i < nh * (D / 2); i += kThreads) {
         const uint64_t row = p.out + static_cast<uint64_t>(seq) * p.out_seq +
                              static_cast<uint64_t>(h0 + i / (D / 2)) * p.out_head;

@@ -291,7 +291,7 @@ cudaError_t take_bulk_faults(uint32_t* bits);
 // returns an empty one in the normal build.  bounds_file names the file of
 // reader i (i < kBoundsReaders).
 struct BoundsFault;
-constexpr int kBoundsReaders = 11;
+constexpr int kBoundsReaders = 12;
 cudaError_t take_bounds_gather(BoundsFault* f);
 cudaError_t take_bounds_bulk(BoundsFault* f);
 cudaError_t take_bounds_fused(BoundsFault* f);
@@ -303,8 +303,11 @@ cudaError_t take_bounds_append(BoundsFault* f);
 cudaError_t take_bounds_attention(BoundsFault* f);
 cudaError_t take_bounds_linear(BoundsFault* f);
 cudaError_t take_bounds_norm(BoundsFault* f);
-// Reads and clears the fault bits of the tensor-core products (dc_linear.cu).
+cudaError_t take_bounds_prefix(BoundsFault* f);
+// Reads and clears the fault bits of the tensor-core products (dc_linear.cu,
+// dc_prefix.cu).
 cudaError_t take_linear_faults(uint32_t* bits);
+cudaError_t take_prefix_faults(uint32_t* bits);
 bool bounds_checked_build();
 
 // One-thread delay of `ns` nanoseconds of the global timer (rank-skew

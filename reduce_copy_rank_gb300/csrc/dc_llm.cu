@@ -140,6 +140,118 @@ dc_status_t take_append(const dc_kv_append_t* a, AppendParams& p, Spans& written
   return DC_OK;
 }
 
+// Checks the arguments of an attention (of at least one sequence); `in` and
+// `out` get what it reads and writes.
+dc_status_t take_attend(const dc_paged_attention_t* a, AttendParams& p, AttendPlan& plan, Spans& in, Spans& out) {
+  if (a->dtype != kBF16 && a->dtype != kF16) return fail(DC_ERR_INVALID, "dtype %d is not DC_BF16 or DC_F16", a->dtype);
+  if (a->page_size < 1) return fail(DC_ERR_INVALID, "page_size = %d is not positive", a->page_size);
+  if (a->window < 0) return fail(DC_ERR_INVALID, "window = %d is negative", a->window);
+  if (!std::isfinite(a->scale)) return fail(DC_ERR_INVALID, "scale is not finite");
+  if (a->seqs == 0) return DC_OK;
+  DC_TRY(check_table(a->page_table, a->seqs, a->table_width, a->table_stride, in));
+  uint64_t most = static_cast<uint64_t>(a->table_width) * static_cast<uint64_t>(a->page_size);
+  if (a->window > 0) most = std::min<uint64_t>(most, static_cast<uint64_t>(a->window));
+  DC_TRY(plan_attend(a->seqs, a->q_heads, a->kv_heads, a->dim, most, &plan));
+  const uint64_t n = static_cast<uint64_t>(a->seqs);
+  DC_TRY(check_tokens(a->q, "q", n, a->q_heads, a->dim, a->q_seq_stride, a->q_head_stride, 2, in));
+  DC_TRY(take(a->lengths, "lengths", n * 4, 4, in));
+  DC_TRY(check_cache(a->k_cache, "k_cache", a->num_pages, a->page_size, a->kv_heads, a->dim, 2, false, &p.kc, in));
+  DC_TRY(check_cache(a->v_cache, "v_cache", a->num_pages, a->page_size, a->kv_heads, a->dim, 2, false, &p.vc, in));
+  DC_TRY(check_tokens(a->out, "out", n, a->q_heads, a->dim, a->out_seq_stride, a->out_head_stride, 2, out));
+  DC_TRY(check_written("out", n, a->q_heads, a->dim, a->out_seq_stride, a->out_head_stride));
+  if (a->lse) DC_TRY(take(a->lse, "lse", n * static_cast<uint64_t>(a->q_heads) * 4, 4, out));
+  if (plan.partial_bytes) {  // the counters, then the pieces' partial results
+    if (kAttendCounterBytes + plan.partial_bytes > a->workspace_bytes)
+      return fail(DC_ERR_INVALID, "the workspace holds %llu bytes; dc_attention_workspace_bytes says %llu",
+                  static_cast<unsigned long long>(a->workspace_bytes),
+                  static_cast<unsigned long long>(dc_attention_workspace_bytes(
+                      a->seqs, a->q_heads, a->kv_heads, a->dim, static_cast<int64_t>(most))));
+    DC_TRY(take(a->workspace, "workspace", a->workspace_bytes, 16, out));
+  }
+  DC_TRY(check_disjoint(out, in));
+  p.q = addr(a->q);
+  p.q_seq = a->q_seq_stride * 2;
+  p.q_head = a->q_head_stride * 2;
+  p.out = addr(a->out);
+  p.out_seq = a->out_seq_stride * 2;
+  p.out_head = a->out_head_stride * 2;
+  p.lse = addr(a->lse);
+  p.table = addr(a->page_table);
+  p.lengths = addr(a->lengths);
+  p.counters = addr(a->workspace);
+  p.partial = addr(a->workspace) + kAttendCounterBytes;
+  p.table_stride = a->seqs > 1 ? a->table_stride : 0;
+  p.num_pages = a->num_pages;
+  p.page_size = static_cast<uint32_t>(a->page_size);
+  p.table_width = static_cast<uint32_t>(a->table_width);
+  p.seqs = static_cast<int32_t>(a->seqs);
+  p.q_heads = a->q_heads;
+  p.kv_heads = a->kv_heads;
+  p.group = a->q_heads / a->kv_heads;
+  p.head_blocks = plan.head_blocks;
+  p.hb = plan.hb;
+  p.window = a->window;
+  p.units = static_cast<int32_t>(plan.units);
+  p.pieces = static_cast<int32_t>(plan.pieces);
+  p.page_shift = (p.page_size & (p.page_size - 1)) == 0 ? __builtin_ctz(p.page_size) : -1;
+  p.scale = a->scale;
+  return DC_OK;
+}
+
+// The last choices, which need the GPU's size, and the launch.
+dc_status_t run_attend(AttendParams& p, const AttendPlan& plan, int dtype, int dim, int sms, dc_stream_t stream) {
+  // Few CTAs, all resident at once, and few enough pieces: a unit's CTAs are a
+  // cluster and join them in shared memory.  Measured, us, workspace / cluster:
+  // one sequence of 1025 tokens, 8/1 heads of 128 (5 pieces): 8.2 / 6.9; of 4096
+  // (16 pieces, two clusters and the workspace): 8.1 / 10.
+  const uint32_t resident = static_cast<uint32_t>(sms) * (dim <= 128 ? 2u : 1u);
+  const uint32_t c = plan.pieces > 4 ? 8u : plan.pieces > 2 ? 4u : 2u;
+  const bool cluster = plan.pieces > 1 && plan.pieces <= c && plan.units * c <= resident;
+  p.cluster = cluster ? static_cast<int32_t>(c) : 1;
+  p.places = cluster ? static_cast<int32_t>(c) : p.pieces;
+  // A table with room for much longer sequences than most are must not flood
+  // the GPU with CTAs that find nothing to do (about 0.5 us each, two at a time
+  // on an SM): beyond four times the CTAs that fill it, a unit's take turns.
+  if (!cluster && plan.pieces > 8 && plan.units * plan.pieces > 4 * kAttendCtas)
+    p.places = static_cast<int32_t>(std::max<uint64_t>(8, std::min<uint64_t>(plan.pieces, 4 * kAttendCtas / plan.units)));
+  // more units than the counters have room for (29127 at least): a CTA each
+  if (!cluster && plan.pieces > 1 && plan.units * attend_counters(plan.pieces) * 4 > kAttendCounterBytes) p.places = 1;
+  int grid = 0;
+  const cudaError_t e = launch_attend(p, dtype, dim, pdl_option(), static_cast<cudaStream_t>(stream), &grid);
+  return check_launch(e, "paged attention", grid);
+}
+
+// Where the parts of an attention to shared prefixes lie in its workspace,
+// behind the one of paged attention.
+struct PrefixSizes {
+  uint64_t raw, raw_rl, partial, partial_rl, end;
+  uint32_t chunks;
+};
+
+dc_status_t plan_prefix(int64_t seqs, int64_t prefixes, int q_heads, int kv_heads, int dim, uint64_t max_tokens,
+                        const AttendPlan& own, PrefixSizes* z) {
+  if (prefixes < 1 || prefixes > 0x7FFFFFFF || seqs % prefixes)
+    return fail(DC_ERR_INVALID, "%lld sequences are not shared out among %lld prefixes", static_cast<long long>(seqs),
+                static_cast<long long>(prefixes));
+  if (max_tokens > 0x7FFFFFFFull)
+    return fail(DC_ERR_INVALID, "prefixes of up to %llu tokens", static_cast<unsigned long long>(max_tokens));
+  const uint64_t tiles = (max_tokens + kPrefixTile - 1) / kPrefixTile;
+  z->chunks = static_cast<uint32_t>(std::max<uint64_t>(1, std::min<uint64_t>(tiles, prefix_most_chunks(kv_heads))));
+  const uint64_t rows = static_cast<uint64_t>(seqs / prefixes) * static_cast<uint64_t>(q_heads / kv_heads);
+  const uint64_t units = static_cast<uint64_t>(prefixes) * static_cast<uint64_t>(kv_heads) * z->chunks;
+  if (rows > 0x7FFFFFFFull - kPrefixRows || units > 0x7FFFFFFFull || units * ((rows + kPrefixRows - 1) / kPrefixRows) > 0x7FFFFFFFull ||
+      static_cast<uint64_t>(seqs) * q_heads * (dim / 4) / 128 > 0x7FFFFFF0ull)
+    return fail(DC_ERR_INVALID, "%lld sequences of %d heads exceed a grid", static_cast<long long>(seqs), q_heads);
+  const uint64_t all = static_cast<uint64_t>(seqs) * static_cast<uint64_t>(q_heads), d = static_cast<uint64_t>(dim);
+  const auto up = [](uint64_t n) { return (n + 255) / 256 * 256; };
+  z->raw = up(kAttendCounterBytes + own.partial_bytes);
+  z->raw_rl = z->raw + up(all * d * 4);
+  z->partial = z->raw_rl + up(all * 8);
+  z->partial_rl = z->partial + up(units * rows * d * 4);
+  z->end = z->partial_rl + up(units * rows * 8);
+  return DC_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -343,82 +455,97 @@ size_t dc_attention_workspace_bytes(int64_t seqs, int q_heads, int kv_heads, int
 dc_status_t dc_paged_attention(const dc_paged_attention_t* a, dc_stream_t stream) {
   read_options();
   if (!a) return fail(DC_ERR_INVALID, "the argument block is NULL");
-  if (a->dtype != kBF16 && a->dtype != kF16) return fail(DC_ERR_INVALID, "dtype %d is not DC_BF16 or DC_F16", a->dtype);
-  if (a->page_size < 1) return fail(DC_ERR_INVALID, "page_size = %d is not positive", a->page_size);
-  if (a->window < 0) return fail(DC_ERR_INVALID, "window = %d is negative", a->window);
-  if (!std::isfinite(a->scale)) return fail(DC_ERR_INVALID, "scale is not finite");
-  Spans in, out;
-  if (a->seqs == 0) return ok();
-  DC_TRY(check_table(a->page_table, a->seqs, a->table_width, a->table_stride, in));
-  uint64_t most = static_cast<uint64_t>(a->table_width) * static_cast<uint64_t>(a->page_size);
-  if (a->window > 0) most = std::min<uint64_t>(most, static_cast<uint64_t>(a->window));
-  AttendPlan plan{};
-  DC_TRY(plan_attend(a->seqs, a->q_heads, a->kv_heads, a->dim, most, &plan));
-  const uint64_t n = static_cast<uint64_t>(a->seqs);
   AttendParams p{};
-  DC_TRY(check_tokens(a->q, "q", n, a->q_heads, a->dim, a->q_seq_stride, a->q_head_stride, 2, in));
-  DC_TRY(take(a->lengths, "lengths", n * 4, 4, in));
-  DC_TRY(check_cache(a->k_cache, "k_cache", a->num_pages, a->page_size, a->kv_heads, a->dim, 2, false, &p.kc, in));
-  DC_TRY(check_cache(a->v_cache, "v_cache", a->num_pages, a->page_size, a->kv_heads, a->dim, 2, false, &p.vc, in));
-  DC_TRY(check_tokens(a->out, "out", n, a->q_heads, a->dim, a->out_seq_stride, a->out_head_stride, 2, out));
-  DC_TRY(check_written("out", n, a->q_heads, a->dim, a->out_seq_stride, a->out_head_stride));
-  if (a->lse) DC_TRY(take(a->lse, "lse", n * static_cast<uint64_t>(a->q_heads) * 4, 4, out));
-  if (plan.partial_bytes) {  // the counters, then the pieces' partial results
-    if (kAttendCounterBytes + plan.partial_bytes > a->workspace_bytes)
-      return fail(DC_ERR_INVALID, "the workspace holds %llu bytes; dc_attention_workspace_bytes says %llu",
-                  static_cast<unsigned long long>(a->workspace_bytes),
-                  static_cast<unsigned long long>(dc_attention_workspace_bytes(
-                      a->seqs, a->q_heads, a->kv_heads, a->dim, static_cast<int64_t>(most))));
-    DC_TRY(take(a->workspace, "workspace", a->workspace_bytes, 16, out));
-  }
-  DC_TRY(check_disjoint(out, in));
+  AttendPlan plan{};
+  Spans in, out;
+  DC_TRY(take_attend(a, p, plan, in, out));
+  if (a->seqs == 0) return ok();
   int sms = 0;
   DC_TRY(device(&sms));
-  p.q = addr(a->q);
-  p.q_seq = a->q_seq_stride * 2;
-  p.q_head = a->q_head_stride * 2;
-  p.out = addr(a->out);
-  p.out_seq = a->out_seq_stride * 2;
-  p.out_head = a->out_head_stride * 2;
-  p.lse = addr(a->lse);
-  p.table = addr(a->page_table);
-  p.lengths = addr(a->lengths);
-  p.counters = addr(a->workspace);
-  p.partial = addr(a->workspace) + kAttendCounterBytes;
-  p.table_stride = a->seqs > 1 ? a->table_stride : 0;
-  p.num_pages = a->num_pages;
-  p.page_size = static_cast<uint32_t>(a->page_size);
-  p.table_width = static_cast<uint32_t>(a->table_width);
-  p.seqs = static_cast<int32_t>(a->seqs);
-  p.q_heads = a->q_heads;
-  p.kv_heads = a->kv_heads;
-  p.group = a->q_heads / a->kv_heads;
-  p.head_blocks = plan.head_blocks;
-  p.hb = plan.hb;
-  p.window = a->window;
-  p.units = static_cast<int32_t>(plan.units);
-  p.pieces = static_cast<int32_t>(plan.pieces);
-  // Few CTAs, all resident at once, and few enough pieces: a unit's CTAs are a
-  // cluster and join them in shared memory.  Measured, us, workspace / cluster:
-  // one sequence of 1025 tokens, 8/1 heads of 128 (5 pieces): 8.2 / 6.9; of 4096
-  // (16 pieces, two clusters and the workspace): 8.1 / 10.
-  const uint32_t resident = static_cast<uint32_t>(sms) * (a->dim <= 128 ? 2u : 1u);
-  const uint32_t c = plan.pieces > 4 ? 8u : plan.pieces > 2 ? 4u : 2u;
-  const bool cluster = plan.pieces > 1 && plan.pieces <= c && plan.units * c <= resident;
-  p.cluster = cluster ? static_cast<int32_t>(c) : 1;
-  p.places = cluster ? static_cast<int32_t>(c) : p.pieces;
-  // A table with room for much longer sequences than most are must not flood
-  // the GPU with CTAs that find nothing to do (about 0.5 us each, two at a time
-  // on an SM): beyond four times the CTAs that fill it, a unit's take turns.
-  if (!cluster && plan.pieces > 8 && plan.units * plan.pieces > 4 * kAttendCtas)
-    p.places = static_cast<int32_t>(std::max<uint64_t>(8, std::min<uint64_t>(plan.pieces, 4 * kAttendCtas / plan.units)));
-  // more units than the counters have room for (29127 at least): a CTA each
-  if (!cluster && plan.pieces > 1 && plan.units * attend_counters(plan.pieces) * 4 > kAttendCounterBytes) p.places = 1;
-  p.page_shift = (p.page_size & (p.page_size - 1)) == 0 ? __builtin_ctz(p.page_size) : -1;
-  p.scale = a->scale;
-  int grid = 0;
-  const cudaError_t e = launch_attend(p, a->dtype, a->dim, pdl_option(), static_cast<cudaStream_t>(stream), &grid);
-  return check_launch(e, "paged attention", grid);
+  return run_attend(p, plan, a->dtype, a->dim, sms, stream);
+}
+
+size_t dc_prefix_attention_workspace_bytes(int64_t seqs, int64_t prefixes, int q_heads, int kv_heads, int dim,
+                                           int64_t max_prefix_tokens, int64_t max_tokens) {
+  AttendPlan plan{};
+  PrefixSizes sizes{};
+  if (max_tokens < 0 || max_prefix_tokens < 0 ||
+      plan_attend(seqs, q_heads, kv_heads, dim, static_cast<uint64_t>(max_tokens), &plan) != DC_OK ||
+      plan_prefix(seqs, prefixes, q_heads, kv_heads, dim, static_cast<uint64_t>(max_prefix_tokens), plan, &sizes) != DC_OK)
+    return 0;
+  return static_cast<size_t>(sizes.end);
+}
+
+dc_status_t dc_prefix_attention(const dc_prefix_attention_t* a, dc_stream_t stream) {
+  read_options();
+  if (!a) return fail(DC_ERR_INVALID, "the argument block is NULL");
+  const dc_paged_attention_t& own = a->own;
+  if (own.window != 0) return fail(DC_ERR_INVALID, "attention to shared prefixes has no window (got %d)", own.window);
+  AttendParams p{};
+  AttendPlan plan{};
+  Spans in, out;
+  DC_TRY(take_attend(&own, p, plan, in, out));
+  if (own.seqs == 0) return ok();
+  PrefixSizes sizes{};
+  const uint64_t most = static_cast<uint64_t>(a->prefix_table_width < 0 ? 0 : a->prefix_table_width) * static_cast<uint64_t>(own.page_size);
+  DC_TRY(plan_prefix(own.seqs, a->prefixes, own.q_heads, own.kv_heads, own.dim, most, plan, &sizes));
+  Spans more;
+  DC_TRY(check_table(a->prefix_table, a->prefixes, a->prefix_table_width, a->prefix_table_stride, more));
+  DC_TRY(take(a->prefix_lengths, "prefix_lengths", static_cast<uint64_t>(a->prefixes) * 4, 4, more));
+  if (own.workspace_bytes < sizes.end)
+    return fail(DC_ERR_INVALID, "the workspace holds %llu bytes; dc_prefix_attention_workspace_bytes says %llu",
+                static_cast<unsigned long long>(own.workspace_bytes), static_cast<unsigned long long>(sizes.end));
+  if (!plan.partial_bytes) {  // (else it is among what is written already)
+    Spans ws;
+    DC_TRY(take(own.workspace, "workspace", own.workspace_bytes, 16, ws));
+    DC_TRY(check_disjoint(ws, in));
+    DC_TRY(check_disjoint(ws, out));
+    DC_TRY(check_disjoint(ws, more));
+  }
+  for (const Span& o : out) DC_TRY(check_apart(o, more));
+  int sms = 0, grid = 0;
+  DC_TRY(device(&sms));
+  const uint64_t ws = addr(own.workspace);
+  PrefixParams x{};
+  x.q = p.q;
+  x.q_seq = p.q_seq;
+  x.q_head = p.q_head;
+  x.out = p.out;
+  x.out_seq = p.out_seq;
+  x.out_head = p.out_head;
+  x.lse = p.lse;
+  x.table = addr(a->prefix_table);
+  x.lengths = addr(a->prefix_lengths);
+  x.raw = ws + sizes.raw;
+  x.raw_rl = ws + sizes.raw_rl;
+  x.partial = ws + sizes.partial;
+  x.partial_rl = ws + sizes.partial_rl;
+  x.table_stride = a->prefixes > 1 ? a->prefix_table_stride : 0;
+  x.num_pages = p.num_pages;
+  x.page_size = p.page_size;
+  x.table_width = static_cast<uint32_t>(a->prefix_table_width);
+  x.page_shift = p.page_shift;
+  x.seqs = p.seqs;
+  x.prefixes = static_cast<int32_t>(a->prefixes);
+  x.each = static_cast<int32_t>(own.seqs / a->prefixes);
+  x.q_heads = p.q_heads;
+  x.kv_heads = p.kv_heads;
+  x.group = p.group;
+  x.rows = x.each * x.group;
+  x.row_tiles = (x.rows + kPrefixRows - 1) / kPrefixRows;
+  x.chunks = static_cast<int32_t>(sizes.chunks);
+  x.scale = own.scale;
+  x.wait_ns = wait_limit_option();
+  x.kc = p.kc;
+  x.vc = p.vc;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_prefix(x, own.dtype, own.dim, pdl_option(), s, &grid);
+  DC_TRY(check_launch(e, "attention to shared prefixes", grid));
+  p.raw = x.raw;
+  p.raw_rl = x.raw_rl;
+  DC_TRY(run_attend(p, plan, own.dtype, own.dim, sms, stream));
+  e = launch_prefix_join(x, own.dtype, own.dim, pdl_option(), s, &grid);
+  return check_launch(e, "attention to shared prefixes", grid);
 }
 
 }  // extern "C"

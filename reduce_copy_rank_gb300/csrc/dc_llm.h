@@ -127,6 +127,8 @@ struct AttendParams {
   uint64_t table, lengths;              // int32
   uint64_t counters;                    // uint32 [units][attend_counters(pieces)], zero between calls
   uint64_t partial;                     // f32 [units][HB * (pieces * (dim + 2) + 2 * kAttendGroups)]
+  uint64_t raw, raw_rl;                 // 0, or where the results go instead of out: f32 [seqs][q_heads][dim]
+                                        // unnormalised, and [seqs][q_heads] (reference, sum)
   int64_t table_stride;
   int64_t num_pages;
   uint32_t page_size, table_width;
@@ -295,5 +297,44 @@ struct NormFinishParams {
   int32_t dim, out32;
 };
 cudaError_t launch_norm_finish(const NormFinishParams& p, int dtype, bool pdl, cudaStream_t s, int* grid);
+
+// -------------------------------------------------- attention to shared prefixes
+// A prefix's tokens are cut into chunks, a CTA each for every key head and 128
+// query rows (a row: one head of one sequence): as many as fill the GPU once, and
+// no shorter than a tile.  The cut follows from the prefix's length and the number
+// of key heads, so that how many sequences share it changes no bit.
+constexpr int kPrefixRows = 128, kPrefixTile = 128;
+__host__ __device__ inline uint32_t prefix_most_chunks(int kv_heads) {
+  const uint32_t n = kAttendSms / static_cast<uint32_t>(kv_heads);
+  return n > 1 ? n : 1;
+}
+__host__ __device__ inline uint32_t prefix_chunk(uint32_t tokens, int kv_heads) {
+  const uint32_t most = prefix_most_chunks(kv_heads), per = tokens / most + (tokens % most != 0);
+  return (per + kPrefixTile - 1) / kPrefixTile * kPrefixTile;
+}
+__host__ __device__ inline uint32_t prefix_chunks(uint32_t tokens, int kv_heads) {
+  if (tokens == 0) return 0;
+  const uint32_t per = prefix_chunk(tokens, kv_heads);
+  return tokens / per + (tokens % per != 0);
+}
+
+struct PrefixParams {
+  uint64_t q, q_seq, q_head;            // bytes
+  uint64_t out, out_seq, out_head, lse; // lse: f32 [seqs, q_heads] or 0
+  uint64_t table, lengths;              // int32 [prefixes][table_width], [prefixes]
+  uint64_t partial, partial_rl;         // f32 [prefixes][kv_heads][chunks][rows][dim], [..][rows] (reference, sum)
+  uint64_t raw, raw_rl;                 // the sequences' own tokens, as AttendParams has them
+  int64_t table_stride, num_pages;
+  uint32_t page_size, table_width;
+  int32_t page_shift;
+  int32_t seqs, prefixes, each, q_heads, kv_heads, group;
+  int32_t rows, row_tiles;              // of a prefix and key head: each * group
+  int32_t chunks;                       // most of one prefix
+  float scale;
+  uint64_t wait_ns;
+  PagedView kc, vc;
+};
+cudaError_t launch_prefix(const PrefixParams& p, int dtype, int dim, bool pdl, cudaStream_t s, int* grid);
+cudaError_t launch_prefix_join(const PrefixParams& p, int dtype, int dim, bool pdl, cudaStream_t s, int* grid);
 
 }  // namespace dc

@@ -1,0 +1,504 @@
+// Attention of one new token per sequence where groups of sequences share a
+// long prefix in the paged cache: the prefix's keys and values are read once for
+// all of a group's queries.
+//
+// Mathematics.  A softmax over the prefix's and the sequence's own tokens is
+// joined from its parts: each keeps a reference r (in units of log2, a whole
+// number), l = sum 2^(s_t - r) and u = sum 2^(s_t - r) v_t, and parts add up
+// after a change of reference, which multiplies by a power of two.  The own
+// tokens' part comes from the kernel of paged attention; the prefix's is
+// computed here in chunks of tokens; a last kernel adds the parts up in order.
+//
+// The rows of one product are the queries of all heads of a key head and of all
+// sequences of the group, 128 at a time; a tile of 128 tokens (64 where heads
+// are above 128) is S = Q K^T on the tensor cores, its weights in registers and
+// back into tensor memory as the left operand of U += P V.  Four warps copy keys
+// and values through page numbers (cp.async, into the swizzled rows that the
+// tensor cores read), one issues the products, four hold a row a thread.  With
+// heads up to 128 two CTAs share an SM: one's products run while the other
+// exponentiates.
+//
+// Bound: memory while a group has up to about 128 rows; above that the
+// exponentials (16 a clock and SM) and the products.
+//
+// Rounding: the weights enter the second product in 16 bits (half a step each,
+// 2^-9 or 2^-12, of either sign); their sum l takes them unrounded.  In
+// binary16 they are held times 2^15, so that what is 2^-29 of the largest is
+// still a normal number.
+#include <atomic>
+
+#include "dc_llm.h"
+#include "dc_numeric.cuh"
+#include "dc_tc.cuh"
+
+namespace dc {
+namespace {
+
+using namespace tc;
+
+enum : uint32_t { kSiteLength = 1, kSiteTable = 2, kSiteQuery = 3, kSiteKey = 4, kSiteValue = 5, kSitePartial = 6, kSiteOut = 7 };
+
+__device__ unsigned int g_prefix_fault_bits;
+
+template <int D>
+struct Shape {
+  static constexpr int kTile = D > 128 ? 64 : 128;       // tokens
+  static constexpr int kBlocks = (D + 63) / 64;          // of 64 columns: swizzled rows of 128 bytes
+  static constexpr int kStages = D > 128 || D == 64 ? 2 : 1;  // of keys, and of values
+  static constexpr int kScores = D > 128 ? 2 : 1;        // buffers of scores
+  static constexpr int kCtas = D > 128 ? 1 : 2;
+  static constexpr int kQ = kBlocks * kPrefixRows * 128, kKV = kBlocks * kTile * 128;
+  static constexpr int kSmem = kQ + 2 * kStages * kKV + 1024;
+  static constexpr uint32_t kOut = kScores * kTile;      // the output's first column of tensor memory
+  static constexpr uint32_t kColumns = kOut + D <= 256 ? 256 : 512;
+  static constexpr int kVecs = D / 8;                    // 16-byte parts of a row
+};
+constexpr int kThreads = 288;
+constexpr int kLoaders = 64;  // threads that copy keys, and as many that copy values
+
+// The weights' unit: 2^15 in binary16.
+template <int DT>
+constexpr float kShift = DT == kF16 ? 15.0f : 0.0f;
+
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, uint64_t src, bool read) {
+  const uint32_t n = read ? 16u : 0u;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+
+// 2^(x - M) for whole numbers x <= M; 0 below 2^-126, and for x = -inf.
+__device__ __forceinline__ float pow2_diff(float x, float M) {
+  const int k = static_cast<int>(fmaxf(x - M, -127.0f));
+  return __int_as_float((k + 127) << 23);
+}
+
+// A prefix's tokens; `bad`: a length past the table.
+__device__ __forceinline__ uint32_t prefix_length(const PrefixParams& p, int prefix, bool* bad) {
+  const int32_t* a = reinterpret_cast<const int32_t*>(p.lengths) + prefix;
+  const int32_t n = in_bounds(a, 4, p.lengths, p.lengths + 4ull * p.prefixes, kSiteLength) ? *a : 0;
+  *bad = n > 0 && static_cast<uint64_t>(n) > static_cast<uint64_t>(p.table_width) * p.page_size;
+  return n < 0 ? 0u : *bad ? 1u : static_cast<uint32_t>(n);
+}
+
+// One warp copies its rows of keys or values, tile by tile.
+template <int D>
+struct Copier {
+  using S = Shape<D>;
+  static constexpr int kRows = S::kTile / 2;  // of a tile: two warps share it
+  static constexpr int kLooks = kRows / 32;
+  const PrefixParams& p;
+  const PagedView& view;
+  uint64_t table_row, head;  // head: bytes of the key head in a token
+  uint32_t row0, end;        // this warp's first row of a tile; the chunk's last token + 1
+  uint32_t site;
+  uint64_t at[kLooks];       // where this lane's rows of the next tile are (0: nowhere)
+  bool missing = false;
+
+  __device__ void look_up(uint32_t tile0) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < kLooks; ++i) {
+      const uint32_t t = tile0 + row0 + i * 32 + lane;
+      at[i] = 0;
+      if (t >= end) continue;
+      const uint32_t pg = p.page_shift >= 0 ? t >> p.page_shift : t / p.page_size;
+      const int32_t* a = reinterpret_cast<const int32_t*>(table_row) + pg;
+      const int32_t id = in_bounds(a, 4, table_row, table_row + 4ull * p.table_width, kSiteTable) ? *a : -1;
+      if (id < 0 || id >= p.num_pages) {
+        missing = true;
+        continue;
+      }
+      at[i] = view.base + static_cast<uint64_t>(id) * view.page + static_cast<uint64_t>(t - pg * p.page_size) * view.token + head;
+    }
+  }
+  __device__ void copy(uint32_t to) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < kLooks; ++i)
+#pragma unroll
+      for (int j = 0; j < S::kVecs; ++j) {
+        const int item = j * 32 + lane, row = item / S::kVecs, c = item % S::kVecs;
+        const uint64_t from = __shfl_sync(~0u, at[i], row);
+        const uint64_t x = from + c * 16;
+        const bool read = from != 0 && in_bounds(reinterpret_cast<const void*>(x), 16, view.lo, view.hi, site);
+        const uint32_t r = row0 + i * 32 + row;
+        cp_async16_or_zero(to + (c / 8) * (S::kTile * 128) + r * 128 + ((c % 8) ^ (r & 7)) * 16, read ? x : view.base, read);
+      }
+  }
+};
+
+template <int DT, int D>
+__global__ __launch_bounds__(kThreads, Shape<D>::kCtas) void dc_prefix_kernel(const __grid_constant__ PrefixParams p) {
+  using S = Shape<D>;
+  extern __shared__ uint8_t smem[];
+  __shared__ __align__(8) uint64_t bars[4 * S::kStages + 2 * S::kScores + 3];
+  __shared__ uint32_t tmem_at;
+  __shared__ volatile uint32_t stop, lost;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // unit: (prefix, key head, chunk, rows)
+  const int tile_rows = static_cast<int>(blockIdx.x % static_cast<uint32_t>(p.row_tiles)) * kPrefixRows;
+  const uint32_t unit = blockIdx.x / static_cast<uint32_t>(p.row_tiles);
+  const uint32_t chunk = unit % static_cast<uint32_t>(p.chunks);
+  const int kh = static_cast<int>(unit / static_cast<uint32_t>(p.chunks) % static_cast<uint32_t>(p.kv_heads));
+  const int prefix = static_cast<int>(unit / static_cast<uint32_t>(p.chunks) / static_cast<uint32_t>(p.kv_heads));
+
+  pdl_enter();
+  bool bad;
+  const uint32_t length = prefix_length(p, prefix, &bad);
+  const uint32_t per = length ? prefix_chunk(length, p.kv_heads) : 1;
+  const uint32_t first = chunk * per;
+  if (first >= length) return;
+  const uint32_t end = min(length, first + per);
+  const uint32_t tiles = (end - first + S::kTile - 1) / S::kTile;
+
+  const uint32_t q_at = (smem_addr(smem) + 1023u) & ~1023u;
+  const uint32_t k_at = q_at + S::kQ, v_at = k_at + S::kStages * S::kKV;
+  const uint32_t k_full = smem_addr(bars), k_empty = k_full + 8 * S::kStages, v_full = k_empty + 8 * S::kStages,
+                 v_empty = v_full + 8 * S::kStages, s_full = v_empty + 8 * S::kStages, p_full = s_full + 8 * S::kScores,
+                 q_full = p_full + 8 * S::kScores, summed = q_full + 8, over = summed + 8;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S::kStages; ++i) {
+      tma::mbar_init(k_full + 8 * i, kLoaders);
+      tma::mbar_init(v_full + 8 * i, kLoaders);
+      tma::mbar_init(k_empty + 8 * i, 1);
+      tma::mbar_init(v_empty + 8 * i, 1);
+    }
+    for (int i = 0; i < S::kScores; ++i) {
+      tma::mbar_init(s_full + 8 * i, 1);
+      tma::mbar_init(p_full + 8 * i, 128);
+    }
+    tma::mbar_init(q_full, 2 * kLoaders);
+    tma::mbar_init(summed, 1);
+    tma::mbar_init(over, 1);
+    tma::mbar_init_fence();
+    stop = 0;
+    lost = bad ? 1u : 0u;
+  }
+  if (warp == 4) tmem_alloc(smem_addr(&tmem_at), S::kColumns);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = tmem_at;
+  const Waits waits{&stop, p.wait_ns};
+
+  if (warp < 4) {
+    // ---- a row a thread
+    const int row = tile_rows + static_cast<int>(threadIdx.x);
+    const bool used = tile_rows + warp * 32 < p.rows;  // (a warp without rows only keeps step)
+    const uint32_t lanes = static_cast<uint32_t>(warp) * 32 << 16;
+    const float sc = p.scale * kLog2E;
+    float ref = neg_inf(), sum = 0.0f;
+    bool ok = true;
+    uint32_t sums = 0;  // tiles whose sums this thread has seen done, each in turn
+    auto wait_sums = [&](uint32_t n) {
+      for (; sums < n && ok; ++sums) ok = wait(waits, summed, sums & 1);
+      return ok;
+    };
+    for (uint32_t i = 0; i < tiles; ++i) {
+      const uint32_t buf = i % S::kScores, at = tmem + lanes + buf * S::kTile;
+      ok = wait(waits, s_full + 8 * buf, (i / S::kScores) & 1);
+      if (i >= S::kScores) wait_sums(i - S::kScores + 1);  // (done already: the scores waited for them)
+      if (!__all_sync(~0u, ok)) break;
+      fence_after();
+      const uint32_t left = end - first - i * S::kTile;  // tokens of this tile, if it is the last
+      if (used) {
+        float most = neg_inf();
+        const float sign = sc < 0.0f ? -1.0f : 1.0f;
+#pragma unroll 1
+        for (uint32_t j0 = 0; j0 < S::kTile; j0 += 32) {
+          float v[32];
+          tmem_ld32(at + j0, v);
+          tmem_wait_ld();
+          if (j0 + 32 <= left) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) most = fmaxf(most, v[j] * sign);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) most = fmaxf(most, j0 + j < left ? v[j] * sign : neg_inf());
+          }
+        }
+        // (of |scale| 0 the largest is 0, whatever the scores)
+        const float up = ceilf(most * fabsf(sc));
+        if (__any_sync(~0u, up > ref)) {
+          const float now = fmaxf(ref, up), f = pow2_diff(ref, now);
+          if (i > 0) {
+            if (!__all_sync(~0u, wait_sums(i))) break;  // the sums so far
+            fence_after();
+#pragma unroll 1
+            for (uint32_t d = 0; d < D; d += 32) {
+              float v[32];
+              tmem_ld32(tmem + lanes + S::kOut + d, v);
+              tmem_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] *= f;
+              tmem_st32(tmem + lanes + S::kOut + d, v);
+            }
+          }
+          sum *= f;
+          ref = now;
+        }
+        const float off = kShift<DT> - (ref == neg_inf() ? 0.0f : ref);
+        float l[4] = {};
+#pragma unroll 1
+        for (uint32_t j0 = 0; j0 < S::kTile; j0 += 32) {
+          float v[32];
+          tmem_ld32(at + j0, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = ex2(__fmaf_rn(v[j], sc, off));
+          if (j0 + 32 > left) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = j0 + j < left ? v[j] : 0.0f;
+          }
+          uint32_t w[16];
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            l[j / 2 & 3] += v[j];
+            l[j / 2 & 3] += v[j + 1];
+            w[j / 2] = Elem<DT>::pack(v[j], v[j + 1]);
+          }
+          tmem_st16(at + j0 / 2, w);  // over scores that have been read
+        }
+        sum += (l[0] + l[1]) + (l[2] + l[3]);
+        tmem_wait_st();
+      }
+      fence_before();
+      mbar_arrive(p_full + 8 * buf);
+    }
+    if (ok) wait_sums(tiles);
+    fence_after();
+    asm volatile("bar.sync 1, 256;" ::: "memory");  // the copying warps have said what they missed
+    if (used && __all_sync(~0u, ok)) {
+      constexpr float kUnit = DT == kF16 ? 1.0f / 32768.0f : 1.0f;
+      const uint64_t at = (static_cast<uint64_t>(prefix) * p.kv_heads + kh) * p.chunks + chunk;
+      const uint64_t all = static_cast<uint64_t>(p.prefixes) * p.kv_heads * p.chunks * p.rows;
+      const uint64_t mine = at * p.rows + row;
+#pragma unroll 1
+      for (uint32_t d = 0; d < D; d += 32) {
+        float v[32];
+        tmem_ld32(tmem + lanes + S::kOut + d, v);
+        tmem_wait_ld();
+        if (row >= p.rows) continue;
+        float4* a = reinterpret_cast<float4*>(p.partial + (mine * D + d) * 4);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (in_bounds(a + j, 16, p.partial, p.partial + all * D * 4, kSitePartial))
+            a[j] = make_float4(v[4 * j] * kUnit, v[4 * j + 1] * kUnit, v[4 * j + 2] * kUnit, v[4 * j + 3] * kUnit);
+      }
+      float2* b = reinterpret_cast<float2*>(p.partial_rl) + mine;
+      if (row < p.rows && in_bounds(b, 8, p.partial_rl, p.partial_rl + all * 8, kSitePartial))
+        *b = make_float2(ref, lost ? __int_as_float(0x7FC00000) : sum * kUnit);
+    }
+  } else if (warp == 4) {
+    // ---- the products
+    if (lane == 0) {
+      constexpr uint32_t score = instruction<DT>(kPrefixRows, S::kTile, 0u), value = instruction<DT>(kPrefixRows, D, kMajorB);
+      uint32_t sums = 0;
+      auto scores = [&](uint32_t i) {
+        // they take the place of the weights kScores tiles before, which the sums have to have read
+        for (; sums + S::kScores <= i; ++sums)
+          if (!wait(waits, summed, sums & 1)) return false;
+        const uint32_t st = i % S::kStages, buf = i % S::kScores, k0 = k_at + st * S::kKV;
+        if (!wait(waits, k_full + 8 * st, (i / S::kStages) & 1)) return false;
+        fence_after();
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          mma(tmem + buf * S::kTile, desc_k(q_at + k / 4 * (kPrefixRows * 128) + k % 4 * 32),
+              desc_k(k0 + k / 4 * (S::kTile * 128) + k % 4 * 32), score, k > 0);
+        commit(s_full + 8 * buf);
+        commit(k_empty + 8 * st);
+        return true;
+      };
+      bool go = wait(waits, q_full, 0);
+      if (go && S::kScores > 1) go = scores(0);
+      for (uint32_t i = 0; i < tiles && go; ++i) {
+        const uint32_t next = S::kScores > 1 ? i + 1 : i;
+        if (next < tiles) go = scores(next);
+        const uint32_t st = i % S::kStages, buf = i % S::kScores, v0 = v_at + st * S::kKV;
+        go = go && wait(waits, p_full + 8 * buf, (i / S::kScores) & 1) && wait(waits, v_full + 8 * st, (i / S::kStages) & 1);
+        if (!go) break;
+        fence_after();
+#pragma unroll
+        for (int k = 0; k < S::kTile / 16; ++k)
+          mma_tmem(tmem + S::kOut, tmem + buf * S::kTile + k * 8, desc_mn(v0 + k * 2048, S::kTile * 128), value, (i | k) != 0);
+        commit(v_empty + 8 * st);
+        commit(summed);
+      }
+      if (stop) {
+        commit(over);
+        tma::mbar_wait_bounded(over, 0, p.wait_ns);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---- copies: queries first, then two warps the keys and two the values
+    const bool values = warp >= 7;
+    const int id = static_cast<int>(threadIdx.x) - 160;
+    for (int item = id; item < kPrefixRows * S::kVecs; item += 2 * kLoaders) {
+      const int r = item / S::kVecs, c = item % S::kVecs, row = tile_rows + r;
+      const int seq = prefix * p.each + row / p.group, head = kh * p.group + row % p.group;
+      const uint64_t from = p.q + static_cast<uint64_t>(seq) * p.q_seq + static_cast<uint64_t>(head) * p.q_head;
+      const uint64_t x = from + c * 16;
+      const bool read = row < p.rows && in_bounds(reinterpret_cast<const void*>(x), 16, from, from + D * 2, kSiteQuery);
+      cp_async16_or_zero(q_at + (c / 8) * (kPrefixRows * 128) + r * 128 + ((c % 8) ^ (r & 7)) * 16, read ? x : p.q, read);
+    }
+    cp_async_commit();
+    const PagedView& view = values ? p.vc : p.kc;
+    Copier<D> copier{p, view, p.table + static_cast<uint64_t>(prefix) * static_cast<uint64_t>(p.table_stride) * 4,
+                     static_cast<uint64_t>(kh) * view.head, static_cast<uint32_t>((warp - 5) & 1) * Copier<D>::kRows, end,
+                     values ? kSiteValue : kSiteKey, {}};
+    const uint32_t full = values ? v_full : k_full, empty = values ? v_empty : k_empty, to = values ? v_at : k_at;
+    if (!bad) copier.look_up(first);
+    uint32_t issued = 0, told = 0;
+    bool q_told = false, go = true;
+    while (told < tiles && go) {
+      const uint32_t st = issued % S::kStages;
+      bool room = issued < tiles && issued - told < S::kStages;
+      if (room && issued >= S::kStages) {
+        // wait for the place where nothing else is left to do
+        const uint32_t parity = (issued / S::kStages - 1) & 1;
+        if (issued == told) go = room = __all_sync(~0u, wait(waits, empty + 8 * st, parity));
+        else room = __all_sync(~0u, tma::mbar_try_wait(empty + 8 * st, parity));
+      }
+      if (room) {
+        copier.copy(to + st * S::kKV);
+        cp_async_commit();
+        ++issued;
+        if (issued < tiles && !bad) copier.look_up(first + issued * S::kTile);
+        if (issued < tiles && issued - told < S::kStages && issued < S::kStages) continue;
+      }
+      if (issued == told) continue;
+      // the oldest copies are there: their place is the tensor cores'
+      if (!q_told) {
+        if (issued - told == 1) cp_async_wait<1>();
+        else cp_async_wait<2>();
+        tma::fence_proxy_async_smem();
+        mbar_arrive(q_full);
+        q_told = true;
+      }
+      if (issued - told == 1) cp_async_wait<0>();
+      else cp_async_wait<1>();
+      tma::fence_proxy_async_smem();
+      mbar_arrive(full + 8 * (told % S::kStages));
+      ++told;
+    }
+    cp_async_wait<0>();
+    if (copier.missing) lost = 1;
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+  }
+  __syncthreads();
+  if (threadIdx.x == 0 && stop) atomicOr(&g_prefix_fault_bits, kFaultTensorWait);
+  if (warp == 4) {
+    fence_after();
+    tmem_free(tmem, S::kColumns);
+  }
+}
+
+// The prefix's chunks in order, then the own tokens: four columns a thread.
+constexpr int kJoinThreads = 128;
+template <int DT, int D>
+__global__ __launch_bounds__(kJoinThreads) void dc_prefix_join_kernel(const __grid_constant__ PrefixParams p) {
+  pdl_enter();
+  const uint64_t item = static_cast<uint64_t>(blockIdx.x) * kJoinThreads + threadIdx.x;
+  const uint64_t n = static_cast<uint64_t>(p.seqs) * p.q_heads, row = item / (D / 4);
+  const int d = static_cast<int>(item % (D / 4)) * 4;
+  if (row >= n) return;
+  const int seq = static_cast<int>(row / static_cast<uint32_t>(p.q_heads)), head = static_cast<int>(row % static_cast<uint32_t>(p.q_heads));
+  const int prefix = seq / p.each;
+  bool bad;
+  const uint32_t length = prefix_length(p, prefix, &bad), chunks = prefix_chunks(length, p.kv_heads);
+  const uint64_t all = static_cast<uint64_t>(p.prefixes) * p.kv_heads * p.chunks * p.rows;
+  const uint64_t at = (static_cast<uint64_t>(prefix) * p.kv_heads + head / p.group) * p.chunks * p.rows +
+                      static_cast<uint64_t>(seq % p.each) * p.group + head % p.group;  // of chunk 0; the next is p.rows on
+  auto rl_of = [&](uint32_t c) {
+    const float2* a = reinterpret_cast<const float2*>(p.partial_rl) + at + static_cast<uint64_t>(c) * p.rows;
+    return in_bounds(a, 8, p.partial_rl, p.partial_rl + all * 8, kSitePartial) ? *a : make_float2(neg_inf(), 0.0f);
+  };
+  const float2 own = reinterpret_cast<const float2*>(p.raw_rl)[row];
+  float most = own.x;
+#pragma unroll 4
+  for (uint32_t c = 0; c < chunks; ++c) most = fmaxf(most, rl_of(c).x);
+  float4 u = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  float l = 0.0f;
+  auto add = [&](const float4& x, const float2& rl) {
+    const float f = pow2_diff(rl.x, most);
+    u.x = __fmaf_rn(x.x, f, u.x);
+    u.y = __fmaf_rn(x.y, f, u.y);
+    u.z = __fmaf_rn(x.z, f, u.z);
+    u.w = __fmaf_rn(x.w, f, u.w);
+    l = __fmaf_rn(rl.y, f, l);
+  };
+#pragma unroll 4
+  for (uint32_t c = 0; c < chunks; ++c) {
+    const float4* a = reinterpret_cast<const float4*>(p.partial + ((at + static_cast<uint64_t>(c) * p.rows) * D + d) * 4);
+    const float4 x = in_bounds(a, 16, p.partial, p.partial + all * D * 4, kSitePartial) ? *a : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    add(x, rl_of(c));
+  }
+  add(*reinterpret_cast<const float4*>(p.raw + (row * D + d) * 4), own);
+  const bool none = l == 0.0f && most == neg_inf();  // nothing to attend to: zeros
+  const float inv = none ? 0.0f : 1.0f / l;
+  const uint64_t out = p.out + static_cast<uint64_t>(seq) * p.out_seq + static_cast<uint64_t>(head) * p.out_head;
+  uint2* a = reinterpret_cast<uint2*>(out + d * 2);
+  if (in_bounds(a, 8, out, out + D * 2, kSiteOut))
+    *a = make_uint2(Elem<DT>::pack(u.x * inv, u.y * inv), Elem<DT>::pack(u.z * inv, u.w * inv));
+  if (d == 0 && p.lse) {
+    float* b = reinterpret_cast<float*>(p.lse) + row;
+    if (in_bounds(b, 4, p.lse, p.lse + n * 4, kSiteOut)) *b = none ? neg_inf() : (most + log2f(l)) * kLn2;
+  }
+}
+
+template <int DT, int D>
+cudaError_t launch_one(const PrefixParams& p, bool pdl, cudaStream_t s, int grid) {
+  static std::atomic<uint64_t> allowed{0};  // devices whose limit is set
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(allowed.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(dc_prefix_kernel<DT, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<D>::kSmem);
+    if (e != cudaSuccess) return e;
+    allowed.fetch_or(bit, std::memory_order_relaxed);
+  }
+  return launch_ex(dc_prefix_kernel<DT, D>, grid, kThreads, pdl, s, p, Shape<D>::kSmem);
+}
+
+template <int DT>
+cudaError_t launch_dim(const PrefixParams& p, int dim, bool join, bool pdl, cudaStream_t s, int grid) {
+  switch (dim) {
+    case 64: return join ? launch_ex(dc_prefix_join_kernel<DT, 64>, grid, kJoinThreads, pdl, s, p) : launch_one<DT, 64>(p, pdl, s, grid);
+    case 96: return join ? launch_ex(dc_prefix_join_kernel<DT, 96>, grid, kJoinThreads, pdl, s, p) : launch_one<DT, 96>(p, pdl, s, grid);
+    case 128: return join ? launch_ex(dc_prefix_join_kernel<DT, 128>, grid, kJoinThreads, pdl, s, p) : launch_one<DT, 128>(p, pdl, s, grid);
+    case 192: return join ? launch_ex(dc_prefix_join_kernel<DT, 192>, grid, kJoinThreads, pdl, s, p) : launch_one<DT, 192>(p, pdl, s, grid);
+    default: return join ? launch_ex(dc_prefix_join_kernel<DT, 256>, grid, kJoinThreads, pdl, s, p) : launch_one<DT, 256>(p, pdl, s, grid);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_prefix(const PrefixParams& p, int dtype, int dim, bool pdl, cudaStream_t s, int* grid) {
+  *grid = p.prefixes * p.kv_heads * p.chunks * p.row_tiles;
+  return dtype == kF16 ? launch_dim<kF16>(p, dim, false, pdl, s, *grid) : launch_dim<kBF16>(p, dim, false, pdl, s, *grid);
+}
+
+cudaError_t launch_prefix_join(const PrefixParams& p, int dtype, int dim, bool pdl, cudaStream_t s, int* grid) {
+  const uint64_t items = static_cast<uint64_t>(p.seqs) * static_cast<uint64_t>(p.q_heads) * static_cast<uint64_t>(dim / 4);
+  *grid = static_cast<int>((items + kJoinThreads - 1) / kJoinThreads);
+  return dtype == kF16 ? launch_dim<kF16>(p, dim, true, pdl, s, *grid) : launch_dim<kBF16>(p, dim, true, pdl, s, *grid);
+}
+
+DC_BOUNDS_READER(take_bounds_prefix)
+
+cudaError_t take_prefix_faults(uint32_t* bits) {
+  *bits = 0;
+  cudaError_t e = cudaDeviceSynchronize();
+  if (e != cudaSuccess) return e;
+  unsigned int v = 0;
+  e = cudaMemcpyFromSymbol(&v, g_prefix_fault_bits, sizeof v);
+  if (e == cudaSuccess && v) {
+    const unsigned int zero = 0;
+    e = cudaMemcpyToSymbol(g_prefix_fault_bits, &zero, sizeof zero);
+  }
+  *bits = v;
+  return e;
+}
+
+}  // namespace dc

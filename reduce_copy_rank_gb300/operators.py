@@ -73,10 +73,13 @@ _NORM_GRAD = _Block("26Q2q7if", _heads("q", "k", "grad_q_out", "grad_k_out", "gr
                     "k_norm grad_q_norm grad_k_norm workspace workspace_bytes tokens cos_sin_rows q_heads kv_heads dim "
                     "rotary_dim interleaved dtype norm_32 eps")
 
+_PREFIX = _Block("19Q4q6ifi2Q3q", " ".join(_ATTEND.names) + " prefix_table prefix_lengths prefixes prefix_table_width "
+                 "prefix_table_stride")
+
 # the entry points, as the extension module takes them
 _ENTRIES = ("dc_token_logprobs", "dc_token_logprobs_backward", "dc_kv_append", "dc_paged_attention",
             "dc_linear_logprobs", "dc_linear_logprobs_backward", "dc_kv_append_norm", "dc_qk_norm_rotate",
-            "dc_qk_norm_rotate_backward")
+            "dc_qk_norm_rotate_backward", "dc_prefix_attention")
 
 _bound = None
 
@@ -92,6 +95,8 @@ def _lib():
         L.dc_attention_workspace_bytes.argtypes = [ctypes.c_int64, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                                    ctypes.c_int64]
         L.dc_attention_workspace_bytes.restype = ctypes.c_size_t
+        L.dc_prefix_attention_workspace_bytes.argtypes = [ctypes.c_int64] * 2 + [ctypes.c_int] * 3 + [ctypes.c_int64] * 2
+        L.dc_prefix_attention_workspace_bytes.restype = ctypes.c_size_t
         L.dc_qk_norm_workspace_bytes.argtypes = [ctypes.c_int64, ctypes.c_int, ctypes.c_int, ctypes.c_int]
         L.dc_qk_norm_workspace_bytes.restype = ctypes.c_size_t
         L.dc_linear_logprobs_workspace_bytes.argtypes = [ctypes.c_int64] * 3 + [ctypes.c_int]
@@ -166,6 +171,15 @@ def dc_qk_norm_rotate_backward(stream: int = 0, **fields) -> int:
 
 def dc_qk_norm_workspace_bytes(tokens: int, q_heads: int, kv_heads: int, dim: int) -> int:
     return int(_lib().dc_qk_norm_workspace_bytes(tokens, q_heads, kv_heads, dim))
+
+
+def dc_prefix_attention(stream: int = 0, **fields) -> int:
+    return _lib().dc_prefix_attention(_PREFIX.of(fields), stream)
+
+
+def dc_prefix_attention_workspace_bytes(seqs: int, prefixes: int, q_heads: int, kv_heads: int, dim: int,
+                                        max_prefix_tokens: int, max_tokens: int) -> int:
+    return int(_lib().dc_prefix_attention_workspace_bytes(seqs, prefixes, q_heads, kv_heads, dim, max_prefix_tokens, max_tokens))
 
 
 # ------------------------------------------------------------ tensor API ---
@@ -565,6 +579,42 @@ def paged_attention(q, k_cache, v_cache, page_table, lengths, out, workspace, sc
     :func:`attention_workspace`.  Returns ``out``."""
     status = (_module or _binding()).paged_attention(q, k_cache, v_cache, page_table, lengths, out, workspace, scale, window,
                                                      lse, stream)
+    if status:
+        _dc._check(status)
+    return out
+
+
+def prefix_attention_workspace(seqs: int, prefixes: int, q_heads: int, kv_heads: int, dim: int, max_prefix_tokens: int,
+                               max_tokens: int, device=None):
+    """A zeroed workspace tensor for :func:`prefix_attention` with ``seqs``
+    sequences behind ``prefixes`` prefixes, prefix tables of up to
+    ``max_prefix_tokens`` and page tables of up to ``max_tokens`` tokens a row.
+    Keep it: a call leaves it ready for the next.  One workspace per stream."""
+    import torch
+
+    n = dc_prefix_attention_workspace_bytes(seqs, prefixes, q_heads, kv_heads, dim, max_prefix_tokens, max_tokens)
+    if n == 0:
+        raise _dc.DCError(1, _dc.last_error() or "no such attention")
+    return torch.zeros(n, dtype=torch.uint8, device=device if device is not None else "cuda")
+
+
+def prefix_attention(q, k_cache, v_cache, prefix_table, prefix_lengths, page_table, lengths, out, workspace,
+                     scale: float | None = None, lse=None, stream=None):
+    """:func:`paged_attention` of sequences that share prefixes, whose keys and
+    values are read once for all of a group: with P rows in ``prefix_table``
+    (int32 [P, pages], pages of the same caches) sequences come in P groups of
+    neighbours of one size, and a sequence attends to the first
+    ``prefix_lengths[g]`` (int32 [P]) tokens of its group's prefix, then to its
+    own ``lengths[b]`` tokens of ``page_table``.
+
+    The other arguments are those of :func:`paged_attention` (no window).
+    Either part may be empty; without any token the result is zeros (lse
+    -inf).  A page number outside the cache, or a length past its table, gives
+    NaN in the sequences that it belongs to.  A sequence's bits do not depend
+    on the other sequences.  ``workspace``: :func:`prefix_attention_workspace`.
+    Returns ``out``."""
+    status = (_module or _binding()).prefix_attention(q, k_cache, v_cache, page_table, lengths, out, workspace, scale, 0, lse,
+                                                      stream, prefix_table, prefix_lengths)
     if status:
         _dc._check(status)
     return out
