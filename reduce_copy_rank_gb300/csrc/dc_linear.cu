@@ -77,7 +77,6 @@ __device__ __forceinline__ void stats(const LinearParams& p, uint32_t at, uint64
     if (j0 >= limit) break;
     float v[32];
     tmem_ld32(at + j0, v);
-    tmem_wait_ld();
     if (j0 + 32 <= limit) {
 #pragma unroll
       for (int j = 0; j < 32; ++j) top = fmaxf(top, v[j] * c);
@@ -95,7 +94,6 @@ __device__ __forceinline__ void stats(const LinearParams& p, uint32_t at, uint64
     if (j0 >= limit) break;
     float v[32];
     tmem_ld32(at + j0, v);
-    tmem_wait_ld();
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
       const float z = v[j] * c;
@@ -153,7 +151,6 @@ __device__ __forceinline__ void dlogits(const LinearParams& p, uint32_t at, uint
   for (uint32_t j0 = 0; j0 < kLinearN && n0 + j0 < ld; j0 += 32) {
     float v[32];
     tmem_ld32(at + j0, v);
-    tmem_wait_ld();
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
       const float x = __fmaf_rn(v[j], c, -lse2);
@@ -177,7 +174,6 @@ __device__ __forceinline__ void result(const LinearParams& p, uint32_t at, uint6
   for (uint32_t j0 = 0; j0 < kLinearN && n0 + j0 < p.n; j0 += 32) {
     float v[32];
     tmem_ld32(at + j0, v);
-    tmem_wait_ld();
     if (!own) continue;
     const int left = static_cast<int>(p.n - n0 - j0);
     if constexpr (MODE == kLinearDHidden) {
@@ -464,9 +460,10 @@ cudaError_t launch_mode(int mode, const LinearParams& p, const LinearOperand& a,
 
 namespace tc {
 
-cudaError_t make_map(CUtensorMap* map, int dtype, uint64_t base, uint64_t rows, uint64_t columns, uint64_t row_stride,
-                     uint32_t tile_rows) {
-  using Encode = decltype(&cuTensorMapEncodeTiled);
+namespace {
+using Encode = decltype(&cuTensorMapEncodeTiled);
+cudaError_t encode_tiled(CUtensorMap* map, int dtype, uint64_t base, int dims, const cuuint64_t* size, const cuuint64_t* stride,
+                         const cuuint32_t* box) {
   static std::atomic<Encode> encode{nullptr};  // the driver's function, looked up once
   Encode f = encode.load(std::memory_order_acquire);
   if (!f) {
@@ -478,12 +475,29 @@ cudaError_t make_map(CUtensorMap* map, int dtype, uint64_t base, uint64_t rows, 
     f = reinterpret_cast<Encode>(at);
     encode.store(f, std::memory_order_release);
   }
-  const cuuint64_t size[2] = {columns, rows}, stride[1] = {row_stride};
-  const cuuint32_t box[2] = {64, tile_rows}, step[2] = {1, 1};
-  const CUresult r = f(map, dtype == kF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-                       reinterpret_cast<void*>(base), size, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const cuuint32_t step[4] = {1, 1, 1, 1};
+  const CUresult r = f(map, dtype == kF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                       static_cast<cuuint32_t>(dims), reinterpret_cast<void*>(base), size, stride, box, step,
+                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+}  // namespace
+
+cudaError_t make_map(CUtensorMap* map, int dtype, uint64_t base, uint64_t rows, uint64_t columns, uint64_t row_stride,
+                     uint32_t tile_rows) {
+  const cuuint64_t size[2] = {columns, rows}, stride[1] = {row_stride};
+  const cuuint32_t box[2] = {64, tile_rows};
+  return encode_tiled(map, dtype, base, 2, size, stride, box);
+}
+
+cudaError_t make_paged_map(CUtensorMap* map, int dtype, const PagedView& v, int dim, int heads, uint32_t page_size,
+                           int64_t pages, uint32_t slots) {
+  const cuuint64_t size[4] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(heads), page_size, static_cast<cuuint64_t>(pages)};
+  // (the stride of a dimension of one place is not used, but has to be a valid one)
+  const cuuint64_t stride[3] = {heads > 1 ? v.head : 16, page_size > 1 ? v.token : 16, pages > 1 ? v.page : 16};
+  const cuuint32_t box[4] = {64, 1, slots, 1};
+  return encode_tiled(map, dtype, v.base, 4, size, stride, box);
 }
 
 }  // namespace tc

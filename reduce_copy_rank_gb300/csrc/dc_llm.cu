@@ -221,6 +221,19 @@ dc_status_t run_attend(AttendParams& p, const AttendPlan& plan, int dtype, int d
   return check_launch(e, "paged attention", grid);
 }
 
+// Neighbouring tokens that a TMA copy can move: as many as divide a page and a
+// tile, 8 at least (the swizzled rows of 128 bytes come in eights), and the
+// caches' strides have to fit a tensor map.  0: none.
+int prefix_slots(const AttendParams& p, const dc_paged_attention_t& a) {
+  int slots = 1;
+  while (slots < kPrefixTile && p.page_size % (2u * static_cast<uint32_t>(slots)) == 0) slots *= 2;
+  const PagedView* const views[2] = {&p.kc, &p.vc};
+  for (const PagedView* v : views)
+    for (const uint64_t stride : {a.kv_heads > 1 ? v->head : 16, a.page_size > 1 ? v->token : 16, a.num_pages > 1 ? v->page : 16})
+      if (stride == 0 || stride % 16 || stride >= 1ull << 40) return 0;
+  return slots >= 8 ? slots : 0;
+}
+
 // Where the parts of an attention to shared prefixes lie in its workspace,
 // behind the one of paged attention.
 struct PrefixSizes {
@@ -534,6 +547,7 @@ dc_status_t dc_prefix_attention(const dc_prefix_attention_t* a, dc_stream_t stre
   x.rows = x.each * x.group;
   x.row_tiles = (x.rows + kPrefixRows - 1) / kPrefixRows;
   x.chunks = static_cast<int32_t>(sizes.chunks);
+  x.slots = prefix_slots(p, own);
   x.scale = own.scale;
   x.wait_ns = wait_limit_option();
   x.kc = p.kc;

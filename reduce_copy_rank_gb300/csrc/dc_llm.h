@@ -303,7 +303,7 @@ cudaError_t launch_norm_finish(const NormFinishParams& p, int dtype, bool pdl, c
 // query rows (a row: one head of one sequence): as many as fill the GPU once, and
 // no shorter than a tile.  The cut follows from the prefix's length and the number
 // of key heads, so that how many sequences share it changes no bit.
-constexpr int kPrefixRows = 128, kPrefixTile = 128;
+constexpr int kPrefixRows = 128, kPrefixTile = 64;
 __host__ __device__ inline uint32_t prefix_most_chunks(int kv_heads) {
   const uint32_t n = kAttendSms / static_cast<uint32_t>(kv_heads);
   return n > 1 ? n : 1;
@@ -330,6 +330,7 @@ struct PrefixParams {
   int32_t seqs, prefixes, each, q_heads, kv_heads, group;
   int32_t rows, row_tiles;              // of a prefix and key head: each * group
   int32_t chunks;                       // most of one prefix
+  int32_t slots;                        // neighbouring tokens that one TMA copy moves; 0: keys and values by cp.async
   float scale;
   uint64_t wait_ns;
   PagedView kc, vc;

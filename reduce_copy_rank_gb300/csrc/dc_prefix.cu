@@ -12,9 +12,10 @@
 // The rows of one product are the queries of all heads of a key head and of all
 // sequences of the group, 128 at a time; a tile of 128 tokens (64 where heads
 // are above 128) is S = Q K^T on the tensor cores, its weights in registers and
-// back into tensor memory as the left operand of U += P V.  Four warps copy keys
-// and values through page numbers (cp.async, into the swizzled rows that the
-// tensor cores read), one issues the products, four hold a row a thread.  With
+// back into tensor memory as the left operand of U += P V.  Two warps copy keys
+// and values through page numbers into the swizzled rows that the tensor cores
+// read (TMA boxes of the tokens that divide a page and a tile; cp.async where
+// those are fewer than 8), one issues the products, four hold a row a thread.  With
 // heads up to 128 two CTAs share an SM: one's products run while the other
 // exponentiates.
 //
@@ -23,8 +24,8 @@
 //
 // Rounding: the weights enter the second product in 16 bits (half a step each,
 // 2^-9 or 2^-12, of either sign); their sum l takes them unrounded.  In
-// binary16 they are held times 2^15, so that what is 2^-29 of the largest is
-// still a normal number.
+// binary16 they are held times 2^7 or more, so that what is 2^-21 of the largest
+// is still a normal number.
 #include <atomic>
 
 #include "dc_llm.h"
@@ -42,10 +43,10 @@ __device__ unsigned int g_prefix_fault_bits;
 
 template <int D>
 struct Shape {
-  static constexpr int kTile = D > 128 ? 64 : 128;       // tokens
+  static constexpr int kTile = kPrefixTile;
   static constexpr int kBlocks = (D + 63) / 64;          // of 64 columns: swizzled rows of 128 bytes
-  static constexpr int kStages = D > 128 || D == 64 ? 2 : 1;  // of keys, and of values
-  static constexpr int kScores = D > 128 ? 2 : 1;        // buffers of scores
+  static constexpr int kStages = D > 64 ? 2 : 4;         // of keys, and of values
+  static constexpr int kScores = 2;                      // buffers of scores
   static constexpr int kCtas = D > 128 ? 1 : 2;
   static constexpr int kQ = kBlocks * kPrefixRows * 128, kKV = kBlocks * kTile * 128;
   static constexpr int kSmem = kQ + 2 * kStages * kKV + 1024;
@@ -53,12 +54,18 @@ struct Shape {
   static constexpr uint32_t kColumns = kOut + D <= 256 ? 256 : 512;
   static constexpr int kVecs = D / 8;                    // 16-byte parts of a row
 };
-constexpr int kThreads = 288;
-constexpr int kLoaders = 64;  // threads that copy keys, and as many that copy values
+// Four warps hold a row a thread, one issues products, one copies keys, one
+// values, and the last helps with the queries (a ninth warp would take a quarter
+// of the registers from all).
+constexpr int kThreads = 256;
+constexpr int kQueryLoaders = 96;
 
-// The weights' unit: 2^15 in binary16.
+// A row's reference is at most kSlack behind its largest score: moving it takes
+// a pass over the output so far, which almost every tile would need for one of a
+// warp's rows.  The weights' unit is 2^7 in binary16, where they stay below 2^16.
+constexpr float kSlack = 8.0f;
 template <int DT>
-constexpr float kShift = DT == kF16 ? 15.0f : 0.0f;
+constexpr float kShift = DT == kF16 ? 7.0f : 0.0f;
 
 __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, uint64_t src, bool read) {
   const uint32_t n = read ? 16u : 0u;
@@ -83,30 +90,41 @@ __device__ __forceinline__ uint32_t prefix_length(const PrefixParams& p, int pre
 template <int D>
 struct Copier {
   using S = Shape<D>;
-  static constexpr int kRows = S::kTile / 2;  // of a tile: two warps share it
-  static constexpr int kLooks = kRows / 32;
+  static constexpr int kLooks = S::kTile / 32;
   const PrefixParams& p;
   const PagedView& view;
   uint64_t table_row, head;  // head: bytes of the key head in a token
-  uint32_t row0, end;        // this warp's first row of a tile; the chunk's last token + 1
+  uint32_t end;              // the chunk's last token + 1
   uint32_t site;
   uint64_t at[kLooks];       // where this lane's rows of the next tile are (0: nowhere)
   bool missing = false;
+  int32_t page = -1, slot = 0;  // (TMA) of this lane's box, -1: none
 
+  __device__ int32_t id_of(uint32_t pg) {
+    const int32_t* a = reinterpret_cast<const int32_t*>(table_row) + pg;
+    const int32_t id = in_bounds(a, 4, table_row, table_row + 4ull * p.table_width, kSiteTable) ? *a : -1;
+    if (id >= 0 && id < p.num_pages) return id;
+    missing = true;
+    return -1;
+  }
+  __device__ void look_up_box(uint32_t tile0, uint32_t boxes) {
+    const uint32_t lane = threadIdx.x & 31, t = tile0 + lane * static_cast<uint32_t>(p.slots);
+    page = -1;
+    if (lane >= boxes || t >= end) return;
+    const uint32_t pg = p.page_shift >= 0 ? t >> p.page_shift : t / p.page_size;
+    page = id_of(pg);
+    slot = static_cast<int32_t>(t - pg * p.page_size);
+  }
   __device__ void look_up(uint32_t tile0) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int i = 0; i < kLooks; ++i) {
-      const uint32_t t = tile0 + row0 + i * 32 + lane;
+      const uint32_t t = tile0 + i * 32 + lane;
       at[i] = 0;
       if (t >= end) continue;
       const uint32_t pg = p.page_shift >= 0 ? t >> p.page_shift : t / p.page_size;
-      const int32_t* a = reinterpret_cast<const int32_t*>(table_row) + pg;
-      const int32_t id = in_bounds(a, 4, table_row, table_row + 4ull * p.table_width, kSiteTable) ? *a : -1;
-      if (id < 0 || id >= p.num_pages) {
-        missing = true;
-        continue;
-      }
+      const int32_t id = id_of(pg);
+      if (id < 0) continue;
       at[i] = view.base + static_cast<uint64_t>(id) * view.page + static_cast<uint64_t>(t - pg * p.page_size) * view.token + head;
     }
   }
@@ -120,17 +138,24 @@ struct Copier {
         const uint64_t from = __shfl_sync(~0u, at[i], row);
         const uint64_t x = from + c * 16;
         const bool read = from != 0 && in_bounds(reinterpret_cast<const void*>(x), 16, view.lo, view.hi, site);
-        const uint32_t r = row0 + i * 32 + row;
+        const uint32_t r = i * 32 + row;
         cp_async16_or_zero(to + (c / 8) * (S::kTile * 128) + r * 128 + ((c % 8) ^ (r & 7)) * 16, read ? x : view.base, read);
       }
   }
 };
 
-template <int DT, int D>
-__global__ __launch_bounds__(kThreads, Shape<D>::kCtas) void dc_prefix_kernel(const __grid_constant__ PrefixParams p) {
+struct PrefixArgs {
+  CUtensorMap k, v;  // (TMA)
+  PrefixParams p;
+};
+
+// TMA: keys and values come in boxes of p.slots tokens of a page.
+template <int DT, int D, bool TMA>
+__global__ __launch_bounds__(kThreads, Shape<D>::kCtas) void dc_prefix_kernel(const __grid_constant__ PrefixArgs args) {
   using S = Shape<D>;
+  const PrefixParams& p = args.p;
   extern __shared__ uint8_t smem[];
-  __shared__ __align__(8) uint64_t bars[4 * S::kStages + 2 * S::kScores + 3];
+  __shared__ __align__(8) uint64_t bars[4 * S::kStages + 3 * S::kScores + 2];
   __shared__ uint32_t tmem_at;
   __shared__ volatile uint32_t stop, lost;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -154,20 +179,20 @@ __global__ __launch_bounds__(kThreads, Shape<D>::kCtas) void dc_prefix_kernel(co
   const uint32_t k_at = q_at + S::kQ, v_at = k_at + S::kStages * S::kKV;
   const uint32_t k_full = smem_addr(bars), k_empty = k_full + 8 * S::kStages, v_full = k_empty + 8 * S::kStages,
                  v_empty = v_full + 8 * S::kStages, s_full = v_empty + 8 * S::kStages, p_full = s_full + 8 * S::kScores,
-                 q_full = p_full + 8 * S::kScores, summed = q_full + 8, over = summed + 8;
+                 summed = p_full + 8 * S::kScores, q_full = summed + 8 * S::kScores, over = q_full + 8;
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::kStages; ++i) {
-      tma::mbar_init(k_full + 8 * i, kLoaders);
-      tma::mbar_init(v_full + 8 * i, kLoaders);
+      tma::mbar_init(k_full + 8 * i, TMA ? 1 : 32);
+      tma::mbar_init(v_full + 8 * i, TMA ? 1 : 32);
       tma::mbar_init(k_empty + 8 * i, 1);
       tma::mbar_init(v_empty + 8 * i, 1);
     }
     for (int i = 0; i < S::kScores; ++i) {
       tma::mbar_init(s_full + 8 * i, 1);
       tma::mbar_init(p_full + 8 * i, 128);
+      tma::mbar_init(summed + 8 * i, 1);
     }
-    tma::mbar_init(q_full, 2 * kLoaders);
-    tma::mbar_init(summed, 1);
+    tma::mbar_init(q_full, kQueryLoaders);
     tma::mbar_init(over, 1);
     tma::mbar_init_fence();
     stop = 0;
@@ -188,46 +213,53 @@ __global__ __launch_bounds__(kThreads, Shape<D>::kCtas) void dc_prefix_kernel(co
     const float sc = p.scale * kLog2E;
     float ref = neg_inf(), sum = 0.0f;
     bool ok = true;
-    uint32_t sums = 0;  // tiles whose sums this thread has seen done, each in turn
-    auto wait_sums = [&](uint32_t n) {
-      for (; sums < n && ok; ++sums) ok = wait(waits, summed, sums & 1);
-      return ok;
-    };
+    // Tile i's sum is done.  (A barrier for each buffer: its next phase needs this
+    // thread's weights, so that it never runs two phases ahead.)
+    auto wait_sum = [&](uint32_t i) { return ok = ok && wait(waits, summed + 8 * (i % S::kScores), (i / S::kScores) & 1); };
     for (uint32_t i = 0; i < tiles; ++i) {
       const uint32_t buf = i % S::kScores, at = tmem + lanes + buf * S::kTile;
       ok = wait(waits, s_full + 8 * buf, (i / S::kScores) & 1);
-      if (i >= S::kScores) wait_sums(i - S::kScores + 1);  // (done already: the scores waited for them)
+      if (i >= S::kScores) wait_sum(i - S::kScores);  // (done already: the scores waited for it)
       if (!__all_sync(~0u, ok)) break;
       fence_after();
       const uint32_t left = end - first - i * S::kTile;  // tokens of this tile, if it is the last
       if (used) {
-        float most = neg_inf();
-        const float sign = sc < 0.0f ? -1.0f : 1.0f;
-#pragma unroll 1
-        for (uint32_t j0 = 0; j0 < S::kTile; j0 += 32) {
-          float v[32];
-          tmem_ld32(at + j0, v);
-          tmem_wait_ld();
-          if (j0 + 32 <= left) {
+        uint32_t r[2][32];
+        tmem_ld32(at, r[0]);
+        tmem_ld32(at + 32, r[1]);
+        tmem_wait_ld(r[0]);
+        tmem_wait_ld(r[1]);
+        // the score that scale makes the largest: the largest, or (scale < 0) the smallest
+        const float none = sc < 0.0f ? -neg_inf() : neg_inf();
+        if (left < S::kTile) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) most = fmaxf(most, v[j] * sign);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) most = fmaxf(most, j0 + j < left ? v[j] * sign : neg_inf());
-          }
+          for (int j = 0; j < S::kTile; ++j)
+            if (static_cast<uint32_t>(j) >= left) r[j / 32][j % 32] = __float_as_uint(none);
         }
-        // (of |scale| 0 the largest is 0, whatever the scores)
-        const float up = ceilf(most * fabsf(sc));
-        if (__any_sync(~0u, up > ref)) {
-          const float now = fmaxf(ref, up), f = pow2_diff(ref, now);
+        float m[4] = {none, none, none, none};
+        if (sc < 0.0f) {
+#pragma unroll
+          for (int j = 0; j < S::kTile; j += 2)
+            m[j / 2 & 3] = min3(m[j / 2 & 3], __uint_as_float(r[j / 32][j % 32]), __uint_as_float(r[j / 32][j % 32 + 1]));
+        } else {
+#pragma unroll
+          for (int j = 0; j < S::kTile; j += 2)
+            m[j / 2 & 3] = max3(m[j / 2 & 3], __uint_as_float(r[j / 32][j % 32]), __uint_as_float(r[j / 32][j % 32 + 1]));
+        }
+        const float most = sc < 0.0f ? fminf(min3(m[0], m[1], m[2]), m[3]) : fmaxf(max3(m[0], m[1], m[2]), m[3]);
+        // (of scale 0 the largest is 0, whatever the scores: NaN here moves nothing)
+        const float up = ceilf(most * sc);
+        // the reference follows once it is kSlack behind: until then weights are up to 2^kSlack
+        const bool move = up > ref + kSlack;
+        if (__any_sync(~0u, move)) {
+          const float now = move ? up : ref, f = pow2_diff(ref, now);
           if (i > 0) {
-            if (!__all_sync(~0u, wait_sums(i))) break;  // the sums so far
+            if (!__all_sync(~0u, wait_sum(i - 1))) break;
             fence_after();
 #pragma unroll 1
             for (uint32_t d = 0; d < D; d += 32) {
               float v[32];
               tmem_ld32(tmem + lanes + S::kOut + d, v);
-              tmem_wait_ld();
 #pragma unroll
               for (int j = 0; j < 32; ++j) v[j] *= f;
               tmem_st32(tmem + lanes + S::kOut + d, v);
@@ -237,38 +269,52 @@ __global__ __launch_bounds__(kThreads, Shape<D>::kCtas) void dc_prefix_kernel(co
           ref = now;
         }
         const float off = kShift<DT> - (ref == neg_inf() ? 0.0f : ref);
-        float l[4] = {};
-#pragma unroll 1
-        for (uint32_t j0 = 0; j0 < S::kTile; j0 += 32) {
-          float v[32];
-          tmem_ld32(at + j0, v);
-          tmem_wait_ld();
+        uint64_t l[2] = {0, 0};  // two sums each
+        const uint64_t sc2 = pack2(sc, sc), off2 = pack2(off, off);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = ex2(__fmaf_rn(v[j], sc, off));
-          if (j0 + 32 > left) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = j0 + j < left ? v[j] : 0.0f;
-          }
+        for (int h = 0; h < 2; ++h) {
           uint32_t w[16];
 #pragma unroll
           for (int j = 0; j < 32; j += 2) {
-            l[j / 2 & 3] += v[j];
-            l[j / 2 & 3] += v[j + 1];
-            w[j / 2] = Elem<DT>::pack(v[j], v[j + 1]);
+            float x, y;
+            unpack2(fma2(pack2(__uint_as_float(r[h][j]), __uint_as_float(r[h][j + 1])), sc2, off2), x, y);
+            x = ex2(x);
+            y = ex2(y);
+            if (sc == 0.0f && left < S::kTile) {  // (what is behind the last token has no score to be told by)
+              x = static_cast<uint32_t>(h * 32 + j) < left ? x : 0.0f;
+              y = static_cast<uint32_t>(h * 32 + j + 1) < left ? y : 0.0f;
+            }
+            l[j / 2 & 1] = add2(l[j / 2 & 1], pack2(x, y));
+            w[j / 2] = Elem<DT>::pack(x, y);
           }
-          tmem_st16(at + j0 / 2, w);  // over scores that have been read
+          tmem_st16(at + h * 16, w);  // over scores that have been read
         }
-        sum += (l[0] + l[1]) + (l[2] + l[3]);
+        float l0, l1;
+        unpack2(add2(l[0], l[1]), l0, l1);
+        sum += l0 + l1;
         tmem_wait_st();
+      }
+      if (TMA && left < S::kTile) {
+        // a copy brings whole boxes: values behind the last token have weight 0, but must be numbers
+        const uint32_t st = i % S::kStages;
+        ok = wait(waits, v_full + 8 * st, (i / S::kStages) & 1);
+        if (!__all_sync(~0u, ok)) break;
+        for (uint32_t c = threadIdx.x; c < (S::kTile - left) * S::kBlocks * 8; c += 128) {
+          const uint32_t r = left + c / (S::kBlocks * 8), b = c / 8 % S::kBlocks;
+          asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v_at + st * S::kKV + b * (S::kTile * 128) + r * 128 + c % 8 * 16),
+                       "r"(0u) : "memory");
+        }
+        tma::fence_proxy_async_smem();
       }
       fence_before();
       mbar_arrive(p_full + 8 * buf);
     }
-    if (ok) wait_sums(tiles);
+    if (tiles > 1) wait_sum(tiles - 2);
+    wait_sum(tiles - 1);
     fence_after();
-    asm volatile("bar.sync 1, 256;" ::: "memory");  // the copying warps have said what they missed
+    asm volatile("bar.sync 1, 224;" ::: "memory");  // the copying warps have said what they missed
     if (used && __all_sync(~0u, ok)) {
-      constexpr float kUnit = DT == kF16 ? 1.0f / 32768.0f : 1.0f;
+      constexpr float kUnit = DT == kF16 ? 1.0f / 128.0f : 1.0f;
       const uint64_t at = (static_cast<uint64_t>(prefix) * p.kv_heads + kh) * p.chunks + chunk;
       const uint64_t all = static_cast<uint64_t>(p.prefixes) * p.kv_heads * p.chunks * p.rows;
       const uint64_t mine = at * p.rows + row;
@@ -276,7 +322,6 @@ __global__ __launch_bounds__(kThreads, Shape<D>::kCtas) void dc_prefix_kernel(co
       for (uint32_t d = 0; d < D; d += 32) {
         float v[32];
         tmem_ld32(tmem + lanes + S::kOut + d, v);
-        tmem_wait_ld();
         if (row >= p.rows) continue;
         float4* a = reinterpret_cast<float4*>(p.partial + (mine * D + d) * 4);
 #pragma unroll
@@ -292,11 +337,9 @@ __global__ __launch_bounds__(kThreads, Shape<D>::kCtas) void dc_prefix_kernel(co
     // ---- the products
     if (lane == 0) {
       constexpr uint32_t score = instruction<DT>(kPrefixRows, S::kTile, 0u), value = instruction<DT>(kPrefixRows, D, kMajorB);
-      uint32_t sums = 0;
       auto scores = [&](uint32_t i) {
-        // they take the place of the weights kScores tiles before, which the sums have to have read
-        for (; sums + S::kScores <= i; ++sums)
-          if (!wait(waits, summed, sums & 1)) return false;
+        // they take the place of the weights kScores tiles before, which that tile's sum has to have read
+        if (i >= S::kScores && !wait(waits, summed + 8 * (i % S::kScores), (i / S::kScores - 1) & 1)) return false;
         const uint32_t st = i % S::kStages, buf = i % S::kScores, k0 = k_at + st * S::kKV;
         if (!wait(waits, k_full + 8 * st, (i / S::kStages) & 1)) return false;
         fence_after();
@@ -314,14 +357,14 @@ __global__ __launch_bounds__(kThreads, Shape<D>::kCtas) void dc_prefix_kernel(co
         const uint32_t next = S::kScores > 1 ? i + 1 : i;
         if (next < tiles) go = scores(next);
         const uint32_t st = i % S::kStages, buf = i % S::kScores, v0 = v_at + st * S::kKV;
-        go = go && wait(waits, p_full + 8 * buf, (i / S::kScores) & 1) && wait(waits, v_full + 8 * st, (i / S::kStages) & 1);
+        go = go && wait(waits, v_full + 8 * st, (i / S::kStages) & 1) && wait(waits, p_full + 8 * buf, (i / S::kScores) & 1);
         if (!go) break;
         fence_after();
 #pragma unroll
         for (int k = 0; k < S::kTile / 16; ++k)
           mma_tmem(tmem + S::kOut, tmem + buf * S::kTile + k * 8, desc_mn(v0 + k * 2048, S::kTile * 128), value, (i | k) != 0);
         commit(v_empty + 8 * st);
-        commit(summed);
+        commit(summed + 8 * buf);
       }
       if (stop) {
         commit(over);
@@ -330,10 +373,10 @@ __global__ __launch_bounds__(kThreads, Shape<D>::kCtas) void dc_prefix_kernel(co
     }
     __syncwarp();
   } else {
-    // ---- copies: queries first, then two warps the keys and two the values
-    const bool values = warp >= 7;
+    // ---- copies: queries first, then one warp the keys and one the values
+    const bool values = warp == 6;
     const int id = static_cast<int>(threadIdx.x) - 160;
-    for (int item = id; item < kPrefixRows * S::kVecs; item += 2 * kLoaders) {
+    for (int item = id; item < kPrefixRows * S::kVecs; item += kQueryLoaders) {
       const int r = item / S::kVecs, c = item % S::kVecs, row = tile_rows + r;
       const int seq = prefix * p.each + row / p.group, head = kh * p.group + row % p.group;
       const uint64_t from = p.q + static_cast<uint64_t>(seq) * p.q_seq + static_cast<uint64_t>(head) * p.q_head;
@@ -344,15 +387,54 @@ __global__ __launch_bounds__(kThreads, Shape<D>::kCtas) void dc_prefix_kernel(co
     cp_async_commit();
     const PagedView& view = values ? p.vc : p.kc;
     Copier<D> copier{p, view, p.table + static_cast<uint64_t>(prefix) * static_cast<uint64_t>(p.table_stride) * 4,
-                     static_cast<uint64_t>(kh) * view.head, static_cast<uint32_t>((warp - 5) & 1) * Copier<D>::kRows, end,
-                     values ? kSiteValue : kSiteKey, {}};
+                     static_cast<uint64_t>(kh) * view.head, end, values ? kSiteValue : kSiteKey, {}};
     const uint32_t full = values ? v_full : k_full, empty = values ? v_empty : k_empty, to = values ? v_at : k_at;
-    if (!bad) copier.look_up(first);
-    uint32_t issued = 0, told = 0;
     bool q_told = false, go = true;
+    if (warp != 7 && !bad) {
+      if (TMA) copier.look_up_box(first, S::kTile / static_cast<uint32_t>(p.slots));
+      else copier.look_up(first);
+    }
+    if (TMA && warp != 7) {
+      // each lane copies a box of the tile
+      const uint32_t boxes = S::kTile / static_cast<uint32_t>(p.slots);
+      const CUtensorMap* map = values ? &args.v : &args.k;
+      uint32_t i = 0;
+      for (; i < tiles; ++i) {
+        const uint32_t st = i % S::kStages, bar = full + 8 * st;
+        if (i >= S::kStages && !__all_sync(~0u, wait(waits, empty + 8 * st, (i / S::kStages - 1) & 1))) break;
+        const int32_t page = copier.page, slot = copier.slot;
+        const uint32_t there = __popc(__ballot_sync(~0u, page >= 0));
+        if (lane == 0) tma::mbar_arrive_expect_tx(bar, there * static_cast<uint32_t>(p.slots) * 128 * S::kBlocks);
+        __syncwarp();
+        if (page >= 0) {
+          const uint32_t dst = to + st * S::kKV + static_cast<uint32_t>(lane * p.slots) * 128;
+#pragma unroll
+          for (int b = 0; b < S::kBlocks; ++b) load_paged(dst + b * (S::kTile * 128), map, bar, b * 64, kh, slot, page);
+        }
+        if (i + 1 < tiles && !bad) copier.look_up_box(first + (i + 1) * S::kTile, boxes);
+        if (i == 0) {
+          cp_async_wait<0>();
+          tma::fence_proxy_async_smem();
+          mbar_arrive(q_full);
+        }
+      }
+      if (stop) {  // no copy may land after this CTA's shared memory is gone
+        for (uint32_t k = i > S::kStages ? i - S::kStages : 0; k < i; ++k)
+          tma::mbar_wait_bounded(full + 8 * (k % S::kStages), (k / S::kStages) & 1, p.wait_ns);
+      }
+      go = false;
+    }
+    if (warp == 7) {
+      cp_async_wait<0>();
+      tma::fence_proxy_async_smem();
+      mbar_arrive(q_full);
+      go = false;
+    }
+    constexpr uint32_t kAhead = 2;  // tiles under way
+    uint32_t issued = 0, told = 0;
     while (told < tiles && go) {
       const uint32_t st = issued % S::kStages;
-      bool room = issued < tiles && issued - told < S::kStages;
+      bool room = issued < tiles && issued - told < kAhead;
       if (room && issued >= S::kStages) {
         // wait for the place where nothing else is left to do
         const uint32_t parity = (issued / S::kStages - 1) & 1;
@@ -364,7 +446,7 @@ __global__ __launch_bounds__(kThreads, Shape<D>::kCtas) void dc_prefix_kernel(co
         cp_async_commit();
         ++issued;
         if (issued < tiles && !bad) copier.look_up(first + issued * S::kTile);
-        if (issued < tiles && issued - told < S::kStages && issued < S::kStages) continue;
+        if (issued < tiles && issued < kAhead) continue;
       }
       if (issued == told) continue;
       // the oldest copies are there: their place is the tensor cores'
@@ -383,7 +465,7 @@ __global__ __launch_bounds__(kThreads, Shape<D>::kCtas) void dc_prefix_kernel(co
     }
     cp_async_wait<0>();
     if (copier.missing) lost = 1;
-    asm volatile("bar.sync 1, 256;" ::: "memory");
+    asm volatile("bar.sync 1, 224;" ::: "memory");
   }
   __syncthreads();
   if (threadIdx.x == 0 && stop) atomicOr(&g_prefix_fault_bits, kFaultTensorWait);
@@ -446,7 +528,7 @@ __global__ __launch_bounds__(kJoinThreads) void dc_prefix_join_kernel(const __gr
   }
 }
 
-template <int DT, int D>
+template <int DT, int D, bool TMA>
 cudaError_t launch_one(const PrefixParams& p, bool pdl, cudaStream_t s, int grid) {
   static std::atomic<uint64_t> allowed{0};  // devices whose limit is set
   int dev = 0;
@@ -454,21 +536,34 @@ cudaError_t launch_one(const PrefixParams& p, bool pdl, cudaStream_t s, int grid
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (!(allowed.load(std::memory_order_relaxed) & bit)) {
-    e = cudaFuncSetAttribute(dc_prefix_kernel<DT, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<D>::kSmem);
+    e = cudaFuncSetAttribute(dc_prefix_kernel<DT, D, TMA>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<D>::kSmem);
     if (e != cudaSuccess) return e;
     allowed.fetch_or(bit, std::memory_order_relaxed);
   }
-  return launch_ex(dc_prefix_kernel<DT, D>, grid, kThreads, pdl, s, p, Shape<D>::kSmem);
+  PrefixArgs args{};
+  args.p = p;
+  if (TMA) {
+    const uint32_t slots = static_cast<uint32_t>(p.slots);
+    e = make_paged_map(&args.k, DT, p.kc, D, p.kv_heads, p.page_size, p.num_pages, slots);
+    if (e == cudaSuccess) e = make_paged_map(&args.v, DT, p.vc, D, p.kv_heads, p.page_size, p.num_pages, slots);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_ex(dc_prefix_kernel<DT, D, TMA>, grid, kThreads, pdl, s, args, Shape<D>::kSmem);
+}
+
+template <int DT, int D>
+cudaError_t launch_loads(const PrefixParams& p, bool pdl, cudaStream_t s, int grid) {
+  return p.slots ? launch_one<DT, D, true>(p, pdl, s, grid) : launch_one<DT, D, false>(p, pdl, s, grid);
 }
 
 template <int DT>
 cudaError_t launch_dim(const PrefixParams& p, int dim, bool join, bool pdl, cudaStream_t s, int grid) {
   switch (dim) {
-    case 64: return join ? launch_ex(dc_prefix_join_kernel<DT, 64>, grid, kJoinThreads, pdl, s, p) : launch_one<DT, 64>(p, pdl, s, grid);
-    case 96: return join ? launch_ex(dc_prefix_join_kernel<DT, 96>, grid, kJoinThreads, pdl, s, p) : launch_one<DT, 96>(p, pdl, s, grid);
-    case 128: return join ? launch_ex(dc_prefix_join_kernel<DT, 128>, grid, kJoinThreads, pdl, s, p) : launch_one<DT, 128>(p, pdl, s, grid);
-    case 192: return join ? launch_ex(dc_prefix_join_kernel<DT, 192>, grid, kJoinThreads, pdl, s, p) : launch_one<DT, 192>(p, pdl, s, grid);
-    default: return join ? launch_ex(dc_prefix_join_kernel<DT, 256>, grid, kJoinThreads, pdl, s, p) : launch_one<DT, 256>(p, pdl, s, grid);
+    case 64: return join ? launch_ex(dc_prefix_join_kernel<DT, 64>, grid, kJoinThreads, pdl, s, p) : launch_loads<DT, 64>(p, pdl, s, grid);
+    case 96: return join ? launch_ex(dc_prefix_join_kernel<DT, 96>, grid, kJoinThreads, pdl, s, p) : launch_loads<DT, 96>(p, pdl, s, grid);
+    case 128: return join ? launch_ex(dc_prefix_join_kernel<DT, 128>, grid, kJoinThreads, pdl, s, p) : launch_loads<DT, 128>(p, pdl, s, grid);
+    case 192: return join ? launch_ex(dc_prefix_join_kernel<DT, 192>, grid, kJoinThreads, pdl, s, p) : launch_loads<DT, 192>(p, pdl, s, grid);
+    default: return join ? launch_ex(dc_prefix_join_kernel<DT, 256>, grid, kJoinThreads, pdl, s, p) : launch_loads<DT, 256>(p, pdl, s, grid);
   }
 }
 

@@ -7,7 +7,7 @@
 #include <cuda.h>
 #include <stdint.h>
 
-#include "dc_internal.h"
+#include "dc_llm.h"
 #include "dc_tma.cuh"
 
 namespace dc {
@@ -86,8 +86,9 @@ __device__ __forceinline__ void tmem_free(uint32_t at, uint32_t columns) {
 
 // 32 columns of this warp's 32 lanes: thread l gets lane l's (the address's
 // lane is the warp's first: 32 * (warp % 4)).
-__device__ __forceinline__ void tmem_ld32(uint32_t at, float (&v)[32]) {
-  uint32_t r[32];
+// (The values may be used after tmem_wait_ld, which names them: loads of other
+// columns can be under way while one's values are worked on.)
+__device__ __forceinline__ void tmem_ld32(uint32_t at, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
       "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
@@ -97,8 +98,37 @@ __device__ __forceinline__ void tmem_ld32(uint32_t at, float (&v)[32]) {
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(at)
       : "memory");
+}
+// Waits for every load of this thread; `r` is what one of them has brought.
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
+                 "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                 "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+// Both: 32 columns as numbers.
+__device__ __forceinline__ void tmem_ld32(uint32_t at, float (&v)[32]) {
+  uint32_t r[32];
+  tmem_ld32(at, r);
+  tmem_wait_ld(r);
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+// f(j0, columns j0 .. j0 + 31) for the first N columns (a multiple of 32), each
+// group's load under way while the one before is worked on.
+template <int N, class F>
+__device__ __forceinline__ void tmem_each32(uint32_t at, F f) {
+  uint32_t r[2][32];
+  tmem_ld32(at, r[0]);
+#pragma unroll
+  for (int j0 = 0; j0 < N; j0 += 32) {
+    tmem_wait_ld(r[j0 / 32 & 1]);
+    if (j0 + 32 < N) tmem_ld32(at + j0 + 32, r[(j0 / 32 + 1) & 1]);
+    f(j0, r[j0 / 32 & 1]);
+  }
 }
 // The other way: 32 or 16 columns from each thread's words.
 __device__ __forceinline__ void tmem_st32(uint32_t at, const float (&v)[32]) {
@@ -121,7 +151,36 @@ __device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&r)[16]) 
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// ------------------------------------------------------------ packed numbers ---
+// Two binary32 numbers an instruction, each rounded as alone.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// The largest or smallest of three numbers.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float r;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 
 // --------------------------------------------------------------- mbarriers ---
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
@@ -133,13 +192,25 @@ struct Waits {
   volatile uint32_t* stop;  // in shared memory, 0 at first
   uint64_t limit_ns;
 };
+// (Each try suspends the thread for a while; the clock, which is slow to read,
+// is looked at now and then.)
 __device__ __forceinline__ bool wait(const Waits& w, uint32_t bar, uint32_t parity) {
-  if (tma::mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = tma::global_ns();
+  uint32_t done;  // (a look that does not suspend is quicker where the phase has completed)
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  if (done) return true;
+  uint64_t t0 = 0;
   for (uint32_t i = 0; i < tma::kMaxPolls; ++i) {
     if (tma::mbar_try_wait(bar, parity)) return true;
     if (*w.stop) return false;
-    if (tma::global_ns() - t0 >= w.limit_ns) break;
+    if ((i & 31) == 31) {
+      const uint64_t now = tma::global_ns();
+      if (t0 == 0) t0 = now;
+      else if (now - t0 >= w.limit_ns) break;
+    }
   }
   *w.stop = 1;
   return false;
@@ -154,6 +225,14 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, 
       "l"(map), "r"(bar), "r"(x), "r"(y)
       : "memory");
 }
+// The same of a paged cache: column x, key head, slot and page.
+__device__ __forceinline__ void load_paged(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x, int32_t head,
+                                           int32_t slot, int32_t page) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(map), "r"(bar), "r"(x), "r"(head), "r"(slot), "r"(page)
+      : "memory");
+}
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
@@ -162,6 +241,10 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
 // of 16), in tiles of 64 columns x tile_rows rows, swizzled by 128 bytes.
 cudaError_t make_map(CUtensorMap* map, int dtype, uint64_t base, uint64_t rows, uint64_t columns, uint64_t row_stride,
                      uint32_t tile_rows);
+// ... over a paged cache (strides in bytes), in boxes of 64 columns of one head
+// and `slots` neighbouring tokens of a page.
+cudaError_t make_paged_map(CUtensorMap* map, int dtype, const PagedView& v, int dim, int heads, uint32_t page_size,
+                           int64_t pages, uint32_t slots);
 
 }  // namespace tc
 }  // namespace dc
