@@ -456,7 +456,7 @@ size_t dc_linear_logprobs_workspace_bytes(int64_t rows, int64_t hidden_size, int
  *
  *   grad_hidden = d W;   grad_weights[r] = (d^T hidden) of the shard's columns.
  *
- * The logits are computed again, 16384 columns of a shard at a time; d is
+ * The logits are computed again, up to 24576 columns of a shard at a time; d is
  * rounded to 16 bits before its products (for DC_F16 times one power of two for
  * all rows, so that the largest d that these g and h allow fits: rows whose g
  * and h are 2^20 times smaller than the largest lose precision), the sums are

@@ -14,8 +14,9 @@
 //    number r in units of log2), sum 2^(z-r) and sum 2^(z-r) (z-r), written as
 //    16 bytes; a second kernel adds a row's parts up in one fixed order, which
 //    depends on the shards' widths alone.
-//  * backward, for up to 16384 columns of a shard at a time: the logits again,
-//    from which d is written in 16 bits; d W added to a binary32 sum; d^T h.
+//  * backward, for up to 24576 columns of a shard at a time: the logits again,
+//    from which d is written in 16 bits; then d W, added to binary32 sums, and
+//    d^T h in one launch, whose tiles are shared out so that all CTAs end together.
 // Neither the number of rows nor the grid changes a bit of a row's results.
 //
 // Rounding: d is rounded to 16 bits before its products (2^-9 of each for
@@ -162,40 +163,44 @@ __device__ __forceinline__ void dlogits(const LinearParams& p, uint32_t at, uint
   }
 }
 
-// A row of a product that is stored: plus what `acc` holds of it, to `acc` or
-// (when complete) to the output.
-template <int MODE, int DT>
-__device__ __forceinline__ void result(const LinearParams& p, uint32_t at, uint64_t row, bool own, uint32_t n0) {
+// A row of a gradient.  dh: plus what `acc` holds of it, to `acc` or (complete)
+// to the output.
+template <int DT>
+__device__ __forceinline__ void result(const LinearParams& p, uint32_t at, uint64_t row, bool own, uint32_t n0, bool weights,
+                                       uint32_t slice, bool empty) {
+  const LinearGrads& g = p.g;
   const float unit = p.scale ? reinterpret_cast<const float*>(p.scale)[1] : 1.0f;
-  const uint64_t out = p.out + row * p.out_stride;
-  float* acc = reinterpret_cast<float*>(p.acc) + row * p.n;
-  const uint64_t acc_hi = p.acc + p.rows * p.n * 4;
+  const uint64_t out = weights ? g.out_w + row * g.out_w_stride : g.out_h + row * g.out_h_stride;
+  const uint64_t acc_lo = g.acc + static_cast<uint64_t>(slice) * p.rows * p.n * 4, acc_hi = acc_lo + p.rows * p.n * 4;
+  const bool sums = !weights && g.acc, add = sums && g.add, last = !sums || g.last;
 #pragma unroll 1
   for (uint32_t j0 = 0; j0 < kLinearN && n0 + j0 < p.n; j0 += 32) {
     float v[32];
     tmem_ld32(at + j0, v);
     if (!own) continue;
+    if (empty) {  // (a slice behind the last column: nothing was multiplied)
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+    }
     const int left = static_cast<int>(p.n - n0 - j0);
-    if constexpr (MODE == kLinearDHidden) {
-      float4* a = reinterpret_cast<float4*>(acc + n0 + j0);
-      if (p.add) {
+    float4* a = reinterpret_cast<float4*>(acc_lo) + (row * p.n + n0 + j0) / 4;
+    if (add) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (4 * j < left && in_bounds(a + j, 16, p.acc, acc_hi, kSiteAcc)) {
-            const float4 x = a[j];
-            v[4 * j] += x.x;
-            v[4 * j + 1] += x.y;
-            v[4 * j + 2] += x.z;
-            v[4 * j + 3] += x.w;
-          }
-      }
-      if (!p.last) {
+      for (int j = 0; j < 8; ++j)
+        if (4 * j < left && in_bounds(a + j, 16, acc_lo, acc_hi, kSiteAcc)) {
+          const float4 x = a[j];
+          v[4 * j] += x.x;
+          v[4 * j + 1] += x.y;
+          v[4 * j + 2] += x.z;
+          v[4 * j + 3] += x.w;
+        }
+    }
+    if (!last) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (4 * j < left && in_bounds(a + j, 16, p.acc, acc_hi, kSiteAcc))
-            a[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-        continue;
-      }
+      for (int j = 0; j < 8; ++j)
+        if (4 * j < left && in_bounds(a + j, 16, acc_lo, acc_hi, kSiteAcc))
+          a[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+      continue;
     }
 #pragma unroll
     for (int j = 0; j < 32; ++j) v[j] *= unit;
@@ -205,8 +210,8 @@ __device__ __forceinline__ void result(const LinearParams& p, uint32_t at, uint6
 
 template <int MODE, int DT, int NB>
 __global__ __launch_bounds__(kThreads, 1) void dc_linear_kernel(const __grid_constant__ LinearArgs<NB> args) {
-  // which operands' rows run across the inner dimension
-  constexpr bool kAcrossA = MODE == kLinearDWeights, kAcrossB = MODE == kLinearDHidden || MODE == kLinearDWeights;
+  // whether B's rows run across the inner dimension (A's do for dW)
+  constexpr bool kAcrossB = MODE == kLinearGrads;
   const LinearParams& p = args.p;
   extern __shared__ uint8_t smem[];
   __shared__ __align__(8) uint64_t bars[2 * kStages + 5];
@@ -240,41 +245,72 @@ __global__ __launch_bounds__(kThreads, 1) void dc_linear_kernel(const __grid_con
   tma::fence_proxy_async_global();  // (the operands may be an earlier kernel's stores)
 
   const Waits waits{&stop, p.wait_ns};
-  const uint32_t tiles = p.m_tiles * p.n_tiles;
-  // tile t: its rows, its columns and the tensor that they belong to
+  // This CTA's n-th tile: its rows, its columns, the tensor that those belong to,
+  // its blocks of the inner dimension.
   struct Place {
-    uint32_t m0, n0;
-    int r;
+    uint32_t m0, n0, k0, blocks;
+    uint32_t tile;    // kLinearStats: of columns; kLinearGrads: slice
+    int r;            // kLinearStats: shard; kLinearGrads: 0 dh, 1 dW
+    bool there;
   };
-  auto place = [&](uint32_t t) {
-    Place x{t % p.m_tiles * kLinearM, t / p.m_tiles, 0};
-    if constexpr (MODE == kLinearStats) {
-      if constexpr (NB > 1)
-        while (x.r + 1 < p.shards && args.shard[x.r + 1].tile0 <= x.n0) ++x.r;
-      x.n0 -= args.shard[x.r].tile0;
+  auto place = [&](uint32_t n) {
+    Place x{0, 0, 0, p.k_blocks, 0, 0, true};
+    const uint32_t c = blockIdx.x, G = gridDim.x;
+    if constexpr (MODE == kLinearGrads) {
+      const LinearGrads& g = p.g;
+      const uint32_t mine = g.rounds + (c < g.rest);
+      if (n < mine) {
+        const uint32_t t = c + n * G, s = t / (g.h_m * g.h_n);
+        x.m0 = t % g.h_m * kLinearM;
+        x.n0 = t / g.h_m % g.h_n * kLinearN;
+        x.k0 = s * g.slice_blocks;
+        x.blocks = min(g.slice_blocks, g.h_blocks > x.k0 ? g.h_blocks - x.k0 : 0u);
+        x.tile = s;
+      } else {
+        const uint32_t k = n - mine, t = k < g.few ? k * G + c : g.few * G + (k - g.few) * (G - g.rest) + c - g.rest;
+        x.there = (k < g.few || (c >= g.rest && k < g.many)) && t < g.w_tiles;
+        x.m0 = t % g.w_m * kLinearM;
+        x.n0 = t / g.w_m * kLinearN;
+        x.blocks = g.w_blocks;
+        x.r = 1;
+      }
+    } else {
+      const uint64_t t = c + static_cast<uint64_t>(n) * G;
+      x.there = t < static_cast<uint64_t>(p.m_tiles) * p.n_tiles;
+      x.m0 = static_cast<uint32_t>(t) % p.m_tiles * kLinearM;
+      x.n0 = x.tile = static_cast<uint32_t>(t) / p.m_tiles;
+      if constexpr (MODE == kLinearStats) {
+        if constexpr (NB > 1)
+          while (x.r + 1 < p.shards && args.shard[x.r + 1].tile0 <= x.n0) ++x.r;
+        x.n0 -= args.shard[x.r].tile0;
+      }
+      x.n0 *= kLinearN;
     }
-    x.n0 *= kLinearN;
     return x;
   };
 
   if (warp == 0) {
     if (lane == 0) {
       uint32_t i = 0;  // stages filled so far
-      for (uint32_t t = blockIdx.x; t < tiles && !stop; t += gridDim.x) {
-        const Place x = place(t);
-        for (uint32_t kb = 0; kb < p.k_blocks; ++kb, ++i) {
+      for (uint32_t n = 0; !stop; ++n) {
+        const Place x = place(n);
+        if (!x.there) break;
+        const bool across_a = MODE == kLinearGrads && x.r == 1;
+        // (dh: the weights' rows are the inner dimension; the logits: they are the columns)
+        const int32_t off = static_cast<int32_t>(MODE == kLinearGrads && x.r == 1 ? 0 : p.b_row0);
+        for (uint32_t kb = 0; kb < x.blocks; ++kb, ++i) {
           const uint32_t st = i % kStages, bar = full + 8 * st, to = ring + st * kStageBytes;
           if (i >= kStages && !wait(waits, empty + 8 * st, (i / kStages - 1) & 1)) break;
           tma::mbar_arrive_expect_tx(bar, kStageBytes);
-          const int32_t k0 = static_cast<int32_t>(kb * kLinearK);
+          const int32_t k0 = static_cast<int32_t>((x.k0 + kb) * kLinearK);
 #pragma unroll
           for (int j = 0; j < kLinearM / 64; ++j) {
             const int32_t mj = static_cast<int32_t>(x.m0) + 64 * j;
-            load_tile(to + j * kTileBytes, &args.a, bar, kAcrossA ? mj : k0, kAcrossA ? k0 : mj);
+            load_tile(to + j * kTileBytes, &args.a, bar, across_a ? mj : k0, across_a ? k0 : mj);
           }
 #pragma unroll
           for (int j = 0; j < kLinearN / 64; ++j) {
-            const int32_t nj = static_cast<int32_t>(x.n0) + 64 * j, off = static_cast<int32_t>(p.b_row0);
+            const int32_t nj = static_cast<int32_t>(x.n0) + 64 * j;
             load_tile(to + kABytes + j * kTileBytes, &args.b[NB > 1 ? x.r : 0], bar, kAcrossB ? nj : k0,
                       kAcrossB ? k0 + off : nj + off);
           }
@@ -288,19 +324,22 @@ __global__ __launch_bounds__(kThreads, 1) void dc_linear_kernel(const __grid_con
     }
   } else if (warp == 1) {
     if (lane == 0) {
-      constexpr uint32_t idesc = instruction<DT>(kLinearM, kLinearN, (kAcrossA ? kMajorA : 0u) | (kAcrossB ? kMajorB : 0u));
-      uint32_t i = 0, n = 0;
-      for (uint32_t t = blockIdx.x; t < tiles && !stop; t += gridDim.x, ++n) {
+      uint32_t i = 0;
+      for (uint32_t n = 0; !stop; ++n) {
+        const Place x = place(n);
+        if (!x.there) break;
+        const bool across_a = MODE == kLinearGrads && x.r == 1;
+        const uint32_t idesc = instruction<DT>(kLinearM, kLinearN, (across_a ? kMajorA : 0u) | (kAcrossB ? kMajorB : 0u));
         const uint32_t buf = n & 1, acc = tmem + buf * kLinearN;
         if (n >= 2 && !wait(waits, drained + 8 * buf, (n / 2 - 1) & 1)) break;
         fence_after();
-        for (uint32_t kb = 0; kb < p.k_blocks; ++kb, ++i) {
+        for (uint32_t kb = 0; kb < x.blocks; ++kb, ++i) {
           const uint32_t st = i % kStages, a = ring + st * kStageBytes, b = a + kABytes;
           if (!wait(waits, full + 8 * st, (i / kStages) & 1)) break;
           fence_after();
 #pragma unroll
           for (int k = 0; k < kLinearK / 16; ++k)
-            mma(acc, kAcrossA ? desc_mn(a + k * 2048, kTileBytes) : desc_k(a + k * 32),
+            mma(acc, across_a ? desc_mn(a + k * 2048, kTileBytes) : desc_k(a + k * 32),
                 kAcrossB ? desc_mn(b + k * 2048, kTileBytes) : desc_k(b + k * 32), idesc, (kb | k) != 0);
           commit(empty + 8 * st);
         }
@@ -313,24 +352,25 @@ __global__ __launch_bounds__(kThreads, 1) void dc_linear_kernel(const __grid_con
     }
   } else {
     const uint32_t quarter = static_cast<uint32_t>(warp & 3) * 32;  // the lanes of tensor memory that this warp reads
-    uint32_t n = 0;
-    for (uint32_t t = blockIdx.x; t < tiles; t += gridDim.x, ++n) {
-      const Place x = place(t);
+    for (uint32_t n = 0;; ++n) {
+      const Place x = place(n);
+      if (!x.there) break;
       const uint32_t buf = n & 1, at = tmem + buf * kLinearN + (quarter << 16);
       const bool there = wait(waits, done + 8 * buf, (n / 2) & 1);
       if (!__all_sync(~0u, there)) break;
       fence_after();
       const uint64_t row = x.m0 + quarter + lane;
-      const bool own = row < p.m;
-      if (x.m0 + quarter < p.m) {
+      const uint32_t rows = MODE == kLinearGrads && x.r == 1 ? p.g.columns : p.m;
+      const bool own = row < rows;
+      if (x.m0 + quarter < rows) {
         if constexpr (MODE == kLinearStats) {
           const LinearShard& s = args.shard[NB > 1 ? x.r : 0];
           const uint32_t column0 = s.first + x.n0;
-          stats(p, at, row, own, t / p.m_tiles, column0, s.end - column0 < kLinearN ? s.end - column0 : kLinearN);
+          stats(p, at, row, own, x.tile, column0, s.end - column0 < kLinearN ? s.end - column0 : kLinearN);
         } else if constexpr (MODE == kLinearDLogits) {
           dlogits<DT>(p, at, row, own, x.n0);
         } else {
-          result<MODE, DT>(p, at, row, own, x.n0);
+          result<DT>(p, at, row, own, x.n0, x.r == 1, x.tile, x.blocks == 0);
         }
       }
       fence_before();
@@ -390,6 +430,31 @@ __global__ __launch_bounds__(kFinishThreads) void dc_linear_finish_kernel(const 
   if (p.lse) put(p.lse, (ref + log_s) * kLn2);
 }
 
+template <int DT>
+__global__ __launch_bounds__(256) void dc_linear_sum_kernel(const __grid_constant__ LinearSumParams p) {
+  pdl_enter();
+  const uint64_t per = p.size / 8, item = static_cast<uint64_t>(blockIdx.x) * 256 + threadIdx.x, row = item / per;
+  if (row >= p.rows) return;
+  const uint32_t c = static_cast<uint32_t>(item % per) * 8;
+  const float unit = p.scale ? reinterpret_cast<const float*>(p.scale)[1] : 1.0f;
+  const uint64_t slice = p.rows * p.size * 4, hi = p.acc + p.slices * slice;
+  float v[8] = {};
+#pragma unroll 4
+  for (uint32_t s = 0; s < p.slices; ++s) {
+    const float4* a = reinterpret_cast<const float4*>(p.acc + s * slice + (row * p.size + c) * 4);
+    if (!in_bounds(a, 32, p.acc, hi, kSiteAcc)) continue;
+    const float4 x = a[0], y = a[1];
+    const float w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += w[j];
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] *= unit;
+  const uint64_t out = p.out + row * p.out_stride;
+  uint4* a = reinterpret_cast<uint4*>(out + c * 2);
+  if (in_bounds(a, 16, out, out + p.size * 2ull, kSiteOut)) st16(a, repack<DT>(v));
+}
+
 // The power of two for DC_F16: no |d_j| is above (|g| + 16 |e|) / temperature,
 // as p |log p| <= 1/e and p entropy <= log DC_MAX_VOCAB < 16.
 __global__ __launch_bounds__(1024) void dc_linear_scale_kernel(uint64_t grad_logprobs, uint64_t grad_entropy, uint64_t tokens,
@@ -432,14 +497,16 @@ cudaError_t launch_one(const LinearParams& p, const LinearOperand& a, const Line
   LinearArgs<NB> args{};
   args.p = p;
   e = make_map(&args.a, DT, a.base, a.rows, a.columns, a.stride, 64);
-  const int nb = MODE == kLinearStats ? p.shards : 1;
+  const int nb = MODE == kLinearStats ? p.shards : NB;
   for (int r = 0; r < nb && e == cudaSuccess; ++r) {
     e = make_map(&args.b[r], DT, b[r].base, b[r].rows, b[r].columns, b[r].stride, 64);
     if (MODE == kLinearStats) args.shard[r] = shards[r];
   }
   if (e != cudaSuccess) return e;
-  const uint64_t tiles = static_cast<uint64_t>(p.m_tiles) * p.n_tiles;
+  const uint64_t tiles = MODE == kLinearGrads ? static_cast<uint64_t>(p.g.h_tiles) + p.g.w_tiles
+                                              : static_cast<uint64_t>(p.m_tiles) * p.n_tiles;
   *grid = static_cast<int>(tiles < static_cast<uint64_t>(sms) ? tiles : static_cast<uint64_t>(sms));
+  if constexpr (MODE == kLinearGrads) plan_linear_grads(&args.p.g, static_cast<uint32_t>(*grid));
   return launch_ex(dc_linear_kernel<MODE, DT, NB>, *grid, kThreads, pdl, s, args, kSmem);
 }
 
@@ -451,8 +518,7 @@ cudaError_t launch_mode(int mode, const LinearParams& p, const LinearOperand& a,
       return p.shards == 1 ? launch_one<kLinearStats, DT, 1>(p, a, b, shards, sms, pdl, s, grid)
                            : launch_one<kLinearStats, DT, kMaxRanks>(p, a, b, shards, sms, pdl, s, grid);
     case kLinearDLogits: return launch_one<kLinearDLogits, DT, 1>(p, a, b, shards, sms, pdl, s, grid);
-    case kLinearDHidden: return launch_one<kLinearDHidden, DT, 1>(p, a, b, shards, sms, pdl, s, grid);
-    default: return launch_one<kLinearDWeights, DT, 1>(p, a, b, shards, sms, pdl, s, grid);
+    default: return launch_one<kLinearGrads, DT, 2>(p, a, b, shards, sms, pdl, s, grid);
   }
 }
 
@@ -506,6 +572,26 @@ cudaError_t launch_linear(int mode, int dtype, const LinearParams& p, const Line
                           const LinearShard* shards, int sms, bool pdl, cudaStream_t s, int* grid) {
   return dtype == kF16 ? launch_mode<kF16>(mode, p, a, b, shards, sms, pdl, s, grid)
                        : launch_mode<kBF16>(mode, p, a, b, shards, sms, pdl, s, grid);
+}
+
+void plan_linear_grads(LinearGrads* g, uint32_t ctas) {
+  g->rounds = g->h_tiles / ctas;
+  g->rest = g->h_tiles % ctas;
+  // blocks of the inner dimension that each CTA should get in all
+  const uint64_t work = static_cast<uint64_t>(g->h_tiles) * g->slice_blocks + static_cast<uint64_t>(g->w_tiles) * g->w_blocks;
+  const uint64_t each = (work + ctas - 1) / ctas, had = (g->rounds + 1ull) * g->slice_blocks;
+  g->few = g->w_blocks && each > had ? static_cast<uint32_t>((each - had) / g->w_blocks) : 0;
+  if (g->rest == 0) g->few = 0;
+  // (g->few * ctas tiles at most: no more than there are)
+  if (static_cast<uint64_t>(g->few) * ctas > g->w_tiles) g->few = g->w_tiles / ctas;
+  const uint32_t left = g->w_tiles - g->few * ctas, on = ctas - g->rest;
+  g->many = g->few + (left + on - 1) / on;
+}
+
+cudaError_t launch_linear_sum(const LinearSumParams& p, int dtype, bool pdl, cudaStream_t s, int* grid) {
+  *grid = static_cast<int>((p.rows * (p.size / 8) + 255) / 256);
+  return dtype == kF16 ? launch_ex(dc_linear_sum_kernel<kF16>, *grid, 256, pdl, s, p)
+                       : launch_ex(dc_linear_sum_kernel<kBF16>, *grid, 256, pdl, s, p);
 }
 
 cudaError_t launch_linear_finish(const LinearFinishParams& p, bool pdl, cudaStream_t s, int* grid) {

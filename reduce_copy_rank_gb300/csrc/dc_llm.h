@@ -199,36 +199,60 @@ cudaError_t launch_attend(const AttendParams& p, int dtype, int dim, bool pdl, c
 // Matrix products on the tensor cores: tiles of kLinearM x kLinearN, kLinearK
 // of the inner dimension a stage.
 constexpr int kLinearM = 128, kLinearN = 256, kLinearK = 64;
-// The gradient takes this many columns of a shard at a time, whatever the call's
-// rows: how the products over the vocabulary are cut decides their bits.
-constexpr uint32_t kLinearChunk = 16384;
+// The gradient takes up to this many columns of a shard at a time, and cuts the
+// products over them into slices, both whatever the call's rows: how a sum is cut
+// decides its bits.
+constexpr uint32_t kLinearChunk = 24576;
+__host__ __device__ inline uint32_t linear_chunk(uint32_t width) {
+  const uint32_t n = (width + kLinearChunk - 1) / kLinearChunk, per = n ? (width + n - 1) / n : 0;
+  return (per + kLinearN - 1) / kLinearN * kLinearN;
+}
+// A row of dh has ceil(size / kLinearN) tiles: with few the sum over a chunk's
+// columns is cut into slices, so that short batches have work for the GPU too.
+__host__ __device__ inline uint32_t linear_slices(uint32_t size) {
+  const uint32_t tiles = (size + kLinearN - 1) / kLinearN;
+  return tiles >= 16 ? 1 : 16 / tiles;
+}
 
-enum : int { kLinearStats = 0, kLinearDLogits = 1, kLinearDHidden = 2, kLinearDWeights = 3 };
+enum : int { kLinearStats = 0, kLinearDLogits = 1, kLinearGrads = 2 };
 
 // Columns [first, end) of the vocabulary, in tiles from tile0 on (end: without padding).
 struct LinearShard {
   uint32_t tile0, first, end, pad;
 };
 
+// Both products of a chunk's gradient in one launch: tiles of dh = d W (in
+// slices of the chunk's columns), then tiles of dW = d^T h.  CTA c of G takes dh
+// tiles c, c + G, ..., then the first `few` rounds of dW tiles like all others;
+// those that had one dh tile less (c >= rest) go on to `many` rounds.
+struct LinearGrads {
+  uint32_t h_tiles, h_m, h_n;  // h_m * h_n * slices
+  uint32_t slice_blocks, h_blocks;
+  uint32_t w_tiles, w_m, w_blocks;
+  uint32_t rounds, rest, few, many;
+  uint32_t columns;            // of the chunk
+  int32_t add, last;           // what `acc` holds is added; the sum is complete (no acc: one slice)
+  uint64_t acc;                // f32 [slices][rows][size] or 0
+  uint64_t out_h, out_h_stride, out_w, out_w_stride;  // bytes
+};
+
 // One product C [m, n] = A B^T over k, and what becomes of it.
 struct LinearParams {
-  uint32_t m, n;               // extents of C (kLinearStats: n is not used)
+  uint32_t m, n;               // extents of C (kLinearStats: n is not used; kLinearGrads: rows and hidden size)
   uint32_t m_tiles, n_tiles, k_blocks;
-  uint32_t b_row0;             // first row of B's tensor (kLinearDLogits: of n; kLinearDHidden: of k)
+  uint32_t b_row0;             // first row of the weights (kLinearDLogits, kLinearGrads)
   uint32_t vocab, first;       // kLinearDLogits: the vocabulary index of column 0
   float inv_t;
   int32_t tokens64;
   int32_t shards;              // kLinearStats
-  int32_t add, last;           // kLinearDHidden: what `acc` holds is added; the sum is complete
   uint64_t rows;
   uint64_t tokens;
   uint64_t part, target;       // kLinearStats: f32 [tiles][rows][4], f32 [rows]
   uint64_t lse, entropy, grad_logprobs, grad_entropy;  // f32 [rows]; the last two or 0
   uint64_t scale;              // f32 [2] or 0: the gradient's power of two and its inverse
   uint64_t d, d_stride;        // kLinearDLogits: [rows] of d_stride bytes
-  uint64_t acc;                // kLinearDHidden: f32 [rows][n] or 0
-  uint64_t out, out_stride;    // kLinearDHidden, kLinearDWeights: bytes
   uint64_t wait_ns;
+  LinearGrads g;               // kLinearGrads
 };
 
 struct LinearFinishParams {
@@ -238,6 +262,13 @@ struct LinearFinishParams {
   int32_t tokens64, pad;
 };
 
+// dh from its slices' sums, which are added in order.
+struct LinearSumParams {
+  uint64_t acc, out, out_stride, scale;
+  uint64_t rows;
+  uint32_t size, slices;
+};
+
 // The operands as tensors of 16-bit rows.
 struct LinearOperand {
   uint64_t base, rows, columns, stride;  // stride in bytes
@@ -245,6 +276,9 @@ struct LinearOperand {
 cudaError_t launch_linear(int mode, int dtype, const LinearParams& p, const LinearOperand& a, const LinearOperand* b,
                           const LinearShard* shards, int sms, bool pdl, cudaStream_t s, int* grid);
 cudaError_t launch_linear_finish(const LinearFinishParams& p, bool pdl, cudaStream_t s, int* grid);
+cudaError_t launch_linear_sum(const LinearSumParams& p, int dtype, bool pdl, cudaStream_t s, int* grid);
+// Fills the schedule of p.g for `ctas` CTAs.
+void plan_linear_grads(LinearGrads* g, uint32_t ctas);
 cudaError_t launch_linear_scale(uint64_t grad_logprobs, uint64_t grad_entropy, uint64_t tokens, bool tokens64, uint64_t rows,
                                 float inv_t, uint64_t scale, bool pdl, cudaStream_t s);
 

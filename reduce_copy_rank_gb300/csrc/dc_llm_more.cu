@@ -74,8 +74,8 @@ dc_status_t check_head(const void* hidden, uint64_t hidden_stride, const void* c
 // The forward's workspace: every tile's parts, then the tokens' logits.
 uint64_t stats_bytes(uint64_t rows, uint64_t tiles) { return rows * (tiles * 16 + 4); }
 // The gradient's: its power of two, then d of one chunk of the vocabulary, then
-// the sum of d W.
-uint64_t chunk_stride(uint64_t columns) { return round_up(std::min<uint64_t>(columns, kLinearChunk), 64) * 2; }
+// the sums of d W, a slice each.
+uint64_t chunk_stride(uint64_t columns) { return round_up(std::min<uint64_t>(columns, kLinearChunk), kLinearN) * 2; }
 uint64_t d_bytes(uint64_t rows, uint64_t stride) { return round_up(rows * stride, 256); }
 
 dc_status_t check_workspace(void* p, uint64_t have, uint64_t need, Spans& out) {
@@ -196,7 +196,8 @@ size_t dc_linear_logprobs_workspace_bytes(int64_t rows, int64_t hidden_size, int
   const uint64_t n = static_cast<uint64_t>(std::max<int64_t>(rows, 1)), v = static_cast<uint64_t>(columns);
   // (a shard's last tile may be narrower: at most one more tile a rank)
   if (!backward) return round_up(stats_bytes(n, (v + kLinearN - 1) / kLinearN + kMaxRanks), 256);
-  return 256 + d_bytes(n, chunk_stride(v)) + round_up(n * static_cast<uint64_t>(hidden_size) * 4, 256);
+  return 256 + d_bytes(n, chunk_stride(v)) +
+         round_up(n * static_cast<uint64_t>(hidden_size) * 4 * linear_slices(static_cast<uint32_t>(hidden_size)), 256);
 }
 
 dc_status_t dc_linear_logprobs(const dc_linear_logprobs_t* a, dc_stream_t stream) {
@@ -286,8 +287,8 @@ dc_status_t dc_linear_logprobs_backward(const dc_linear_logprobs_backward_t* a, 
       DC_TRY(check_matrix(a->grad_weights[r], a->widths[r], size, a->grad_weight_row_strides[r], "grad_weights", r, &m));
     gw.add(m);
     const uint64_t held = first < vocab ? std::min<uint64_t>(a->widths[r], vocab - first) : 0;
-    widest = std::max(widest, held);
-    chunks += (held + kLinearChunk - 1) / kLinearChunk;
+    widest = std::max<uint64_t>(widest, linear_chunk(static_cast<uint32_t>(held)));
+    if (held) chunks += (held + linear_chunk(static_cast<uint32_t>(held)) - 1) / linear_chunk(static_cast<uint32_t>(held));
     first += a->widths[r];
   }
   auto apart = [&](const Strided& x, const char* name, int r) -> dc_status_t {
@@ -304,7 +305,8 @@ dc_status_t dc_linear_logprobs_backward(const dc_linear_logprobs_backward_t* a, 
   for (int r = 0; r < gw.n; ++r) DC_TRY(apart(gw[r], "grad_weights", r));
   Spans out;
   const uint64_t stride = chunk_stride(widest);
-  const bool sum = want_h && chunks > 1;
+  const uint32_t slices = linear_slices(static_cast<uint32_t>(size));
+  const bool sum = want_h && (chunks > 1 || slices > 1);
   if (n) {
     DC_TRY(take(a->lse, "lse", n * 4, 4, h.in));
     if (a->grad_logprobs) DC_TRY(take(a->grad_logprobs, "grad_logprobs", n * 4, 4, h.in));
@@ -312,7 +314,7 @@ dc_status_t dc_linear_logprobs_backward(const dc_linear_logprobs_backward_t* a, 
       DC_TRY(take(a->grad_entropy, "grad_entropy", n * 4, 4, h.in));
       DC_TRY(take(a->entropy, "entropy", n * 4, 4, h.in));
     }
-    DC_TRY(check_workspace(a->workspace, a->workspace_bytes, 256 + d_bytes(n, stride) + (sum ? n * size * 4 : 0), out));
+    DC_TRY(check_workspace(a->workspace, a->workspace_bytes, 256 + d_bytes(n, stride) + (sum ? n * size * 4 * slices : 0), out));
     DC_TRY(check_head_outputs(out, h));
     Shards written = gw;
     DC_TRY(outside_shards(out, written, "a shard of grad_weights"));
@@ -339,7 +341,7 @@ dc_status_t dc_linear_logprobs_backward(const dc_linear_logprobs_backward_t* a, 
   p.grad_entropy = addr(a->grad_entropy);
   p.d = addr(a->workspace) + 256;
   p.d_stride = stride;
-  p.acc = sum ? p.d + d_bytes(n, stride) : 0;
+  const uint64_t acc = sum ? p.d + d_bytes(n, stride) : 0;
   p.wait_ns = wait_limit_option();
   if (n && a->dtype == kF16) {
     p.scale = addr(a->workspace);
@@ -360,8 +362,9 @@ dc_status_t dc_linear_logprobs_backward(const dc_linear_logprobs_backward_t* a, 
         return fail(DC_ERR_CUDA, "clearing the padding's gradient failed: %s", cudaGetErrorString(e));
       }
     }
-    for (uint64_t c = 0; c < held; c += kLinearChunk, ++chunk) {
-      const uint32_t columns = static_cast<uint32_t>(std::min<uint64_t>(kLinearChunk, held - c));
+    const uint64_t step = linear_chunk(static_cast<uint32_t>(held));
+    for (uint64_t c = 0; c < held; c += step, ++chunk) {
+      const uint32_t columns = static_cast<uint32_t>(std::min<uint64_t>(step, held - c));
       const LinearOperand w{h.weights[r].base, c + columns, size, h.weights[r].stride};
       const LinearOperand d{p.d, n, columns, stride};
       LinearParams l = p;
@@ -374,34 +377,36 @@ dc_status_t dc_linear_logprobs_backward(const dc_linear_logprobs_backward_t* a, 
       l.first = static_cast<uint32_t>(at + c);
       cudaError_t e = launch_linear(kLinearDLogits, a->dtype, l, x, &w, nullptr, sms, pdl, s, &grid);
       DC_TRY(check_launch(e, "a linear head's gradient", grid));
-      if (want_h) {
-        LinearParams q = p;
-        q.m = static_cast<uint32_t>(n);
-        q.n = static_cast<uint32_t>(size);
-        q.m_tiles = m_rows;
-        q.n_tiles = size_tiles;
-        q.k_blocks = (columns + kLinearK - 1) / kLinearK;
-        q.b_row0 = static_cast<uint32_t>(c);
-        q.add = chunk > 0;
-        q.last = chunk + 1 == chunks;
-        q.out = gh.base;
-        q.out_stride = gh.stride;
-        e = launch_linear(kLinearDHidden, a->dtype, q, d, &w, nullptr, sms, pdl, s, &grid);
-        DC_TRY(check_launch(e, "a linear head's gradient", grid));
-      }
-      if (want_w) {
-        LinearParams q = p;
-        q.m = columns;
-        q.n = static_cast<uint32_t>(size);
-        q.m_tiles = (columns + kLinearM - 1) / kLinearM;
-        q.n_tiles = size_tiles;
-        q.k_blocks = static_cast<uint32_t>((n + kLinearK - 1) / kLinearK);
-        q.out = gw[r].base + c * gw[r].stride;
-        q.out_stride = gw[r].stride;
-        e = launch_linear(kLinearDWeights, a->dtype, q, d, &x, nullptr, sms, pdl, s, &grid);
-        DC_TRY(check_launch(e, "a linear head's gradient", grid));
-      }
+      LinearParams q = p;
+      q.m = static_cast<uint32_t>(n);
+      q.n = static_cast<uint32_t>(size);
+      q.b_row0 = static_cast<uint32_t>(c);
+      LinearGrads& g = q.g;
+      g.columns = columns;
+      g.h_blocks = (columns + kLinearK - 1) / kLinearK;
+      g.slice_blocks = (g.h_blocks + slices - 1) / slices;
+      g.h_m = m_rows;
+      g.h_n = size_tiles;
+      g.h_tiles = want_h ? m_rows * size_tiles * slices : 0;
+      g.w_m = (columns + kLinearM - 1) / kLinearM;
+      g.w_blocks = static_cast<uint32_t>((n + kLinearK - 1) / kLinearK);
+      g.w_tiles = want_w ? g.w_m * size_tiles : 0;
+      g.add = chunk > 0;
+      g.last = slices == 1 && chunk + 1 == chunks;
+      g.acc = acc;
+      g.out_h = gh.base;
+      g.out_h_stride = gh.stride;
+      g.out_w = gw[r].base + c * gw[r].stride;
+      g.out_w_stride = gw[r].stride;
+      const LinearOperand b[2] = {w, x};
+      e = launch_linear(kLinearGrads, a->dtype, q, d, b, nullptr, sms, pdl, s, &grid);
+      DC_TRY(check_launch(e, "a linear head's gradient", grid));
     }
+  }
+  if (want_h && n && slices > 1) {
+    const LinearSumParams f{acc, gh.base, gh.stride, p.scale, n, static_cast<uint32_t>(size), slices};
+    const cudaError_t e = launch_linear_sum(f, a->dtype, pdl, s, &grid);
+    return check_launch(e, "a linear head's gradient", grid);
   }
   return ok();
 }

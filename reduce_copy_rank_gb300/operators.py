@@ -347,7 +347,7 @@ def linear_logprobs_backward(hidden, weights: Sequence, tokens, lse, grad_logpro
     ``grad_entropy``); the upstream gradients are float32 [rows], either may be
     None.
 
-    The logits are computed again, 16384 columns at a time; their gradient is
+    The logits are computed again, up to 24576 columns at a time; their gradient is
     rounded to 16 bits before its products, whose sums are binary32.  Rows of
     the weights' gradient past ``vocab`` receive 0.  ``workspace``:
     :func:`linear_logprobs_workspace` with ``backward``.  Returns
