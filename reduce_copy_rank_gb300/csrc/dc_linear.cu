@@ -8,8 +8,10 @@
 // dh = d W, dW = d^T h.
 //
 // The products run on the tensor cores (tcgen05.mma, operands by TMA, binary32
-// accumulators in tensor memory).  A CTA takes tiles of 128 x 256 in turn; while
-// one is computed four warps reduce the one before from tensor memory:
+// accumulators in tensor memory).  A pair of CTAs on two SMs takes tiles of 256 x
+// 256 in turn, each with 128 of the rows and half of B's columns in its shared
+// memory; while one is computed eight warps reduce the one before from tensor
+// memory:
 //  * forward: a row's part of the tile as its maximum (rounded up to a whole
 //    number r in units of log2), sum 2^(z-r) and sum 2^(z-r) (z-r), written as
 //    16 bytes; a second kernel adds a row's parts up in one fixed order, which
@@ -26,6 +28,7 @@
 // still a normal number.
 //
 // Bound: the tensor cores for training batches, the weights' bytes for few rows.
+#include <algorithm>
 #include <atomic>
 
 #include "dc_llm.h"
@@ -41,12 +44,14 @@ enum : uint32_t { kSitePart = 1, kSiteRow = 2, kSiteD = 3, kSiteAcc = 4, kSiteOu
 
 __device__ unsigned int g_linear_fault_bits;
 
-constexpr int kStages = 4;
+constexpr int kStages = 6;
 constexpr int kTileBytes = 64 * 128;                  // 64 rows of 64 elements: what one TMA copy loads
-constexpr int kABytes = kLinearM / 64 * kTileBytes, kBBytes = kLinearN / 64 * kTileBytes;
-constexpr int kStageBytes = kABytes + kBBytes;
+constexpr int kHalfM = kLinearM / 2, kHalfN = kLinearN / 2;  // a CTA's rows of A and of B
+constexpr int kABytes = kHalfM / 64 * kTileBytes, kBBytes = kHalfN / 64 * kTileBytes;
+constexpr int kStageBytes = kABytes + kBBytes;        // of one CTA
 constexpr int kSmem = kStages * kStageBytes + 1024;   // (the ring starts at a multiple of 1024)
-constexpr int kThreads = 192;                         // loads, products, four warps of results
+constexpr int kResultThreads = 256;                   // eight warps of results: a row and half of the columns a thread
+constexpr int kThreads = 64 + kResultThreads;         // one warp loads, one issues products
 constexpr uint32_t kColumns = 2 * kLinearN;           // of tensor memory: two tiles' accumulators
 
 template <int NB>
@@ -65,16 +70,16 @@ __device__ __forceinline__ float ld_row(uint64_t base, uint64_t row, uint64_t ro
 }
 
 // ------------------------------------------------------------- the results ---
-// Each runs in a thread that has row `row` of C (of rows0 = kLinearM tile rows)
-// and the tile's accumulators at `at` in tensor memory.
+// Each runs in a thread that has row `row` of C and kLinearPart columns of the
+// tile's accumulators from `at` on in tensor memory.
 
-// Forward: one row's part of a tile.  limit: the tile's columns that exist.
-__device__ __forceinline__ void stats(const LinearParams& p, uint32_t at, uint64_t row, bool own, uint32_t tile,
+// Forward: one row's part of a tile.  limit: its columns that exist.
+__device__ __forceinline__ void stats(const LinearParams& p, uint32_t at, uint64_t row, bool own, uint32_t part,
                                       uint32_t column0, uint32_t limit) {
   const float c = p.inv_t * kLog2E;
   float top = neg_inf();
 #pragma unroll 1
-  for (uint32_t j0 = 0; j0 < kLinearN; j0 += 32) {
+  for (uint32_t j0 = 0; j0 < kLinearPart; j0 += 32) {
     if (j0 >= limit) break;
     float v[32];
     tmem_ld32(at + j0, v);
@@ -91,7 +96,7 @@ __device__ __forceinline__ void stats(const LinearParams& p, uint32_t at, uint64
   const int64_t token = own ? token_of(p.tokens, p.tokens64, row) : -1;
   const int64_t mine = token - static_cast<int64_t>(column0);  // the token's column in this tile, if it has it
 #pragma unroll 1
-  for (uint32_t j0 = 0; j0 < kLinearN; j0 += 32) {
+  for (uint32_t j0 = 0; j0 < kLinearPart; j0 += 32) {
     if (j0 >= limit) break;
     float v[32];
     tmem_ld32(at + j0, v);
@@ -109,8 +114,8 @@ __device__ __forceinline__ void stats(const LinearParams& p, uint32_t at, uint64
     }
   }
   if (!own) return;
-  float4* a = reinterpret_cast<float4*>(p.part) + static_cast<uint64_t>(tile) * p.rows + row;
-  if (in_bounds(a, 16, p.part, p.part + static_cast<uint64_t>(p.n_tiles) * p.rows * 16, kSitePart))
+  float4* a = reinterpret_cast<float4*>(p.part) + static_cast<uint64_t>(part) * p.rows + row;
+  if (in_bounds(a, 16, p.part, p.target, kSitePart))
     *a = make_float4(ref, (s[0] + s[1]) + (s[2] + s[3]), (t[0] + t[1]) + (t[2] + t[3]), 0.0f);
 }
 
@@ -149,7 +154,7 @@ __device__ __forceinline__ void dlogits(const LinearParams& p, uint32_t at, uint
   const uint32_t exist = p.vocab > p.first + n0 ? p.vocab - p.first - n0 : 0;  // columns before the padding
   const uint64_t lo = p.d + row * p.d_stride;
 #pragma unroll 1
-  for (uint32_t j0 = 0; j0 < kLinearN && n0 + j0 < ld; j0 += 32) {
+  for (uint32_t j0 = 0; j0 < kLinearPart && n0 + j0 < ld; j0 += 32) {
     float v[32];
     tmem_ld32(at + j0, v);
 #pragma unroll
@@ -174,7 +179,7 @@ __device__ __forceinline__ void result(const LinearParams& p, uint32_t at, uint6
   const uint64_t acc_lo = g.acc + static_cast<uint64_t>(slice) * p.rows * p.n * 4, acc_hi = acc_lo + p.rows * p.n * 4;
   const bool sums = !weights && g.acc, add = sums && g.add, last = !sums || g.last;
 #pragma unroll 1
-  for (uint32_t j0 = 0; j0 < kLinearN && n0 + j0 < p.n; j0 += 32) {
+  for (uint32_t j0 = 0; j0 < kLinearPart && n0 + j0 < p.n; j0 += 32) {
     float v[32];
     tmem_ld32(at + j0, v);
     if (!own) continue;
@@ -221,6 +226,7 @@ __global__ __launch_bounds__(kThreads, 1) void dc_linear_kernel(const __grid_con
   const uint32_t ring = (smem_addr(smem) + 1023u) & ~1023u;
   const uint32_t full = smem_addr(bars), empty = full + 8 * kStages;
   const uint32_t done = empty + 8 * kStages, drained = done + 16, over = drained + 16;
+  const uint32_t rank = cluster_rank();
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       tma::mbar_init(full + 8 * i, 1);
@@ -228,7 +234,7 @@ __global__ __launch_bounds__(kThreads, 1) void dc_linear_kernel(const __grid_con
     }
     for (int i = 0; i < 2; ++i) {
       tma::mbar_init(done + 8 * i, 1);
-      tma::mbar_init(drained + 8 * i, 128);
+      tma::mbar_init(drained + 8 * i, 2 * kResultThreads);
     }
     tma::mbar_init(over, 1);
     tma::mbar_init_fence();
@@ -236,16 +242,18 @@ __global__ __launch_bounds__(kThreads, 1) void dc_linear_kernel(const __grid_con
     prefetch_map(&args.a);
     prefetch_map(&args.b[0]);
   }
-  if (warp == 1) tmem_alloc(smem_addr(&tmem_at), kColumns);
+  __syncwarp();
+  if (warp == 1) tmem_alloc_pair(smem_addr(&tmem_at), kColumns);
   fence_before();
   __syncthreads();
+  cluster_barrier();  // (each CTA's barriers are used by the other)
   fence_after();
   const uint32_t tmem = tmem_at;
   pdl_enter();
   tma::fence_proxy_async_global();  // (the operands may be an earlier kernel's stores)
 
   const Waits waits{&stop, p.wait_ns};
-  // This CTA's n-th tile: its rows, its columns, the tensor that those belong to,
+  // This pair's n-th tile: its rows, its columns, the tensor that those belong to,
   // its blocks of the inner dimension.
   struct Place {
     uint32_t m0, n0, k0, blocks;
@@ -255,7 +263,7 @@ __global__ __launch_bounds__(kThreads, 1) void dc_linear_kernel(const __grid_con
   };
   auto place = [&](uint32_t n) {
     Place x{0, 0, 0, p.k_blocks, 0, 0, true};
-    const uint32_t c = blockIdx.x, G = gridDim.x;
+    const uint32_t c = blockIdx.x / 2, G = gridDim.x / 2;
     if constexpr (MODE == kLinearGrads) {
       const LinearGrads& g = p.g;
       const uint32_t mine = g.rounds + (c < g.rest);
@@ -301,29 +309,31 @@ __global__ __launch_bounds__(kThreads, 1) void dc_linear_kernel(const __grid_con
         for (uint32_t kb = 0; kb < x.blocks; ++kb, ++i) {
           const uint32_t st = i % kStages, bar = full + 8 * st, to = ring + st * kStageBytes;
           if (i >= kStages && !wait(waits, empty + 8 * st, (i / kStages - 1) & 1)) break;
-          tma::mbar_arrive_expect_tx(bar, kStageBytes);
+          // (the products wait at the even CTA, for both CTAs' operands)
+          if (rank == 0) tma::mbar_arrive_expect_tx(bar, 2 * kStageBytes);
+          const uint32_t told = cluster_addr(bar, 0);
           const int32_t k0 = static_cast<int32_t>((x.k0 + kb) * kLinearK);
 #pragma unroll
-          for (int j = 0; j < kLinearM / 64; ++j) {
-            const int32_t mj = static_cast<int32_t>(x.m0) + 64 * j;
-            load_tile(to + j * kTileBytes, &args.a, bar, across_a ? mj : k0, across_a ? k0 : mj);
+          for (int j = 0; j < kHalfM / 64; ++j) {
+            const int32_t mj = static_cast<int32_t>(x.m0 + rank * kHalfM) + 64 * j;
+            load_tile_pair(to + j * kTileBytes, &args.a, told, across_a ? mj : k0, across_a ? k0 : mj);
           }
 #pragma unroll
-          for (int j = 0; j < kLinearN / 64; ++j) {
-            const int32_t nj = static_cast<int32_t>(x.n0) + 64 * j;
-            load_tile(to + kABytes + j * kTileBytes, &args.b[NB > 1 ? x.r : 0], bar, kAcrossB ? nj : k0,
-                      kAcrossB ? k0 + off : nj + off);
+          for (int j = 0; j < kHalfN / 64; ++j) {
+            const int32_t nj = static_cast<int32_t>(x.n0 + rank * kHalfN) + 64 * j;
+            load_tile_pair(to + kABytes + j * kTileBytes, &args.b[NB > 1 ? x.r : 0], told, kAcrossB ? nj : k0,
+                           kAcrossB ? k0 + off : nj + off);
           }
         }
       }
-      if (stop) {  // no copy may land after this CTA's shared memory is gone
+      if (stop && rank == 0) {  // no copy may land after the CTAs' shared memory is gone
         const uint32_t from = i > kStages ? i - kStages : 0;
         for (uint32_t k = from; k < i; ++k)
           tma::mbar_wait_bounded(full + 8 * (k % kStages), (k / kStages) & 1, p.wait_ns);
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (lane == 0 && rank == 0) {
       uint32_t i = 0;
       for (uint32_t n = 0; !stop; ++n) {
         const Place x = place(n);
@@ -339,51 +349,53 @@ __global__ __launch_bounds__(kThreads, 1) void dc_linear_kernel(const __grid_con
           fence_after();
 #pragma unroll
           for (int k = 0; k < kLinearK / 16; ++k)
-            mma(acc, across_a ? desc_mn(a + k * 2048, kTileBytes) : desc_k(a + k * 32),
+            mma_pair(acc, across_a ? desc_mn(a + k * 2048, kTileBytes) : desc_k(a + k * 32),
                 kAcrossB ? desc_mn(b + k * 2048, kTileBytes) : desc_k(b + k * 32), idesc, (kb | k) != 0);
-          commit(empty + 8 * st);
+          commit_pair(empty + 8 * st);
         }
-        commit(done + 8 * buf);
+        commit_pair(done + 8 * buf);
       }
       if (stop) {
-        commit(over);
+        commit_pair(over);
         tma::mbar_wait_bounded(over, 0, p.wait_ns);
       }
     }
   } else {
-    const uint32_t quarter = static_cast<uint32_t>(warp & 3) * 32;  // the lanes of tensor memory that this warp reads
+    // the lanes of tensor memory that this warp reads, and which half of the columns
+    const uint32_t quarter = static_cast<uint32_t>(warp & 3) * 32, half = static_cast<uint32_t>(warp - 2) / 4;
     for (uint32_t n = 0;; ++n) {
       const Place x = place(n);
       if (!x.there) break;
-      const uint32_t buf = n & 1, at = tmem + buf * kLinearN + (quarter << 16);
+      const uint32_t buf = n & 1, at = tmem + buf * kLinearN + half * kLinearPart + (quarter << 16);
       const bool there = wait(waits, done + 8 * buf, (n / 2) & 1);
       if (!__all_sync(~0u, there)) break;
       fence_after();
-      const uint64_t row = x.m0 + quarter + lane;
+      const uint32_t row0 = x.m0 + rank * kHalfM + quarter, n0 = x.n0 + half * kLinearPart;
+      const uint64_t row = row0 + lane;
       const uint32_t rows = MODE == kLinearGrads && x.r == 1 ? p.g.columns : p.m;
       const bool own = row < rows;
-      if (x.m0 + quarter < rows) {
+      if (row0 < rows) {
         if constexpr (MODE == kLinearStats) {
           const LinearShard& s = args.shard[NB > 1 ? x.r : 0];
-          const uint32_t column0 = s.first + x.n0;
-          stats(p, at, row, own, x.tile, column0, s.end - column0 < kLinearN ? s.end - column0 : kLinearN);
+          const uint32_t column0 = s.first + n0;
+          stats(p, at, row, own, 2 * x.tile + half, column0, column0 < s.end ? min(s.end - column0, static_cast<uint32_t>(kLinearPart)) : 0u);
         } else if constexpr (MODE == kLinearDLogits) {
-          dlogits<DT>(p, at, row, own, x.n0);
+          dlogits<DT>(p, at, row, own, n0);
         } else {
-          result<DT>(p, at, row, own, x.n0, x.r == 1, x.tile, x.blocks == 0);
+          result<DT>(p, at, row, own, n0, x.r == 1, x.tile, x.blocks == 0);
         }
       }
       fence_before();
-      mbar_arrive(drained + 8 * buf);
+      arrive_cluster(cluster_addr(drained + 8 * buf, 0));
     }
   }
   __syncwarp();
   __syncthreads();
   if (threadIdx.x == 0 && stop) atomicOr(&g_linear_fault_bits, kFaultTensorWait);
-  if (warp == 1) {
-    fence_after();
-    tmem_free(tmem, kColumns);
-  }
+  fence_before();
+  cluster_barrier();  // no CTA leaves while the other's products read its shared memory, or its barriers are told
+  fence_after();
+  if (warp == 1) tmem_free_pair(tmem, kColumns);
 }
 
 // One warp adds a row's parts up: lane l takes parts l, l + 32, ..., then the
@@ -404,9 +416,9 @@ __global__ __launch_bounds__(kFinishThreads) void dc_linear_finish_kernel(const 
     s = __fmaf_rn(f0, s, f1 * s1);
     ref = m;
   };
-  for (uint32_t i = lane; i < p.tiles; i += 32) {
+  for (uint32_t i = lane; i < p.parts; i += 32) {
     const float4* a = reinterpret_cast<const float4*>(p.part) + static_cast<uint64_t>(i) * p.rows + row;
-    const float4 x = in_bounds(a, 16, p.part, p.part + static_cast<uint64_t>(p.tiles) * p.rows * 16, kSitePart)
+    const float4 x = in_bounds(a, 16, p.part, p.part + static_cast<uint64_t>(p.parts) * p.rows * 16, kSitePart)
                          ? *a : make_float4(neg_inf(), 0.0f, 0.0f, 0.0f);
     add(x.x, x.y, x.z);
   }
@@ -505,9 +517,24 @@ cudaError_t launch_one(const LinearParams& p, const LinearOperand& a, const Line
   if (e != cudaSuccess) return e;
   const uint64_t tiles = MODE == kLinearGrads ? static_cast<uint64_t>(p.g.h_tiles) + p.g.w_tiles
                                               : static_cast<uint64_t>(p.m_tiles) * p.n_tiles;
-  *grid = static_cast<int>(tiles < static_cast<uint64_t>(sms) ? tiles : static_cast<uint64_t>(sms));
-  if constexpr (MODE == kLinearGrads) plan_linear_grads(&args.p.g, static_cast<uint32_t>(*grid));
-  return launch_ex(dc_linear_kernel<MODE, DT, NB>, *grid, kThreads, pdl, s, args, kSmem);
+  const uint64_t pairs = std::min<uint64_t>(tiles, static_cast<uint64_t>(std::max(sms / 2, 1)));
+  if constexpr (MODE == kLinearGrads) plan_linear_grads(&args.p.g, static_cast<uint32_t>(pairs));
+  *grid = static_cast<int>(2 * pairs);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(*grid));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, dc_linear_kernel<MODE, DT, NB>, args);
 }
 
 template <int DT>
@@ -574,17 +601,17 @@ cudaError_t launch_linear(int mode, int dtype, const LinearParams& p, const Line
                        : launch_mode<kBF16>(mode, p, a, b, shards, sms, pdl, s, grid);
 }
 
-void plan_linear_grads(LinearGrads* g, uint32_t ctas) {
-  g->rounds = g->h_tiles / ctas;
-  g->rest = g->h_tiles % ctas;
-  // blocks of the inner dimension that each CTA should get in all
+void plan_linear_grads(LinearGrads* g, uint32_t pairs) {
+  g->rounds = g->h_tiles / pairs;
+  g->rest = g->h_tiles % pairs;
+  // blocks of the inner dimension that each pair should get in all
   const uint64_t work = static_cast<uint64_t>(g->h_tiles) * g->slice_blocks + static_cast<uint64_t>(g->w_tiles) * g->w_blocks;
-  const uint64_t each = (work + ctas - 1) / ctas, had = (g->rounds + 1ull) * g->slice_blocks;
+  const uint64_t each = (work + pairs - 1) / pairs, had = (g->rounds + 1ull) * g->slice_blocks;
   g->few = g->w_blocks && each > had ? static_cast<uint32_t>((each - had) / g->w_blocks) : 0;
   if (g->rest == 0) g->few = 0;
-  // (g->few * ctas tiles at most: no more than there are)
-  if (static_cast<uint64_t>(g->few) * ctas > g->w_tiles) g->few = g->w_tiles / ctas;
-  const uint32_t left = g->w_tiles - g->few * ctas, on = ctas - g->rest;
+  // (g->few * pairs tiles at most: no more than there are)
+  if (static_cast<uint64_t>(g->few) * pairs > g->w_tiles) g->few = g->w_tiles / pairs;
+  const uint32_t left = g->w_tiles - g->few * pairs, on = pairs - g->rest;
   g->many = g->few + (left + on - 1) / on;
 }
 

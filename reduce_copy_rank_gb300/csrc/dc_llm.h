@@ -196,9 +196,10 @@ __host__ __device__ inline int attend_head_block(int group, uint64_t kv_units, u
 cudaError_t launch_attend(const AttendParams& p, int dtype, int dim, bool pdl, cudaStream_t s, int* grid);
 
 // ------------------------------------------- log probabilities of a linear head
-// Matrix products on the tensor cores: tiles of kLinearM x kLinearN, kLinearK
-// of the inner dimension a stage.
-constexpr int kLinearM = 128, kLinearN = 256, kLinearK = 64;
+// Matrix products on the tensor cores: tiles of kLinearM x kLinearN, which a pair
+// of CTAs share, kLinearK of the inner dimension a stage.
+constexpr int kLinearM = 256, kLinearN = 256, kLinearK = 64;
+constexpr int kLinearPart = 128;  // columns that one thread reduces of a row of the logits
 // The gradient takes up to this many columns of a shard at a time, and cuts the
 // products over them into slices, both whatever the call's rows: how a sum is cut
 // decides its bits.
@@ -222,7 +223,7 @@ struct LinearShard {
 };
 
 // Both products of a chunk's gradient in one launch: tiles of dh = d W (in
-// slices of the chunk's columns), then tiles of dW = d^T h.  CTA c of G takes dh
+// slices of the chunk's columns), then tiles of dW = d^T h.  CTA pair c of G takes dh
 // tiles c, c + G, ..., then the first `few` rounds of dW tiles like all others;
 // those that had one dh tile less (c >= rest) go on to `many` rounds.
 struct LinearGrads {
@@ -247,7 +248,7 @@ struct LinearParams {
   int32_t shards;              // kLinearStats
   uint64_t rows;
   uint64_t tokens;
-  uint64_t part, target;       // kLinearStats: f32 [tiles][rows][4], f32 [rows]
+  uint64_t part, target;       // kLinearStats: f32 [2 tiles][rows][4], f32 [rows]
   uint64_t lse, entropy, grad_logprobs, grad_entropy;  // f32 [rows]; the last two or 0
   uint64_t scale;              // f32 [2] or 0: the gradient's power of two and its inverse
   uint64_t d, d_stride;        // kLinearDLogits: [rows] of d_stride bytes
@@ -258,7 +259,7 @@ struct LinearParams {
 struct LinearFinishParams {
   uint64_t part, target, tokens, logprobs, entropy, lse;  // the last three f32 [rows], two of them or 0
   uint64_t rows;
-  uint32_t tiles, vocab;
+  uint32_t parts, vocab;
   int32_t tokens64, pad;
 };
 
@@ -277,8 +278,8 @@ cudaError_t launch_linear(int mode, int dtype, const LinearParams& p, const Line
                           const LinearShard* shards, int sms, bool pdl, cudaStream_t s, int* grid);
 cudaError_t launch_linear_finish(const LinearFinishParams& p, bool pdl, cudaStream_t s, int* grid);
 cudaError_t launch_linear_sum(const LinearSumParams& p, int dtype, bool pdl, cudaStream_t s, int* grid);
-// Fills the schedule of p.g for `ctas` CTAs.
-void plan_linear_grads(LinearGrads* g, uint32_t ctas);
+// Fills the schedule of p.g for `pairs` CTA pairs.
+void plan_linear_grads(LinearGrads* g, uint32_t pairs);
 cudaError_t launch_linear_scale(uint64_t grad_logprobs, uint64_t grad_entropy, uint64_t tokens, bool tokens64, uint64_t rows,
                                 float inv_t, uint64_t scale, bool pdl, cudaStream_t s);
 

@@ -72,7 +72,7 @@ dc_status_t check_head(const void* hidden, uint64_t hidden_stride, const void* c
 }
 
 // The forward's workspace: every tile's parts, then the tokens' logits.
-uint64_t stats_bytes(uint64_t rows, uint64_t tiles) { return rows * (tiles * 16 + 4); }
+uint64_t stats_bytes(uint64_t rows, uint64_t tiles) { return rows * (tiles * (kLinearN / kLinearPart) * 16 + 4); }
 // The gradient's: its power of two, then d of one chunk of the vocabulary, then
 // the sums of d W, a slice each.
 uint64_t chunk_stride(uint64_t columns) { return round_up(std::min<uint64_t>(columns, kLinearChunk), kLinearN) * 2; }
@@ -240,7 +240,7 @@ dc_status_t dc_linear_logprobs(const dc_linear_logprobs_t* a, dc_stream_t stream
   p.rows = n;
   p.tokens = addr(a->tokens);
   p.part = addr(a->workspace);
-  p.target = p.part + tiles * n * 16;
+  p.target = p.part + tiles * (kLinearN / kLinearPart) * n * 16;
   p.wait_ns = wait_limit_option();
   const LinearOperand x{h.hidden.base, n, size, h.hidden.stride};
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -255,7 +255,7 @@ dc_status_t dc_linear_logprobs(const dc_linear_logprobs_t* a, dc_stream_t stream
   f.entropy = addr(a->entropy);
   f.lse = addr(a->lse);
   f.rows = n;
-  f.tiles = p.n_tiles;
+  f.parts = p.n_tiles * (kLinearN / kLinearPart);
   f.vocab = p.vocab;
   f.tokens64 = p.tokens64;
   e = launch_linear_finish(f, pdl_option(), s, &grid);
