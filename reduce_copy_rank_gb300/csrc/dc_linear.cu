@@ -398,14 +398,14 @@ __global__ __launch_bounds__(kThreads, 1) void dc_linear_kernel(const __grid_con
   if (warp == 1) tmem_free_pair(tmem, kColumns);
 }
 
-// One warp adds a row's parts up: lane l takes parts l, l + 32, ..., then the
-// lanes join in pairs.
+// A CTA adds a row's parts up: thread t takes parts t, t + 128, ..., then the lanes
+// join in pairs and the warps in order.
 constexpr int kFinishThreads = 128;
 __global__ __launch_bounds__(kFinishThreads) void dc_linear_finish_kernel(const __grid_constant__ LinearFinishParams p) {
   pdl_enter();
-  const uint64_t row = static_cast<uint64_t>(blockIdx.x) * (kFinishThreads / 32) + (threadIdx.x >> 5);
-  const uint32_t lane = threadIdx.x & 31;
-  if (row >= p.rows) return;
+  __shared__ float4 joined[kFinishThreads / 32];
+  const uint64_t row = blockIdx.x;
+  const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float ref = neg_inf(), s = 0.0f, t = 0.0f;
   auto add = [&](float r, float s1, float t1) {
     // t = sum 2^(z-ref) (z-ref): moving ref by k adds k times the sum
@@ -416,18 +416,29 @@ __global__ __launch_bounds__(kFinishThreads) void dc_linear_finish_kernel(const 
     s = __fmaf_rn(f0, s, f1 * s1);
     ref = m;
   };
-  for (uint32_t i = lane; i < p.parts; i += 32) {
-    const float4* a = reinterpret_cast<const float4*>(p.part) + static_cast<uint64_t>(i) * p.rows + row;
-    const float4 x = in_bounds(a, 16, p.part, p.part + static_cast<uint64_t>(p.parts) * p.rows * 16, kSitePart)
-                         ? *a : make_float4(neg_inf(), 0.0f, 0.0f, 0.0f);
-    add(x.x, x.y, x.z);
+  constexpr int kAtOnce = 4;
+  for (uint32_t i0 = threadIdx.x; i0 < p.parts; i0 += kAtOnce * kFinishThreads) {
+    float4 x[kAtOnce];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const uint32_t i = i0 + k * kFinishThreads;
+      const float4* a = reinterpret_cast<const float4*>(p.part) + static_cast<uint64_t>(i) * p.rows + row;
+      x[k] = i < p.parts && in_bounds(a, 16, p.part, p.part + static_cast<uint64_t>(p.parts) * p.rows * 16, kSitePart)
+                 ? *a : make_float4(neg_inf(), 0.0f, 0.0f, 0.0f);
+    }
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k)
+      if (i0 + k * kFinishThreads < p.parts) add(x[k].x, x[k].y, x[k].z);
   }
 #pragma unroll
   for (int d = 1; d < 32; d *= 2) {
     const float r1 = __shfl_xor_sync(~0u, ref, d), s1 = __shfl_xor_sync(~0u, s, d), t1 = __shfl_xor_sync(~0u, t, d);
     add(r1, s1, t1);
   }
-  if (lane) return;
+  if (lane == 0) joined[warp] = make_float4(ref, s, t, 0.0f);
+  __syncthreads();
+  if (threadIdx.x) return;
+  for (int w = 1; w < kFinishThreads / 32; ++w) add(joined[w].x, joined[w].y, joined[w].z);
   const float log_s = log2f(s), nan = __int_as_float(0x7FC00000);
   const int64_t token = token_of(p.tokens, p.tokens64, row);
   auto put = [&](uint64_t base, float v) {
@@ -542,8 +553,10 @@ cudaError_t launch_mode(int mode, const LinearParams& p, const LinearOperand& a,
                         const LinearShard* shards, int sms, bool pdl, cudaStream_t s, int* grid) {
   switch (mode) {
     case kLinearStats:
-      return p.shards == 1 ? launch_one<kLinearStats, DT, 1>(p, a, b, shards, sms, pdl, s, grid)
-                           : launch_one<kLinearStats, DT, kMaxRanks>(p, a, b, shards, sms, pdl, s, grid);
+      // (a parameter block of 64 tensor maps has 9 KB)
+      return p.shards == 1   ? launch_one<kLinearStats, DT, 1>(p, a, b, shards, sms, pdl, s, grid)
+             : p.shards <= 8 ? launch_one<kLinearStats, DT, 8>(p, a, b, shards, sms, pdl, s, grid)
+                             : launch_one<kLinearStats, DT, kMaxRanks>(p, a, b, shards, sms, pdl, s, grid);
     case kLinearDLogits: return launch_one<kLinearDLogits, DT, 1>(p, a, b, shards, sms, pdl, s, grid);
     default: return launch_one<kLinearGrads, DT, 2>(p, a, b, shards, sms, pdl, s, grid);
   }
@@ -622,8 +635,7 @@ cudaError_t launch_linear_sum(const LinearSumParams& p, int dtype, bool pdl, cud
 }
 
 cudaError_t launch_linear_finish(const LinearFinishParams& p, bool pdl, cudaStream_t s, int* grid) {
-  constexpr uint64_t per = kFinishThreads / 32;
-  *grid = static_cast<int>((p.rows + per - 1) / per);
+  *grid = static_cast<int>(p.rows);
   return launch_ex(dc_linear_finish_kernel, *grid, kFinishThreads, pdl, s, p);
 }
 

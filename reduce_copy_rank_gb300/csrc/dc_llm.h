@@ -292,7 +292,7 @@ struct HeadsView {
 
 // CTAs of a launch, by a constant: the weights' gradient is added up over them.
 constexpr int kNormThreads = 128;
-constexpr int kNormCtas = 152 * 8;
+constexpr int kNormCtas = 152 * 6;
 constexpr int kNormGradCtas = 152 * 4;
 constexpr int kNormMaxDim = 512;  // at most 128 work units a head
 
@@ -318,10 +318,11 @@ struct NormParams {
   PagedView kc, vc;
   int32_t jobs, cached;
   int32_t dim, rot, w32;       // w32: the weights are binary32, else of the heads' type
-  int32_t units, lanes;        // of a head: work units, and lanes that share it (a power of two)
-  float eps;
+  int32_t units, lanes;        // of a head: work units, and lanes that share it
+  int32_t angles_aligned;      // cos_sin: to 16 bytes
+  float eps, inv_dim;          // 1 / dim
 };
-// Fills units, lanes, split, cta0 and ctas.
+// Fills inv_dim, units, lanes, angles_aligned, split, cta0 and ctas.
 void plan_norm(NormParams* p, int dtype, bool interleaved, bool gradient);
 cudaError_t launch_norm(const NormParams& p, int dtype, bool interleaved, bool gradient, bool pdl, cudaStream_t s, int* grid);
 

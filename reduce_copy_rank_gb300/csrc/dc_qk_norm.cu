@@ -10,8 +10,8 @@
 //
 // Bound: memory, every element read and written once.  A warp takes a token:
 // its lanes hold the cosines and sines of their elements and go through the
-// token's heads, 32 / lanes heads at a time, the next ones' loads in flight
-// while they work; where there are few tokens several warps share one.  Queries,
+// token's heads, as many at a time as 32 lanes hold, the next ones' loads in
+// flight while they work; where there are few tokens several warps share one.  Queries,
 // keys and values are CTAs of their own, so that the weights stay in registers
 // and, for the gradient, the sums over a warp's tokens do too; the CTAs' sums
 // are added up by a second kernel in one fixed order.
@@ -26,10 +26,19 @@ namespace {
 enum : uint32_t { kSiteToken = 1, kSiteTable = 2, kSiteIn = 3, kSiteOut = 4, kSiteAngle = 5, kSiteWeight = 6, kSitePartial = 7 };
 
 constexpr int kWarps = kNormThreads / 32;
+constexpr int norm_ctas_per_sm(int units, bool gradient) { return units > 2 ? 1 : units == 2 ? 2 : gradient ? 4 : 6; }
 
 __device__ __forceinline__ int32_t ld_i32(uint64_t base, uint64_t i, uint64_t n) {
   const int32_t* a = reinterpret_cast<const int32_t*>(base) + i;
   return in_bounds(a, 4, base, base + n * 4, kSiteToken) ? *a : -1;
+}
+
+// 1 / sqrt(x), within an ulp or so: the hardware's estimate and one step of
+// Newton's iteration (0 and infinity as they are).
+__device__ __forceinline__ float inverse_root(float x) {
+  const float r = rsqrtf(x);
+  const float s = __fmaf_rn(-0.5f * x * r, r, 1.5f) * r;
+  return r > 0.0f && r < __int_as_float(0x7F800000) ? s : r;
 }
 
 // UNITS work units of a head for a lane: a pair of 16-byte vectors half the
@@ -57,8 +66,8 @@ struct Kernel {
     half = static_cast<uint32_t>(p.rot / 2) * Elem<DT>::kBytes;
 #pragma unroll
     for (int i = 0; i < UNITS; ++i) {
-      const int u = (lane & (p.lanes - 1)) + i * p.lanes;
-      there[i] = u < p.units;
+      const int u = lane % p.lanes + i * p.lanes;
+      there[i] = u < p.units && lane / p.lanes < 32 / p.lanes;
       turns[i] = u < turning;
       off[i] = turns[i] ? static_cast<uint32_t>(u) * 16
                         : static_cast<uint32_t>(p.rot * Elem<DT>::kBytes) + static_cast<uint32_t>(u - turning) * 16;
@@ -107,8 +116,21 @@ struct Kernel {
       for (int h = 0; h < kHalves; ++h)
 #pragma unroll
         for (int e = 0; e < kPer; ++e) s = __fmaf_rn(a.v[i][h][e], b.v[i][h][e], s);
-    for (int d = 1; d < p.lanes; d *= 2) s += __shfl_xor_sync(~0u, s, d);
-    return s;
+    if ((p.lanes & (p.lanes - 1)) == 0) {
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2)
+        if (d < p.lanes) s += __shfl_xor_sync(~0u, s, d);
+      return s;
+    }
+    // neighbours in pairs, then pairs of pairs, ..., into a head's first lane
+    const int lane = threadIdx.x & 31, u = lane % p.lanes;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      if (d >= p.lanes) break;
+      const float t = __shfl_down_sync(~0u, s, d);
+      if (u + d < p.lanes) s += t;
+    }
+    return __shfl_sync(~0u, s, lane - u);
   }
   // Rotates the units that turn, by the angles or (BACK) their negatives.
   template <bool BACK>
@@ -142,7 +164,7 @@ struct Kernel {
 };
 
 template <int DT, bool INTERLEAVED, int UNITS, bool GRADIENT>
-__global__ __launch_bounds__(kNormThreads) void dc_norm_kernel(const __grid_constant__ NormParams p) {
+__global__ __launch_bounds__(kNormThreads, norm_ctas_per_sm(UNITS, GRADIENT)) void dc_norm_kernel(const __grid_constant__ NormParams p) {
   using K = Kernel<DT, INTERLEAVED, UNITS, GRADIENT>;
   constexpr int kB = Elem<DT>::kBytes;
   extern __shared__ float sums[];  // (gradient) [warps][heads at a time][dim]
@@ -153,7 +175,7 @@ __global__ __launch_bounds__(kNormThreads) void dc_norm_kernel(const __grid_cons
   const NormJob& job = p.job[j];
   const bool copy = job.w == 0;
   const K k(p, lane);
-  const int heads_at_once = 32 / p.lanes, sub = lane / p.lanes;
+  const int heads_at_once = 32 / p.lanes, sub = lane / p.lanes;  // (lanes left over go with no head)
   const int step = heads_at_once * job.split;
   const uint64_t row_bytes = static_cast<uint64_t>(p.dim) * kB;
   typename K::Values w, dw;
@@ -176,7 +198,7 @@ __global__ __launch_bounds__(kNormThreads) void dc_norm_kernel(const __grid_cons
     typename K::Raw next;
     [[maybe_unused]] typename K::Raw next_dy;
     auto fetch = [&](int h) {
-      const bool read = h < job.heads;
+      const bool read = h < job.heads && sub < heads_at_once;
       k.load(next, x_row + static_cast<uint64_t>(read ? h : 0) * job.x.head, read);
       if constexpr (GRADIENT) k.load(next_dy, dy_row + static_cast<uint64_t>(read ? h : 0) * job.dy.head, read);
     };
@@ -211,17 +233,34 @@ __global__ __launch_bounds__(kNormThreads) void dc_norm_kernel(const __grid_cons
     for (int i = 0; i < UNITS; ++i) {
       const uint64_t base = p.cos_sin + static_cast<uint64_t>(ok ? pos : 0) * p.rot * 4;
       const float* c = reinterpret_cast<const float*>(base) + k.off[i] / 16 * K::kAngles;
+      const bool read = ok && !copy && k.turns[i] && in_bounds(c, K::kAngles * 4, base, base + p.rot * 4ull, kSiteAngle) &&
+                        in_bounds(c + p.rot / 2, K::kAngles * 4, base, base + p.rot * 4ull, kSiteAngle);
+      constexpr int kWide = K::kAngles < 4 ? 2 : 4;  // floats of a load, where the table is aligned for it
+      if (read && p.angles_aligned) {
 #pragma unroll
-      for (int e = 0; e < K::kAngles; ++e) {
-        const bool read = ok && !copy && k.turns[i] && in_bounds(c + e, 4, base, base + p.rot * 4ull, kSiteAngle);
-        cs[i][e] = read ? __ldg(c + e) : 0.0f;
-        sn[i][e] = read ? __ldg(c + e + p.rot / 2) : 0.0f;
+        for (int e = 0; e < K::kAngles; e += kWide) {
+          if constexpr (kWide == 4) {
+            const float4 x = __ldg(reinterpret_cast<const float4*>(c + e)), y = __ldg(reinterpret_cast<const float4*>(c + e + p.rot / 2));
+            cs[i][e] = x.x, cs[i][e + 1] = x.y, cs[i][e + 2] = x.z, cs[i][e + 3] = x.w;
+            sn[i][e] = y.x, sn[i][e + 1] = y.y, sn[i][e + 2] = y.z, sn[i][e + 3] = y.w;
+          } else {
+            const float2 x = __ldg(reinterpret_cast<const float2*>(c + e)), y = __ldg(reinterpret_cast<const float2*>(c + e + p.rot / 2));
+            cs[i][e] = x.x, cs[i][e + 1] = x.y;
+            sn[i][e] = y.x, sn[i][e + 1] = y.y;
+          }
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < K::kAngles; ++e) {
+          cs[i][e] = read ? __ldg(c + e) : 0.0f;
+          sn[i][e] = read ? __ldg(c + e + p.rot / 2) : 0.0f;
+        }
       }
     }
     // (the lanes of a warp go through the loop together: they share sums)
     for (int h0 = first; h0 < job.heads; h0 += step) {
       const int h = h0 + sub;
-      const bool mine = h < job.heads;
+      const bool mine = h < job.heads && sub < heads_at_once;
       typename K::Raw now = next;
       [[maybe_unused]] typename K::Raw now_dy;
       if constexpr (GRADIENT) now_dy = next_dy;
@@ -231,8 +270,7 @@ __global__ __launch_bounds__(kNormThreads) void dc_norm_kernel(const __grid_cons
         typename K::Values x;
         k.widen(now, x);
         const float nan = __int_as_float(0x7FC00000);
-        const float mean = k.dot(x, x) / static_cast<float>(p.dim);
-        const float r = ok ? 1.0f / sqrtf(mean + p.eps) : nan;
+        const float r = ok ? inverse_root(__fmaf_rn(k.dot(x, x), p.inv_dim, p.eps)) : nan;
 #pragma unroll
         for (int i = 0; i < UNITS; ++i)
 #pragma unroll
@@ -260,7 +298,7 @@ __global__ __launch_bounds__(kNormThreads) void dc_norm_kernel(const __grid_cons
                 if (mine && !padding && k.has(i, a)) dw.v[i][a][e] = __fmaf_rn(g.v[i][a][e], x.v[i][a][e], dw.v[i][a][e]);
                 g.v[i][a][e] *= w.v[i][a][e];
               }
-          const float c = k.dot(g, x) / static_cast<float>(p.dim);
+          const float c = k.dot(g, x) * p.inv_dim;
 #pragma unroll
           for (int i = 0; i < UNITS; ++i)
 #pragma unroll
@@ -282,7 +320,7 @@ __global__ __launch_bounds__(kNormThreads) void dc_norm_kernel(const __grid_cons
     for (int i = 0; i < UNITS; ++i)
 #pragma unroll
       for (int h = 0; h < K::kHalves; ++h)
-        if (k.has(i, h)) {
+        if (k.has(i, h) && sub < heads_at_once) {
 #pragma unroll
           for (int e = 0; e < K::kPer; ++e) to[(k.off[i] + (h ? k.half : 0)) / kB + e] = dw.v[i][h][e];
         }
@@ -354,8 +392,13 @@ cudaError_t launch_dt(const NormParams& p, bool interleaved, bool gradient, bool
 void plan_norm(NormParams* p, int dtype, bool interleaved, bool gradient) {
   const int per = dtype == kF32 ? 4 : 8;
   p->units = interleaved ? p->dim / per : p->rot / (2 * per) + (p->dim - p->rot) / per;
+  // a head's lanes: as many as it has units, or a power of two where as many heads
+  // fit a warp so (their sums take fewer steps)
   p->lanes = 1;
   while (p->lanes < 32 && p->lanes < p->units) p->lanes *= 2;
+  if (p->units < 32 && 32 / p->units > 32 / p->lanes) p->lanes = p->units;
+  p->angles_aligned = p->cos_sin % 16 == 0;
+  p->inv_dim = 1.0f / static_cast<float>(p->dim);
   const int at_once = 32 / p->lanes;
   const int cap = gradient ? kNormGradCtas : kNormCtas;
   int heads = 0;
