@@ -253,7 +253,7 @@ dc_status_t plan_prefix(int64_t seqs, int64_t prefixes, int q_heads, int kv_head
   const uint64_t rows = static_cast<uint64_t>(seqs / prefixes) * static_cast<uint64_t>(q_heads / kv_heads);
   const uint64_t units = static_cast<uint64_t>(prefixes) * static_cast<uint64_t>(kv_heads) * z->chunks;
   if (rows > 0x7FFFFFFFull - kPrefixRows || units > 0x7FFFFFFFull || units * ((rows + kPrefixRows - 1) / kPrefixRows) > 0x7FFFFFFFull ||
-      static_cast<uint64_t>(seqs) * q_heads * (dim / 4) / 128 > 0x7FFFFFF0ull)
+      static_cast<uint64_t>(seqs) * q_heads > 0x7FFFFFF0ull)
     return fail(DC_ERR_INVALID, "%lld sequences of %d heads exceed a grid", static_cast<long long>(seqs), q_heads);
   const uint64_t all = static_cast<uint64_t>(seqs) * static_cast<uint64_t>(q_heads), d = static_cast<uint64_t>(dim);
   const auto up = [](uint64_t n) { return (n + 255) / 256 * 256; };

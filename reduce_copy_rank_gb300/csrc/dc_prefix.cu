@@ -475,14 +475,16 @@ __global__ __launch_bounds__(kThreads, Shape<D>::kCtas) void dc_prefix_kernel(co
   }
 }
 
-// The prefix's chunks in order, then the own tokens: four columns a thread.
+// The prefix's chunks in order, then the own tokens: a warp a row, a lane every
+// 32nd four columns.
 constexpr int kJoinThreads = 128;
 template <int DT, int D>
 __global__ __launch_bounds__(kJoinThreads) void dc_prefix_join_kernel(const __grid_constant__ PrefixParams p) {
   pdl_enter();
-  const uint64_t item = static_cast<uint64_t>(blockIdx.x) * kJoinThreads + threadIdx.x;
-  const uint64_t n = static_cast<uint64_t>(p.seqs) * p.q_heads, row = item / (D / 4);
-  const int d = static_cast<int>(item % (D / 4)) * 4;
+  constexpr int kVecs = (D / 4 + 31) / 32;
+  const int lane = threadIdx.x & 31;
+  const uint64_t row = static_cast<uint64_t>(blockIdx.x) * (kJoinThreads / 32) + (threadIdx.x >> 5);
+  const uint64_t n = static_cast<uint64_t>(p.seqs) * p.q_heads;
   if (row >= n) return;
   const int seq = static_cast<int>(row / static_cast<uint32_t>(p.q_heads)), head = static_cast<int>(row % static_cast<uint32_t>(p.q_heads));
   const int prefix = seq / p.each;
@@ -491,38 +493,72 @@ __global__ __launch_bounds__(kJoinThreads) void dc_prefix_join_kernel(const __gr
   const uint64_t all = static_cast<uint64_t>(p.prefixes) * p.kv_heads * p.chunks * p.rows;
   const uint64_t at = (static_cast<uint64_t>(prefix) * p.kv_heads + head / p.group) * p.chunks * p.rows +
                       static_cast<uint64_t>(seq % p.each) * p.group + head % p.group;  // of chunk 0; the next is p.rows on
-  auto rl_of = [&](uint32_t c) {
-    const float2* a = reinterpret_cast<const float2*>(p.partial_rl) + at + static_cast<uint64_t>(c) * p.rows;
-    return in_bounds(a, 8, p.partial_rl, p.partial_rl + all * 8, kSitePartial) ? *a : make_float2(neg_inf(), 0.0f);
-  };
+  // lane l holds the references and sums of chunks l, l + 32, ...
+  constexpr int kHeld = (kAttendSms + 31) / 32;  // (as many chunks as there are SMs, at most)
+  float ref[kHeld], sum[kHeld];
   const float2 own = reinterpret_cast<const float2*>(p.raw_rl)[row];
   float most = own.x;
-#pragma unroll 4
-  for (uint32_t c = 0; c < chunks; ++c) most = fmaxf(most, rl_of(c).x);
-  float4 u = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  float l = 0.0f;
-  auto add = [&](const float4& x, const float2& rl) {
-    const float f = pow2_diff(rl.x, most);
-    u.x = __fmaf_rn(x.x, f, u.x);
-    u.y = __fmaf_rn(x.y, f, u.y);
-    u.z = __fmaf_rn(x.z, f, u.z);
-    u.w = __fmaf_rn(x.w, f, u.w);
-    l = __fmaf_rn(rl.y, f, l);
-  };
-#pragma unroll 4
-  for (uint32_t c = 0; c < chunks; ++c) {
-    const float4* a = reinterpret_cast<const float4*>(p.partial + ((at + static_cast<uint64_t>(c) * p.rows) * D + d) * 4);
-    const float4 x = in_bounds(a, 16, p.partial, p.partial + all * D * 4, kSitePartial) ? *a : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    add(x, rl_of(c));
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k) {
+    const uint32_t c = static_cast<uint32_t>(k * 32 + lane);
+    const float2* a = reinterpret_cast<const float2*>(p.partial_rl) + at + static_cast<uint64_t>(c) * p.rows;
+    const float2 x = c < chunks && in_bounds(a, 8, p.partial_rl, p.partial_rl + all * 8, kSitePartial) ? *a : make_float2(neg_inf(), 0.0f);
+    ref[k] = x.x;
+    sum[k] = x.y;
+    most = fmaxf(most, x.x);
   }
-  add(*reinterpret_cast<const float4*>(p.raw + (row * D + d) * 4), own);
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) most = fmaxf(most, __shfl_xor_sync(~0u, most, d));
+  float4 u[kVecs];
+#pragma unroll
+  for (int v = 0; v < kVecs; ++v) u[v] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  float l = 0.0f;
+  auto add = [&](const float4 (&x)[kVecs], float f, float part) {
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v) {
+      u[v].x = __fmaf_rn(x[v].x, f, u[v].x);
+      u[v].y = __fmaf_rn(x[v].y, f, u[v].y);
+      u[v].z = __fmaf_rn(x[v].z, f, u[v].z);
+      u[v].w = __fmaf_rn(x[v].w, f, u[v].w);
+    }
+    l = __fmaf_rn(part, f, l);
+  };
+  auto load = [&](float4 (&x)[kVecs], uint64_t from, uint64_t lo, uint64_t hi) {
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v) {
+      const float4* a = reinterpret_cast<const float4*>(from) + v * 32 + lane;
+      x[v] = (v * 32 + lane) * 4 < D && in_bounds(a, 16, lo, hi, kSitePartial) ? *a : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+  };
+  constexpr int kAtOnce = kVecs > 1 ? 4 : 8;
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k)
+    for (uint32_t c0 = k * 32; c0 < min(chunks, static_cast<uint32_t>(k * 32 + 32)); c0 += kAtOnce) {
+      float4 x[kAtOnce][kVecs];
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j)
+        if (c0 + j < chunks)
+          load(x[j], p.partial + (at + static_cast<uint64_t>(c0 + j) * p.rows) * D * 4, p.partial, p.partial + all * D * 4);
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j)
+        if (c0 + j < chunks) {
+          const float r = __shfl_sync(~0u, ref[k], (c0 + j) % 32), s = __shfl_sync(~0u, sum[k], (c0 + j) % 32);
+          add(x[j], pow2_diff(r, most), s);
+        }
+    }
+  float4 x[kVecs];
+  load(x, p.raw + row * D * 4, p.raw, p.raw + n * D * 4);
+  add(x, pow2_diff(own.x, most), own.y);
   const bool none = l == 0.0f && most == neg_inf();  // nothing to attend to: zeros
   const float inv = none ? 0.0f : 1.0f / l;
   const uint64_t out = p.out + static_cast<uint64_t>(seq) * p.out_seq + static_cast<uint64_t>(head) * p.out_head;
-  uint2* a = reinterpret_cast<uint2*>(out + d * 2);
-  if (in_bounds(a, 8, out, out + D * 2, kSiteOut))
-    *a = make_uint2(Elem<DT>::pack(u.x * inv, u.y * inv), Elem<DT>::pack(u.z * inv, u.w * inv));
-  if (d == 0 && p.lse) {
+#pragma unroll
+  for (int v = 0; v < kVecs; ++v) {
+    uint2* a = reinterpret_cast<uint2*>(out) + v * 32 + lane;
+    if ((v * 32 + lane) * 4 < D && in_bounds(a, 8, out, out + D * 2, kSiteOut))
+      *a = make_uint2(Elem<DT>::pack(u[v].x * inv, u[v].y * inv), Elem<DT>::pack(u[v].z * inv, u[v].w * inv));
+  }
+  if (lane == 0 && p.lse) {
     float* b = reinterpret_cast<float*>(p.lse) + row;
     if (in_bounds(b, 4, p.lse, p.lse + n * 4, kSiteOut)) *b = none ? neg_inf() : (most + log2f(l)) * kLn2;
   }
@@ -575,8 +611,8 @@ cudaError_t launch_prefix(const PrefixParams& p, int dtype, int dim, bool pdl, c
 }
 
 cudaError_t launch_prefix_join(const PrefixParams& p, int dtype, int dim, bool pdl, cudaStream_t s, int* grid) {
-  const uint64_t items = static_cast<uint64_t>(p.seqs) * static_cast<uint64_t>(p.q_heads) * static_cast<uint64_t>(dim / 4);
-  *grid = static_cast<int>((items + kJoinThreads - 1) / kJoinThreads);
+  const uint64_t rows = static_cast<uint64_t>(p.seqs) * static_cast<uint64_t>(p.q_heads);
+  *grid = static_cast<int>((rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32));
   return dtype == kF16 ? launch_dim<kF16>(p, dim, true, pdl, s, *grid) : launch_dim<kBF16>(p, dim, true, pdl, s, *grid);
 }
 

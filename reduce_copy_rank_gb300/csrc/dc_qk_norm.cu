@@ -48,6 +48,7 @@ struct Kernel {
   static constexpr int kPer = Elem<DT>::kPerVec;
   static constexpr int kHalves = INTERLEAVED ? 1 : 2;
   static constexpr int kAngles = INTERLEAVED ? kPer / 2 : kPer;
+  static constexpr int kAhead = INTERLEAVED && UNITS == 1 ? 2 : 1;  // heads whose loads are in flight
 
   struct Raw {
     uint4 v[UNITS][kHalves];
@@ -143,8 +144,8 @@ struct Kernel {
         float& a = INTERLEAVED ? x.v[i][0][2 * e] : x.v[i][0][e];
         float& b = INTERLEAVED ? x.v[i][0][2 * e + 1] : x.v[i][kHalves - 1][e];
         const float s = BACK ? -sn[i][e] : sn[i][e];
-        const float lo = a * cs[i][e] - b * s;
-        b = b * cs[i][e] + a * s;
+        const float lo = __fmaf_rn(a, cs[i][e], -(b * s));
+        b = __fmaf_rn(b, cs[i][e], a * s);
         a = lo;
       }
     }
@@ -195,19 +196,35 @@ __global__ __launch_bounds__(kNormThreads, norm_ctas_per_sm(UNITS, GRADIENT)) vo
     const int first = static_cast<int>(item % static_cast<uint32_t>(job.split)) * heads_at_once;
     const uint64_t x_row = job.x.base + token * job.x.token;
     [[maybe_unused]] const uint64_t dy_row = job.dy.base + token * job.dy.token;
-    typename K::Raw next;
-    [[maybe_unused]] typename K::Raw next_dy;
-    auto fetch = [&](int h) {
+    typename K::Raw next[K::kAhead];
+    [[maybe_unused]] typename K::Raw next_dy[K::kAhead];
+    auto fetch = [&](int a, int h) {
       const bool read = h < job.heads && sub < heads_at_once;
-      k.load(next, x_row + static_cast<uint64_t>(read ? h : 0) * job.x.head, read);
-      if constexpr (GRADIENT) k.load(next_dy, dy_row + static_cast<uint64_t>(read ? h : 0) * job.dy.head, read);
+      k.load(next[a], x_row + static_cast<uint64_t>(read ? h : 0) * job.x.head, read);
+      if constexpr (GRADIENT) k.load(next_dy[a], dy_row + static_cast<uint64_t>(read ? h : 0) * job.dy.head, read);
     };
-    fetch(first + sub);
+#pragma unroll
+    for (int a = 0; a < K::kAhead; ++a) fetch(a, first + a * step + sub);
 
     const int32_t pos = ld_i32(p.positions, token, p.tokens);
     const bool padding = pos < 0;
     bool ok = !padding && (p.rot == 0 || static_cast<int64_t>(pos) < p.cos_rows);
     uint64_t y_row = job.y.base + token * job.y.token;
+    // all of this warp's heads of the token become one number
+    auto fill = [&](uint64_t row, float value) {
+      typename K::Values v;
+      typename K::Raw r;
+#pragma unroll
+      for (int i = 0; i < UNITS; ++i)
+#pragma unroll
+        for (int a = 0; a < K::kHalves; ++a)
+#pragma unroll
+          for (int e = 0; e < K::kPer; ++e) v.v[i][a][e] = value;
+      k.narrow(v, r);
+      for (int h = first + sub; h < job.heads; h += step)
+        k.store(r, row + static_cast<uint64_t>(h) * job.y.head, sub < heads_at_once, row,
+                row + static_cast<uint64_t>(job.heads - 1) * job.y.head + row_bytes);
+    };
     if (p.cached) {
       if (padding) continue;  // nothing is written for it
       // where the token goes; a place that does not exist is never touched
@@ -227,13 +244,26 @@ __global__ __launch_bounds__(kNormThreads, norm_ctas_per_sm(UNITS, GRADIENT)) vo
         y_row = c.base + static_cast<uint64_t>(page) * c.page + slot * c.token;
       }
     }
+    if (!ok) {  // padding: zeros; a place that does not exist: NaN
+      const float value = padding ? 0.0f : __int_as_float(0x7FC00000);
+      fill(y_row, value);
+      if constexpr (GRADIENT) {
+#pragma unroll
+        for (int i = 0; i < UNITS; ++i)
+#pragma unroll
+          for (int a = 0; a < K::kHalves; ++a)
+#pragma unroll
+            for (int e = 0; e < K::kPer; ++e) dw.v[i][a][e] += value;
+      }
+      continue;
+    }
     const uint64_t y_hi = y_row + static_cast<uint64_t>(job.heads - 1) * job.y.head + row_bytes;
     float cs[UNITS][K::kAngles], sn[UNITS][K::kAngles];
 #pragma unroll
     for (int i = 0; i < UNITS; ++i) {
-      const uint64_t base = p.cos_sin + static_cast<uint64_t>(ok ? pos : 0) * p.rot * 4;
+      const uint64_t base = p.cos_sin + static_cast<uint64_t>(pos) * p.rot * 4;
       const float* c = reinterpret_cast<const float*>(base) + k.off[i] / 16 * K::kAngles;
-      const bool read = ok && !copy && k.turns[i] && in_bounds(c, K::kAngles * 4, base, base + p.rot * 4ull, kSiteAngle) &&
+      const bool read = !copy && k.turns[i] && in_bounds(c, K::kAngles * 4, base, base + p.rot * 4ull, kSiteAngle) &&
                         in_bounds(c + p.rot / 2, K::kAngles * 4, base, base + p.rot * 4ull, kSiteAngle);
       constexpr int kWide = K::kAngles < 4 ? 2 : 4;  // floats of a load, where the table is aligned for it
       if (read && p.angles_aligned) {
@@ -258,19 +288,21 @@ __global__ __launch_bounds__(kNormThreads, norm_ctas_per_sm(UNITS, GRADIENT)) vo
       }
     }
     // (the lanes of a warp go through the loop together: they share sums)
-    for (int h0 = first; h0 < job.heads; h0 += step) {
-      const int h = h0 + sub;
+    for (int hb = first; hb < job.heads; hb += K::kAhead * step) {
+#pragma unroll
+     for (int ahead = 0; ahead < K::kAhead; ++ahead) {
+      const int h0 = hb + ahead * step, h = h0 + sub;
+      if (h0 >= job.heads) break;
       const bool mine = h < job.heads && sub < heads_at_once;
-      typename K::Raw now = next;
+      typename K::Raw now = next[ahead];
       [[maybe_unused]] typename K::Raw now_dy;
-      if constexpr (GRADIENT) now_dy = next_dy;
-      if (h0 + step < job.heads) fetch(h + step);
+      if constexpr (GRADIENT) now_dy = next_dy[ahead];
+      if (h0 + K::kAhead * step < job.heads) fetch(ahead, h + K::kAhead * step);
       const uint64_t out = y_row + static_cast<uint64_t>(mine ? h : 0) * job.y.head;
       if (!copy) {
         typename K::Values x;
         k.widen(now, x);
-        const float nan = __int_as_float(0x7FC00000);
-        const float r = ok ? inverse_root(__fmaf_rn(k.dot(x, x), p.inv_dim, p.eps)) : nan;
+        const float r = inverse_root(__fmaf_rn(k.dot(x, x), p.inv_dim, p.eps));
 #pragma unroll
         for (int i = 0; i < UNITS; ++i)
 #pragma unroll
@@ -283,19 +315,20 @@ __global__ __launch_bounds__(kNormThreads, norm_ctas_per_sm(UNITS, GRADIENT)) vo
 #pragma unroll
             for (int a = 0; a < K::kHalves; ++a)
 #pragma unroll
-              for (int e = 0; e < K::kPer; ++e) x.v[i][a][e] = padding ? 0.0f : x.v[i][a][e] * w.v[i][a][e];
-          if (ok) k.template rotate<false>(x, cs, sn);
+              for (int e = 0; e < K::kPer; ++e) x.v[i][a][e] *= w.v[i][a][e];
+          k.template rotate<false>(x, cs, sn);
         } else {
           typename K::Values g;
           k.widen(now_dy, g);
-          if (ok) k.template rotate<true>(g, cs, sn);
+          k.template rotate<true>(g, cs, sn);
 #pragma unroll
           for (int i = 0; i < UNITS; ++i)
 #pragma unroll
             for (int a = 0; a < K::kHalves; ++a)
 #pragma unroll
               for (int e = 0; e < K::kPer; ++e) {
-                if (mine && !padding && k.has(i, a)) dw.v[i][a][e] = __fmaf_rn(g.v[i][a][e], x.v[i][a][e], dw.v[i][a][e]);
+                // (where there is no head, g is 0 and x is 0 or NaN, of eps 0)
+                if (mine) dw.v[i][a][e] = __fmaf_rn(g.v[i][a][e], x.v[i][a][e], dw.v[i][a][e]);
                 g.v[i][a][e] *= w.v[i][a][e];
               }
           const float c = k.dot(g, x) * p.inv_dim;
@@ -305,11 +338,12 @@ __global__ __launch_bounds__(kNormThreads, norm_ctas_per_sm(UNITS, GRADIENT)) vo
             for (int a = 0; a < K::kHalves; ++a)
 #pragma unroll
               for (int e = 0; e < K::kPer; ++e)
-                x.v[i][a][e] = padding ? 0.0f : r * (g.v[i][a][e] - x.v[i][a][e] * c);
+                x.v[i][a][e] = r * __fmaf_rn(-c, x.v[i][a][e], g.v[i][a][e]);
         }
         k.narrow(x, now);
       }
       k.store(now, out, mine, y_row, y_hi);
+     }
     }
   }
   if constexpr (GRADIENT) {
