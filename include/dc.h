@@ -14,7 +14,7 @@
  *     managed memory).  The caller owns all memory.
  *   - The work is enqueued on `stream` (NULL = the legacy default stream) and
  *     runs asynchronously.  A call allocates no memory, never synchronises,
- *     launches at most one kernel, and copies every pointer and size into the
+ *     launches at most one kernel (or as many as its description says), and copies every pointer and size into the
  *     kernel's parameters, so it may be captured into a CUDA graph and the
  *     host arrays may be freed as soon as it returns.
  *   - Arguments are checked before any CUDA call; a rejected call launches
@@ -305,7 +305,8 @@ dc_status_t dc_fused_all_gather_static(const void *const *in_ptrs, void *const *
  * rollouts and training on them: log probabilities over the vocabulary shards
  * of a tensor-parallel head (with their gradient), and the paged key-value
  * cache with the attention of single new tokens over it.  They follow the
- * conventions above (one kernel a call, no allocation, checks first), and
+ * conventions above (one kernel a call where nothing else is said, no
+ * allocation, checks first), and
  * their results depend on no other row or sequence of the call, on no grid
  * and, for the log probabilities, on no sharding: a token has the same bits
  * in a batch of one and in a batch of a thousand.
@@ -466,8 +467,9 @@ size_t dc_linear_logprobs_workspace_bytes(int64_t rows, int64_t hidden_size, int
  *   `ranks` pointers, shaped as the weights, or NULL; either is needed.  They
  *   replace what was there.  Rows of the weights' gradient past `vocab` are 0,
  *   as are all of them if there are no rows.  No output may meet an input.
- * A row of grad_hidden does not depend on the other rows (for DC_F16: beyond
- * the power of two); the order of every sum is fixed.
+ * A row whose lse is -1e30 or less has no gradient.  A row of grad_hidden does
+ * not depend on the other rows (for DC_F16: beyond the power of two); the order
+ * of every sum is fixed.
  * workspace: dc_linear_logprobs_workspace_bytes(rows, hidden_size, columns, 1)
  * bytes, as above.  Several kernels.
  */

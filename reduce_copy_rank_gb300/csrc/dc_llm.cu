@@ -418,8 +418,8 @@ dc_status_t dc_kv_append_norm(const dc_kv_append_norm_t* a, dc_stream_t stream) 
   if (!a) return fail(DC_ERR_INVALID, "the argument block is NULL");
   AppendParams x{};
   Spans written, in;
-  DC_TRY(take_append(&a->append, x, written));
   DC_TRY(check_norm(a->append.dim, a->eps));
+  DC_TRY(take_append(&a->append, x, written));
   const int es = a->norm_32 ? 4 : elem_bytes(a->append.dtype);
   const uint64_t bytes = static_cast<uint64_t>(a->append.dim) * static_cast<uint64_t>(es);
   if (a->append.q_heads) DC_TRY(take(a->q_norm, "q_norm", bytes, es, in));

@@ -324,6 +324,7 @@ dc_status_t dc_linear_logprobs_backward(const dc_linear_logprobs_backward_t* a, 
     DC_TRY(outside_shards(out, hidden, "grad_hidden"));
     DC_TRY(outside_shards(h.in, hidden, "grad_hidden"));
   }
+  if (n == 0 && !want_w) return ok();
   int sms = 0;
   DC_TRY(device(&sms));
   const cudaStream_t s = static_cast<cudaStream_t>(stream);

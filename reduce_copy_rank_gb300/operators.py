@@ -410,6 +410,11 @@ def linear_logprobs_and_entropy(hidden, weights: Sequence, tokens, vocab: int | 
     return _linear_function.apply(tokens, vocab, temperature, hidden, *weights)
 
 
+def _aligned(t):
+    """`t`, or a copy of it where it does not start at a multiple of 16 bytes."""
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 def _first_derivative(name: str):
     """A function that passes gradients on with the tensors that they depend on: their own derivative is refused."""
     import torch
@@ -532,7 +537,7 @@ def normed_queries_and_keys(q, k, positions, cos_sin, q_norm, k_norm, eps: float
                 q, k, q_norm, k_norm, positions, *rest = ctx.saved_tensors
                 cos_sin = rest[0] if rest else None
                 # upstream gradients may be broadcast, or laid out in a way that the kernel does not read
-                gq, gk = (g.to(t.dtype).contiguous() for g, t in zip((gq, gk), (q, k)))
+                gq, gk = (_aligned(g.to(t.dtype).contiguous()) for g, t in zip((gq, gk), (q, k)))
                 grads = [torch.empty_like(t, memory_format=torch.contiguous_format) for t in (q, k)]
                 want = any(ctx.needs_input_grad[2:4])
                 sums = [torch.empty_like(t, memory_format=torch.contiguous_format) for t in (q_norm, k_norm)] if want else [None] * 2

@@ -242,6 +242,17 @@ def test_no_rows():
     assert all(bool((g == 0).all()) for g in grads)
 
 
+def test_rows_without_a_finite_logit_have_no_gradient():
+    hidden, weights, tokens = build(20, 64, [300], 300)
+    saved = forward(hidden, weights, tokens)
+    want = backward(hidden, weights, tokens, 300, *upstream(20), saved=saved)
+    saved[2][[3, 11]] = -math.inf
+    got = backward(hidden, weights, tokens, 300, *upstream(20), saved=saved)
+    keep = [i for i in range(20) if i not in (3, 11)]
+    assert bool((got[0][[3, 11]] == 0).all()) and torch.equal(got[0][keep], want[0][keep])
+    assert bool(torch.isfinite(got[1][0]).all())
+
+
 def test_one_workspace_for_smaller_calls_and_its_contents_do_not_matter():
     ws = dc.linear_logprobs_workspace(200, 128, 3000, backward=True).fill_(255)
     fs = dc.linear_logprobs_workspace(200, 128, 3000).fill_(255)

@@ -247,6 +247,10 @@ def test_autograd(w32):
     # a broadcast upstream gradient, one output alone
     (g,) = torch.autograd.grad(out[0].sum(), [leaves[0]], retain_graph=True)
     check_backward(g, None, q, w[0], torch.ones_like(dy[0]), pos, cs, True, "bf16", keep)
+    # ... and one that starts off the kernels' alignment
+    odd = torch.empty(dy[0].numel() + 1, device="cuda", dtype=dy[0].dtype)[1:].view_as(dy[0]).copy_(dy[0])
+    (g,) = torch.autograd.grad(out[0], [leaves[0]], odd, retain_graph=True)
+    assert torch.equal(g, grads[0])
     (g,) = torch.autograd.grad(out[0].sum(), [leaves[0]], create_graph=True)
     with pytest.raises(RuntimeError, match="second derivative"):
         g.sum().backward()
