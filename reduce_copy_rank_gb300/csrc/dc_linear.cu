@@ -122,15 +122,33 @@ __device__ __forceinline__ void gather_part(uint32_t at, bool set, float (&v)[kL
   }
 }
 
+// 32 bytes, to a multiple of 32.
+__device__ __forceinline__ void st32(uint64_t at, const uint4& a, const uint4& b) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w),
+               "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
+}
+
 // Stores 32 results of a row as 16-bit elements; `left` of them exist (a
 // multiple of 8, or more than 32).
 template <int DT>
 __device__ __forceinline__ void st_row32(uint64_t at, const float (&v)[32], int left, uint64_t lo, uint64_t hi, uint32_t site) {
+  uint4 w[4];
 #pragma unroll
-  for (int j = 0; j < 32; j += 8) {
-    uint4* a = reinterpret_cast<uint4*>(at + j * 2);
-    const float x[8] = {v[j], v[j + 1], v[j + 2], v[j + 3], v[j + 4], v[j + 5], v[j + 6], v[j + 7]};
-    if (j < left && in_bounds(a, 16, lo, hi, site)) st16(a, repack<DT>(x));
+  for (int j = 0; j < 4; ++j) {
+    const float x[8] = {v[8 * j], v[8 * j + 1], v[8 * j + 2], v[8 * j + 3], v[8 * j + 4], v[8 * j + 5], v[8 * j + 6], v[8 * j + 7]};
+    w[j] = repack<DT>(x);
+  }
+  if (left >= 32 && at % 32 == 0) {  // whole sectors of memory at a time
+#pragma unroll
+    for (int j = 0; j < 4; j += 2)
+      if (in_bounds(reinterpret_cast<const void*>(at + j * 16), 32, lo, hi, site)) st32(at + j * 16, w[j], w[j + 1]);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint4* a = reinterpret_cast<uint4*>(at + j * 16);
+    if (8 * j < left && in_bounds(a, 16, lo, hi, site)) st16(a, w[j]);
   }
 }
 
