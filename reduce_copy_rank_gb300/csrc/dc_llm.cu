@@ -553,11 +553,11 @@ dc_status_t dc_prefix_attention(const dc_prefix_attention_t* a, dc_stream_t stre
   x.kc = p.kc;
   x.vc = p.vc;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_prefix(x, own.dtype, own.dim, pdl_option(), s, &grid);
-  DC_TRY(check_launch(e, "attention to shared prefixes", grid));
   p.raw = x.raw;
   p.raw_rl = x.raw_rl;
   DC_TRY(run_attend(p, plan, own.dtype, own.dim, sms, stream));
+  cudaError_t e = launch_prefix(x, own.dtype, own.dim, pdl_option(), s, &grid);
+  DC_TRY(check_launch(e, "attention to shared prefixes", grid));
   e = launch_prefix_join(x, own.dtype, own.dim, pdl_option(), s, &grid);
   return check_launch(e, "attention to shared prefixes", grid);
 }

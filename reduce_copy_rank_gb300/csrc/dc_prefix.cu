@@ -166,12 +166,20 @@ __global__ __launch_bounds__(kThreads, Shape<D>::kCtas) void dc_prefix_kernel(co
   const int kh = static_cast<int>(unit / static_cast<uint32_t>(p.chunks) % static_cast<uint32_t>(p.kv_heads));
   const int prefix = static_cast<int>(unit / static_cast<uint32_t>(p.chunks) / static_cast<uint32_t>(p.kv_heads));
 
-  pdl_enter();
+  // The kernel before, over the own tokens, has waited for all work before it in
+  // every CTA by the time this one starts, and nothing here reads what it writes:
+  // the two run side by side, and this one ends after it.  Measured, one after
+  // the other / side by side: 8 sequences of a group with 1025 tokens 20.6 / 14.7
+  // us, 4 groups of 16 with 7001 tokens each 49.7 / 45.2 us.
+  pdl_launch_dependents();
   bool bad;
   const uint32_t length = prefix_length(p, prefix, &bad);
   const uint32_t per = length ? prefix_chunk(length, p.kv_heads) : 1;
   const uint32_t first = chunk * per;
-  if (first >= length) return;
+  if (first >= length) {
+    pdl_wait();
+    return;
+  }
   const uint32_t end = min(length, first + per);
   const uint32_t tiles = (end - first + S::kTile - 1) / S::kTile;
 
@@ -468,6 +476,7 @@ __global__ __launch_bounds__(kThreads, Shape<D>::kCtas) void dc_prefix_kernel(co
     asm volatile("bar.sync 1, 224;" ::: "memory");
   }
   __syncthreads();
+  pdl_wait();
   if (threadIdx.x == 0 && stop) atomicOr(&g_prefix_fault_bits, kFaultTensorWait);
   if (warp == 4) {
     fence_after();
