@@ -460,15 +460,17 @@ size_t dc_linear_logprobs_workspace_bytes(int64_t rows, int64_t hidden_size, int
  * The logits are computed again, up to 24576 columns of a shard at a time; d is
  * rounded to 16 bits before its products (for DC_F16 times one power of two for
  * all rows, so that the largest d that these g and h allow fits: rows whose g
- * and h are 2^20 times smaller than the largest lose precision), the sums are
- * binary32 and rounded once.
+ * and h are 2^20 times smaller than the largest lose precision); what that takes
+ * from d at the row's token is kept in binary32 and added to both products.  The
+ * sums are binary32 and rounded once.
  *
  * grad_hidden [rows, hidden_size] or NULL; grad_weights: host array of
  *   `ranks` pointers, shaped as the weights, or NULL; either is needed.  They
  *   replace what was there.  Rows of the weights' gradient past `vocab` are 0,
  *   as are all of them if there are no rows.  No output may meet an input.
- * A row whose lse is -1e30 or less has no gradient.  A row of grad_hidden does
- * not depend on the other rows (for DC_F16: beyond the power of two); the order
+ * A row whose lse is -1e30 or less, or whose g and h are 0, has no gradient (its
+ * hidden row still has to be finite where grad_weights are wanted: 0 times NaN is
+ * NaN there).  A row of grad_hidden does not depend on the other rows (for DC_F16: beyond the power of two); the order
  * of every sum is fixed.
  * workspace: dc_linear_logprobs_workspace_bytes(rows, hidden_size, columns, 1)
  * bytes, as above.  Several kernels.

@@ -21,9 +21,14 @@
 //    d^T h in one launch, whose tiles are shared out so that all CTAs end together.
 // Neither the number of rows nor the grid changes a bit of a row's results.
 //
-// Rounding: d is rounded to 16 bits before its products (2^-9 of each for
-// DC_BF16, 2^-12 for DC_F16), as an activation's gradient is; the sums are
-// binary32.  For DC_F16 d is multiplied by one power of two for all rows, so
+// Rounding: d is rounded to 16 bits before its products (half a step of each: 2^-8
+// of it for DC_BF16, 2^-11 for DC_F16), as an activation's gradient is; the sums are
+// binary32.  What that takes from the largest element of most rows, the token's, is
+// kept in 32 bits and put back into both products where they are stored: d e_y^T is
+// one row of the weights for dh, and one row of h for the token's row of dW.  The
+// gradients' errors are then those of their last rounding where single tokens make
+// them up (4096 rows, 127900 columns: 0.0017 of the gradients, 0.0025 without; the
+// time of that batch does not change, 509 rows of 50021 columns take 194 for 177 us).  For DC_F16 d is multiplied by one power of two for all rows, so
 // that the largest possible is between 2^14 and 2^15: what is 2^-29 of that is
 // still a normal number.
 //
@@ -57,6 +62,10 @@ constexpr int kSmem = kStages * kStageBytes + 1024;   // (the ring starts at a m
 // relative error of the log probabilities and lse 2.0e-7 / 4.2e-7 / 8.9e-7 / 3.6e-6
 // (binary32 matrix product: 5e-7), 2.67 / 2.60 / 2.51 / 2.52 ms.
 constexpr uint32_t kRunBlocks = 16;
+// The gradient's products are rounded to 16 bits afterwards: 24576 rows (or columns
+// of a chunk) at a time.  Measured, FP16, dW of terms of one sign, 131072 / 2^20 rows,
+// error against its last rounding's 2.1e-4: in one run 5.9e-4 / 4.5e-3.
+constexpr uint32_t kGradBlocks = kLinearChunk / kLinearK;
 constexpr int kResultThreads = 256;                   // eight warps of results: a row and half of the columns a thread
 constexpr int kThreads = 64 + kResultThreads;         // one warp loads, one issues products
 constexpr uint32_t kColumns = 2 * kLinearN;           // of tensor memory: two tiles' accumulators
@@ -158,7 +167,7 @@ __device__ __forceinline__ void dlogits(const LinearParams& p, uint32_t at, uint
   const float c = p.inv_t * kLog2E;
   float lse2 = 0.0f, a0 = 0.0f, a1 = 0.0f, hot = 0.0f;
   int64_t token = -1;
-  bool none = false;  // a row without a finite logit has no gradient
+  bool none = false;  // a row without a finite logit, or without upstream gradients, has no gradient
   if (own) {
     token = token_of(p.tokens, p.tokens64, row);
     const float unit = p.scale ? *reinterpret_cast<const float*>(p.scale) : 1.0f;
@@ -166,53 +175,193 @@ __device__ __forceinline__ void dlogits(const LinearParams& p, uint32_t at, uint
     const float e = p.grad_entropy ? ld_row(p.grad_entropy, row, p.rows) : 0.0f;
     const float h = p.grad_entropy ? ld_row(p.entropy, row, p.rows) : 0.0f;
     const float lse = ld_row(p.lse, row, p.rows);
-    none = lse <= -1e30f;
     lse2 = lse * kLog2E;
     const float f = p.inv_t * unit;
     hot = g * f;
     a0 = -(g + e * h) * f;   // d = p (a0 + a1 log2 p), and hot at the token
     a1 = -(e * kLn2) * f;
+    none = lse <= -1e30f || (hot == 0.0f && a0 == 0.0f && a1 == 0.0f);
   }
-  const int64_t mine = token - static_cast<int64_t>(p.first) - n0;
+  const int64_t column = token - static_cast<int64_t>(p.first) - n0;
+  const uint32_t mine = column >= 0 && column < kLinearPart ? static_cast<uint32_t>(column) : kLinearPart;
   const uint32_t ld = static_cast<uint32_t>(p.d_stride / 2);
   const uint32_t exist = !none && p.vocab > p.first + n0 ? p.vocab - p.first - n0 : 0;  // columns before the padding
   const uint64_t lo = p.d + row * p.d_stride;
+  if (n0 % kLinearN == 0) {
+    const uint32_t marked = __ballot_sync(~0u, own && column >= 0 && column < kLinearN);
+    uint32_t* a = reinterpret_cast<uint32_t*>(p.marks) + static_cast<uint64_t>(n0 / kLinearN) * linear_groups(p.rows) + row / 32;
+    if ((threadIdx.x & 31) == 0 && in_bounds(a, 4, p.marks, p.marks + linear_marks(p.rows, p.d_stride), kSiteRow)) *a = marked;
+  }
 #pragma unroll 1
   for (uint32_t j0 = 0; j0 < kLinearPart && n0 + j0 < ld; j0 += 32) {
-    float v[32];
+    float v[32], exact = 0.0f;
     tmem_ld32(at + j0, v);
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
       const float x = __fmaf_rn(v[j], c, -lse2);
       v[j] = ex2(x) * __fmaf_rn(a1, x < -1e4f ? -1e4f : x, a0);
-      if (mine == static_cast<int64_t>(j0 + j)) v[j] += hot;
+      if (j0 + j == mine) v[j] += hot;
       if (j0 + j >= exist) v[j] = 0.0f;
+      if (j0 + j == mine) exact = v[j];
+    }
+    if (own && mine - j0 < 32) {
+      const float off = exact - Elem<DT>::one(Elem<DT>::bits(exact));
+      float* a = reinterpret_cast<float*>(p.lost) + row;
+      if (in_bounds(a, 4, p.lost, p.lost + p.rows * 4, kSiteRow)) *a = fabsf(off) < -neg_inf() ? off : 0.0f;
     }
     if (own) st_row32<DT>(lo + (n0 + j0) * 2, v, static_cast<int>(ld - n0 - j0), lo, lo + p.d_stride, kSiteD);
   }
 }
 
-// A row of a gradient.  dh: plus what `acc` holds of it, to `acc` or (complete)
-// to the output.
+// What the rounding of d took from a row of a gradient: `f` times a row of the other
+// operand for each token.  dh: the row's own token.  dW: the rows of the batch whose
+// token is this column, in order; `list` has (row, lane) pairs of the warp's 32
+// columns, kHits at a time.
+constexpr uint32_t kHits = 64;
+struct Lost {
+  float f;         // the first
+  uint64_t row;
+  uint4 w[4];      // 32 elements of that row
+  uint64_t more;   // dW: the list's others for this lane, a bit each,
+  uint32_t next;   // and the group of 32 rows of the batch after the list's
+};
+
+// Fills the list from groups of 32 rows, from `from` on.  Returns this lane's.
+__device__ __forceinline__ uint64_t find_hits(const LinearParams& p, uint32_t column0, uint32_t from, uint32_t* list, uint32_t* next) {
+  const uint32_t lane = threadIdx.x & 31, exist = p.g.columns - column0, groups = linear_groups(p.rows);
+  const int64_t first = static_cast<int64_t>(p.first) + column0;
+  const uint32_t* marks = reinterpret_cast<const uint32_t*>(p.marks) + static_cast<uint64_t>(column0 / kLinearN) * groups;
+  const uint64_t marks_hi = p.marks + linear_marks(p.rows, p.d_stride);
+  constexpr int kAtOnce = 4;
+  uint32_t n = 0;
+  bool room = true;
+  __syncwarp();
+  for (*next = groups; room && from < groups; from += 32) {
+    const uint32_t* a = marks + from + lane;
+    const uint32_t word = from + lane < groups && in_bounds(a, 4, p.marks, marks_hi, kSiteRow) ? *a : 0u;
+    uint32_t some = __ballot_sync(~0u, word != 0);
+    while (room && some) {
+      int64_t t[kAtOnce];
+      uint32_t at[kAtOnce];
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        at[k] = some ? static_cast<uint32_t>(__ffs(static_cast<int>(some)) - 1) : 0u;
+        const uint32_t bits = __shfl_sync(~0u, word, static_cast<int>(at[k]));
+        const bool marked = some && (bits >> lane & 1);
+        some &= some - 1;
+        at[k] += from;
+        t[k] = marked ? token_of(p.tokens, p.tokens64, 32ull * at[k] + lane) - first : -1;
+      }
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        const bool hit = t[k] >= 0 && t[k] < 32 && t[k] < exist;
+        const uint32_t all = __ballot_sync(~0u, hit), count = static_cast<uint32_t>(__popc(all));
+        if (room && n + count > kHits) {
+          room = false;
+          *next = at[k];
+        }
+        if (!room) continue;
+        if (hit) list[n + static_cast<uint32_t>(__popc(all & ((1u << lane) - 1)))] = (32 * at[k] + lane) << 5 | static_cast<uint32_t>(t[k]);
+        n += count;
+      }
+    }
+  }
+  __syncwarp();
+  uint64_t mine = 0;
+  for (uint32_t k = 0; k < n; ++k)
+    if ((list[k] & 31) == lane) mine |= 1ull << k;
+  return mine;
+}
+
+// 32 elements of a row of `size`, from `first` on.
+__device__ __forceinline__ void ld_row32(uint4 (&w)[4], uint64_t row, uint32_t first, uint32_t size) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint4* a = reinterpret_cast<const uint4*>(row + first * 2ull) + j;
+    w[j] = first + 8 * j < size && in_bounds(a, 16, row, row + size * 2ull, kSiteRow) ? *a : make_uint4(0, 0, 0, 0);
+  }
+}
+template <int DT>
+__device__ __forceinline__ void add_row32(float (&v)[32], float f, const uint4 (&w)[4]) {
+  if (f == 0.0f) return;  // (whatever the row holds)
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float x[8];
+    unpack<DT>(w[j], x);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[8 * j + k] = __fmaf_rn(f, x[k], v[8 * j + k]);
+  }
+}
+
+// Looked up before the products are there: `row` of C, k0 and blocks of dh's inner dimension.
+__device__ __forceinline__ void look_up(const LinearParams& p, uint64_t row, bool own, uint32_t n0, bool weights, uint32_t k0,
+                                        uint32_t blocks, uint32_t* list, Lost* x) {
+  const LinearGrads& g = p.g;
+  *x = Lost{0.0f, 0, {}, 0, ~0u};
+  if (weights) {
+    x->more = find_hits(p, static_cast<uint32_t>(row) & ~31u, 0, list, &x->next);
+    if (x->more) {
+      const uint64_t i = list[__ffsll(static_cast<long long>(x->more)) - 1] >> 5;
+      x->more &= x->more - 1;
+      x->f = ld_row(p.lost, i, p.rows);
+      x->row = g.x + i * g.x_stride;
+    }
+  } else if (own) {
+    const int64_t column = token_of(p.tokens, p.tokens64, row) - static_cast<int64_t>(p.first);
+    if (column >= k0 && column < min(g.columns, k0 + blocks * kLinearK)) {
+      x->f = ld_row(p.lost, row, p.rows);
+      x->row = g.w + static_cast<uint64_t>(column) * g.w_stride;
+    }
+  }
+  if (x->f != 0.0f) ld_row32(x->w, x->row, n0, p.n);
+}
+
+// A row of a gradient.  Plus what `acc` (dh: of chunks and slices, dW: of this
+// tile's runs) holds of it, to `acc` or (complete) to the output.
 template <int DT>
 __device__ __forceinline__ void result(const LinearParams& p, uint32_t at, uint64_t row, bool own, uint32_t n0, bool weights,
-                                       uint32_t slice, bool empty) {
+                                       uint32_t slice, bool empty, bool again, bool whole, Lost& lost, uint32_t* list) {
   const LinearGrads& g = p.g;
   const float unit = p.scale ? reinterpret_cast<const float*>(p.scale)[1] : 1.0f;
   const uint64_t out = weights ? g.out_w + row * g.out_w_stride : g.out_h + row * g.out_h_stride;
-  const uint64_t acc_lo = g.acc + static_cast<uint64_t>(slice) * p.rows * p.n * 4, acc_hi = acc_lo + p.rows * p.n * 4;
-  const bool sums = !weights && g.acc, add = sums && g.add, last = !sums || g.last;
+  const uint64_t tile = static_cast<uint64_t>(kLinearM) * kLinearN * 4;
+  const uint64_t acc_lo = weights ? g.tile + blockIdx.x / 2 * tile : g.acc + static_cast<uint64_t>(slice) * p.rows * p.n * 4;
+  const uint64_t acc_hi = acc_lo + (weights ? tile : p.rows * p.n * 4);
+  const uint64_t acc_row = weights ? row % kLinearM * kLinearN + n0 % kLinearN : row * p.n + n0;
+  const bool sums = !weights && g.acc, add = weights ? again : sums && g.add, last = weights ? whole : !sums || g.last;
 #pragma unroll 1
   for (uint32_t j0 = 0; j0 < kLinearPart && n0 + j0 < p.n; j0 += 32) {
     float v[32];
     tmem_ld32(at + j0, v);
-    if (!own) continue;
+    const int left = static_cast<int>(min(p.n - n0 - j0, 32u));
     if (empty) {  // (a slice behind the last column: nothing was multiplied)
 #pragma unroll
       for (int j = 0; j < 32; ++j) v[j] = 0.0f;
     }
-    const int left = static_cast<int>(p.n - n0 - j0);
-    float4* a = reinterpret_cast<float4*>(acc_lo) + (row * p.n + n0 + j0) / 4;
+    const float f = last || !weights ? lost.f : 0.0f;  // (dW: with the last run)
+    add_row32<DT>(v, f, lost.w);
+    if (f != 0.0f && j0 + 32 < kLinearPart) ld_row32(lost.w, lost.row, n0 + j0 + 32, p.n);  // (for the next columns)
+    if (weights && last) {
+      const uint32_t groups = linear_groups(p.rows);
+      uint64_t more = lost.more;
+      uint32_t next = lost.next;
+      while (true) {
+        for (; more; more &= more - 1) {
+          const uint64_t i = list[__ffsll(static_cast<long long>(more)) - 1] >> 5;
+          uint4 w[4];
+          ld_row32(w, g.x + i * g.x_stride, n0 + j0, p.n);
+          add_row32<DT>(v, ld_row(p.lost, i, p.rows), w);
+        }
+        if (next >= groups) break;
+        more = find_hits(p, static_cast<uint32_t>(row) & ~31u, next, list, &next);
+      }
+      if (lost.next < groups) {  // the list again
+        const uint64_t all = find_hits(p, static_cast<uint32_t>(row) & ~31u, 0, list, &next);
+        lost.more = all & (all - 1);
+      }
+    }
+    if (!own) continue;
+    float4* a = reinterpret_cast<float4*>(acc_lo) + (acc_row + j0) / 4;
     if (add) {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
@@ -241,11 +390,14 @@ template <int MODE, int DT, int NB>
 __global__ __launch_bounds__(kThreads, 1) void dc_linear_kernel(const __grid_constant__ LinearArgs<NB> args) {
   // whether B's rows run across the inner dimension (A's do for dW)
   constexpr bool kAcrossB = MODE == kLinearGrads;
+  // blocks of the inner dimension that the tensor cores sum, or all
+  constexpr uint32_t kRun = MODE == kLinearStats ? kRunBlocks : MODE == kLinearGrads ? kGradBlocks : 0;
   const LinearParams& p = args.p;
   extern __shared__ uint8_t smem[];
   __shared__ __align__(8) uint64_t bars[2 * kStages + 5];
   __shared__ uint32_t tmem_at;
   __shared__ volatile uint32_t stop;
+  __shared__ uint32_t hit_list[MODE == kLinearGrads ? kResultThreads / 32 : 1][kHits];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t ring = (smem_addr(smem) + 1023u) & ~1023u;
   const uint32_t full = smem_addr(bars), empty = full + 8 * kStages;
@@ -367,7 +519,7 @@ __global__ __launch_bounds__(kThreads, 1) void dc_linear_kernel(const __grid_con
         uint32_t kb = 0;
         do {
           const uint32_t buf = runs & 1, acc = tmem + buf * kLinearN;
-          const uint32_t from = kb, to = MODE == kLinearStats ? min(kb + kRunBlocks, x.blocks) : x.blocks;
+          const uint32_t from = kb, to = kRun ? min(kb + kRun, x.blocks) : x.blocks;
           if (runs >= 2 && !wait(waits, drained + 8 * buf, (runs / 2 - 1) & 1)) break;
           fence_after();
           for (; kb < to; ++kb, ++i) {
@@ -402,6 +554,9 @@ __global__ __launch_bounds__(kThreads, 1) void dc_linear_kernel(const __grid_con
       const uint32_t rows = MODE == kLinearGrads && x.r == 1 ? p.g.columns : p.m;
       const bool own = row < rows;
       [[maybe_unused]] float v[MODE == kLinearStats ? kLinearPart : 1];
+      [[maybe_unused]] Lost lost;
+      if constexpr (MODE == kLinearGrads)
+        if (row0 < rows) look_up(p, row, own, n0, x.r == 1, x.k0 * kLinearK, x.blocks, hit_list[warp - 2], &lost);
       uint32_t kb = 0;
       do {
         const uint32_t buf = runs & 1, at = tmem + buf * kLinearN + half * kLinearPart + (quarter << 16);
@@ -411,12 +566,12 @@ __global__ __launch_bounds__(kThreads, 1) void dc_linear_kernel(const __grid_con
         if (row0 < rows) {
           if constexpr (MODE == kLinearStats) gather_part(at, kb == 0, v);
           else if constexpr (MODE == kLinearDLogits) dlogits<DT>(p, at, row, own, n0);
-          else result<DT>(p, at, row, own, n0, x.r == 1, x.tile, x.blocks == 0);
+          else result<DT>(p, at, row, own, n0, x.r == 1, x.tile, x.blocks == 0, kb > 0, kb + kRun >= x.blocks, lost, hit_list[warp - 2]);
         }
         fence_before();
         arrive_cluster(cluster_addr(drained + 8 * buf, 0));
         ++runs;
-        kb = MODE == kLinearStats ? kb + kRunBlocks : x.blocks;
+        kb = kRun ? kb + kRun : x.blocks;
       } while (kb < x.blocks);
       if constexpr (MODE == kLinearStats) {
         const LinearShard& s = args.shard[NB > 1 ? x.r : 0];
@@ -565,7 +720,7 @@ cudaError_t launch_one(const LinearParams& p, const LinearOperand& a, const Line
   if (e != cudaSuccess) return e;
   const uint64_t tiles = MODE == kLinearGrads ? static_cast<uint64_t>(p.g.h_tiles) + p.g.w_tiles
                                               : static_cast<uint64_t>(p.m_tiles) * p.n_tiles;
-  const uint64_t pairs = std::min<uint64_t>(tiles, static_cast<uint64_t>(std::max(sms / 2, 1)));
+  const uint64_t pairs = std::min<uint64_t>(tiles, std::min(std::max(static_cast<uint32_t>(sms) / 2, 1u), kLinearPairs));
   if constexpr (MODE == kLinearGrads) plan_linear_grads(&args.p.g, static_cast<uint32_t>(pairs));
   *grid = static_cast<int>(2 * pairs);
   cudaLaunchConfig_t cfg = {};

@@ -199,6 +199,7 @@ cudaError_t launch_attend(const AttendParams& p, int dtype, int dim, bool pdl, c
 // Matrix products on the tensor cores: tiles of kLinearM x kLinearN, which a pair
 // of CTAs share, kLinearK of the inner dimension a stage.
 constexpr int kLinearM = 256, kLinearN = 256, kLinearK = 64;
+constexpr uint32_t kLinearPairs = kAttendSms / 2;  // at most, at work
 constexpr int kLinearPart = 128;  // columns that one thread reduces of a row of the logits
 // The gradient takes up to this many columns of a shard at a time, and cuts the
 // products over them into slices, both whatever the call's rows: how a sum is cut
@@ -207,6 +208,11 @@ constexpr uint32_t kLinearChunk = 24576;
 __host__ __device__ inline uint32_t linear_chunk(uint32_t width) {
   const uint32_t n = (width + kLinearChunk - 1) / kLinearChunk, per = n ? (width + n - 1) / n : 0;
   return (per + kLinearN - 1) / kLinearN * kLinearN;
+}
+__host__ __device__ inline uint32_t linear_groups(uint64_t rows) { return static_cast<uint32_t>((rows + 31) / 32); }
+// Bytes of the marks for a chunk whose rows of d take d_stride bytes.
+__host__ __device__ inline uint64_t linear_marks(uint64_t rows, uint64_t d_stride) {
+  return d_stride / (2 * kLinearN) * linear_groups(rows) * 4;
 }
 // A row of dh has ceil(size / kLinearN) tiles: with few the sum over a chunk's
 // columns is cut into slices, so that short batches have work for the GPU too.
@@ -234,7 +240,9 @@ struct LinearGrads {
   uint32_t columns;            // of the chunk
   int32_t add, last;           // what `acc` holds is added; the sum is complete (no acc: one slice)
   uint64_t acc;                // f32 [slices][rows][size] or 0
+  uint64_t tile;               // f32 [kLinearPairs][kLinearM][kLinearN] or 0: sums of dW's runs
   uint64_t out_h, out_h_stride, out_w, out_w_stride;  // bytes
+  uint64_t x, x_stride, w, w_stride;                  // the hidden rows, the chunk's rows of the weights
 };
 
 // One product C [m, n] = A B^T over k, and what becomes of it.
@@ -242,7 +250,7 @@ struct LinearParams {
   uint32_t m, n;               // extents of C (kLinearStats: n is not used; kLinearGrads: rows and hidden size)
   uint32_t m_tiles, n_tiles, k_blocks;
   uint32_t b_row0;             // first row of the weights (kLinearDLogits, kLinearGrads)
-  uint32_t vocab, first;       // kLinearDLogits: the vocabulary index of column 0
+  uint32_t vocab, first;       // the vocabulary index of column 0 (kLinearDLogits, kLinearGrads)
   float inv_t;
   int32_t tokens64;
   int32_t shards;              // kLinearStats
@@ -252,6 +260,8 @@ struct LinearParams {
   uint64_t lse, entropy, grad_logprobs, grad_entropy;  // f32 [rows]; the last two or 0
   uint64_t scale;              // f32 [2] or 0: the gradient's power of two and its inverse
   uint64_t d, d_stride;        // kLinearDLogits: [rows] of d_stride bytes
+  uint64_t lost;               // f32 [rows]: what d lost of each row's token
+  uint64_t marks;              // [tiles of kLinearN columns][groups of 32 rows]: a bit a row whose token is there
   uint64_t wait_ns;
   LinearGrads g;               // kLinearGrads
 };

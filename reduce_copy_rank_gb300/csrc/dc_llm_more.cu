@@ -73,10 +73,19 @@ dc_status_t check_head(const void* hidden, uint64_t hidden_stride, const void* c
 
 // The forward's workspace: every tile's parts, then the tokens' logits.
 uint64_t stats_bytes(uint64_t rows, uint64_t tiles) { return rows * (tiles * (kLinearN / kLinearPart) * 16 + 4); }
-// The gradient's: its power of two, then d of one chunk of the vocabulary, then
-// the sums of d W, a slice each.
+// The gradient's: its power of two, then what d loses at the rows' tokens and where
+// those are, d of one chunk of the vocabulary, and the sums of d W, a slice each.
+uint64_t lost_bytes(uint64_t rows) { return round_up(rows * 4, 256); }
+uint64_t marks_bytes(uint64_t rows, uint64_t stride) { return round_up(linear_marks(rows, stride), 256); }
 uint64_t chunk_stride(uint64_t columns) { return round_up(std::min<uint64_t>(columns, kLinearChunk), kLinearN) * 2; }
 uint64_t d_bytes(uint64_t rows, uint64_t stride) { return round_up(rows * stride, 256); }
+
+// dW's sums of one tile a pair of CTAs, where a sum takes more than one run.
+uint64_t tile_bytes(uint64_t rows) { return rows > kLinearChunk ? kLinearPairs * static_cast<uint64_t>(kLinearM) * kLinearN * 4 : 0; }
+// All of it but the sums of d W.
+uint64_t fixed_bytes(uint64_t rows, uint64_t stride) {
+  return 256 + lost_bytes(rows) + marks_bytes(rows, stride) + d_bytes(rows, stride) + tile_bytes(rows);
+}
 
 dc_status_t check_workspace(void* p, uint64_t have, uint64_t need, Spans& out) {
   if (have < need)
@@ -196,7 +205,7 @@ size_t dc_linear_logprobs_workspace_bytes(int64_t rows, int64_t hidden_size, int
   const uint64_t n = static_cast<uint64_t>(std::max<int64_t>(rows, 1)), v = static_cast<uint64_t>(columns);
   // (a shard's last tile may be narrower: at most one more tile a rank)
   if (!backward) return round_up(stats_bytes(n, (v + kLinearN - 1) / kLinearN + kMaxRanks), 256);
-  return 256 + d_bytes(n, chunk_stride(v)) +
+  return fixed_bytes(n, chunk_stride(v)) +
          round_up(n * static_cast<uint64_t>(hidden_size) * 4 * linear_slices(static_cast<uint32_t>(hidden_size)), 256);
 }
 
@@ -314,7 +323,7 @@ dc_status_t dc_linear_logprobs_backward(const dc_linear_logprobs_backward_t* a, 
       DC_TRY(take(a->grad_entropy, "grad_entropy", n * 4, 4, h.in));
       DC_TRY(take(a->entropy, "entropy", n * 4, 4, h.in));
     }
-    DC_TRY(check_workspace(a->workspace, a->workspace_bytes, 256 + d_bytes(n, stride) + (sum ? n * size * 4 * slices : 0), out));
+    DC_TRY(check_workspace(a->workspace, a->workspace_bytes, fixed_bytes(n, stride) + (sum ? n * size * 4 * slices : 0), out));
     DC_TRY(check_head_outputs(out, h));
     Shards written = gw;
     DC_TRY(outside_shards(out, written, "a shard of grad_weights"));
@@ -340,9 +349,12 @@ dc_status_t dc_linear_logprobs_backward(const dc_linear_logprobs_backward_t* a, 
   p.entropy = addr(a->entropy);
   p.grad_logprobs = addr(a->grad_logprobs);
   p.grad_entropy = addr(a->grad_entropy);
-  p.d = addr(a->workspace) + 256;
+  p.lost = addr(a->workspace) + 256;
+  p.marks = p.lost + lost_bytes(n);
+  p.d = p.marks + marks_bytes(n, stride);
+  const uint64_t tile = tile_bytes(n) ? p.d + d_bytes(n, stride) : 0;
   p.d_stride = stride;
-  const uint64_t acc = sum ? p.d + d_bytes(n, stride) : 0;
+  const uint64_t acc = sum ? addr(a->workspace) + fixed_bytes(n, stride) : 0;
   p.wait_ns = wait_limit_option();
   if (n && a->dtype == kF16) {
     p.scale = addr(a->workspace);
@@ -382,7 +394,12 @@ dc_status_t dc_linear_logprobs_backward(const dc_linear_logprobs_backward_t* a, 
       q.m = static_cast<uint32_t>(n);
       q.n = static_cast<uint32_t>(size);
       q.b_row0 = static_cast<uint32_t>(c);
+      q.first = l.first;
       LinearGrads& g = q.g;
+      g.x = x.base;
+      g.x_stride = x.stride;
+      g.w = w.base + c * w.stride;
+      g.w_stride = w.stride;
       g.columns = columns;
       g.h_blocks = (columns + kLinearK - 1) / kLinearK;
       g.slice_blocks = (g.h_blocks + slices - 1) / slices;
@@ -395,6 +412,7 @@ dc_status_t dc_linear_logprobs_backward(const dc_linear_logprobs_backward_t* a, 
       g.add = chunk > 0;
       g.last = slices == 1 && chunk + 1 == chunks;
       g.acc = acc;
+      g.tile = tile;
       g.out_h = gh.base;
       g.out_h_stride = gh.stride;
       g.out_w = gw[r].base + c * gw[r].stride;

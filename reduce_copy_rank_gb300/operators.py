@@ -348,8 +348,10 @@ def linear_logprobs_backward(hidden, weights: Sequence, tokens, lse, grad_logpro
     None.
 
     The logits are computed again, up to 24576 columns at a time; their gradient is
-    rounded to 16 bits before its products, whose sums are binary32.  Rows of
-    the weights' gradient past ``vocab`` receive 0.  ``workspace``:
+    rounded to 16 bits before its products, but for the tokens' own elements; the
+    sums are binary32.  Rows of the weights' gradient past ``vocab`` receive 0.
+    A row without upstream gradients (padding) has none, but its hidden row has
+    to be finite: the weights' gradient is a product with all of them.  ``workspace``:
     :func:`linear_logprobs_workspace` with ``backward``.  Returns
     ``(grad_hidden, grad_weights)``."""
     status = (_module or _binding()).linear_logprobs_backward(hidden, weights, tokens, lse, grad_logprobs, grad_hidden,

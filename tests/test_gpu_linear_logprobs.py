@@ -362,3 +362,78 @@ def test_offsets_past_32_bits():
     want = d @ w[some].double()
     tol = UNIT["bf16"] * want.abs() + (UNIT["bf16"] + 2.0 ** -8) * (d.abs() @ w[some].double().abs())
     assert bool(((gh.double() - want).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_tokens_that_many_rows_share(dtype):
+    a = build(700, 72, [300, 500], 790, dtype, seed=4)
+    up = upstream(700)
+    for tokens in (torch.full((700,), 311, device="cuda"), torch.arange(700, device="cuda") % 40 + 280):
+        b = (*a[:2], tokens.to(a[2].dtype))
+        check_backward(backward(*b, 790, *up), *b, 790, *up, dtype=dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_sums_over_many_rows(dtype):
+    """More rows than one sum on the tensor cores takes."""
+    rows = 60000
+    a = build(rows, 72, [300, 257], 557, dtype, seed=5)
+    up = upstream(rows)
+    ws = dc.linear_logprobs_workspace(rows, 72, 557, backward=True).fill_(255)
+    check_backward(backward(*a, 557, *up, workspace=ws), *a, 557, *up, dtype=dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_the_tokens_gradient_is_rounded_once(dtype):
+    """Where the tokens' own columns make a gradient up (flat rows: the others have 2^-12 of its square), it has the
+    error of its last rounding: half a step at most, UNIT / sqrt(3) in the root mean square."""
+    hidden, weights, tokens = build(200, 64, [5000], 5000, dtype, seed=6)
+    weights[0].mul_(2.0 ** -6)
+    g, _ = upstream(200)
+    gh, (gw,) = backward(hidden, weights, tokens, 5000, g, None)
+    z, _, w, _ = truth(hidden, weights, 5000, 1.0)
+    d = -torch.softmax(z, 1) * g.double()[:, None]
+    d.scatter_add_(1, tokens.long()[:, None], g.double()[:, None])
+    for have, want in ((gh, d @ w), (gw, d.t() @ hidden.double())):
+        assert float((have.double() - want).norm()) <= 0.6 * UNIT[dtype] * float(want.norm())
+
+
+def test_rows_without_upstream_gradients_have_none():
+    """... whatever they hold.  (The weights' gradient is a product with all hidden rows: those have to be finite.)"""
+    hidden, weights, tokens = build(200, 64, [400], 400)
+    masked = torch.arange(200, device="cuda") % 3 == 0
+    tokens[masked] = -100
+    g, e = upstream(200)
+    e[masked] = 0
+    saved = forward(hidden, weights, tokens)
+    want = backward(hidden, weights, tokens, 400, g, e, saved=saved)
+    hidden[masked] = math.nan
+    saved[2][masked] = math.nan
+    saved[1][masked] = 0
+    got = backward(hidden, weights, tokens, 400, g, e, saved=saved, weights_too=False)
+    assert torch.equal(got[0], want[0]) and bool((got[0][masked] == 0).all())
+
+
+def test_autograd_in_a_graph():
+    hidden, weights, tokens = build(50, 64, [300, 200], 500)
+    leaves = [t.detach().clone().requires_grad_() for t in (hidden, *weights)]
+    g, e = upstream(50)
+
+    def step():
+        lp, ent = dc.linear_logprobs_and_entropy(leaves[0], leaves[1:], tokens)
+        return torch.autograd.grad((lp * g + ent * e).sum(), leaves)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        want = [t.clone() for t in step()]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for _ in range(2):
+        for t in got:
+            t.fill_(3)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))

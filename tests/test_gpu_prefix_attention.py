@@ -269,3 +269,36 @@ def test_streams_graphs_and_versions():
     graph.replay()
     torch.cuda.synchronize()
     check((out, lse), *a)
+
+
+@pytest.mark.parametrize("prefixes,own", [([900, 40], [0, 300, 7, 64]), ([0, 3000], [0, 0, 1, 2])])
+def test_follows_the_calls_before_and_after_it(prefixes, own):
+    """Calls without a wait between them: appends write both parts' slots and the queries, each attention reads them,
+    and the next append overwrites them."""
+    hq, hk, d, page = 16, 2, 128, 16
+    q, kc, vc, pt, pl, ot, ol = build(prefixes, own, hq, hk, d, page)
+    tables = torch.full((6, max(pt.shape[1], ot.shape[1])), -1, dtype=torch.int32, device="cuda")
+    tables[:2, :pt.shape[1]] = pt
+    tables[2:, :ot.shape[1]] = ot
+    where = [(s, t) for s, n in enumerate(prefixes + own) for t in sorted({0, n // 2, n - 1}) if n > 0]  # (a slot once)
+    seqs, pos = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in zip(*where))
+    steps = 12
+    g = torch.Generator(device="cuda").manual_seed(9)
+    k, v = (torch.randn(steps, len(where), hk, d, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    new = torch.randn(steps, *q.shape, generator=g, device="cuda").to(torch.bfloat16)
+    ws = dc.prefix_attention_workspace(4, 2, hq, hk, d, pt.shape[1] * page, ot.shape[1] * page)
+    results = []
+    for wait in (True, False):
+        out = torch.zeros(steps, *q.shape, device="cuda", dtype=q.dtype)
+        torch.cuda.synchronize()
+        for i in range(steps):
+            dc.kv_append(k[i], v[i], pos, seqs, tables, kc, vc)
+            q.copy_(new[i])
+            if wait:
+                torch.cuda.synchronize()
+            dc.prefix_attention(q, kc, vc, pt, pl, ot, ol, out[i], ws)
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        results.append(out)
+    assert torch.equal(*results)

@@ -306,3 +306,26 @@ def test_streams_graphs_and_versions():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(written, want))
+
+
+def test_autograd_in_a_graph():
+    q, k, _, pos, cs, w, dy = build(70, 4, 2, 64, 64)
+    leaves = [t.detach().clone().requires_grad_() for t in (q, k, *w)]
+
+    def step():
+        return torch.autograd.grad(dc.normed_queries_and_keys(*leaves[:2], pos, cs, *leaves[2:], eps=EPS), leaves, dy)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        want = [t.clone() for t in step()]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for _ in range(2):
+        for t in got:
+            t.fill_(3)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
