@@ -195,6 +195,7 @@ __device__ __forceinline__ void dlogits(const LinearParams& p, uint32_t at, uint
 #pragma unroll 1
   for (uint32_t j0 = 0; j0 < kLinearPart && n0 + j0 < ld; j0 += 32) {
     float v[32], exact = 0.0f;
+    __syncwarp();
     tmem_ld32(at + j0, v);
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
@@ -332,6 +333,7 @@ __device__ __forceinline__ void result(const LinearParams& p, uint32_t at, uint6
 #pragma unroll 1
   for (uint32_t j0 = 0; j0 < kLinearPart && n0 + j0 < p.n; j0 += 32) {
     float v[32];
+    __syncwarp();
     tmem_ld32(at + j0, v);
     const int left = static_cast<int>(min(p.n - n0 - j0, 32u));
     if (empty) {  // (a slice behind the last column: nothing was multiplied)
@@ -809,15 +811,18 @@ cudaError_t launch_linear(int mode, int dtype, const LinearParams& p, const Line
 void plan_linear_grads(LinearGrads* g, uint32_t pairs) {
   g->rounds = g->h_tiles / pairs;
   g->rest = g->h_tiles % pairs;
-  // blocks of the inner dimension that each pair should get in all
-  const uint64_t work = static_cast<uint64_t>(g->h_tiles) * g->slice_blocks + static_cast<uint64_t>(g->w_tiles) * g->w_blocks;
-  const uint64_t each = (work + pairs - 1) / pairs, had = (g->rounds + 1ull) * g->slice_blocks;
-  g->few = g->w_blocks && each > had ? static_cast<uint32_t>((each - had) / g->w_blocks) : 0;
-  if (g->rest == 0) g->few = 0;
-  // (g->few * pairs tiles at most: no more than there are)
-  if (static_cast<uint64_t>(g->few) * pairs > g->w_tiles) g->few = g->w_tiles / pairs;
-  const uint32_t left = g->w_tiles - g->few * pairs, on = pairs - g->rest;
-  g->many = g->few + (left + on - 1) / on;
+  // The number of common rounds after which those who had a dh tile less end with the others.
+  const uint32_t on = pairs - g->rest;
+  uint64_t best = ~0ull;
+  for (uint32_t few = 0; few <= (g->rest ? g->w_tiles / pairs : 0); ++few) {
+    const uint32_t many = few + (g->w_tiles - few * pairs + on - 1) / on;
+    const uint64_t end = std::max((g->rest ? g->slice_blocks : 0) + static_cast<uint64_t>(few) * g->w_blocks,
+                                  static_cast<uint64_t>(many) * g->w_blocks);
+    if (end >= best) continue;
+    best = end;
+    g->few = few;
+    g->many = many;
+  }
 }
 
 cudaError_t launch_linear_sum(const LinearSumParams& p, int dtype, bool pdl, cudaStream_t s, int* grid) {
