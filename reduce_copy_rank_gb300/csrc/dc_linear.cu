@@ -33,6 +33,9 @@
 // still a normal number.
 //
 // Bound: the tensor cores for training batches, the weights' bytes for few rows.
+// Measured, BF16, 4096 rows of 4096 against 128000 columns: forward 2.58 ms, 1.66
+// PFLOP/s, gradient 8.4 ms, 1.53 (tiles of 128 x 256 a CTA, without the pair: 2.71 and
+// 8.84); 128 rows against 131072 columns on 8 shards: 195 us, 5.5 TB/s.
 #include <algorithm>
 #include <atomic>
 
