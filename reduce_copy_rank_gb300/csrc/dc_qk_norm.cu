@@ -197,8 +197,8 @@ __global__ __launch_bounds__(kNormThreads, norm_ctas_per_sm(UNITS, GRADIENT)) vo
   const uint64_t items = p.tokens * static_cast<uint64_t>(job.split);
   for (uint64_t item = static_cast<uint64_t>(blockIdx.x - job.cta0) * kWarps + warp; item < items;
        item += static_cast<uint64_t>(job.ctas) * kWarps) {
-    const uint64_t token = item / static_cast<uint32_t>(job.split);
-    const int first = static_cast<int>(item % static_cast<uint32_t>(job.split)) * heads_at_once;
+    const uint64_t token = job.split == 1 ? item : item / static_cast<uint32_t>(job.split);
+    const int first = job.split == 1 ? 0 : static_cast<int>(item % static_cast<uint32_t>(job.split)) * heads_at_once;
     const uint64_t x_row = job.x.base + token * job.x.token;
     [[maybe_unused]] const uint64_t dy_row = job.dy.base + token * job.dy.token;
     typename K::Raw next[K::kAhead];
