@@ -391,6 +391,22 @@ __device__ __forceinline__ void result(const LinearParams& p, uint32_t at, uint6
   }
 }
 
+// Tile t of fast x slow, in bands of `band` of the first, so that the tiles that run at
+// the same time share their operands and a band's stay in L2.  Bands of 16 rows of
+// tiles for the logits, of 8 for dh, of 8 columns for dW.  Measured, BF16, against all
+// rows first (dW: all of the vocabulary first): 4096 rows of 4096 and 128000 columns,
+// gradient 8.67 -> 8.03 ms; 16384 rows and 64000 columns, forward 5.15 -> 4.62 (1.86
+// PFLOP/s), gradient 17.2 -> 15.0 ms (1.72).  Bands of 8 for the logits cost that
+// forward nothing and 4096 rows 3 %; of 16 for dh and dW: 8.11 and 15.4 ms.
+struct Spot {
+  uint32_t fast, slow;
+};
+__device__ __forceinline__ Spot spot(uint32_t t, uint32_t fast, uint32_t slow, uint32_t band) {
+  const uint32_t b = t / (band * slow), r = t - b * (band * slow), w = max(1u, min(band, fast - b * band));
+  return {b * band + r % w, r / w};
+}
+constexpr uint32_t kLogitBand = 16, kGradBand = 8;
+
 template <int MODE, int DT, int NB>
 __global__ __launch_bounds__(kThreads, 1) void dc_linear_kernel(const __grid_constant__ LinearArgs<NB> args) {
   // whether B's rows run across the inner dimension (A's do for dW)
@@ -450,24 +466,27 @@ __global__ __launch_bounds__(kThreads, 1) void dc_linear_kernel(const __grid_con
       const uint32_t mine = g.rounds + (c < g.rest);
       if (n < mine) {
         const uint32_t t = c + n * G, s = t / (g.h_m * g.h_n);
-        x.m0 = t % g.h_m * kLinearM;
-        x.n0 = t / g.h_m % g.h_n * kLinearN;
+        const Spot at = spot(t - s * (g.h_m * g.h_n), g.h_m, g.h_n, kGradBand);
+        x.m0 = at.fast * kLinearM;
+        x.n0 = at.slow * kLinearN;
         x.k0 = s * g.slice_blocks;
         x.blocks = min(g.slice_blocks, g.h_blocks > x.k0 ? g.h_blocks - x.k0 : 0u);
         x.tile = s;
       } else {
         const uint32_t k = n - mine, t = k < g.few ? k * G + c : g.few * G + (k - g.few) * (G - g.rest) + c - g.rest;
         x.there = (k < g.few || (c >= g.rest && k < g.many)) && t < g.w_tiles;
-        x.m0 = t % g.w_m * kLinearM;
-        x.n0 = t / g.w_m * kLinearN;
+        const Spot at = spot(t, g.h_n, g.w_m, kGradBand);
+        x.m0 = at.slow * kLinearM;
+        x.n0 = at.fast * kLinearN;
         x.blocks = g.w_blocks;
         x.r = 1;
       }
     } else {
       const uint64_t t = c + static_cast<uint64_t>(n) * G;
       x.there = t < static_cast<uint64_t>(p.m_tiles) * p.n_tiles;
-      x.m0 = static_cast<uint32_t>(t) % p.m_tiles * kLinearM;
-      x.n0 = x.tile = static_cast<uint32_t>(t) / p.m_tiles;
+      const Spot at = spot(static_cast<uint32_t>(t), p.m_tiles, p.n_tiles, kLogitBand);
+      x.m0 = at.fast * kLinearM;
+      x.n0 = x.tile = at.slow;
       if constexpr (MODE == kLinearStats) {
         if constexpr (NB > 1)
           while (x.r + 1 < p.shards && args.shard[x.r + 1].tile0 <= x.n0) ++x.r;
