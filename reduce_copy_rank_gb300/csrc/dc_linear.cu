@@ -33,9 +33,9 @@
 // still a normal number.
 //
 // Bound: the tensor cores for training batches, the weights' bytes for few rows.
-// Measured, BF16, 4096 rows of 4096 against 128000 columns: forward 2.58 ms, 1.66
-// PFLOP/s, gradient 8.4 ms, 1.53 (tiles of 128 x 256 a CTA, without the pair: 2.71 and
-// 8.84); 128 rows against 131072 columns on 8 shards: 195 us, 5.5 TB/s.
+// Measured, BF16, 4096 rows of 4096 against 128000 columns: forward 2.63 ms, 1.63
+// PFLOP/s, gradient 8.05 ms, 1.60 (tiles of 128 x 256 a CTA, without the pair: 2.71 and
+// 8.84); 128 rows against 131072 columns on 8 shards: 204 us, 5.3 TB/s.
 #include <algorithm>
 #include <atomic>
 
@@ -59,12 +59,13 @@ constexpr int kABytes = kHalfM / 64 * kTileBytes, kBBytes = kHalfN / 64 * kTileB
 constexpr int kStageBytes = kABytes + kBBytes;        // of one CTA
 constexpr int kSmem = kStages * kStageBytes + 1024;   // (the ring starts at a multiple of 1024)
 // The tensor cores' sums lose more than a rounding a step (the error grows with
-// their number, not its root).  The logits of the forward are therefore summed 1024
-// elements at a time, and those sums added up, rounded, in registers.  Measured, 4096
-// rows of 4096 against 128000 columns, runs of 512 / 1024 / 2048 / 4096 elements:
-// relative error of the log probabilities and lse 2.0e-7 / 4.2e-7 / 8.9e-7 / 3.6e-6
-// (binary32 matrix product: 5e-7), 2.67 / 2.60 / 2.51 / 2.52 ms.
-constexpr uint32_t kRunBlocks = 16;
+// their number, not its root).  The logits of the forward are therefore summed 512
+// elements at a time, and those sums added up, rounded, in registers.  Measured, 1543
+// rows of 4040 against 41592 columns, runs of 512 / 768 / 1024 elements: relative
+// error of the log probabilities 1.7e-7 / 2.6e-7 / 3.5e-7 and the entropies 2.6e-7 /
+// 3.9e-7 / 5.4e-7 (a binary32 matrix product: 3.3e-7, 3.1e-7); 4096 rows of 4096
+// against 128000: 2.63 / 2.58 / 2.55 ms, of 256: 3.2 ms.
+constexpr uint32_t kRunBlocks = 8;
 // The gradient's products are rounded to 16 bits afterwards: 24576 rows (or columns
 // of a chunk) at a time.  Measured, FP16, dW of terms of one sign, 131072 / 2^20 rows,
 // error against its last rounding's 2.1e-4: in one run 5.9e-4 / 4.5e-3.
@@ -97,8 +98,10 @@ __device__ __forceinline__ void stats(const LinearParams& p, float (&v)[kLinearP
                                       uint32_t limit) {
   const float c = p.inv_t * kLog2E;
   const int64_t mine = token_of(p.tokens, p.tokens64, row) - static_cast<int64_t>(column0);  // the token's column, if it is here
+  if (limit < kLinearPart) {
 #pragma unroll
-  for (int j = 0; j < kLinearPart; ++j) v[j] = static_cast<uint32_t>(j) < limit ? v[j] * c : neg_inf();
+    for (int j = 0; j < kLinearPart; ++j) v[j] = static_cast<uint32_t>(j) < limit ? v[j] : neg_inf();
+  }
   if (mine >= 0 && mine < static_cast<int64_t>(limit)) {
     float z = 0.0f;
 #pragma unroll
@@ -109,14 +112,14 @@ __device__ __forceinline__ void stats(const LinearParams& p, float (&v)[kLinearP
   float m[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
 #pragma unroll
   for (int j = 0; j < kLinearPart; j += 2) m[j / 2 & 3] = max3(m[j / 2 & 3], v[j], v[j + 1]);
-  const float top = fmaxf(max3(m[0], m[1], m[2]), m[3]);
+  const float top = fmaxf(max3(m[0], m[1], m[2]), m[3]) * c;
   const float ref = ceilf(top), base = ref == neg_inf() ? 0.0f : ref;
   float s[4] = {}, t[4] = {};
 #pragma unroll
   for (int j = 0; j < kLinearPart; ++j) {
-    const float x = v[j] - base, e = ex2(x);
+    const float x = __fmaf_rn(v[j], c, -base), e = ex2(x);
     s[j & 3] += e;
-    t[j & 3] = __fmaf_rn(e, x < -1e4f ? -1e4f : x, t[j & 3]);
+    t[j & 3] = __fmaf_rn(e, fmaxf(x, -1e4f), t[j & 3]);  // (e is 0 or NaN where that matters)
   }
   float4* a = reinterpret_cast<float4*>(p.part) + static_cast<uint64_t>(part) * p.rows + row;
   if (in_bounds(a, 16, p.part, p.target, kSitePart))
@@ -663,7 +666,7 @@ __global__ __launch_bounds__(kFinishThreads) void dc_linear_finish_kernel(const 
   };
   float lp = 0.0f;
   if (token >= static_cast<int64_t>(p.vocab)) lp = nan;
-  else if (token >= 0) lp = ((ld_row(p.target, row, p.rows) - ref) - log_s) * kLn2;
+  else if (token >= 0) lp = (__fmaf_rn(ld_row(p.target, row, p.rows), p.inv_t * kLog2E, -ref) - log_s) * kLn2;
   put(p.logprobs, lp);
   if (p.entropy) put(p.entropy, (log_s - t / s) * kLn2);
   if (p.lse) put(p.lse, (ref + log_s) * kLn2);

@@ -270,7 +270,8 @@ struct LinearFinishParams {
   uint64_t part, target, tokens, logprobs, entropy, lse;  // the last three f32 [rows], two of them or 0
   uint64_t rows;
   uint32_t parts, vocab;
-  int32_t tokens64, pad;
+  int32_t tokens64;
+  float inv_t;
 };
 
 // dh from its slices' sums, which are added in order.

@@ -267,6 +267,7 @@ dc_status_t dc_linear_logprobs(const dc_linear_logprobs_t* a, dc_stream_t stream
   f.parts = p.n_tiles * (kLinearN / kLinearPart);
   f.vocab = p.vocab;
   f.tokens64 = p.tokens64;
+  f.inv_t = p.inv_t;
   e = launch_linear_finish(f, pdl_option(), s, &grid);
   return check_launch(e, "log probabilities of a linear head", grid);
 }
