@@ -60,12 +60,14 @@ constexpr int kStageBytes = kABytes + kBBytes;        // of one CTA
 constexpr int kSmem = kStages * kStageBytes + 1024;   // (the ring starts at a multiple of 1024)
 // The tensor cores' sums lose more than a rounding a step (the error grows with
 // their number, not its root).  The logits of the forward are therefore summed 512
-// elements at a time, and those sums added up, rounded, in registers.  Measured, 1543
-// rows of 4040 against 41592 columns, runs of 512 / 768 / 1024 elements: relative
-// error of the log probabilities 1.7e-7 / 2.6e-7 / 3.5e-7 and the entropies 2.6e-7 /
-// 3.9e-7 / 5.4e-7 (a binary32 matrix product: 3.3e-7, 3.1e-7); 4096 rows of 4096
-// against 128000: 2.63 / 2.58 / 2.55 ms, of 256: 3.2 ms.
-constexpr uint32_t kRunBlocks = 8;
+// elements at a time, or 256 of hidden sizes up to 1024 (whose binary32 sums would be
+// that good), and those sums added up, rounded, in registers.  Measured, 1543 rows of
+// 4040 against 41592 columns, runs of 512 / 768 / 1024 elements: relative error of
+// the log probabilities 1.7e-7 / 2.6e-7 / 3.5e-7 and the entropies 2.6e-7 / 3.9e-7 /
+// 5.4e-7 (a binary32 matrix product: 3.3e-7, 3.1e-7); 4096 rows of 4096 against
+// 128000: 2.63 / 2.58 / 2.55 ms, of 256: 2.96 ms.  4 rows of 512, runs of 512 / 256:
+// entropies 5e-7 / 1.5e-7, 10.2 us either way.
+constexpr uint32_t kRunBlocks = 8, kShortRunBlocks = 4, kShortBlocks = 16;
 // The gradient's products are rounded to 16 bits afterwards: 24576 rows (or columns
 // of a chunk) at a time.  Measured, FP16, dW of terms of one sign, 131072 / 2^20 rows,
 // error against its last rounding's 2.1e-4: in one run 5.9e-4 / 4.5e-3.
@@ -126,14 +128,14 @@ __device__ __forceinline__ void stats(const LinearParams& p, float (&v)[kLinearP
     *a = make_float4(ref, (s[0] + s[1]) + (s[2] + s[3]), (t[0] + t[1]) + (t[2] + t[3]), 0.0f);
 }
 
-// Adds the tile's accumulators to v (or, the first time, sets it).
-__device__ __forceinline__ void gather_part(uint32_t at, bool set, float (&v)[kLinearPart]) {
+// Adds the tile's accumulators to v.
+__device__ __forceinline__ void gather_part(uint32_t at, float (&v)[kLinearPart]) {
 #pragma unroll
   for (int j0 = 0; j0 < kLinearPart; j0 += 16) {  // (16 at a time: v leaves room for no more)
     float x[16];
     tmem_ld16(at + j0, x);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) v[j0 + j] = set ? x[j] : v[j0 + j] + x[j];
+    for (int j = 0; j < 16; ++j) v[j0 + j] += x[j];
   }
 }
 
@@ -414,9 +416,9 @@ template <int MODE, int DT, int NB>
 __global__ __launch_bounds__(kThreads, 1) void dc_linear_kernel(const __grid_constant__ LinearArgs<NB> args) {
   // whether B's rows run across the inner dimension (A's do for dW)
   constexpr bool kAcrossB = MODE == kLinearGrads;
-  // blocks of the inner dimension that the tensor cores sum, or all
-  constexpr uint32_t kRun = MODE == kLinearStats ? kRunBlocks : MODE == kLinearGrads ? kGradBlocks : 0;
   const LinearParams& p = args.p;
+  // blocks of the inner dimension that the tensor cores sum
+  const uint32_t run = MODE == kLinearStats ? p.run : MODE == kLinearGrads ? kGradBlocks : 1u << 30;
   extern __shared__ uint8_t smem[];
   __shared__ __align__(8) uint64_t bars[2 * kStages + 5];
   __shared__ uint32_t tmem_at;
@@ -434,7 +436,7 @@ __global__ __launch_bounds__(kThreads, 1) void dc_linear_kernel(const __grid_con
     }
     for (int i = 0; i < 2; ++i) {
       tma::mbar_init(done + 8 * i, 1);
-      tma::mbar_init(drained + 8 * i, 2 * kResultThreads);
+      tma::mbar_init(drained + 8 * i, 2 * kResultThreads / 32);
     }
     tma::mbar_init(over, 1);
     tma::mbar_init_fence();
@@ -546,7 +548,7 @@ __global__ __launch_bounds__(kThreads, 1) void dc_linear_kernel(const __grid_con
         uint32_t kb = 0;
         do {
           const uint32_t buf = runs & 1, acc = tmem + buf * kLinearN;
-          const uint32_t from = kb, to = kRun ? min(kb + kRun, x.blocks) : x.blocks;
+          const uint32_t from = kb, to = min(kb + run, x.blocks);
           if (runs >= 2 && !wait(waits, drained + 8 * buf, (runs / 2 - 1) & 1)) break;
           fence_after();
           for (; kb < to; ++kb, ++i) {
@@ -580,7 +582,7 @@ __global__ __launch_bounds__(kThreads, 1) void dc_linear_kernel(const __grid_con
       const uint64_t row = row0 + lane;
       const uint32_t rows = MODE == kLinearGrads && x.r == 1 ? p.g.columns : p.m;
       const bool own = row < rows;
-      [[maybe_unused]] float v[MODE == kLinearStats ? kLinearPart : 1];
+      [[maybe_unused]] float v[MODE == kLinearStats ? kLinearPart : 1] = {};
       [[maybe_unused]] Lost lost;
       if constexpr (MODE == kLinearGrads)
         if (row0 < rows) look_up(p, row, own, n0, x.r == 1, x.k0 * kLinearK, x.blocks, hit_list[warp - 2], &lost);
@@ -591,14 +593,15 @@ __global__ __launch_bounds__(kThreads, 1) void dc_linear_kernel(const __grid_con
         if (!there) break;
         fence_after();
         if (row0 < rows) {
-          if constexpr (MODE == kLinearStats) gather_part(at, kb == 0, v);
+          if constexpr (MODE == kLinearStats) gather_part(at, v);
           else if constexpr (MODE == kLinearDLogits) dlogits<DT>(p, at, row, own, n0);
-          else result<DT>(p, at, row, own, n0, x.r == 1, x.tile, x.blocks == 0, kb > 0, kb + kRun >= x.blocks, lost, hit_list[warp - 2]);
+          else result<DT>(p, at, row, own, n0, x.r == 1, x.tile, x.blocks == 0, kb > 0, kb + run >= x.blocks, lost, hit_list[warp - 2]);
         }
         fence_before();
-        arrive_cluster(cluster_addr(drained + 8 * buf, 0));
+        __syncwarp();
+        if (lane == 0) arrive_cluster(cluster_addr(drained + 8 * buf, 0));  // (of every thread, 512 of them took longer than the reading)
         ++runs;
-        kb = kRun ? kb + kRun : x.blocks;
+        kb += run;
       } while (kb < x.blocks);
       if constexpr (MODE == kLinearStats) {
         const LinearShard& s = args.shard[NB > 1 ? x.r : 0];
@@ -747,6 +750,7 @@ cudaError_t launch_one(const LinearParams& p, const LinearOperand& a, const Line
   if (e != cudaSuccess) return e;
   const uint64_t tiles = MODE == kLinearGrads ? static_cast<uint64_t>(p.g.h_tiles) + p.g.w_tiles
                                               : static_cast<uint64_t>(p.m_tiles) * p.n_tiles;
+  args.p.run = p.k_blocks <= kShortBlocks ? kShortRunBlocks : kRunBlocks;
   const uint64_t pairs = std::min<uint64_t>(tiles, std::min(std::max(static_cast<uint32_t>(sms) / 2, 1u), kLinearPairs));
   if constexpr (MODE == kLinearGrads) plan_linear_grads(&args.p.g, static_cast<uint32_t>(pairs));
   *grid = static_cast<int>(2 * pairs);
@@ -789,7 +793,7 @@ namespace {
 using Encode = decltype(&cuTensorMapEncodeTiled);
 cudaError_t encode_tiled(CUtensorMap* map, int dtype, uint64_t base, int dims, const cuuint64_t* size, const cuuint64_t* stride,
                          const cuuint32_t* box) {
-  static std::atomic<Encode> encode{nullptr};  // the driver's function, looked up once
+  static std::atomic<Encode> encode{nullptr};  // the CUDA driver's function, looked up once
   Encode f = encode.load(std::memory_order_acquire);
   if (!f) {
     void* at = nullptr;

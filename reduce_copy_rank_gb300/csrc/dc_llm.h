@@ -249,6 +249,7 @@ struct LinearGrads {
 struct LinearParams {
   uint32_t m, n;               // extents of C (kLinearStats: n is not used; kLinearGrads: rows and hidden size)
   uint32_t m_tiles, n_tiles, k_blocks;
+  uint32_t run;                // kLinearStats: blocks of a sum on the tensor cores
   uint32_t b_row0;             // first row of the weights (kLinearDLogits, kLinearGrads)
   uint32_t vocab, first;       // the vocabulary index of column 0 (kLinearDLogits, kLinearGrads)
   float inv_t;
