@@ -1300,11 +1300,11 @@ dc_status_t dc_check_device(void) {
   static cudaError_t (*const kReaders[kBoundsReaders])(BoundsFault*) = {
       take_bounds_gather, take_bounds_bulk, take_bounds_fused,
       take_bounds_reduce_bf16, take_bounds_reduce_f16, take_bounds_reduce_f32,
-      take_bounds_logprobs, take_bounds_append, take_bounds_attention, take_bounds_linear,
+      take_bounds_logprobs, take_bounds_append, take_bounds_attention, take_bounds_attention_parts, take_bounds_linear,
       take_bounds_norm, take_bounds_prefix};
   static const char* const kFiles[kBoundsReaders] = {"dc_gather.cu", "dc_bulk.cu", "dc_fused.cu",
                                                      "dc_reduce_bf16.cu", "dc_reduce_f16.cu", "dc_reduce_f32.cu",
-                                                     "dc_logprobs.cu", "dc_kv_append.cu", "dc_attention.cu",
+                                                     "dc_logprobs.cu", "dc_kv_append.cu", "dc_attention.cu", "dc_attention_parts.cu",
                                                      "dc_linear.cu", "dc_qk_norm.cu", "dc_prefix.cu"};
   BoundsFault first{};
   int first_file = -1;

@@ -291,7 +291,7 @@ cudaError_t take_bulk_faults(uint32_t* bits);
 // returns an empty one in the normal build.  bounds_file names the file of
 // reader i (i < kBoundsReaders).
 struct BoundsFault;
-constexpr int kBoundsReaders = 12;
+constexpr int kBoundsReaders = 13;
 cudaError_t take_bounds_gather(BoundsFault* f);
 cudaError_t take_bounds_bulk(BoundsFault* f);
 cudaError_t take_bounds_fused(BoundsFault* f);
@@ -301,6 +301,7 @@ cudaError_t take_bounds_reduce_f32(BoundsFault* f);
 cudaError_t take_bounds_logprobs(BoundsFault* f);
 cudaError_t take_bounds_append(BoundsFault* f);
 cudaError_t take_bounds_attention(BoundsFault* f);
+cudaError_t take_bounds_attention_parts(BoundsFault* f);
 cudaError_t take_bounds_linear(BoundsFault* f);
 cudaError_t take_bounds_norm(BoundsFault* f);
 cudaError_t take_bounds_prefix(BoundsFault* f);

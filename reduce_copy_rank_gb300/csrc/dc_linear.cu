@@ -33,9 +33,9 @@
 // still a normal number.
 //
 // Bound: the tensor cores for training batches, the weights' bytes for few rows.
-// Measured, BF16, 4096 rows of 4096 against 128000 columns: forward 2.63 ms, 1.63
-// PFLOP/s, gradient 8.05 ms, 1.60 (tiles of 128 x 256 a CTA, without the pair: 2.71 and
-// 8.84); 128 rows against 131072 columns on 8 shards: 204 us, 5.3 TB/s.
+// Measured, BF16, 4096 rows of 4096 against 128000 columns: forward 2.66 ms, 1.61
+// PFLOP/s, gradient 8.14 ms, 1.58 (tiles of 128 x 256 a CTA, without the pair: 2.71 and
+// 8.84); 128 rows against 131072 columns on 8 shards: 201 us, 5.3 TB/s.
 #include <algorithm>
 #include <atomic>
 
@@ -65,7 +65,7 @@ constexpr int kSmem = kStages * kStageBytes + 1024;   // (the ring starts at a m
 // 4040 against 41592 columns, runs of 512 / 768 / 1024 elements: relative error of
 // the log probabilities 1.7e-7 / 2.6e-7 / 3.5e-7 and the entropies 2.6e-7 / 3.9e-7 /
 // 5.4e-7 (a binary32 matrix product: 3.3e-7, 3.1e-7); 4096 rows of 4096 against
-// 128000: 2.63 / 2.58 / 2.55 ms, of 256: 2.96 ms.  4 rows of 512, runs of 512 / 256:
+// 128000: 2.66 / 2.60 / 2.57 ms, of 256: 2.96 ms.  4 rows of 512, runs of 512 / 256:
 // entropies 5e-7 / 1.5e-7, 10.2 us either way.
 constexpr uint32_t kRunBlocks = 8, kShortRunBlocks = 4, kShortBlocks = 16;
 // The gradient's products are rounded to 16 bits afterwards: 24576 rows (or columns

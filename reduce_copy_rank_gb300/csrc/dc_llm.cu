@@ -217,7 +217,7 @@ dc_status_t run_attend(AttendParams& p, const AttendPlan& plan, int dtype, int d
   // more units than the counters have room for (29127 at least): a CTA each
   if (!cluster && plan.pieces > 1 && plan.units * attend_counters(plan.pieces) * 4 > kAttendCounterBytes) p.places = 1;
   int grid = 0;
-  const cudaError_t e = launch_attend(p, dtype, dim, pdl_option(), static_cast<cudaStream_t>(stream), &grid);
+  const cudaError_t e = (p.raw ? launch_attend_parts : launch_attend)(p, dtype, dim, pdl_option(), static_cast<cudaStream_t>(stream), &grid);
   return check_launch(e, "paged attention", grid);
 }
 

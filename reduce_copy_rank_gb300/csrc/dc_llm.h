@@ -194,6 +194,7 @@ __host__ __device__ inline int attend_head_block(int group, uint64_t kv_units, u
   return group > 8 && ctas > kAttendSms * static_cast<uint64_t>(attend_ctas_per_sm(dim, 8)) ? 16 : 8;
 }
 cudaError_t launch_attend(const AttendParams& p, int dtype, int dim, bool pdl, cudaStream_t s, int* grid);
+cudaError_t launch_attend_parts(const AttendParams& p, int dtype, int dim, bool pdl, cudaStream_t s, int* grid);  // to raw, raw_rl
 
 // ------------------------------------------- log probabilities of a linear head
 // Matrix products on the tensor cores: tiles of kLinearM x kLinearN, which a pair
