@@ -728,8 +728,9 @@ size_t dc_attention_workspace_bytes(int64_t seqs, int q_heads, int kv_heads, int
  * empty, or both (zeros and lse = -inf).  A page outside the cache, or a length
  * past its table, gives NaN in the sequences that it belongs to.
  * The prefix's weights are rounded to 16 bits before they meet the values (half
- * a step each, of either sign), everything else as in dc_paged_attention; an
- * infinite value gives infinities or NaN.
+ * a step each, of either sign; for DC_F16 down to 2^-31 of the row's largest),
+ * everything else as in dc_paged_attention; an infinite value gives infinities
+ * or NaN.
  * A sequence's bits depend on its own tokens and its prefix's, not on the other
  * sequences or prefixes.
  * own.workspace: dc_prefix_attention_workspace_bytes(seqs, prefixes, q_heads,
