@@ -761,7 +761,10 @@ size_t dc_prefix_attention_workspace_bytes(int64_t seqs, int64_t prefixes, int q
  * in a device word, waits with the same bound for its own copies in flight
  * and returns, leaving that call's output incomplete.  No correct bulk launch
  * on a working GPU ever runs out; a fused launch runs out when a rank never
- * arrives.
+ * arrives.  The tensor-core kernels of dc_linear_logprobs, its gradient and
+ * dc_prefix_attention bound their waits for operands, products and results the
+ * same way; what they still have in flight then is waited for with a limit of its own (ten
+ * seconds).  None of them runs out on a working GPU at the default.
  *
  * Synchronous: it first waits for all work on the current device
  * (cudaDeviceSynchronize), then reads and clears the fault words.
@@ -843,6 +846,10 @@ const char *dc_status_name(int status);
  *                             at least 1000)
  *   "test_bulk_short_tx"      1 = every bulk CTA's first wait runs out (tests
  *                             of dc_check_device)
+ *   "test_tensor_late"        tests of the tensor-core kernels' bounded waits:
+ *                             1 or 2 = results of the even or odd CTAs are
+ *                             late, 3 or 4 = their copies; attention to shared
+ *                             prefixes: 1 = a tile's weights, 2 = its values
  *   "gather_realign_warp"     1 (default) = a dc_all_gather whose payloads or
  *                             output are not 16-byte aligned (at least 128
  *                             bytes per rank, output under 4 GiB), and the

@@ -89,6 +89,7 @@ struct Options {
   std::atomic<long long> test_fused_absent{0};
   std::atomic<long long> wait_limit_ns{1000000000};
   std::atomic<long long> test_bulk_short_tx{0};
+  std::atomic<long long> test_tensor_late{0};
 };
 constexpr int kMaxDevices = 64;
 std::atomic<int> g_sms[kMaxDevices];  // SM counts read so far
@@ -131,6 +132,7 @@ const OptionKey kKeys[] = {
     {"test_fused_absent_ranks", nullptr, &g_opt.test_fused_absent},
     {"wait_limit_ns", "DC_WAIT_LIMIT_NS", &g_opt.wait_limit_ns},
     {"test_bulk_short_tx", nullptr, &g_opt.test_bulk_short_tx},
+    {"test_tensor_late", nullptr, &g_opt.test_tensor_late},
 };
 
 void read_env_once() {
@@ -158,6 +160,8 @@ bool pdl_option() { return g_opt.pdl.load() != 0; }
 bool launch_failure_injected() { return g_opt.test_fail_launch.load() != 0; }
 
 uint64_t wait_limit_option() { return static_cast<uint64_t>(std::max(g_opt.wait_limit_ns.load(), 1000LL)); }
+
+int tensor_late_option() { return static_cast<int>(g_opt.test_tensor_late.load()); }
 
 dc_status_t fail(dc_status_t s, const char* fmt, ...) {
   va_list ap;
@@ -1342,8 +1346,9 @@ dc_status_t dc_check_device(void) {
                 "its output is incomplete");
   if ((tensor | prefix) & kFaultTensorWait)
     return fail(DC_ERR_TIMEOUT,
-                "%s gave up waiting for a matrix product's operands after wait_limit_ns; its output is incomplete",
-                tensor ? "a linear head's log probabilities or gradient" : "an attention to shared prefixes");
+                "%s gave up waiting for a matrix product's operands after wait_limit_ns; its output is incomplete%s",
+                tensor ? "a linear head's log probabilities or gradient" : "an attention to shared prefixes",
+                (tensor | prefix) & kFaultTensorDrain ? ", and what was under way did not end" : "");
   return ok();
 }
 

@@ -23,5 +23,6 @@ void read_options();               // the environment's initial values, once
 bool pdl_option();                 // "pdl"
 bool launch_failure_injected();    // "test_fail_launch"
 uint64_t wait_limit_option();      // "wait_limit_ns"
+int tensor_late_option();          // "test_tensor_late"
 
 }  // namespace dc

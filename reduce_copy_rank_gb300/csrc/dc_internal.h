@@ -151,7 +151,7 @@ struct BulkParams {
 };
 enum : uint32_t { kBulkTestShortTx = 1u };
 // Device fault bits (sticky until read by dc_check_device).
-enum : uint32_t { kFaultBulkWait = 1u, kFaultFusedWait = 2u, kFaultTensorWait = 4u };
+enum : uint32_t { kFaultBulkWait = 1u, kFaultFusedWait = 2u, kFaultTensorWait = 4u, kFaultTensorDrain = 8u };
 
 // The staged all-gather protocol (dc_fused.cu): P ranks, each a group of G
 // CTAs of one cooperative launch; rank r's bytes are cut into G chunks of

@@ -38,6 +38,7 @@
 // 8.84); 128 rows against 131072 columns on 8 shards: 201 us, 5.3 TB/s.
 #include <algorithm>
 #include <atomic>
+#include <cstddef>
 
 #include "dc_llm.h"
 #include "dc_numeric.cuh"
@@ -412,6 +413,44 @@ __device__ __forceinline__ Spot spot(uint32_t t, uint32_t fast, uint32_t slow, u
 }
 constexpr uint32_t kLogitBand = 16, kGradBand = 8;
 
+// What a CTA has to tell its pair before both may leave.
+struct Leave {
+  uint32_t told;            // the other has given up
+  uint32_t filled;          // stages that this CTA's loader filled
+  uint32_t used, runs;      // (even CTA) stages that products read, and sums of them
+};
+
+// A wait of the pair has run out.  Every thread of both CTAs has stopped; their copies
+// and products in flight are waited for, and the arrivals that those bring.  A stage's
+// barrier is told by both CTAs' copies: where one loader was ahead, what the other
+// would have copied or announced is made up for.
+__device__ __noinline__ void give_up(const Leave* leave, uint32_t rank, uint32_t full, uint32_t empty, uint32_t done, uint32_t over) {
+  const uint32_t at = smem_addr(leave);
+  bool ended = true;
+  auto drain = [&](uint32_t bar, uint32_t parity) { ended = tma::mbar_wait_bounded(bar, parity, kDrainNs) && ended; };
+  if (threadIdx.x == 32) {  // (the thread that issued the products)
+    if (rank == 0) commit_pair(over);
+    drain(over, 0);
+    const uint32_t even = cluster_addr(at, 0);
+    const uint32_t used = ld_cluster(even + offsetof(Leave, used)), runs = ld_cluster(even + offsetof(Leave, runs));
+    for (uint32_t k = used > kStages ? used - kStages : 0; k < used; ++k) drain(empty + 8 * (k % kStages), (k / kStages) & 1);
+    for (uint32_t k = runs > 2 ? runs - 2 : 0; k < runs; ++k) drain(done + 8 * (k & 1), (k / 2) & 1);
+  }
+  if (threadIdx.x == 0 && rank == 0) {
+    const uint32_t mine = leave->filled, other = ld_cluster(cluster_addr(at, 1) + offsetof(Leave, filled));
+    const uint32_t both = min(mine, other), end = max(mine, other);
+    for (uint32_t k = both; k < end; ++k) {
+      const uint32_t bar = full + 8 * (k % kStages);
+      if (k < mine) tma::mbar_complete_tx(bar, kStageBytes);
+      else tma::mbar_arrive_expect_tx(bar, kStageBytes);
+    }
+    for (uint32_t k = end > kStages ? end - kStages : 0; k < end; ++k) drain(full + 8 * (k % kStages), (k / kStages) & 1);
+  }
+  if (!ended) atomicOr(&g_linear_fault_bits, kFaultTensorDrain);
+  __syncwarp();
+  cluster_barrier();
+}
+
 template <int MODE, int DT, int NB>
 __global__ __launch_bounds__(kThreads, 1) void dc_linear_kernel(const __grid_constant__ LinearArgs<NB> args) {
   // whether B's rows run across the inner dimension (A's do for dW)
@@ -423,6 +462,7 @@ __global__ __launch_bounds__(kThreads, 1) void dc_linear_kernel(const __grid_con
   __shared__ __align__(8) uint64_t bars[2 * kStages + 5];
   __shared__ uint32_t tmem_at;
   __shared__ volatile uint32_t stop;
+  __shared__ Leave leave;
   __shared__ uint32_t hit_list[MODE == kLinearGrads ? kResultThreads / 32 : 1][kHits];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t ring = (smem_addr(smem) + 1023u) & ~1023u;
@@ -441,6 +481,7 @@ __global__ __launch_bounds__(kThreads, 1) void dc_linear_kernel(const __grid_con
     tma::mbar_init(over, 1);
     tma::mbar_init_fence();
     stop = 0;
+    leave = Leave{};
     prefetch_map(&args.a);
     prefetch_map(&args.b[0]);
   }
@@ -514,6 +555,10 @@ __global__ __launch_bounds__(kThreads, 1) void dc_linear_kernel(const __grid_con
         for (uint32_t kb = 0; kb < x.blocks; ++kb, ++i) {
           const uint32_t st = i % kStages, bar = full + 8 * st, to = ring + st * kStageBytes;
           if (i >= kStages && !wait(waits, empty + 8 * st, (i / kStages - 1) & 1)) break;
+          if (i == 2 && p.late == static_cast<int32_t>(3 + rank)) {
+            come_late(p.wait_ns);
+            if (stop) break;
+          }
           // (the products wait at the even CTA, for both CTAs' operands)
           if (rank == 0) tma::mbar_arrive_expect_tx(bar, 2 * kStageBytes);
           const uint32_t told = cluster_addr(bar, 0);
@@ -531,11 +576,9 @@ __global__ __launch_bounds__(kThreads, 1) void dc_linear_kernel(const __grid_con
           }
         }
       }
-      if (stop && rank == 0) {  // no copy may land after the CTAs' shared memory is gone
-        const uint32_t from = i > kStages ? i - kStages : 0;
-        for (uint32_t k = from; k < i; ++k)
-          tma::mbar_wait_bounded(full + 8 * (k % kStages), (k / kStages) & 1, p.wait_ns);
-      }
+      leave.filled = i;
+      // (the even CTA's products tell this barrier too: it may go when they have)
+      for (uint32_t k = i > kStages ? i - kStages : 0; k < i && !stop; ++k) wait(waits, empty + 8 * (k % kStages), (k / kStages) & 1);
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
@@ -565,10 +608,8 @@ __global__ __launch_bounds__(kThreads, 1) void dc_linear_kernel(const __grid_con
           ++runs;
         } while (kb < x.blocks && !stop);
       }
-      if (stop) {
-        commit_pair(over);
-        tma::mbar_wait_bounded(over, 0, p.wait_ns);
-      }
+      leave.used = i;
+      leave.runs = runs;
     }
   } else {
     // the lanes of tensor memory that this warp reads, and which half of the columns
@@ -592,6 +633,7 @@ __global__ __launch_bounds__(kThreads, 1) void dc_linear_kernel(const __grid_con
         there = __all_sync(~0u, wait(waits, done + 8 * buf, (runs / 2) & 1));
         if (!there) break;
         fence_after();
+        if (p.late == static_cast<int32_t>(1 + rank) && runs == 0) come_late(p.wait_ns);
         if (row0 < rows) {
           if constexpr (MODE == kLinearStats) gather_part(at, v);
           else if constexpr (MODE == kLinearDLogits) dlogits<DT>(p, at, row, own, n0);
@@ -613,9 +655,13 @@ __global__ __launch_bounds__(kThreads, 1) void dc_linear_kernel(const __grid_con
   }
   __syncwarp();
   __syncthreads();
-  if (threadIdx.x == 0 && stop) atomicOr(&g_linear_fault_bits, kFaultTensorWait);
+  if (threadIdx.x == 0 && stop) {
+    atomicOr(&g_linear_fault_bits, kFaultTensorWait);
+    st_cluster(cluster_addr(smem_addr(&leave.told), rank ^ 1), 1);
+  }
   fence_before();
   cluster_barrier();  // no CTA leaves while the other's products read its shared memory, or its barriers are told
+  if (stop || *const_cast<volatile uint32_t*>(&leave.told)) give_up(&leave, rank, full, empty, done, over);
   fence_after();
   if (warp == 1) tmem_free_pair(tmem, kColumns);
 }

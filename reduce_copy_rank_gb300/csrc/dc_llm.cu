@@ -550,6 +550,7 @@ dc_status_t dc_prefix_attention(const dc_prefix_attention_t* a, dc_stream_t stre
   x.slots = prefix_slots(p, own);
   x.scale = own.scale;
   x.wait_ns = wait_limit_option();
+  x.late = tensor_late_option();
   x.kc = p.kc;
   x.vc = p.vc;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);

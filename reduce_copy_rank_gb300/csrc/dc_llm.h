@@ -265,6 +265,7 @@ struct LinearParams {
   uint64_t lost;               // f32 [rows]: what d lost of each row's token
   uint64_t marks;              // [tiles of kLinearN columns][groups of 32 rows]: a bit a row whose token is there
   uint64_t wait_ns;
+  int32_t late;                // test: 1 or 2: the even or odd CTAs' first results are late, 3 or 4: their third copies
   LinearGrads g;               // kLinearGrads
 };
 
@@ -381,6 +382,7 @@ struct PrefixParams {
   int32_t chunks;                       // most of one prefix
   int32_t slots;                        // neighbouring tokens that one TMA copy moves; 0: keys and values by cp.async
   float scale;
+  int32_t late;                         // test: 1: the first weights are late, 2: the second tile's values
   uint64_t wait_ns;
   PagedView kc, vc;
 };

@@ -251,6 +251,7 @@ dc_status_t dc_linear_logprobs(const dc_linear_logprobs_t* a, dc_stream_t stream
   p.part = addr(a->workspace);
   p.target = p.part + tiles * (kLinearN / kLinearPart) * n * 16;
   p.wait_ns = wait_limit_option();
+  p.late = tensor_late_option();
   const LinearOperand x{h.hidden.base, n, size, h.hidden.stride};
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   int grid = 0;
@@ -357,6 +358,7 @@ dc_status_t dc_linear_logprobs_backward(const dc_linear_logprobs_backward_t* a, 
   p.d_stride = stride;
   const uint64_t acc = sum ? addr(a->workspace) + fixed_bytes(n, stride) : 0;
   p.wait_ns = wait_limit_option();
+  p.late = tensor_late_option();
   if (n && a->dtype == kF16) {
     p.scale = addr(a->workspace);
     const cudaError_t e = launch_linear_scale(p.grad_logprobs, p.grad_entropy, p.tokens, p.tokens64 != 0, n, p.inv_t, p.scale, pdl, s);

@@ -162,6 +162,7 @@ __global__ __launch_bounds__(kThreads, Shape<D>::kCtas) void dc_prefix_kernel(co
   __shared__ __align__(8) uint64_t bars[4 * S::kStages + 3 * S::kScores + 2];
   __shared__ uint32_t tmem_at;
   __shared__ volatile uint32_t stop, lost;
+  __shared__ uint32_t filled[2];  // (TMA) tiles whose copies were issued, of keys and of values
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // unit: (prefix, key head, chunk, rows)
   const int tile_rows = static_cast<int>(blockIdx.x % static_cast<uint32_t>(p.row_tiles)) * kPrefixRows;
@@ -209,6 +210,7 @@ __global__ __launch_bounds__(kThreads, Shape<D>::kCtas) void dc_prefix_kernel(co
     tma::mbar_init_fence();
     stop = 0;
     lost = bad ? 1u : 0u;
+    filled[0] = filled[1] = 0;
   }
   if (warp == 4) tmem_alloc(smem_addr(&tmem_at), S::kColumns);
   fence_before();
@@ -319,6 +321,7 @@ __global__ __launch_bounds__(kThreads, Shape<D>::kCtas) void dc_prefix_kernel(co
         tma::fence_proxy_async_smem();
       }
       fence_before();
+      if (i == 0 && p.late == 1) come_late(p.wait_ns);
       mbar_arrive(p_full + 8 * buf);
     }
     if (tiles > 1) wait_sum(tiles - 2);
@@ -378,10 +381,6 @@ __global__ __launch_bounds__(kThreads, Shape<D>::kCtas) void dc_prefix_kernel(co
         commit(v_empty + 8 * st);
         commit(summed + 8 * buf);
       }
-      if (stop) {
-        commit(over);
-        tma::mbar_wait_bounded(over, 0, p.wait_ns);
-      }
     }
     __syncwarp();
   } else {
@@ -414,6 +413,7 @@ __global__ __launch_bounds__(kThreads, Shape<D>::kCtas) void dc_prefix_kernel(co
       for (; i < tiles; ++i) {
         const uint32_t st = i % S::kStages, bar = full + 8 * st;
         if (i >= S::kStages && !__all_sync(~0u, wait(waits, empty + 8 * st, (i / S::kStages - 1) & 1))) break;
+        if (i == 1 && values && p.late == 2) come_late(p.wait_ns);
         const int32_t page = copier.page, slot = copier.slot;
         const uint32_t there = __popc(__ballot_sync(~0u, page >= 0));
         if (lane == 0) tma::mbar_arrive_expect_tx(bar, there * static_cast<uint32_t>(p.slots) * 128 * S::kBlocks);
@@ -430,10 +430,7 @@ __global__ __launch_bounds__(kThreads, Shape<D>::kCtas) void dc_prefix_kernel(co
           mbar_arrive(q_full);
         }
       }
-      if (stop) {  // no copy may land after this CTA's shared memory is gone
-        for (uint32_t k = i > S::kStages ? i - S::kStages : 0; k < i; ++k)
-          tma::mbar_wait_bounded(full + 8 * (k % S::kStages), (k / S::kStages) & 1, p.wait_ns);
-      }
+      if (lane == 0) filled[values] = i;
       go = false;
     }
     if (warp == 7) {
@@ -454,6 +451,7 @@ __global__ __launch_bounds__(kThreads, Shape<D>::kCtas) void dc_prefix_kernel(co
         else room = __all_sync(~0u, tma::mbar_try_wait(empty + 8 * st, parity));
       }
       if (room) {
+        if (issued == 1 && values && p.late == 2) come_late(p.wait_ns);
         copier.copy(to + st * S::kKV);
         cp_async_commit();
         ++issued;
@@ -481,7 +479,23 @@ __global__ __launch_bounds__(kThreads, Shape<D>::kCtas) void dc_prefix_kernel(co
   }
   __syncthreads();
   pdl_wait();
-  if (threadIdx.x == 0 && stop) atomicOr(&g_prefix_fault_bits, kFaultTensorWait);
+  if (stop) {
+    // Every thread has stopped: the copies and products in flight are waited for, which
+    // read and write this CTA's shared and tensor memory.
+    if (threadIdx.x == 0) atomicOr(&g_prefix_fault_bits, kFaultTensorWait);
+    bool ended = true;
+    if (threadIdx.x == 128) {  // (the thread that issued the products)
+      commit(over);
+      ended = tma::mbar_wait_bounded(over, 0, kDrainNs);
+    }
+    if (TMA && threadIdx.x < 2) {
+      const uint32_t full = threadIdx.x ? v_full : k_full, end = filled[threadIdx.x];
+      for (uint32_t k = end > S::kStages ? end - S::kStages : 0; k < end; ++k)
+        ended = tma::mbar_wait_bounded(full + 8 * (k % S::kStages), (k / S::kStages) & 1, kDrainNs) && ended;
+    }
+    if (!ended) atomicOr(&g_prefix_fault_bits, kFaultTensorDrain);
+    __syncthreads();
+  }
   if (warp == 4) {
     fence_after();
     tmem_free(tmem, S::kColumns);

@@ -94,6 +94,14 @@ __device__ __forceinline__ void cluster_barrier() {
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {  // (of cluster_addr)
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+__device__ __forceinline__ void st_cluster(uint32_t at, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t ld_cluster(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
 __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
@@ -270,6 +278,17 @@ __device__ __forceinline__ bool wait(const Waits& w, uint32_t bar, uint32_t pari
   }
   *w.stop = 1;
   return false;
+}
+
+// Once a CTA has given up, its copies and products in flight still read and write
+// shared and tensor memory: it leaves when they are done, however short the limit
+// was that ran out.
+constexpr uint64_t kDrainNs = 10000000000ull;
+
+// Test kernels' lateness: twice the limit (bounded also where the clock stands still).
+__device__ __forceinline__ void come_late(uint64_t limit_ns) {
+  const uint64_t t0 = tma::global_ns();
+  for (uint32_t i = 0; i < 1u << 22 && tma::global_ns() - t0 < 2 * limit_ns; ++i) __nanosleep(1000);
 }
 
 // ------------------------------------------------------------- tiled loads ---
