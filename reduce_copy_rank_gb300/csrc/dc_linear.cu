@@ -27,10 +27,9 @@
 // kept in 32 bits and put back into both products where they are stored: d e_y^T is
 // one row of the weights for dh, and one row of h for the token's row of dW.  The
 // gradients' errors are then those of their last rounding where single tokens make
-// them up (4096 rows, 127900 columns: 0.0017 of the gradients, 0.0025 without; the
-// time of that batch does not change, 509 rows of 50021 columns take 194 for 177 us).  For DC_F16 d is multiplied by one power of two for all rows, so
-// that the largest possible is between 2^14 and 2^15: what is 2^-29 of that is
-// still a normal number.
+// them up (4096 rows, 127900 columns: 0.0017 of the gradients, 0.0025 without).  For
+// DC_F16 d is multiplied by one power of two for all rows, so that the largest possible
+// is between 2^14 and 2^15: what is 2^-29 of that is still a normal number.
 //
 // Bound: the tensor cores for training batches, the weights' bytes for few rows.
 // Measured, BF16, 4096 rows of 4096 against 128000 columns: forward 2.66 ms, 1.61
@@ -197,7 +196,7 @@ __device__ __forceinline__ void dlogits(const LinearParams& p, uint32_t at, uint
   const uint32_t exist = !none && p.vocab > p.first + n0 ? p.vocab - p.first - n0 : 0;  // columns before the padding
   const uint64_t lo = p.d + row * p.d_stride;
   if (n0 % kLinearN == 0) {
-    const uint32_t marked = __ballot_sync(~0u, own && column >= 0 && column < kLinearN);
+    const uint32_t marked = __ballot_sync(~0u, own && !none && column >= 0 && column < min(kLinearN, static_cast<int>(p.n - n0)));
     uint32_t* a = reinterpret_cast<uint32_t*>(p.marks) + static_cast<uint64_t>(n0 / kLinearN) * linear_groups(p.rows) + row / 32;
     if ((threadIdx.x & 31) == 0 && in_bounds(a, 4, p.marks, p.marks + linear_marks(p.rows, p.d_stride), kSiteRow)) *a = marked;
   }
@@ -223,114 +222,121 @@ __device__ __forceinline__ void dlogits(const LinearParams& p, uint32_t at, uint
   }
 }
 
-// What the rounding of d took from a row of a gradient: `f` times a row of the other
-// operand for each token.  dh: the row's own token.  dW: the rows of the batch whose
-// token is this column, in order; `list` has (row, lane) pairs of the warp's 32
-// columns, kHits at a time.
-constexpr uint32_t kHits = 64;
+// What the rounding of d took from a row of a gradient.  dh: a factor times a row of
+// the weights, its own token's.  dW: the same of the rows of the batch whose token this
+// column is, in order, up to kLostAlone of them (or any of kLostFew rows in all), or one
+// row of binary32 sums where there are more (dc_linear_lost_kernel).
 struct Lost {
-  float f;         // the first
-  uint64_t row;
-  uint4 w[4];      // 32 elements of that row
-  uint64_t more;   // dW: the list's others for this lane, a bit each,
-  uint32_t next;   // and the group of 32 rows of the batch after the list's
+  float f[2];
+  uint64_t row[2];  // 0: none
+  uint4 w[8];       // 32 elements of each, or 32 sums
+  uint32_t hits;
+  bool sum;
+};
+// The rows' numbers for a warp's 32 columns: of kLostFew rows in all a byte each.
+union LostList {
+  uint32_t some[32][kLostAlone];
+  uint8_t few[32][kLostFew];
 };
 
-// Fills the list from groups of 32 rows, from `from` on.  Returns this lane's.
-__device__ __forceinline__ uint64_t find_hits(const LinearParams& p, uint32_t column0, uint32_t from, uint32_t* list, uint32_t* next) {
-  const uint32_t lane = threadIdx.x & 31, exist = p.g.columns - column0, groups = linear_groups(p.rows);
-  const int64_t first = static_cast<int64_t>(p.first) + column0;
-  const uint32_t* marks = reinterpret_cast<const uint32_t*>(p.marks) + static_cast<uint64_t>(column0 / kLinearN) * groups;
-  const uint64_t marks_hi = p.marks + linear_marks(p.rows, p.d_stride);
-  constexpr int kAtOnce = 4;
-  uint32_t n = 0;
-  bool room = true;
-  __syncwarp();
-  for (*next = groups; room && from < groups; from += 32) {
-    const uint32_t* a = marks + from + lane;
-    const uint32_t word = from + lane < groups && in_bounds(a, 4, p.marks, marks_hi, kSiteRow) ? *a : 0u;
-    uint32_t some = __ballot_sync(~0u, word != 0);
-    while (room && some) {
-      int64_t t[kAtOnce];
-      uint32_t at[kAtOnce];
+// 32 elements of a row of `size`, from `first` on, of 16 bits (4 vectors) or 32 (8).
+template <int BYTES>
+__device__ __forceinline__ void ld_row32(uint4* w, uint64_t row, uint32_t first, uint32_t size) {
+  constexpr uint32_t kPer = 16 / BYTES;
 #pragma unroll
-      for (int k = 0; k < kAtOnce; ++k) {
-        at[k] = some ? static_cast<uint32_t>(__ffs(static_cast<int>(some)) - 1) : 0u;
-        const uint32_t bits = __shfl_sync(~0u, word, static_cast<int>(at[k]));
-        const bool marked = some && (bits >> lane & 1);
-        some &= some - 1;
-        at[k] += from;
-        t[k] = marked ? token_of(p.tokens, p.tokens64, 32ull * at[k] + lane) - first : -1;
-      }
-#pragma unroll
-      for (int k = 0; k < kAtOnce; ++k) {
-        const bool hit = t[k] >= 0 && t[k] < 32 && t[k] < exist;
-        const uint32_t all = __ballot_sync(~0u, hit), count = static_cast<uint32_t>(__popc(all));
-        if (room && n + count > kHits) {
-          room = false;
-          *next = at[k];
-        }
-        if (!room) continue;
-        if (hit) list[n + static_cast<uint32_t>(__popc(all & ((1u << lane) - 1)))] = (32 * at[k] + lane) << 5 | static_cast<uint32_t>(t[k]);
-        n += count;
-      }
-    }
+  for (uint32_t j = 0; j < 2 * BYTES; ++j) {
+    const uint4* a = reinterpret_cast<const uint4*>(row + static_cast<uint64_t>(first) * BYTES) + j;
+    w[j] = row && first + kPer * j < size && in_bounds(a, 16, row, row + static_cast<uint64_t>(size) * BYTES, kSiteRow) ? *a : make_uint4(0, 0, 0, 0);
   }
-  __syncwarp();
-  uint64_t mine = 0;
-  for (uint32_t k = 0; k < n; ++k)
-    if ((list[k] & 31) == lane) mine |= 1ull << k;
-  return mine;
 }
-
-// 32 elements of a row of `size`, from `first` on.
-__device__ __forceinline__ void ld_row32(uint4 (&w)[4], uint64_t row, uint32_t first, uint32_t size) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint4* a = reinterpret_cast<const uint4*>(row + first * 2ull) + j;
-    w[j] = first + 8 * j < size && in_bounds(a, 16, row, row + size * 2ull, kSiteRow) ? *a : make_uint4(0, 0, 0, 0);
+__device__ __forceinline__ void ld_lost(Lost& x, uint32_t first, uint32_t size) {
+  if (x.sum) {
+    ld_row32<4>(x.w, x.row[0], first, size);
+  } else {
+    ld_row32<2>(x.w, x.row[0], first, size);
+    ld_row32<2>(x.w + 4, x.row[1], first, size);
   }
 }
 template <int DT>
-__device__ __forceinline__ void add_row32(float (&v)[32], float f, const uint4 (&w)[4]) {
-  if (f == 0.0f) return;  // (whatever the row holds)
+__device__ __forceinline__ void add_lost(float (&v)[32], const Lost& x) {
+  if (x.sum) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    float x[8];
-    unpack<DT>(w[j], x);
+    for (int j = 0; j < 8; ++j) {
+      v[4 * j] += __uint_as_float(x.w[j].x);
+      v[4 * j + 1] += __uint_as_float(x.w[j].y);
+      v[4 * j + 2] += __uint_as_float(x.w[j].z);
+      v[4 * j + 3] += __uint_as_float(x.w[j].w);
+    }
+    return;
+  }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[8 * j + k] = __fmaf_rn(f, x[k], v[8 * j + k]);
+  for (int i = 0; i < 2; ++i) {
+    if (x.f[i] == 0.0f) continue;  // (whatever the row holds)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float y[8];
+      unpack<DT>(x.w[4 * i + j], y);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[8 * j + k] = __fmaf_rn(x.f[i], y[k], v[8 * j + k]);
+    }
+  }
+}
+// The lane's rows k and k + 1 of the list.
+__device__ __forceinline__ void lost_pair(const LinearParams& p, Lost& x, uint32_t k, const LostList& list) {
+  const uint32_t lane = threadIdx.x & 31;
+#pragma unroll
+  for (uint32_t i = 0; i < 2; ++i) {
+    const bool there = k + i < x.hits;
+    const uint64_t row = !there ? 0 : p.rows <= kLostFew ? list.few[lane][k + i] : list.some[lane][k + i];
+    x.f[i] = there ? ld_row(p.lost, row, p.rows) : 0.0f;
+    x.row[i] = there ? p.g.x + row * p.g.x_stride : 0;
   }
 }
 
 // Looked up before the products are there: `row` of C, k0 and blocks of dh's inner dimension.
 __device__ __forceinline__ void look_up(const LinearParams& p, uint64_t row, bool own, uint32_t n0, bool weights, uint32_t k0,
-                                        uint32_t blocks, uint32_t* list, Lost* x) {
+                                        uint32_t blocks, LostList& list, Lost* x) {
   const LinearGrads& g = p.g;
-  *x = Lost{0.0f, 0, {}, 0, ~0u};
-  if (weights) {
-    x->more = find_hits(p, static_cast<uint32_t>(row) & ~31u, 0, list, &x->next);
-    if (x->more) {
-      const uint64_t i = list[__ffsll(static_cast<long long>(x->more)) - 1] >> 5;
-      x->more &= x->more - 1;
-      x->f = ld_row(p.lost, i, p.rows);
-      x->row = g.x + i * g.x_stride;
+  const uint32_t lane = threadIdx.x & 31;
+  *x = Lost{};
+  if (!weights) {
+    if (own) {
+      const int64_t column = token_of(p.tokens, p.tokens64, row) - static_cast<int64_t>(p.first);
+      if (column >= k0 && column < min(g.columns, k0 + blocks * kLinearK)) {
+        x->f[0] = ld_row(p.lost, row, p.rows);
+        x->row[0] = x->f[0] != 0.0f ? g.w + static_cast<uint64_t>(column) * g.w_stride : 0;
+      }
+    }
+    x->hits = x->row[0] != 0;
+  } else if (p.rows <= kLostFew) {
+    for (uint32_t r0 = 0; r0 < p.rows; r0 += 32) {
+      const int64_t t = r0 + lane < p.rows ? token_of(p.tokens, p.tokens64, r0 + lane) - static_cast<int64_t>(p.first) : -1;
+      for (uint32_t k = 0; k < min(32u, static_cast<uint32_t>(p.rows) - r0); ++k)
+        if (__shfl_sync(~0u, t, k) == static_cast<int64_t>(row) && own) list.few[lane][x->hits++] = static_cast<uint8_t>(r0 + k);
     }
   } else if (own) {
-    const int64_t column = token_of(p.tokens, p.tokens64, row) - static_cast<int64_t>(p.first);
-    if (column >= k0 && column < min(g.columns, k0 + blocks * kLinearK)) {
-      x->f = ld_row(p.lost, row, p.rows);
-      x->row = g.w + static_cast<uint64_t>(column) * g.w_stride;
+    const int32_t* a = reinterpret_cast<const int32_t*>(g.table) + row;
+    int32_t at = in_bounds(a, 4, g.table, g.table + g.columns * 4ull, kSiteRow) ? *a : -1;
+    if (at < -1) {
+      x->sum = true;
+      x->row[0] = g.sums + static_cast<uint64_t>(-2 - at) * p.n * 4;
+      x->hits = 1;
+    }
+    while (at >= 0 && x->hits < kLostAlone) {
+      list.some[lane][x->hits++] = static_cast<uint32_t>(at);
+      a = reinterpret_cast<const int32_t*>(g.next) + at;
+      at = in_bounds(a, 4, g.next, g.next + p.rows * 4, kSiteRow) ? *a : -1;
     }
   }
-  if (x->f != 0.0f) ld_row32(x->w, x->row, n0, p.n);
+  if (weights && !x->sum) lost_pair(p, *x, 0, list);
+  if (x->hits) ld_lost(*x, n0, p.n);
 }
 
 // A row of a gradient.  Plus what `acc` (dh: of chunks and slices, dW: of this
 // tile's runs) holds of it, to `acc` or (complete) to the output.
 template <int DT>
 __device__ __forceinline__ void result(const LinearParams& p, uint32_t at, uint64_t row, bool own, uint32_t n0, bool weights,
-                                       uint32_t slice, bool empty, bool again, bool whole, Lost& lost, uint32_t* list) {
+                                       uint32_t slice, bool empty, bool again, bool whole, Lost& lost, const LostList& list) {
   const LinearGrads& g = p.g;
   const float unit = p.scale ? reinterpret_cast<const float*>(p.scale)[1] : 1.0f;
   const uint64_t out = weights ? g.out_w + row * g.out_w_stride : g.out_h + row * g.out_h_stride;
@@ -349,27 +355,15 @@ __device__ __forceinline__ void result(const LinearParams& p, uint32_t at, uint6
 #pragma unroll
       for (int j = 0; j < 32; ++j) v[j] = 0.0f;
     }
-    const float f = last || !weights ? lost.f : 0.0f;  // (dW: with the last run)
-    add_row32<DT>(v, f, lost.w);
-    if (f != 0.0f && j0 + 32 < kLinearPart) ld_row32(lost.w, lost.row, n0 + j0 + 32, p.n);  // (for the next columns)
-    if (weights && last) {
-      const uint32_t groups = linear_groups(p.rows);
-      uint64_t more = lost.more;
-      uint32_t next = lost.next;
-      while (true) {
-        for (; more; more &= more - 1) {
-          const uint64_t i = list[__ffsll(static_cast<long long>(more)) - 1] >> 5;
-          uint4 w[4];
-          ld_row32(w, g.x + i * g.x_stride, n0 + j0, p.n);
-          add_row32<DT>(v, ld_row(p.lost, i, p.rows), w);
-        }
-        if (next >= groups) break;
-        more = find_hits(p, static_cast<uint32_t>(row) & ~31u, next, list, &next);
+    if (lost.hits && (last || !weights)) {  // (dW: with the last run)
+      add_lost<DT>(v, lost);
+      for (uint32_t k = 2; k < lost.hits; k += 2) {
+        lost_pair(p, lost, k, list);
+        ld_lost(lost, n0 + j0, p.n);
+        add_lost<DT>(v, lost);
       }
-      if (lost.next < groups) {  // the list again
-        const uint64_t all = find_hits(p, static_cast<uint32_t>(row) & ~31u, 0, list, &next);
-        lost.more = all & (all - 1);
-      }
+      if (lost.hits > 2) lost_pair(p, lost, 0, list);
+      if (j0 + 32 < kLinearPart) ld_lost(lost, n0 + j0 + 32, p.n);  // (for the next columns)
     }
     if (!own) continue;
     float4* a = reinterpret_cast<float4*>(acc_lo) + (acc_row + j0) / 4;
@@ -463,7 +457,7 @@ __global__ __launch_bounds__(kThreads, 1) void dc_linear_kernel(const __grid_con
   __shared__ uint32_t tmem_at;
   __shared__ volatile uint32_t stop;
   __shared__ Leave leave;
-  __shared__ uint32_t hit_list[MODE == kLinearGrads ? kResultThreads / 32 : 1][kHits];
+  __shared__ LostList lists[MODE == kLinearGrads ? kResultThreads / 32 : 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t ring = (smem_addr(smem) + 1023u) & ~1023u;
   const uint32_t full = smem_addr(bars), empty = full + 8 * kStages;
@@ -626,7 +620,7 @@ __global__ __launch_bounds__(kThreads, 1) void dc_linear_kernel(const __grid_con
       [[maybe_unused]] float v[MODE == kLinearStats ? kLinearPart : 1] = {};
       [[maybe_unused]] Lost lost;
       if constexpr (MODE == kLinearGrads)
-        if (row0 < rows) look_up(p, row, own, n0, x.r == 1, x.k0 * kLinearK, x.blocks, hit_list[warp - 2], &lost);
+        if (row0 < rows) look_up(p, row, own, n0, x.r == 1, x.k0 * kLinearK, x.blocks, lists[warp - 2], &lost);
       uint32_t kb = 0;
       do {
         const uint32_t buf = runs & 1, at = tmem + buf * kLinearN + half * kLinearPart + (quarter << 16);
@@ -637,7 +631,7 @@ __global__ __launch_bounds__(kThreads, 1) void dc_linear_kernel(const __grid_con
         if (row0 < rows) {
           if constexpr (MODE == kLinearStats) gather_part(at, v);
           else if constexpr (MODE == kLinearDLogits) dlogits<DT>(p, at, row, own, n0);
-          else result<DT>(p, at, row, own, n0, x.r == 1, x.tile, x.blocks == 0, kb > 0, kb + run >= x.blocks, lost, hit_list[warp - 2]);
+          else result<DT>(p, at, row, own, n0, x.r == 1, x.tile, x.blocks == 0, kb > 0, kb + run >= x.blocks, lost, lists[warp - 2]);
         }
         fence_before();
         __syncwarp();
@@ -719,6 +713,181 @@ __global__ __launch_bounds__(kFinishThreads) void dc_linear_finish_kernel(const 
   put(p.logprobs, lp);
   if (p.entropy) put(p.entropy, (log_s - t / s) * kLn2);
   if (p.lse) put(p.lse, (ref + log_s) * kLn2);
+}
+
+// Where dW's columns find what d lost of the rows whose token they are, for calls of
+// more than kLostFew rows: a column of up to kLostAlone such rows the first of them, each
+// row the next (in order), and a column of more the sum, in binary32, of what d lost times
+// the hidden rows.  So no tile's results take longer the more rows share a token.
+// A CTA has 256 columns (the marks say which rows have their token there) and every
+// gridDim.y-th 256 elements of the hidden rows.  kLostRows rows at a time are put in order
+// by column and, in one, the rows' order; the CTA's warps sum a column's rows and join in
+// order.
+// Measured, BF16, 16384 rows of 4096 against 64000 columns, tokens spread evenly / half of
+// the rows one token's / as often as the n-th word of a text: 16.3 / 16.5 / 16.9 ms (all of
+// it by the tile's own warps: 15.5 / 30.9 / 18.0 to 21.5); 509 rows of 1000 against 50021:
+// 210 / 237 / 245 us (200 / 534 / 284).  13 and 5 us a chunk of columns.
+constexpr int kLostThreads = 256, kLostWarps = kLostThreads / 32;
+constexpr uint32_t kLostRows = 4096, kLostWords = kLostRows / 32;
+constexpr uint32_t kLostAtOnce = 8;  // rows whose loads a warp has in flight
+
+// Exclusive sums over the CTA; every thread gets the total.
+__device__ __forceinline__ uint32_t scan_cta(uint32_t n, uint32_t* warps, uint32_t* total) {
+  const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t s = n;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const uint32_t t = __shfl_up_sync(~0u, s, d);
+    if (lane >= static_cast<uint32_t>(d)) s += t;
+  }
+  __syncthreads();  // (warps: of the call before)
+  if (lane == 31) warps[warp] = s;
+  __syncthreads();
+  uint32_t before = 0, all = 0;
+#pragma unroll
+  for (uint32_t w = 0; w < kLostWarps; ++w) {
+    before += w < warp ? warps[w] : 0u;
+    all += warps[w];
+  }
+  *total = all;
+  return before + s - n;
+}
+
+template <int DT>
+__global__ __launch_bounds__(kLostThreads) void dc_linear_lost_kernel(const __grid_constant__ LinearLostParams p) {
+  static_assert(kLostThreads == kLinearN, "a thread a column");
+  pdl_enter();
+  __shared__ uint32_t hits[kLostRows];    // the marked rows: row of these kLostRows, column (8 bits)
+  __shared__ uint16_t order[kLostRows];   // their rows, by column
+  __shared__ float joined[kLostWarps][kLinearN];
+  __shared__ uint32_t total[kLinearN], count[kLinearN], start[kLinearN], warps[kLostWarps];
+  __shared__ int32_t place[kLinearN];     // of a column's sum, -1: it has none yet
+  __shared__ uint16_t many[kLinearN];     // the columns that have sums
+  const uint32_t t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const uint32_t column0 = blockIdx.x * kLinearN, groups = linear_groups(p.rows);
+  const uint64_t marks = p.marks + static_cast<uint64_t>(blockIdx.x) * groups * 4, marks_hi = marks + groups * 4ull;
+  const int64_t first = static_cast<int64_t>(p.first) + column0;
+  auto mark = [&](uint32_t g) {
+    const uint32_t* a = reinterpret_cast<const uint32_t*>(marks) + g;
+    return g < groups && in_bounds(a, 4, marks, marks_hi, kSiteRow) ? *a : 0u;
+  };
+  // (a mark says that the row's token is one of these)
+  auto column_of = [&](uint64_t row) { return static_cast<uint32_t>(token_of(p.tokens, p.tokens64, row) - first) & (kLinearN - 1); };
+
+  // how many rows each column has
+  total[t] = 0;
+  place[t] = -1;
+  __syncthreads();
+  for (uint32_t g0 = warp * 32; g0 < groups; g0 += kLostThreads) {
+    const uint32_t word = mark(g0 + lane);
+    uint32_t some = __ballot_sync(~0u, word != 0);
+    while (some) {
+      constexpr int kWords = 4;
+      uint32_t column[kWords];
+#pragma unroll
+      for (int k = 0; k < kWords; ++k) {
+        const uint32_t at = some ? static_cast<uint32_t>(__ffs(static_cast<int>(some)) - 1) : 0u;
+        const uint32_t bits = __shfl_sync(~0u, word, static_cast<int>(at));
+        column[k] = some && (bits >> lane & 1) ? column_of(32ull * (g0 + at) + lane) : static_cast<uint32_t>(kLinearN);
+        some &= some - 1;
+      }
+#pragma unroll
+      for (int k = 0; k < kWords; ++k)
+        if (column[k] < kLinearN) atomicAdd(&total[column[k]], 1u);
+    }
+  }
+  __syncthreads();
+  const bool shared = total[t] > kLostAlone;
+  uint32_t n_many;
+  const uint32_t i_many = scan_cta(shared, warps, &n_many);
+  if (shared) many[i_many] = static_cast<uint16_t>(t);
+  const bool links = blockIdx.y == 0;
+  if (!links && n_many == 0) return;
+
+  int32_t head = -1, last = -1;  // this thread's column's first row, and the last so far
+  for (uint32_t g0 = 0; g0 < groups; g0 += kLostWords) {
+    const uint32_t row0 = 32 * g0;
+    uint32_t word = t < kLostWords ? mark(g0 + t) : 0u, n, all;
+    uint32_t at = scan_cta(static_cast<uint32_t>(__popc(word)), warps, &n);
+    if (n == 0) continue;
+    count[t] = 0;
+    for (; word; word &= word - 1) hits[at++] = 32 * t + static_cast<uint32_t>(__ffs(static_cast<int>(word)) - 1);
+    __syncthreads();
+    for (uint32_t k = t; k < n; k += kLostThreads) {
+      const uint32_t column = column_of(row0 + hits[k]);
+      hits[k] = hits[k] << 8 | column;
+      atomicAdd(&count[column], 1u);
+    }
+    __syncthreads();
+    const uint32_t mine = count[t];
+    at = scan_cta(mine, warps, &all);
+    start[t] = at;
+    for (uint32_t k = 0, left = mine; left && k < n; ++k) {  // (all threads read the same one)
+      if ((hits[k] & 255) != t) continue;
+      const uint32_t r = hits[k] >> 8;
+      order[at++] = static_cast<uint16_t>(r);
+      --left;
+      const int32_t row = static_cast<int32_t>(row0 + r);
+      if (head < 0) head = row;
+      else if (links && !shared) {
+        int32_t* a = reinterpret_cast<int32_t*>(p.next) + last;
+        if (in_bounds(a, 4, p.next, p.next + p.rows * 4, kSitePart)) *a = row;
+      }
+      last = row;
+    }
+    __syncthreads();
+    // (the next scan waits for all threads before anything of this is written again)
+    for (uint32_t s = blockIdx.y; n_many && s * kLinearN < p.size; s += gridDim.y) {
+      const uint32_t e0 = s * kLinearN + lane * 8;
+      for (uint32_t i = 0; i < n_many; ++i) {
+        const uint32_t column = many[i], rows = count[column];
+        if (rows == 0) continue;
+        float acc[8] = {};
+        for (uint32_t k0 = warp * kLostAtOnce; k0 < rows; k0 += kLostWarps * kLostAtOnce) {
+          float f[kLostAtOnce];
+          uint4 x[kLostAtOnce];
+#pragma unroll
+          for (uint32_t j = 0; j < kLostAtOnce; ++j) {
+            const bool there = k0 + j < rows;
+            const uint64_t row = row0 + order[start[column] + (there ? k0 + j : k0)], from = p.x + row * p.x_stride;
+            const uint4* a = reinterpret_cast<const uint4*>(from + e0 * 2ull);
+            f[j] = there ? ld_row(p.lost, row, p.rows) : 0.0f;
+            x[j] = there && e0 < p.size && in_bounds(a, 16, from, from + p.size * 2ull, kSiteRow) ? *a : make_uint4(0, 0, 0, 0);
+          }
+#pragma unroll
+          for (uint32_t j = 0; j < kLostAtOnce; ++j) {
+            float y[8];
+            unpack<DT>(x[j], y);
+#pragma unroll
+            for (int v = 0; v < 8; ++v) acc[v] = __fmaf_rn(f[j], y[v], acc[v]);
+          }
+        }
+        float4* to = reinterpret_cast<float4*>(&joined[warp][lane * 8]);
+        to[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        to[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+        __syncthreads();
+        const uint32_t e = s * kLinearN + t;
+        // one place for each column, whatever the order: its first row's, or its own, of which there are fewer
+        const int32_t old = place[column], now = old >= 0 ? old : static_cast<int32_t>(p.by_row ? row0 + order[start[column]] : column0 + column);
+        float* a = reinterpret_cast<float*>(p.sums) + static_cast<uint64_t>(now) * p.size + e;
+        if (e < p.size && in_bounds(a, 4, p.sums, p.sums + p.places * p.size * 4, kSiteAcc)) {
+          float sum = joined[0][t];
+          for (int w = 1; w < kLostWarps; ++w) sum += joined[w][t];
+          *a = old >= 0 ? *a + sum : sum;
+        }
+        __syncthreads();
+      }
+    }
+    __syncthreads();
+    if (shared && mine && place[t] < 0) place[t] = p.by_row ? head : static_cast<int32_t>(column0 + t);
+  }
+  if (!links) return;
+  if (head >= 0 && !shared) {
+    int32_t* a = reinterpret_cast<int32_t*>(p.next) + last;
+    if (in_bounds(a, 4, p.next, p.next + p.rows * 4, kSitePart)) *a = -1;
+  }
+  int32_t* a = reinterpret_cast<int32_t*>(p.table) + column0 + t;
+  if (in_bounds(a, 4, p.table, p.table + p.d_stride * 2, kSitePart)) *a = shared ? -2 - place[t] : head;
 }
 
 template <int DT>
@@ -904,6 +1073,21 @@ cudaError_t launch_linear_sum(const LinearSumParams& p, int dtype, bool pdl, cud
   *grid = static_cast<int>((p.rows * (p.size / 8) + 255) / 256);
   return dtype == kF16 ? launch_ex(dc_linear_sum_kernel<kF16>, *grid, 256, pdl, s, p)
                        : launch_ex(dc_linear_sum_kernel<kBF16>, *grid, 256, pdl, s, p);
+}
+
+cudaError_t launch_linear_lost(const LinearLostParams& p, int dtype, bool pdl, cudaStream_t s, int* grid) {
+  const dim3 g((p.columns + kLinearN - 1) / kLinearN, (p.size + kLinearN - 1) / kLinearN);
+  *grid = static_cast<int>(g.x * g.y);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = g;
+  cfg.blockDim = dim3(kLostThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = pdl ? attr : nullptr;
+  cfg.numAttrs = pdl ? 1 : 0;
+  return dtype == kF16 ? cudaLaunchKernelEx(&cfg, dc_linear_lost_kernel<kF16>, p) : cudaLaunchKernelEx(&cfg, dc_linear_lost_kernel<kBF16>, p);
 }
 
 cudaError_t launch_linear_finish(const LinearFinishParams& p, bool pdl, cudaStream_t s, int* grid) {

@@ -244,6 +244,7 @@ struct LinearGrads {
   uint64_t tile;               // f32 [kLinearPairs][kLinearM][kLinearN] or 0: sums of dW's runs
   uint64_t out_h, out_h_stride, out_w, out_w_stride;  // bytes
   uint64_t x, x_stride, w, w_stride;                  // the hidden rows, the chunk's rows of the weights
+  uint64_t table, next, sums;  // what dW's rows get back: as LinearLostParams has them (not of kLostFew rows)
 };
 
 // One product C [m, n] = A B^T over k, and what becomes of it.
@@ -263,11 +264,31 @@ struct LinearParams {
   uint64_t scale;              // f32 [2] or 0: the gradient's power of two and its inverse
   uint64_t d, d_stride;        // kLinearDLogits: [rows] of d_stride bytes
   uint64_t lost;               // f32 [rows]: what d lost of each row's token
-  uint64_t marks;              // [tiles of kLinearN columns][groups of 32 rows]: a bit a row whose token is there
+  uint64_t marks;              // [tiles of kLinearN columns][groups of 32 rows]: a bit a row that has a gradient and its token there
   uint64_t wait_ns;
   int32_t late;                // test: 1 or 2: the even or odd CTAs' first results are late, 3 or 4: their third copies
   LinearGrads g;               // kLinearGrads
 };
+
+// What dW's rows get back of what d lost, for calls of more than kLostFew rows.  A
+// column that up to kLostAlone rows have as their token: its first row's number, and
+// each row's next one (-1: none).  A column of more: -2 - its place in the sums.
+constexpr uint32_t kLostFew = 64, kLostAlone = 16;
+struct LinearLostParams {
+  uint64_t tokens, lost, marks;
+  uint64_t table, next;        // int32 [d_stride / 2], [rows]
+  uint64_t sums, places;       // f32 [places][size]
+  uint64_t x, x_stride;        // the hidden rows
+  uint64_t rows, d_stride;
+  uint32_t first, columns, size;
+  int32_t tokens64, by_row;    // by_row: a column's place is its first row's, else its own
+};
+// Places for sums: a chunk's columns, or the rows that can be the first of a column's
+// more than kLostAlone.
+__host__ __device__ inline uint64_t linear_lost_places(uint64_t rows, uint64_t d_stride) {
+  if (rows <= kLostFew) return 0;
+  return rows - kLostAlone < d_stride / 2 ? rows - kLostAlone : d_stride / 2;
+}
 
 struct LinearFinishParams {
   uint64_t part, target, tokens, logprobs, entropy, lse;  // the last three f32 [rows], two of them or 0
@@ -291,6 +312,7 @@ struct LinearOperand {
 cudaError_t launch_linear(int mode, int dtype, const LinearParams& p, const LinearOperand& a, const LinearOperand* b,
                           const LinearShard* shards, int sms, bool pdl, cudaStream_t s, int* grid);
 cudaError_t launch_linear_finish(const LinearFinishParams& p, bool pdl, cudaStream_t s, int* grid);
+cudaError_t launch_linear_lost(const LinearLostParams& p, int dtype, bool pdl, cudaStream_t s, int* grid);
 cudaError_t launch_linear_sum(const LinearSumParams& p, int dtype, bool pdl, cudaStream_t s, int* grid);
 // Fills the schedule of p.g for `pairs` CTA pairs.
 void plan_linear_grads(LinearGrads* g, uint32_t pairs);

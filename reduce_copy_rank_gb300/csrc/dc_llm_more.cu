@@ -73,8 +73,9 @@ dc_status_t check_head(const void* hidden, uint64_t hidden_stride, const void* c
 
 // The forward's workspace: every tile's parts, then the tokens' logits.
 uint64_t stats_bytes(uint64_t rows, uint64_t tiles) { return rows * (tiles * (kLinearN / kLinearPart) * 16 + 4); }
-// The gradient's: its power of two, then what d loses at the rows' tokens and where
-// those are, d of one chunk of the vocabulary, and the sums of d W, a slice each.
+// The gradient's: its power of two, then what d loses at the rows' tokens, where those
+// are, and how dW's rows find it; d of one chunk of the vocabulary, and the sums of d W,
+// a slice each.
 uint64_t lost_bytes(uint64_t rows) { return round_up(rows * 4, 256); }
 uint64_t marks_bytes(uint64_t rows, uint64_t stride) { return round_up(linear_marks(rows, stride), 256); }
 uint64_t chunk_stride(uint64_t columns) { return round_up(std::min<uint64_t>(columns, kLinearChunk), kLinearN) * 2; }
@@ -82,9 +83,13 @@ uint64_t d_bytes(uint64_t rows, uint64_t stride) { return round_up(rows * stride
 
 // dW's sums of one tile a pair of CTAs, where a sum takes more than one run.
 uint64_t tile_bytes(uint64_t rows) { return rows > kLinearChunk ? kLinearPairs * static_cast<uint64_t>(kLinearM) * kLinearN * 4 : 0; }
+uint64_t table_bytes(uint64_t rows, uint64_t stride) { return rows > kLostFew ? round_up(stride * 2, 256) : 0; }
+uint64_t next_bytes(uint64_t rows) { return rows > kLostFew ? round_up(rows * 4, 256) : 0; }
+uint64_t sums_bytes(uint64_t rows, uint64_t stride, uint64_t size) { return round_up(linear_lost_places(rows, stride) * size * 4, 256); }
 // All of it but the sums of d W.
-uint64_t fixed_bytes(uint64_t rows, uint64_t stride) {
-  return 256 + lost_bytes(rows) + marks_bytes(rows, stride) + d_bytes(rows, stride) + tile_bytes(rows);
+uint64_t fixed_bytes(uint64_t rows, uint64_t stride, uint64_t size) {
+  return 256 + lost_bytes(rows) + marks_bytes(rows, stride) + table_bytes(rows, stride) + next_bytes(rows) + sums_bytes(rows, stride, size) +
+         d_bytes(rows, stride) + tile_bytes(rows);
 }
 
 dc_status_t check_workspace(void* p, uint64_t have, uint64_t need, Spans& out) {
@@ -205,7 +210,7 @@ size_t dc_linear_logprobs_workspace_bytes(int64_t rows, int64_t hidden_size, int
   const uint64_t n = static_cast<uint64_t>(std::max<int64_t>(rows, 1)), v = static_cast<uint64_t>(columns);
   // (a shard's last tile may be narrower: at most one more tile a rank)
   if (!backward) return round_up(stats_bytes(n, (v + kLinearN - 1) / kLinearN + kMaxRanks), 256);
-  return fixed_bytes(n, chunk_stride(v)) +
+  return fixed_bytes(n, chunk_stride(v), static_cast<uint64_t>(hidden_size)) +
          round_up(n * static_cast<uint64_t>(hidden_size) * 4 * linear_slices(static_cast<uint32_t>(hidden_size)), 256);
 }
 
@@ -325,7 +330,7 @@ dc_status_t dc_linear_logprobs_backward(const dc_linear_logprobs_backward_t* a, 
       DC_TRY(take(a->grad_entropy, "grad_entropy", n * 4, 4, h.in));
       DC_TRY(take(a->entropy, "entropy", n * 4, 4, h.in));
     }
-    DC_TRY(check_workspace(a->workspace, a->workspace_bytes, fixed_bytes(n, stride) + (sum ? n * size * 4 * slices : 0), out));
+    DC_TRY(check_workspace(a->workspace, a->workspace_bytes, fixed_bytes(n, stride, size) + (sum ? n * size * 4 * slices : 0), out));
     DC_TRY(check_head_outputs(out, h));
     Shards written = gw;
     DC_TRY(outside_shards(out, written, "a shard of grad_weights"));
@@ -353,10 +358,11 @@ dc_status_t dc_linear_logprobs_backward(const dc_linear_logprobs_backward_t* a, 
   p.grad_entropy = addr(a->grad_entropy);
   p.lost = addr(a->workspace) + 256;
   p.marks = p.lost + lost_bytes(n);
-  p.d = p.marks + marks_bytes(n, stride);
+  const uint64_t table = p.marks + marks_bytes(n, stride), next = table + table_bytes(n, stride), lost_sums = next + next_bytes(n);
+  p.d = lost_sums + sums_bytes(n, stride, size);
   const uint64_t tile = tile_bytes(n) ? p.d + d_bytes(n, stride) : 0;
   p.d_stride = stride;
-  const uint64_t acc = sum ? addr(a->workspace) + fixed_bytes(n, stride) : 0;
+  const uint64_t acc = sum ? addr(a->workspace) + fixed_bytes(n, stride, size) : 0;
   p.wait_ns = wait_limit_option();
   p.late = tensor_late_option();
   if (n && a->dtype == kF16) {
@@ -393,6 +399,27 @@ dc_status_t dc_linear_logprobs_backward(const dc_linear_logprobs_backward_t* a, 
       l.first = static_cast<uint32_t>(at + c);
       cudaError_t e = launch_linear(kLinearDLogits, a->dtype, l, x, &w, nullptr, sms, pdl, s, &grid);
       DC_TRY(check_launch(e, "a linear head's gradient", grid));
+      if (want_w && n > kLostFew) {
+        LinearLostParams t{};
+        t.tokens = p.tokens;
+        t.lost = p.lost;
+        t.marks = p.marks;
+        t.table = table;
+        t.next = next;
+        t.sums = lost_sums;
+        t.places = linear_lost_places(n, stride);
+        t.x = x.base;
+        t.x_stride = x.stride;
+        t.rows = n;
+        t.d_stride = stride;
+        t.first = l.first;
+        t.columns = columns;
+        t.size = static_cast<uint32_t>(size);
+        t.tokens64 = p.tokens64;
+        t.by_row = n - kLostAlone < stride / 2;
+        e = launch_linear_lost(t, a->dtype, pdl, s, &grid);
+        DC_TRY(check_launch(e, "a linear head's gradient", grid));
+      }
       LinearParams q = p;
       q.m = static_cast<uint32_t>(n);
       q.n = static_cast<uint32_t>(size);
@@ -401,6 +428,9 @@ dc_status_t dc_linear_logprobs_backward(const dc_linear_logprobs_backward_t* a, 
       LinearGrads& g = q.g;
       g.x = x.base;
       g.x_stride = x.stride;
+      g.table = table;
+      g.next = next;
+      g.sums = lost_sums;
       g.w = w.base + c * w.stride;
       g.w_stride = w.stride;
       g.columns = columns;

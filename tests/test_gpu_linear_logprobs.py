@@ -437,3 +437,71 @@ def test_autograd_in_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def shared_tokens(kind, rows, vocab, g):
+    if kind == "one":
+        return torch.full((rows,), vocab // 3, device="cuda")
+    if kind == "half":
+        return torch.where(torch.rand(rows, generator=g, device="cuda") < 0.5, vocab // 3,
+                           torch.randint(0, vocab, (rows,), generator=g, device="cuda"))
+    if kind == "counts":  # token k belongs to k rows: 1, 2, ..., as long as there are rows
+        return torch.repeat_interleave(torch.arange(200, device="cuda"), torch.arange(200, device="cuda"))[:rows][torch.randperm(rows, generator=g, device="cuda")]
+    p = 1 / torch.arange(1, vocab + 1, device="cuda").double()  # as text has them
+    return torch.multinomial(p, rows, replacement=True, generator=g)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("rows,size,widths,kind", [
+    (63, 264, [300], "one"), (64, 520, [300, 40], "half"), (65, 520, [300, 40], "half"), (80, 72, [300], "one"), (16, 64, [50], "one"),
+    (4095, 264, [513, 700], "half"), (4500, 264, [600], "counts"), (9000, 72, [700], "one"), (9000, 520, [400, 400], "zipf"),
+    (30000, 72, [26000], "zipf"), (2500, 8, [1000], "zipf")])
+def test_tokens_that_any_number_of_rows_share(rows, size, widths, kind, dtype):
+    """Some of the rows (half of those that share) without a gradient."""
+    vocab = sum(widths)
+    hidden, weights, tokens = build(rows, size, widths, vocab, dtype, seed=7)
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    tokens = shared_tokens(kind, rows, vocab, g)
+    gl, ge = upstream(rows)
+    none = torch.rand(rows, generator=g, device="cuda") < 0.4
+    gl[none], ge[none] = 0, 0
+    a = hidden, weights, tokens
+    ws = dc.linear_logprobs_workspace(rows, size, vocab, backward=True).fill_(255)
+    saved = forward(*a)
+    want = backward(*a, vocab, gl, ge, saved=saved, workspace=ws)
+    check_backward(want, *a, vocab, gl, ge, dtype=dtype)
+    again = backward(*a, vocab, gl, ge, saved=saved, workspace=ws)
+    assert torch.equal(want[0], again[0]) and all(torch.equal(x, y) for x, y in zip(want[1], again[1]))
+
+
+def test_the_sum_of_shared_tokens_is_rounded_once():
+    """As test_the_tokens_gradient_is_rounded_once, for tokens that 9 and 900 rows share: rows that point the same way."""
+    hidden, weights, _ = build(1800, 64, [5000], 5000, seed=6)
+    weights[0].mul_(2.0 ** -6)
+    hidden.copy_(hidden[:1] + 0.25 * hidden)
+    for each in (9, 900):
+        tokens = torch.arange(1800, device="cuda") // each
+        gl = upstream(1800)[0].abs()
+        _, (gw,) = backward(hidden, weights, tokens, 5000, gl, None)
+        z, _, _, _ = truth(hidden, weights, 5000, 1.0)
+        d = -torch.softmax(z, 1) * gl.double()[:, None]
+        d.scatter_add_(1, tokens[:, None], gl.double()[:, None])
+        want = (d.t() @ hidden.double())[:1800 // each]
+        assert float((gw[:1800 // each].double() - want).norm()) <= 0.6 * UNIT["bf16"] * float(want.norm())
+
+
+@pytest.mark.parametrize("upstream_too", [True, False])
+def test_no_wait_runs_out_where_thousands_of_rows_share_a_token(upstream_too):
+    rows, size, vocab = 12000, 1024, 20000
+    hidden, weights, tokens = build(rows, size, [vocab], vocab, seed=8)
+    half = torch.arange(rows, device="cuda") % 2 == 0
+    tokens[half] = 7
+    gl, ge = upstream(rows)
+    if not upstream_too:
+        gl[half], ge[half] = 0, 0
+    a = hidden, weights, tokens
+    saved = forward(*a)
+    with dc.options(wait_limit_ns=2_000_000):
+        got = backward(*a, vocab, gl, ge, saved=saved)
+        assert dc.dc_check_device() == 0, dc.last_error()
+    check_backward(got, *a, vocab, gl, ge)
