@@ -736,7 +736,8 @@ size_t dc_attention_workspace_bytes(int64_t seqs, int q_heads, int kv_heads, int
  * own.workspace: dc_prefix_attention_workspace_bytes(seqs, prefixes, q_heads,
  * kv_heads, dim, max_prefix_tokens, max_tokens) bytes (widths of the tables
  * times the page size), 16-byte aligned, zero before its first use; each call
- * leaves it ready for the next of these sizes.  One per stream.  Three kernels.
+ * leaves it ready for the next of these sizes (one that returned DC_ERR_CUDA may
+ * not: zero it again).  One per stream.  Three kernels.
  */
 typedef struct {
     dc_paged_attention_t own;

@@ -317,7 +317,18 @@ __global__ __launch_bounds__(Shape<D, HB, APART>::kThreads, Shape<D, HB, APART>:
   const int seq = static_cast<int>(unit / static_cast<uint32_t>(p.head_blocks) / static_cast<uint32_t>(p.kv_heads));
   const int h0 = kh * p.group + hb * HB;          // first query head
   const int nh = min(HB, p.group - hb * HB);      // query heads of this CTA
-  pdl_enter();
+  if constexpr (PARTS) {
+    // the prefix's kernel runs beside this one: what came before both is done and seen
+    // here, which is passed on; in this order (dc_prefix_kernel)
+    pdl_wait();
+    if (blockIdx.x == 0) {
+      if (threadIdx.x == 0) st_release(p.ready, 1);
+      __syncthreads();
+    }
+    pdl_launch_dependents();
+  } else {
+    pdl_enter();
+  }
 
   const int32_t* lp = reinterpret_cast<const int32_t*>(p.lengths) + seq;
   int32_t len = in_bounds(lp, 4, p.lengths, p.lengths + 4ull * p.seqs, kSiteLength) ? *lp : 0;

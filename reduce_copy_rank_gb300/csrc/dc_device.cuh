@@ -93,6 +93,16 @@ __device__ __forceinline__ void pdl_launch_dependents() {
 }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// A word by which one kernel tells the next that what came before both is done.
+__device__ __forceinline__ void st_release(uint64_t at, uint32_t v) {
+  asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(at), "r"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t ld_acquire(uint64_t at) {
+  uint32_t v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(at) : "memory");
+  return v;
+}
+
 // Bulk prefetch of [p, p + bytes) from HBM into L2 (p 16-byte aligned, bytes a
 // multiple of 16).  It moves data between HBM and L2 only; L2 is where every
 // SM's loads and stores meet, so a later load still sees any store made in

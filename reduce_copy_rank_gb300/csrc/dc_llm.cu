@@ -215,7 +215,7 @@ dc_status_t run_attend(AttendParams& p, const AttendPlan& plan, int dtype, int d
   if (!cluster && plan.pieces > 8 && plan.units * plan.pieces > 4 * kAttendCtas)
     p.places = static_cast<int32_t>(std::max<uint64_t>(8, std::min<uint64_t>(plan.pieces, 4 * kAttendCtas / plan.units)));
   // more units than the counters have room for (29127 at least): a CTA each
-  if (!cluster && plan.pieces > 1 && plan.units * attend_counters(plan.pieces) * 4 > kAttendCounterBytes) p.places = 1;
+  if (!cluster && plan.pieces > 1 && plan.units * attend_counters(plan.pieces) > kAttendCounters) p.places = 1;
   int grid = 0;
   const cudaError_t e = (p.raw ? launch_attend_parts : launch_attend)(p, dtype, dim, pdl_option(), static_cast<cudaStream_t>(stream), &grid);
   return check_launch(e, "paged attention", grid);
@@ -556,6 +556,9 @@ dc_status_t dc_prefix_attention(const dc_prefix_attention_t* a, dc_stream_t stre
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   p.raw = x.raw;
   p.raw_rl = x.raw_rl;
+  x.ready = p.ready = ws + kAttendCounters * 4;
+  // (the prefix's kernel may start before the own tokens' has ended: that one waits for
+  // what came before the call, and only then lets this one start)
   DC_TRY(run_attend(p, plan, own.dtype, own.dim, sms, stream));
   cudaError_t e = launch_prefix(x, own.dtype, own.dim, pdl_option(), s, &grid);
   DC_TRY(check_launch(e, "attention to shared prefixes", grid));

@@ -114,8 +114,9 @@ constexpr int kAttendGroups = 8;      // groups of them, at most (128 pieces)
 // the workspace's, so that calls on parts of it of different lengths agree on
 // what has to be zero.  A unit has one, or, if it may have several groups, one
 // for them and one for each group's pieces; units beyond the area's room are
-// computed by a CTA each.
+// computed by a CTA each.  Its last word is attention to shared prefixes' (PrefixParams).
 constexpr uint64_t kAttendCounterBytes = 1 << 20;
+constexpr uint64_t kAttendCounters = kAttendCounterBytes / 4 - 1;
 __host__ __device__ constexpr uint32_t attend_counters(uint32_t pieces) {
   return pieces <= static_cast<uint32_t>(kAttendJoin) ? 1u : 1u + (pieces + kAttendJoin - 1) / kAttendJoin;
 }
@@ -129,6 +130,7 @@ struct AttendParams {
   uint64_t partial;                     // f32 [units][HB * (pieces * (dim + 2) + 2 * kAttendGroups)]
   uint64_t raw, raw_rl;                 // 0, or where the results go instead of out: f32 [seqs][q_heads][dim]
                                         // unnormalised, and [seqs][q_heads] (reference, sum)
+  uint64_t ready;                       // (with raw) uint32, as PrefixParams has it
   int64_t table_stride;
   int64_t num_pages;
   uint32_t page_size, table_width;
@@ -396,6 +398,7 @@ struct PrefixParams {
   uint64_t table, lengths;              // int32 [prefixes][table_width], [prefixes]
   uint64_t partial, partial_rl;         // f32 [prefixes][kv_heads][chunks][rows][dim], [..][rows] (reference, sum)
   uint64_t raw, raw_rl;                 // the sequences' own tokens, as AttendParams has them
+  uint64_t ready;                       // uint32, 0 between calls; 1: what came before the call is done
   int64_t table_stride, num_pages;
   uint32_t page_size, table_width;
   int32_t page_shift;

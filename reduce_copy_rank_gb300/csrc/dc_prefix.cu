@@ -173,10 +173,13 @@ __global__ __launch_bounds__(kThreads, Shape<D>::kCtas) void dc_prefix_kernel(co
 
   // The kernel before, over the own tokens, has waited for all work before it in
   // every CTA by the time this one starts, and nothing here reads what it writes:
-  // the two run side by side, and this one ends after it.  Measured, one after
-  // the other / side by side: 8 sequences of a group with 1025 tokens 20.6 / 14.7
-  // us, 4 groups of 16 with 7001 tokens each 49.7 / 45.2 us.
+  // the two run side by side, and this one ends after it.  That what the work before
+  // wrote is seen here too follows from the word that the other has released after its
+  // wait; where it is not there yet, this kernel waits for all of the other.  Measured,
+  // one after the other / side by side: 8 sequences of a group with 1025 tokens 20.6 /
+  // 14.7 us, 4 groups of 16 with 7001 tokens each 49.7 / 45.2 us.
   pdl_launch_dependents();
+  if (ld_acquire(p.ready) != 1) pdl_wait();
   bool bad;
   const uint32_t length = prefix_length(p, prefix, &bad);
   const uint32_t per = length ? prefix_chunk(length, p.kv_heads) : 1;
@@ -396,6 +399,7 @@ __global__ __launch_bounds__(kThreads, Shape<D>::kCtas) void dc_prefix_kernel(co
       cp_async16_or_zero(q_at + (c / 8) * (kPrefixRows * 128) + r * 128 + ((c % 8) ^ (r & 7)) * 16, read ? x : p.q, read);
     }
     cp_async_commit();
+    tma::fence_proxy_async_global();  // (keys and values may be an earlier kernel's stores)
     const PagedView& view = values ? p.vc : p.kc;
     Copier<D> copier{p, view, p.table + static_cast<uint64_t>(prefix) * static_cast<uint64_t>(p.table_stride) * 4,
                      static_cast<uint64_t>(kh) * view.head, end, values ? kSiteValue : kSiteKey, {}};
@@ -512,6 +516,7 @@ __global__ __launch_bounds__(kJoinThreads) void dc_prefix_join_kernel(const __gr
   const int lane = threadIdx.x & 31;
   const uint64_t row = static_cast<uint64_t>(blockIdx.x) * (kJoinThreads / 32) + (threadIdx.x >> 5);
   const uint64_t n = static_cast<uint64_t>(p.seqs) * p.q_heads;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *reinterpret_cast<uint32_t*>(p.ready) = 0;  // (for the next call)
   if (row >= n) return;
   const int seq = static_cast<int>(row / static_cast<uint32_t>(p.q_heads)), head = static_cast<int>(row % static_cast<uint32_t>(p.q_heads));
   const int prefix = seq / p.each;

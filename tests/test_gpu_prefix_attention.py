@@ -302,3 +302,42 @@ def test_follows_the_calls_before_and_after_it(prefixes, own):
         torch.cuda.synchronize()
         results.append(out)
     assert torch.equal(*results)
+
+
+@pytest.mark.parametrize("page", [16, 7])
+def test_tables_and_lengths_that_change_between_calls(page):
+    """... without a wait: each call reads the tables, lengths, keys and values that were written just before it."""
+    hq, hk, d, steps = 8, 2, 128, 16
+    q, kc, vc, pt, pl, ot, ol = build([900, 300], [200, 0, 7, 64], hq, hk, d, page)
+    g = torch.Generator(device="cuda").manual_seed(10)
+    held = torch.cat([t[t >= 0] for t in (pt, ot)])
+    kc.nan_to_num_(0.0)
+    vc.nan_to_num_(0.0)
+    pick = lambda t: held[torch.randint(0, len(held), t.shape, generator=g, device="cuda")]
+    tables = [(pick(pt), pick(ot)) for _ in range(steps)]
+    lengths = [tuple(torch.randint(0, t.shape[1] * page + 1, (len(t),), generator=g, device="cuda").int() for t in (pt, ot)) for _ in range(steps)]
+    new = torch.randn(steps, 5, hk, d, generator=g, device="cuda").to(torch.bfloat16)
+    pos = torch.arange(5, dtype=torch.int32, device="cuda") * page
+    zero = torch.zeros(5, dtype=torch.int32, device="cuda")
+    where = torch.stack([held[torch.randperm(len(held), generator=g, device="cuda")[:5]] for _ in range(steps)])  # (a slot once a call)
+    caches = kc.clone(), vc.clone()
+    ws = dc.prefix_attention_workspace(4, 2, hq, hk, d, pt.shape[1] * page, ot.shape[1] * page)
+    results = []
+    for wait in (True, False):
+        out, lse = torch.zeros(steps, *q.shape, device="cuda", dtype=q.dtype), torch.zeros(steps, 4, hq, device="cuda")
+        kc.copy_(caches[0])
+        vc.copy_(caches[1])
+        torch.cuda.synchronize()
+        for i in range(steps):
+            for to, have in zip((pt, ot, pl, ol), (*tables[i], *lengths[i])):
+                to.copy_(have)
+            dc.kv_append(new[i], new[i], pos, zero, where[i:i + 1], kc, vc)
+            if wait:
+                torch.cuda.synchronize()
+            dc.prefix_attention(q, kc, vc, pt, pl, ot, ol, out[i], ws, lse=lse[i])
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        results.append((out, lse))
+    check((results[0][0][-1], results[0][1][-1]), q, kc, vc, pt, pl, ot, ol)
+    assert torch.equal(results[0][0], results[1][0]) and torch.equal(results[0][1], results[1][1])
