@@ -249,7 +249,8 @@ dc_status_t plan_prefix(int64_t seqs, int64_t prefixes, int q_heads, int kv_head
   if (max_tokens > 0x7FFFFFFFull)
     return fail(DC_ERR_INVALID, "prefixes of up to %llu tokens", static_cast<unsigned long long>(max_tokens));
   const uint64_t tiles = (max_tokens + kPrefixTile - 1) / kPrefixTile;
-  z->chunks = static_cast<uint32_t>(std::max<uint64_t>(1, std::min<uint64_t>(tiles, prefix_most_chunks(kv_heads))));
+  const uint64_t most = std::max<uint64_t>(prefix_most_chunks(kv_heads), (max_tokens + kPrefixChunk - 1) / kPrefixChunk);
+  z->chunks = static_cast<uint32_t>(std::max<uint64_t>(1, std::min<uint64_t>(tiles, most)));
   const uint64_t rows = static_cast<uint64_t>(seqs / prefixes) * static_cast<uint64_t>(q_heads / kv_heads);
   const uint64_t units = static_cast<uint64_t>(prefixes) * static_cast<uint64_t>(kv_heads) * z->chunks;
   if (rows > 0x7FFFFFFFull - kPrefixRows || units > 0x7FFFFFFFull || units * ((rows + kPrefixRows - 1) / kPrefixRows) > 0x7FFFFFFFull ||

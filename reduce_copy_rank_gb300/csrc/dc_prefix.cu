@@ -525,20 +525,14 @@ __global__ __launch_bounds__(kJoinThreads) void dc_prefix_join_kernel(const __gr
   const uint64_t all = static_cast<uint64_t>(p.prefixes) * p.kv_heads * p.chunks * p.rows;
   const uint64_t at = (static_cast<uint64_t>(prefix) * p.kv_heads + head / p.group) * p.chunks * p.rows +
                       static_cast<uint64_t>(seq % p.each) * p.group + head % p.group;  // of chunk 0; the next is p.rows on
-  // lane l holds the references and sums of chunks l, l + 32, ...
-  constexpr int kHeld = (kAttendSms + 31) / 32;  // (as many chunks as there are SMs, at most)
-  float ref[kHeld], sum[kHeld];
   const float2 own = reinterpret_cast<const float2*>(p.raw_rl)[row];
-  float most = own.x;
-#pragma unroll
-  for (int k = 0; k < kHeld; ++k) {
-    const uint32_t c = static_cast<uint32_t>(k * 32 + lane);
+  auto chunk = [&](uint32_t c) {  // its reference and sum
     const float2* a = reinterpret_cast<const float2*>(p.partial_rl) + at + static_cast<uint64_t>(c) * p.rows;
-    const float2 x = c < chunks && in_bounds(a, 8, p.partial_rl, p.partial_rl + all * 8, kSitePartial) ? *a : make_float2(neg_inf(), 0.0f);
-    ref[k] = x.x;
-    sum[k] = x.y;
-    most = fmaxf(most, x.x);
-  }
+    return c < chunks && in_bounds(a, 8, p.partial_rl, p.partial_rl + all * 8, kSitePartial) ? *a : make_float2(neg_inf(), 0.0f);
+  };
+  float2 held = chunk(lane);  // lane l's: of 32 chunks the l-th
+  float most = fmaxf(own.x, held.x);
+  for (uint32_t c = lane + 32; c < chunks; c += 32) most = fmaxf(most, chunk(c).x);
 #pragma unroll
   for (int d = 16; d > 0; d /= 2) most = fmaxf(most, __shfl_xor_sync(~0u, most, d));
   float4 u[kVecs];
@@ -563,9 +557,9 @@ __global__ __launch_bounds__(kJoinThreads) void dc_prefix_join_kernel(const __gr
     }
   };
   constexpr int kAtOnce = kVecs > 1 ? 4 : 8;
-#pragma unroll
-  for (int k = 0; k < kHeld; ++k)
-    for (uint32_t c0 = k * 32; c0 < min(chunks, static_cast<uint32_t>(k * 32 + 32)); c0 += kAtOnce) {
+  for (uint32_t k = 0; k < chunks; k += 32) {
+    if (k) held = chunk(k + lane);
+    for (uint32_t c0 = k; c0 < min(chunks, k + 32); c0 += kAtOnce) {
       float4 x[kAtOnce][kVecs];
 #pragma unroll
       for (int j = 0; j < kAtOnce; ++j)
@@ -574,10 +568,11 @@ __global__ __launch_bounds__(kJoinThreads) void dc_prefix_join_kernel(const __gr
 #pragma unroll
       for (int j = 0; j < kAtOnce; ++j)
         if (c0 + j < chunks) {
-          const float r = __shfl_sync(~0u, ref[k], (c0 + j) % 32), s = __shfl_sync(~0u, sum[k], (c0 + j) % 32);
+          const float r = __shfl_sync(~0u, held.x, (c0 + j) % 32), s = __shfl_sync(~0u, held.y, (c0 + j) % 32);
           add(x[j], pow2_diff(r, most), s);
         }
     }
+  }
   float4 x[kVecs];
   load(x, p.raw + row * D * 4, p.raw, p.raw + n * D * 4);
   add(x, pow2_diff(own.x, most), own.y);

@@ -341,3 +341,42 @@ def test_tables_and_lengths_that_change_between_calls(page):
         results.append((out, lse))
     check((results[0][0][-1], results[0][1][-1]), q, kc, vc, pt, pl, ot, ol)
     assert torch.equal(results[0][0], results[1][0]) and torch.equal(results[0][1], results[1][1])
+
+
+def test_sums_over_long_prefixes_are_cut():
+    """Flat scores and positive values of a million tokens, few CTAs a key head (the tokens' pages come again and
+    again).  Weights are 1, so the output is off by its last rounding (2^-11), and by sums of at most 24576 tokens on
+    the tensor cores, 16 at a time, each cut rather than rounded at worst (1536 times 2^-23); 2^-15 for the others."""
+    tokens, hk, d, page = 1 << 20, 32, 64, 64
+    g = torch.Generator(device="cuda").manual_seed(1)
+    kc = torch.randn(9, page, hk, d, generator=g, device="cuda").half()
+    vc = (1 + torch.rand(9, page, hk, d, generator=g, device="cuda")).half()
+    pt = (torch.arange(tokens // page, device="cuda") % 8).int()[None]
+    q = torch.zeros(2, hk, d, device="cuda", dtype=torch.float16)
+    one = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    out, lse = attend(q, kc, vc, pt, one(tokens), one(8, 8)[:, None], one(0, 1))
+    want = vc[:8].double().mean((0, 1))
+    for b in range(2):
+        assert float(((out[b].double() - want).abs() / want).max()) <= 2.0 ** -11 + 1536 * 2.0 ** -23 + 2.0 ** -15
+        assert float((lse[b] - math.log(tokens + b)).abs().max()) <= 2.0 ** -18 * (1 + math.log(tokens))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("hk,tokens", [(1, 1 << 22), (160, 1 << 15)])
+def test_more_chunks_than_fill_the_gpu(hk, tokens, dtype):
+    """(Pages that come again and again: the softmax is that over each once.)"""
+    d, page, pages = 64, 64, 8
+    g = torch.Generator(device="cuda").manual_seed(2)
+    kc, vc = (torch.randn(pages + 1, page, hk, d, generator=g, device="cuda").to(DT[dtype]) for _ in range(2))
+    pt = (torch.arange(tokens // page, device="cuda") % pages).int()[None]
+    q = torch.randn(2, hk, d, generator=g, device="cuda").to(DT[dtype])
+    one = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    out, lse = attend(q, kc, vc, pt, one(tokens), one(8, 8)[:, None], one(0, 0))
+    again = torch.log(torch.tensor(tokens // (page * pages), dtype=torch.float64))
+    table = torch.arange(pages, device="cuda").int()[None]
+    check((out, (lse.double() - again.item()).float()), q, kc, vc, table, one(pages * page), one(8, 8)[:, None], one(0, 0), dtype=dtype)
+
+
+def test_a_chunk_at_a_time_of_many_key_heads():
+    a = build([50000, 24577], [30, 0], 80, 80, 64, 64, "f16")
+    check(attend(*a), *a, dtype="f16")
