@@ -412,8 +412,8 @@ dc_status_t dc_token_logprobs_backward(const dc_token_logprobs_backward_t *args,
  *   DC_F16, rows 16-byte aligned, hidden_size a multiple of 8 up to 2^20.
  *   The products are exact and their sums binary32, as are all statistics.
  * ranks, widths, vocab, temperature, tokens: as for dc_token_logprobs (rows of
- *   the weights past `vocab` are not read).  Infinities and NaN are those of
- *   the formulas.  Up to 2^24 rows.
+ *   the weights past `vocab` are not read), and so are rows of nothing but -inf
+ *   and rows with NaN or +inf.  Up to 2^24 rows.
  * logprobs [rows]; entropy, lse [rows] or NULL.
  * A row's bits do not depend on the other rows, and not on the shards where
  * every shard but the last is a multiple of 256 wide.

@@ -12,10 +12,10 @@
 // 256 in turn, each with 128 of the rows and half of B's columns in its shared
 // memory; while one is computed eight warps reduce the one before from tensor
 // memory:
-//  * forward: a row's part of the tile as its maximum (rounded up to a whole
-//    number r in units of log2), sum 2^(z-r) and sum 2^(z-r) (z-r), written as
-//    16 bytes; a second kernel adds a row's parts up in one fixed order, which
-//    depends on the shards' widths alone.
+//  * forward: a row's part of the tile as its largest logit m, sum 2^(z-r) and sum
+//    2^(z-r) (z-r), z in units of log2 and r that of m, written as 16 bytes; a
+//    second kernel adds a row's parts up in one fixed order, which depends on the
+//    shards' widths alone.
 //  * backward, for up to 24576 columns of a shard at a time: the logits again,
 //    from which d is written in 16 bits; then d W, added to binary32 sums, and
 //    d^T h in one launch, whose tiles are shared out so that all CTAs end together.
@@ -114,8 +114,16 @@ __device__ __forceinline__ void stats(const LinearParams& p, float (&v)[kLinearP
   float m[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
 #pragma unroll
   for (int j = 0; j < kLinearPart; j += 2) m[j / 2 & 3] = max3(m[j / 2 & 3], v[j], v[j + 1]);
-  const float top = fmaxf(max3(m[0], m[1], m[2]), m[3]) * c;
-  const float ref = ceilf(top), base = ref == neg_inf() ? 0.0f : ref;
+  const float most = fmaxf(max3(m[0], m[1], m[2]), m[3]), top = most * c;
+  // Exponents are taken from top, one fused multiply-add each, and what its rounding took
+  // is put back into the sums; where that is more than a quarter (logits of millions, or
+  // temperatures that make them so) from the logits' differences.
+  float base = most == neg_inf() ? 0.0f : top, off = most == neg_inf() ? 0.0f : __fmaf_rn(most, c, -top);
+  if (most != neg_inf() && !(fabsf(top) < 4194304.0f)) {
+#pragma unroll
+    for (int j = 0; j < kLinearPart; ++j) v[j] -= most;
+    base = off = 0.0f;
+  }
   float s[4] = {}, t[4] = {};
 #pragma unroll
   for (int j = 0; j < kLinearPart; ++j) {
@@ -123,9 +131,10 @@ __device__ __forceinline__ void stats(const LinearParams& p, float (&v)[kLinearP
     s[j & 3] += e;
     t[j & 3] = __fmaf_rn(e, fmaxf(x, -1e4f), t[j & 3]);  // (e is 0 or NaN where that matters)
   }
+  const float sum = (s[0] + s[1]) + (s[2] + s[3]), f = ex2(-off);
   float4* a = reinterpret_cast<float4*>(p.part) + static_cast<uint64_t>(part) * p.rows + row;
   if (in_bounds(a, 16, p.part, p.target, kSitePart))
-    *a = make_float4(ref, (s[0] + s[1]) + (s[2] + s[3]), (t[0] + t[1]) + (t[2] + t[3]), 0.0f);
+    *a = make_float4(most, f * sum, f * __fmaf_rn(-off, sum, (t[0] + t[1]) + (t[2] + t[3])), 0.0f);
 }
 
 // Adds the tile's accumulators to v.
@@ -669,10 +678,11 @@ __global__ __launch_bounds__(kFinishThreads) void dc_linear_finish_kernel(const 
   const uint64_t row = blockIdx.x;
   const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float ref = neg_inf(), s = 0.0f, t = 0.0f;
+  const float c = p.inv_t * kLog2E;
   auto add = [&](float r, float s1, float t1) {
-    // t = sum 2^(z-ref) (z-ref): moving ref by k adds k times the sum
+    // t = sum 2^(z-ref) (z-ref): moving ref by k adds k times the sum (2^-10000 is 0, and NaN is in the sums)
     const float m = fmaxf(ref, r);
-    const float k0 = ref == neg_inf() ? 0.0f : ref - m, k1 = r == neg_inf() ? 0.0f : r - m;
+    const float k0 = ref == neg_inf() ? 0.0f : fmaxf((ref - m) * c, -1e4f), k1 = r == neg_inf() ? 0.0f : fmaxf((r - m) * c, -1e4f);
     const float f0 = ex2(k0), f1 = ex2(k1);
     t = __fmaf_rn(f0, __fmaf_rn(s, k0, t), f1 * __fmaf_rn(s1, k1, t1));
     s = __fmaf_rn(f0, s, f1 * s1);
@@ -701,7 +711,8 @@ __global__ __launch_bounds__(kFinishThreads) void dc_linear_finish_kernel(const 
   __syncthreads();
   if (threadIdx.x) return;
   for (int w = 1; w < kFinishThreads / 32; ++w) add(joined[w].x, joined[w].y, joined[w].z);
-  const float log_s = log2f(s), nan = __int_as_float(0x7FC00000);
+  const bool none = ref == neg_inf() && s == 0.0f;  // nothing but -inf
+  const float log_2 = log2f(s), log_s = log_2 * kLn2, nan = __int_as_float(0x7FC00000);
   const int64_t token = token_of(p.tokens, p.tokens64, row);
   auto put = [&](uint64_t base, float v) {
     float* a = reinterpret_cast<float*>(base) + row;
@@ -709,10 +720,10 @@ __global__ __launch_bounds__(kFinishThreads) void dc_linear_finish_kernel(const 
   };
   float lp = 0.0f;
   if (token >= static_cast<int64_t>(p.vocab)) lp = nan;
-  else if (token >= 0) lp = (__fmaf_rn(ld_row(p.target, row, p.rows), p.inv_t * kLog2E, -ref) - log_s) * kLn2;
+  else if (token >= 0) lp = none ? neg_inf() : __fmaf_rn(ld_row(p.target, row, p.rows) - ref, p.inv_t, -log_s);
   put(p.logprobs, lp);
-  if (p.entropy) put(p.entropy, (log_s - t / s) * kLn2);
-  if (p.lse) put(p.lse, (ref + log_s) * kLn2);
+  if (p.entropy) put(p.entropy, none ? 0.0f : (log_2 - t / s) * kLn2);
+  if (p.lse) put(p.lse, none ? neg_inf() : __fmaf_rn(ref, p.inv_t, log_s));
 }
 
 // Where dW's columns find what d lost of the rows whose token they are, for calls of

@@ -505,3 +505,37 @@ def test_no_wait_runs_out_where_thousands_of_rows_share_a_token(upstream_too):
         got = backward(*a, vocab, gl, ge, saved=saved)
         assert dc.dc_check_device() == 0, dc.last_error()
     check_backward(got, *a, vocab, gl, ge)
+
+
+@pytest.mark.parametrize("dtype,power,temperature", [
+    ("bf16", 0, 1e-7), ("bf16", 0, 1e-9), ("bf16", 0, 1e-20), ("bf16", 0, 1e-36), ("bf16", 0, 4.3e-39), ("bf16", 27, 1.0), ("bf16", 60, 1.0),
+    ("bf16", 105, 1e-3), ("f16", 12, 1e-9), ("f16", 0, 4.3e-39)])
+def test_temperatures_and_logits_at_which_only_the_largest_count(dtype, power, temperature):
+    """Whole numbers times a power of two, so that the logits are exact: the largest of a row share the probability
+    evenly, and nothing overflows to NaN."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    hidden = torch.randint(-3, 4, (140, 72), generator=g, device="cuda")
+    weights = [torch.randint(-3, 4, (n, 72), generator=g, device="cuda") for n in (700, 513)]
+    z = hidden.double() @ torch.cat(weights).double().t()
+    hidden = (hidden.double() * 2.0 ** power).to(DT[dtype])
+    tokens = z.argmax(1)
+    tokens[7], tokens[100] = z[7].argmin(), z[100].argmin()
+    lp, ent, lse = forward(hidden, [w.to(DT[dtype]) for w in weights], tokens, temperature=temperature)
+    ties = (z == z.amax(1, keepdim=True)).sum(1).double().log()
+    tol = 2.0 ** -20 * (1 + math.log(1213))
+    assert int((ties > 0).sum()) > 3
+    assert float((ent.double() - ties).abs().max()) <= tol
+    rest = [i for i in range(140) if i not in (7, 100)]
+    assert float((lp.double() + ties)[rest].abs().max()) <= tol
+    assert bool((lp[[7, 100]] < -1e6).all()) and not bool(torch.isnan(lse).any())
+
+
+def test_rows_of_nothing_but_minus_infinity():
+    hidden, weights, tokens = build(5, 64, [300], 300)
+    weights[0].abs_().neg_()
+    hidden[1] = 3e38  # (its logits are sums that leave binary32)
+    tokens[1] = 7
+    lp, ent, lse = forward(hidden, weights, tokens)
+    assert float(lse[1]) == -math.inf and float(lp[1]) == -math.inf and float(ent[1]) == 0
+    keep = [0, 2, 3, 4]
+    check_forward([t[keep] for t in (lp, ent, lse)], hidden[keep], weights, tokens[keep], 300)
