@@ -468,7 +468,8 @@ size_t dc_linear_logprobs_workspace_bytes(int64_t rows, int64_t hidden_size, int
  *   `ranks` pointers, shaped as the weights, or NULL; either is needed.  They
  *   replace what was there.  Rows of the weights' gradient past `vocab` are 0,
  *   as are all of them if there are no rows.  No output may meet an input.
- * A row whose lse is -1e30 or less, or whose g and h are 0, has no gradient (its
+ * A row whose token is vocab or more has NaN for one, as there; one whose lse is
+ * -1e30 or less, or whose g and h are 0, has no gradient (its
  * hidden row still has to be finite where grad_weights are wanted: 0 times NaN is
  * NaN there).  A row of grad_hidden does not depend on the other rows (for DC_F16: beyond the power of two); the order
  * of every sum is fixed.

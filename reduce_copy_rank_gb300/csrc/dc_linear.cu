@@ -188,8 +188,9 @@ __device__ __forceinline__ void dlogits(const LinearParams& p, uint32_t at, uint
   if (own) {
     token = token_of(p.tokens, p.tokens64, row);
     const float unit = p.scale ? *reinterpret_cast<const float*>(p.scale) : 1.0f;
-    const float g = p.grad_logprobs && token >= 0 ? ld_row(p.grad_logprobs, row, p.rows) : 0.0f;
     const float e = p.grad_entropy ? ld_row(p.grad_entropy, row, p.rows) : 0.0f;
+    float g = p.grad_logprobs && token >= 0 ? ld_row(p.grad_logprobs, row, p.rows) : 0.0f;
+    if (token >= static_cast<int64_t>(p.vocab) && (g != 0.0f || e != 0.0f)) g = __int_as_float(0x7FC00000);
     const float h = p.grad_entropy ? ld_row(p.entropy, row, p.rows) : 0.0f;
     const float lse = ld_row(p.lse, row, p.rows);
     lse2 = lse * kLog2E;

@@ -539,3 +539,30 @@ def test_rows_of_nothing_but_minus_infinity():
     assert float(lse[1]) == -math.inf and float(lp[1]) == -math.inf and float(ent[1]) == 0
     keep = [0, 2, 3, 4]
     check_forward([t[keep] for t in (lp, ent, lse)], hidden[keep], weights, tokens[keep], 300)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("entropy", [True, False])
+def test_tokens_past_the_vocabulary_have_no_gradient_that_is_a_number(entropy, dtype):
+    """... unless nothing comes from above: what token_logprobs_backward of the same logits gives their rows."""
+    hidden, weights, tokens = build(90, 64, [300, 100], 380, dtype)
+    gl, ge = upstream(90, entropy=entropy)
+    saved = forward(hidden, weights, tokens, 380)
+    tokens[[5, 40]] = torch.tensor([380, 5000], device="cuda")
+    tokens[70] = 399
+    gl[70] = 0
+    if entropy:
+        ge[70] = 0
+    gh, gw = backward(hidden, weights, tokens, 380, gl, ge, saved=saved)
+    bad = torch.tensor([5, 40], device="cuda")
+    logits = [(hidden.double() @ w.nan_to_num().double().t()).to(DT[dtype]) for w in weights]
+    grads = [torch.empty_like(x) for x in logits]
+    dc.token_logprobs_backward(logits, tokens, saved[2], gl, grads, entropy=saved[1], grad_entropy=ge, vocab=380)
+    assert all(bool(torch.isnan(g[bad][:, :w]).all()) for g, w in zip(grads, (300, 80)))
+    assert bool(torch.isnan(gh[bad]).all()) and bool((gh[70] == 0).all())
+    keep = [i for i in range(90) if i not in (5, 40)]
+    assert bool(torch.isfinite(gh[keep]).all())
+    assert bool(torch.isnan(gw[0]).all()) and bool((gw[1][80:] == 0).all())
+    a = hidden[keep], weights, torch.where(tokens[keep] >= 380, -1, tokens[keep])
+    check_backward((backward(*a, 380, gl[keep], ge[keep] if entropy else None, saved=[t[keep] for t in saved])[0], None), *a, 380,
+                   gl[keep], ge[keep] if entropy else None, dtype=dtype)
