@@ -285,9 +285,18 @@ __global__ __launch_bounds__(kThreads, Shape<D>::kCtas) void dc_prefix_kernel(co
           sum *= f;
           ref = now;
         }
-        const float off = kShift<DT> - (ref == neg_inf() ? 0.0f : ref);
+        float off = kShift<DT> - (ref == neg_inf() ? 0.0f : ref), by = sc;
         uint64_t l[2] = {0, 0};  // two sums each
-        const uint64_t sc2 = pack2(sc, sc), off2 = pack2(off, off);
+        // A fused multiply-add takes the reference from a product that is not rounded, as the
+        // own tokens' and the reference's are: beyond 2^14 that would show in the weights, and
+        // far beyond in nothing else.
+        if (fabsf(ref) >= 16384.0f && ref != neg_inf()) {
+#pragma unroll
+          for (int j = 0; j < S::kTile; ++j) r[j / 32][j % 32] = __float_as_uint(__uint_as_float(r[j / 32][j % 32]) * sc - ref);
+          off = kShift<DT>;
+          by = 1.0f;
+        }
+        const uint64_t sc2 = pack2(by, by), off2 = pack2(off, off);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t w[16];

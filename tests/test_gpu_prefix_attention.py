@@ -380,3 +380,15 @@ def test_more_chunks_than_fill_the_gpu(hk, tokens, dtype):
 def test_a_chunk_at_a_time_of_many_key_heads():
     a = build([50000, 24577], [30, 0], 80, 80, 64, 64, "f16")
     check(attend(*a), *a, dtype="f16")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("scale", [2.0 ** 12, 2.0 ** 16, 2.0 ** 20, 2.0 ** 27, -2.0 ** 33, 2.0 ** 33])
+def test_scores_of_which_only_the_largest_count(scale, dtype):
+    """Whole numbers, so that the scores are exact: tokens with the largest share the weight evenly.  (Scores of 2^39
+    are as far as the reference's lse holds the log of how many they are.)"""
+    a = build([2000, 700], [50, 0, 7, 300], 8, 2, 64, 16, dtype)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    for t in (a[0], a[1]):
+        t.copy_(torch.randint(-2, 3, t.shape, generator=g, device="cuda").to(t.dtype))
+    check(attend(*a, scale=scale), *a, scale=scale, dtype=dtype)
