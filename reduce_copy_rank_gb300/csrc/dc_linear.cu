@@ -181,8 +181,7 @@ __device__ __forceinline__ void st_row32(uint64_t at, const float (&v)[32], int 
 // Backward: the gradient of one row's logits in a tile.
 template <int DT>
 __device__ __forceinline__ void dlogits(const LinearParams& p, uint32_t at, uint64_t row, bool own, uint32_t n0) {
-  const float c = p.inv_t * kLog2E;
-  float lse2 = 0.0f, a0 = 0.0f, a1 = 0.0f, hot = 0.0f;
+  float lse = 0.0f, a0 = 0.0f, a1 = 0.0f, hot = 0.0f;
   int64_t token = -1;
   bool none = false;  // a row without a finite logit, or without upstream gradients, has no gradient
   if (own) {
@@ -192,8 +191,7 @@ __device__ __forceinline__ void dlogits(const LinearParams& p, uint32_t at, uint
     float g = p.grad_logprobs && token >= 0 ? ld_row(p.grad_logprobs, row, p.rows) : 0.0f;
     if (token >= static_cast<int64_t>(p.vocab) && (g != 0.0f || e != 0.0f)) g = __int_as_float(0x7FC00000);
     const float h = p.grad_entropy ? ld_row(p.entropy, row, p.rows) : 0.0f;
-    const float lse = ld_row(p.lse, row, p.rows);
-    lse2 = lse * kLog2E;
+    lse = ld_row(p.lse, row, p.rows);
     const float f = p.inv_t * unit;
     hot = g * f;
     a0 = -(g + e * h) * f;   // d = p (a0 + a1 log2 p), and hot at the token
@@ -217,7 +215,7 @@ __device__ __forceinline__ void dlogits(const LinearParams& p, uint32_t at, uint
     tmem_ld32(at + j0, v);
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
-      const float x = __fmaf_rn(v[j], c, -lse2);
+      const float x = __fmaf_rn(v[j], p.inv_t, -lse) * kLog2E;
       v[j] = ex2(x) * __fmaf_rn(a1, x < -1e4f ? -1e4f : x, a0);
       if (j0 + j == mine) v[j] += hot;
       if (j0 + j >= exist) v[j] = 0.0f;

@@ -566,3 +566,27 @@ def test_tokens_past_the_vocabulary_have_no_gradient_that_is_a_number(entropy, d
     a = hidden[keep], weights, torch.where(tokens[keep] >= 380, -1, tokens[keep])
     check_backward((backward(*a, 380, gl[keep], ge[keep] if entropy else None, saved=[t[keep] for t in saved])[0], None), *a, 380,
                    gl[keep], ge[keep] if entropy else None, dtype=dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_probabilities_from_a_large_lse(dtype):
+    """Whole numbers and a temperature of 2^-14, so that z is exact: log p = z - lse is off by the rounding of lse that
+    it is given and no more, p by 2^-20 of itself for the exponential, and d by half a step."""
+    g = torch.Generator(device="cuda").manual_seed(12)
+    hidden = torch.randint(-3, 4, (100, 72), generator=g, device="cuda").to(DT[dtype])
+    weights = [torch.randint(-3, 4, (900, 72), generator=g, device="cuda").to(DT[dtype])]
+    tokens = torch.full((100,), -1, device="cuda")
+    tokens[::2] = (hidden.float() @ weights[0].float().t()).argmax(1)[::2]
+    saved = forward(hidden, weights, tokens, temperature=2.0 ** -14)
+    assert float(saved[2].max()) > 2e6
+    up = upstream(100)[0] * 2.0 ** -8  # (gradients that binary16 holds)
+    gh, (gw,) = backward(hidden, weights, tokens, 900, up, None, temperature=2.0 ** -14, saved=saved)
+    z = hidden.double() @ weights[0].double().t() * 2.0 ** 14
+    kept = (tokens >= 0).double()[:, None]
+    d = -(z - saved[2].double()[:, None]).exp() * up.double()[:, None] * kept
+    loss = d.abs() * (UNIT[dtype] + 2.0 ** -20)
+    d = (d + torch.nn.functional.one_hot(tokens.clamp(min=0), 900) * up.double()[:, None] * kept) * 2.0 ** 14
+    loss = loss * 2.0 ** 14 + d.abs() * UNIT[dtype]
+    for have, want, off in ((gh, d @ weights[0].double(), loss @ weights[0].double().abs()), (gw, d.t() @ hidden.double(), loss.t() @ hidden.double().abs())):
+        tol = UNIT[dtype] * (want.abs() + off) + off + 2.0 ** -10
+        assert float(((have.double() - want).abs() - tol).max()) <= 0
