@@ -296,6 +296,7 @@ __global__ __launch_bounds__(kThreads, Shape<D>::kCtas) void dc_prefix_kernel(co
           off = kShift<DT>;
           by = 1.0f;
         }
+        __syncwarp();  // (tensor memory is a warp's to read and write)
         const uint64_t sc2 = pack2(by, by), off2 = pack2(off, off);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -348,6 +349,7 @@ __global__ __launch_bounds__(kThreads, Shape<D>::kCtas) void dc_prefix_kernel(co
 #pragma unroll 1
       for (uint32_t d = 0; d < D; d += 32) {
         float v[32];
+        __syncwarp();
         tmem_ld32(tmem + lanes + S::kOut + d, v);
         if (row >= p.rows) continue;
         float4* a = reinterpret_cast<float4*>(p.partial + (mine * D + d) * 4);
