@@ -471,8 +471,10 @@ size_t dc_linear_logprobs_workspace_bytes(int64_t rows, int64_t hidden_size, int
  * A row whose token is vocab or more has NaN for one, as there; one whose lse is
  * -1e30 or less, or whose g and h are 0, has no gradient (its
  * hidden row still has to be finite where grad_weights are wanted: 0 times NaN is
- * NaN there).  A row of grad_hidden does not depend on the other rows (for DC_F16: beyond the power of two); the order
- * of every sum is fixed.
+ * NaN there).  A row of grad_hidden does not depend on the other rows (for DC_F16:
+ * beyond the power of two).  The order of every sum is fixed; that of
+ * grad_hidden's follows from the shards, so that one shard and eight give other
+ * bits, within the roundings above.
  * workspace: dc_linear_logprobs_workspace_bytes(rows, hidden_size, columns, 1)
  * bytes, as above.  Several kernels.
  */
@@ -729,7 +731,7 @@ size_t dc_attention_workspace_bytes(int64_t seqs, int q_heads, int kv_heads, int
  * empty, or both (zeros and lse = -inf).  A page outside the cache, or a length
  * past its table, gives NaN in the sequences that it belongs to.
  * The prefix's weights are rounded to 16 bits before they meet the values (half
- * a step each, of either sign; for DC_F16 down to 2^-31 of the row's largest),
+ * a step each, of either sign; for DC_F16 down to 2^-30 of the row's largest),
  * everything else as in dc_paged_attention; an infinite value gives infinities
  * or NaN.
  * A sequence's bits depend on its own tokens and its prefix's, not on the other

@@ -19,7 +19,9 @@
 //  * backward, for up to 24576 columns of a shard at a time: the logits again,
 //    from which d is written in 16 bits; then d W, added to binary32 sums, and
 //    d^T h in one launch, whose tiles are shared out so that all CTAs end together.
-// Neither the number of rows nor the grid changes a bit of a row's results.
+// Neither the number of rows nor the grid changes a bit of a row's results (DC_F16's
+// gradient: beyond its power of two, which all rows' upstream gradients decide).  How the
+// vocabulary is cut into shards and chunks decides the order of dh's sums.
 //
 // Rounding: d is rounded to 16 bits before its products (half a step of each: 2^-8
 // of it for DC_BF16, 2^-11 for DC_F16), as an activation's gradient is; the sums are
@@ -32,9 +34,11 @@
 // is between 2^14 and 2^15: what is 2^-29 of that is still a normal number.
 //
 // Bound: the tensor cores for training batches, the weights' bytes for few rows.
-// Measured, BF16, 4096 rows of 4096 against 128000 columns: forward 2.66 ms, 1.61
-// PFLOP/s, gradient 8.14 ms, 1.58 (tiles of 128 x 256 a CTA, without the pair: 2.71 and
-// 8.84); 128 rows against 131072 columns on 8 shards: 201 us, 5.3 TB/s.
+// Measured, BF16, 4096 rows of 4096 against 128000 columns: forward 2.64 ms, 1.63
+// PFLOP/s, gradient 8.0 to 8.4 ms, 1.53 to 1.61 (tiles of 128 x 256 a CTA, without the pair:
+// 2.71 and 8.84); 128 rows against 131072 columns on 8 shards: 194 us, 5.5 TB/s (179 and 6.0
+// with tiles of 128 x 256 and one run: a row of tiles has half of its rows to spare here, and
+// shorter runs are read more often).
 #include <algorithm>
 #include <atomic>
 #include <cstddef>
@@ -1121,18 +1125,6 @@ cudaError_t launch_linear_scale(uint64_t grad_logprobs, uint64_t grad_entropy, u
 
 DC_BOUNDS_READER(take_bounds_linear)
 
-cudaError_t take_linear_faults(uint32_t* bits) {
-  *bits = 0;
-  cudaError_t e = cudaDeviceSynchronize();
-  if (e != cudaSuccess) return e;
-  unsigned int v = 0;
-  e = cudaMemcpyFromSymbol(&v, g_linear_fault_bits, sizeof v);
-  if (e == cudaSuccess && v) {
-    const unsigned int zero = 0;
-    e = cudaMemcpyToSymbol(g_linear_fault_bits, &zero, sizeof zero);
-  }
-  *bits = v;
-  return e;
-}
+DC_FAULT_READER(take_linear_faults, g_linear_fault_bits)
 
 }  // namespace dc

@@ -26,10 +26,13 @@
 // a CTA 186 to 198 us.  64 sequences in four groups of 7001 tokens, 12/12 heads of
 // 64, FP16: 24 us.
 //
-// Rounding: the weights enter the second product in 16 bits (half a step each,
-// 2^-9 or 2^-12, of either sign); their sum l takes them unrounded.  In
-// binary16 they are held times 2^7 or more, so that what is 2^-21 of the largest
-// is still a normal number.
+// Rounding: the weights enter the second product in 16 bits (half a step each at
+// most, 2^-8 or 2^-11 of it, of either sign); their sum l takes them unrounded.  In
+// binary16 they are held times 2^7, a row's largest between 2^6 and 2^15, so that what is
+// 2^-20 of that is still a normal number.  (The own tokens' weights enter as two numbers
+// each, so that the last rounding is theirs alone: 2 products for 1, which their kernel has
+// to spare and this one's chain has not.  Error of the outputs, BF16 / FP16: 2.4e-3 /
+// 2.9e-4, with weights in 32 bits 1.7e-3 / 2.1e-4.)
 #include <atomic>
 
 #include "dc_llm.h"
@@ -50,7 +53,7 @@ struct Shape {
   static constexpr int kTile = kPrefixTile;
   static constexpr int kBlocks = (D + 63) / 64;          // of 64 columns: swizzled rows of 128 bytes
   static constexpr int kStages = D > 64 ? 2 : 4;         // of keys, and of values
-  static constexpr int kScores = 2;                      // buffers of scores
+  static constexpr int kScores = 2;                      // buffers of scores: the next tile's are under way
   static constexpr int kCtas = D > 128 ? 1 : 2;
   static constexpr int kQ = kBlocks * kPrefixRows * 128, kKV = kBlocks * kTile * 128;
   static constexpr int kSmem = kQ + 2 * kStages * kKV + 1024;
@@ -380,11 +383,9 @@ __global__ __launch_bounds__(kThreads, Shape<D>::kCtas) void dc_prefix_kernel(co
         commit(k_empty + 8 * st);
         return true;
       };
-      bool go = wait(waits, q_full, 0);
-      if (go && S::kScores > 1) go = scores(0);
+      bool go = wait(waits, q_full, 0) && scores(0);
       for (uint32_t i = 0; i < tiles && go; ++i) {
-        const uint32_t next = S::kScores > 1 ? i + 1 : i;
-        if (next < tiles) go = scores(next);
+        if (i + 1 < tiles) go = scores(i + 1);
         const uint32_t st = i % S::kStages, buf = i % S::kScores, v0 = v_at + st * S::kKV;
         go = go && wait(waits, v_full + 8 * st, (i / S::kStages) & 1) && wait(waits, p_full + 8 * buf, (i / S::kScores) & 1);
         if (!go) break;
@@ -656,18 +657,6 @@ cudaError_t launch_prefix_join(const PrefixParams& p, int dtype, int dim, bool p
 
 DC_BOUNDS_READER(take_bounds_prefix)
 
-cudaError_t take_prefix_faults(uint32_t* bits) {
-  *bits = 0;
-  cudaError_t e = cudaDeviceSynchronize();
-  if (e != cudaSuccess) return e;
-  unsigned int v = 0;
-  e = cudaMemcpyFromSymbol(&v, g_prefix_fault_bits, sizeof v);
-  if (e == cudaSuccess && v) {
-    const unsigned int zero = 0;
-    e = cudaMemcpyToSymbol(g_prefix_fault_bits, &zero, sizeof zero);
-  }
-  *bits = v;
-  return e;
-}
+DC_FAULT_READER(take_prefix_faults, g_prefix_fault_bits)
 
 }  // namespace dc

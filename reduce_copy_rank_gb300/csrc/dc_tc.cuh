@@ -181,19 +181,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t at, float (&v)[32]) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
-// f(j0, columns j0 .. j0 + 31) for the first N columns (a multiple of 32), each
-// group's load under way while the one before is worked on.
-template <int N, class F>
-__device__ __forceinline__ void tmem_each32(uint32_t at, F f) {
-  uint32_t r[2][32];
-  tmem_ld32(at, r[0]);
-#pragma unroll
-  for (int j0 = 0; j0 < N; j0 += 32) {
-    tmem_wait_ld(r[j0 / 32 & 1]);
-    if (j0 + 32 < N) tmem_ld32(at + j0 + 32, r[(j0 / 32 + 1) & 1]);
-    f(j0, r[j0 / 32 & 1]);
-  }
-}
 // The other way: 32 or 16 columns from each thread's words.
 __device__ __forceinline__ void tmem_st32(uint32_t at, const float (&v)[32]) {
   uint32_t r[32];
@@ -292,15 +279,8 @@ __device__ __forceinline__ void come_late(uint64_t limit_ns) {
 }
 
 // ------------------------------------------------------------- tiled loads ---
-// The tile of `map` at column x (a multiple of 16 bytes) and row y; places
-// outside the tensor read 0.
-__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x, int32_t y) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
-      "l"(map), "r"(bar), "r"(x), "r"(y)
-      : "memory");
-}
-// The same of a paged cache: column x, key head, slot and page.
+// The box of `map` at column x (a multiple of 16 bytes) of a paged cache: key head, slot
+// and page; places outside the tensor read 0.
 __device__ __forceinline__ void load_paged(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x, int32_t head,
                                            int32_t slot, int32_t page) {
   asm volatile(
@@ -308,8 +288,8 @@ __device__ __forceinline__ void load_paged(uint32_t dst, const CUtensorMap* map,
       "l"(map), "r"(bar), "r"(x), "r"(head), "r"(slot), "r"(page)
       : "memory");
 }
-// ... into this CTA's shared memory, counted by a barrier of either CTA of the
-// pair (a cluster_addr).
+// The tile at column x and row y of a matrix, into this CTA's shared memory, counted by
+// a barrier of either CTA of the pair (a cluster_addr).
 __device__ __forceinline__ void load_tile_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x, int32_t y) {
   asm volatile(
       "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
@@ -328,6 +308,22 @@ cudaError_t make_map(CUtensorMap* map, int dtype, uint64_t base, uint64_t rows, 
 // and `slots` neighbouring tokens of a page.
 cudaError_t make_paged_map(CUtensorMap* map, int dtype, const PagedView& v, int dim, int heads, uint32_t page_size,
                            int64_t pages, uint32_t slots);
+
+// cudaError_t NAME(uint32_t* bits): reads and clears a file's fault word WORD.
+#define DC_FAULT_READER(NAME, WORD)                              \
+  cudaError_t NAME(uint32_t* bits) {                             \
+    *bits = 0;                                                   \
+    cudaError_t e = cudaDeviceSynchronize();                     \
+    if (e != cudaSuccess) return e;                              \
+    unsigned int v = 0;                                          \
+    e = cudaMemcpyFromSymbol(&v, WORD, sizeof v);                \
+    if (e == cudaSuccess && v) {                                 \
+      const unsigned int zero = 0;                               \
+      e = cudaMemcpyToSymbol(WORD, &zero, sizeof zero);          \
+    }                                                            \
+    *bits = v;                                                   \
+    return e;                                                    \
+  }
 
 }  // namespace tc
 }  // namespace dc

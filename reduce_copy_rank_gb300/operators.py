@@ -349,8 +349,9 @@ def linear_logprobs_backward(hidden, weights: Sequence, tokens, lse, grad_logpro
 
     The logits are computed again, up to 24576 columns at a time; their gradient is
     rounded to 16 bits before its products, but for the tokens' own elements; the
-    sums are binary32.  Rows of the weights' gradient past ``vocab`` receive 0.
-    A row without upstream gradients (padding) has none, but its hidden row has
+    sums are binary32, in an order that is fixed but, for the hidden rows' gradient,
+    depends on the sharding.  Rows of the weights' gradient past ``vocab`` receive 0.
+    A token past the vocabulary gives NaN.  A row without upstream gradients (padding) has none, but its hidden row has
     to be finite: the weights' gradient is a product with all of them.  ``workspace``:
     :func:`linear_logprobs_workspace` with ``backward``.  Returns
     ``(grad_hidden, grad_weights)``."""
@@ -618,7 +619,10 @@ def prefix_attention(q, k_cache, v_cache, prefix_table, prefix_lengths, page_tab
     Either part may be empty; without any token the result is zeros (lse
     -inf).  A page number outside the cache, or a length past its table, gives
     NaN in the sequences that it belongs to.  A sequence's bits do not depend
-    on the other sequences.  ``workspace``: :func:`prefix_attention_workspace`.
+    on the other sequences.  The prefix's weights are rounded to 16 bits before
+    they meet the values, where :func:`paged_attention` rounds nothing but the
+    output (error 2.4e-3 for 1.7e-3 in bfloat16, 2.9e-4 for 2.1e-4 in float16).
+    ``workspace``: :func:`prefix_attention_workspace`.
     Returns ``out``."""
     status = (_module or _binding()).prefix_attention(q, k_cache, v_cache, page_table, lengths, out, workspace, scale, 0, lse,
                                                       stream, prefix_table, prefix_lengths)
