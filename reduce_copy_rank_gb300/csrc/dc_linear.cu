@@ -774,7 +774,7 @@ __global__ __launch_bounds__(kLostThreads) void dc_linear_lost_kernel(const __gr
   __shared__ uint32_t hits[kLostRows];    // the marked rows: row of these kLostRows, column (8 bits)
   __shared__ uint16_t order[kLostRows];   // their rows, by column
   __shared__ float joined[kLostWarps][kLinearN];
-  __shared__ uint32_t total[kLinearN], count[kLinearN], start[kLinearN], warps[kLostWarps];
+  __shared__ uint32_t count[kLinearN], start[kLinearN], warps[kLostWarps];
   __shared__ int32_t place[kLinearN];     // of a column's sum, -1: it has none yet
   __shared__ uint16_t many[kLinearN];     // the columns that have sums
   const uint32_t t = threadIdx.x, lane = t & 31, warp = t >> 5;
@@ -788,35 +788,41 @@ __global__ __launch_bounds__(kLostThreads) void dc_linear_lost_kernel(const __gr
   // (a mark says that the row's token is one of these)
   auto column_of = [&](uint64_t row) { return static_cast<uint32_t>(token_of(p.tokens, p.tokens64, row) - first) & (kLinearN - 1); };
 
-  // how many rows each column has
-  total[t] = 0;
+  // which columns have sums: how many rows each has, counted first where those come in parts
+  const bool links = blockIdx.y == 0, parts = groups > kLostWords;
+  bool shared = false;
+  uint32_t n_many = 0;
+  auto decide = [&](uint32_t rows) {
+    shared = rows > kLostAlone;
+    const uint32_t at = scan_cta(shared, warps, &n_many);
+    if (shared) many[at] = static_cast<uint16_t>(t);
+  };
+  count[t] = 0;
   place[t] = -1;
-  __syncthreads();
-  for (uint32_t g0 = warp * 32; g0 < groups; g0 += kLostThreads) {
-    const uint32_t word = mark(g0 + lane);
-    uint32_t some = __ballot_sync(~0u, word != 0);
-    while (some) {
-      constexpr int kWords = 4;
-      uint32_t column[kWords];
+  if (parts) {
+    __syncthreads();
+    for (uint32_t g0 = warp * 32; g0 < groups; g0 += kLostThreads) {
+      const uint32_t word = mark(g0 + lane);
+      uint32_t some = __ballot_sync(~0u, word != 0);
+      while (some) {
+        constexpr int kWords = 4;
+        uint32_t column[kWords];
 #pragma unroll
-      for (int k = 0; k < kWords; ++k) {
-        const uint32_t at = some ? static_cast<uint32_t>(__ffs(static_cast<int>(some)) - 1) : 0u;
-        const uint32_t bits = __shfl_sync(~0u, word, static_cast<int>(at));
-        column[k] = some && (bits >> lane & 1) ? column_of(32ull * (g0 + at) + lane) : static_cast<uint32_t>(kLinearN);
-        some &= some - 1;
+        for (int k = 0; k < kWords; ++k) {
+          const uint32_t at = some ? static_cast<uint32_t>(__ffs(static_cast<int>(some)) - 1) : 0u;
+          const uint32_t bits = __shfl_sync(~0u, word, static_cast<int>(at));
+          column[k] = some && (bits >> lane & 1) ? column_of(32ull * (g0 + at) + lane) : static_cast<uint32_t>(kLinearN);
+          some &= some - 1;
+        }
+#pragma unroll
+        for (int k = 0; k < kWords; ++k)
+          if (column[k] < kLinearN) atomicAdd(&count[column[k]], 1u);
       }
-#pragma unroll
-      for (int k = 0; k < kWords; ++k)
-        if (column[k] < kLinearN) atomicAdd(&total[column[k]], 1u);
     }
+    __syncthreads();
+    decide(count[t]);
+    if (!links && n_many == 0) return;
   }
-  __syncthreads();
-  const bool shared = total[t] > kLostAlone;
-  uint32_t n_many;
-  const uint32_t i_many = scan_cta(shared, warps, &n_many);
-  if (shared) many[i_many] = static_cast<uint16_t>(t);
-  const bool links = blockIdx.y == 0;
-  if (!links && n_many == 0) return;
 
   int32_t head = -1, last = -1;  // this thread's column's first row, and the last so far
   for (uint32_t g0 = 0; g0 < groups; g0 += kLostWords) {
@@ -834,6 +840,10 @@ __global__ __launch_bounds__(kLostThreads) void dc_linear_lost_kernel(const __gr
     }
     __syncthreads();
     const uint32_t mine = count[t];
+    if (!parts) {
+      decide(mine);
+      if (!links && n_many == 0) return;
+    }
     at = scan_cta(mine, warps, &all);
     start[t] = at;
     for (uint32_t k = 0, left = mine; left && k < n; ++k) {  // (all threads read the same one)
