@@ -34,9 +34,9 @@
 // is between 2^14 and 2^15: what is 2^-29 of that is still a normal number.
 //
 // Bound: the tensor cores for training batches, the weights' bytes for few rows.
-// Measured, BF16, 4096 rows of 4096 against 128000 columns: forward 2.64 ms, 1.63
-// PFLOP/s, gradient 8.0 to 8.4 ms, 1.53 to 1.61 (tiles of 128 x 256 a CTA, without the pair:
-// 2.71 and 8.84); 128 rows against 131072 columns on 8 shards: 194 us, 5.5 TB/s (179 and 6.0
+// Measured, BF16, 4096 rows of 4096 against 128000 columns: forward 2.62 to 2.69
+// ms, 1.6 PFLOP/s, gradient 8.0 to 8.4 ms, 1.53 to 1.61 (tiles of 128 x 256 a CTA, without the pair:
+// 2.71 and 8.84); 128 rows against 131072 columns on 8 shards: 194 to 201 us, 5.3 to 5.5 TB/s (179 and 6.0
 // with tiles of 128 x 256 and one run: a row of tiles has half of its rows to spare here, and
 // shorter runs are read more often).
 #include <algorithm>
@@ -740,7 +740,7 @@ __global__ __launch_bounds__(kFinishThreads) void dc_linear_finish_kernel(const 
 // Measured, BF16, 16384 rows of 4096 against 64000 columns, tokens spread evenly / half of
 // the rows one token's / as often as the n-th word of a text: 16.3 / 16.5 / 16.9 ms (all of
 // it by the tile's own warps: 15.5 / 30.9 / 18.0 to 21.5); 509 rows of 1000 against 50021:
-// 210 / 237 / 245 us (200 / 534 / 284).  13 and 5 us a chunk of columns.
+// 208 / 235 / 242 us (200 / 534 / 284).  13 and 5 us a chunk of columns.
 constexpr int kLostThreads = 256, kLostWarps = kLostThreads / 32;
 constexpr uint32_t kLostRows = 4096, kLostWords = kLostRows / 32;
 constexpr uint32_t kLostAtOnce = 8;  // rows whose loads a warp has in flight
